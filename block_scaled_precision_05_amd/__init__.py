@@ -20,12 +20,19 @@ if ``libbsg.so`` is missing or cannot be loaded, every call raises.
     D = moe_ffn_fp8(A, sfa, W13, sfw13, W2, sfw2, offsets)   # grouped up, SwiGLU, grouped down
     moe_ffn_fp8_noalloc(A, sfa, W13, sfw13, W2, sfw2, offsets, out=D)   # no workspace, no allocation
     L = mqa_logits(fmt, Q, sfq, K, sfk, W, ks, ke, S)  # sum_h w * max(0, q_h . k) in key windows
+    plan = sort_tokens(ids, G, align=128)       # expert ids [T, k] -> rows grouped by expert
+    A = moe_dispatch_bf16(X, plan)              # token rows -> their experts' rows
+    A, sfa = moe_dispatch_fp8(X, plan)          # the same, quantised on the way (also _fp4)
+    D = moe_combine(Y, plan, W)                 # sum_j w * experts' row, back in token order
+    dY, dW = moe_combine_backward(dD, Y, plan, W)
+    D = lora_add_bf16(X, A, B, plan, scale, base)  # base + s_g B_g (A_g x), an adapter per token
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -80,6 +87,23 @@ EXPORTS = {
                             _vp, _i64, _i64, _vp, _i64, _i64,
                             _vp, _i32, _i64, _i64, _i64,
                             _vp, _i64, _i32, _vp],
+    "sort_tokens": [_vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
+                    _vp],
+    "moe_dispatch_bf16": [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp],
+    "moe_dispatch_fp8": [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32,
+                         _vp],
+    "moe_dispatch_fp4": [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32,
+                         _vp],
+    "moe_combine": [_vp, _i64, _vp, _vp, _i64, _i64, _i32, _i64, _i64, _vp, _i64, _vp],
+    "moe_combine_backward": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i64, _i64,
+                             _vp, _i64, _vp, _i64, _vp],
+    "lora_add_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
+                      _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp],
+}
+# functions that return a number of bytes, not a status
+SIZES = {
+    "sort_tokens_workspace": [_i64, _i32],
+    "lora_add_workspace": [_i64, _i64, _i32],
 }
 
 
@@ -103,6 +127,10 @@ def lib() -> ctypes.CDLL:
                 f = getattr(l, name)
                 f.argtypes = argtypes
                 f.restype = ctypes.c_int
+            for name, argtypes in SIZES.items():
+                f = getattr(l, name)
+                f.argtypes = argtypes
+                f.restype = _i64
             l.bsg_status_string.argtypes = [ctypes.c_int]
             l.bsg_status_string.restype = ctypes.c_char_p
             _lib = l
@@ -134,6 +162,8 @@ def _mat(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    if t.numel() == 0:      # an empty tensor's strides mean nothing
+        return t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -565,4 +595,286 @@ def mqa_logits(fmt: str, Q, sfq, K, sfk, W, ks, ke, S: int, q_per_group: int | N
         _ptr(Q), _mat(Q, "Q"), _ptr(sfq), _packed(sfq, "sfq"), _ptr(K), _mat(K, "K"), _ptr(sfk),
         _packed(sfk, "sfk"), _ptr(W), _mat(W, "W"), _ptr(ks), _ptr(ke), _ptr(out), _mat(out, "out"),
         T, S, H, max(per, 1), int(group_rows), _stream(stream)))
+    return out
+
+
+class _Place:
+    """Device and stream of a call: makes the operands' device current (launches and
+    allocations go there) and, for a stream other than the device's current one, makes
+    that current too, so that buffers allocated for the call belong to it."""
+
+    __slots__ = ("device", "stream", "handle")
+
+    def __init__(self, t: torch.Tensor, stream):
+        index = t.device.index
+        self.device = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+        self.stream = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream(index).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            elif stream.device != t.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+            self.stream = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _one_device(first, *ts):
+    _dev(first, *ts)
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must live on the same GPU")
+
+
+class TokenSort(NamedTuple):
+    """The plan of sort_tokens.  The operators below take it, or any four such tensors."""
+    offsets: torch.Tensor    # int32 [G+1] row ranges of the groups; masked layout: counts [G]
+    row_of: torch.Tensor     # int32 [T, k] row of each pair, -1 without one
+    pair_of: torch.Tensor    # int32 [rows] pair t*k + j in a row; -1 padding, -2 no group's row
+    row_group: torch.Tensor  # int32 [rows] group of a row that holds a pair, -1 elsewhere
+
+
+def sort_tokens(ids, G: int, align: int = 1, cap: int = 0, out: TokenSort | None = None,
+                workspace=None, stream=None) -> TokenSort:
+    """Stable sort of token-expert pairs by expert.  ids int32 [T, k] (values outside
+    [0, G) have no row).  Contiguous layout (cap = 0): every group's count is rounded up
+    to a multiple of ``align`` rows and plan.offsets are the M-grouped GEMMs' offsets;
+    masked layout (cap > 0): group g owns rows g*cap .., keeps its first cap pairs, and
+    plan.offsets are the masked GEMM's counts.  ``out`` may pass a plan's four tensors
+    (rows at least T*k + min(G, T*k)*(align-1), or G*cap), ``workspace`` an int32 tensor
+    of at least sort_tokens_workspace(T*k, G) bytes."""
+    _dev(ids)
+    if ids.dtype != torch.int32 or ids.dim() != 2:
+        raise TypeError("ids must be an int32 tensor [T, k]")
+    T, k = ids.shape
+    n = T * k
+    if align < 1 or cap < 0 or G < 0:
+        raise ValueError("align must be at least 1, cap and G not negative")
+    rows = G * cap if cap else (n + min(G, n) * (align - 1) if G else 0)
+    need = lib().sort_tokens_workspace(n, G)
+    with _Place(ids, stream) as st:
+        if out is None:
+            e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
+            plan = TokenSort(e(G if cap else G + 1), e(T, k), e(rows), e(rows))
+        else:
+            plan = TokenSort(*out)
+            _one_device(ids, *plan)
+            for t in plan:
+                if t.dtype != torch.int32 or not t.is_contiguous():
+                    raise TypeError("out must hold contiguous int32 tensors")
+            rows = plan.pair_of.numel()
+            if plan.offsets.numel() != (G if cap else G + 1) or plan.row_of.shape != ids.shape or \
+                    plan.row_group.numel() != rows:
+                raise ValueError("out must hold offsets [G+1] (masked: [G]), row_of [T, k] and "
+                                 "pair_of, row_group [rows]")
+        if workspace is None and need:
+            workspace = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
+        if workspace is not None:
+            _one_device(ids, workspace)
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check("sort_tokens", lib().sort_tokens(
+            _ptr(ids), _mat(ids, "ids"), T, k, G, align, cap, _ptr(plan.offsets),
+            _ptr(plan.row_of), _ptr(plan.pair_of), _ptr(plan.row_group), rows, _ptr(workspace),
+            size, st))
+    return plan
+
+
+def _plan(plan, *ts):
+    """The plan's row_of, pair_of and row_group, checked against the other operands' device."""
+    offsets, row_of, pair_of, row_group = plan
+    _one_device(row_of, pair_of, row_group, *ts)
+    for t in (row_of, pair_of, row_group):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise TypeError("the plan must hold contiguous int32 tensors")
+    if row_of.dim() != 2 or pair_of.dim() != 1 or row_group.shape != pair_of.shape:
+        raise ValueError("the plan must hold row_of [T, k] and pair_of, row_group [rows]")
+    return row_of, pair_of, row_group
+
+
+def _bf16(t, name, rows, cols):
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    return _mat(t, name)
+
+
+def moe_dispatch_bf16(X, plan, out=None, stream=None):
+    """bf16 X [T, H] -> bf16 [rows, H]: row plan.row_of[t, j] is token t's row; padding
+    rows are zero and rows of no group (pair_of -2) keep what ``out`` held (they are
+    uninitialised in a tensor allocated here).  The gradient with respect to X is
+    moe_combine(gradient, plan)."""
+    row_of, pair_of, _ = _plan(plan, X, out)
+    T, k = row_of.shape
+    rows = pair_of.numel()
+    if X.dim() != 2:
+        raise ValueError("X must be [T, H]")
+    H = X.shape[1]
+    ldx = _bf16(X, "X", T, H)
+    with _Place(X, stream) as st:
+        if out is None:
+            out = torch.empty((rows, H), dtype=torch.bfloat16, device=X.device)
+        ldo = _bf16(out, "out", rows, H)
+        _check("moe_dispatch_bf16", lib().moe_dispatch_bf16(
+            _ptr(X), ldx, _ptr(row_of), _ptr(pair_of), T, k, rows, H, _ptr(out), ldo, st))
+    return out
+
+
+def _dispatch_quant(fn, X, plan, rule, per, gk, out, sf_out, stream):
+    row_of, pair_of, _ = _plan(plan, X, out, sf_out)
+    T, k = row_of.shape
+    rows = pair_of.numel()
+    if X.dim() != 2:
+        raise ValueError("X must be [T, H]")
+    H = X.shape[1]
+    ldx = _bf16(X, "X", T, H)
+    if rule not in SCALE_RULES:
+        raise ValueError(f"rule must be one of {sorted(SCALE_RULES)}")
+    kp = (H // gk + 1) // 2
+    with _Place(X, stream) as st:
+        if out is None:
+            Q = torch.empty((rows, H // per), dtype=torch.uint8, device=X.device)
+        else:
+            Q = _bytes_u8(out)
+            if Q.element_size() != 1 or Q.dim() != 2 or Q.shape[0] != rows or Q.shape[1] != H // per:
+                raise ValueError(f"out must hold the codes of [{rows}, {H // per}] bytes")
+        if sf_out is None:
+            sf_out = torch.empty((kp, rows), dtype=torch.int16, device=X.device)
+        ld_sf = _packed(sf_out, "sf_out")
+        if sf_out.shape[0] != kp or sf_out.shape[1] < rows:
+            raise ValueError(f"sf_out must be packed int16 [{kp}, >={rows}]")
+        _check(fn, getattr(lib(), fn)(
+            _ptr(X), ldx, _ptr(row_of), _ptr(pair_of), T, k, rows, H, _ptr(Q), _mat(Q, "out"),
+            _ptr(sf_out), ld_sf, SCALE_RULES[rule], st))
+    return Q, sf_out
+
+
+def moe_dispatch_fp8(X, plan, rule: str = "ceil", out=None, sf_out=None, stream=None):
+    """bf16 X [T, H] -> (e4m3 codes uint8 [rows, H], packed int16 scales [ceil(H/256), rows])
+    in the groups' rows: quantize_fp8_per_token's codes and scales, each token quantised
+    once and written to its k rows.  Padding rows are a quantised zero row; rows of no
+    group are left as they were."""
+    return _dispatch_quant("moe_dispatch_fp8", X, plan, rule, 1, 128, out, sf_out, stream)
+
+
+def moe_dispatch_fp4(X, plan, rule: str = "ceil", out=None, sf_out=None, stream=None):
+    """bf16 X [T, H] -> (e2m1 codes uint8 [rows, H/2], packed int16 scales [ceil(H/64), rows])
+    in the groups' rows, as moe_dispatch_fp8 with quantize_fp4_per_token's format."""
+    return _dispatch_quant("moe_dispatch_fp4", X, plan, rule, 2, 32, out, sf_out, stream)
+
+
+def _weights(W, T, k, name):
+    if W is None:
+        return 0
+    if W.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if W.dim() != 2 or W.shape[0] != T or W.shape[1] != k:
+        raise ValueError(f"{name} must be [{T}, {k}], got {list(W.shape)}")
+    return _mat(W, name)
+
+
+def moe_combine(Y, plan, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * Y[plan.row_of[t, j]] (bf16 [T, H], fp32 sums, rounded
+    once); weights float32 [T, k], or None for ones (the gradient of the dispatch).  A
+    pair without a row adds nothing."""
+    row_of, pair_of, _ = _plan(plan, Y, weights, out)
+    T, k = row_of.shape
+    rows = pair_of.numel()
+    if Y.dim() != 2:
+        raise ValueError("Y must be [rows, H]")
+    H = Y.shape[1]
+    ldy = _bf16(Y, "Y", rows, H)
+    ldw = _weights(weights, T, k, "weights")
+    with _Place(Y, stream) as st:
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=Y.device)
+        ldo = _bf16(out, "out", T, H)
+        _check("moe_combine", lib().moe_combine(
+            _ptr(Y), ldy, _ptr(row_of), _ptr(weights), ldw, T, k, rows, H, _ptr(out), ldo, st))
+    return out
+
+
+def moe_combine_backward(dout, Y, plan, weights=None, need_weights: bool = True, out=None,
+                         stream=None):
+    """Gradients of moe_combine: (dY bf16 [rows, H], dW float32 [T, k]) from dout bf16
+    [T, H].  Padding rows of dY are zero, rows of no group keep what ``out`` held.  With
+    need_weights False dW is None and Y is not read (it may be None)."""
+    row_of, pair_of, _ = _plan(plan, dout, Y, weights, out)
+    T, k = row_of.shape
+    rows = pair_of.numel()
+    if dout.dim() != 2:
+        raise ValueError("dout must be [T, H]")
+    H = dout.shape[1]
+    ldd = _bf16(dout, "dout", T, H)
+    if need_weights and Y is None:
+        raise ValueError("the weights' gradient needs Y")
+    ldy = 0 if Y is None else _bf16(Y, "Y", rows, H)
+    ldw = _weights(weights, T, k, "weights")
+    with _Place(dout, stream) as st:
+        if out is None:
+            out = torch.empty((rows, H), dtype=torch.bfloat16, device=dout.device)
+        dW = torch.empty((T, k), dtype=torch.float32, device=dout.device) if need_weights else None
+        _check("moe_combine_backward", lib().moe_combine_backward(
+            _ptr(dout), ldd, _ptr(Y), ldy, _ptr(row_of), _ptr(pair_of), _ptr(weights), ldw, T, k,
+            rows, H, _ptr(out), _bf16(out, "out", rows, H), _ptr(dW), k, st))
+    return out, dW
+
+
+def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None, stream=None):
+    """out[t] = base[t] + scale[g] * B[g] (A[g] x_t) for token t of adapter g, base[t] for a
+    token without one.  X bf16 [T, K]; A bf16 [G, r, K] and B bf16 [G, N, r] (r a multiple
+    of 8, at most 128; lower ranks padded with zeros); plan of sort_tokens(ids [T, 1], G,
+    align) with align a multiple of 16; scale float32 [G] or None; base bf16 [T, N] or
+    None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
+    aligned tensor of at least lora_add_workspace(rows, K, r) bytes."""
+    row_of, pair_of, row_group = _plan(plan, X, A, B, scale, base, out, workspace)
+    T, k = row_of.shape
+    rows = pair_of.numel()
+    if k != 1:
+        raise ValueError("a token takes one adapter: the plan must come from ids [T, 1]")
+    if A.dim() != 3 or B.dim() != 3 or X.dim() != 2:
+        raise ValueError("X must be [T, K], A [G, r, K] and B [G, N, r]")
+    G, r, K = A.shape
+    N = B.shape[1]
+    if B.shape[0] != G or B.shape[2] != r:
+        raise ValueError("A and B disagree on the adapters or the rank")
+    if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
+        raise TypeError("A and B must be bfloat16")
+    if (K > 1 and A.stride(2) != 1) or (r > 1 and B.stride(2) != 1):
+        raise ValueError("A and B must be contiguous along their last dimension")
+    ldx = _bf16(X, "X", T, K)
+    ld_base = 0 if base is None else _bf16(base, "base", T, N)
+    if scale is not None and (scale.dtype != torch.float32 or scale.dim() != 1 or
+                              scale.numel() != G or not scale.is_contiguous()):
+        raise TypeError("scale must be a contiguous float32 vector [G]")
+    need = lib().lora_add_workspace(rows, K, r)
+    with _Place(X, stream) as st:
+        if out is None:
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
+        ldo = _bf16(out, "out", T, N)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check("lora_add_bf16", lib().lora_add_bf16(
+            _ptr(X), ldx, _ptr(A), A.stride(1), A.stride(0), _ptr(B), B.stride(1), B.stride(0),
+            _ptr(scale), _ptr(row_of), _ptr(pair_of), _ptr(row_group), rows, _ptr(base), ld_base,
+            _ptr(out), ldo, T, G, N, K, r, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), st))
     return out

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libbsg.so")
 SOURCES = [os.path.join(HERE, "csrc", "api.hip"), os.path.join(HERE, "csrc", "quant.hip"),
-           os.path.join(HERE, "csrc", "mqa.hip")]
+           os.path.join(HERE, "csrc", "mqa.hip"), os.path.join(HERE, "csrc", "route.hip"),
+           os.path.join(HERE, "csrc", "lora.hip")]
 PROBE_LIB = os.path.join(HERE, "libbsg_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "probe.hip")]
 HEADERS = [os.path.join(HERE, "csrc", h) for h in ("gemm_kernel.h", "configs.h", "internal.h",

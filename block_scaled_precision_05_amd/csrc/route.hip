@@ -1,0 +1,788 @@
+// route.hip -- rows grouped by a device-side id: tokens sorted by expert (or by
+// adapter), their rows dispatched to the groups (bf16 copies, or quantised on the way
+// to FP8 / FP4 with packed UE8M0 scales, the operands of the grouped GEMMs), the
+// experts' output rows combined with the router's weights, and the gradient of that.
+//
+// A pair p = t*k + j is token t's j-th choice.  Four index arrays connect the steps
+// (include/bsg.h): offsets, row_of[p], pair_of[row], row_group[row].  Every kernel
+// checks an index it reads from them against its arrays' sizes, so broken indices give
+// wrong rows but no access outside the operands.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/bsg.h"
+#include "quant_math.h"
+
+namespace bsg_route {
+
+using namespace bsg_qm;
+
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(2))) short short2_t;
+typedef __attribute__((ext_vector_type(2))) unsigned short ushort2_t;
+
+constexpr int kNone = -1;      // row_of: no row; pair_of: a padding row; row_group: no pair
+constexpr int kOutside = -2;   // pair_of: a row that belongs to no group
+constexpr int kMaxGroups = 1024;
+
+static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP; }
+
+// ---------------------------------------------------------------------------
+// Stable counting sort of the pairs by group.
+//
+// Only a few bytes per pair move (4 read, 12 written), so the cost is latency: launches
+// and dependent steps.  Up to kSingle pairs one workgroup does everything in one
+// launch; more pairs are cut into chunks, counted by a first launch (hist[chunk][g]),
+// and a second launch, in which every workgroup sums the counts of all chunks itself
+// (coalesced reads from L2) instead of waiting for a scan launch, ranks its chunk.
+//
+// Rank inside a chunk, in pair order: a wave takes 64 pairs; a lane's peers, the lanes
+// with its id, come from one ballot per id bit; its rank in the wave is the number of
+// peers below it and the lowest peer adds the wave's count to LDS.  A scan over the
+// waves per group then gives every wave its base.  No atomic decides an order, so the
+// result is the same on every run.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSingle = 4096;        // most pairs one workgroup sorts alone
+constexpr int kMaxChunks = 256;      // workgroups of the two-launch form
+
+struct SortArgs {
+  const int32_t* ids;
+  int64_t ld_ids;
+  int32_t k;
+  int32_t n;         // pairs, T*k
+  int32_t G;
+  int32_t align;
+  int32_t cap;       // > 0: masked layout
+  int32_t chunk;     // pairs per workgroup, a multiple of kSortThreads
+  int32_t nchunks;
+  int32_t* offsets;
+  int32_t* row_of;
+  int32_t* pair_of;
+  int32_t* row_group;
+  int32_t rows;
+  int32_t* hist;     // [nchunks][G]; unused with one chunk
+};
+
+// Group of pair p, or -1 (an id outside [0, G), or p past the end).
+__device__ __forceinline__ int pair_group(const SortArgs& a, int p) {
+  if (p >= a.n) return -1;
+  const int t = p / a.k;
+  const int id = a.ids[(int64_t)t * a.ld_ids + (p - t * a.k)];
+  return (uint32_t)id < (uint32_t)a.G ? id : -1;
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs a) {
+  __shared__ int32_t cnt[kMaxGroups];
+  for (int g = threadIdx.x; g < a.G; g += kSortThreads) cnt[g] = 0;
+  __syncthreads();
+  const int p0 = blockIdx.x * a.chunk;
+  for (int i = threadIdx.x; i < a.chunk; i += kSortThreads) {
+    const int g = pair_group(a, p0 + i);
+    if (g >= 0) atomicAdd(&cnt[g], 1);   // a sum: the order does not matter
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < a.G; g += kSortThreads) a.hist[blockIdx.x * a.G + g] = cnt[g];
+}
+
+// Inclusive scan over the workgroup, one value per thread.
+__device__ __forceinline__ int block_incl_scan(int v, int32_t* wave_sum) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  if (lane == 63) wave_sum[wave] = v;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += wave_sum[w];
+  __syncthreads();
+  return v + before;
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortArgs a) {
+  __shared__ int32_t total[kMaxGroups];      // pairs of each group
+  __shared__ int32_t next[kMaxGroups];       // pairs of each group in earlier chunks / steps
+  __shared__ int32_t start[kMaxGroups + 1];  // first row of each group
+  __shared__ uint16_t wcnt[kSortWaves][kMaxGroups];
+  __shared__ int32_t wave_sum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int p0 = blockIdx.x * a.chunk;
+
+  for (int g = tid; g < kMaxGroups; g += kSortThreads) total[g] = next[g] = 0;
+  __syncthreads();
+  if (a.nchunks == 1) {
+    for (int i = tid; i < a.chunk; i += kSortThreads) {
+      const int g = pair_group(a, i);
+      if (g >= 0) atomicAdd(&total[g], 1);
+    }
+  } else {
+    // 2^s threads share a group and take every 2^s-th chunk (integer sums by LDS
+    // atomics: any order gives the same result)
+    int s = 0;
+    while ((a.G << (s + 1)) <= kSortThreads) ++s;
+    const int parts = 1 << s, g = tid % a.G, part = tid / a.G;
+    if (part < parts) {
+      int sum = 0, mine = 0;
+#pragma unroll 4
+      for (int c = part; c < a.nchunks; c += parts) {
+        const int v = a.hist[c * a.G + g];
+        sum += v;
+        mine += c < (int)blockIdx.x ? v : 0;
+      }
+      atomicAdd(&total[g], sum);
+      atomicAdd(&next[g], mine);
+    }
+  }
+  __syncthreads();
+
+  // group starts: padded counts, scanned (G <= kSortThreads: one group per thread)
+  const int cnt = tid < a.G ? total[tid] : 0;
+  if (a.cap > 0) {
+    if (tid < a.G) {
+      start[tid] = tid * a.cap;
+      if (blockIdx.x == 0) a.offsets[tid] = cnt < a.cap ? cnt : a.cap;
+    }
+    if (tid == 0) start[a.G] = a.G * a.cap;
+    __syncthreads();
+  } else {
+    const int pad = (cnt + a.align - 1) / a.align * a.align;
+    const int incl = block_incl_scan(pad, wave_sum);
+    if (tid < a.G) start[tid + 1] = incl;
+    if (tid == 0) start[0] = 0;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int g = tid; g <= a.G; g += kSortThreads) a.offsets[g] = start[g];
+  }
+
+  // ranks, kSortThreads pairs at a time
+  for (int i0 = 0; i0 < a.chunk; i0 += kSortThreads) {
+    if (p0 + i0 >= a.n) break;   // uniform over the workgroup
+    for (int x = tid; x < kSortWaves * (kMaxGroups / 2); x += kSortThreads)
+      ((uint32_t*)&wcnt[0][0])[x] = 0;
+    __syncthreads();
+    const int p = p0 + i0 + tid;
+    const int g = pair_group(a, p);
+    uint64_t peers = __ballot(g >= 0);
+    if (g < 0) peers = ~peers;
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const uint64_t set = __ballot(g >= 0 && ((g >> b) & 1));
+      peers &= (g >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    if (g >= 0 && rank == 0) wcnt[wave][g] = (uint16_t)__popcll(peers);
+    __syncthreads();
+    for (int gg = tid; gg < a.G; gg += kSortThreads) {
+      int run = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int c = wcnt[w][gg];
+        wcnt[w][gg] = (uint16_t)run;
+        run += c;
+      }
+      total[gg] = run;   // (the group totals are in `start` by now): this step's pairs
+    }
+    __syncthreads();
+    if (p < a.n) {
+      int row = kNone;
+      if (g >= 0) {
+        const int at = next[g] + wcnt[wave][g] + rank;
+        if (a.cap == 0 || at < a.cap) row = start[g] + at;
+        if (row >= a.rows) row = kNone;   // the host's capacity check makes this unreachable
+      }
+      a.row_of[p] = row;
+      if (row >= 0) {
+        a.pair_of[row] = p;
+        a.row_group[row] = g;
+      }
+    }
+    __syncthreads();
+    for (int gg = tid; gg < a.G; gg += kSortThreads) next[gg] += total[gg];
+    __syncthreads();
+  }
+
+  // rows without a pair: a group's padding (or, masked, the rest of its capacity), one
+  // wave per group, then the rows behind the last group
+  const int nw = gridDim.x * kSortWaves, gw = blockIdx.x * kSortWaves + wave;
+  for (int g = gw; g < a.G; g += nw) {
+    int c;
+    if (a.nchunks == 1) {
+      c = next[g];
+    } else {
+      c = 0;
+      for (int ch = lane; ch < a.nchunks; ch += 64) c += a.hist[ch * a.G + g];
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, 64);
+    }
+    for (int r = start[g] + c + lane; r < start[g + 1]; r += 64) {
+      a.pair_of[r] = a.cap > 0 ? kOutside : kNone;
+      a.row_group[r] = kNone;
+    }
+  }
+  for (int r = start[a.G] + blockIdx.x * kSortThreads + tid; r < a.rows;
+       r += gridDim.x * kSortThreads) {
+    a.pair_of[r] = kOutside;
+    a.row_group[r] = kNone;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Padding rows (pair_of == -1) zeroed by extra workgroups of the dispatch and backward
+// kernels: each looks at 64 rows and clears those that are padding.
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kPadRows = 64;
+
+// fill(row, lane) is called by one whole wave for every padding row of this block.
+template <class F>
+__device__ __forceinline__ void padding_rows(const int32_t* pair_of, int rows, int block, F&& fill) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = block * kPadRows + lane;
+  uint64_t pads = __ballot(r < rows && pair_of[r < rows ? r : rows - 1] == kNone);
+  int i = 0;
+  while (pads) {
+    const int b = __builtin_ctzll(pads);
+    pads &= pads - 1;
+    if (i++ % kWaves == wave) fill(block * kPadRows + b, lane);
+  }
+}
+
+// Buffer over one row: `bytes` long, or empty when the row index is not in [0, rows),
+// so that loads give zeros and stores are dropped.  The index is wave-uniform.
+constexpr int kRsrcWord3 = 0x00020000;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* base, int64_t row, int64_t rows,
+                                                           int64_t stride_bytes, uint32_t bytes) {
+  const bool in = row >= 0 && row < rows;
+  const uint64_t at = (uint64_t)base + (in ? row * stride_bytes : 0);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(lo | (hi << 32)), (short)0,
+                                           __builtin_amdgcn_readfirstlane(in ? (int)bytes : 0), kRsrcWord3);
+}
+
+// Loads and stores of VEC bf16 elements a lane: 8 (one 16-byte access) or 1.
+template <int VEC>
+struct Vec;
+template <>
+struct Vec<8> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  }
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_bit_cast(uint32_t, (bf16x2_t){(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+  }
+};
+template <>
+struct Vec<1> {
+  uint16_t w;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    w = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+  }
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+    __builtin_amdgcn_raw_buffer_store_b16(w, r, off, 0, 0);
+  }
+  __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)w << 16); }
+  __device__ __forceinline__ void set(const float (&v)[1]) {
+    w = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Dispatch, bf16: row row_of[t][j] of the output is token t's row.  A wave owns one
+// segment of 64*VEC elements of one token, reads it once and writes it k times.
+// ---------------------------------------------------------------------------
+template <int VEC>
+__global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
+    const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ row_of,
+    const int32_t* __restrict__ pair_of, int T, int k, int rows, int H, uint16_t* __restrict__ out,
+    int64_t ldo, int segs, int token_blocks) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t row_bytes = 2u * (uint32_t)H;
+  if ((int)blockIdx.x >= token_blocks) {
+    padding_rows(pair_of, rows, blockIdx.x - token_blocks, [&](int r, int ln) {
+      const __amdgpu_buffer_rsrc_t o = row_rsrc(out, r, rows, 2 * ldo, row_bytes);
+      Vec<VEC> z;
+      const float zero[VEC] = {};
+      z.set(zero);
+      for (uint32_t off = 2u * VEC * ln; off < row_bytes; off += 128u * VEC) z.store(o, off);
+    });
+    return;
+  }
+  const int64_t task = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
+  if (t >= T) return;
+  const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
+  Vec<VEC> v;
+  v.load(row_rsrc(X, t, T, 2 * ldx, row_bytes), off);
+  for (int j = 0; j < k; ++j)
+    v.store(row_rsrc(out, row_of[(int64_t)t * k + j], rows, 2 * ldo, row_bytes), off);
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch with quantisation: token t's row is quantised once (the codes and scale
+// bytes of the per-token quantisers, bit for bit) and its codes and packed scale words
+// written to its k rows.  A wave owns 1024 elements of one token, 16 a lane, so a
+// row's codes leave in 16-byte (e4m3) or 8-byte (e2m1) stores.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a),
+                                                                __builtin_bit_cast(ushort2_t, b)));
+}
+__device__ __forceinline__ uint32_t pk_min_u16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(ushort2_t, a),
+                                                                __builtin_bit_cast(ushort2_t, b)));
+}
+
+constexpr int kQElems = 1024;   // elements of a wave's segment
+
+// Sixteen bf16 values of one row a lane (two per word): their codes in q (4 words e4m3,
+// 2 words e2m1) and their block's scale byte.
+template <int FMT, int RULE>
+__device__ __forceinline__ int quantize16(uint32_t (&w)[8], uint32_t (&q)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = pk_max_u16(m, w[i] & 0x7FFF7FFFu);
+  uint32_t h = max(m & 0xFFFFu, m >> 16);
+  // the block's lanes: 2 (e2m1) or 8 (e4m3), by DPP moves (quad_perm [1,0,3,2] and
+  // [2,3,0,1], then row_half_mirror, which pairs the two quads of eight lanes)
+  h = max(h, (uint32_t)__builtin_amdgcn_mov_dpp((int)h, 0xB1, 0xF, 0xF, false));
+  if (FMT == FMT_E4M3) {
+    h = max(h, (uint32_t)__builtin_amdgcn_mov_dpp((int)h, 0x4E, 0xF, 0xF, false));
+    h = max(h, (uint32_t)__builtin_amdgcn_mov_dpp((int)h, 0x141, 0xF, 0xF, false));
+  }
+  const int byte = scale_byte<FMT, RULE>(h << 16);
+  const float sc = scale_f32(byte);
+  if (FMT == FMT_E4M3) {
+    if (RULE == BSG_SCALE_OCP_MX) {
+      // saturate at 448 * sc first, where the conversion would give NaN
+      const uint32_t lim = 0x43E0u + (uint32_t)((byte - 127) << 7);
+      const uint32_t lim2 = lim | (lim << 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pk_min_u16(w[i] & 0x7FFF7FFFu, lim2) | (w[i] & 0x80008000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      short2_t c = {0, 0};
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, __builtin_bit_cast(bf16x2_t, w[2 * i]), sc, false);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, __builtin_bit_cast(bf16x2_t, w[2 * i + 1]), sc, true);
+      q[i] = __builtin_bit_cast(uint32_t, c);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t c = 0;
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, w[4 * i]), sc, 0);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, w[4 * i + 1]), sc, 1);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, w[4 * i + 2]), sc, 2);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, w[4 * i + 3]), sc, 3);
+      q[i] = c;
+    }
+  }
+  return byte;
+}
+
+template <int FMT, int RULE>
+__global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
+    const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ row_of,
+    const int32_t* __restrict__ pair_of, int T, int k, int rows, int H, uint8_t* __restrict__ Q,
+    int64_t ldq, int16_t* __restrict__ sf, int64_t ld_sf, int segs, int token_blocks) {
+  constexpr int GK = Fmt<FMT>::GK;
+  constexpr int LPB = GK / 16;               // lanes per block
+  constexpr int WPS = kQElems / GK / 2;      // packed words per segment: 4 (e4m3), 16 (e2m1)
+  const int lane = threadIdx.x & 63;
+  const uint32_t q_bytes = FMT == FMT_E4M3 ? (uint32_t)H : (uint32_t)H / 2;
+  const int kb = H / GK, kp = (kb + 1) / 2;
+  if ((int)blockIdx.x >= token_blocks) {
+    // a padding row is a quantised zero row: codes 0, scale bytes 0 (the filler 0x7F)
+    padding_rows(pair_of, rows, blockIdx.x - token_blocks, [&](int r, int ln) {
+      const __amdgpu_buffer_rsrc_t o = row_rsrc(Q, r, rows, ldq, q_bytes);
+      for (uint32_t off = 8u * ln; off < q_bytes; off += 512u)
+        __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){0, 0}, o, off, 0, 0);
+      for (int i = ln; i < kp; i += 64)
+        sf[(int64_t)i * ld_sf + r] = (int16_t)(2 * i + 1 < kb ? 0 : 0x7F00);
+    });
+    return;
+  }
+  const int64_t task = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
+  if (t >= T) return;
+  const __amdgpu_buffer_rsrc_t xr = row_rsrc(X, t, T, 2 * ldx, 2u * (uint32_t)H);
+  const uint32_t e0 = (uint32_t)(s * kQElems + 16 * lane);   // lane's first element
+  const u32x4_t x0 = __builtin_amdgcn_raw_buffer_load_b128(xr, 2 * e0, 0, 0);
+  const u32x4_t x1 = __builtin_amdgcn_raw_buffer_load_b128(xr, 2 * e0 + 16, 0, 0);
+  uint32_t w[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+  uint32_t q[4] = {};
+  const int byte = quantize16<FMT, RULE>(w, q);
+  // packed words of the segment: lane 2*LPB*i holds word i's low byte, lane
+  // 2*LPB*i + LPB its high byte; spread so that lane i (mod WPS) holds word i
+  const int wi = lane % WPS;
+  const int lo = __shfl(byte, 2 * LPB * wi), hi = __shfl(byte, 2 * LPB * wi + LPB);
+  const int pair = s * WPS + wi;
+  const int word = lo | ((2 * pair + 1 < kb ? hi : 0x7F) << 8);
+  for (int j = 0; j < k; ++j) {
+    const __amdgpu_buffer_rsrc_t o =
+        row_rsrc(Q, row_of[(int64_t)t * k + j], rows, ldq, q_bytes);
+    if (FMT == FMT_E4M3)
+      __builtin_amdgcn_raw_buffer_store_b128((u32x4_t){q[0], q[1], q[2], q[3]}, o, e0, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){q[0], q[1]}, o, e0 / 2, 0, 0);
+  }
+  // lanes WPS*j .. WPS*j + WPS-1 store row j's words
+  for (int j0 = 0; j0 < k; j0 += 64 / WPS) {
+    const int j = j0 + lane / WPS;
+    if (j < k && pair < kp) {
+      const int r = row_of[(int64_t)t * k + j];
+      if ((uint32_t)r < (uint32_t)rows) sf[(int64_t)pair * ld_sf + r] = (int16_t)word;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = bf16( sum_j w[t][j] * Y[row_of[t][j]] ), fp32 sums in the order of
+// j, rounded once.  A wave owns 64*VEC elements of one token; the loads of up to eight
+// rows are in flight together.  A pair without a row reads zeros through an empty
+// buffer and its weight counts as zero.
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 8;   // rows in flight
+
+template <int VEC, int KC>
+__device__ __forceinline__ void combine_chunk(const uint16_t* Y, int64_t ldy, int rows, int H,
+                                              const int32_t* row_of, const float* w, int n, uint32_t off,
+                                              float (&acc)[VEC]) {
+  Vec<VEC> v[KC];
+  float ww[KC];
+#pragma unroll
+  for (int j = 0; j < KC; ++j) {
+    const int r = j < n ? row_of[j] : kNone;
+    v[j].load(row_rsrc(Y, r, rows, 2 * ldy, 2u * (uint32_t)H), off);
+    ww[j] = (uint32_t)r < (uint32_t)rows ? (w ? w[j] : 1.0f) : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < KC; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(ww[j], v[j].get(i), acc[i]);
+}
+
+template <int VEC>
+__global__ __launch_bounds__(kThreads) void combine_kernel(
+    const uint16_t* __restrict__ Y, int64_t ldy, const int32_t* __restrict__ row_of,
+    const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
+    uint16_t* __restrict__ out, int64_t ldo, int segs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t task = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
+  if (t >= T) return;
+  const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
+  const int32_t* ro = row_of + (int64_t)t * k;
+  const float* w = W ? W + (int64_t)t * ldw : nullptr;
+  float acc[VEC] = {};
+  for (int j = 0; j < k; j += kChunk)
+    combine_chunk<VEC, kChunk>(Y, ldy, rows, H, ro + j, w ? w + j : nullptr, min(kChunk, k - j), off, acc);
+  Vec<VEC> o;
+  o.set(acc);
+  o.store(row_rsrc(out, t, T, 2 * ldo, 2u * (uint32_t)H), off);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of combine: dY[row_of[t][j]] = bf16( w[t][j] * dO[t] ) and dW[t][j] =
+// <dO[t], Y[row_of[t][j]]> in fp32.  A workgroup owns a token: its waves take the
+// token's segments in turn, keep one partial dot product per choice and lane, and add
+// them over lanes and waves in a fixed order.  dO is read once per eight choices, Y
+// once, dY written once.
+// ---------------------------------------------------------------------------
+template <int VEC, int NW>
+__global__ __launch_bounds__(64 * NW) void combine_backward_kernel(
+    const uint16_t* __restrict__ dO, int64_t ldo, const uint16_t* __restrict__ Y, int64_t ldy,
+    const int32_t* __restrict__ row_of, const int32_t* __restrict__ pair_of,
+    const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
+    uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw, int segs) {
+  __shared__ float part[NW][kChunk];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t row_bytes = 2u * (uint32_t)H;
+  if ((int)blockIdx.x >= T) {
+    padding_rows(pair_of, rows, blockIdx.x - T, [&](int r, int ln) {
+      const __amdgpu_buffer_rsrc_t o = row_rsrc(dY, r, rows, 2 * lddy, row_bytes);
+      Vec<VEC> z;
+      const float zero[VEC] = {};
+      z.set(zero);
+      for (uint32_t off = 2u * VEC * ln; off < row_bytes; off += 128u * VEC) z.store(o, off);
+    });
+    return;
+  }
+  const int t = blockIdx.x;
+  const __amdgpu_buffer_rsrc_t g = row_rsrc(dO, t, T, 2 * ldo, row_bytes);
+  for (int j0 = 0; j0 < k; j0 += kChunk) {
+    const int32_t* ro = row_of + (int64_t)t * k + j0;
+    const int n = min(kChunk, k - j0);
+    int r[kChunk];
+    float w[kChunk], dot[kChunk] = {};
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      r[j] = j < n ? ro[j] : kNone;
+      w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
+    }
+    for (int s = wave; s < segs; s += NW) {
+      const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
+      Vec<VEC> d, y[kChunk];
+      d.load(g, off);
+      if (dW) {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) y[j].load(row_rsrc(Y, r[j], rows, 2 * ldy, row_bytes), off);
+      }
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        if (j >= n) break;
+        float v[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = w[j] * d.get(i);
+        Vec<VEC> o;
+        o.set(v);
+        o.store(row_rsrc(dY, r[j], rows, 2 * lddy, row_bytes), off);
+      }
+      if (dW) {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
+      }
+    }
+    if (!dW) continue;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      float v = dot[j];
+#pragma unroll
+      for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+      if (lane == 0) part[wave][j] = v;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < n) {
+      float v = 0.0f;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) v += part[x][threadIdx.x];
+      // (a pair without a row has read zeros; an infinity in dO must not turn its
+      // gradient into NaN)
+      const int rr = ro[threadIdx.x];
+      dW[(int64_t)t * lddw + j0 + threadIdx.x] = (uint32_t)rr < (uint32_t)rows ? v : 0.0f;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int kMaxK = 64;
+
+// Checks shared by the operators that use a sorted plan.  rows_used: tensors indexed by
+// row are touched.
+static int plan_check(const int32_t* row_of, const int32_t* pair_of, bool need_pairs, int64_t T,
+                      int32_t k, int64_t rows, int64_t H) {
+  if (T < 0 || k < 0 || rows < 0 || H < 0) return BSG_ERR_INVALID_ARG;
+  if (k > kMaxK || rows > kMaxDim - kSortThreads || (k > 0 && T > (kMaxDim - kSortThreads) / k) ||
+      T > kMaxDim - kSortThreads || H > (int64_t(1) << 28))
+    return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (T * k > 0 && !row_of) return BSG_ERR_INVALID_ARG;
+  if (need_pairs && rows > 0 && !pair_of) return BSG_ERR_INVALID_ARG;
+  if (((uintptr_t)row_of | (uintptr_t)pair_of) & 3) return BSG_ERR_MISALIGNED;
+  return BSG_OK;
+}
+
+// A bf16 matrix operand: present, rows of at least H elements, 2-byte aligned.
+static int mat_check(const void* p, int64_t ld, int64_t H) {
+  if (!p || ld < H) return BSG_ERR_INVALID_ARG;
+  if (ld > (int64_t(1) << 40)) return BSG_ERR_UNSUPPORTED_SHAPE;
+  return ((uintptr_t)p & 1) ? BSG_ERR_MISALIGNED : BSG_OK;
+}
+static bool vec8(const void* p, int64_t ld, int64_t H) {
+  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && H % 8 == 0;
+}
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace bsg_route
+
+using namespace bsg_route;
+
+extern "C" {
+
+int64_t sort_tokens_workspace(int64_t pairs, int32_t G) {
+  if (pairs <= kSingle || G <= 0) return 0;
+  return int64_t(4) * kMaxChunks * (G < kMaxGroups ? G : kMaxGroups);
+}
+
+int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_t G, int32_t align,
+                int32_t cap, int32_t* offsets, int32_t* row_of, int32_t* pair_of, int32_t* row_group,
+                int64_t rows, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (T < 0 || k < 0 || G < 0 || align < 1 || cap < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
+  if (cap > 0 && align != 1) return BSG_ERR_INVALID_ARG;
+  if (G > kMaxGroups) return BSG_ERR_UNSUPPORTED_SHAPE;
+  const int st = plan_check(row_of, pair_of, true, T, k, rows, 0);
+  if (st != BSG_OK) return st;
+  const int64_t n = T * k;
+  if (n > 0 && (!ids || ld_ids < k)) return BSG_ERR_INVALID_ARG;
+  if (!offsets && !(cap > 0 && G == 0)) return BSG_ERR_INVALID_ARG;
+  if (rows > 0 && !row_group) return BSG_ERR_INVALID_ARG;
+  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)row_group | (uintptr_t)workspace) & 3)
+    return BSG_ERR_MISALIGNED;
+  // every possible outcome must fit: all pairs in the groups that pad most
+  if (align > kMaxDim / (2 * kMaxGroups) || (cap > 0 && G > 0 && cap > kMaxDim / (2 * G)))
+    return BSG_ERR_UNSUPPORTED_SHAPE;
+  const int64_t need = cap > 0 ? (int64_t)G * cap
+                               : (G > 0 ? n + (G < n ? G : n) * (int64_t)(align - 1) : 0);
+  if (rows < need) return BSG_ERR_INVALID_ARG;
+  if (need > kMaxDim - kSortThreads) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < sort_tokens_workspace(n, G) || (sort_tokens_workspace(n, G) > 0 && !workspace))
+    return BSG_ERR_INVALID_ARG;
+  SortArgs a = {};
+  a.ids = ids;
+  a.ld_ids = ld_ids;
+  a.k = k > 0 ? k : 1;
+  a.n = (int32_t)n;
+  a.G = G;
+  a.align = align;
+  a.cap = cap;
+  a.offsets = offsets;
+  a.row_of = row_of;
+  a.pair_of = pair_of;
+  a.row_group = row_group;
+  a.rows = (int32_t)rows;
+  a.hist = (int32_t*)workspace;
+  const int64_t steps = ceil_div(n > 0 ? n : 1, kSortThreads);
+  const bool single = n <= kSingle || G == 0;
+  a.nchunks = single ? 1 : (int32_t)(steps < kMaxChunks ? steps : kMaxChunks);
+  a.chunk = (int32_t)(ceil_div(steps, a.nchunks) * kSortThreads);
+  a.nchunks = (int32_t)ceil_div(n > 0 ? n : 1, a.chunk);
+  (void)hipGetLastError();
+  if (a.nchunks > 1)
+    hipLaunchKernelGGL(sort_hist_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, (hipStream_t)stream, a);
+  hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, (hipStream_t)stream, a);
+  return launch_status();
+}
+
+int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                      int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo,
+                      void* stream) {
+  int st = plan_check(row_of, pair_of, true, T, k, rows, H);
+  if (st != BSG_OK || rows == 0 || H == 0) return st;
+  if (T > 0 && (st = mat_check(X, ldx, H)) != BSG_OK) return st;
+  if ((st = mat_check(out, ldo, H)) != BSG_OK) return st;
+  const bool v = vec8(X, ldx, H) && vec8(out, ldo, H);
+  const int64_t segs = ceil_div(H, v ? 512 : 64);
+  const int64_t tb = k > 0 ? ceil_div(T * segs, kWaves) : 0, blocks = tb + ceil_div(rows, kPadRows);
+  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(v ? dispatch_bf16_kernel<8> : dispatch_bf16_kernel<1>, dim3((unsigned)blocks),
+                     dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)X, ldx, row_of, pair_of,
+                     (int)T, k, (int)rows, (int)H, (uint16_t*)out, ldo, (int)segs, (int)tb);
+  return launch_status();
+}
+
+}  // extern "C"
+
+namespace bsg_route {
+
+template <int FMT>
+static int dispatch_quant(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                          int64_t T, int32_t k, int64_t rows, int64_t H, void* Q, int64_t ldq,
+                          int16_t* sf, int64_t ld_sf, int32_t rule, void* stream) {
+  constexpr int64_t GK = Fmt<FMT>::GK, per = FMT == FMT_E4M3 ? 1 : 2, qa = FMT == FMT_E4M3 ? 16 : 8;
+  int st = plan_check(row_of, pair_of, true, T, k, rows, H);
+  if (st != BSG_OK) return st;
+  if (rule != BSG_SCALE_CEIL && rule != BSG_SCALE_OCP_MX) return BSG_ERR_INVALID_ARG;
+  if (H % GK) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || H == 0) return BSG_OK;
+  if (T > 0 && (st = mat_check(X, ldx, H)) != BSG_OK) return st;
+  if (!Q || !sf || ldq < H / per || ld_sf < rows) return BSG_ERR_INVALID_ARG;
+  if (ldq > (int64_t(1) << 40) || ld_sf > (int64_t(1) << 40)) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && (((uintptr_t)X & 15) || ldx % 8)) return BSG_ERR_MISALIGNED;
+  if (((uintptr_t)Q & (qa - 1)) || ldq % qa || ((uintptr_t)sf & 1)) return BSG_ERR_MISALIGNED;
+  const int64_t segs = ceil_div(H, kQElems);
+  const int64_t tb = k > 0 ? ceil_div(T * segs, kWaves) : 0, blocks = tb + ceil_div(rows, kPadRows);
+  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((rule == BSG_SCALE_CEIL ? dispatch_quant_kernel<FMT, BSG_SCALE_CEIL>
+                                             : dispatch_quant_kernel<FMT, BSG_SCALE_OCP_MX>),
+                     dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream,
+                     (const uint16_t*)X, ldx, row_of, pair_of, (int)T, k, (int)rows, (int)H,
+                     (uint8_t*)Q, ldq, sf, ld_sf, (int)segs, (int)tb);
+  return launch_status();
+}
+
+}  // namespace bsg_route
+
+extern "C" {
+
+int moe_dispatch_fp8(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                     int64_t T, int32_t k, int64_t rows, int64_t H, void* Q, int64_t ldq, int16_t* sf,
+                     int64_t ld_sf, int32_t rule, void* stream) {
+  return dispatch_quant<FMT_E4M3>(X, ldx, row_of, pair_of, T, k, rows, H, Q, ldq, sf, ld_sf, rule, stream);
+}
+
+int moe_dispatch_fp4(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                     int64_t T, int32_t k, int64_t rows, int64_t H, void* Q, int64_t ldq, int16_t* sf,
+                     int64_t ld_sf, int32_t rule, void* stream) {
+  return dispatch_quant<FMT_E2M1>(X, ldx, row_of, pair_of, T, k, rows, H, Q, ldq, sf, ld_sf, rule, stream);
+}
+
+int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* W, int64_t ldw,
+                int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo, void* stream) {
+  int st = plan_check(row_of, nullptr, false, T, k, rows, H);
+  if (st != BSG_OK || T == 0 || H == 0) return st;
+  if (rows > 0 && (st = mat_check(Y, ldy, H)) != BSG_OK) return st;
+  if ((st = mat_check(out, ldo, H)) != BSG_OK) return st;
+  if (W && ldw < k) return BSG_ERR_INVALID_ARG;
+  if ((uintptr_t)W & 3) return BSG_ERR_MISALIGNED;
+  const bool v = (rows == 0 || vec8(Y, ldy, H)) && vec8(out, ldo, H);
+  const int64_t segs = ceil_div(H, v ? 512 : 64), blocks = ceil_div(T * segs, kWaves);
+  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(v ? combine_kernel<8> : combine_kernel<1>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                     (hipStream_t)stream, (const uint16_t*)Y, ldy, row_of, W, ldw, (int)T, k, (int)rows,
+                     (int)H, (uint16_t*)out, ldo, (int)segs);
+  return launch_status();
+}
+
+int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy, const int32_t* row_of,
+                         const int32_t* pair_of, const float* W, int64_t ldw, int64_t T, int32_t k,
+                         int64_t rows, int64_t H, void* dY, int64_t lddy, float* dW, int64_t lddw,
+                         void* stream) {
+  int st = plan_check(row_of, pair_of, true, T, k, rows, H);
+  if (st != BSG_OK) return st;
+  if ((W && ldw < k) || (dW && lddw < k)) return BSG_ERR_INVALID_ARG;
+  if (((uintptr_t)W | (uintptr_t)dW) & 3) return BSG_ERR_MISALIGNED;
+  if (H > 0 && T > 0 && (st = mat_check(dO, ldo, H)) != BSG_OK) return st;
+  if (H > 0 && rows > 0) {
+    if ((st = mat_check(dY, lddy, H)) != BSG_OK) return st;
+    if (dW && (st = mat_check(Y, ldy, H)) != BSG_OK) return st;
+  }
+  const bool v = (T == 0 || vec8(dO, ldo, H)) && (rows == 0 || vec8(dY, lddy, H)) &&
+                 (!dW || rows == 0 || vec8(Y, ldy, H));
+  const int64_t segs = ceil_div(H, v ? 512 : 64);
+  const int64_t tb = k > 0 ? T : 0, blocks = tb + ceil_div(rows, kPadRows);
+  if (blocks == 0) return BSG_OK;
+  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((v ? combine_backward_kernel<8, 4> : combine_backward_kernel<1, 4>),
+                     dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,
+                     ldo, (const uint16_t*)Y, ldy, row_of, pair_of, W, ldw, (int)tb, k, (int)rows, (int)H,
+                     (uint16_t*)dY, lddy, dW, lddw, (int)segs);
+  return launch_status();
+}
+
+}  // extern "C"

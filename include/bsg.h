@@ -12,7 +12,10 @@
  * read, quantises bf16 rows into that format (the producer side), runs the MoE
  * FFN core on one GPU's share (grouped up-projection with SwiGLU and FP8
  * requantisation fused into its epilogue, grouped down-projection), and computes
- * the MQA logits of a lightning-indexer step in FP8 and FP4.
+ * the MQA logits of a lightning-indexer step in FP8 and FP4.  Around the grouped
+ * products it sorts tokens by expert (or adapter), dispatches their rows, combines
+ * the experts' rows with the router's weights, gives the gradient of that, and adds
+ * low-rank adapters to a shared projection.
  *
  * The pages this follows list BF16, FP8 and FP4 dense GEMM plus grouped (MoE)
  * GEMM as the library's coverage ("DeepGEMM-Ascend cobre quantas operacoes no
@@ -375,6 +378,131 @@ int moe_ffn_fp8_noalloc(const void* A, int64_t lda, const int16_t* sfa, int64_t 
                         int64_t ld_sfw2, int64_t stride_sfw2,
                         const int32_t* group_offsets, int32_t G, int64_t M_total, int64_t hidden,
                         int64_t inter, void* D, int64_t ldd, int32_t rule, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows grouped by a device-side id.  A router (or a table of adapters) gives every
+ * token t of T a choice of k groups; pair p = t*k + j is token t's j-th choice.  A
+ * sorted plan places the pairs in the rows of a matrix, group after group, and
+ * connects both sides with four DEVICE int32 arrays:
+ *   offsets   [G+1]   contiguous layout: group g owns rows [offsets[g], offsets[g+1]),
+ *                     the group_offsets of the M-grouped GEMMs and moe_ffn_fp8;
+ *             [G]     masked layout: the number of pairs of group g, whose rows start
+ *                     at g*cap: the masked_m of m_grouped_gemm_fp8_masked;
+ *   row_of    [T*k]   the row of pair p, or -1 when the pair has none;
+ *   pair_of   [rows]  the pair in a row; -1: padding inside a group (a zero row); -2: a
+ *                     row of no group, which no operator here writes;
+ *   row_group [rows]  the group of a row that holds a pair, -1 elsewhere.
+ * The operators below take these arrays from sort_tokens or from the caller.  They
+ * check every index they read against the sizes given (T, k, rows, G) and skip it
+ * when it lies outside: broken arrays give wrong rows, never an access outside the
+ * operands.  Two pairs in one row would race.
+ * ------------------------------------------------------------------------- */
+
+/* Sort pairs by group.
+ *   ids: DEVICE int32 [T][ld_ids >= k]; a value outside [0, G) (an expert of another
+ *   GPU, a dropped choice, no adapter) leaves its pair without a row.
+ * The sort is stable: inside a group pairs keep the order of p, and the result is the
+ * same on every run.  A token may choose a group twice: two pairs, two rows.
+ *   cap == 0, contiguous: group g gets its pairs' count rounded up to a multiple of
+ *     align rows (an empty group none); the rows behind its pairs are padding (-1), the
+ *     rows from offsets[G] on belong to no group (-2).  Requires
+ *     rows >= T*k + min(G, T*k) * (align - 1), which every outcome fits in.
+ *   cap > 0, masked: group g gets the rows g*cap .. and keeps its first cap pairs;
+ *     later ones get no row.  The rest of its rows are -2.  Requires align == 1 and
+ *     rows >= G*cap.
+ *   All of offsets, row_of, pair_of and row_group (rows entries) are written, for any T
+ *   (T == 0 gives empty groups).
+ *   workspace: sort_tokens_workspace(T*k, G) bytes, 4-byte aligned (may be NULL when
+ *   that is 0); its contents need no initial value.  Calls that overlap need a
+ *   workspace each.
+ *   Requires G <= 1024, k <= 64, T*k and rows below 2^31 - 1024. */
+int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_t G, int32_t align,
+                int32_t cap, int32_t* offsets, int32_t* row_of, int32_t* pair_of, int32_t* row_group,
+                int64_t rows, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sort_tokens for that many pairs and groups. */
+int64_t sort_tokens_workspace(int64_t pairs, int32_t G);
+
+/* Dispatch tokens to their groups' rows, bf16:
+ *   out[row_of[t*k + j]] = X[t];  padding rows (pair_of == -1) are zeroed, rows of no
+ *   group (-2) are left as they were.
+ *   X: bf16 [T][ldx], out: bf16 [rows][ldo], H elements a row; any H, 2-byte aligned
+ *   (X and out 16-byte aligned with ldx, ldo and H multiples of 8 move 16 bytes at a
+ *   time).  X and out must not overlap.
+ *   The gradient with respect to X is moe_combine of the gradient of out, without
+ *   weights.  k <= 64, H <= 2^28. */
+int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                      int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo,
+                      void* stream);
+
+/* Dispatch with quantisation: each token's row is quantised once, to the codes and
+ * scale bytes of quantize_fp8_per_token / quantize_fp4_per_token (same rules, bit for
+ * bit; finite values), and written to its k rows, the packed scales straight into the
+ * layout the grouped GEMMs take as sfa:
+ *   Q: FP8: e4m3 [rows][ldq >= H] bytes;  FP4: e2m1 [rows][ldq >= H/2] bytes;
+ *   sf: packed int16 [ceil(H/256)][ld_sf >= rows] (FP8), [ceil(H/64)][..] (FP4).
+ *   Padding rows are a quantised zero row (codes 0, scale bytes 0); rows of no group
+ *   are left as they were, in Q and in sf.
+ *   Requires H % 128 == 0 (FP8), H % 32 == 0 (FP4); X 16-byte aligned with ldx % 8 == 0;
+ *   Q 16-byte (FP8) or 8-byte (FP4) aligned with ldq a multiple of that; sf 2-byte
+ *   aligned. */
+int moe_dispatch_fp8(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                     int64_t T, int32_t k, int64_t rows, int64_t H, void* Q, int64_t ldq, int16_t* sf,
+                     int64_t ld_sf, int32_t rule, void* stream);
+
+int moe_dispatch_fp4(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
+                     int64_t T, int32_t k, int64_t rows, int64_t H, void* Q, int64_t ldq, int16_t* sf,
+                     int64_t ld_sf, int32_t rule, void* stream);
+
+/* Combine the groups' rows back into tokens, with weights applied:
+ *   out[t] = bf16( sum_{j < k} W[t][j] * Y[row_of[t*k + j]] ),
+ * fp32 sums in the order of j, rounded once; a pair without a row adds nothing (whatever
+ * its weight holds), a token without any gives zeros.
+ *   Y: bf16 [rows][ldy]; W: fp32 [T][ldw >= k], NULL for weights of one (the gradient
+ *   of the dispatch); out: bf16 [T][ldo]; alignment as moe_dispatch_bf16.  out must not
+ *   overlap Y. */
+int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* W, int64_t ldw,
+                int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo, void* stream);
+
+/* Gradient of moe_combine, from dO, the gradient of its output (bf16 [T][ldo]):
+ *   dY[row_of[t*k + j]] = bf16( W[t][j] * dO[t] );  padding rows zeroed, rows of no
+ *                         group left as they were;
+ *   dW[t][j] = sum_h dO[t][h] * Y[row_of[t*k + j]][h]  (fp32; 0 for a pair without a
+ *              row), in an order that is the same on every run.
+ *   dW may be NULL (then Y is not read and may be NULL); W NULL means weights of one.
+ *   dY must not overlap dO or Y.  Alignment as moe_dispatch_bf16. */
+int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy, const int32_t* row_of,
+                         const int32_t* pair_of, const float* W, int64_t ldw, int64_t T, int32_t k,
+                         int64_t rows, int64_t H, void* dY, int64_t lddy, float* dW, int64_t lddw,
+                         void* stream);
+
+/* Low-rank adapters of many requests at once, beside a shared projection:
+ *   out[t] = bf16( base[t] + scale[g] * B_g (A_g x_t) ),  g = the adapter of token t,
+ *   out[t] = base[t] for a token without an adapter (row_of[t] < 0).
+ * A_g x_t is summed in fp32 and enters the second product with a relative error of at
+ * most 2^-16; the result is rounded once.
+ *   X: bf16 [T][ldx], K wide; A: bf16 [G][r][lda >= K], B: bf16 [G][N][ldb >= r] (expert
+ *   strides in elements; adapters of lower rank are padded with zero rows of A and
+ *   columns of B); scale: fp32 [G], or NULL for one.
+ *   base, out: bf16 [T][.. >= N]; base NULL counts as zeros; base == out adds in place
+ *   (rows of tokens without an adapter are then not touched), any other overlap of out
+ *   with an input is not allowed.
+ *   row_of, pair_of, row_group: the plan of sort_tokens over the adapters' ids (k = 1)
+ *   with an alignment that is a multiple of 16, so that the 16 rows of a tile belong to
+ *   one adapter (a plan that breaks this gives wrong rows).
+ *   workspace: lora_add_workspace(rows, K, r) bytes, 16-byte aligned, no initial value
+ *   needed; calls that overlap need one each.
+ *   Requires r % 8 == 0, r <= 128, K % 8 == 0, G <= 1024; X, A, B 16-byte aligned with
+ *   leading dimensions and strides multiples of 8; any N (base and out 16-byte aligned
+ *   with leading dimensions multiples of 8 move 16 bytes at a time). */
+int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
+                  int64_t ldb, int64_t stride_b, const float* scale, const int32_t* row_of,
+                  const int32_t* pair_of, const int32_t* row_group, int64_t rows, const void* base,
+                  int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
+                  int32_t r, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_add_bf16 for a plan of that many rows. */
+int64_t lora_add_workspace(int64_t rows, int64_t K, int32_t r);
 
 #ifdef __cplusplus
 }

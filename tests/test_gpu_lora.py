@@ -1,0 +1,172 @@
+"""GPU parity of lora_add_bf16 against the fp64 form of oracle/routing.py, whose bound on
+the error before the final rounding is derived there; the final rounding to bf16 adds at
+most 2^-8 of the value."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_05_amd as bsg
+from oracle import routing
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U8 = 2.0 ** -8
+
+
+def _say(msg):
+    print(f"[gpu-test] {msg}", flush=True)
+
+
+def _f64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def _case(T, G, K, N, r, seed, align=16, missing=0.2, pad=0):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(0, max(G, 1), (T, 1)).astype(np.int32)
+    ids[rng.random((T, 1)) < missing] = -1
+    if T > 4:
+        ids[4] = G                            # no such adapter
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def mat(*shape, ld=0, by=1.0):
+        x = by * torch.randn(*shape[:-1], shape[-1] + ld, generator=g, device=DEV)
+        return x.to(torch.bfloat16)[..., :shape[-1]]
+    ids = torch.from_numpy(ids).to(DEV)
+    plan = bsg.sort_tokens(ids, G, align=align)
+    X, base = mat(T, K, ld=8 * pad), mat(T, N, ld=pad)
+    A, B = mat(G, r, K, ld=8 * pad, by=0.125), mat(G, N, r, ld=8 * pad)
+    scale = torch.rand(G, generator=g, device=DEV) + 0.1
+    return ids, plan, X, A, B, scale, base
+
+
+def _check(out, X, A, B, ids, scale, base, what):
+    want, err = routing.lora(_f64(X), _f64(A), _f64(B), ids.cpu().numpy()[:, 0],
+                             None if scale is None else _f64(scale), None if base is None else _f64(base))
+    got = _f64(out)
+    tol = U8 * np.abs(want) + (1 + U8) * err
+    d = np.abs(got - want)
+    assert np.all(np.isfinite(got)) and np.all(d <= tol), f"{what}: {np.max(d - tol):.3e} over the bound"
+    _say(f"  {what}: {np.max(np.where(tol > 0, d / np.where(tol > 0, tol, 1), 0)):.2f} of the bound")
+
+
+CASES = [  # T, G, K, N, r, align
+    (1, 1, 8, 1, 8, 16), (1, 4, 7168, 2048, 8, 16), (5, 3, 40, 65, 24, 16), (64, 32, 1032, 512, 16, 16),
+    (33, 2, 520, 257, 40, 32), (130, 5, 2056, 384, 64, 16), (200, 3, 1024, 304, 128, 48),
+    (70, 100, 256, 1000, 32, 16), (17, 1, 64, 63, 104, 16), (300, 6, 4096, 129, 96, 128)]
+
+
+@pytest.mark.parametrize("T,G,K,N,r,align", CASES)
+def test_lora_matches_oracle(T, G, K, N, r, align):
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r} align={align}")
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T + K, align, missing=0.0 if T == 1 else 0.2)
+    out = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    _check(out, X, A, B, ids, scale, base, "base, scale")
+    none = plan.row_of[:, 0] < 0
+    assert torch.equal(out[none], base[none])
+    out = bsg.lora_add_bf16(X, A, B, plan)
+    _check(out, X, A, B, ids, None, None, "neither")
+    assert torch.all(out[none] == 0)
+    mine = base.clone()
+    assert bsg.lora_add_bf16(X, A, B, plan, scale, mine, out=mine) is mine
+    _check(mine, X, A, B, ids, scale, base, "in place")
+
+
+# rows enough for two and four tiles a workgroup: 512 and 1024 tiles of 16 rows
+@pytest.mark.parametrize("T,G,K,N,r", [(8000, 7, 128, 72, 16), (9000, 40, 64, 40, 64), (16300, 3, 136, 24, 8),
+                                       (15500, 90, 96, 33, 128), (16000, 1, 64, 64, 40)])
+def test_lora_many_tokens(T, G, K, N, r):
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r}")
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T)
+    _check(bsg.lora_add_bf16(X, A, B, plan, scale, base), X, A, B, ids, scale, base, "many tokens")
+
+
+def test_lora_strided_operands_and_workspace():
+    _say("lora_add with padded leading dimensions, unaligned base, a given workspace")
+    for pad in (8, 3):                        # 3: base rows not 16-byte aligned
+        ids, plan, X, A, B, scale, base = _case(90, 4, 264, 200, 16, 7, pad=pad)
+        rows = plan.pair_of.numel()
+        need = bsg.lib().lora_add_workspace(rows, 264, 16)
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)     # NaN as floats
+        buf = torch.full((90, 211), 3.0, dtype=torch.bfloat16, device=DEV)
+        out = bsg.lora_add_bf16(X, A, B, plan, scale, base, out=buf[:, :200], workspace=ws)
+        _check(out, X, A, B, ids, scale, base, f"pad {pad}")
+        assert torch.all(buf[:, 200:] == 3.0) and torch.all(ws[need:] == 255)
+
+
+def test_lora_rows_that_must_not_spread():
+    """A token full of NaN and an adapter full of infinities touch their own rows only."""
+    ids, plan, X, A, B, scale, base = _case(80, 4, 512, 128, 16, 3)
+    want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    t = int(torch.nonzero(ids[:, 0] == 1)[0])
+    X2, A2 = X.clone(), A.clone()
+    X2[t] = float("nan")
+    A2[2] = float("inf")
+    got = bsg.lora_add_bf16(X2, A2, B, plan, scale, base)
+    rest = (ids[:, 0] != 2) & (torch.arange(80, device=DEV) != t)
+    assert torch.equal(got[rest], want[rest])
+    assert torch.all(torch.isnan(got[t]))
+    # a token without an adapter is copied whatever X holds
+    none = torch.nonzero(plan.row_of[:, 0] < 0)[:, 0]
+    X2[none] = float("nan")
+    assert torch.equal(bsg.lora_add_bf16(X2, A2, B, plan, scale, base)[none], base[none])
+
+
+def test_lora_empty():
+    """No adapters, no tokens, nobody with an adapter, no columns, K = 0, rank 0."""
+    _say("lora_add empty cases")
+    e = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)
+    for T, G, K, N, r in ((0, 2, 64, 32, 8), (5, 0, 64, 32, 8), (5, 2, 64, 0, 8), (5, 2, 0, 32, 8),
+                          (5, 2, 64, 32, 0)):
+        ids = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+        plan = bsg.sort_tokens(ids, G, align=16)
+        out = bsg.lora_add_bf16(e(T, K), e(G, r, K), e(G, N, r), plan, base=e(T, N))
+        assert torch.equal(out, e(T, N)), (T, G, K, N, r)
+    plan = bsg.sort_tokens(torch.full((20, 1), -1, dtype=torch.int32, device=DEV), 2, align=16)
+    assert torch.equal(bsg.lora_add_bf16(e(20, 64), e(2, 8, 64), e(2, 32, 8), plan, base=e(20, 32)), e(20, 32))
+
+
+def test_lora_broken_plan_stays_in_bounds():
+    """Groups, pairs and rows out of range are skipped."""
+    ids, plan, X, A, B, scale, base = _case(64, 4, 128, 64, 16, 5, missing=0.0)
+    plan.row_group[:16] = 4
+    plan.row_group[16:32] = 2 ** 31 - 1
+    plan.pair_of[40:] = 2 ** 31 - 1
+    bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    torch.cuda.synchronize()
+
+
+def test_lora_beside_a_projection_captured_and_streamed():
+    """The operators as they are used: a shared projection, the sort and the adapters added in
+    place; run twice, on a side stream, and captured, then replayed on new requests with
+    eager calls in between."""
+    _say("gemm_bf16 + sort_tokens + lora_add: determinism, side stream, graph")
+    T, G, K, N, r = 96, 9, 512, 384, 16
+    ids, _, X, A, B, scale, _ = _case(T, G, K, N, r, 1)
+    Wt = torch.randn(N, K, device=DEV).to(torch.bfloat16)
+
+    def step(stream=None):
+        plan = bsg.sort_tokens(ids, G, align=16, stream=stream)
+        D = bsg.gemm_bf16(X, Wt, stream=stream)
+        return bsg.lora_add_bf16(X, A, B, plan, scale, D, out=D, stream=stream)
+
+    def done(D):
+        torch.cuda.synchronize()
+        return D.clone()
+    first = done(step())
+    _check(first, X, A, B, ids, scale, bsg.gemm_bf16(X, Wt), "beside gemm_bf16")
+    assert torch.equal(first, done(step()))
+    side = torch.cuda.Stream()
+    assert torch.equal(first, done(step(side)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    rng = np.random.default_rng(0)
+    for i in range(4):
+        ids.copy_(torch.from_numpy(rng.integers(-1, G, (T, 1)).astype(np.int32)))
+        X.copy_(torch.randn(T, K, device=DEV))
+        torch.cuda.synchronize()
+        graph.replay()
+        got = done(captured)
+        assert torch.equal(got, done(step()))

@@ -1,0 +1,135 @@
+"""Host-side checks of the operators on grouped rows that need no GPU: bad arguments are
+refused with the documented status before any HIP call, and the binding refuses wrong
+types, shapes and devices."""
+import pytest
+import torch
+
+import block_scaled_precision_05_amd as bsg
+
+INV, SHAPE, ALIGN, OK = (bsg.BSG_ERR_INVALID_ARG, bsg.BSG_ERR_UNSUPPORTED_SHAPE,
+                         bsg.BSG_ERR_MISALIGNED, bsg.BSG_OK)
+# fake, never-dereferenced device addresses: validation fails before any HIP call
+P, P2, P3, P4, P5 = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000
+
+
+def _try(f, good, changes):
+    """Each change ({index: value}, status) of the good arguments gives that status."""
+    for change, status in changes:
+        a = list(good)
+        for i, v in change.items():
+            a[i] = v
+        assert f(*a) == status, (change, status)
+
+
+def test_sort_refusals():
+    L = bsg.lib()
+    #       ids ld T    k  G  al cap off row pair grp rows ws bytes stream
+    good = [P, 4, 100, 4, 8, 16, 0, P2, P3, P4, P5, 520, 0, 0, None]
+    _try(L.sort_tokens, good, [
+        ({2: -1}, INV), ({3: -1}, INV), ({4: -1}, INV), ({5: 0}, INV), ({6: -1}, INV), ({11: -1}, INV),
+        ({1: 3}, INV),                        # ld_ids < k
+        ({0: 0}, INV), ({7: 0}, INV), ({8: 0}, INV), ({9: 0}, INV), ({10: 0}, INV),
+        ({11: 519}, INV),                     # 400 pairs + 8 * 15 padding rows
+        ({4: 1025}, SHAPE), ({3: 65, 1: 65}, SHAPE),
+        ({2: 1 << 31, 11: 1 << 40}, SHAPE), ({11: 1 << 31}, SHAPE),
+        ({5: 1 << 30}, SHAPE),
+        ({6: 8}, INV),                        # masked layout takes align 1
+        ({6: 100, 5: 1}, INV),                # 8 * 100 rows do not fit 520
+        ({6: 1 << 30, 5: 1}, SHAPE),
+        ({0: P + 2}, ALIGN), ({7: P2 + 1}, ALIGN), ({8: P3 + 2}, ALIGN), ({9: P4 + 2}, ALIGN),
+        ({10: P5 + 2}, ALIGN),
+    ])
+    # many pairs need a workspace
+    assert L.sort_tokens_workspace(400, 8) == 0
+    need = L.sort_tokens_workspace(40000, 8)
+    assert need > 0
+    big = list(good)
+    big[2], big[11] = 10000, 40120
+    _try(L.sort_tokens, big, [({}, INV), ({12: P, 13: need - 1}, INV), ({12: 0, 13: need}, INV),
+                              ({12: P + 1, 13: need}, ALIGN)])
+
+
+def test_dispatch_refusals():
+    L = bsg.lib()
+    #       X  ldx  row pair T   k  rows H    out ldo stream
+    good = [P, 256, P2, P3, 100, 4, 500, 256, P4, 256, None]
+    _try(L.moe_dispatch_bf16, good, [
+        ({4: -1}, INV), ({5: -1}, INV), ({6: -1}, INV), ({7: -1}, INV),
+        ({0: 0}, INV), ({2: 0}, INV), ({3: 0}, INV), ({8: 0}, INV), ({1: 255}, INV), ({9: 255}, INV),
+        ({5: 65}, SHAPE), ({6: 1 << 31}, SHAPE), ({7: 1 << 29, 1: 1 << 29, 9: 1 << 29}, SHAPE),
+        ({4: 1 << 30}, SHAPE), ({0: P + 1}, ALIGN), ({8: P4 + 1}, ALIGN), ({2: P2 + 2}, ALIGN),
+        ({6: 0}, OK), ({7: 0}, OK),           # nothing to write
+    ])
+    for name, H in (("moe_dispatch_fp8", 256), ("moe_dispatch_fp4", 256)):
+        per = 1 if name.endswith("fp8") else 2
+        #       X  ldx  row pair T   k  rows H  Q   ldq      sf  ld_sf rule stream
+        good = [P, 256, P2, P3, 100, 4, 500, H, P4, H // per, P5, 500, 0, None]
+        _try(getattr(L, name), good, [
+            ({4: -1}, INV), ({0: 0}, INV), ({8: 0}, INV), ({10: 0}, INV), ({12: 2}, INV),
+            ({9: H // per - 1}, INV), ({11: 499}, INV), ({1: 248}, INV),
+            ({7: 240}, SHAPE), ({5: 65}, SHAPE),
+            ({0: P + 8}, ALIGN), ({1: 260}, ALIGN), ({8: P4 + 4}, ALIGN), ({9: H // per + 4}, ALIGN),
+            ({10: P5 + 1}, ALIGN), ({6: 0}, OK), ({7: 0}, OK),
+        ])
+
+
+def test_combine_refusals():
+    L = bsg.lib()
+    #       Y  ldy  row W  ldw T   k  rows H    out ldo stream
+    good = [P, 256, P2, P3, 4, 100, 4, 500, 256, P4, 256, None]
+    _try(L.moe_combine, good, [
+        ({5: -1}, INV), ({6: -1}, INV), ({7: -1}, INV), ({8: -1}, INV),
+        ({0: 0}, INV), ({2: 0}, INV), ({9: 0}, INV), ({1: 255}, INV), ({10: 255}, INV), ({4: 3}, INV),
+        ({6: 65}, SHAPE), ({0: P + 1}, ALIGN), ({3: P3 + 2}, ALIGN), ({9: P4 + 1}, ALIGN),
+        ({5: 0}, OK), ({8: 0}, OK),
+    ])
+    #       dO ldo  Y  ldy  row pair W  ldw T   k  rows H    dY  lddy dW  lddw stream
+    good = [P, 256, P, 256, P2, P3, P4, 4, 100, 4, 500, 256, P5, 256, P2, 4, None]
+    _try(L.moe_combine_backward, good, [
+        ({8: -1}, INV), ({9: -1}, INV), ({10: -1}, INV), ({11: -1}, INV),
+        ({0: 0}, INV), ({2: 0}, INV), ({4: 0}, INV), ({5: 0}, INV), ({12: 0}, INV),
+        ({1: 255}, INV), ({3: 255}, INV), ({13: 255}, INV), ({7: 3}, INV), ({15: 3}, INV),
+        ({9: 65}, SHAPE), ({0: P + 1}, ALIGN), ({12: P5 + 1}, ALIGN), ({14: P2 + 2}, ALIGN),
+        ({6: P4 + 1}, ALIGN), ({8: 0, 10: 0}, OK),
+    ])
+
+
+def test_lora_refusals():
+    L = bsg.lib()
+    need = L.lora_add_workspace(256, 512, 16)
+    assert need >= 256 * 16 * 4 and L.lora_add_workspace(0, 512, 16) == 0
+    #   0  1    2  3    4         5  6   7         8  9   10  11  12   13  14   15   16   17   18 19   20
+    #   X  ldx  A  lda  stride_a  B  ldb stride_b  s  row pr  grp rows bs  ldb  out  ldo  T    G  N    K
+    good = [P, 512, P, 512, 16 * 512, P, 16, 256 * 16, P2, P2, P3, P4, 256, P5, 256, 0x90000, 256, 100, 4,
+            256, 512, 16, 0x80000, need, None]
+    _try(L.lora_add_bf16, good, [
+        ({17: -1}, INV), ({18: -1}, INV), ({19: -1}, INV), ({20: -1}, INV), ({21: -1}, INV), ({12: -1}, INV),
+        ({0: 0}, INV), ({2: 0}, INV), ({5: 0}, INV), ({9: 0}, INV), ({10: 0}, INV), ({11: 0}, INV),
+        ({15: 0}, INV), ({1: 504}, INV), ({3: 504}, INV), ({6: 8}, INV), ({14: 255}, INV), ({16: 255}, INV),
+        ({4: 16 * 512 - 8}, INV), ({7: 256 * 16 - 8}, INV),
+        ({22: 0}, INV), ({23: need - 1}, INV),
+        ({15: P5, 16: 264}, INV),             # in place with another leading dimension
+        ({21: 12}, SHAPE), ({21: 136, 6: 136}, SHAPE), ({20: 508}, SHAPE), ({18: 1025}, SHAPE),
+        ({0: P + 8}, ALIGN), ({2: P + 2}, ALIGN), ({5: P + 8}, ALIGN), ({1: 516}, ALIGN), ({3: 516, 4: 16 * 516}, ALIGN),
+        ({6: 20, 7: 256 * 24}, ALIGN), ({22: 0x80008}, ALIGN), ({15: 0x90001}, ALIGN), ({13: P5 + 1}, ALIGN),
+        ({8: P2 + 2}, ALIGN),
+        ({17: 0}, OK), ({19: 0}, OK),
+    ])
+
+
+def _plan(T=4, k=2, rows=8):
+    e = lambda *s: torch.zeros(s, dtype=torch.int32)
+    return bsg.TokenSort(e(3), e(T, k), e(rows), e(rows))
+
+
+def test_binding_refuses_host_tensors():
+    X = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        bsg.sort_tokens(torch.zeros(4, 2, dtype=torch.int32), 2)
+    for f in (bsg.moe_dispatch_bf16, bsg.moe_dispatch_fp8, bsg.moe_dispatch_fp4, bsg.moe_combine):
+        with pytest.raises(ValueError):
+            f(X, _plan())
+    with pytest.raises(ValueError):
+        bsg.moe_combine_backward(X, X, _plan())
+    with pytest.raises(ValueError):
+        bsg.lora_add_bf16(X, X[None], X[None], _plan(k=1))
