@@ -598,46 +598,49 @@ def mqa_logits(fmt: str, Q, sfq, K, sfk, W, ks, ke, S: int, q_per_group: int | N
     return out
 
 
-class _Place:
-    """Device and stream of a call: makes the operands' device current (launches and
-    allocations go there) and, for a stream other than the device's current one, makes
-    that current too, so that buffers allocated for the call belong to it."""
-
-    __slots__ = ("device", "stream", "handle")
-
-    def __init__(self, t: torch.Tensor, stream):
-        index = t.device.index
-        self.device = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-        self.stream = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(index).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-            elif stream.device != t.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-            self.stream = torch.cuda.stream(stream)
-            self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+# The calls below are short (a decode step's combine runs 4 us on the GPU), so their
+# host side is kept short too: checks that pass cost a few attribute reads.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _one_device(first, *ts):
-    _dev(first, *ts)
+def _launch(t, stream, body):
+    """body(stream handle) with t's device current (launches and allocations go there) and,
+    for a stream given by the caller, with that stream current, so that buffers allocated
+    for the call belong to it."""
+    index = t.get_device()
+    if stream is None:
+        if index == _current_device():
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _one_gpu(first, *ts):
+    index = first.get_device()
     for t in ts:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must live on the same GPU")
+    if index < 0:
+        raise ValueError("all tensors must live on the GPU")
+
+
+def _ld(t, name, dtype, rows, cols):
+    """Leading dimension of a [rows, cols] tensor of that type with contiguous rows."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    ld, step = t.stride()
+    if step == 1 and ld >= cols:
+        return ld
+    return _mat(t, name)
 
 
 class TokenSort(NamedTuple):
@@ -655,64 +658,73 @@ def sort_tokens(ids, G: int, align: int = 1, cap: int = 0, out: TokenSort | None
     to a multiple of ``align`` rows and plan.offsets are the M-grouped GEMMs' offsets;
     masked layout (cap > 0): group g owns rows g*cap .., keeps its first cap pairs, and
     plan.offsets are the masked GEMM's counts.  ``out`` may pass a plan's four tensors
-    (rows at least T*k + min(G, T*k)*(align-1), or G*cap), ``workspace`` an int32 tensor
-    of at least sort_tokens_workspace(T*k, G) bytes."""
-    _dev(ids)
+    (rows at least T*k + min(G, T*k)*(align-1), or G*cap), ``workspace`` a contiguous
+    tensor of at least sort_tokens_workspace(T*k, G) bytes."""
     if ids.dtype != torch.int32 or ids.dim() != 2:
         raise TypeError("ids must be an int32 tensor [T, k]")
     T, k = ids.shape
+    ld = _ld(ids, "ids", torch.int32, T, k)
     n = T * k
     if align < 1 or cap < 0 or G < 0:
         raise ValueError("align must be at least 1, cap and G not negative")
-    rows = G * cap if cap else (n + min(G, n) * (align - 1) if G else 0)
-    need = lib().sort_tokens_workspace(n, G)
-    with _Place(ids, stream) as st:
-        if out is None:
-            e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
-            plan = TokenSort(e(G if cap else G + 1), e(T, k), e(rows), e(rows))
-        else:
-            plan = TokenSort(*out)
-            _one_device(ids, *plan)
-            for t in plan:
-                if t.dtype != torch.int32 or not t.is_contiguous():
-                    raise TypeError("out must hold contiguous int32 tensors")
-            rows = plan.pair_of.numel()
-            if plan.offsets.numel() != (G if cap else G + 1) or plan.row_of.shape != ids.shape or \
-                    plan.row_group.numel() != rows:
-                raise ValueError("out must hold offsets [G+1] (masked: [G]), row_of [T, k] and "
-                                 "pair_of, row_group [rows]")
-        if workspace is None and need:
-            workspace = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
-        if workspace is not None:
-            _one_device(ids, workspace)
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check("sort_tokens", lib().sort_tokens(
-            _ptr(ids), _mat(ids, "ids"), T, k, G, align, cap, _ptr(plan.offsets),
-            _ptr(plan.row_of), _ptr(plan.pair_of), _ptr(plan.row_group), rows, _ptr(workspace),
-            size, st))
-    return plan
+    heads = G if cap else G + 1
+    if out is None:
+        rows = G * cap if cap else (n + min(G, n) * (align - 1) if G else 0)
+        _one_gpu(ids, workspace)
+    else:
+        out = TokenSort(*out)
+        _one_gpu(ids, workspace, *out)
+        rows = out.pair_of.numel()
+        for t in out:
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise TypeError("out must hold contiguous int32 tensors")
+        if out.offsets.numel() != heads or out.row_of.shape != ids.shape or \
+                out.row_group.numel() != rows:
+            raise ValueError("out must hold offsets [G+1] (masked: [G]), row_of [T, k] and "
+                             "pair_of, row_group [rows]")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    L = lib()
+
+    def body(st):
+        plan, ws, size = out, workspace, 0
+        if plan is None:
+            # one allocation, cut into the plan's four tensors
+            o, r, p, g = torch.empty(heads + n + 2 * rows, dtype=torch.int32,
+                                     device=ids.device).split_with_sizes((heads, n, rows, rows))
+            plan = TokenSort(o, r.view(T, k), p, g)
+        if ws is None:
+            need = L.sort_tokens_workspace(n, G)
+            if need:
+                ws = torch.empty(need // 4, dtype=torch.int32, device=ids.device)
+        if ws is not None:
+            size = ws.numel() * ws.element_size()
+        _check("sort_tokens", L.sort_tokens(
+            ids.data_ptr(), ld, T, k, G, align, cap, plan[0].data_ptr(), plan[1].data_ptr(),
+            plan[2].data_ptr(), plan[3].data_ptr(), rows, _ptr(ws), size, st))
+        return plan
+    return _launch(ids, stream, body)
 
 
 def _plan(plan, *ts):
-    """The plan's row_of, pair_of and row_group, checked against the other operands' device."""
+    """A plan's row_of, pair_of and row_group, T, k and rows, checked against the other
+    operands' device."""
     offsets, row_of, pair_of, row_group = plan
-    _one_device(row_of, pair_of, row_group, *ts)
+    _one_gpu(row_of, pair_of, row_group, *ts)
     for t in (row_of, pair_of, row_group):
         if t.dtype != torch.int32 or not t.is_contiguous():
             raise TypeError("the plan must hold contiguous int32 tensors")
-    if row_of.dim() != 2 or pair_of.dim() != 1 or row_group.shape != pair_of.shape:
+    rows = pair_of.numel()
+    if row_of.dim() != 2 or pair_of.dim() != 1 or row_group.numel() != rows:
         raise ValueError("the plan must hold row_of [T, k] and pair_of, row_group [rows]")
-    return row_of, pair_of, row_group
+    T, k = row_of.shape
+    return row_of, pair_of, row_group, T, k, rows
 
 
-def _bf16(t, name, rows, cols):
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    return _mat(t, name)
+def _width(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {list(t.shape)}")
+    return t.shape[1]
 
 
 def moe_dispatch_bf16(X, plan, out=None, stream=None):
@@ -720,49 +732,44 @@ def moe_dispatch_bf16(X, plan, out=None, stream=None):
     rows are zero and rows of no group (pair_of -2) keep what ``out`` held (they are
     uninitialised in a tensor allocated here).  The gradient with respect to X is
     moe_combine(gradient, plan)."""
-    row_of, pair_of, _ = _plan(plan, X, out)
-    T, k = row_of.shape
-    rows = pair_of.numel()
-    if X.dim() != 2:
-        raise ValueError("X must be [T, H]")
-    H = X.shape[1]
-    ldx = _bf16(X, "X", T, H)
-    with _Place(X, stream) as st:
-        if out is None:
-            out = torch.empty((rows, H), dtype=torch.bfloat16, device=X.device)
-        ldo = _bf16(out, "out", rows, H)
+    row_of, pair_of, _, T, k, rows = _plan(plan, X, out)
+    H = _width(X, "X")
+    ldx = _ld(X, "X", torch.bfloat16, T, H)
+    ldo = H if out is None else _ld(out, "out", torch.bfloat16, rows, H)
+
+    def body(st):
+        D = torch.empty((rows, H), dtype=torch.bfloat16, device=X.device) if out is None else out
         _check("moe_dispatch_bf16", lib().moe_dispatch_bf16(
-            _ptr(X), ldx, _ptr(row_of), _ptr(pair_of), T, k, rows, H, _ptr(out), ldo, st))
-    return out
+            X.data_ptr(), ldx, row_of.data_ptr(), pair_of.data_ptr(), T, k, rows, H,
+            D.data_ptr(), ldo, st))
+        return D
+    return _launch(X, stream, body)
 
 
 def _dispatch_quant(fn, X, plan, rule, per, gk, out, sf_out, stream):
-    row_of, pair_of, _ = _plan(plan, X, out, sf_out)
-    T, k = row_of.shape
-    rows = pair_of.numel()
-    if X.dim() != 2:
-        raise ValueError("X must be [T, H]")
-    H = X.shape[1]
-    ldx = _bf16(X, "X", T, H)
+    row_of, pair_of, _, T, k, rows = _plan(plan, X, out, sf_out)
+    H = _width(X, "X")
+    ldx = _ld(X, "X", torch.bfloat16, T, H)
     if rule not in SCALE_RULES:
         raise ValueError(f"rule must be one of {sorted(SCALE_RULES)}")
     kp = (H // gk + 1) // 2
-    with _Place(X, stream) as st:
-        if out is None:
-            Q = torch.empty((rows, H // per), dtype=torch.uint8, device=X.device)
-        else:
-            Q = _bytes_u8(out)
-            if Q.element_size() != 1 or Q.dim() != 2 or Q.shape[0] != rows or Q.shape[1] != H // per:
-                raise ValueError(f"out must hold the codes of [{rows}, {H // per}] bytes")
-        if sf_out is None:
-            sf_out = torch.empty((kp, rows), dtype=torch.int16, device=X.device)
+    ldq, ld_sf = H // per, rows
+    if out is not None:
+        out = _bytes_u8(out)
+        ldq = _ld(out, "out", torch.uint8, rows, H // per)
+    if sf_out is not None:
         ld_sf = _packed(sf_out, "sf_out")
         if sf_out.shape[0] != kp or sf_out.shape[1] < rows:
             raise ValueError(f"sf_out must be packed int16 [{kp}, >={rows}]")
+
+    def body(st):
+        Q = torch.empty((rows, ldq), dtype=torch.uint8, device=X.device) if out is None else out
+        P = torch.empty((kp, rows), dtype=torch.int16, device=X.device) if sf_out is None else sf_out
         _check(fn, getattr(lib(), fn)(
-            _ptr(X), ldx, _ptr(row_of), _ptr(pair_of), T, k, rows, H, _ptr(Q), _mat(Q, "out"),
-            _ptr(sf_out), ld_sf, SCALE_RULES[rule], st))
-    return Q, sf_out
+            X.data_ptr(), ldx, row_of.data_ptr(), pair_of.data_ptr(), T, k, rows, H,
+            Q.data_ptr(), ldq, P.data_ptr(), ld_sf, SCALE_RULES[rule], st))
+        return Q, P
+    return _launch(X, stream, body)
 
 
 def moe_dispatch_fp8(X, plan, rule: str = "ceil", out=None, sf_out=None, stream=None):
@@ -779,35 +786,23 @@ def moe_dispatch_fp4(X, plan, rule: str = "ceil", out=None, sf_out=None, stream=
     return _dispatch_quant("moe_dispatch_fp4", X, plan, rule, 2, 32, out, sf_out, stream)
 
 
-def _weights(W, T, k, name):
-    if W is None:
-        return 0
-    if W.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32")
-    if W.dim() != 2 or W.shape[0] != T or W.shape[1] != k:
-        raise ValueError(f"{name} must be [{T}, {k}], got {list(W.shape)}")
-    return _mat(W, name)
-
-
 def moe_combine(Y, plan, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * Y[plan.row_of[t, j]] (bf16 [T, H], fp32 sums, rounded
     once); weights float32 [T, k], or None for ones (the gradient of the dispatch).  A
     pair without a row adds nothing."""
-    row_of, pair_of, _ = _plan(plan, Y, weights, out)
-    T, k = row_of.shape
-    rows = pair_of.numel()
-    if Y.dim() != 2:
-        raise ValueError("Y must be [rows, H]")
-    H = Y.shape[1]
-    ldy = _bf16(Y, "Y", rows, H)
-    ldw = _weights(weights, T, k, "weights")
-    with _Place(Y, stream) as st:
-        if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=Y.device)
-        ldo = _bf16(out, "out", T, H)
+    row_of, _, _, T, k, rows = _plan(plan, Y, weights, out)
+    H = _width(Y, "Y")
+    ldy = _ld(Y, "Y", torch.bfloat16, rows, H)
+    ldw = k if weights is None else _ld(weights, "weights", torch.float32, T, k)
+    ldo = H if out is None else _ld(out, "out", torch.bfloat16, T, H)
+
+    def body(st):
+        D = torch.empty((T, H), dtype=torch.bfloat16, device=Y.device) if out is None else out
         _check("moe_combine", lib().moe_combine(
-            _ptr(Y), ldy, _ptr(row_of), _ptr(weights), ldw, T, k, rows, H, _ptr(out), ldo, st))
-    return out
+            Y.data_ptr(), ldy, row_of.data_ptr(), _ptr(weights), ldw, T, k, rows, H,
+            D.data_ptr(), ldo, st))
+        return D
+    return _launch(Y, stream, body)
 
 
 def moe_combine_backward(dout, Y, plan, weights=None, need_weights: bool = True, out=None,
@@ -815,25 +810,23 @@ def moe_combine_backward(dout, Y, plan, weights=None, need_weights: bool = True,
     """Gradients of moe_combine: (dY bf16 [rows, H], dW float32 [T, k]) from dout bf16
     [T, H].  Padding rows of dY are zero, rows of no group keep what ``out`` held.  With
     need_weights False dW is None and Y is not read (it may be None)."""
-    row_of, pair_of, _ = _plan(plan, dout, Y, weights, out)
-    T, k = row_of.shape
-    rows = pair_of.numel()
-    if dout.dim() != 2:
-        raise ValueError("dout must be [T, H]")
-    H = dout.shape[1]
-    ldd = _bf16(dout, "dout", T, H)
+    row_of, pair_of, _, T, k, rows = _plan(plan, dout, Y, weights, out)
+    H = _width(dout, "dout")
+    ldd = _ld(dout, "dout", torch.bfloat16, T, H)
     if need_weights and Y is None:
         raise ValueError("the weights' gradient needs Y")
-    ldy = 0 if Y is None else _bf16(Y, "Y", rows, H)
-    ldw = _weights(weights, T, k, "weights")
-    with _Place(dout, stream) as st:
-        if out is None:
-            out = torch.empty((rows, H), dtype=torch.bfloat16, device=dout.device)
+    ldy = 0 if Y is None else _ld(Y, "Y", torch.bfloat16, rows, H)
+    ldw = k if weights is None else _ld(weights, "weights", torch.float32, T, k)
+    ldo = H if out is None else _ld(out, "out", torch.bfloat16, rows, H)
+
+    def body(st):
+        dY = torch.empty((rows, H), dtype=torch.bfloat16, device=dout.device) if out is None else out
         dW = torch.empty((T, k), dtype=torch.float32, device=dout.device) if need_weights else None
         _check("moe_combine_backward", lib().moe_combine_backward(
-            _ptr(dout), ldd, _ptr(Y), ldy, _ptr(row_of), _ptr(pair_of), _ptr(weights), ldw, T, k,
-            rows, H, _ptr(out), _bf16(out, "out", rows, H), _ptr(dW), k, st))
-    return out, dW
+            dout.data_ptr(), ldd, _ptr(Y), ldy, row_of.data_ptr(), pair_of.data_ptr(),
+            _ptr(weights), ldw, T, k, rows, H, dY.data_ptr(), ldo, _ptr(dW), k, st))
+        return dY, dW
+    return _launch(dout, stream, body)
 
 
 def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None, stream=None):
@@ -842,39 +835,40 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     of 8, at most 128; lower ranks padded with zeros); plan of sort_tokens(ids [T, 1], G,
     align) with align a multiple of 16; scale float32 [G] or None; base bf16 [T, N] or
     None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
-    aligned tensor of at least lora_add_workspace(rows, K, r) bytes."""
-    row_of, pair_of, row_group = _plan(plan, X, A, B, scale, base, out, workspace)
-    T, k = row_of.shape
-    rows = pair_of.numel()
+    aligned contiguous tensor of at least lora_add_workspace(rows, K, r) bytes."""
+    row_of, pair_of, row_group, T, k, rows = _plan(plan, X, A, B, scale, base, out, workspace)
     if k != 1:
         raise ValueError("a token takes one adapter: the plan must come from ids [T, 1]")
-    if A.dim() != 3 or B.dim() != 3 or X.dim() != 2:
-        raise ValueError("X must be [T, K], A [G, r, K] and B [G, N, r]")
-    G, r, K = A.shape
-    N = B.shape[1]
-    if B.shape[0] != G or B.shape[2] != r:
-        raise ValueError("A and B disagree on the adapters or the rank")
     if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
         raise TypeError("A and B must be bfloat16")
-    if (K > 1 and A.stride(2) != 1) or (r > 1 and B.stride(2) != 1):
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [G, r, K] and B [G, N, r]")
+    G, r, K = A.shape
+    N = B.shape[1]
+    if B.shape != (G, N, r):
+        raise ValueError("A and B disagree on the adapters or the rank")
+    sa, sb = A.stride(), B.stride()
+    if (K > 1 and sa[2] != 1) or (r > 1 and sb[2] != 1):
         raise ValueError("A and B must be contiguous along their last dimension")
-    ldx = _bf16(X, "X", T, K)
-    ld_base = 0 if base is None else _bf16(base, "base", T, N)
-    if scale is not None and (scale.dtype != torch.float32 or scale.dim() != 1 or
-                              scale.numel() != G or not scale.is_contiguous()):
+    ldx = _ld(X, "X", torch.bfloat16, T, K)
+    ld_base = 0 if base is None else _ld(base, "base", torch.bfloat16, T, N)
+    ldo = N if out is None else _ld(out, "out", torch.bfloat16, T, N)
+    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (G,) or
+                              not scale.is_contiguous()):
         raise TypeError("scale must be a contiguous float32 vector [G]")
-    need = lib().lora_add_workspace(rows, K, r)
-    with _Place(X, stream) as st:
-        if out is None:
-            out = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
-        ldo = _bf16(out, "out", T, N)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        _check("lora_add_bf16", lib().lora_add_bf16(
-            _ptr(X), ldx, _ptr(A), A.stride(1), A.stride(0), _ptr(B), B.stride(1), B.stride(0),
-            _ptr(scale), _ptr(row_of), _ptr(pair_of), _ptr(row_group), rows, _ptr(base), ld_base,
-            _ptr(out), ldo, T, G, N, K, r, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), st))
-    return out
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    L = lib()
+
+    def body(st):
+        D = torch.empty((T, N), dtype=torch.bfloat16, device=X.device) if out is None else out
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(L.lora_add_workspace(rows, K, r), dtype=torch.uint8, device=X.device)
+        _check("lora_add_bf16", L.lora_add_bf16(
+            X.data_ptr(), ldx, A.data_ptr(), sa[1], sa[0], B.data_ptr(), sb[1], sb[0],
+            _ptr(scale), row_of.data_ptr(), pair_of.data_ptr(), row_group.data_ptr(), rows,
+            _ptr(base), ld_base, D.data_ptr(), ldo, T, G, N, K, r, ws.data_ptr(),
+            ws.numel() * ws.element_size(), st))
+        return D
+    return _launch(X, stream, body)
