@@ -103,7 +103,7 @@ EXPORTS = {
 # functions that return a number of bytes, not a status
 SIZES = {
     "sort_tokens_workspace": [_i64, _i32],
-    "lora_add_workspace": [_i64, _i64, _i32],
+    "lora_add_workspace": [_i64, _i64, _i32, _i64, _i64, _i32],
 }
 
 
@@ -835,7 +835,7 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     of 8, at most 128; lower ranks padded with zeros); plan of sort_tokens(ids [T, 1], G,
     align) with align a multiple of 16; scale float32 [G] or None; base bf16 [T, N] or
     None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
-    aligned contiguous tensor of at least lora_add_workspace(rows, K, r) bytes."""
+    aligned contiguous tensor of at least lora_add_workspace(T, rows, G, N, K, r) bytes."""
     row_of, pair_of, row_group, T, k, rows = _plan(plan, X, A, B, scale, base, out, workspace)
     if k != 1:
         raise ValueError("a token takes one adapter: the plan must come from ids [T, 1]")
@@ -862,13 +862,16 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
 
     def body(st):
         D = torch.empty((T, N), dtype=torch.bfloat16, device=X.device) if out is None else out
-        ws = workspace
+        ws, size = workspace, 0
         if ws is None:
-            ws = torch.empty(L.lora_add_workspace(rows, K, r), dtype=torch.uint8, device=X.device)
+            need = L.lora_add_workspace(T, rows, G, N, K, r)
+            if need:
+                ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+        if ws is not None:
+            size = ws.numel() * ws.element_size()
         _check("lora_add_bf16", L.lora_add_bf16(
             X.data_ptr(), ldx, A.data_ptr(), sa[1], sa[0], B.data_ptr(), sb[1], sb[0],
             _ptr(scale), row_of.data_ptr(), pair_of.data_ptr(), row_group.data_ptr(), rows,
-            _ptr(base), ld_base, D.data_ptr(), ldo, T, G, N, K, r, ws.data_ptr(),
-            ws.numel() * ws.element_size(), st))
+            _ptr(base), ld_base, D.data_ptr(), ldo, T, G, N, K, r, _ptr(ws), size, st))
         return D
     return _launch(X, stream, body)

@@ -6,17 +6,16 @@
 // 16), so that 16 consecutive rows of the plan, a tile, belong to one adapter.  The
 // rows of X, base and out stay where they are: a tile gathers its 16 tokens.
 //
-// Two launches.  shrink: U[row][r] = A_g x in fp32, the long sum over K split over the
-// waves of a workgroup and, when there are few tiles, over S workgroups whose partial
-// sums go to S slabs of U.  expand: out = base + s_g B_g U, the S slabs added in order.
-// Both are bound by memory (an adapter of rank r does r multiply-adds per element of
-// X and of out, far under the matrix cores' rate), so operands go straight from global
-// memory to MFMA fragments (v_mfma_f32_16x16x32_bf16: 16 rows of A_g or B_g against 16
-// tokens) and the tiles are shaped to touch X, base and out once: several token tiles
-// of one adapter share each fragment of A_g or B_g.
+// An adapter of rank r does r multiply-adds per element of X and of out, far under the
+// matrix cores' rate: the work is bound by memory, and for few tokens by latency.  So
+// operands go straight from global memory to MFMA fragments (v_mfma_f32_16x16x32_bf16:
+// 16 rows of A_g or B_g against 16 tokens), X, base and out are touched once, and the
+// adapters come from L2 (consecutive tiles, which mostly share an adapter, run on one
+// XCD).
 //
-// U keeps fp32 precision through the second product: it enters as two bf16 terms, U =
-// hi + lo with lo = bf16(U - hi), two MFMAs, a relative error of at most 2^-16.
+// U = s_g A_g x is summed in fp32 and keeps that precision through the second product:
+// it enters as two bf16 terms, U = hi + lo with lo = bf16(U - hi), two MFMAs, a relative
+// error of at most 2^-16.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,9 +27,8 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
 constexpr int kTile = 16;      // rows of the plan per MFMA tile
 
 struct LoraArgs {
@@ -48,16 +46,26 @@ struct LoraArgs {
   int64_t ld_base;
   uint16_t* out;
   int64_t ldo;
-  float* U;               // [S][tiles*16][r]
+  float* U;               // two launches: [S][tiles*16][r]
+  __bf16* UW;             // many tokens: [tiles*16][hi, lo][rank padded to 32]
   int32_t T, G, K, N, r, rows, tiles, S;
-  int32_t units;          // 64-element units of K
+  int32_t k_per;          // elements of K per slice, a multiple of 64
   int32_t plain;          // K, r or G is 0: no token has anything to add
-  int32_t row_blocks;     // workgroups (x) that hold tiles; the rest copy tokens
+  int32_t vec;            // base and out allow 16-byte accesses
+  int32_t items;          // first launch: workgroups with tiles; the others copy tokens
+  int32_t col_blocks;     // second launch: workgroups that share a tile's columns, and the
+  int32_t cols_per;       // 64-column blocks of each
 };
+
+// The work item of workgroup b of n: workgroups are dealt round-robin to the 8 XCDs, so
+// XCD x gets a contiguous chunk of the items.
+__device__ __forceinline__ int xcd_item(int b, int n) {
+  const int x = b & 7, q = n >> 3, rem = n & 7;
+  return x * q + min(x, rem) + (b >> 3);
+}
 
 // The adapter of a tile (that of its first row), or -1 when the tile holds no token.
 __device__ __forceinline__ int tile_group(const LoraArgs& a, int tile) {
-  if (tile >= a.tiles) return -1;
   const int g = a.row_group[tile * kTile];
   return (uint32_t)g < (uint32_t)a.G ? g : -1;
 }
@@ -68,254 +76,682 @@ __device__ __forceinline__ int row_token(const LoraArgs& a, int row) {
   return (uint32_t)p < (uint32_t)a.T ? p : -1;
 }
 
-// shrink.  A workgroup takes NT tiles and slice blockIdx.y of K; its four waves take the
-// slice's 64-element units in turn (neighbouring waves read neighbouring lines) and their
-// sums meet in LDS.  RF fragments of 16 rank rows.
-template <int RF, int NT>
-__global__ __launch_bounds__(kThreads) void shrink_kernel(const LoraArgs a) {
-  __shared__ f32x4_t sums[kWaves - 1][RF][NT][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
-  const int per = (a.units + a.S - 1) / a.S;
-  const int u0 = blockIdx.y * per, u1 = min(a.units, u0 + per);
+// One k-step of 32: acc += (16 RF rank rows) x (16 tokens), lane chunks from registers.
+template <int RF>
+__device__ __forceinline__ void mul_step(const u32x4_t& x, const u32x4_t (&av)[RF], f32x4_t (&acc)[RF]) {
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av[f]),
+                                                     __builtin_bit_cast(bf16x8_t, x), acc[f], 0, 0, 0);
+}
 
-  // tiles of this workgroup, taken together as long as they share the adapter
-  for (int i = 0; i < NT;) {
-    const int tile0 = blockIdx.x * NT + i;
-    const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile0));
-    if (g < 0) {
-      ++i;
-      continue;
-    }
-    int nt = 1;
-    while (i + nt < NT && __builtin_amdgcn_readfirstlane(tile_group(a, tile0 + nt)) == g) ++nt;
+// The lane's row (l16) of each fragment of A_g, from its first chunk (lq) on.  Rows past r
+// repeat the last row; their sums are not used.
+template <int RF>
+__device__ __forceinline__ void a_rows(const LoraArgs& a, int g, const uint16_t* (&ap)[RF]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+    ap[f] = a.A + (int64_t)g * a.stride_a + (int64_t)min(16 * f + (lane & 15), a.r - 1) * a.lda + 8 * (lane >> 4);
+}
 
-    // rows past r repeat the last row: their sums are not stored
-    const uint16_t* ap[RF];
+// k-steps k, k + stride, ... below k_hi, the last one partial: K is a multiple of 8, so a
+// lane's chunk is whole or empty.
+template <int RF>
+__device__ __forceinline__ void tail_steps(const uint16_t* x, const uint16_t* const (&ap)[RF], int k, int k_hi,
+                                           int stride, f32x4_t (&acc)[RF]) {
+  const int lq = (threadIdx.x & 63) >> 4;
+  for (; k < k_hi; k += stride) {
+    u32x4_t xv = {0, 0, 0, 0}, av[RF] = {};
+    if (k + 8 * lq < k_hi) {
+      xv = *(const u32x4_t*)(x + k);
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
-      ap[f] = a.A + (int64_t)g * a.stride_a + (int64_t)min(16 * f + l16, a.r - 1) * a.lda;
-    // rows without a token (and tiles past nt) read the first row's token: theirs are
-    // columns of their own in the product, and not used
-    const int t0 = row_token(a, tile0 * kTile);
-    const uint16_t* xp[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = n < nt ? row_token(a, (tile0 + n) * kTile + l16) : t0;
-      xp[n] = a.X + (int64_t)max(t < 0 ? t0 : t, 0) * a.ldx;
+      for (int f = 0; f < RF; ++f) av[f] = *(const u32x4_t*)(ap[f] + k);
     }
-    f32x4_t acc[RF][NT];
-#pragma unroll
-    for (int f = 0; f < RF; ++f)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[f][n] = (f32x4_t){0, 0, 0, 0};
-
-    constexpr int UN = (RF + NT) <= 4 ? 4 : ((RF + NT) <= 8 ? 2 : 1);   // units in flight
-    for (int u = u0 + wave; u < u1; u += kWaves * UN) {
-      bf16x8_t xa[UN][2][NT], aa[UN][2][RF];
-#pragma unroll
-      for (int v = 0; v < UN; ++v)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = (u + v * kWaves) * 64 + 32 * h + 8 * lq;
-          const bool in = u + v * kWaves < u1 && k < a.K;   // K % 8 == 0
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            u32x4_t w = {0, 0, 0, 0};
-            if (in) w = *(const u32x4_t*)(xp[n] + k);
-            xa[v][h][n] = __builtin_bit_cast(bf16x8_t, w);
-          }
-#pragma unroll
-          for (int f = 0; f < RF; ++f) {
-            u32x4_t w = {0, 0, 0, 0};
-            if (in) w = *(const u32x4_t*)(ap[f] + k);
-            aa[v][h][f] = __builtin_bit_cast(bf16x8_t, w);
-          }
-        }
-#pragma unroll
-      for (int v = 0; v < UN; ++v)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int f = 0; f < RF; ++f)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aa[v][h][f], xa[v][h][n], acc[f][n], 0, 0, 0);
-    }
-    __syncthreads();   // (the previous tiles' sums have been read)
-    if (wave > 0) {
-#pragma unroll
-      for (int f = 0; f < RF; ++f)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sums[wave - 1][f][n][lane] = acc[f][n];
-    }
-    __syncthreads();
-    if (wave == 0) {
-      // lane (lq, l16) holds rank rows 16f + 4 lq .. +3 of token l16
-#pragma unroll
-      for (int f = 0; f < RF; ++f)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          f32x4_t v = acc[f][n];
-#pragma unroll
-          for (int w = 0; w < kWaves - 1; ++w) v += sums[w][f][n][lane];
-          const int row = (tile0 + n) * kTile + l16, rr = 16 * f + 4 * lq;
-          if (n < nt && rr < a.r)   // r % 8 == 0
-            *(f32x4_t*)(a.U + ((int64_t)blockIdx.y * a.tiles * kTile + row) * a.r + rr) = v;
-        }
-    }
-    i += nt;
+    mul_step<RF>(xv, av, acc);
   }
 }
 
-// expand.  A workgroup takes NT tiles and 256 columns, a wave 64 of them: four fragments
-// of 16 rows of B_g.  Fragment f's row 4q + i is column 16q + 4f + i, so that a lane ends
-// up with 16 consecutive columns of one token (32 bytes) and four lanes with 128 bytes.
-// RK: k-steps of 32 rank elements.
-__device__ __forceinline__ bool vec_ok(const void* p, int64_t ld) {
-  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0;
+// ---------------------------------------------------------------------------
+// First product for few tokens: the wave's share of A_g x for one tile, columns [k_lo,
+// k_hi) of K (k_lo a multiple of 32).  The wave takes units of 32*KS elements, every
+// nw-th one, straight from global memory to fragments, with the next unit's loads in
+// flight while this one's MFMAs run; the last, partial unit goes in k-steps.  The two
+// halves of a 128-byte line are requested back to back.  Lane (lq, l16) ends up with
+// rank rows 16f + 4lq .. +3 of token l16.
+// ---------------------------------------------------------------------------
+template <int RF, int KS>
+__device__ __forceinline__ void low_rank_rows(const LoraArgs& a, int g, const uint16_t* x, int k_lo, int k_hi,
+                                              int w, int nw, f32x4_t (&acc)[RF]) {
+  const uint16_t* ap[RF];
+  a_rows<RF>(a, g, ap);
+  x += 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+  for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+  struct Unit {
+    u32x4_t x[KS], a[KS][RF];
+  };
+  auto load = [&](Unit& v, int u) {
+    const int k = k_lo + u * KS * 32;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) v.x[s] = *(const u32x4_t*)(x + k + 32 * s);
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) v.a[s][f] = *(const u32x4_t*)(ap[f] + k + 32 * s);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mul = [&](const Unit& v) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) mul_step<RF>(v.x[s], v.a[s], acc);
+  };
+  const int units = (k_hi - k_lo) / (32 * KS);
+  Unit p, q;
+  int u = w;
+  if (u < units) load(p, u);
+  for (; u < units; u += 2 * nw) {
+    if (u + nw < units) load(q, u + nw);
+    mul(p);
+    if (u + nw >= units) break;
+    if (u + 2 * nw < units) load(p, u + 2 * nw);
+    mul(q);
+  }
+  tail_steps<RF>(x, ap, k_lo + (units * KS + w) * 32, k_hi, 32 * nw, acc);
 }
 
-template <int RK, int NT>
-__global__ __launch_bounds__(kThreads) void expand_kernel(const LoraArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.y * 256 + wave * 64;
-  const bool vec = vec_ok(a.out, a.ldo) && (!a.base || vec_ok(a.base, a.ld_base));
+// x = hi + lo to 2^-16 of x; an infinite or NaN x has no low term.
+__device__ __forceinline__ void split_bf16(float x, __bf16& hi, __bf16& lo) {
+  hi = (__bf16)x;
+  const float d = x - (float)hi;
+  lo = (__bf16)(__builtin_isfinite(d) ? d : 0.0f);
+}
 
-  if ((int)blockIdx.x >= a.row_blocks) {
-    // 16 tokens a workgroup: those without an adapter take base as it is, or zeros
-    for (int i = 0; i < 16; ++i) {
-      const int t = ((int)blockIdx.x - a.row_blocks) * 16 + i;
-      if (t >= a.T || (!a.plain && a.row_of[t] >= 0)) continue;
-      const int n = blockIdx.y * 256 + threadIdx.x;
-      if (n < a.N) a.out[(int64_t)t * a.ldo + n] = a.base ? a.base[(int64_t)t * a.ld_base + n] : 0;
+// U in LDS as the second product's operand: hi and lo bf16 terms, [token][rank], zeros
+// past r.  The rows are 16 bytes longer than the rank so that 16 tokens' reads spread
+// over the banks.
+template <int RF>
+struct URows {
+  static constexpr int RK = (RF + 1) / 2;        // k-steps of 32 rank elements
+  static constexpr int PITCH = 32 * RK + 8;
+  static constexpr int QUADS = 8 * RK;           // groups of four ranks a token
+  __bf16 hi[kTile][PITCH], lo[kTile][PITCH];
+  __device__ __forceinline__ void put(int token, int rank, f32x4_t v, int r) {
+    bf16x4_t h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      __bf16 hh, ll;
+      split_bf16(rank < r ? v[e] : 0.0f, hh, ll);    // r % 8 == 0
+      h[e] = hh;
+      l[e] = ll;
     }
+    *(bf16x4_t*)&hi[token][rank] = h;
+    *(bf16x4_t*)&lo[token][rank] = l;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Second product and the addition for one tile: columns 64*c .. for c = c0, c0 + step,
+// ... below c1; one wave.  Fragment f of B_g is the columns 16f ..; the fp32 products of
+// a tile go through the wave's own LDS scratch to a layout in which eight lanes hold the
+// 64 columns of one token, so that base is read and out written by whole 128-byte lines
+// (16 rows of 64 bytes an instruction reach 4.0 TB/s in a copy, 8 rows of 128 bytes 4.7).
+// t[j]: the token of row 8j + lane/8, -1 for none.  The next block's B_g and
+// base are in flight while this one is formed, the first block's while form_u puts U into
+// LDS.  out is stored with the non-temporal hint: it is not read here, and left in L2 it
+// would evict the adapters.
+// ---------------------------------------------------------------------------
+// Four columns (quad) of a row sit at quad ^ row, so that 16 rows' writes of one quad, and
+// two rows' reads of eight, cover the banks once.
+struct Scratch {
+  f32x4_t v[kTile][16];
+  __device__ __forceinline__ f32x4_t& at(int row, int quad) { return v[row][quad ^ row]; }
+};
+
+// base of one tile's 64 columns from 64*c on, 16 bytes a lane of rows 8j + lane/8.
+__device__ __forceinline__ void load_base(const LoraArgs& a, const int (&t)[2], int c, u32x4_t (&base)[2]) {
+  const int n0 = 64 * c + 8 * (threadIdx.x & 7);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    base[j] = (u32x4_t){0, 0, 0, 0};
+    if (a.base && t[j] >= 0 && a.vec && n0 + 8 <= a.N)
+      base[j] = *(const u32x4_t*)(a.base + (int64_t)t[j] * a.ld_base + n0);
+  }
+}
+
+// One tile's 64 columns: the products b x (hi + lo), through the scratch, base added,
+// rounded and stored.
+template <int RK>
+__device__ __forceinline__ void add_block(const LoraArgs& a, const int (&t)[2], int c, const u32x4_t (&b)[RK][4],
+                                          const bf16x8_t (&uh)[RK], const bf16x8_t (&ul)[RK],
+                                          const u32x4_t (&base)[2], Scratch& scratch) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
+  const int col8 = 8 * (lane & 7), n0 = 64 * c + col8;
+  f32x4_t acc[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < RK; ++k)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b[k][f]), ul[k], acc[f], 0, 0, 0);
+      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b[k][f]), uh[k], acc[f], 0, 0, 0);
+    }
+  // (the wave's own scratch: its LDS accesses execute in order)
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+  for (int f = 0; f < 4; ++f) scratch.at(l16, 4 * f + lq) = acc[f];
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const f32x4_t d0 = scratch.at(8 * j + (lane >> 3), 2 * (lane & 7));
+    const f32x4_t d1 = scratch.at(8 * j + (lane >> 3), 2 * (lane & 7) + 1);
+    if (t[j] < 0) continue;
+    uint16_t* orow = a.out + (int64_t)t[j] * a.ldo + n0;
+    if (a.vec && n0 + 8 <= a.N) {
+      u32x4_t o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = (e < 2 ? d0[2 * e] : d1[2 * e - 4]) + __uint_as_float(base[j][e] << 16);
+        const float x1 = (e < 2 ? d0[2 * e + 1] : d1[2 * e - 3]) + __uint_as_float(base[j][e] & 0xFFFF0000u);
+        o[e] = __builtin_bit_cast(uint32_t, (bf16x2_t){(__bf16)x0, (__bf16)x1});
+      }
+      __builtin_nontemporal_store(o, (u32x4_t*)orow);
+    } else {
+      const uint16_t* brow = a.base + (int64_t)t[j] * a.ld_base + n0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n0 + e < a.N) {
+          const float x = a.base ? __uint_as_float((uint32_t)brow[e] << 16) : 0.0f;
+          orow[e] = __builtin_bit_cast(uint16_t, (__bf16)((e < 4 ? d0[e & 3] : d1[e & 3]) + x));
+        }
+    }
+  }
+}
+
+template <int RF, class F>
+__device__ __forceinline__ void add_columns(const LoraArgs& a, int g, const int (&t)[2], const URows<RF>& u,
+                                            Scratch& scratch, int c0, int c1, int step, F&& form_u) {
+  constexpr int RK = URows<RF>::RK;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
+  const uint16_t* bg = a.B + (int64_t)g * a.stride_b;
+  struct Block {
+    u32x4_t b[RK][4], base[2];
+  };
+  auto load = [&](Block& v, int c) {
+    load_base(a, t, c, v.base);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const uint16_t* brow = bg + (int64_t)min(64 * c + 16 * f + l16, a.N - 1) * a.ldb + 8 * lq;
+#pragma unroll
+      for (int k = 0; k < RK; ++k) {
+        v.b[k][f] = (u32x4_t){0, 0, 0, 0};
+        if (32 * k + 8 * lq < a.r) v.b[k][f] = *(const u32x4_t*)(brow + 32 * k);
+      }
+    }
+  };
+  bf16x8_t uh[RK], ul[RK];
+  auto finish = [&](const Block& v, int c) { add_block<RK>(a, t, c, v.b, uh, ul, v.base, scratch); };
+  Block p, q;
+  int c = c0;
+  if (c < c1) load(p, c);
+  form_u();
+#pragma unroll
+  for (int k = 0; k < RK; ++k) {
+    uh[k] = *(const bf16x8_t*)&u.hi[l16][32 * k + 8 * lq];
+    ul[k] = *(const bf16x8_t*)&u.lo[l16][32 * k + 8 * lq];
+  }
+  for (; c < c1; c += 2 * step) {
+    if (c + step < c1) load(q, c + step);
+    finish(p, c);
+    if (c + step >= c1) break;
+    if (c + 2 * step < c1) load(p, c + 2 * step);
+    finish(q, c + step);
+  }
+}
+
+// Tokens without an adapter: base as it is, or zeros.  16 tokens a workgroup, whose waves
+// share them out.
+__device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int waves) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mine = block * 16 + lane;
+  uint64_t rest = __ballot(lane < 16 && mine < a.T && (a.plain || a.row_of[mine < a.T ? mine : 0] < 0));
+  const int nv = a.vec ? a.N / 8 : 0;
+  for (int i = 0; rest; ++i, rest &= rest - 1) {
+    if (i % waves != wave) continue;
+    const int64_t t = block * 16 + __builtin_ctzll(rest);
+    const uint16_t* src = a.base + t * a.ld_base;
+    uint16_t* dst = a.out + t * a.ldo;
+#pragma unroll 4
+    for (int v = lane; v < nv; v += 64)
+      *(u32x4_t*)(dst + 8 * v) = a.base ? *(const u32x4_t*)(src + 8 * v) : (u32x4_t){0, 0, 0, 0};
+    for (int n = 8 * nv + lane; n < a.N; n += 64) dst[n] = a.base ? src[n] : (uint16_t)0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One launch: a workgroup of 16 waves does a tile from X to out.  U stays in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kFusedWaves = 16;
+
+template <int RF>
+__global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(const LoraArgs a) {
+  constexpr int NW = kFusedWaves;
+  __shared__ f32x4_t sums[NW][RF][64];
+  __shared__ URows<RF> u;
+  __shared__ Scratch scratch[NW];
+  if ((int)blockIdx.x >= a.tiles) {
+    copy_tokens(a, blockIdx.x - a.tiles, NW);
     return;
   }
-  if (n0 >= a.N) return;
-  int g_have = -1;
-  bf16x8_t b[RK][4];
-  float s = 1.0f;
-  for (int i = 0; i < NT; ++i) {
-    const int tile = blockIdx.x * NT + i;
-    const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
-    if (g < 0) continue;
-    if (g != g_have) {
-      g_have = g;
-      s = a.scale ? a.scale[g] : 1.0f;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x;
+  const int t = row_token(a, tile * kTile + (lane & 15));
+  const int tr[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
+  const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
+  if (g < 0) return;
+  // rows without a token read the first row's: theirs are columns of their own in the
+  // products, and not stored
+  const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
+  f32x4_t acc[RF];
+  low_rank_rows<RF, RF == 1 ? 6 : 4 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, 0, a.K, wave, NW,
+                                          acc);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int n = n0 + 16 * (l16 >> 2) + 4 * f + (l16 & 3);
-        const uint16_t* bp = a.B + (int64_t)g * a.stride_b + (int64_t)min(n, a.N - 1) * a.ldb;
+  for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
+  __syncthreads();
+  const float s = a.scale ? a.scale[g] : 1.0f;
+  for (int i = threadIdx.x; i < URows<RF>::QUADS * kTile; i += 64 * NW) {
+    const int token = i & 15, r4 = i >> 4;       // ranks 4*r4 ..: fragment r4/4, lane group r4%4
+    f32x4_t v = {0, 0, 0, 0};
+    if (r4 < 4 * RF) {
 #pragma unroll
-        for (int k = 0; k < RK; ++k) {
-          u32x4_t w = {0, 0, 0, 0};
-          if (32 * k + 8 * lq < a.r) w = *(const u32x4_t*)(bp + 32 * k + 8 * lq);
-          b[k][f] = __builtin_bit_cast(bf16x8_t, w);
-        }
-      }
+      for (int w = 0; w < NW; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
     }
-    const int row = tile * kTile + l16, t = row_token(a, row);
-    const int n = n0 + 16 * lq;
-    // base first: the longest wait
-    u32x4_t bv[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    const bool whole = vec && n + 16 <= a.N;
-    const uint16_t* bp = a.base + (int64_t)max(t, 0) * a.ld_base + n;
-    if (a.base && t >= 0 && whole) {
-      bv[0] = *(const u32x4_t*)bp;
-      bv[1] = *(const u32x4_t*)(bp + 8);
+    u.put(token, 4 * r4, s * v, a.r);
+  }
+  __syncthreads();
+  add_columns<RF>(a, g, tr, u, scratch[wave], wave, (a.N + 63) / 64, NW, [] {});
+}
+
+// ---------------------------------------------------------------------------
+// Two launches.  What one CU can keep in flight bounds a workgroup to some 25 bytes per
+// ns, so NT tiles' slices of K and blocks of columns go to workgroups of their own.  The
+// S slices' sums of the first launch lie in slabs of U that every workgroup of the second
+// adds in order.  NT tiles of one adapter share each fragment of A_g and B_g; tiles of
+// different adapters in a workgroup are taken one adapter after the other.
+// ---------------------------------------------------------------------------
+constexpr int kSplitWaves = 4;
+
+template <int RF>
+__global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs a) {
+  __shared__ f32x4_t sums[kSplitWaves][RF][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if ((int)blockIdx.x >= a.items) {
+    copy_tokens(a, blockIdx.x - a.items, kSplitWaves);
+    return;
+  }
+  const int item = xcd_item(blockIdx.x, a.items);
+  const int tile = item / a.S, slice = item % a.S;
+  const int t = row_token(a, tile * kTile + (lane & 15));
+  const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
+  if (g < 0) return;
+  const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
+  const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
+  f32x4_t acc[RF];
+  low_rank_rows<RF, 8 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
+#pragma unroll
+  for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
+  __syncthreads();
+  for (int j = threadIdx.x; j < 4 * RF * kTile; j += 64 * kSplitWaves) {
+    const int r4 = j % (4 * RF), token = j / (4 * RF);
+    f32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kSplitWaves; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
+    if (4 * r4 < a.r)
+      *(f32x4_t*)(a.U + (((int64_t)slice * a.tiles + tile) * kTile + token) * a.r + 4 * r4) = v;
+  }
+}
+
+// First product for many tokens: 64 rows of the plan against the whole rank, K in stages of
+// 64 elements (128 bytes a row).  Fragments straight from global memory would ask for 64
+// bytes of each of 16 rows at a time, and what bounds the kernel is the number of requests
+// a CU keeps in flight; here the stages of X and A_g are copied to LDS by whole lines,
+// NS - 1 stages ahead, and each wave reads its 16 tokens' and A_g's fragments from there.
+// 16-byte chunk c of row r sits at chunk c ^ (r/2 % 8), so that 16 rows' reads of one chunk
+// cover the banks once.
+constexpr int kStageRows = 64;
+constexpr int kStageTiles = kStageRows / kTile;
+
+// The adapters of kStageTiles tiles from tile0 on (-1: no token, or past the end), and the
+// runs of tiles that share one: next() moves to the tiles [i, i + n) of adapter g.
+// Wave-uniform; one load.
+struct Runs {
+  int group[kStageTiles], i, n, g;
+  __device__ __forceinline__ Runs(const LoraArgs& a, int tile0) : i(0), n(0), g(-1) {
+    const int tile = tile0 + (int)(threadIdx.x & (kStageTiles - 1));
+    const int v = tile < a.tiles ? tile_group(a, tile) : -1;
+#pragma unroll
+    for (int j = 0; j < kStageTiles; ++j) group[j] = __builtin_amdgcn_readlane(v, j);
+  }
+  __device__ __forceinline__ bool next() {
+    i += n;
+    n = 1;
+#pragma unroll
+    for (int j = 0; j < kStageTiles; ++j)
+      if (j >= i && group[j] < 0 && j == i) ++i;
+    if (i >= kStageTiles) return false;
+#pragma unroll
+    for (int j = 0; j < kStageTiles; ++j)
+      if (j == i) g = group[j];
+#pragma unroll
+    for (int j = 1; j < kStageTiles; ++j)
+      if (j == i + n && group[j] == g) ++n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void lds_copy(const uint16_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Waits until at most VM of the wave's loads are outstanding and its LDS reads are done,
+// then for the workgroup; unlike __syncthreads() it leaves later copies in flight.
+template <int VM>
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+template <int RF, int NS>
+__global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const LoraArgs a) {
+  constexpr int X_BYTES = kStageRows * 128, STAGE = X_BYTES + 16 * RF * 128;
+  constexpr int AC = RF >= 2 ? RF / 2 : 1;      // copies of A_g per wave and stage (RF 1: half of one)
+  constexpr int COPIES = 2 + AC;
+  static_assert((NS - 1) * COPIES <= 63, "outstanding copies must fit the vmcnt counter");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  if ((int)blockIdx.x >= a.items) {
+    copy_tokens(a, blockIdx.x - a.items, kSplitWaves);
+    return;
+  }
+  const int item = xcd_item(blockIdx.x, a.items);
+  const int tile0 = item / a.S * kStageTiles, slice = item % a.S;
+  const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
+  const int stages = (k_hi - k_lo) / 64;
+
+  Runs run(a, tile0);
+  while (run.next()) {
+    const int i = run.i, nt = run.n, g = run.g;
+    // this run's rows are [16 i, 16 (i + nt)) of the 64; the others, and rows without a
+    // token, read the run's first token (columns of their own, not used)
+    const int t0 = max(__builtin_amdgcn_readfirstlane(row_token(a, (tile0 + i) * kTile)), 0);
+    const uint16_t *xs[2], *as[AC];
+    const int cr = lane >> 3;                   // row of an 8-row copy
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 16 * wave + 8 * c + cr;
+      const int t = wave >= i && wave < i + nt ? row_token(a, tile0 * kTile + row) : -1;
+      xs[c] = a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane & 7) ^ ((row >> 1) & 7));
     }
-    f32x4_t acc[4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < RK; ++k) {
-      float u[8] = {};
-      if (32 * k + 8 * lq < a.r && t >= 0) {
-        for (int sl = 0; sl < a.S; ++sl) {
-          const float* up = a.U + ((int64_t)sl * a.tiles * kTile + row) * a.r + 32 * k + 8 * lq;
-          const f32x4_t v0 = *(const f32x4_t*)up, v1 = *(const f32x4_t*)(up + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            u[e] += v0[e];
-            u[4 + e] += v1[e];
-          }
-        }
-      }
-      bf16x8_t hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = s * u[e];
-        hi[e] = (__bf16)v;
-        lo[e] = (__bf16)(v - (float)hi[e]);
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[k][f], lo, acc[f], 0, 0, 0);
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[k][f], hi, acc[f], 0, 0, 0);
-      }
+    for (int c = 0; c < AC; ++c) {
+      const int row = (RF >= 2 ? 4 * RF * wave + 8 * c : 4 * wave) + cr;
+      as[c] = a.A + (int64_t)g * a.stride_a + (int64_t)min(row, a.r - 1) * a.lda + k_lo +
+              8 * ((lane & 7) ^ ((row >> 1) & 7));
     }
-    if (t < 0) continue;
-    uint16_t* op = a.out + (int64_t)t * a.ldo + n;
-    if (whole) {
+    auto issue = [&](int s, int buf) {
+      uint8_t* const b = ring + buf * STAGE;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) lds_copy(xs[c] + 64 * s, b + (16 * wave + 8 * c) * 128);
+      if (RF >= 2) {
+#pragma unroll
+        for (int c = 0; c < AC; ++c) lds_copy(as[c] + 64 * s, b + X_BYTES + (4 * RF * wave + 8 * c) * 128);
+      } else if (lane < 32) {
+        lds_copy(as[0] + 64 * s, b + X_BYTES + 4 * wave * 128);
+      }
+    };
+    f32x4_t acc[RF];
+#pragma unroll
+    for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+    const int sw = (l16 >> 1) & 7;              // (rows 16 apart share the swizzle)
+    auto compute = [&](int buf) {
+      const uint8_t* const b = ring + buf * STAGE;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        u32x4_t o;
+        const int off = l16 * 128 + (((4 * h + lq) ^ sw) << 4);
+        const u32x4_t xv = *(const u32x4_t*)(b + 16 * wave * 128 + off);
+        u32x4_t av[RF];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // columns 8h + 2e, +1 of the lane's 16: register (2e) % 4 of fragment 2h + e/2
-          const float x0 = acc[2 * h + e / 2][2 * (e % 2)] + __uint_as_float(bv[h][e] << 16);
-          const float x1 = acc[2 * h + e / 2][2 * (e % 2) + 1] + __uint_as_float(bv[h][e] & 0xFFFF0000u);
-          o[e] = __builtin_bit_cast(uint32_t, (bf16x2_t){(__bf16)x0, (__bf16)x1});
-        }
-        *(u32x4_t*)(op + 8 * h) = o;
+        for (int f = 0; f < RF; ++f) av[f] = *(const u32x4_t*)(b + X_BYTES + 16 * f * 128 + off);
+        mul_step<RF>(xv, av, acc);
       }
-    } else {
+    };
+    // (every wave has read the previous run's stages)
+    stage_barrier<0>();
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+    for (int s = 0; s < NS - 1; ++s)
+      if (s < stages) issue(s, s);
+    int s = 0, buf = 0;
+    for (; s + NS - 1 < stages; ++s) {
+      // stage s has landed; the buffer of stage s - 1 has been read by every wave
+      stage_barrier<(NS - 2) * COPIES>();
+      issue(s + NS - 1, buf == 0 ? NS - 1 : buf - 1);
+      compute(buf);
+      buf = buf + 1 == NS ? 0 : buf + 1;
+    }
+    stage_barrier<0>();
+    for (; s < stages; ++s) {
+      compute(buf);
+      buf = buf + 1 == NS ? 0 : buf + 1;
+    }
+    if (wave >= i && wave < i + nt) {
+      const int row = (tile0 + wave) * kTile + l16;
+      if (k_lo + 64 * stages < k_hi) {          // K's last elements
+        const int t = row_token(a, row);
+        const uint16_t* ap[RF];
+        a_rows<RF>(a, g, ap);
+        tail_steps<RF>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + 64 * stages, k_hi, 32, acc);
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + 4 * f + e < a.N) {
-            const float x = a.base ? __uint_as_float((uint32_t)bp[4 * f + e] << 16) : 0.0f;
-            op[4 * f + e] = __builtin_bit_cast(uint16_t, (__bf16)(acc[f][e] + x));
+      for (int f = 0; f < RF; ++f)
+        if (16 * f + 4 * lq < a.r)              // r % 8 == 0
+          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles * kTile + row) * a.r + 16 * f + 4 * lq) = acc[f];
+    }
+  }
+}
+
+template <int RF>
+__global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const LoraArgs a) {
+  __shared__ URows<RF> u;
+  __shared__ Scratch scratch[kSplitWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const int tile = item / a.col_blocks, cb = item % a.col_blocks;
+  const int blocks = (a.N + 63) / 64, c_lo = cb * a.cols_per, c_hi = min(blocks, c_lo + a.cols_per);
+  const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
+  const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
+  if (g < 0) return;
+  add_columns<RF>(a, g, t, u, scratch[wave], c_lo + wave, c_hi, kSplitWaves, [&] {
+    const float s = a.scale ? a.scale[g] : 1.0f;
+    constexpr int QUADS = URows<RF>::QUADS;
+    for (int j = threadIdx.x; j < QUADS * kTile; j += 64 * kSplitWaves) {
+      const int r4 = j % QUADS, row = j / QUADS;
+      f32x4_t v = {0, 0, 0, 0};
+      if (4 * r4 < a.r) {
+        const float* up = a.U + ((int64_t)tile * kTile + row) * a.r + 4 * r4;
+#pragma unroll 8
+        for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles * kTile * a.r);
+      }
+      u.put(row, 4 * r4, s * v, a.r);
+    }
+    __syncthreads();
+  });
+}
+
+// Between the two for many tokens: the slabs of U summed, scaled and split into the second
+// product's two bf16 terms once, instead of by every workgroup that needs a row.  Row
+// layout of UW: 32*RK hi terms, then 32*RK lo terms, zeros past r.
+__global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) {
+  const int quads = ranks / 4;
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int row = (int)(j / quads), r4 = (int)(j - (int64_t)row * quads);
+  if (row >= a.tiles * kTile) return;
+  const int g = a.row_group[min(row / kTile * kTile, a.rows - 1)];
+  if ((uint32_t)g >= (uint32_t)a.G) return;
+  const float s = a.scale ? a.scale[g] : 1.0f;
+  f32x4_t v = {0, 0, 0, 0};
+  if (4 * r4 < a.r) {
+    const float* up = a.U + (int64_t)row * a.r + 4 * r4;
+#pragma unroll 4
+    for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles * kTile * a.r);
+  }
+  bf16x4_t h, l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    __bf16 hh, ll;
+    split_bf16(s * v[e], hh, ll);
+    h[e] = hh;
+    l[e] = ll;
+  }
+  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * ranks + 4 * r4) = h;
+  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * ranks + ranks + 4 * r4) = l;
+}
+
+// Second product for many tokens: a workgroup takes 64 rows, a tile a wave, and CB blocks
+// of 64 columns, whose rows of B_g it copies to LDS once for its waves.  Everything a
+// wave reads from memory (base, U, its share of B_g) is asked for at once; workgroups side
+// by side on a CU cover the wait.  Chunk c of B_g row n sits at chunk c ^ (n * row bytes /
+// 256 % chunks), as in the first product's ring.
+template <int RF, int CB>
+__global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_eu(RF == 8 ? 2 : 3))) void expand_many_kernel(
+    const LoraArgs a) {
+  constexpr int RK = URows<RF>::RK, NC = 4 * RK, ROW = 16 * NC;   // 16-byte chunks and bytes of a row
+  constexpr int ROWS = 64 * CB, RPC = 1024 / ROW;                   // rows, and rows of one wave copy
+  __shared__ __attribute__((aligned(1024))) uint8_t bl[ROWS * ROW];
+  __shared__ Scratch scratch[kSplitWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const int tile0 = item / a.col_blocks * kStageTiles, c0 = item % a.col_blocks * CB;
+  const int tile = tile0 + wave;
+  const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
+  Runs run(a, tile0);
+  bool first = true;
+  while (run.next()) {
+    const bool mine = wave >= run.i && wave < run.i + run.n;
+    const uint16_t* const bg = a.B + (int64_t)run.g * a.stride_b;
+    if (!first) stage_barrier<0>();     // (every wave has read the previous run's rows)
+    first = false;
+#pragma unroll
+    for (int q = 0; q < ROWS / RPC / kSplitWaves; ++q) {
+      const int row0 = (q * kSplitWaves + wave) * RPC, row = row0 + lane / NC;
+      const int chunk = (lane % NC) ^ ((row * ROW / 256) % NC);
+      // rows past N repeat the last one, chunks past r the first: neither is used
+      lds_copy(bg + (int64_t)min(64 * c0 + row, a.N - 1) * a.ldb + (8 * chunk < a.r ? 8 * chunk : 0), bl + row0 * ROW);
+    }
+    u32x4_t base[CB][2];
+    bf16x8_t uh[RK], ul[RK];
+    if (mine) {
+      const __bf16* up = a.UW + ((int64_t)tile * kTile + l16) * (64 * RK) + 8 * lq;
+#pragma unroll
+      for (int k = 0; k < RK; ++k) {
+        uh[k] = *(const bf16x8_t*)(up + 32 * k);
+        ul[k] = *(const bf16x8_t*)(up + 32 * RK + 32 * k);
+      }
+#pragma unroll
+      for (int c = 0; c < CB; ++c) load_base(a, t, c0 + c, base[c]);
+    }
+    stage_barrier<0>();
+    if (mine) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        if (64 * (c0 + c) >= a.N) break;
+        u32x4_t b[RK][4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+          for (int k = 0; k < RK; ++k) {
+            const int row = 64 * c + 16 * f + l16;
+            b[k][f] = *(const u32x4_t*)(bl + row * ROW + (((4 * k + lq) ^ ((row * ROW / 256) % NC)) << 4));
           }
+        if (a.r % 32) {
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int k = 0; k < RK; ++k)
+              if (32 * k + 8 * lq >= a.r) b[k][f] = (u32x4_t){0, 0, 0, 0};
+        }
+        add_block<RK>(a, t, c0 + c, b, uh, ul, base[c], scratch[wave]);
+      }
     }
   }
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static bool vec_ok(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
-// Tiles that share a fragment of the adapter: all four while there are tiles to fill
-// the chip, one when there are few.
-static int tiles_per_wg(int64_t tiles) { return tiles >= 1024 ? 4 : (tiles >= 512 ? 2 : 1); }
-
-// Slices of K: enough workgroups to fill the chip, at least 512 elements a slice.
-static int slices(int64_t tiles, int64_t K) {
-  const int64_t wgs = ceil_div(tiles, tiles_per_wg(tiles));
-  int64_t s = ceil_div(1024, wgs > 0 ? wgs : 1);
-  const int64_t most = K / 512 > 0 ? K / 512 : 1;
-  return (int)(s < most ? s : most);
+// Whether a problem takes one launch: the adapter small enough for one workgroup to
+// stream, and tiles few enough that each has a CU.
+static bool one_launch(int64_t tiles, int64_t K, int64_t N, int64_t r) {
+  return r <= 32 && tiles <= 256 && r * (K + N) * 2 <= (int64_t(160) << 10);
 }
 
-template <int NT>
-static void launch_shrink(int rf, const LoraArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)ceil_div(a.tiles, NT), (unsigned)a.S);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, a); };
-  if (rf == 1) go(shrink_kernel<1, NT>);
-  else if (rf == 2) go(shrink_kernel<2, NT>);
-  else if (rf <= 4) go(shrink_kernel<4, NT>);
-  else go(shrink_kernel<8, NT>);
+// Whether the two-launch form takes several tiles of an adapter together: adapters with
+// tokens for that on average, and tiles enough to fill the chip with groups of them.
+static bool many_tokens(int64_t T, int64_t G, int64_t tiles) { return T >= 48 * G && tiles >= 256; }
+
+// The rank up to which the kernels' fragments reach.
+static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
+
+// Slices of K in the two-launch form: workgroups for the whole chip, at least 256
+// elements a slice.
+static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K) {
+  const int64_t s = 512 / (many_tokens(T, G, tiles) ? ceil_div(tiles, kStageTiles) : tiles);
+  const int64_t most = ceil_div(K, 256);
+  return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
 
-template <int NT>
-static void launch_expand(int rk, const LoraArgs& a, unsigned x, hipStream_t st) {
-  const dim3 grid(x, (unsigned)ceil_div(a.N, 256));
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, st, a); };
-  if (rk == 1) go(expand_kernel<1, NT>);
-  else if (rk == 2) go(expand_kernel<2, NT>);
-  else go(expand_kernel<4, NT>);
+template <int RF>
+static void launch_two(LoraArgs& a, int copy_blocks, hipStream_t st) {
+  a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 64) * 64;
+  const dim3 threads(64 * kSplitWaves);
+  const int blocks = (int)ceil_div(a.N, 64);
+  if (many_tokens(a.T, a.G, a.tiles)) {
+    constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
+    constexpr int CB = RF == 8 ? 2 : 4;
+    const int groups = (int)ceil_div(a.tiles, kStageTiles);
+    a.items = groups * a.S;
+    hipLaunchKernelGGL((shrink_many_kernel<RF, NS>), dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+    constexpr int ranks = 32 * URows<RF>::RK;
+    a.UW = (__bf16*)(a.U + (int64_t)a.S * a.tiles * kTile * a.r);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div((int64_t)a.tiles * kTile * (ranks / 4), 256)), dim3(256), 0,
+                       st, a, ranks);
+    a.col_blocks = (int)ceil_div(blocks, CB);
+    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)(groups * a.col_blocks)), threads, 0, st, a);
+    return;
+  }
+  a.items = a.tiles * a.S;
+  hipLaunchKernelGGL(shrink_kernel<RF>, dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+  // columns: workgroups for the whole chip, at least one block of 64 a wave
+  const int want = (int)ceil_div(1024, a.tiles), most = (int)ceil_div(blocks, kSplitWaves);
+  a.cols_per = (int)ceil_div(ceil_div(blocks, want < most ? want : most), kSplitWaves) * kSplitWaves;
+  a.col_blocks = (int)ceil_div(blocks, a.cols_per);
+  hipLaunchKernelGGL(expand_kernel<RF>, dim3((unsigned)(a.tiles * a.col_blocks)), threads, 0, st, a);
+}
+
+template <int RF>
+static void launch(LoraArgs& a, int copy_blocks, bool one, hipStream_t st) {
+  if (one)
+    hipLaunchKernelGGL((fused_kernel<RF <= 2 ? RF : 1>), dim3((unsigned)(a.tiles + copy_blocks)),
+                       dim3(64 * kFusedWaves), 0, st, a);
+  else
+    launch_two<RF>(a, copy_blocks, st);
 }
 
 }  // namespace bsg_lora
@@ -324,10 +760,12 @@ using namespace bsg_lora;
 
 extern "C" {
 
-int64_t lora_add_workspace(int64_t rows, int64_t K, int32_t r) {
-  if (rows <= 0 || K <= 0 || r <= 0) return 0;
+int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
+  if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  return 4 * (int64_t)slices(tiles, K) * tiles * kTile * r;
+  if (one_launch(tiles, K, N, r)) return 0;
+  const int64_t joined = many_tokens(T, G, tiles) ? 4 * tiles * kTile * padded_rank(r) : 0;
+  return 4 * (int64_t)slices(T, G, tiles, K) * tiles * kTile * r + joined;
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
@@ -357,7 +795,8 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
       return BSG_ERR_UNSUPPORTED_SHAPE;
     if (((uintptr_t)X | (uintptr_t)A | (uintptr_t)B) & 15) return BSG_ERR_MISALIGNED;
     if (ldx % 8 || lda % 8 || ldb % 8 || stride_a % 8 || stride_b % 8) return BSG_ERR_MISALIGNED;
-    if (!workspace || workspace_bytes < lora_add_workspace(rows, K, r)) return BSG_ERR_INVALID_ARG;
+    const int64_t need = lora_add_workspace(T, rows, G, N, K, r);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return BSG_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 15) return BSG_ERR_MISALIGNED;
   }
   if (ldo > big || ld_base > big) return BSG_ERR_UNSUPPORTED_SHAPE;
@@ -387,27 +826,18 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   a.rows = (int32_t)rows;
   a.tiles = adapt ? (int32_t)ceil_div(rows, kTile) : 0;
   a.plain = !adapt;
-  a.S = slices(a.tiles, K);
-  a.units = (int32_t)ceil_div(K, 64);
+  a.vec = vec_ok(out, ldo) && (!base || vec_ok(base, ld_base));
+  const bool one = !adapt || one_launch(a.tiles, K, N, r);
+  a.S = one ? 1 : slices(T, G, a.tiles, K);
   const hipStream_t st = (hipStream_t)stream;
-  const int nt = tiles_per_wg(a.tiles);
-  a.row_blocks = (int32_t)ceil_div(a.tiles, nt);
   // tokens without an adapter: nothing to do in place
-  const int64_t rest = base == out ? 0 : ceil_div(T, 16);
+  const int copy_blocks = base == out ? 0 : (int)ceil_div(T, 16);
+  if (a.tiles + copy_blocks == 0) return BSG_OK;
   (void)hipGetLastError();
-  if (a.tiles > 0) {
-    const int rf = (r + 15) / 16;
-    if (nt == 4) launch_shrink<4>(rf, a, st);
-    else if (nt == 2) launch_shrink<2>(rf, a, st);
-    else launch_shrink<1>(rf, a, st);
-  }
-  const int64_t x = a.row_blocks + rest;
-  if (x > 0) {
-    const int rk = (r + 31) / 32;
-    if (nt == 4) launch_expand<4>(rk, a, (unsigned)x, st);
-    else if (nt == 2) launch_expand<2>(rk, a, (unsigned)x, st);
-    else launch_expand<1>(rk, a, (unsigned)x, st);
-  }
+  if (r <= 16) launch<1>(a, copy_blocks, one, st);
+  else if (r <= 32) launch<2>(a, copy_blocks, one, st);
+  else if (r <= 64) launch<4>(a, copy_blocks, one, st);
+  else launch<8>(a, copy_blocks, one, st);
   return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
 }
 

@@ -96,18 +96,17 @@ def test_combine_refusals():
 
 def test_lora_refusals():
     L = bsg.lib()
-    need = L.lora_add_workspace(256, 512, 16)
-    assert need >= 256 * 16 * 4 and L.lora_add_workspace(0, 512, 16) == 0
+    assert L.lora_add_workspace(100, 0, 4, 256, 512, 16) == 0 and L.lora_add_workspace(100, 256, 4, 256, 512, 16) == 0
     #   0  1    2  3    4         5  6   7         8  9   10  11  12   13  14   15   16   17   18 19   20
     #   X  ldx  A  lda  stride_a  B  ldb stride_b  s  row pr  grp rows bs  ldb  out  ldo  T    G  N    K
     good = [P, 512, P, 512, 16 * 512, P, 16, 256 * 16, P2, P2, P3, P4, 256, P5, 256, 0x90000, 256, 100, 4,
-            256, 512, 16, 0x80000, need, None]
+            256, 512, 16, 0, 0, None]
     _try(L.lora_add_bf16, good, [
         ({17: -1}, INV), ({18: -1}, INV), ({19: -1}, INV), ({20: -1}, INV), ({21: -1}, INV), ({12: -1}, INV),
         ({0: 0}, INV), ({2: 0}, INV), ({5: 0}, INV), ({9: 0}, INV), ({10: 0}, INV), ({11: 0}, INV),
         ({15: 0}, INV), ({1: 504}, INV), ({3: 504}, INV), ({6: 8}, INV), ({14: 255}, INV), ({16: 255}, INV),
         ({4: 16 * 512 - 8}, INV), ({7: 256 * 16 - 8}, INV),
-        ({22: 0}, INV), ({23: need - 1}, INV),
+        ({23: -1}, INV),
         ({15: P5, 16: 264}, INV),             # in place with another leading dimension
         ({21: 12}, SHAPE), ({21: 136, 6: 136}, SHAPE), ({20: 508}, SHAPE), ({18: 1025}, SHAPE),
         ({0: P + 8}, ALIGN), ({2: P + 2}, ALIGN), ({5: P + 8}, ALIGN), ({1: 516}, ALIGN), ({3: 516, 4: 16 * 516}, ALIGN),
@@ -115,6 +114,12 @@ def test_lora_refusals():
         ({8: P2 + 2}, ALIGN),
         ({17: 0}, OK), ({19: 0}, OK),
     ])
+    # few tokens of large adapters need a workspace
+    need = L.lora_add_workspace(100, 256, 4, 4096, 8192, 128)
+    assert need >= 256 * 128 * 4
+    big = [P, 8192, P, 8192, 128 * 8192, P, 128, 4096 * 128, P2, P2, P3, P4, 256, P5, 4096, 0x90000, 4096, 100,
+           4, 4096, 8192, 128, 0x80000, need, None]
+    _try(L.lora_add_bf16, big, [({22: 0}, INV), ({23: need - 1}, INV), ({22: 0x80008}, ALIGN)])
 
 
 def _plan(T=4, k=2, rows=8):
