@@ -97,8 +97,8 @@ EXPORTS = {
     "moe_combine": [_vp, _i64, _vp, _vp, _i64, _i64, _i32, _i64, _i64, _vp, _i64, _vp],
     "moe_combine_backward": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i64, _i64,
                              _vp, _i64, _vp, _i64, _vp],
-    "lora_add_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
-                      _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp],
+    "lora_add_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
+                      _vp, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp],
 }
 # functions that return a number of bytes, not a status
 SIZES = {
@@ -710,7 +710,7 @@ def _plan(plan, *ts):
     """A plan's row_of, pair_of and row_group, T, k and rows, checked against the other
     operands' device."""
     offsets, row_of, pair_of, row_group = plan
-    _one_gpu(row_of, pair_of, row_group, *ts)
+    _one_gpu(row_of, pair_of, row_group, offsets, *ts)
     for t in (row_of, pair_of, row_group):
         if t.dtype != torch.int32 or not t.is_contiguous():
             raise TypeError("the plan must hold contiguous int32 tensors")
@@ -837,6 +837,7 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
     aligned contiguous tensor of at least lora_add_workspace(T, rows, G, N, K, r) bytes."""
     row_of, pair_of, row_group, T, k, rows = _plan(plan, X, A, B, scale, base, out, workspace)
+    offsets = plan[0]
     if k != 1:
         raise ValueError("a token takes one adapter: the plan must come from ids [T, 1]")
     if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
@@ -847,6 +848,7 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     N = B.shape[1]
     if B.shape != (G, N, r):
         raise ValueError("A and B disagree on the adapters or the rank")
+    _offsets_check(offsets, G)
     sa, sb = A.stride(), B.stride()
     if (K > 1 and sa[2] != 1) or (r > 1 and sb[2] != 1):
         raise ValueError("A and B must be contiguous along their last dimension")
@@ -871,7 +873,8 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
             size = ws.numel() * ws.element_size()
         _check("lora_add_bf16", L.lora_add_bf16(
             X.data_ptr(), ldx, A.data_ptr(), sa[1], sa[0], B.data_ptr(), sb[1], sb[0],
-            _ptr(scale), row_of.data_ptr(), pair_of.data_ptr(), row_group.data_ptr(), rows,
+            _ptr(scale), offsets.data_ptr(), row_of.data_ptr(), pair_of.data_ptr(),
+            row_group.data_ptr(), rows,
             _ptr(base), ld_base, D.data_ptr(), ldo, T, G, N, K, r, _ptr(ws), size, st))
         return D
     return _launch(X, stream, body)

@@ -39,6 +39,7 @@ struct LoraArgs {
   const uint16_t* B;      // [G][N][r]
   int64_t ldb, stride_b;
   const float* scale;     // [G] or null
+  const int32_t* offsets; // [G+1]
   const int32_t* row_of;  // [T]
   const int32_t* pair_of;
   const int32_t* row_group;
@@ -49,7 +50,7 @@ struct LoraArgs {
   float* U;               // two launches: [S][tiles*16][r]
   __bf16* UW;             // many tokens: [tiles*16][hi, lo][rank padded to 32]
   int32_t T, G, K, N, r, rows, tiles, S;
-  int32_t k_per;          // elements of K per slice, a multiple of 64
+  int32_t k_per;          // elements of K per slice, a multiple of 128
   int32_t plain;          // K, r or G is 0: no token has anything to add
   int32_t vec;            // base and out allow 16-byte accesses
   int32_t items;          // first launch: workgroups with tiles; the others copy tokens
@@ -352,24 +353,24 @@ __global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(const LoraArgs 
   // rows without a token read the first row's: theirs are columns of their own in the
   // products, and not stored
   const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
-  f32x4_t acc[RF];
-  low_rank_rows<RF, RF == 1 ? 6 : 4 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, 0, a.K, wave, NW,
-                                          acc);
+  add_columns<RF>(a, g, tr, u, scratch[wave], wave, (a.N + 63) / 64, NW, [&] {
+    f32x4_t acc[RF];
+    low_rank_rows<RF, 4 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, 0, a.K, wave, NW, acc);
 #pragma unroll
-  for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
-  __syncthreads();
-  const float s = a.scale ? a.scale[g] : 1.0f;
-  for (int i = threadIdx.x; i < URows<RF>::QUADS * kTile; i += 64 * NW) {
-    const int token = i & 15, r4 = i >> 4;       // ranks 4*r4 ..: fragment r4/4, lane group r4%4
-    f32x4_t v = {0, 0, 0, 0};
-    if (r4 < 4 * RF) {
+    for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
+    __syncthreads();
+    const float s = a.scale ? a.scale[g] : 1.0f;
+    for (int i = threadIdx.x; i < URows<RF>::QUADS * kTile; i += 64 * NW) {
+      const int token = i & 15, r4 = i >> 4;       // ranks 4*r4 ..: fragment r4/4, lane group r4%4
+      f32x4_t v = {0, 0, 0, 0};
+      if (r4 < 4 * RF) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
+        for (int w = 0; w < NW; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
+      }
+      u.put(token, 4 * r4, s * v, a.r);
     }
-    u.put(token, 4 * r4, s * v, a.r);
-  }
-  __syncthreads();
-  add_columns<RF>(a, g, tr, u, scratch[wave], wave, (a.N + 63) / 64, NW, [] {});
+    __syncthreads();
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
   const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
   const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
   f32x4_t acc[RF];
-  low_rank_rows<RF, 8 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
+  low_rank_rows<RF, RF <= 2 ? 4 / RF : 2>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
 #pragma unroll
   for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
   __syncthreads();
@@ -412,14 +413,24 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
 }
 
 // First product for many tokens: 64 rows of the plan against the whole rank, K in stages of
-// 64 elements (128 bytes a row).  Fragments straight from global memory would ask for 64
+// KC elements (128 or 256 bytes a row).  Fragments straight from global memory would ask for 64
 // bytes of each of 16 rows at a time, and what bounds the kernel is the number of requests
 // a CU keeps in flight; here the stages of X and A_g are copied to LDS by whole lines,
 // NS - 1 stages ahead, and each wave reads its 16 tokens' and A_g's fragments from there.
-// 16-byte chunk c of row r sits at chunk c ^ (r/2 % 8), so that 16 rows' reads of one chunk
-// cover the banks once.
+// 16-byte chunk c of row r sits at chunk c ^ (r * row bytes / 256 % chunks), so that 16
+// rows' reads of one chunk cover the banks once.
+//
+// The plan's capacity exceeds the rows in use (padding, tokens without an adapter), and
+// the unused rows are the last ones: only the used ones are dealt to the XCDs, or the
+// last XCD would stand idle.
 constexpr int kStageRows = 64;
 constexpr int kStageTiles = kStageRows / kTile;
+
+// Work items per 64 rows times the 64-row groups in use.
+__device__ __forceinline__ int used_items(const LoraArgs& a, int per_group) {
+  const int used = min(max(a.offsets[a.G], 0), a.rows);
+  return (used + kStageRows - 1) / kStageRows * per_group;
+}
 
 // The adapters of kStageTiles tiles from tile0 on (-1: no token, or past the end), and the
 // runs of tiles that share one: next() moves to the tiles [i, i + n) of adapter g.
@@ -449,10 +460,12 @@ struct Runs {
   }
 };
 
+template <int AUX = 0>
 __device__ __forceinline__ void lds_copy(const uint16_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, AUX);
 }
+constexpr int kNonTemporal = 2;     // cache policy bit of lines read once
 
 // Waits until at most VM of the wave's loads are outstanding and its LDS reads are done,
 // then for the workgroup; unlike __syncthreads() it leaves later copies in flight.
@@ -466,23 +479,29 @@ __device__ __forceinline__ void stage_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-template <int RF, int NS>
+template <int RF, int KC, int NS>
 __global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const LoraArgs a) {
-  constexpr int X_BYTES = kStageRows * 128, STAGE = X_BYTES + 16 * RF * 128;
-  constexpr int AC = RF >= 2 ? RF / 2 : 1;      // copies of A_g per wave and stage (RF 1: half of one)
-  constexpr int COPIES = 2 + AC;
+  constexpr int ROW = 2 * KC, NC = KC / 8;      // bytes and 16-byte chunks of a row
+  constexpr int RPC = 1024 / ROW;               // rows of one wave copy
+  constexpr int X_BYTES = kStageRows * ROW, STAGE = X_BYTES + 16 * RF * ROW;
+  constexpr int XC = 16 / RPC;                  // copies of X per wave and stage: its own tile
+  constexpr int AR = 4 * RF;                    // rows of A_g a wave copies
+  constexpr int AC = AR >= RPC ? AR / RPC : 1;  // (fewer than a copy holds: part of its lanes)
+  constexpr int COPIES = XC + AC;
   static_assert((NS - 1) * COPIES <= 63, "outstanding copies must fit the vmcnt counter");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
   if ((int)blockIdx.x >= a.items) {
     copy_tokens(a, blockIdx.x - a.items, kSplitWaves);
     return;
   }
-  const int item = xcd_item(blockIdx.x, a.items);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  const int items = used_items(a, a.S);
+  if ((int)blockIdx.x >= items) return;
+  const int item = xcd_item(blockIdx.x, items);
   const int tile0 = item / a.S * kStageTiles, slice = item % a.S;
   const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
-  const int stages = (k_hi - k_lo) / 64;
+  const int stages = (k_hi - k_lo) / KC;
 
   Runs run(a, tile0);
   while (run.next()) {
@@ -490,44 +509,41 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const Lor
     // this run's rows are [16 i, 16 (i + nt)) of the 64; the others, and rows without a
     // token, read the run's first token (columns of their own, not used)
     const int t0 = max(__builtin_amdgcn_readfirstlane(row_token(a, (tile0 + i) * kTile)), 0);
-    const uint16_t *xs[2], *as[AC];
-    const int cr = lane >> 3;                   // row of an 8-row copy
+    const uint16_t *xs[XC], *as[AC];
+    const int cr = lane / NC;                   // row of a copy
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int row = 16 * wave + 8 * c + cr;
+    for (int c = 0; c < XC; ++c) {
+      const int row = 16 * wave + RPC * c + cr;
       const int t = wave >= i && wave < i + nt ? row_token(a, tile0 * kTile + row) : -1;
-      xs[c] = a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+      xs[c] = a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane % NC) ^ (row * ROW / 256 % NC));
     }
 #pragma unroll
     for (int c = 0; c < AC; ++c) {
-      const int row = (RF >= 2 ? 4 * RF * wave + 8 * c : 4 * wave) + cr;
+      const int row = AR * wave + RPC * c + cr;
       as[c] = a.A + (int64_t)g * a.stride_a + (int64_t)min(row, a.r - 1) * a.lda + k_lo +
-              8 * ((lane & 7) ^ ((row >> 1) & 7));
+              8 * ((lane % NC) ^ (row * ROW / 256 % NC));
     }
     auto issue = [&](int s, int buf) {
       uint8_t* const b = ring + buf * STAGE;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) lds_copy(xs[c] + 64 * s, b + (16 * wave + 8 * c) * 128);
-      if (RF >= 2) {
+      for (int c = 0; c < XC; ++c) lds_copy<kNonTemporal>(xs[c] + KC * s, b + (16 * wave + RPC * c) * ROW);
 #pragma unroll
-        for (int c = 0; c < AC; ++c) lds_copy(as[c] + 64 * s, b + X_BYTES + (4 * RF * wave + 8 * c) * 128);
-      } else if (lane < 32) {
-        lds_copy(as[0] + 64 * s, b + X_BYTES + 4 * wave * 128);
-      }
+      for (int c = 0; c < AC; ++c)
+        if (AR >= RPC || cr < AR) lds_copy(as[c] + KC * s, b + X_BYTES + (AR * wave + RPC * c) * ROW);
     };
     f32x4_t acc[RF];
 #pragma unroll
     for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
-    const int sw = (l16 >> 1) & 7;              // (rows 16 apart share the swizzle)
     auto compute = [&](int buf) {
       const uint8_t* const b = ring + buf * STAGE;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int off = l16 * 128 + (((4 * h + lq) ^ sw) << 4);
-        const u32x4_t xv = *(const u32x4_t*)(b + 16 * wave * 128 + off);
+      for (int h = 0; h < KC / 32; ++h) {
+        // (rows 16 apart share the swizzle)
+        const int off = l16 * ROW + (((4 * h + lq) ^ (l16 * ROW / 256 % NC)) << 4);
+        const u32x4_t xv = *(const u32x4_t*)(b + 16 * wave * ROW + off);
         u32x4_t av[RF];
 #pragma unroll
-        for (int f = 0; f < RF; ++f) av[f] = *(const u32x4_t*)(b + X_BYTES + 16 * f * 128 + off);
+        for (int f = 0; f < RF; ++f) av[f] = *(const u32x4_t*)(b + X_BYTES + 16 * f * ROW + off);
         mul_step<RF>(xv, av, acc);
       }
     };
@@ -551,11 +567,11 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const Lor
     }
     if (wave >= i && wave < i + nt) {
       const int row = (tile0 + wave) * kTile + l16;
-      if (k_lo + 64 * stages < k_hi) {          // K's last elements
+      if (k_lo + KC * stages < k_hi) {          // K's last elements
         const int t = row_token(a, row);
         const uint16_t* ap[RF];
         a_rows<RF>(a, g, ap);
-        tail_steps<RF>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + 64 * stages, k_hi, 32, acc);
+        tail_steps<RF>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + KC * stages, k_hi, 32, acc);
       }
 #pragma unroll
       for (int f = 0; f < RF; ++f)
@@ -636,7 +652,9 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   __shared__ Scratch scratch[kSplitWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const int items = used_items(a, a.col_blocks);
+  if ((int)blockIdx.x >= items) return;
+  const int item = xcd_item(blockIdx.x, items);
   const int tile0 = item / a.col_blocks * kStageTiles, c0 = item % a.col_blocks * CB;
   const int tile = tile0 + wave;
   const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
@@ -709,25 +727,27 @@ static bool many_tokens(int64_t T, int64_t G, int64_t tiles) { return T >= 48 * 
 // The rank up to which the kernels' fragments reach.
 static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
 
-// Slices of K in the two-launch form: workgroups for the whole chip, at least 256
-// elements a slice.
+// Slices of K in the two-launch form: workgroups for the whole chip; with few tokens at
+// least 1024 elements a slice (two units a wave), as every workgroup of the second launch
+// adds the slabs.
 static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K) {
-  const int64_t s = 512 / (many_tokens(T, G, tiles) ? ceil_div(tiles, kStageTiles) : tiles);
-  const int64_t most = ceil_div(K, 256);
+  const bool many = many_tokens(T, G, tiles);
+  const int64_t s = many ? ceil_div(512, ceil_div(tiles, kStageTiles)) : 512 / tiles;
+  const int64_t most = ceil_div(K, many ? 256 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
 
 template <int RF>
 static void launch_two(LoraArgs& a, int copy_blocks, hipStream_t st) {
-  a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 64) * 64;
+  a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 128) * 128;
   const dim3 threads(64 * kSplitWaves);
   const int blocks = (int)ceil_div(a.N, 64);
   if (many_tokens(a.T, a.G, a.tiles)) {
-    constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
+    constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
     constexpr int CB = RF == 8 ? 2 : 4;
     const int groups = (int)ceil_div(a.tiles, kStageTiles);
     a.items = groups * a.S;
-    hipLaunchKernelGGL((shrink_many_kernel<RF, NS>), dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+    hipLaunchKernelGGL((shrink_many_kernel<RF, KC, NS>), dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
     constexpr int ranks = 32 * URows<RF>::RK;
     a.UW = (__bf16*)(a.U + (int64_t)a.S * a.tiles * kTile * a.r);
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div((int64_t)a.tiles * kTile * (ranks / 4), 256)), dim3(256), 0,
@@ -769,9 +789,9 @@ int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
-                  int64_t ldb, int64_t stride_b, const float* scale, const int32_t* row_of,
-                  const int32_t* pair_of, const int32_t* row_group, int64_t rows, const void* base,
-                  int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
+                  int64_t ldb, int64_t stride_b, const float* scale, const int32_t* offsets,
+                  const int32_t* row_of, const int32_t* pair_of, const int32_t* row_group, int64_t rows,
+                  const void* base, int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
                   int32_t r, void* workspace, int64_t workspace_bytes, void* stream) {
   if (T < 0 || G < 0 || N < 0 || K < 0 || r < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
   if (r > 128 || r % 8 || K % 8) return BSG_ERR_UNSUPPORTED_SHAPE;
@@ -783,9 +803,9 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   // in place only onto the same elements
   if (base == out && ld_base != ldo) return BSG_ERR_INVALID_ARG;
   const bool adapt = rows > 0 && G > 0 && K > 0 && r > 0;
-  if (((uintptr_t)row_of | (uintptr_t)pair_of | (uintptr_t)row_group | (uintptr_t)scale) & 3)
+  if (((uintptr_t)offsets | (uintptr_t)row_of | (uintptr_t)pair_of | (uintptr_t)row_group | (uintptr_t)scale) & 3)
     return BSG_ERR_MISALIGNED;
-  if (rows > 0 && (!pair_of || !row_group)) return BSG_ERR_INVALID_ARG;
+  if (rows > 0 && (!pair_of || !row_group || !offsets)) return BSG_ERR_INVALID_ARG;
   const int64_t big = int64_t(1) << 40;
   if (adapt) {
     if (!X || !A || !B || ldx < K || lda < K || ldb < r || stride_a < 0 || stride_b < 0)
@@ -810,6 +830,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   a.ldb = ldb;
   a.stride_b = stride_b;
   a.scale = scale;
+  a.offsets = offsets;
   a.row_of = row_of;
   a.pair_of = pair_of;
   a.row_group = row_group;

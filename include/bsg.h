@@ -487,7 +487,7 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   base, out: bf16 [T][.. >= N]; base NULL counts as zeros; base == out adds in place
  *   (rows of tokens without an adapter are then not touched), any other overlap of out
  *   with an input is not allowed.
- *   row_of, pair_of, row_group: the plan of sort_tokens over the adapters' ids (k = 1)
+ *   offsets, row_of, pair_of, row_group: the plan of sort_tokens over the adapters' ids (k = 1)
  *   with an alignment that is a multiple of 16, so that the 16 rows of a tile belong to
  *   one adapter (a plan that breaks this gives wrong rows).
  *   workspace: lora_add_workspace(T, rows, G, N, K, r) bytes, 16-byte aligned, no initial value
@@ -496,9 +496,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   leading dimensions and strides multiples of 8; any N (base and out 16-byte aligned
  *   with leading dimensions multiples of 8 move 16 bytes at a time). */
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
-                  int64_t ldb, int64_t stride_b, const float* scale, const int32_t* row_of,
-                  const int32_t* pair_of, const int32_t* row_group, int64_t rows, const void* base,
-                  int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
+                  int64_t ldb, int64_t stride_b, const float* scale, const int32_t* offsets,
+                  const int32_t* row_of, const int32_t* pair_of, const int32_t* row_group, int64_t rows,
+                  const void* base, int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
                   int32_t r, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of lora_add_bf16 for a plan of that many rows (0: none needed). */

@@ -97,29 +97,39 @@ def test_combine_refusals():
 def test_lora_refusals():
     L = bsg.lib()
     assert L.lora_add_workspace(100, 0, 4, 256, 512, 16) == 0 and L.lora_add_workspace(100, 256, 4, 256, 512, 16) == 0
-    #   0  1    2  3    4         5  6   7         8  9   10  11  12   13  14   15   16   17   18 19   20
-    #   X  ldx  A  lda  stride_a  B  ldb stride_b  s  row pr  grp rows bs  ldb  out  ldo  T    G  N    K
-    good = [P, 512, P, 512, 16 * 512, P, 16, 256 * 16, P2, P2, P3, P4, 256, P5, 256, 0x90000, 256, 100, 4,
-            256, 512, 16, 0, 0, None]
-    _try(L.lora_add_bf16, good, [
-        ({17: -1}, INV), ({18: -1}, INV), ({19: -1}, INV), ({20: -1}, INV), ({21: -1}, INV), ({12: -1}, INV),
-        ({0: 0}, INV), ({2: 0}, INV), ({5: 0}, INV), ({9: 0}, INV), ({10: 0}, INV), ({11: 0}, INV),
-        ({15: 0}, INV), ({1: 504}, INV), ({3: 504}, INV), ({6: 8}, INV), ({14: 255}, INV), ({16: 255}, INV),
-        ({4: 16 * 512 - 8}, INV), ({7: 256 * 16 - 8}, INV),
-        ({23: -1}, INV),
-        ({15: P5, 16: 264}, INV),             # in place with another leading dimension
-        ({21: 12}, SHAPE), ({21: 136, 6: 136}, SHAPE), ({20: 508}, SHAPE), ({18: 1025}, SHAPE),
-        ({0: P + 8}, ALIGN), ({2: P + 2}, ALIGN), ({5: P + 8}, ALIGN), ({1: 516}, ALIGN), ({3: 516, 4: 16 * 516}, ALIGN),
-        ({6: 20, 7: 256 * 24}, ALIGN), ({22: 0x80008}, ALIGN), ({15: 0x90001}, ALIGN), ({13: P5 + 1}, ALIGN),
-        ({8: P2 + 2}, ALIGN),
-        ({17: 0}, OK), ({19: 0}, OK),
+    names = ("X ldx A lda stride_a B ldb stride_b scale off row pair grp rows base ldbase out ldo T G N K r ws "
+             "wsbytes stream").split()
+    at = {n: i for i, n in enumerate(names)}
+
+    def args(**kw):
+        return [kw[n] for n in names]
+
+    def refuse(good, changes):
+        _try(L.lora_add_bf16, good, [({at[n]: v for n, v in c.items()}, st) for c, st in changes])
+    good = args(X=P, ldx=512, A=P, lda=512, stride_a=16 * 512, B=P, ldb=16, stride_b=256 * 16, scale=P2, off=P2, row=P2,
+                pair=P3, grp=P4, rows=256, base=P5, ldbase=256, out=0x90000, ldo=256, T=100, G=4, N=256, K=512, r=16,
+                ws=0, wsbytes=0, stream=None)
+    refuse(good, [
+        *[({n: -1}, INV) for n in ("T", "G", "N", "K", "r", "rows", "wsbytes")],
+        *[({n: 0}, INV) for n in ("X", "A", "B", "off", "row", "pair", "grp", "out")],
+        ({"ldx": 504}, INV), ({"lda": 504}, INV), ({"ldb": 8}, INV), ({"ldbase": 255}, INV), ({"ldo": 255}, INV),
+        ({"stride_a": 16 * 512 - 8}, INV), ({"stride_b": 256 * 16 - 8}, INV),
+        ({"out": P5, "ldo": 264}, INV),       # in place with another leading dimension
+        ({"r": 12}, SHAPE), ({"r": 136, "ldb": 136}, SHAPE), ({"K": 508}, SHAPE), ({"G": 1025}, SHAPE),
+        *[({n: P + 8}, ALIGN) for n in ("X", "A", "B")],
+        *[({n: P2 + 2}, ALIGN) for n in ("scale", "off", "row", "pair", "grp")],
+        ({"ldx": 516}, ALIGN), ({"lda": 516, "stride_a": 16 * 516}, ALIGN), ({"ldb": 20, "stride_b": 256 * 24}, ALIGN),
+        ({"ws": 0x80008}, ALIGN), ({"out": 0x90001}, ALIGN), ({"base": P5 + 1}, ALIGN),
+        ({"T": 0}, OK), ({"N": 0}, OK),
     ])
-    # few tokens of large adapters need a workspace
-    need = L.lora_add_workspace(100, 256, 4, 4096, 8192, 128)
-    assert need >= 256 * 128 * 4
-    big = [P, 8192, P, 8192, 128 * 8192, P, 128, 4096 * 128, P2, P2, P3, P4, 256, P5, 4096, 0x90000, 4096, 100,
-           4, 4096, 8192, 128, 0x80000, need, None]
-    _try(L.lora_add_bf16, big, [({22: 0}, INV), ({23: need - 1}, INV), ({22: 0x80008}, ALIGN)])
+    # large adapters, and many tokens, need a workspace
+    for T, rows, K, N, r in ((100, 256, 8192, 4096, 128), (8192, 8256, 512, 256, 16)):
+        need = L.lora_add_workspace(T, rows, 4, N, K, r)
+        assert need >= rows * r * 4
+        big = args(X=P, ldx=K, A=P, lda=K, stride_a=r * K, B=P, ldb=r, stride_b=N * r, scale=P2, off=P2, row=P2, pair=P3,
+                   grp=P4, rows=rows, base=P5, ldbase=N, out=0x90000, ldo=N, T=T, G=4, N=N, K=K, r=r, ws=0x80000,
+                   wsbytes=need, stream=None)
+        refuse(big, [({"ws": 0}, INV), ({"wsbytes": need - 1}, INV), ({"ws": 0x80008}, ALIGN)])
 
 
 def _plan(T=4, k=2, rows=8):
