@@ -33,28 +33,31 @@ static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : B
 // Stable counting sort of the pairs by group.
 //
 // Only a few bytes per pair move (4 read, 12 written), so the cost is latency: launches
-// and dependent steps.  Up to kSingle pairs one workgroup does everything in one
-// launch; more pairs are cut into chunks, counted by a first launch (hist[chunk][g]),
-// and a second launch, in which every workgroup sums the counts of all chunks itself
-// (coalesced reads from L2) instead of waiting for a scan launch, ranks its chunk.
+// and dependent steps.  Up to kSingle pairs one workgroup does everything in one launch.
+// More pairs are cut into chunks, counted by a first launch (hist[chunk][g]); in a second
+// one every workgroup sums the counts of all chunks itself (coalesced reads from L2)
+// instead of waiting for a scan launch, and places its chunk.
 //
-// Rank inside a chunk, in pair order: a wave takes 64 pairs; a lane's peers, the lanes
-// with its id, come from one ballot per id bit; its rank in the wave is the number of
-// peers below it and the lowest peer adds the wave's count to LDS.  A scan over the
-// waves per group then gives every wave its base.  No atomic decides an order, so the
-// result is the same on every run.
+// Ranks, in pair order: a wave takes 64 pairs; a lane's peers, the lanes with its id,
+// come from one ballot per id bit; its rank in the wave is the number of peers below it,
+// and the first peer stores the wave's count of that id in LDS.  A scan over the waves
+// per group then gives every wave its base, and the groups' sizes.  No atomic decides an
+// order, so the result is the same on every run.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSingle = 4096;        // most pairs one workgroup sorts alone
-constexpr int kMaxChunks = 256;      // workgroups of the two-launch form
+constexpr int kMaxSteps = 4;
+constexpr int kSingle = kMaxSteps * kSortThreads;   // most pairs one workgroup sorts alone
+constexpr int kMaxChunks = 256;                     // workgroups of the two-launch form
 
 struct SortArgs {
   const int32_t* ids;
   int64_t ld_ids;
   int32_t k;
+  int32_t flat;      // ids are contiguous: pair p's id is ids[p]
   int32_t n;         // pairs, T*k
   int32_t G;
+  int32_t bits;      // of the largest id, G - 1
   int32_t align;
   int32_t cap;       // > 0: masked layout
   int32_t chunk;     // pairs per workgroup, a multiple of kSortThreads
@@ -70,9 +73,24 @@ struct SortArgs {
 // Group of pair p, or -1 (an id outside [0, G), or p past the end).
 __device__ __forceinline__ int pair_group(const SortArgs& a, int p) {
   if (p >= a.n) return -1;
-  const int t = p / a.k;
-  const int id = a.ids[(int64_t)t * a.ld_ids + (p - t * a.k)];
+  int id;
+  if (a.flat) {
+    id = a.ids[p];
+  } else {
+    const int t = p / a.k;
+    id = a.ids[(int64_t)t * a.ld_ids + (p - t * a.k)];
+  }
   return (uint32_t)id < (uint32_t)a.G ? id : -1;
+}
+
+// Lanes of the wave whose g equals this lane's (g >= 0; for g = -1 the result is not used).
+__device__ __forceinline__ uint64_t same_group(int g, int bits) {
+  uint64_t peers = __ballot(g >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((g >> b) & 1);
+    peers &= (g >> b) & 1 ? set : ~set;
+  }
+  return peers;
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs a) {
@@ -88,7 +106,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs 
   for (int g = threadIdx.x; g < a.G; g += kSortThreads) a.hist[blockIdx.x * a.G + g] = cnt[g];
 }
 
-// Inclusive scan over the workgroup, one value per thread.
+// Inclusive scan over the workgroup, one value per thread (wave_sum is free on entry).
 __device__ __forceinline__ int block_incl_scan(int v, int32_t* wave_sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -98,12 +116,112 @@ __device__ __forceinline__ int block_incl_scan(int v, int32_t* wave_sum) {
   }
   if (lane == 63) wave_sum[wave] = v;
   __syncthreads();
-  int before = 0;
-  for (int w = 0; w < wave; ++w) before += wave_sum[w];
-  __syncthreads();
-  return v + before;
+  // the waves before this one: lanes 0 .. wave-1 hold their sums
+  int before = lane < wave ? wave_sum[lane & (kSortWaves - 1)] : 0;
+#pragma unroll
+  for (int d = 1; d < kSortWaves; d <<= 1) before += __shfl_xor(before, d, 64);
+  return v + __shfl(before, 0, 64);
 }
 
+// First rows of the groups from their sizes (cnt: thread g's group; 0 for g >= G), into
+// start[0 .. G]; workgroup 0 writes offsets.  Ends with a barrier.
+__device__ __forceinline__ void group_starts(const SortArgs& a, int cnt, int32_t* start, int32_t* wave_sum) {
+  const int tid = threadIdx.x;
+  if (a.cap > 0) {
+    if (tid <= a.G) start[tid] = tid * a.cap;
+    if (tid == 0) start[a.G] = a.G * a.cap;      // (G may be the number of threads)
+    if (blockIdx.x == 0 && tid < a.G) a.offsets[tid] = cnt < a.cap ? cnt : a.cap;
+  } else {
+    const int incl = block_incl_scan((cnt + a.align - 1) / a.align * a.align, wave_sum);
+    if (tid < a.G) start[tid + 1] = incl;
+    if (tid == 0) start[0] = 0;
+    if (blockIdx.x == 0) {
+      if (tid < a.G) a.offsets[tid + 1] = incl;
+      if (tid == 0) a.offsets[0] = 0;
+    }
+  }
+  __syncthreads();
+}
+
+// Places pair p of group g at position `at` of its group.
+__device__ __forceinline__ void place(const SortArgs& a, int p, int g, int at, const int32_t* start) {
+  if (p >= a.n) return;
+  int row = kNone;
+  if (g >= 0) {
+    if (a.cap == 0 || at < a.cap) row = start[g] + at;
+    if (row >= a.rows) row = kNone;   // the host's capacity check makes this unreachable
+  }
+  a.row_of[p] = row;
+  if (row >= 0) {
+    a.pair_of[row] = p;
+    a.row_group[row] = g;
+  }
+}
+
+// Rows without a pair: each group's from start + size on, and those behind the last group.
+// size(g): group g's pairs.  One thread per group for short paddings, a wave for long.
+template <class F>
+__device__ __forceinline__ void fill_rest(const SortArgs& a, const int32_t* start, F&& size) {
+  const int tid = blockIdx.x * kSortThreads + threadIdx.x, threads = gridDim.x * kSortThreads;
+  if (a.align > 1 || a.cap > 0) {
+    const int tpg = a.cap > 0 || a.align > 32 ? 64 : 1;
+    for (int g = tid / tpg; g < a.G; g += threads / tpg)
+      for (int r = start[g] + size(g) + tid % tpg; r < start[g + 1]; r += tpg) {
+        a.pair_of[r] = a.cap > 0 ? kOutside : kNone;
+        a.row_group[r] = kNone;
+      }
+  }
+  for (int r = start[a.G] + tid; r < a.rows; r += threads) {
+    a.pair_of[r] = kOutside;
+    a.row_group[r] = kNone;
+  }
+}
+
+// One workgroup, at most STEPS * kSortThreads pairs.
+template <int STEPS>
+__global__ __launch_bounds__(kSortThreads) void sort_single_kernel(const SortArgs a) {
+  constexpr int W = STEPS * kSortWaves;
+  __shared__ uint16_t wcnt[W][kMaxGroups];
+  __shared__ int32_t total[kMaxGroups], start[kMaxGroups + 1], wave_sum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int g[STEPS], rank[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) g[s] = pair_group(a, s * kSortThreads + tid);
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    uint16_t* const mine = wcnt[s * kSortWaves + wave];
+    for (int x = lane; x < (a.G + 1) / 2; x += 64) ((uint32_t*)mine)[x] = 0;
+    // (a wave's own row: its LDS accesses execute in order)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    const uint64_t peers = same_group(g[s], a.bits);
+    rank[s] = __popcll(peers & ((1ull << lane) - 1));
+    if (g[s] >= 0 && rank[s] == 0) mine[g[s]] = (uint16_t)__popcll(peers);
+  }
+  __syncthreads();
+  int cnt = 0;
+  if (tid < a.G) {
+#pragma unroll 16
+    for (int w = 0; w < W; ++w) {
+      const int c = wcnt[w][tid];
+      wcnt[w][tid] = (uint16_t)cnt;
+      cnt += c;
+    }
+    total[tid] = cnt;
+  }
+  group_starts(a, cnt, start, wave_sum);
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+    place(a, s * kSortThreads + tid, g[s],
+          g[s] >= 0 ? wcnt[s * kSortWaves + wave][g[s]] + rank[s] : 0, start);
+  fill_rest(a, start, [&](int gg) { return total[gg]; });
+}
+
+__global__ __launch_bounds__(kSortThreads) void no_rows_kernel(int32_t* row_of, int n) {
+  const int p = blockIdx.x * kSortThreads + threadIdx.x;
+  if (p < n) row_of[p] = kNone;
+}
+
+// Chunk blockIdx.x of several, after sort_hist_kernel.
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortArgs a) {
   __shared__ int32_t total[kMaxGroups];      // pairs of each group
   __shared__ int32_t next[kMaxGroups];       // pairs of each group in earlier chunks / steps
@@ -112,123 +230,56 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
   __shared__ int32_t wave_sum[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int p0 = blockIdx.x * a.chunk;
+  int g = pair_group(a, p0 + tid);
 
-  for (int g = tid; g < kMaxGroups; g += kSortThreads) total[g] = next[g] = 0;
+  if (tid < a.G) total[tid] = next[tid] = 0;
   __syncthreads();
-  if (a.nchunks == 1) {
-    for (int i = tid; i < a.chunk; i += kSortThreads) {
-      const int g = pair_group(a, i);
-      if (g >= 0) atomicAdd(&total[g], 1);
-    }
-  } else {
+  {
     // 2^s threads share a group and take every 2^s-th chunk (integer sums by LDS
     // atomics: any order gives the same result)
     int s = 0;
     while ((a.G << (s + 1)) <= kSortThreads) ++s;
-    const int parts = 1 << s, g = tid % a.G, part = tid / a.G;
+    const int parts = 1 << s, gg = tid % a.G, part = tid / a.G;
     if (part < parts) {
       int sum = 0, mine = 0;
-#pragma unroll 4
+#pragma unroll 16
       for (int c = part; c < a.nchunks; c += parts) {
-        const int v = a.hist[c * a.G + g];
+        const int v = a.hist[c * a.G + gg];
         sum += v;
         mine += c < (int)blockIdx.x ? v : 0;
       }
-      atomicAdd(&total[g], sum);
-      atomicAdd(&next[g], mine);
+      atomicAdd(&total[gg], sum);
+      atomicAdd(&next[gg], mine);
     }
   }
   __syncthreads();
+  group_starts(a, tid < a.G ? total[tid] : 0, start, wave_sum);
 
-  // group starts: padded counts, scanned (G <= kSortThreads: one group per thread)
-  const int cnt = tid < a.G ? total[tid] : 0;
-  if (a.cap > 0) {
-    if (tid < a.G) {
-      start[tid] = tid * a.cap;
-      if (blockIdx.x == 0) a.offsets[tid] = cnt < a.cap ? cnt : a.cap;
-    }
-    if (tid == 0) start[a.G] = a.G * a.cap;
-    __syncthreads();
-  } else {
-    const int pad = (cnt + a.align - 1) / a.align * a.align;
-    const int incl = block_incl_scan(pad, wave_sum);
-    if (tid < a.G) start[tid + 1] = incl;
-    if (tid == 0) start[0] = 0;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int g = tid; g <= a.G; g += kSortThreads) a.offsets[g] = start[g];
-  }
-
-  // ranks, kSortThreads pairs at a time
-  for (int i0 = 0; i0 < a.chunk; i0 += kSortThreads) {
-    if (p0 + i0 >= a.n) break;   // uniform over the workgroup
-    for (int x = tid; x < kSortWaves * (kMaxGroups / 2); x += kSortThreads)
-      ((uint32_t*)&wcnt[0][0])[x] = 0;
-    __syncthreads();
-    const int p = p0 + i0 + tid;
-    const int g = pair_group(a, p);
-    uint64_t peers = __ballot(g >= 0);
-    if (g < 0) peers = ~peers;
-#pragma unroll
-    for (int b = 0; b < 10; ++b) {
-      const uint64_t set = __ballot(g >= 0 && ((g >> b) & 1));
-      peers &= (g >> b) & 1 ? set : ~set;
-    }
+  for (int i0 = 0; i0 < a.chunk && p0 + i0 < a.n; i0 += kSortThreads) {   // uniform over the workgroup
+    if (i0 > 0) g = pair_group(a, p0 + i0 + tid);
+    for (int x = lane; x < (a.G + 1) / 2; x += 64) ((uint32_t*)&wcnt[wave][0])[x] = 0;
+    // (a wave's own row: its LDS accesses execute in order)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    const uint64_t peers = same_group(g, a.bits);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
     if (g >= 0 && rank == 0) wcnt[wave][g] = (uint16_t)__popcll(peers);
     __syncthreads();
-    for (int gg = tid; gg < a.G; gg += kSortThreads) {
-      int run = 0;
+    int run = 0;
+    if (tid < a.G) {
 #pragma unroll
       for (int w = 0; w < kSortWaves; ++w) {
-        const int c = wcnt[w][gg];
-        wcnt[w][gg] = (uint16_t)run;
+        const int c = wcnt[w][tid];
+        wcnt[w][tid] = (uint16_t)run;
         run += c;
       }
-      total[gg] = run;   // (the group totals are in `start` by now): this step's pairs
     }
     __syncthreads();
-    if (p < a.n) {
-      int row = kNone;
-      if (g >= 0) {
-        const int at = next[g] + wcnt[wave][g] + rank;
-        if (a.cap == 0 || at < a.cap) row = start[g] + at;
-        if (row >= a.rows) row = kNone;   // the host's capacity check makes this unreachable
-      }
-      a.row_of[p] = row;
-      if (row >= 0) {
-        a.pair_of[row] = p;
-        a.row_group[row] = g;
-      }
-    }
+    place(a, p0 + i0 + tid, g, g >= 0 ? next[g] + wcnt[wave][g] + rank : 0, start);
     __syncthreads();
-    for (int gg = tid; gg < a.G; gg += kSortThreads) next[gg] += total[gg];
+    if (tid < a.G) next[tid] += run;
     __syncthreads();
   }
-
-  // rows without a pair: a group's padding (or, masked, the rest of its capacity), one
-  // wave per group, then the rows behind the last group
-  const int nw = gridDim.x * kSortWaves, gw = blockIdx.x * kSortWaves + wave;
-  for (int g = gw; g < a.G; g += nw) {
-    int c;
-    if (a.nchunks == 1) {
-      c = next[g];
-    } else {
-      c = 0;
-      for (int ch = lane; ch < a.nchunks; ch += 64) c += a.hist[ch * a.G + g];
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, 64);
-    }
-    for (int r = start[g] + c + lane; r < start[g + 1]; r += 64) {
-      a.pair_of[r] = a.cap > 0 ? kOutside : kNone;
-      a.row_group[r] = kNone;
-    }
-  }
-  for (int r = start[a.G] + blockIdx.x * kSortThreads + tid; r < a.rows;
-       r += gridDim.x * kSortThreads) {
-    a.pair_of[r] = kOutside;
-    a.row_group[r] = kNone;
-  }
+  fill_rest(a, start, [&](int gg) { return total[gg]; });
 }
 
 // ---------------------------------------------------------------------------
@@ -663,15 +714,28 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
   a.row_group = row_group;
   a.rows = (int32_t)rows;
   a.hist = (int32_t*)workspace;
+  a.flat = ld_ids == k || T <= 1;
+  a.bits = G > 1 ? 32 - __builtin_clz((unsigned)(G - 1)) : 0;
   const int64_t steps = ceil_div(n > 0 ? n : 1, kSortThreads);
-  const bool single = n <= kSingle || G == 0;
-  a.nchunks = single ? 1 : (int32_t)(steps < kMaxChunks ? steps : kMaxChunks);
-  a.chunk = (int32_t)(ceil_div(steps, a.nchunks) * kSortThreads);
-  a.nchunks = (int32_t)ceil_div(n > 0 ? n : 1, a.chunk);
+  const hipStream_t st_ = (hipStream_t)stream;
   (void)hipGetLastError();
-  if (a.nchunks > 1)
-    hipLaunchKernelGGL(sort_hist_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, (hipStream_t)stream, a);
-  hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, (hipStream_t)stream, a);
+  if (G == 0 && n > 0) {      // no pair has a row
+    hipLaunchKernelGGL(no_rows_kernel, dim3((unsigned)ceil_div(n, kSortThreads)), dim3(kSortThreads), 0, st_, row_of,
+                       (int)n);
+    a.n = 0;
+  }
+  if (n <= kSingle || G == 0) {
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(1), dim3(kSortThreads), 0, st_, a); };
+    a.nchunks = 1;
+    if (steps <= 1 || G == 0) go(sort_single_kernel<1>);
+    else if (steps <= 2) go(sort_single_kernel<2>);
+    else go(sort_single_kernel<4>);
+  } else {
+    a.chunk = (int32_t)(ceil_div(steps, kMaxChunks) * kSortThreads);
+    a.nchunks = (int32_t)ceil_div(n, a.chunk);
+    hipLaunchKernelGGL(sort_hist_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, st_, a);
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, st_, a);
+  }
   return launch_status();
 }
 
