@@ -49,6 +49,8 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxSteps = 4;
 constexpr int kSingle = kMaxSteps * kSortThreads;   // most pairs one workgroup sorts alone
 constexpr int kMaxChunks = 256;                     // workgroups of the two-launch form
+constexpr int64_t kMaxPairs = int64_t(1) << 23;      // a chunk's counts fit 16 bits
+static_assert(kMaxGroups == kSortThreads && kMaxPairs / kMaxChunks < 65536, "one thread a group, 16-bit counts");
 
 struct SortArgs {
   const int32_t* ids;
@@ -67,7 +69,7 @@ struct SortArgs {
   int32_t* pair_of;
   int32_t* row_group;
   int32_t rows;
-  int32_t* hist;     // [nchunks][G]; unused with one chunk
+  uint32_t* hist;    // [nchunks][ceil(G/2)], two 16-bit counts a word; unused with one chunk
 };
 
 // Group of pair p, or -1 (an id outside [0, G), or p past the end).
@@ -95,7 +97,8 @@ __device__ __forceinline__ uint64_t same_group(int g, int bits) {
 
 __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs a) {
   __shared__ int32_t cnt[kMaxGroups];
-  for (int g = threadIdx.x; g < a.G; g += kSortThreads) cnt[g] = 0;
+  const int words = (a.G + 1) / 2;
+  for (int g = threadIdx.x; g < 2 * words; g += kSortThreads) cnt[g] = 0;
   __syncthreads();
   const int p0 = blockIdx.x * a.chunk;
   for (int i = threadIdx.x; i < a.chunk; i += kSortThreads) {
@@ -103,7 +106,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs 
     if (g >= 0) atomicAdd(&cnt[g], 1);   // a sum: the order does not matter
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < a.G; g += kSortThreads) a.hist[blockIdx.x * a.G + g] = cnt[g];
+  for (int w = threadIdx.x; w < words; w += kSortThreads)
+    a.hist[blockIdx.x * words + w] = (uint32_t)cnt[2 * w] | (uint32_t)cnt[2 * w + 1] << 16;
 }
 
 // Inclusive scan over the workgroup, one value per thread (wave_sum is free on entry).
@@ -232,24 +236,38 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
   const int p0 = blockIdx.x * a.chunk;
   int g = pair_group(a, p0 + tid);
 
-  if (tid < a.G) total[tid] = next[tid] = 0;
+  total[tid] = next[tid] = 0;      // kSortThreads == kMaxGroups
   __syncthreads();
   {
-    // 2^s threads share a group and take every 2^s-th chunk (integer sums by LDS
-    // atomics: any order gives the same result)
+    // 2^s threads share a word (two groups) and take every 2^s-th chunk (integer sums by
+    // LDS atomics: any order gives the same result)
+    const int words = (a.G + 1) / 2;
     int s = 0;
-    while ((a.G << (s + 1)) <= kSortThreads) ++s;
-    const int parts = 1 << s, gg = tid % a.G, part = tid / a.G;
+    while ((words << (s + 1)) <= kSortThreads) ++s;
+    const int parts = 1 << s, w = tid % words, part = tid / words;
     if (part < parts) {
-      int sum = 0, mine = 0;
-#pragma unroll 16
-      for (int c = part; c < a.nchunks; c += parts) {
-        const int v = a.hist[c * a.G + gg];
-        sum += v;
-        mine += c < (int)blockIdx.x ? v : 0;
+      int sum0 = 0, sum1 = 0, mine0 = 0, mine1 = 0;
+      for (int c0 = part; c0 < a.nchunks; c0 += 16 * parts) {
+        uint32_t v[16];       // in flight together
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = c0 + i * parts;
+          v[i] = a.hist[min(c, a.nchunks - 1) * words + w];
+          if (c >= a.nchunks) v[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const bool before = c0 + i * parts < (int)blockIdx.x;
+          sum0 += v[i] & 0xFFFF;
+          sum1 += v[i] >> 16;
+          mine0 += before ? v[i] & 0xFFFF : 0;
+          mine1 += before ? v[i] >> 16 : 0;
+        }
       }
-      atomicAdd(&total[gg], sum);
-      atomicAdd(&next[gg], mine);
+      atomicAdd(&total[2 * w], sum0);
+      atomicAdd(&total[2 * w + 1], sum1);
+      atomicAdd(&next[2 * w], mine0);
+      atomicAdd(&next[2 * w + 1], mine1);
     }
   }
   __syncthreads();
@@ -674,7 +692,7 @@ extern "C" {
 
 int64_t sort_tokens_workspace(int64_t pairs, int32_t G) {
   if (pairs <= kSingle || G <= 0) return 0;
-  return int64_t(4) * kMaxChunks * (G < kMaxGroups ? G : kMaxGroups);
+  return int64_t(4) * kMaxChunks * (((G < kMaxGroups ? G : kMaxGroups) + 1) / 2);
 }
 
 int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_t G, int32_t align,
@@ -682,7 +700,7 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
                 int64_t rows, void* workspace, int64_t workspace_bytes, void* stream) {
   if (T < 0 || k < 0 || G < 0 || align < 1 || cap < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
   if (cap > 0 && align != 1) return BSG_ERR_INVALID_ARG;
-  if (G > kMaxGroups) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (G > kMaxGroups || (k > 0 && T > kMaxPairs / k)) return BSG_ERR_UNSUPPORTED_SHAPE;
   const int st = plan_check(row_of, pair_of, true, T, k, rows, 0);
   if (st != BSG_OK) return st;
   const int64_t n = T * k;
@@ -713,7 +731,7 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
   a.pair_of = pair_of;
   a.row_group = row_group;
   a.rows = (int32_t)rows;
-  a.hist = (int32_t*)workspace;
+  a.hist = (uint32_t*)workspace;
   a.flat = ld_ids == k || T <= 1;
   a.bits = G > 1 ? 32 - __builtin_clz((unsigned)(G - 1)) : 0;
   const int64_t steps = ceil_div(n > 0 ? n : 1, kSortThreads);
