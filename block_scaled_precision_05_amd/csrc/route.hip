@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/bsg.h"
 #include "quant_math.h"
 
@@ -301,25 +303,33 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
 }
 
 // ---------------------------------------------------------------------------
-// Padding rows (pair_of == -1) zeroed by extra workgroups of the dispatch and backward
-// kernels: each looks at 64 rows and clears those that are padding.
+// The copying kernels move each byte once, and rows scattered over the matrices, so they
+// are bound by HBM; what helps is many requests in flight (a wave's loads are issued
+// together, 16 bytes a lane, 1 KiB an instruction) and, for matrices beyond the L2s (32
+// MiB in all), the non-temporal hint on what is read or written once and not shared:
+// rows that will not be read again then evict nothing (16384 tokens, 6 choices, 7168
+// wide: combine 273 against 320 us, FP8 dispatch 215 against 232; the gradient at 8192
+// tokens 353 against 378).  Smaller matrices keep the plain policy, so that the next
+// kernel finds them in L2.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kPadRows = 64;
+constexpr int kStreamAux = 2;                        // the non-temporal hint
+constexpr int64_t kStreamBytes = int64_t(32) << 20;  // matrices from this size on take it
+constexpr int kChunk = 8;                            // rows of a token in flight together
 
+// Padding rows (pair_of == -1) are zeroed by the kernels' first workgroups, each of which
+// looks at kPadRows rows (few: padding comes in runs, which many workgroups then share).
 // fill(row, lane) is called by one whole wave for every padding row of this block.
+constexpr int kPadRows = 16;
+
 template <class F>
 __device__ __forceinline__ void padding_rows(const int32_t* pair_of, int rows, int block, F&& fill) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = block * kPadRows + lane;
-  uint64_t pads = __ballot(r < rows && pair_of[r < rows ? r : rows - 1] == kNone);
-  int i = 0;
-  while (pads) {
-    const int b = __builtin_ctzll(pads);
-    pads &= pads - 1;
-    if (i++ % kWaves == wave) fill(block * kPadRows + b, lane);
-  }
+  uint64_t pads = __ballot(lane < kPadRows && r < rows && pair_of[r < rows ? r : rows - 1] == kNone);
+  for (int i = 0; pads; ++i, pads &= pads - 1)
+    if (i % kWaves == wave) fill(block * kPadRows + __builtin_ctzll(pads), lane);
 }
 
 // Buffer over one row: `bytes` long, or empty when the row index is not in [0, rows),
@@ -341,11 +351,13 @@ struct Vec;
 template <>
 struct Vec<8> {
   u32x4_t w;
+  template <int AUX>
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, AUX);
   }
+  template <int AUX>
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
-    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, AUX);
   }
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
@@ -359,11 +371,13 @@ struct Vec<8> {
 template <>
 struct Vec<1> {
   uint16_t w;
+  template <int AUX>
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    w = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    w = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, AUX);
   }
+  template <int AUX>
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
-    __builtin_amdgcn_raw_buffer_store_b16(w, r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(w, r, off, 0, AUX);
   }
   __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)w << 16); }
   __device__ __forceinline__ void set(const float (&v)[1]) {
@@ -371,35 +385,54 @@ struct Vec<1> {
   }
 };
 
+// Zeroes one row; one wave.
+template <int VEC, int AUX>
+__device__ __forceinline__ void zero_row(__amdgpu_buffer_rsrc_t row, uint32_t row_bytes, int lane) {
+  Vec<VEC> z;
+  const float zero[VEC] = {};
+  z.set(zero);
+  for (uint32_t off = 2u * VEC * lane; off < row_bytes; off += 128u * VEC) z.template store<AUX>(row, off);
+}
+
+// Rows of choices j .. j + KC - 1 of a token (n of them exist), -1 past the last.
+template <int KC>
+__device__ __forceinline__ void choice_rows(const int32_t* row_of, int n, int (&r)[KC]) {
+#pragma unroll
+  for (int j = 0; j < KC; ++j) r[j] = j < n ? row_of[j] : kNone;
+}
+
 // ---------------------------------------------------------------------------
 // Dispatch, bf16: row row_of[t][j] of the output is token t's row.  A wave owns one
 // segment of 64*VEC elements of one token, reads it once and writes it k times.
 // ---------------------------------------------------------------------------
-template <int VEC>
+template <int VEC, int AUX>
 __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ row_of,
     const int32_t* __restrict__ pair_of, int T, int k, int rows, int H, uint16_t* __restrict__ out,
-    int64_t ldo, int segs, int token_blocks) {
+    int64_t ldo, int segs, int pad_blocks) {
   const int lane = threadIdx.x & 63;
   const uint32_t row_bytes = 2u * (uint32_t)H;
-  if ((int)blockIdx.x >= token_blocks) {
-    padding_rows(pair_of, rows, blockIdx.x - token_blocks, [&](int r, int ln) {
-      const __amdgpu_buffer_rsrc_t o = row_rsrc(out, r, rows, 2 * ldo, row_bytes);
-      Vec<VEC> z;
-      const float zero[VEC] = {};
-      z.set(zero);
-      for (uint32_t off = 2u * VEC * ln; off < row_bytes; off += 128u * VEC) z.store(o, off);
+  if ((int)blockIdx.x < pad_blocks) {
+    padding_rows(pair_of, rows, blockIdx.x, [&](int r, int ln) {
+      zero_row<VEC, AUX>(row_rsrc(out, r, rows, 2 * ldo, row_bytes), row_bytes, ln);
     });
     return;
   }
-  const int64_t task = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task =
+      (int64_t)(blockIdx.x - pad_blocks) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
   if (t >= T) return;
   const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
+  const int32_t* ro = row_of + (int64_t)t * k;
   Vec<VEC> v;
-  v.load(row_rsrc(X, t, T, 2 * ldx, row_bytes), off);
-  for (int j = 0; j < k; ++j)
-    v.store(row_rsrc(out, row_of[(int64_t)t * k + j], rows, 2 * ldo, row_bytes), off);
+  v.template load<0>(row_rsrc(X, t, T, 2 * ldx, row_bytes), off);
+  for (int j0 = 0; j0 < k; j0 += kChunk) {
+    int r[kChunk];
+    choice_rows(ro + j0, k - j0, r);
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+      if (j0 + j < k) v.template store<AUX>(row_rsrc(out, r[j], rows, 2 * ldo, row_bytes), off);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -465,29 +498,30 @@ __device__ __forceinline__ int quantize16(uint32_t (&w)[8], uint32_t (&q)[4]) {
   return byte;
 }
 
-template <int FMT, int RULE>
+template <int FMT, int RULE, int AUX>
 __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ row_of,
     const int32_t* __restrict__ pair_of, int T, int k, int rows, int H, uint8_t* __restrict__ Q,
-    int64_t ldq, int16_t* __restrict__ sf, int64_t ld_sf, int segs, int token_blocks) {
+    int64_t ldq, int16_t* __restrict__ sf, int64_t ld_sf, int segs, int pad_blocks) {
   constexpr int GK = Fmt<FMT>::GK;
   constexpr int LPB = GK / 16;               // lanes per block
   constexpr int WPS = kQElems / GK / 2;      // packed words per segment: 4 (e4m3), 16 (e2m1)
   const int lane = threadIdx.x & 63;
   const uint32_t q_bytes = FMT == FMT_E4M3 ? (uint32_t)H : (uint32_t)H / 2;
   const int kb = H / GK, kp = (kb + 1) / 2;
-  if ((int)blockIdx.x >= token_blocks) {
+  if ((int)blockIdx.x < pad_blocks) {
     // a padding row is a quantised zero row: codes 0, scale bytes 0 (the filler 0x7F)
-    padding_rows(pair_of, rows, blockIdx.x - token_blocks, [&](int r, int ln) {
+    padding_rows(pair_of, rows, blockIdx.x, [&](int r, int ln) {
       const __amdgpu_buffer_rsrc_t o = row_rsrc(Q, r, rows, ldq, q_bytes);
-      for (uint32_t off = 8u * ln; off < q_bytes; off += 512u)
-        __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){0, 0}, o, off, 0, 0);
+      for (uint32_t off = 16u * ln; off < q_bytes; off += 1024u)
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4_t){0, 0, 0, 0}, o, off, 0, AUX);
       for (int i = ln; i < kp; i += 64)
         sf[(int64_t)i * ld_sf + r] = (int16_t)(2 * i + 1 < kb ? 0 : 0x7F00);
     });
     return;
   }
-  const int64_t task = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task =
+      (int64_t)(blockIdx.x - pad_blocks) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
   if (t >= T) return;
   const __amdgpu_buffer_rsrc_t xr = row_rsrc(X, t, T, 2 * ldx, 2u * (uint32_t)H);
@@ -503,13 +537,18 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
   const int lo = __shfl(byte, 2 * LPB * wi), hi = __shfl(byte, 2 * LPB * wi + LPB);
   const int pair = s * WPS + wi;
   const int word = lo | ((2 * pair + 1 < kb ? hi : 0x7F) << 8);
-  for (int j = 0; j < k; ++j) {
-    const __amdgpu_buffer_rsrc_t o =
-        row_rsrc(Q, row_of[(int64_t)t * k + j], rows, ldq, q_bytes);
-    if (FMT == FMT_E4M3)
-      __builtin_amdgcn_raw_buffer_store_b128((u32x4_t){q[0], q[1], q[2], q[3]}, o, e0, 0, 0);
-    else
-      __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){q[0], q[1]}, o, e0 / 2, 0, 0);
+  for (int j0 = 0; j0 < k; j0 += kChunk) {
+    int r[kChunk];
+    choice_rows(row_of + (int64_t)t * k + j0, k - j0, r);
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      if (j0 + j >= k) break;
+      const __amdgpu_buffer_rsrc_t o = row_rsrc(Q, r[j], rows, ldq, q_bytes);
+      if (FMT == FMT_E4M3)
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4_t){q[0], q[1], q[2], q[3]}, o, e0, 0, AUX);
+      else
+        __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){q[0], q[1]}, o, e0 / 2, 0, AUX);
+    }
   }
   // lanes WPS*j .. WPS*j + WPS-1 store row j's words
   for (int j0 = 0; j0 < k; j0 += 64 / WPS) {
@@ -523,31 +562,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
 
 // ---------------------------------------------------------------------------
 // Combine: out[t] = bf16( sum_j w[t][j] * Y[row_of[t][j]] ), fp32 sums in the order of
-// j, rounded once.  A wave owns 64*VEC elements of one token; the loads of up to eight
-// rows are in flight together.  A pair without a row reads zeros through an empty
-// buffer and its weight counts as zero.
+// j, rounded once.  A wave owns 64*VEC elements of one token; the loads of KC rows (all
+// of them up to eight choices) are in flight together.  A pair without a row reads zeros
+// through an empty buffer and its weight counts as zero.
 // ---------------------------------------------------------------------------
-constexpr int kChunk = 8;   // rows in flight
-
-template <int VEC, int KC>
-__device__ __forceinline__ void combine_chunk(const uint16_t* Y, int64_t ldy, int rows, int H,
-                                              const int32_t* row_of, const float* w, int n, uint32_t off,
-                                              float (&acc)[VEC]) {
-  Vec<VEC> v[KC];
-  float ww[KC];
-#pragma unroll
-  for (int j = 0; j < KC; ++j) {
-    const int r = j < n ? row_of[j] : kNone;
-    v[j].load(row_rsrc(Y, r, rows, 2 * ldy, 2u * (uint32_t)H), off);
-    ww[j] = (uint32_t)r < (uint32_t)rows ? (w ? w[j] : 1.0f) : 0.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < KC; ++j)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(ww[j], v[j].get(i), acc[i]);
-}
-
-template <int VEC>
+template <int VEC, int KC, int AUX>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
     const uint16_t* __restrict__ Y, int64_t ldy, const int32_t* __restrict__ row_of,
     const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
@@ -557,98 +576,123 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
   const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
   if (t >= T) return;
   const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
-  const int32_t* ro = row_of + (int64_t)t * k;
-  const float* w = W ? W + (int64_t)t * ldw : nullptr;
   float acc[VEC] = {};
-  for (int j = 0; j < k; j += kChunk)
-    combine_chunk<VEC, kChunk>(Y, ldy, rows, H, ro + j, w ? w + j : nullptr, min(kChunk, k - j), off, acc);
+  for (int j0 = 0; j0 < k; j0 += KC) {
+    int r[KC];
+    float w[KC];
+    Vec<VEC> v[KC];
+    choice_rows(row_of + (int64_t)t * k + j0, k - j0, r);
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      v[j].template load<AUX>(row_rsrc(Y, r[j], rows, 2 * ldy, 2u * (uint32_t)H), off);
+      w[j] = (uint32_t)r[j] < (uint32_t)rows ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(w[j], v[j].get(i), acc[i]);
+  }
   Vec<VEC> o;
   o.set(acc);
-  o.store(row_rsrc(out, t, T, 2 * ldo, 2u * (uint32_t)H), off);
+  o.template store<0>(row_rsrc(out, t, T, 2 * ldo, 2u * (uint32_t)H), off);
 }
 
 // ---------------------------------------------------------------------------
 // Gradient of combine: dY[row_of[t][j]] = bf16( w[t][j] * dO[t] ) and dW[t][j] =
 // <dO[t], Y[row_of[t][j]]> in fp32.  A workgroup owns a token: its waves take the
 // token's segments in turn, keep one partial dot product per choice and lane, and add
-// them over lanes and waves in a fixed order.  dO is read once per eight choices, Y
-// once, dY written once.
+// them over lanes and waves in a fixed order.  dO is read once per KC choices (all of
+// them up to eight), Y once, dY written once.
 // ---------------------------------------------------------------------------
-template <int VEC, int NW>
-__global__ __launch_bounds__(64 * NW) void combine_backward_kernel(
+template <int VEC, int KC, int AUX>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ dO, int64_t ldo, const uint16_t* __restrict__ Y, int64_t ldy,
     const int32_t* __restrict__ row_of, const int32_t* __restrict__ pair_of,
     const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
-    uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw, int segs) {
-  __shared__ float part[NW][kChunk];
+    uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw, int segs,
+    int pad_blocks) {
+  __shared__ float part[kWaves][KC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t row_bytes = 2u * (uint32_t)H;
-  if ((int)blockIdx.x >= T) {
-    padding_rows(pair_of, rows, blockIdx.x - T, [&](int r, int ln) {
-      const __amdgpu_buffer_rsrc_t o = row_rsrc(dY, r, rows, 2 * lddy, row_bytes);
-      Vec<VEC> z;
-      const float zero[VEC] = {};
-      z.set(zero);
-      for (uint32_t off = 2u * VEC * ln; off < row_bytes; off += 128u * VEC) z.store(o, off);
+  if ((int)blockIdx.x < pad_blocks) {
+    padding_rows(pair_of, rows, blockIdx.x, [&](int r, int ln) {
+      zero_row<VEC, AUX>(row_rsrc(dY, r, rows, 2 * lddy, row_bytes), row_bytes, ln);
     });
     return;
   }
-  const int t = blockIdx.x;
+  const int t = blockIdx.x - pad_blocks;
   const __amdgpu_buffer_rsrc_t g = row_rsrc(dO, t, T, 2 * ldo, row_bytes);
-  for (int j0 = 0; j0 < k; j0 += kChunk) {
-    const int32_t* ro = row_of + (int64_t)t * k + j0;
-    const int n = min(kChunk, k - j0);
-    int r[kChunk];
-    float w[kChunk], dot[kChunk] = {};
+  for (int j0 = 0; j0 < k; j0 += KC) {
+    const int n = k - j0;      // choices left; the last round may hold fewer than KC
+    int r[KC];
+    float w[KC], dot[KC] = {};
+    choice_rows(row_of + (int64_t)t * k + j0, n, r);
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      r[j] = j < n ? ro[j] : kNone;
-      w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
-    }
-    for (int s = wave; s < segs; s += NW) {
+    for (int j = 0; j < KC; ++j) w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
+    for (int s = wave; s < segs; s += kWaves) {
       const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
-      Vec<VEC> d, y[kChunk];
-      d.load(g, off);
+      Vec<VEC> d, y[KC];
+      d.template load<0>(g, off);
       if (dW) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) y[j].load(row_rsrc(Y, r[j], rows, 2 * ldy, row_bytes), off);
+        for (int j = 0; j < KC; ++j) y[j].template load<AUX>(row_rsrc(Y, r[j], rows, 2 * ldy, row_bytes), off);
       }
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        if (j >= n) break;
+      for (int j = 0; j < KC; ++j) {
         float v[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = w[j] * d.get(i);
         Vec<VEC> o;
         o.set(v);
-        o.store(row_rsrc(dY, r[j], rows, 2 * lddy, row_bytes), off);
+        // (choices past the last have no row: the store is dropped)
+        o.template store<AUX>(row_rsrc(dY, r[j], rows, 2 * lddy, row_bytes), off);
       }
       if (dW) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j)
+        for (int j = 0; j < KC; ++j)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
       }
     }
     if (!dW) continue;
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
+    for (int j = 0; j < KC; ++j) {
       float v = dot[j];
 #pragma unroll
       for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
       if (lane == 0) part[wave][j] = v;
     }
     __syncthreads();
-    if ((int)threadIdx.x < n) {
+    if ((int)threadIdx.x < (n < KC ? n : KC)) {
       float v = 0.0f;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) v += part[x][threadIdx.x];
+      for (int x = 0; x < kWaves; ++x) v += part[x][threadIdx.x];
       // (a pair without a row has read zeros; an infinity in dO must not turn its
       // gradient into NaN)
-      const int rr = ro[threadIdx.x];
+      const int rr = row_of[(int64_t)t * k + j0 + threadIdx.x];
       dW[(int64_t)t * lddw + j0 + threadIdx.x] = (uint32_t)rr < (uint32_t)rows ? v : 0.0f;
     }
     __syncthreads();
+  }
+}
+
+// f(KC, AUX) as compile-time constants: rows in flight (k up to kChunk), and the stream
+// hint or not.
+template <class F>
+static void with_chunk(int k, bool stream, F&& f) {
+  auto go = [&](auto kc) {
+    if (stream) f(kc, std::integral_constant<int, kStreamAux>{});
+    else f(kc, std::integral_constant<int, 0>{});
+  };
+  switch (k) {
+    case 0: case 1: go(std::integral_constant<int, 1>{}); break;
+    case 2: go(std::integral_constant<int, 2>{}); break;
+    case 3: go(std::integral_constant<int, 3>{}); break;
+    case 4: go(std::integral_constant<int, 4>{}); break;
+    case 5: go(std::integral_constant<int, 5>{}); break;
+    case 6: go(std::integral_constant<int, 6>{}); break;
+    case 7: go(std::integral_constant<int, 7>{}); break;
+    default: go(std::integral_constant<int, kChunk>{}); break;
   }
 }
 
@@ -766,12 +810,14 @@ int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const i
   if ((st = mat_check(out, ldo, H)) != BSG_OK) return st;
   const bool v = vec8(X, ldx, H) && vec8(out, ldo, H);
   const int64_t segs = ceil_div(H, v ? 512 : 64);
-  const int64_t tb = k > 0 ? ceil_div(T * segs, kWaves) : 0, blocks = tb + ceil_div(rows, kPadRows);
+  const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? ceil_div(T * segs, kWaves) : 0);
   if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  const bool big = 2 * T * k * H >= kStreamBytes;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(v ? dispatch_bf16_kernel<8> : dispatch_bf16_kernel<1>, dim3((unsigned)blocks),
-                     dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)X, ldx, row_of, pair_of,
-                     (int)T, k, (int)rows, (int)H, (uint16_t*)out, ldo, (int)segs, (int)tb);
+  hipLaunchKernelGGL((v ? (big ? dispatch_bf16_kernel<8, kStreamAux> : dispatch_bf16_kernel<8, 0>)
+                        : dispatch_bf16_kernel<1, 0>),
+                     dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)X, ldx,
+                     row_of, pair_of, (int)T, k, (int)rows, (int)H, (uint16_t*)out, ldo, (int)segs, (int)pads);
   return launch_status();
 }
 
@@ -795,14 +841,19 @@ static int dispatch_quant(const void* X, int64_t ldx, const int32_t* row_of, con
   if (T > 0 && (((uintptr_t)X & 15) || ldx % 8)) return BSG_ERR_MISALIGNED;
   if (((uintptr_t)Q & (qa - 1)) || ldq % qa || ((uintptr_t)sf & 1)) return BSG_ERR_MISALIGNED;
   const int64_t segs = ceil_div(H, kQElems);
-  const int64_t tb = k > 0 ? ceil_div(T * segs, kWaves) : 0, blocks = tb + ceil_div(rows, kPadRows);
+  const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? ceil_div(T * segs, kWaves) : 0);
   if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  const bool big = T * k * H / per >= kStreamBytes;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((rule == BSG_SCALE_CEIL ? dispatch_quant_kernel<FMT, BSG_SCALE_CEIL>
-                                             : dispatch_quant_kernel<FMT, BSG_SCALE_OCP_MX>),
-                     dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream,
-                     (const uint16_t*)X, ldx, row_of, pair_of, (int)T, k, (int)rows, (int)H,
-                     (uint8_t*)Q, ldq, sf, ld_sf, (int)segs, (int)tb);
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)X,
+                       ldx, row_of, pair_of, (int)T, k, (int)rows, (int)H, (uint8_t*)Q, ldq, sf, ld_sf,
+                       (int)segs, (int)pads);
+  };
+  if (rule == BSG_SCALE_CEIL)
+    big ? go(dispatch_quant_kernel<FMT, BSG_SCALE_CEIL, kStreamAux>) : go(dispatch_quant_kernel<FMT, BSG_SCALE_CEIL, 0>);
+  else
+    big ? go(dispatch_quant_kernel<FMT, BSG_SCALE_OCP_MX, kStreamAux>) : go(dispatch_quant_kernel<FMT, BSG_SCALE_OCP_MX, 0>);
   return launch_status();
 }
 
@@ -834,9 +885,14 @@ int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* 
   const int64_t segs = ceil_div(H, v ? 512 : 64), blocks = ceil_div(T * segs, kWaves);
   if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(v ? combine_kernel<8> : combine_kernel<1>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                     (hipStream_t)stream, (const uint16_t*)Y, ldy, row_of, W, ldw, (int)T, k, (int)rows,
-                     (int)H, (uint16_t*)out, ldo, (int)segs);
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)Y,
+                       ldy, row_of, W, ldw, (int)T, k, (int)rows, (int)H, (uint16_t*)out, ldo, (int)segs);
+  };
+  if (v)
+    with_chunk(k, 2 * T * k * H >= kStreamBytes, [&](auto kc, auto aux) { go(combine_kernel<8, kc.value, aux.value>); });
+  else
+    go(combine_kernel<1, kChunk, 0>);
   return launch_status();
 }
 
@@ -856,14 +912,20 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
   const bool v = (T == 0 || vec8(dO, ldo, H)) && (rows == 0 || vec8(dY, lddy, H)) &&
                  (!dW || rows == 0 || vec8(Y, ldy, H));
   const int64_t segs = ceil_div(H, v ? 512 : 64);
-  const int64_t tb = k > 0 ? T : 0, blocks = tb + ceil_div(rows, kPadRows);
+  const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? T : 0);
   if (blocks == 0) return BSG_OK;
   if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((v ? combine_backward_kernel<8, 4> : combine_backward_kernel<1, 4>),
-                     dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,
-                     ldo, (const uint16_t*)Y, ldy, row_of, pair_of, W, ldw, (int)tb, k, (int)rows, (int)H,
-                     (uint16_t*)dY, lddy, dW, lddw, (int)segs);
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,
+                       ldo, (const uint16_t*)Y, ldy, row_of, pair_of, W, ldw, (int)T, k, (int)rows, (int)H,
+                       (uint16_t*)dY, lddy, dW, lddw, (int)segs, (int)pads);
+  };
+  if (v)
+    with_chunk(k, 2 * T * k * H >= kStreamBytes,
+               [&](auto kc, auto aux) { go(combine_backward_kernel<8, kc.value, aux.value>); });
+  else
+    go(combine_backward_kernel<1, kChunk, 0>);
   return launch_status();
 }
 
