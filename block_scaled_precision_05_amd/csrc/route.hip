@@ -394,11 +394,27 @@ __device__ __forceinline__ void zero_row(__amdgpu_buffer_rsrc_t row, uint32_t ro
   for (uint32_t off = 2u * VEC * lane; off < row_bytes; off += 128u * VEC) z.template store<AUX>(row, off);
 }
 
-// Rows of choices j .. j + KC - 1 of a token (n of them exist), -1 past the last.
+// Rows of choices j .. j + KC - 1 of a token (n of them exist), -1 past the last; whether
+// any is a row.
 template <int KC>
-__device__ __forceinline__ void choice_rows(const int32_t* row_of, int n, int (&r)[KC]) {
+__device__ __forceinline__ bool choice_rows(const int32_t* row_of, int n, int (&r)[KC]) {
+  int all = kNone;      // the sign bit stays set unless a row clears it
 #pragma unroll
-  for (int j = 0; j < KC; ++j) r[j] = j < n ? row_of[j] : kNone;
+  for (int j = 0; j < KC; ++j) {
+    r[j] = j < n ? row_of[j] : kNone;
+    all &= r[j];
+  }
+  return all >= 0;
+}
+
+// Whether token t has a row at all.  With experts spread over GPUs many tokens have none
+// here, and are not read.
+__device__ __forceinline__ bool has_rows(const int32_t* row_of, int k) {
+  for (int j0 = 0; j0 < k; j0 += kChunk) {
+    int r[kChunk];
+    if (choice_rows(row_of + j0, k - j0, r)) return true;
+  }
+  return false;
 }
 
 // ---------------------------------------------------------------------------
@@ -424,6 +440,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
   if (t >= T) return;
   const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
   const int32_t* ro = row_of + (int64_t)t * k;
+  if (!has_rows(ro, k)) return;
   Vec<VEC> v;
   v.template load<0>(row_rsrc(X, t, T, 2 * ldx, row_bytes), off);
   for (int j0 = 0; j0 < k; j0 += kChunk) {
@@ -523,7 +540,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
   const int64_t task =
       (int64_t)(blockIdx.x - pad_blocks) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
-  if (t >= T) return;
+  if (t >= T || !has_rows(row_of + (int64_t)t * k, k)) return;
   const __amdgpu_buffer_rsrc_t xr = row_rsrc(X, t, T, 2 * ldx, 2u * (uint32_t)H);
   const uint32_t e0 = (uint32_t)(s * kQElems + 16 * lane);   // lane's first element
   const u32x4_t x0 = __builtin_amdgcn_raw_buffer_load_b128(xr, 2 * e0, 0, 0);
@@ -626,10 +643,11 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const int n = k - j0;      // choices left; the last round may hold fewer than KC
     int r[KC];
     float w[KC], dot[KC] = {};
-    choice_rows(row_of + (int64_t)t * k + j0, n, r);
+    // (a token without rows in this round reads nothing; its gradients are zeros)
+    const int my_segs = choice_rows(row_of + (int64_t)t * k + j0, n, r) ? segs : 0;
 #pragma unroll
     for (int j = 0; j < KC; ++j) w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
-    for (int s = wave; s < segs; s += kWaves) {
+    for (int s = wave; s < my_segs; s += kWaves) {
       const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
       Vec<VEC> d, y[KC];
       d.template load<0>(g, off);
