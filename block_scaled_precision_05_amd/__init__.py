@@ -599,9 +599,31 @@ def mqa_logits(fmt: str, Q, sfq, K, sfk, W, ks, ke, S: int, q_per_group: int | N
 
 
 # The calls below are short (a decode step's combine runs 4 us on the GPU), so their
-# host side is kept short too: checks that pass cost a few attribute reads.
+# host side is kept short too: on the current stream a call first goes to the compiled
+# marshalling, which takes it whole or returns None; what it leaves (empty tensors, other
+# streams and devices, every wrong argument) is checked and called here.
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_native_lock = threading.Lock()
+_native_module = None
+
+
+def _native():
+    """The compiled marshalling of these operators' usual calls (csrc/binding.cpp), on the
+    loaded libbsg.so."""
+    global _native_module
+    if _native_module is None:
+        from . import _binding
+        with _native_lock:
+            _binding.init(TokenSort, {n: ctypes.cast(getattr(lib(), n), _vp).value
+                                      for n in ("sort_tokens", "sort_tokens_workspace", "moe_dispatch_bf16",
+                                                "moe_dispatch_fp8", "moe_dispatch_fp4", "moe_combine",
+                                                "moe_combine_backward", "lora_add_bf16",
+                                                "lora_add_workspace")})
+            _native_module = _binding
+    return _native_module
 
 
 def _launch(t, stream, body):
@@ -660,6 +682,12 @@ def sort_tokens(ids, G: int, align: int = 1, cap: int = 0, out: TokenSort | None
     plan.offsets are the masked GEMM's counts.  ``out`` may pass a plan's four tensors
     (rows at least T*k + min(G, T*k)*(align-1), or G*cap), ``workspace`` a contiguous
     tensor of at least sort_tokens_workspace(T*k, G) bytes."""
+    if stream is None and ids.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).sort_tokens(dev, _raw_stream(dev), ids, G, align, cap) if out is workspace is None \
+            else None
+        if r is not None:
+            return r
     if ids.dtype != torch.int32 or ids.dim() != 2:
         raise TypeError("ids must be an int32 tensor [T, k]")
     T, k = ids.shape
@@ -732,6 +760,11 @@ def moe_dispatch_bf16(X, plan, out=None, stream=None):
     rows are zero and rows of no group (pair_of -2) keep what ``out`` held (they are
     uninitialised in a tensor allocated here).  The gradient with respect to X is
     moe_combine(gradient, plan)."""
+    if stream is None and X.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).moe_dispatch_bf16(dev, _raw_stream(dev), X, plan, out)
+        if r is not None:
+            return r
     row_of, pair_of, _, T, k, rows = _plan(plan, X, out)
     H = _width(X, "X")
     ldx = _ld(X, "X", torch.bfloat16, T, H)
@@ -747,6 +780,12 @@ def moe_dispatch_bf16(X, plan, out=None, stream=None):
 
 
 def _dispatch_quant(fn, X, plan, rule, per, gk, out, sf_out, stream):
+    if stream is None and X.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).moe_dispatch_quantized(
+            dev, _raw_stream(dev), per == 2, X, plan, SCALE_RULES.get(rule, -1), out, sf_out)
+        if r is not None:
+            return r
     row_of, pair_of, _, T, k, rows = _plan(plan, X, out, sf_out)
     H = _width(X, "X")
     ldx = _ld(X, "X", torch.bfloat16, T, H)
@@ -790,6 +829,11 @@ def moe_combine(Y, plan, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * Y[plan.row_of[t, j]] (bf16 [T, H], fp32 sums, rounded
     once); weights float32 [T, k], or None for ones (the gradient of the dispatch).  A
     pair without a row adds nothing."""
+    if stream is None and Y.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).moe_combine(dev, _raw_stream(dev), Y, plan, weights, out)
+        if r is not None:
+            return r
     row_of, _, _, T, k, rows = _plan(plan, Y, weights, out)
     H = _width(Y, "Y")
     ldy = _ld(Y, "Y", torch.bfloat16, rows, H)
@@ -810,6 +854,12 @@ def moe_combine_backward(dout, Y, plan, weights=None, need_weights: bool = True,
     """Gradients of moe_combine: (dY bf16 [rows, H], dW float32 [T, k]) from dout bf16
     [T, H].  Padding rows of dY are zero, rows of no group keep what ``out`` held.  With
     need_weights False dW is None and Y is not read (it may be None)."""
+    if stream is None and dout.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).moe_combine_backward(
+            dev, _raw_stream(dev), dout, Y, plan, weights, out) if need_weights else None
+        if r is not None:
+            return r
     row_of, pair_of, _, T, k, rows = _plan(plan, dout, Y, weights, out)
     H = _width(dout, "dout")
     ldd = _ld(dout, "dout", torch.bfloat16, T, H)
@@ -836,6 +886,12 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     align) with align a multiple of 16; scale float32 [G] or None; base bf16 [T, N] or
     None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
     aligned contiguous tensor of at least lora_add_workspace(T, rows, G, N, K, r) bytes."""
+    if stream is None and X.is_cuda:
+        dev = _current_device()
+        r = (_native_module or _native()).lora_add_bf16(
+            dev, _raw_stream(dev), X, A, B, plan, scale, base, out) if workspace is None else None
+        if r is not None:
+            return r
     row_of, pair_of, row_group, T, k, rows = _plan(plan, X, A, B, scale, base, out, workspace)
     offsets = plan[0]
     if k != 1:
