@@ -330,55 +330,11 @@ __device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int wa
 }
 
 // ---------------------------------------------------------------------------
-// One launch: a workgroup of 16 waves does a tile from X to out.  U stays in LDS.
-// ---------------------------------------------------------------------------
-constexpr int kFusedWaves = 16;
-
-template <int RF>
-__global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(const LoraArgs a) {
-  constexpr int NW = kFusedWaves;
-  __shared__ f32x4_t sums[NW][RF][64];
-  __shared__ URows<RF> u;
-  __shared__ Scratch scratch[NW];
-  if ((int)blockIdx.x >= a.tiles) {
-    copy_tokens(a, blockIdx.x - a.tiles, NW);
-    return;
-  }
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x;
-  const int t = row_token(a, tile * kTile + (lane & 15));
-  const int tr[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
-  const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
-  if (g < 0) return;
-  // rows without a token read the first row's: theirs are columns of their own in the
-  // products, and not stored
-  const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
-  add_columns<RF>(a, g, tr, u, scratch[wave], wave, (a.N + 63) / 64, NW, [&] {
-    f32x4_t acc[RF];
-    low_rank_rows<RF, 4 / RF>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, 0, a.K, wave, NW, acc);
-#pragma unroll
-    for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
-    __syncthreads();
-    const float s = a.scale ? a.scale[g] : 1.0f;
-    for (int i = threadIdx.x; i < URows<RF>::QUADS * kTile; i += 64 * NW) {
-      const int token = i & 15, r4 = i >> 4;       // ranks 4*r4 ..: fragment r4/4, lane group r4%4
-      f32x4_t v = {0, 0, 0, 0};
-      if (r4 < 4 * RF) {
-#pragma unroll
-        for (int w = 0; w < NW; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
-      }
-      u.put(token, 4 * r4, s * v, a.r);
-    }
-    __syncthreads();
-  });
-}
-
-// ---------------------------------------------------------------------------
-// Two launches.  What one CU can keep in flight bounds a workgroup to some 25 bytes per
-// ns, so NT tiles' slices of K and blocks of columns go to workgroups of their own.  The
-// S slices' sums of the first launch lie in slabs of U that every workgroup of the second
-// adds in order.  NT tiles of one adapter share each fragment of A_g and B_g; tiles of
-// different adapters in a workgroup are taken one adapter after the other.
+// Few tokens: two launches.  What one CU can keep in flight bounds a workgroup to some 25
+// bytes per ns (one launch in which a workgroup took its tile from X to out: one token of
+// rank 8, 7168 to 2048 wide, 10 us against 4 + 4), so each tile's slices of K, and then
+// its blocks of columns, go to workgroups of their own.  The S slices' sums lie in slabs
+// of U that every workgroup of the second launch adds in order.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWaves = 4;
 
@@ -714,12 +670,6 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static bool vec_ok(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
-// Whether a problem takes one launch: the adapter small enough for one workgroup to
-// stream, and tiles few enough that each has a CU.
-static bool one_launch(int64_t tiles, int64_t K, int64_t N, int64_t r) {
-  return r <= 32 && tiles <= 256 && r * (K + N) * 2 <= (int64_t(160) << 10);
-}
-
 // Whether the two-launch form takes several tiles of an adapter together: adapters with
 // tokens for that on average, and tiles enough to fill the chip with groups of them.
 static bool many_tokens(int64_t T, int64_t G, int64_t tiles) { return T >= 48 * G && tiles >= 256; }
@@ -738,7 +688,7 @@ static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K) {
 }
 
 template <int RF>
-static void launch_two(LoraArgs& a, int copy_blocks, hipStream_t st) {
+static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
   a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 128) * 128;
   const dim3 threads(64 * kSplitWaves);
   const int blocks = (int)ceil_div(a.N, 64);
@@ -758,20 +708,12 @@ static void launch_two(LoraArgs& a, int copy_blocks, hipStream_t st) {
   }
   a.items = a.tiles * a.S;
   hipLaunchKernelGGL(shrink_kernel<RF>, dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+  if (a.tiles == 0) return;
   // columns: workgroups for the whole chip, at least one block of 64 a wave
   const int want = (int)ceil_div(1024, a.tiles), most = (int)ceil_div(blocks, kSplitWaves);
   a.cols_per = (int)ceil_div(ceil_div(blocks, want < most ? want : most), kSplitWaves) * kSplitWaves;
   a.col_blocks = (int)ceil_div(blocks, a.cols_per);
   hipLaunchKernelGGL(expand_kernel<RF>, dim3((unsigned)(a.tiles * a.col_blocks)), threads, 0, st, a);
-}
-
-template <int RF>
-static void launch(LoraArgs& a, int copy_blocks, bool one, hipStream_t st) {
-  if (one)
-    hipLaunchKernelGGL((fused_kernel<RF <= 2 ? RF : 1>), dim3((unsigned)(a.tiles + copy_blocks)),
-                       dim3(64 * kFusedWaves), 0, st, a);
-  else
-    launch_two<RF>(a, copy_blocks, st);
 }
 
 }  // namespace bsg_lora
@@ -783,7 +725,6 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  if (one_launch(tiles, K, N, r)) return 0;
   const int64_t joined = many_tokens(T, G, tiles) ? 4 * tiles * kTile * padded_rank(r) : 0;
   return 4 * (int64_t)slices(T, G, tiles, K) * tiles * kTile * r + joined;
 }
@@ -848,17 +789,16 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   a.tiles = adapt ? (int32_t)ceil_div(rows, kTile) : 0;
   a.plain = !adapt;
   a.vec = vec_ok(out, ldo) && (!base || vec_ok(base, ld_base));
-  const bool one = !adapt || one_launch(a.tiles, K, N, r);
-  a.S = one ? 1 : slices(T, G, a.tiles, K);
+  a.S = adapt ? slices(T, G, a.tiles, K) : 1;
   const hipStream_t st = (hipStream_t)stream;
   // tokens without an adapter: nothing to do in place
   const int copy_blocks = base == out ? 0 : (int)ceil_div(T, 16);
-  if (a.tiles + copy_blocks == 0) return BSG_OK;
+  if (a.tiles + copy_blocks == 0) return BSG_OK;      // in place and nothing to add
   (void)hipGetLastError();
-  if (r <= 16) launch<1>(a, copy_blocks, one, st);
-  else if (r <= 32) launch<2>(a, copy_blocks, one, st);
-  else if (r <= 64) launch<4>(a, copy_blocks, one, st);
-  else launch<8>(a, copy_blocks, one, st);
+  if (r <= 16) launch<1>(a, copy_blocks, st);
+  else if (r <= 32) launch<2>(a, copy_blocks, st);
+  else if (r <= 64) launch<4>(a, copy_blocks, st);
+  else launch<8>(a, copy_blocks, st);
   return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
 }
 

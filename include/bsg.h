@@ -491,7 +491,7 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   with an alignment that is a multiple of 16, so that the 16 rows of a tile belong to
  *   one adapter (a plan that breaks this gives wrong rows).
  *   workspace: lora_add_workspace(T, rows, G, N, K, r) bytes, 16-byte aligned, no initial value
- *   needed (may be NULL when that is 0); calls that overlap need one each.
+ *   needed; calls that overlap need one each.
  *   Requires r % 8 == 0, r <= 128, K % 8 == 0, G <= 1024; X, A, B 16-byte aligned with
  *   leading dimensions and strides multiples of 8; any N (base and out 16-byte aligned
  *   with leading dimensions multiples of 8 move 16 bytes at a time). */
@@ -501,7 +501,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
                   const void* base, int64_t ld_base, void* out, int64_t ldo, int64_t T, int32_t G, int64_t N, int64_t K,
                   int32_t r, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of lora_add_bf16 for a plan of that many rows (0: none needed). */
+/* Workspace bytes of lora_add_bf16 for a plan of that many rows. */
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r);
 
 #ifdef __cplusplus

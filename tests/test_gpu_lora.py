@@ -55,7 +55,7 @@ CASES = [  # T, G, K, N, r, align
     (1, 1, 8, 1, 8, 16), (1, 4, 7168, 2048, 8, 16), (5, 3, 40, 65, 24, 16), (64, 32, 1032, 512, 16, 16),
     (33, 2, 520, 257, 40, 32), (130, 5, 2056, 384, 64, 16), (200, 3, 1024, 304, 128, 48),
     (70, 100, 256, 1000, 32, 16), (17, 1, 64, 63, 104, 16), (300, 6, 4096, 129, 96, 128),
-    # few tokens of large adapters: slices of K and blocks of columns of their own
+    # long rows: several slices of K
     (3, 2, 7168, 2048, 64, 16), (40, 5, 4104, 1001, 128, 16), (20, 3, 9000, 260, 72, 16)]
 
 
@@ -90,7 +90,6 @@ def test_lora_strided_operands_and_workspace():
         ids, plan, X, A, B, scale, base = _case(90, 4, K, 200, r, 7, pad=pad)
         rows = plan.pair_of.numel()
         need = bsg.lib().lora_add_workspace(90, rows, 4, 200, K, r)
-        assert (need > 0) == (K == 6000)
         ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)     # NaN as floats
         buf = torch.full((90, 211), 3.0, dtype=torch.bfloat16, device=DEV)
         out = bsg.lora_add_bf16(X, A, B, plan, scale, base, out=buf[:, :200], workspace=ws)

@@ -96,7 +96,9 @@ def test_combine_refusals():
 
 def test_lora_refusals():
     L = bsg.lib()
-    assert L.lora_add_workspace(100, 0, 4, 256, 512, 16) == 0 and L.lora_add_workspace(100, 256, 4, 256, 512, 16) == 0
+    assert L.lora_add_workspace(100, 0, 4, 256, 512, 16) == 0
+    need = L.lora_add_workspace(100, 256, 4, 256, 512, 16)
+    assert need >= 256 * 16 * 4
     names = ("X ldx A lda stride_a B ldb stride_b scale off row pair grp rows base ldbase out ldo T G N K r ws "
              "wsbytes stream").split()
     at = {n: i for i, n in enumerate(names)}
@@ -108,8 +110,9 @@ def test_lora_refusals():
         _try(L.lora_add_bf16, good, [({at[n]: v for n, v in c.items()}, st) for c, st in changes])
     good = args(X=P, ldx=512, A=P, lda=512, stride_a=16 * 512, B=P, ldb=16, stride_b=256 * 16, scale=P2, off=P2, row=P2,
                 pair=P3, grp=P4, rows=256, base=P5, ldbase=256, out=0x90000, ldo=256, T=100, G=4, N=256, K=512, r=16,
-                ws=0, wsbytes=0, stream=None)
+                ws=0x80000, wsbytes=need, stream=None)
     refuse(good, [
+        ({"ws": 0}, INV), ({"wsbytes": need - 1}, INV),
         *[({n: -1}, INV) for n in ("T", "G", "N", "K", "r", "rows", "wsbytes")],
         *[({n: 0}, INV) for n in ("X", "A", "B", "off", "row", "pair", "grp", "out")],
         ({"ldx": 504}, INV), ({"lda": 504}, INV), ({"ldb": 8}, INV), ({"ldbase": 255}, INV), ({"ldo": 255}, INV),
@@ -122,7 +125,6 @@ def test_lora_refusals():
         ({"ws": 0x80008}, ALIGN), ({"out": 0x90001}, ALIGN), ({"base": P5 + 1}, ALIGN),
         ({"T": 0}, OK), ({"N": 0}, OK),
     ])
-    # large adapters, and many tokens, need a workspace
     for T, rows, K, N, r in ((100, 256, 8192, 4096, 128), (8192, 8256, 512, 256, 16)):
         need = L.lora_add_workspace(T, rows, 4, N, K, r)
         assert need >= rows * r * 4
