@@ -86,14 +86,14 @@ __device__ __forceinline__ void mul_step(const u32x4_t& x, const u32x4_t (&av)[R
                                                      __builtin_bit_cast(bf16x8_t, x), acc[f], 0, 0, 0);
 }
 
-// The lane's row (l16) of each fragment of A_g, from its first chunk (lq) on.  Rows past r
+// The lane's row (l16) of RF fragments of A_g from f0 on, from its first chunk (lq) on.  Rows past r
 // repeat the last row; their sums are not used.
 template <int RF>
-__device__ __forceinline__ void a_rows(const LoraArgs& a, int g, const uint16_t* (&ap)[RF]) {
+__device__ __forceinline__ void a_rows(const LoraArgs& a, int g, int f0, const uint16_t* (&ap)[RF]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int f = 0; f < RF; ++f)
-    ap[f] = a.A + (int64_t)g * a.stride_a + (int64_t)min(16 * f + (lane & 15), a.r - 1) * a.lda + 8 * (lane >> 4);
+    ap[f] = a.A + (int64_t)g * a.stride_a + (int64_t)min(16 * (f0 + f) + (lane & 15), a.r - 1) * a.lda + 8 * (lane >> 4);
 }
 
 // k-steps k, k + stride, ... below k_hi, the last one partial: K is a multiple of 8, so a
@@ -125,7 +125,7 @@ template <int RF, int KS>
 __device__ __forceinline__ void low_rank_rows(const LoraArgs& a, int g, const uint16_t* x, int k_lo, int k_hi,
                                               int w, int nw, f32x4_t (&acc)[RF]) {
   const uint16_t* ap[RF];
-  a_rows<RF>(a, g, ap);
+  a_rows<RF>(a, g, 0, ap);
   x += 8 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
   for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
   }
 }
 
-// First product for many tokens: 64 rows of the plan against the whole rank, K in stages of
+// First product for many tokens: NT tiles of the plan against the whole rank, K in stages of
 // KC elements (128 or 256 bytes a row).  Fragments straight from global memory would ask for 64
 // bytes of each of 16 rows at a time, and what bounds the kernel is the number of requests
 // a CU keeps in flight; here the stages of X and A_g are copied to LDS by whole lines,
@@ -379,38 +379,37 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
 // The plan's capacity exceeds the rows in use (padding, tokens without an adapter), and
 // the unused rows are the last ones: only the used ones are dealt to the XCDs, or the
 // last XCD would stand idle.
-constexpr int kStageRows = 64;
-constexpr int kStageTiles = kStageRows / kTile;
-
-// Work items per 64 rows times the 64-row groups in use.
+// Work items per group of NT tiles times the groups in use.
+template <int NT>
 __device__ __forceinline__ int used_items(const LoraArgs& a, int per_group) {
   const int used = min(max(a.offsets[a.G], 0), a.rows);
-  return (used + kStageRows - 1) / kStageRows * per_group;
+  return (used + NT * kTile - 1) / (NT * kTile) * per_group;
 }
 
-// The adapters of kStageTiles tiles from tile0 on (-1: no token, or past the end), and the
-// runs of tiles that share one: next() moves to the tiles [i, i + n) of adapter g.
-// Wave-uniform; one load.
+// The adapters of NT tiles from tile0 on (-1: no token, or past the end), and the runs of
+// tiles that share one: next() moves to the tiles [i, i + n) of adapter g.  Wave-uniform;
+// one load.
+template <int NT>
 struct Runs {
-  int group[kStageTiles], i, n, g;
+  int group[NT], i, n, g;
   __device__ __forceinline__ Runs(const LoraArgs& a, int tile0) : i(0), n(0), g(-1) {
-    const int tile = tile0 + (int)(threadIdx.x & (kStageTiles - 1));
+    const int tile = tile0 + (int)(threadIdx.x & (NT - 1));
     const int v = tile < a.tiles ? tile_group(a, tile) : -1;
 #pragma unroll
-    for (int j = 0; j < kStageTiles; ++j) group[j] = __builtin_amdgcn_readlane(v, j);
+    for (int j = 0; j < NT; ++j) group[j] = __builtin_amdgcn_readlane(v, j);
   }
   __device__ __forceinline__ bool next() {
     i += n;
     n = 1;
 #pragma unroll
-    for (int j = 0; j < kStageTiles; ++j)
+    for (int j = 0; j < NT; ++j)
       if (j >= i && group[j] < 0 && j == i) ++i;
-    if (i >= kStageTiles) return false;
+    if (i >= NT) return false;
 #pragma unroll
-    for (int j = 0; j < kStageTiles; ++j)
+    for (int j = 0; j < NT; ++j)
       if (j == i) g = group[j];
 #pragma unroll
-    for (int j = 1; j < kStageTiles; ++j)
+    for (int j = 1; j < NT; ++j)
       if (j == i + n && group[j] == g) ++n;
     return true;
   }
@@ -435,34 +434,41 @@ __device__ __forceinline__ void stage_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-template <int RF, int KC, int NS>
-__global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const LoraArgs a) {
+constexpr int kShrinkTiles = 4;     // tiles of a workgroup, as many as waves
+constexpr int kExpandTiles = 4;
+
+template <int RF, int NT, int KC, int NS>
+__global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const LoraArgs a) {
   constexpr int ROW = 2 * KC, NC = KC / 8;      // bytes and 16-byte chunks of a row
   constexpr int RPC = 1024 / ROW;               // rows of one wave copy
-  constexpr int X_BYTES = kStageRows * ROW, STAGE = X_BYTES + 16 * RF * ROW;
+  constexpr int X_BYTES = NT * kTile * ROW, STAGE = X_BYTES + 16 * RF * ROW;
   constexpr int XC = 16 / RPC;                  // copies of X per wave and stage: its own tile
-  constexpr int AR = 4 * RF;                    // rows of A_g a wave copies
+  constexpr int AR = 16 * RF / NT;              // rows of A_g a wave copies
   constexpr int AC = AR >= RPC ? AR / RPC : 1;  // (fewer than a copy holds: part of its lanes)
   constexpr int COPIES = XC + AC;
   static_assert((NS - 1) * COPIES <= 63, "outstanding copies must fit the vmcnt counter");
+  // Waves: each its own tile and the whole rank or, from four rank fragments on, two
+  // tiles and half of the rank, which reads fewer fragments from LDS per MFMA.
+  constexpr int TW = RF >= 4 ? 2 : 1, FW = RF / TW;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE];
   if ((int)blockIdx.x >= a.items) {
-    copy_tokens(a, blockIdx.x - a.items, kSplitWaves);
+    copy_tokens(a, blockIdx.x - a.items, NT);
     return;
   }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int items = used_items(a, a.S);
+  const int tile_w = wave / TW * TW, frag_w = wave % TW * FW;
+  const int items = used_items<NT>(a, a.S);
   if ((int)blockIdx.x >= items) return;
   const int item = xcd_item(blockIdx.x, items);
-  const int tile0 = item / a.S * kStageTiles, slice = item % a.S;
+  const int tile0 = item / a.S * NT, slice = item % a.S;
   const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
   const int stages = (k_hi - k_lo) / KC;
 
-  Runs run(a, tile0);
+  Runs<NT> run(a, tile0);
   while (run.next()) {
     const int i = run.i, nt = run.n, g = run.g;
-    // this run's rows are [16 i, 16 (i + nt)) of the 64; the others, and rows without a
+    // this run's rows are [16 i, 16 (i + nt)) of the group; the others, and rows without a
     // token, read the run's first token (columns of their own, not used)
     const int t0 = max(__builtin_amdgcn_readfirstlane(row_token(a, (tile0 + i) * kTile)), 0);
     const uint16_t *xs[XC], *as[AC];
@@ -487,20 +493,24 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const Lor
       for (int c = 0; c < AC; ++c)
         if (AR >= RPC || cr < AR) lds_copy(as[c] + KC * s, b + X_BYTES + (AR * wave + RPC * c) * ROW);
     };
-    f32x4_t acc[RF];
+    f32x4_t acc[TW][FW];
 #pragma unroll
-    for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+    for (int j = 0; j < TW; ++j)
+#pragma unroll
+      for (int f = 0; f < FW; ++f) acc[j][f] = (f32x4_t){0, 0, 0, 0};
     auto compute = [&](int buf) {
       const uint8_t* const b = ring + buf * STAGE;
 #pragma unroll
       for (int h = 0; h < KC / 32; ++h) {
         // (rows 16 apart share the swizzle)
         const int off = l16 * ROW + (((4 * h + lq) ^ (l16 * ROW / 256 % NC)) << 4);
-        const u32x4_t xv = *(const u32x4_t*)(b + 16 * wave * ROW + off);
-        u32x4_t av[RF];
+        u32x4_t xv[TW], av[FW];
 #pragma unroll
-        for (int f = 0; f < RF; ++f) av[f] = *(const u32x4_t*)(b + X_BYTES + 16 * f * ROW + off);
-        mul_step<RF>(xv, av, acc);
+        for (int j = 0; j < TW; ++j) xv[j] = *(const u32x4_t*)(b + 16 * (tile_w + j) * ROW + off);
+#pragma unroll
+        for (int f = 0; f < FW; ++f) av[f] = *(const u32x4_t*)(b + X_BYTES + 16 * (frag_w + f) * ROW + off);
+#pragma unroll
+        for (int j = 0; j < TW; ++j) mul_step<FW>(xv[j], av, acc[j]);
       }
     };
     // (every wave has read the previous run's stages)
@@ -521,18 +531,21 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_many_kernel(const Lor
       compute(buf);
       buf = buf + 1 == NS ? 0 : buf + 1;
     }
-    if (wave >= i && wave < i + nt) {
-      const int row = (tile0 + wave) * kTile + l16;
+#pragma unroll
+    for (int j = 0; j < TW; ++j) {
+      const int tile = tile_w + j;
+      if (tile < i || tile >= i + nt) continue;
+      const int row = (tile0 + tile) * kTile + l16;
       if (k_lo + KC * stages < k_hi) {          // K's last elements
         const int t = row_token(a, row);
-        const uint16_t* ap[RF];
-        a_rows<RF>(a, g, ap);
-        tail_steps<RF>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + KC * stages, k_hi, 32, acc);
+        const uint16_t* ap[FW];
+        a_rows<FW>(a, g, frag_w, ap);
+        tail_steps<FW>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + KC * stages, k_hi, 32, acc[j]);
       }
 #pragma unroll
-      for (int f = 0; f < RF; ++f)
-        if (16 * f + 4 * lq < a.r)              // r % 8 == 0
-          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles * kTile + row) * a.r + 16 * f + 4 * lq) = acc[f];
+      for (int f = 0; f < FW; ++f)
+        if (16 * (frag_w + f) + 4 * lq < a.r)   // r % 8 == 0
+          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles * kTile + row) * a.r + 16 * (frag_w + f) + 4 * lq) = acc[j][f];
     }
   }
 }
@@ -608,13 +621,13 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   __shared__ Scratch scratch[kSplitWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int items = used_items(a, a.col_blocks);
+  const int items = used_items<kExpandTiles>(a, a.col_blocks);
   if ((int)blockIdx.x >= items) return;
   const int item = xcd_item(blockIdx.x, items);
-  const int tile0 = item / a.col_blocks * kStageTiles, c0 = item % a.col_blocks * CB;
+  const int tile0 = item / a.col_blocks * kExpandTiles, c0 = item % a.col_blocks * CB;
   const int tile = tile0 + wave;
   const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
-  Runs run(a, tile0);
+  Runs<kExpandTiles> run(a, tile0);
   bool first = true;
   while (run.next()) {
     const bool mine = wave >= run.i && wave < run.i + run.n;
@@ -682,7 +695,7 @@ static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 12
 // adds the slabs.
 static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K) {
   const bool many = many_tokens(T, G, tiles);
-  const int64_t s = many ? ceil_div(512, ceil_div(tiles, kStageTiles)) : 512 / tiles;
+  const int64_t s = many ? ceil_div(512, ceil_div(tiles, kShrinkTiles)) : 512 / tiles;
   const int64_t most = ceil_div(K, many ? 256 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
@@ -695,15 +708,16 @@ static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
   if (many_tokens(a.T, a.G, a.tiles)) {
     constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
     constexpr int CB = RF == 8 ? 2 : 4;
-    const int groups = (int)ceil_div(a.tiles, kStageTiles);
-    a.items = groups * a.S;
-    hipLaunchKernelGGL((shrink_many_kernel<RF, KC, NS>), dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+    a.items = (int)ceil_div(a.tiles, kShrinkTiles) * a.S;
+    hipLaunchKernelGGL((shrink_many_kernel<RF, kShrinkTiles, KC, NS>), dim3((unsigned)(a.items + copy_blocks)),
+                       dim3(64 * kShrinkTiles), 0, st, a);
     constexpr int ranks = 32 * URows<RF>::RK;
     a.UW = (__bf16*)(a.U + (int64_t)a.S * a.tiles * kTile * a.r);
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div((int64_t)a.tiles * kTile * (ranks / 4), 256)), dim3(256), 0,
                        st, a, ranks);
     a.col_blocks = (int)ceil_div(blocks, CB);
-    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)(groups * a.col_blocks)), threads, 0, st, a);
+    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)(ceil_div(a.tiles, kExpandTiles) * a.col_blocks)),
+                       threads, 0, st, a);
     return;
   }
   a.items = a.tiles * a.S;
