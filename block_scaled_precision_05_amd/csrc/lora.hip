@@ -683,9 +683,13 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static bool vec_ok(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
-// Whether the two-launch form takes several tiles of an adapter together: adapters with
-// tokens for that on average, and tiles enough to fill the chip with groups of them.
-static bool many_tokens(int64_t T, int64_t G, int64_t tiles) { return T >= 48 * G && tiles >= 256; }
+// Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
+// read a whole adapter from L2, T r / 16 elements a column; grouped, 64 tokens share it,
+// for one more launch and a pass per adapter in a group.  K = N = 4096, in us, tile by
+// tile / grouped:  T 512, r 128, G 1: 28 / 19;  T 1024, r 64, G 1: 24 / 18, G 8: 23 / 25;
+// T 4096, r 16, G 1: 32 / 26, G 8: 32 / 32, G 64: 35 / 40;  T 4096, r 64, G 64: 72 / 60;
+// T 1024, r 8, G 8: 13 / 20.
+static bool many_tokens(int64_t T, int64_t G, int64_t r) { return T * r >= 2048 * (30 + G); }
 
 // The rank up to which the kernels' fragments reach.
 static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
@@ -693,8 +697,8 @@ static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 12
 // Slices of K in the two-launch form: workgroups for the whole chip; with few tokens at
 // least 1024 elements a slice (two units a wave), as every workgroup of the second launch
 // adds the slabs.
-static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K) {
-  const bool many = many_tokens(T, G, tiles);
+static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K, int64_t r) {
+  const bool many = many_tokens(T, G, r);
   const int64_t s = many ? ceil_div(512, ceil_div(tiles, kShrinkTiles)) : 512 / tiles;
   const int64_t most = ceil_div(K, many ? 256 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
@@ -705,7 +709,7 @@ static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
   a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 128) * 128;
   const dim3 threads(64 * kSplitWaves);
   const int blocks = (int)ceil_div(a.N, 64);
-  if (many_tokens(a.T, a.G, a.tiles)) {
+  if (many_tokens(a.T, a.G, a.r)) {
     constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
     constexpr int CB = RF == 8 ? 2 : 4;
     a.items = (int)ceil_div(a.tiles, kShrinkTiles) * a.S;
@@ -739,8 +743,8 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  const int64_t joined = many_tokens(T, G, tiles) ? 4 * tiles * kTile * padded_rank(r) : 0;
-  return 4 * (int64_t)slices(T, G, tiles, K) * tiles * kTile * r + joined;
+  const int64_t joined = many_tokens(T, G, r) ? 4 * tiles * kTile * padded_rank(r) : 0;
+  return 4 * (int64_t)slices(T, G, tiles, K, r) * tiles * kTile * r + joined;
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
@@ -803,7 +807,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   a.tiles = adapt ? (int32_t)ceil_div(rows, kTile) : 0;
   a.plain = !adapt;
   a.vec = vec_ok(out, ldo) && (!base || vec_ok(base, ld_base));
-  a.S = adapt ? slices(T, G, a.tiles, K) : 1;
+  a.S = adapt ? slices(T, G, a.tiles, K, r) : 1;
   const hipStream_t st = (hipStream_t)stream;
   // tokens without an adapter: nothing to do in place
   const int copy_blocks = base == out ? 0 : (int)ceil_div(T, 16);

@@ -75,9 +75,11 @@ def test_lora_matches_oracle(T, G, K, N, r, align):
     _check(mine, X, A, B, ids, scale, base, "in place")
 
 
-# rows enough for two and four tiles a workgroup: 512 and 1024 tiles of 16 rows
+# T * r large for the number of adapters: tiles taken in groups; several adapters to a group
+# of 64 rows; K with and without elements past the last whole stage of 64
 @pytest.mark.parametrize("T,G,K,N,r", [(8000, 7, 128, 72, 16), (9000, 40, 64, 40, 64), (16300, 3, 136, 24, 8),
-                                       (15500, 90, 96, 33, 128), (16000, 1, 64, 64, 40)])
+                                       (15500, 90, 96, 33, 128), (16000, 1, 64, 64, 40), (4096, 100, 264, 130, 128),
+                                       (3000, 20, 1032, 520, 64), (2100, 2, 40, 300, 48), (2500, 1, 2048, 257, 104)])
 def test_lora_many_tokens(T, G, K, N, r):
     _say(f"lora_add T={T} G={G} K={K} N={N} r={r}")
     ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T)
