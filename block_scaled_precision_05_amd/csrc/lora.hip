@@ -599,7 +599,7 @@ __global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) 
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     __bf16 hh, ll;
-    split_bf16(s * v[e], hh, ll);
+    split_bf16(4 * r4 < a.r ? s * v[e] : 0.0f, hh, ll);    // (zero also where s is infinite)
     h[e] = hh;
     l[e] = ll;
   }
@@ -679,7 +679,9 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   }
 }
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxRows = int64_t(1) << 26;          // with kMaxBlocks: work-items of a launch
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // (256 a workgroup) fit 32 bits
+constexpr int64_t kMaxK = int64_t(1) << 30;
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static bool vec_ok(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
@@ -709,7 +711,7 @@ static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
   a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 128) * 128;
   const dim3 threads(64 * kSplitWaves);
   const int blocks = (int)ceil_div(a.N, 64);
-  if (many_tokens(a.T, a.G, a.r)) {
+  if (a.tiles > 0 && many_tokens(a.T, a.G, a.r)) {
     constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
     constexpr int CB = RF == 8 ? 2 : 4;
     a.items = (int)ceil_div(a.tiles, kShrinkTiles) * a.S;
@@ -754,7 +756,8 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
                   int32_t r, void* workspace, int64_t workspace_bytes, void* stream) {
   if (T < 0 || G < 0 || N < 0 || K < 0 || r < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
   if (r > 128 || r % 8 || K % 8) return BSG_ERR_UNSUPPORTED_SHAPE;
-  if (T > kMaxDim / 2 || rows > kMaxDim / 2 || N > (int64_t(1) << 23) || K > kMaxDim / 2 || G > 1024)
+  if (T > kMaxRows || rows > kMaxRows || N > (int64_t(1) << 23) || K > kMaxK || G > 1024 ||
+      ceil_div(rows, kExpandTiles * kTile) * ceil_div(N, 128) > kMaxBlocks)
     return BSG_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || N == 0) return BSG_OK;
   if (!out || ldo < N || !row_of || (base && ld_base < N)) return BSG_ERR_INVALID_ARG;

@@ -34,11 +34,16 @@ static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : B
 // ---------------------------------------------------------------------------
 // Stable counting sort of the pairs by group.
 //
-// Only a few bytes per pair move (4 read, 12 written), so the cost is latency: launches
-// and dependent steps.  Up to kSingle pairs one workgroup does everything in one launch.
-// More pairs are cut into chunks, counted by a first launch (hist[chunk][g]); in a second
-// one every workgroup sums the counts of all chunks itself (coalesced reads from L2)
-// instead of waiting for a scan launch, and places its chunk.
+// Only a few bytes per pair move (4 read, 12 written), so the cost is latency: launches,
+// dependent steps, and the scattered 4-byte writes, of which one CU finishes some two a
+// ns.  Up to kSingle pairs there is one launch, in which every workgroup sorts all the
+// pairs for itself, in LDS, and writes a share of the results (4096 pairs, 256 groups
+// padded to 128 rows: 7.4 us, 10.9 where one workgroup writes everything, 9.1 in two
+// launches; 768 pairs, 384 groups: 3.6 us).  More pairs are cut into chunks, counted by a
+// first launch (hist[chunk][g]); in a second one every workgroup sums the counts of all
+// chunks itself (coalesced reads from L2) instead of waiting for a scan launch, and
+// places its chunk, or a share of it where chunks are few (98304 pairs, 384 groups: 12.6
+// us with the gap between the launches; 24576 pairs 9.2, unshared 9.7).
 //
 // Ranks, in pair order: a wave takes 64 pairs; a lane's peers, the lanes with its id,
 // come from one ballot per id bit; its rank in the wave is the number of peers below it,
@@ -49,9 +54,10 @@ static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : B
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxSteps = 4;
-constexpr int kSingle = kMaxSteps * kSortThreads;   // most pairs one workgroup sorts alone
+constexpr int kSingle = kMaxSteps * kSortThreads;   // most pairs a workgroup sorts alone
 constexpr int kMaxChunks = 256;                     // workgroups of the two-launch form
 constexpr int64_t kMaxPairs = int64_t(1) << 23;      // a chunk's counts fit 16 bits
+constexpr int kSharePairs = 64, kFillRows = 2048;   // pairs and rows that a workgroup of the one-launch form writes
 static_assert(kMaxGroups == kSortThreads && kMaxPairs / kMaxChunks < 65536, "one thread a group, 16-bit counts");
 
 struct SortArgs {
@@ -66,6 +72,7 @@ struct SortArgs {
   int32_t cap;       // > 0: masked layout
   int32_t chunk;     // pairs per workgroup, a multiple of kSortThreads
   int32_t nchunks;
+  int32_t share;     // workgroups that share the placing of a chunk
   int32_t* offsets;
   int32_t* row_of;
   int32_t* pair_of;
@@ -183,7 +190,8 @@ __device__ __forceinline__ void fill_rest(const SortArgs& a, const int32_t* star
   }
 }
 
-// One workgroup, at most STEPS * kSortThreads pairs.
+// At most STEPS * kSortThreads pairs.  Every workgroup sorts them all; wave w's pairs are
+// written by workgroup w % workgroups, and the rows without a pair are shared out too.
 template <int STEPS>
 __global__ __launch_bounds__(kSortThreads) void sort_single_kernel(const SortArgs a) {
   constexpr int W = STEPS * kSortWaves;
@@ -206,19 +214,26 @@ __global__ __launch_bounds__(kSortThreads) void sort_single_kernel(const SortArg
   __syncthreads();
   int cnt = 0;
   if (tid < a.G) {
-#pragma unroll 16
-    for (int w = 0; w < W; ++w) {
-      const int c = wcnt[w][tid];
-      wcnt[w][tid] = (uint16_t)cnt;
-      cnt += c;
+#pragma unroll 1
+    for (int w0 = 0; w0 < W; w0 += 16) {
+      int c[16];      // read together: a store between two reads would make each wait
+#pragma unroll
+      for (int w = 0; w < 16; ++w) c[w] = wcnt[w0 + w][tid];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        wcnt[w0 + w][tid] = (uint16_t)cnt;
+        cnt += c[w];
+      }
     }
     total[tid] = cnt;
   }
   group_starts(a, cnt, start, wave_sum);
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s)
-    place(a, s * kSortThreads + tid, g[s],
-          g[s] >= 0 ? wcnt[s * kSortWaves + wave][g[s]] + rank[s] : 0, start);
+  for (int s = 0; s < STEPS; ++s) {
+    const int w = s * kSortWaves + wave;
+    if (w % gridDim.x == blockIdx.x)
+      place(a, s * kSortThreads + tid, g[s], g[s] >= 0 ? wcnt[w][g[s]] + rank[s] : 0, start);
+  }
   fill_rest(a, start, [&](int gg) { return total[gg]; });
 }
 
@@ -227,7 +242,7 @@ __global__ __launch_bounds__(kSortThreads) void no_rows_kernel(int32_t* row_of, 
   if (p < n) row_of[p] = kNone;
 }
 
-// Chunk blockIdx.x of several, after sort_hist_kernel.
+// One chunk of several, after sort_hist_kernel.
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortArgs a) {
   __shared__ int32_t total[kMaxGroups];      // pairs of each group
   __shared__ int32_t next[kMaxGroups];       // pairs of each group in earlier chunks / steps
@@ -235,7 +250,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
   __shared__ uint16_t wcnt[kSortWaves][kMaxGroups];
   __shared__ int32_t wave_sum[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int p0 = blockIdx.x * a.chunk;
+  const int chunk = blockIdx.x / a.share, part = blockIdx.x % a.share;
+  const int p0 = chunk * a.chunk;
   int g = pair_group(a, p0 + tid);
 
   total[tid] = next[tid] = 0;      // kSortThreads == kMaxGroups
@@ -246,10 +262,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
     const int words = (a.G + 1) / 2;
     int s = 0;
     while ((words << (s + 1)) <= kSortThreads) ++s;
-    const int parts = 1 << s, w = tid % words, part = tid / words;
-    if (part < parts) {
+    const int parts = 1 << s, w = tid % words, first = tid / words;
+    if (first < parts) {
       int sum0 = 0, sum1 = 0, mine0 = 0, mine1 = 0;
-      for (int c0 = part; c0 < a.nchunks; c0 += 16 * parts) {
+      for (int c0 = first; c0 < a.nchunks; c0 += 16 * parts) {
         uint32_t v[16];       // in flight together
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -259,7 +275,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const bool before = c0 + i * parts < (int)blockIdx.x;
+          const bool before = c0 + i * parts < chunk;
           sum0 += v[i] & 0xFFFF;
           sum1 += v[i] >> 16;
           mine0 += before ? v[i] & 0xFFFF : 0;
@@ -286,15 +302,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
     __syncthreads();
     int run = 0;
     if (tid < a.G) {
+      int c[kSortWaves];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) c[w] = wcnt[w][tid];
 #pragma unroll
       for (int w = 0; w < kSortWaves; ++w) {
-        const int c = wcnt[w][tid];
         wcnt[w][tid] = (uint16_t)run;
-        run += c;
+        run += c[w];
       }
     }
     __syncthreads();
-    place(a, p0 + i0 + tid, g, g >= 0 ? next[g] + wcnt[wave][g] + rank : 0, start);
+    if (wave % a.share == part) place(a, p0 + i0 + tid, g, g >= 0 ? next[g] + wcnt[wave][g] + rank : 0, start);
     __syncthreads();
     if (tid < a.G) next[tid] += run;
     __syncthreads();
@@ -718,7 +736,9 @@ static void with_chunk(int k, bool stream, F&& f) {
 // Host side
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;   // of kThreads: work-items of a launch fit 32 bits
 constexpr int kMaxK = 64;
+static_assert(kMaxBlocks * kThreads <= 0xFFFFFFFFll, "work-items of a launch");
 
 // Checks shared by the operators that use a sorted plan.  rows_used: tensors indexed by
 // row are touched.
@@ -805,7 +825,10 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
     a.n = 0;
   }
   if (n <= kSingle || G == 0) {
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(1), dim3(kSortThreads), 0, st_, a); };
+    int64_t blocks = ceil_div(n, kSharePairs);
+    blocks = blocks > ceil_div(rows, kFillRows) ? blocks : ceil_div(rows, kFillRows);
+    blocks = blocks < 1 ? 1 : (blocks < kMaxChunks ? blocks : kMaxChunks);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kSortThreads), 0, st_, a); };
     a.nchunks = 1;
     if (steps <= 1 || G == 0) go(sort_single_kernel<1>);
     else if (steps <= 2) go(sort_single_kernel<2>);
@@ -814,7 +837,8 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
     a.chunk = (int32_t)(ceil_div(steps, kMaxChunks) * kSortThreads);
     a.nchunks = (int32_t)ceil_div(n, a.chunk);
     hipLaunchKernelGGL(sort_hist_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, st_, a);
-    hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, st_, a);
+    a.share = kMaxChunks / a.nchunks < kSortWaves ? kMaxChunks / a.nchunks : kSortWaves;
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks * a.share), dim3(kSortThreads), 0, st_, a);
   }
   return launch_status();
 }
@@ -829,7 +853,7 @@ int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const i
   const bool v = vec8(X, ldx, H) && vec8(out, ldo, H);
   const int64_t segs = ceil_div(H, v ? 512 : 64);
   const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? ceil_div(T * segs, kWaves) : 0);
-  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   const bool big = 2 * T * k * H >= kStreamBytes;
   (void)hipGetLastError();
   hipLaunchKernelGGL((v ? (big ? dispatch_bf16_kernel<8, kStreamAux> : dispatch_bf16_kernel<8, 0>)
@@ -860,7 +884,7 @@ static int dispatch_quant(const void* X, int64_t ldx, const int32_t* row_of, con
   if (((uintptr_t)Q & (qa - 1)) || ldq % qa || ((uintptr_t)sf & 1)) return BSG_ERR_MISALIGNED;
   const int64_t segs = ceil_div(H, kQElems);
   const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? ceil_div(T * segs, kWaves) : 0);
-  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   const bool big = T * k * H / per >= kStreamBytes;
   (void)hipGetLastError();
   auto go = [&](auto kern) {
@@ -901,7 +925,7 @@ int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* 
   if ((uintptr_t)W & 3) return BSG_ERR_MISALIGNED;
   const bool v = (rows == 0 || vec8(Y, ldy, H)) && vec8(out, ldo, H);
   const int64_t segs = ceil_div(H, v ? 512 : 64), blocks = ceil_div(T * segs, kWaves);
-  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)Y,
@@ -932,7 +956,7 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
   const int64_t segs = ceil_div(H, v ? 512 : 64);
   const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? T : 0);
   if (blocks == 0) return BSG_OK;
-  if (blocks > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,

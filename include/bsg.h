@@ -430,7 +430,9 @@ int64_t sort_tokens_workspace(int64_t pairs, int32_t G);
  *   (X and out 16-byte aligned with ldx, ldo and H multiples of 8 move 16 bytes at a
  *   time).  X and out must not overlap.
  *   The gradient with respect to X is moe_combine of the gradient of out, without
- *   weights.  k <= 64, H <= 2^28. */
+ *   weights.  k <= 64, H <= 2^28; a call of more than 2^24 - 1 workgroups (one per 16
+ *   rows and one per 4 KiB of X, per 512 bytes where it moves single elements) is
+ *   refused, as in the operators below. */
 int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
                       int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo,
                       void* stream);
@@ -470,6 +472,7 @@ int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* 
  *   dW[t][j] = sum_h dO[t][h] * Y[row_of[t*k + j]][h]  (fp32; 0 for a pair without a
  *              row), in an order that is the same on every run.
  *   dW may be NULL (then Y is not read and may be NULL); W NULL means weights of one.
+ *   T + rows / 16 < 2^24.
  *   dY must not overlap dO or Y.  Alignment as moe_dispatch_bf16. */
 int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy, const int32_t* row_of,
                          const int32_t* pair_of, const float* W, int64_t ldw, int64_t T, int32_t k,
@@ -479,8 +482,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
 /* Low-rank adapters of many requests at once, beside a shared projection:
  *   out[t] = bf16( base[t] + scale[g] * B_g (A_g x_t) ),  g = the adapter of token t,
  *   out[t] = base[t] for a token without an adapter (row_of[t] < 0).
- * A_g x_t is summed in fp32 and enters the second product with a relative error of at
- * most 2^-16; the result is rounded once.
+ * A_g x_t is summed in fp32 and enters the second product as two bf16 terms, with a
+ * relative error of at most 2^-16; the result is rounded once.  (A zero second term
+ * against an infinite element of B_g gives NaN where the product would be infinite.)
  *   X: bf16 [T][ldx], K wide; A: bf16 [G][r][lda >= K], B: bf16 [G][N][ldb >= r] (expert
  *   strides in elements; adapters of lower rank are padded with zero rows of A and
  *   columns of B); scale: fp32 [G], or NULL for one.
@@ -492,7 +496,8 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   one adapter (a plan that breaks this gives wrong rows).
  *   workspace: lora_add_workspace(T, rows, G, N, K, r) bytes, 16-byte aligned, no initial value
  *   needed; calls that overlap need one each.
- *   Requires r % 8 == 0, r <= 128, K % 8 == 0, G <= 1024; X, A, B 16-byte aligned with
+ *   Requires r % 8 == 0, r <= 128, K % 8 == 0, G <= 1024, T and rows <= 2^26, N <= 2^23,
+ *   rows * N below 2^37; X, A, B 16-byte aligned with
  *   leading dimensions and strides multiples of 8; any N (base and out 16-byte aligned
  *   with leading dimensions multiples of 8 move 16 bytes at a time). */
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,

@@ -174,3 +174,76 @@ def test_lora_beside_a_projection_captured_and_streamed():
         graph.replay()
         got = done(captured)
         assert torch.equal(got, done(step()))
+
+
+def test_lora_many_tokens_without_anything_to_add():
+    """K = 0 and a plan of no rows, with as many tokens as the grouped forms take."""
+    _say("lora_add many tokens, K = 0, no rows")
+    e = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)
+    T, G, N, r = 4096, 2, 40, 64
+    plan = bsg.sort_tokens(torch.zeros(T, 1, dtype=torch.int32, device=DEV), G, align=16)
+    assert torch.equal(bsg.lora_add_bf16(e(T, 0), e(G, r, 0), e(G, N, r), plan, base=e(T, N)), e(T, N))
+    i = lambda *s: torch.full(s, -1, dtype=torch.int32, device=DEV)
+    none = (i(G + 1), i(T, 1), i(0), i(0))
+    assert torch.equal(bsg.lora_add_bf16(e(T, 64), e(G, r, 64), e(G, N, r), none, base=e(T, N)), e(T, N))
+
+
+def test_lora_many_tokens_that_must_not_spread():
+    """As above where tiles are grouped; an infinite scale, at a rank that is not a multiple
+    of 32, gives infinities and no NaN."""
+    T, G, K, N, r = 4200, 4, 192, 72, 40
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 3)
+    want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    t = int(torch.nonzero(ids[:, 0] == 1)[0])
+    X2, A2 = X.clone(), A.clone()
+    X2[t] = float("nan")
+    A2[2] = float("inf")
+    got = bsg.lora_add_bf16(X2, A2, B, plan, scale, base)
+    rest = (ids[:, 0] != 2) & (torch.arange(T, device=DEV) != t)
+    assert torch.equal(got[rest], want[rest]) and torch.all(torch.isnan(got[t]))
+    for T in (T, 60):       # grouped, and few tokens
+        ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 4)
+        scale[1] = float("inf")
+        got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
+        one = ids[:, 0] == 1
+        assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
+
+
+def test_lora_many_tokens_broken_plan_stays_in_bounds():
+    ids, plan, X, A, B, scale, base = _case(4096, 4, 128, 64, 16, 5, missing=0.0)
+    plan.row_group[:16] = 4
+    plan.row_group[16:32] = 2 ** 31 - 1
+    plan.pair_of[40::3] = 2 ** 31 - 1
+    for end in (2 ** 31 - 1, -5):
+        plan.offsets[-1] = end
+        bsg.lora_add_bf16(X, A, B, plan, scale, base)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [50, 5000])
+def test_lora_calls_with_and_without_a_stream_agree(T):
+    ids, plan, X, A, B, scale, base = _case(T, 4, 264, 200, 24, 3, pad=8)
+    cur = torch.cuda.current_stream()
+    for args in ((scale, base), (None, base), (scale, None), (None, None)):
+        assert torch.equal(bsg.lora_add_bf16(X, A, B, plan, *args), bsg.lora_add_bf16(X, A, B, plan, *args, stream=cur))
+    wide = torch.zeros(T, 211, dtype=torch.bfloat16, device=DEV)
+    bsg.lora_add_bf16(X, A, B, plan, scale, base, out=wide[:, :200])
+    assert torch.equal(wide[:, :200], bsg.lora_add_bf16(X, A, B, plan, scale, base)) and torch.all(wide[:, 200:] == 0)
+
+
+def test_lora_wrong_arguments_raise_on_the_gpu():
+    ids, plan, X, A, B, scale, base = _case(50, 4, 264, 200, 24, 3)
+    masked = bsg.sort_tokens(ids, 4, cap=64)
+    two = bsg.sort_tokens(ids.expand(50, 2).contiguous(), 4, align=16)
+    for f, error in ((lambda: bsg.lora_add_bf16(X, A, B, masked), ValueError),
+                     (lambda: bsg.lora_add_bf16(X, A, B, two), ValueError),
+                     (lambda: bsg.lora_add_bf16(X.half(), A, B, plan), TypeError),
+                     (lambda: bsg.lora_add_bf16(X, A.float(), B, plan), TypeError),
+                     (lambda: bsg.lora_add_bf16(X, A, B[:, :, :16], plan), ValueError),
+                     (lambda: bsg.lora_add_bf16(X, A, B, plan, scale[:3]), TypeError),
+                     (lambda: bsg.lora_add_bf16(X, A, B, plan, scale, base[:, :199]), ValueError),
+                     (lambda: bsg.lora_add_bf16(X, A, B, plan, out=base[:, :199]), ValueError),
+                     (lambda: bsg.lora_add_bf16(X[:, :260], A[:, :, :260], B, plan), bsg.BsgError),
+                     (lambda: bsg.lora_add_bf16(X, A, B, plan, workspace=scale), bsg.BsgError)):
+        with pytest.raises(error):
+            f()

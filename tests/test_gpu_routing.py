@@ -389,3 +389,100 @@ def test_masked_decode_layer():
     assert np.array_equal(_f64(Y)[kept], want_rows[kept])
     want, mag = routing.combine(want_rows, row_of, _np(W))
     _close(_f64(out), want, U8 * np.abs(want) + (1 + U8) * k * U24 * mag, "out")
+
+
+@pytest.mark.parametrize("T,k,G,align,cap", [
+    (64, 6, 256, 1, 1024), (700, 4, 37, 1, 3001), (30, 2, 1024, 512, 0), (900, 4, 64, 4096, 0), (1, 1, 3, 1, 70000)])
+def test_sort_with_many_more_rows_than_pairs(T, k, G, align, cap):
+    _say(f"sort_tokens T={T} k={k} G={G} align={align} cap={cap}")
+    ids = _ids(T, k, G, T + G)
+    rows = routing.rows_needed(T, k, G, align, cap) + 8192
+    e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+    out = bsg.TokenSort(e(G if cap else G + 1), e(T, k), e(rows), e(rows))
+    bsg.sort_tokens(torch.from_numpy(ids).to(DEV), G, align=align, cap=cap, out=out)
+    _check_plan(out, ids, G, align, cap, rows=rows)
+
+
+def test_calls_with_and_without_a_stream_agree():
+    """A call on the current stream goes through the compiled marshalling, one that names its
+    stream does not: same results, with and without given outputs, contiguous or not."""
+    _say("both ways into the library")
+    cur = torch.cuda.current_stream()
+    T, k, G, H = 300, 4, 12, 512
+
+    def agree(f, *args, **kw):
+        def run(**more):
+            for n in ("out", "sf_out"):
+                if n in kw:
+                    kw[n].zero_()
+            r = f(*args, **kw, **more)
+            return [x.clone() for x in ((r,) if torch.is_tensor(r) else r)]
+        a, b = run(), run(stream=cur)
+        for x, y in zip(a, b, strict=True):
+            assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y), f.__name__
+        return a
+
+    def filled(*s, dtype=torch.bfloat16):
+        return torch.zeros(s, dtype=dtype, device=DEV)
+    plan, X, Y, W, dO, rows = _case(T, k, G, 16, H, 3, ld_pad=8)
+    ids = torch.from_numpy(_ids(T, k, G, 3)).to(DEV)
+    for kw in ({}, {"align": 32}, {"cap": 40}):
+        assert isinstance(bsg.sort_tokens(ids, G, **kw), bsg.TokenSort)
+        agree(bsg.sort_tokens, ids, G, **kw)
+    # (rows of no group are not written: outputs that held zeros are compared whole)
+    agree(bsg.moe_dispatch_bf16, X, plan, out=filled(rows, H))
+    assert bsg.moe_dispatch_bf16(X, plan).shape == (rows, H)
+    for f, per, gk in ((bsg.moe_dispatch_fp8, 1, 128), (bsg.moe_dispatch_fp4, 2, 32)):
+        for rule in ("ceil", "ocp_mx"):
+            q, sf = filled(rows, H // per, dtype=torch.uint8), filled(H // gk // 2, rows + 3, dtype=torch.int16)
+            agree(f, X, plan, rule, out=q, sf_out=sf)
+            got = f(X, plan, rule)
+            real = plan.pair_of > -2
+            assert torch.equal(got[0][real], q[real]) and torch.equal(got[1][:, real], sf[:, :rows][:, real])
+    e4m3 = filled(rows, H, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    assert torch.equal(bsg.moe_dispatch_fp8(X, plan, out=e4m3)[0].view(torch.uint8), agree(
+        bsg.moe_dispatch_fp8, X, plan, out=filled(rows, H, dtype=torch.uint8), sf_out=sf.new_zeros(2, rows))[0])
+    agree(bsg.moe_combine, Y, plan, W)
+    agree(bsg.moe_combine, Y, tuple(plan))
+    wide = filled(T, H + 5)
+    agree(bsg.moe_combine, Y, plan, W, out=wide[:, :H])
+    assert torch.all(wide[:, H:] == 0)
+    agree(bsg.moe_combine_backward, dO, Y, plan, W, out=filled(rows, H))
+    agree(bsg.moe_combine_backward, dO, Y, plan, out=filled(rows, H))
+    dY, none = bsg.moe_combine_backward(dO, None, plan, W, need_weights=False, out=filled(rows, H))
+    assert none is None and torch.equal(dY, bsg.moe_combine_backward(dO, Y, plan, W, out=filled(rows, H))[0])
+
+
+def test_wrong_arguments_raise_on_the_gpu():
+    _say("refusals with tensors on the GPU")
+    plan, X, Y, W, dO, rows = _case(20, 3, 4, 16, 256, 3)
+    ids = torch.from_numpy(_ids(20, 3, 4, 3)).to(DEV)
+    half, host = X.half(), X.cpu()
+    bad_plan = bsg.TokenSort(plan.offsets, plan.row_of.long(), plan.pair_of, plan.row_group)
+    short = torch.zeros(rows - 1, 256, dtype=torch.bfloat16, device=DEV)
+    every_second = torch.zeros(rows, 512, dtype=torch.bfloat16, device=DEV)[:, ::2]
+    for f, error in (
+            (lambda: bsg.sort_tokens(ids.long(), 4), TypeError),
+            (lambda: bsg.sort_tokens(ids[:, 0], 4), TypeError),
+            (lambda: bsg.sort_tokens(ids, 4, align=0), ValueError),
+            (lambda: bsg.sort_tokens(ids, -1), ValueError),
+            (lambda: bsg.sort_tokens(ids, 1025), bsg.BsgError),
+            (lambda: bsg.sort_tokens(ids, 4, align=16, cap=8), bsg.BsgError),
+            (lambda: bsg.moe_dispatch_bf16(half, plan), TypeError),
+            (lambda: bsg.moe_dispatch_bf16(X, bad_plan), TypeError),
+            (lambda: bsg.moe_dispatch_bf16(X[:19], plan), ValueError),
+            (lambda: bsg.moe_dispatch_bf16(X, plan, out=short), ValueError),
+            (lambda: bsg.moe_dispatch_bf16(X, plan, out=every_second), ValueError),
+            (lambda: bsg.moe_dispatch_bf16(host, plan), ValueError),
+            (lambda: bsg.moe_dispatch_fp8(X, plan, rule="floor"), ValueError),
+            (lambda: bsg.moe_dispatch_fp8(X[:, :200], plan), bsg.BsgError),
+            (lambda: bsg.moe_dispatch_fp8(X[:, 4:132], plan), bsg.BsgError),
+            (lambda: bsg.moe_dispatch_fp8(X, plan, sf_out=torch.zeros(1, rows - 1, dtype=torch.int16, device=DEV)),
+             ValueError),
+            (lambda: bsg.moe_combine(short, plan), ValueError),
+            (lambda: bsg.moe_combine(Y, plan, W.bfloat16()), TypeError),
+            (lambda: bsg.moe_combine(Y, plan, W[:, :2]), ValueError),
+            (lambda: bsg.moe_combine_backward(dO, None, plan, W), ValueError),
+            (lambda: bsg.moe_combine_backward(dO, short, plan, W), ValueError)):
+        with pytest.raises(error):
+            f()

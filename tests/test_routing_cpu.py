@@ -134,6 +134,26 @@ def test_lora_refusals():
         refuse(big, [({"ws": 0}, INV), ({"wsbytes": need - 1}, INV), ({"ws": 0x80008}, ALIGN)])
 
 
+def test_launches_past_the_grid_limit_are_refused():
+    """2^24 workgroups of 256 work-items would not fit a launch."""
+    L = bsg.lib()
+    #                         X  ldx   row pair T        k  rows     H     out ldo   stream
+    _try(L.moe_dispatch_bf16, [P, 2048, P2, P3, 1 << 24, 1, 1, 2048, P4, 2048, None], [({}, SHAPE)])
+    _try(L.moe_dispatch_bf16, [P, 8, P2, P3, 1, 1, 1 << 28, 8, P4, 8, None], [({}, SHAPE)])
+    _try(L.moe_dispatch_fp8, [P, 4096, P2, P3, 1 << 24, 1, 1, 4096, P4, 4096, P5, 1, 0, None], [({}, SHAPE)])
+    #                   Y  ldy   row W  ldw T        k  rows H     out ldo   stream
+    _try(L.moe_combine, [P, 2048, P2, P3, 1, 1 << 24, 1, 1, 2048, P4, 2048, None],
+         [({}, SHAPE), ({5: 1 << 23, 8: 2047}, SHAPE)])      # an odd width: element-wise
+    #                            dO ldo Y ldy row pair W  ldw T      k  rows H  dY lddy dW  lddw stream
+    _try(L.moe_combine_backward, [P, 8, P, 8, P2, P3, P4, 1, 1 << 24, 1, 1, 8, P5, 8, P2, 1, None], [({}, SHAPE)])
+    T, G, N, K, r = 1 << 20, 4, 1 << 22, 64, 16
+    need = L.lora_add_workspace(T, T, G, N, K, r)
+    #                     X  ldx A  lda sa      B  ldb sb      sc off row pair grp rows base ldb out ldo
+    _try(L.lora_add_bf16, [P, K, P, K, r * K, P, r, N * r, 0, P2, P2, P3, P4, T, P5, N, 0x90000, N, T, G, N, K, r,
+                           0x80000, need, None],
+         [({}, SHAPE), ({13: (1 << 26) + 1}, SHAPE), ({18: (1 << 26) + 1}, SHAPE), ({20: (1 << 23) + 8}, SHAPE)])
+
+
 def _plan(T=4, k=2, rows=8):
     e = lambda *s: torch.zeros(s, dtype=torch.int32)
     return bsg.TokenSort(e(3), e(T, k), e(rows), e(rows))
