@@ -7,11 +7,16 @@
 // rows of X, base and out stay where they are: a tile gathers its 16 tokens.
 //
 // An adapter of rank r does r multiply-adds per element of X and of out, far under the
-// matrix cores' rate: the work is bound by memory, and for few tokens by latency.  So
-// operands go straight from global memory to MFMA fragments (v_mfma_f32_16x16x32_bf16:
-// 16 rows of A_g or B_g against 16 tokens), X, base and out are touched once, and the
-// adapters come from L2 (consecutive tiles, which mostly share an adapter, run on one
-// XCD).
+// matrix cores' rate (v_mfma_f32_16x16x32_bf16, 16 rows of A_g or B_g against 16 tokens):
+// the work is bound by memory, and for few tokens by latency.  X, base and out should
+// move once, at the rate of HBM, and the adapters come from L2.
+//   Few tokens: shrink_kernel (U in S slices of K), expand_kernel; operands go straight
+//     from global memory to MFMA fragments.  64 tokens of 32 adapters, rank 16, 7168 to
+//     2048 wide: 4.7 + 5.2 us; 1 token, rank 8: 3.8 + 5.0.
+//   Many tokens: shrink_many_kernel, join_kernel, expand_many_kernel; 64 tokens share an
+//     adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64, 7168 to 4096
+//     wide: 36 + 5 + 27 us, where the 263 MB take 54 us at the rate of a copy.
+// A token without an adapter is copied by the first launch's last workgroups.
 //
 // U = s_g A_g x is summed in fp32 and keeps that precision through the second product:
 // it enters as two bf16 terms, U = hi + lo with lo = bf16(U - hi), two MFMAs, a relative
@@ -26,6 +31,7 @@ namespace bsg_lora {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any_t;   // at any element
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
 
@@ -51,8 +57,8 @@ struct LoraArgs {
   __bf16* UW;             // many tokens: [tiles*16][hi, lo][rank padded to 32]
   int32_t T, G, K, N, r, rows, tiles, S;
   int32_t k_per;          // elements of K per slice, a multiple of 128
+  int32_t parts;          // few tokens: workgroups that share the rank of a slice
   int32_t plain;          // K, r or G is 0: no token has anything to add
-  int32_t vec;            // base and out allow 16-byte accesses
   int32_t items;          // first launch: workgroups with tiles; the others copy tokens
   int32_t col_blocks;     // second launch: workgroups that share a tile's columns, and the
   int32_t cols_per;       // 64-column blocks of each
@@ -114,18 +120,18 @@ __device__ __forceinline__ void tail_steps(const uint16_t* x, const uint16_t* co
 }
 
 // ---------------------------------------------------------------------------
-// First product for few tokens: the wave's share of A_g x for one tile, columns [k_lo,
-// k_hi) of K (k_lo a multiple of 32).  The wave takes units of 32*KS elements, every
+// First product for few tokens: the wave's share of A_g x for one tile, rank rows 16 f0 ..
+// 16 (f0 + RF), columns [k_lo, k_hi) of K (k_lo a multiple of 32).  The wave takes units of 32*KS elements, every
 // nw-th one, straight from global memory to fragments, with the next unit's loads in
 // flight while this one's MFMAs run; the last, partial unit goes in k-steps.  The two
 // halves of a 128-byte line are requested back to back.  Lane (lq, l16) ends up with
 // rank rows 16f + 4lq .. +3 of token l16.
 // ---------------------------------------------------------------------------
 template <int RF, int KS>
-__device__ __forceinline__ void low_rank_rows(const LoraArgs& a, int g, const uint16_t* x, int k_lo, int k_hi,
+__device__ __forceinline__ void low_rank_rows(const LoraArgs& a, int g, int f0, const uint16_t* x, int k_lo, int k_hi,
                                               int w, int nw, f32x4_t (&acc)[RF]) {
   const uint16_t* ap[RF];
-  a_rows<RF>(a, g, 0, ap);
+  a_rows<RF>(a, g, f0, ap);
   x += 8 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
   for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
@@ -199,7 +205,8 @@ struct URows {
 // t[j]: the token of row 8j + lane/8, -1 for none.  The next block's B_g and
 // base are in flight while this one is formed, the first block's while form_u puts U into
 // LDS.  out is stored with the non-temporal hint: it is not read here, and left in L2 it
-// would evict the adapters.
+// would evict the adapters.  base and out may start at any element (8192 tokens, rank 64,
+// 7168 to 4097 wide: 95 us, by single elements 149; 4096 wide 73).
 // ---------------------------------------------------------------------------
 // Four columns (quad) of a row sit at quad ^ row, so that 16 rows' writes of one quad, and
 // two rows' reads of eight, cover the banks once.
@@ -214,8 +221,8 @@ __device__ __forceinline__ void load_base(const LoraArgs& a, const int (&t)[2], 
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     base[j] = (u32x4_t){0, 0, 0, 0};
-    if (a.base && t[j] >= 0 && a.vec && n0 + 8 <= a.N)
-      base[j] = *(const u32x4_t*)(a.base + (int64_t)t[j] * a.ld_base + n0);
+    if (a.base && t[j] >= 0 && n0 + 8 <= a.N)
+      base[j] = *(const u32x4_any_t*)(a.base + (int64_t)t[j] * a.ld_base + n0);
   }
 }
 
@@ -248,7 +255,7 @@ __device__ __forceinline__ void add_block(const LoraArgs& a, const int (&t)[2], 
     const f32x4_t d1 = scratch.at(8 * j + (lane >> 3), 2 * (lane & 7) + 1);
     if (t[j] < 0) continue;
     uint16_t* orow = a.out + (int64_t)t[j] * a.ldo + n0;
-    if (a.vec && n0 + 8 <= a.N) {
+    if (n0 + 8 <= a.N) {
       u32x4_t o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -256,7 +263,7 @@ __device__ __forceinline__ void add_block(const LoraArgs& a, const int (&t)[2], 
         const float x1 = (e < 2 ? d0[2 * e + 1] : d1[2 * e - 3]) + __uint_as_float(base[j][e] & 0xFFFF0000u);
         o[e] = __builtin_bit_cast(uint32_t, (bf16x2_t){(__bf16)x0, (__bf16)x1});
       }
-      __builtin_nontemporal_store(o, (u32x4_t*)orow);
+      __builtin_nontemporal_store(o, (u32x4_any_t*)orow);
     } else {
       const uint16_t* brow = a.base + (int64_t)t[j] * a.ld_base + n0;
 #pragma unroll
@@ -316,7 +323,7 @@ __device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int wa
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mine = block * 16 + lane;
   uint64_t rest = __ballot(lane < 16 && mine < a.T && (a.plain || a.row_of[mine < a.T ? mine : 0] < 0));
-  const int nv = a.vec ? a.N / 8 : 0;
+  const int nv = a.N / 8;
   for (int i = 0; rest; ++i, rest &= rest - 1) {
     if (i % waves != wave) continue;
     const int64_t t = block * 16 + __builtin_ctzll(rest);
@@ -324,7 +331,7 @@ __device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int wa
     uint16_t* dst = a.out + t * a.ldo;
 #pragma unroll 4
     for (int v = lane; v < nv; v += 64)
-      *(u32x4_t*)(dst + 8 * v) = a.base ? *(const u32x4_t*)(src + 8 * v) : (u32x4_t){0, 0, 0, 0};
+      *(u32x4_any_t*)(dst + 8 * v) = a.base ? *(const u32x4_any_t*)(src + 8 * v) : (u32x4_t){0, 0, 0, 0};
     for (int n = 8 * nv + lane; n < a.N; n += 64) dst[n] = a.base ? src[n] : (uint16_t)0;
   }
 }
@@ -332,8 +339,8 @@ __device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int wa
 // ---------------------------------------------------------------------------
 // Few tokens: two launches.  What one CU can keep in flight bounds a workgroup to some 25
 // bytes per ns (one launch in which a workgroup took its tile from X to out: one token of
-// rank 8, 7168 to 2048 wide, 10 us against 4 + 4), so each tile's slices of K, and then
-// its blocks of columns, go to workgroups of their own.  The S slices' sums lie in slabs
+// rank 8, 7168 to 2048 wide, 10 us against 4 + 4), so each tile's slices of K and parts of
+// the rank, and then its blocks of columns, go to workgroups of their own.  The S slices' sums lie in slabs
 // of U that every workgroup of the second launch adds in order.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWaves = 4;
@@ -347,24 +354,28 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
     return;
   }
   const int item = xcd_item(blockIdx.x, a.items);
-  const int tile = item / a.S, slice = item % a.S;
+  int f0 = 0, part = item;
+  if (a.parts > 1) {
+    part = item / a.parts;
+    f0 = (item - part * a.parts) * RF;
+  }
+  const int tile = part / a.S, slice = part - tile * a.S;
   const int t = row_token(a, tile * kTile + (lane & 15));
   const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
   if (g < 0) return;
   const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
   const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
   f32x4_t acc[RF];
-  low_rank_rows<RF, RF <= 2 ? 4 / RF : 2>(a, g, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
+  low_rank_rows<RF, RF <= 2 ? 4 / RF : 2>(a, g, f0, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
 #pragma unroll
   for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
   __syncthreads();
   for (int j = threadIdx.x; j < 4 * RF * kTile; j += 64 * kSplitWaves) {
-    const int r4 = j % (4 * RF), token = j / (4 * RF);
+    const int r4 = j % (4 * RF), token = j / (4 * RF), rank = 16 * f0 + 4 * r4;
     f32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kSplitWaves; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
-    if (4 * r4 < a.r)
-      *(f32x4_t*)(a.U + (((int64_t)slice * a.tiles + tile) * kTile + token) * a.r + 4 * r4) = v;
+    if (rank < a.r) *(f32x4_t*)(a.U + (((int64_t)slice * a.tiles + tile) * kTile + token) * a.r + rank) = v;
   }
 }
 
@@ -567,7 +578,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const LoraArgs
     for (int j = threadIdx.x; j < QUADS * kTile; j += 64 * kSplitWaves) {
       const int r4 = j % QUADS, row = j / QUADS;
       f32x4_t v = {0, 0, 0, 0};
-      if (4 * r4 < a.r) {
+      if (4 * r4 < a.r && row_token(a, tile * kTile + row) >= 0) {
         const float* up = a.U + ((int64_t)tile * kTile + row) * a.r + 4 * r4;
 #pragma unroll 8
         for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles * kTile * a.r);
@@ -683,15 +694,30 @@ constexpr int64_t kMaxRows = int64_t(1) << 26;          // with kMaxBlocks: work
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // (256 a workgroup) fit 32 bits
 constexpr int64_t kMaxK = int64_t(1) << 30;
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-static bool vec_ok(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
 // read a whole adapter from L2, T r / 16 elements a column; grouped, 64 tokens share it,
-// for one more launch and a pass per adapter in a group.  K = N = 4096, in us, tile by
-// tile / grouped:  T 512, r 128, G 1: 28 / 19;  T 1024, r 64, G 1: 24 / 18, G 8: 23 / 25;
-// T 4096, r 16, G 1: 32 / 26, G 8: 32 / 32, G 64: 35 / 40;  T 4096, r 64, G 64: 72 / 60;
-// T 1024, r 8, G 8: 13 / 20.
-static bool many_tokens(int64_t T, int64_t G, int64_t r) { return T * r >= 2048 * (30 + G); }
+// for one more launch and a pass per adapter in a group, of which there are more the more
+// adapters there are, four at most.  K = N = 4096, in us, tile by tile / grouped:
+//   G 1:  r 8, T 2048 16.3 / 16.7, T 4096 28.7 / 24.7;  r 128, T 256 16.6 / 15.2;
+//   G 8:  r 16, T 4096 32 / 33, r 32 40 / 34;  r 64, T 1024 21 / 24, T 2048 33 / 31;
+//   G 64: r 32, T 2048 27 / 30, T 4096 42 / 37;  r 64, T 1024 31 / 37, T 2048 40 / 38.
+static bool many_tokens(int64_t T, int64_t G, int64_t r) {
+  return T * r >= 2048 * (G < 15 ? 12 + 3 * G : 57);
+}
+
+// Rank fragments of a workgroup of the first product for few tokens: the whole rank, or
+// parts of it, each of which reads X again, for about 1024 workgroups (1 token, rank 128:
+// 17.6 us with the whole rank, 9.3 in 8 parts; 1024 tokens of 64 adapters, rank 64: 29.5
+// whole, 30.8 in halves, 34.1 in quarters; 256 tokens, rank 128: 45 whole, 38 in halves,
+// 36 in quarters).
+constexpr int kFewItems = 1024;
+static int rank_fragments(int64_t tiles, int64_t S, int64_t r) {
+  const int64_t all = r <= 16 ? 1 : (r <= 32 ? 2 : (r <= 64 ? 4 : 8)), frags = ceil_div(r, 16);
+  int rf = 1;
+  while (rf < all && tiles * S * ceil_div(frags, rf) > kFewItems) rf *= 2;
+  return rf;
+}
 
 // The rank up to which the kernels' fragments reach.
 static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
@@ -726,8 +752,11 @@ static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
                        threads, 0, st, a);
     return;
   }
-  a.items = a.tiles * a.S;
-  hipLaunchKernelGGL(shrink_kernel<RF>, dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
+  const int rf = rank_fragments(a.tiles, a.S, a.r);
+  a.parts = (int)ceil_div(a.r, 16 * rf);
+  a.items = a.tiles * a.S * a.parts;
+  auto* const shrink = rf == 1 ? shrink_kernel<1> : (rf == 2 ? shrink_kernel<2> : (rf == 4 ? shrink_kernel<4> : shrink_kernel<8>));
+  hipLaunchKernelGGL(shrink, dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
   if (a.tiles == 0) return;
   // columns: workgroups for the whole chip, at least one block of 64 a wave
   const int want = (int)ceil_div(1024, a.tiles), most = (int)ceil_div(blocks, kSplitWaves);
@@ -809,7 +838,6 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   a.rows = (int32_t)rows;
   a.tiles = adapt ? (int32_t)ceil_div(rows, kTile) : 0;
   a.plain = !adapt;
-  a.vec = vec_ok(out, ldo) && (!base || vec_ok(base, ld_base));
   a.S = adapt ? slices(T, G, a.tiles, K, r) : 1;
   const hipStream_t st = (hipStream_t)stream;
   // tokens without an adapter: nothing to do in place
