@@ -81,6 +81,16 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int64_t dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (at::DeviceIndex)dev)));
 }
 
+// A tensor on part of another's storage (as_strided without its trip through the
+// dispatcher: sort_tokens makes four: 6.1 -> 5.4 us a call).
+at::Tensor piece(const at::Tensor& of, int64_t offset, at::IntArrayRef size, at::IntArrayRef stride) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(), of.dtype());
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(offset);
+  impl->set_sizes_and_strides(size, stride);
+  return t;
+}
+
 struct Plan {
   const at::Tensor *offsets, *row_of, *pair_of, *row_group;
   int64_t T = 0, k = 0, rows = 0;
@@ -140,7 +150,7 @@ PyObject* sort_tokens_(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t size[4] = {heads, pairs, rows, rows};
     int64_t off = 0;
     for (int i = 0; i < 4; ++i) {
-      part[i] = i == 1 ? all.as_strided({T, k}, {k, 1}, off) : all.as_strided({size[i]}, {1}, off);
+      part[i] = i == 1 ? piece(all, off, {T, k}, {k, 1}) : piece(all, off, {size[i]}, {1});
       off += size[i];
     }
     const int64_t need = p_sort_tokens_workspace(pairs, (int32_t)G);

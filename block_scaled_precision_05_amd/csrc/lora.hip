@@ -53,7 +53,7 @@ struct LoraArgs {
   int64_t ld_base;
   uint16_t* out;
   int64_t ldo;
-  float* U;               // two launches: [S][tiles*16][r]
+  float* U;               // [S][tiles*16][r]
   __bf16* UW;             // many tokens: [tiles*16][hi, lo][rank padded to 32]
   int32_t T, G, K, N, r, rows, tiles, S;
   int32_t k_per;          // elements of K per slice, a multiple of 128
