@@ -37,32 +37,53 @@ typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
 
 constexpr int kTile = 16;      // rows of the plan per MFMA tile
 
-struct LoraArgs {
-  const uint16_t* X;
-  int64_t ldx;
-  const uint16_t* A;      // [G][r][K]
-  int64_t lda, stride_a;
-  const uint16_t* B;      // [G][N][r]
-  int64_t ldb, stride_b;
-  const float* scale;     // [G] or null
-  const int32_t* offsets; // [G+1]
-  const int32_t* row_of;  // [T]
+// Arguments, one struct a launch and each at most 112 bytes for few tokens: a launch whose
+// arguments pass that size (gridDim and the like bring 256 bytes of their own) costs up to
+// 1 us more on the host, which is what bounds those calls.  Strides of X, A and B count 8
+// elements.
+struct Rows {              // what a row of the plan is
   const int32_t* pair_of;
   const int32_t* row_group;
-  const uint16_t* base;   // or null
-  int64_t ld_base;
+  const uint16_t* base;    // or null
   uint16_t* out;
-  int64_t ldo;
-  float* U;               // [S][tiles*16][r]
-  __bf16* UW;             // many tokens: [tiles*16][hi, lo][rank padded to 32]
-  int32_t T, G, K, N, r, rows, tiles, S;
-  int32_t k_per;          // elements of K per slice, a multiple of 128
-  int32_t parts;          // few tokens: workgroups that share the rank of a slice
-  int32_t plain;          // K, r or G is 0: no token has anything to add
-  int32_t items;          // first launch: workgroups with tiles; the others copy tokens
-  int32_t col_blocks;     // second launch: workgroups that share a tile's columns, and the
-  int32_t cols_per;       // 64-column blocks of each
+  int32_t ld_base, ldo;
+  int32_t T, N, rows, items;   // items: workgroups with tiles; those behind them copy tokens
+  uint16_t G, r, S;        // S: slices of K ..
+  uint16_t k_units;        // .. of that many times 128 elements
+  __device__ __forceinline__ int tiles() const { return (rows + kTile - 1) / kTile; }
 };
+struct First : Rows {
+  const uint16_t* X;
+  const uint16_t* A;       // [G][r][K]
+  const int32_t* row_of;   // [T]
+  float* U;                // [S][tiles*16][r]
+  int32_t ldx, lda, stride_a, K;
+};
+struct FirstMany : First {
+  const int32_t* offsets;  // [G+1]
+};
+struct Second : Rows {
+  const uint16_t* B;       // [G][N][r]
+  const float* scale;      // [G] or null
+  const float* U;
+  int32_t ldb, stride_b;
+  int32_t col_blocks, cols_per;   // workgroups that share a tile's columns, 64-column blocks of each
+};
+struct SecondMany : Rows {
+  const uint16_t* B;
+  const __bf16* UW;        // [tiles*16][hi, lo][rank padded to 32]
+  const int32_t* offsets;
+  int32_t ldb, stride_b;
+  int32_t col_blocks;
+};
+struct Join {
+  const float* U;
+  __bf16* UW;
+  const float* scale;
+  const int32_t* row_group;
+  int32_t rows, G, r, S, ranks;   // ranks: r padded to 32
+};
+static_assert(sizeof(First) <= 112 && sizeof(Second) <= 112, "see above");
 
 // The work item of workgroup b of n: workgroups are dealt round-robin to the 8 XCDs, so
 // XCD x gets a contiguous chunk of the items.
@@ -72,13 +93,13 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
 }
 
 // The adapter of a tile (that of its first row), or -1 when the tile holds no token.
-__device__ __forceinline__ int tile_group(const LoraArgs& a, int tile) {
+__device__ __forceinline__ int tile_group(const Rows& a, int tile) {
   const int g = a.row_group[tile * kTile];
   return (uint32_t)g < (uint32_t)a.G ? g : -1;
 }
 
 // The token of a row, or -1.
-__device__ __forceinline__ int row_token(const LoraArgs& a, int row) {
+__device__ __forceinline__ int row_token(const Rows& a, int row) {
   const int p = row < a.rows ? a.pair_of[row] : -1;
   return (uint32_t)p < (uint32_t)a.T ? p : -1;
 }
@@ -95,11 +116,11 @@ __device__ __forceinline__ void mul_step(const u32x4_t& x, const u32x4_t (&av)[R
 // The lane's row (l16) of RF fragments of A_g from f0 on, from its first chunk (lq) on.  Rows past r
 // repeat the last row; their sums are not used.
 template <int RF>
-__device__ __forceinline__ void a_rows(const LoraArgs& a, int g, int f0, const uint16_t* (&ap)[RF]) {
+__device__ __forceinline__ void a_rows(const First& a, int g, int f0, const uint16_t* (&ap)[RF]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int f = 0; f < RF; ++f)
-    ap[f] = a.A + (int64_t)g * a.stride_a + (int64_t)min(16 * (f0 + f) + (lane & 15), a.r - 1) * a.lda + 8 * (lane >> 4);
+    ap[f] = a.A + 8 * ((int64_t)g * a.stride_a + (int64_t)min(16 * (f0 + f) + (lane & 15), a.r - 1) * a.lda + (lane >> 4));
 }
 
 // k-steps k, k + stride, ... below k_hi, the last one partial: K is a multiple of 8, so a
@@ -128,7 +149,7 @@ __device__ __forceinline__ void tail_steps(const uint16_t* x, const uint16_t* co
 // rank rows 16f + 4lq .. +3 of token l16.
 // ---------------------------------------------------------------------------
 template <int RF, int KS>
-__device__ __forceinline__ void low_rank_rows(const LoraArgs& a, int g, int f0, const uint16_t* x, int k_lo, int k_hi,
+__device__ __forceinline__ void low_rank_rows(const First& a, int g, int f0, const uint16_t* x, int k_lo, int k_hi,
                                               int w, int nw, f32x4_t (&acc)[RF]) {
   const uint16_t* ap[RF];
   a_rows<RF>(a, g, f0, ap);
@@ -216,7 +237,7 @@ struct Scratch {
 };
 
 // base of one tile's 64 columns from 64*c on, 16 bytes a lane of rows 8j + lane/8.
-__device__ __forceinline__ void load_base(const LoraArgs& a, const int (&t)[2], int c, u32x4_t (&base)[2]) {
+__device__ __forceinline__ void load_base(const Rows& a, const int (&t)[2], int c, u32x4_t (&base)[2]) {
   const int n0 = 64 * c + 8 * (threadIdx.x & 7);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -229,7 +250,7 @@ __device__ __forceinline__ void load_base(const LoraArgs& a, const int (&t)[2], 
 // One tile's 64 columns: the products b x (hi + lo), through the scratch, base added,
 // rounded and stored.
 template <int RK>
-__device__ __forceinline__ void add_block(const LoraArgs& a, const int (&t)[2], int c, const u32x4_t (&b)[RK][4],
+__device__ __forceinline__ void add_block(const Rows& a, const int (&t)[2], int c, const u32x4_t (&b)[RK][4],
                                           const bf16x8_t (&uh)[RK], const bf16x8_t (&ul)[RK],
                                           const u32x4_t (&base)[2], Scratch& scratch) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
@@ -277,11 +298,11 @@ __device__ __forceinline__ void add_block(const LoraArgs& a, const int (&t)[2], 
 }
 
 template <int RF, class F>
-__device__ __forceinline__ void add_columns(const LoraArgs& a, int g, const int (&t)[2], const URows<RF>& u,
+__device__ __forceinline__ void add_columns(const Second& a, int g, const int (&t)[2], const URows<RF>& u,
                                             Scratch& scratch, int c0, int c1, int step, F&& form_u) {
   constexpr int RK = URows<RF>::RK;
   const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
-  const uint16_t* bg = a.B + (int64_t)g * a.stride_b;
+  const uint16_t* bg = a.B + 8 * (int64_t)g * a.stride_b;
   struct Block {
     u32x4_t b[RK][4], base[2];
   };
@@ -289,7 +310,7 @@ __device__ __forceinline__ void add_columns(const LoraArgs& a, int g, const int 
     load_base(a, t, c, v.base);
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      const uint16_t* brow = bg + (int64_t)min(64 * c + 16 * f + l16, a.N - 1) * a.ldb + 8 * lq;
+      const uint16_t* brow = bg + 8 * ((int64_t)min(64 * c + 16 * f + l16, a.N - 1) * a.ldb + lq);
 #pragma unroll
       for (int k = 0; k < RK; ++k) {
         v.b[k][f] = (u32x4_t){0, 0, 0, 0};
@@ -317,12 +338,12 @@ __device__ __forceinline__ void add_columns(const LoraArgs& a, int g, const int 
   }
 }
 
-// Tokens without an adapter: base as it is, or zeros.  16 tokens a workgroup, whose waves
+// Tokens without an adapter (all of them where nothing has tiles): base as it is, or zeros.  16 tokens a workgroup, whose waves
 // share them out.
-__device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int waves) {
+__device__ __forceinline__ void copy_tokens(const First& a, int block, int waves) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mine = block * 16 + lane;
-  uint64_t rest = __ballot(lane < 16 && mine < a.T && (a.plain || a.row_of[mine < a.T ? mine : 0] < 0));
+  uint64_t rest = __ballot(lane < 16 && mine < a.T && (a.items == 0 || a.row_of[mine < a.T ? mine : 0] < 0));
   const int nv = a.N / 8;
   for (int i = 0; rest; ++i, rest &= rest - 1) {
     if (i % waves != wave) continue;
@@ -346,7 +367,7 @@ __device__ __forceinline__ void copy_tokens(const LoraArgs& a, int block, int wa
 constexpr int kSplitWaves = 4;
 
 template <int RF>
-__global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs a) {
+__global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const First a) {
   __shared__ f32x4_t sums[kSplitWaves][RF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if ((int)blockIdx.x >= a.items) {
@@ -354,19 +375,21 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
     return;
   }
   const int item = xcd_item(blockIdx.x, a.items);
+  // rank rows 16 f0 .. of one slice: the parts of a slice, which read the same X, side by side
+  const int parts = (a.r + 16 * RF - 1) / (16 * RF);
   int f0 = 0, part = item;
-  if (a.parts > 1) {
-    part = item / a.parts;
-    f0 = (item - part * a.parts) * RF;
+  if (parts > 1) {
+    part = item / parts;
+    f0 = (item - part * parts) * RF;
   }
   const int tile = part / a.S, slice = part - tile * a.S;
   const int t = row_token(a, tile * kTile + (lane & 15));
   const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
   if (g < 0) return;
-  const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
+  const int k_per = 128 * a.k_units, k_lo = min(a.K, slice * k_per), k_hi = min(a.K, k_lo + k_per);
   const int t0 = max(__builtin_amdgcn_readfirstlane(t), 0);
   f32x4_t acc[RF];
-  low_rank_rows<RF, RF <= 2 ? 4 / RF : 2>(a, g, f0, a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
+  low_rank_rows<RF, RF <= 2 ? 4 / RF : 2>(a, g, f0, a.X + 8 * (int64_t)(t < 0 ? t0 : t) * a.ldx, k_lo, k_hi, wave, kSplitWaves, acc);
 #pragma unroll
   for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
   __syncthreads();
@@ -375,7 +398,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
     f32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kSplitWaves; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + token];
-    if (rank < a.r) *(f32x4_t*)(a.U + (((int64_t)slice * a.tiles + tile) * kTile + token) * a.r + rank) = v;
+    if (rank < a.r) *(f32x4_t*)(a.U + (((int64_t)slice * a.tiles() + tile) * kTile + token) * a.r + rank) = v;
   }
 }
 
@@ -392,8 +415,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const LoraArgs
 // last XCD would stand idle.
 // Work items per group of NT tiles times the groups in use.
 template <int NT>
-__device__ __forceinline__ int used_items(const LoraArgs& a, int per_group) {
-  const int used = min(max(a.offsets[a.G], 0), a.rows);
+__device__ __forceinline__ int used_items(const int32_t* offsets, const Rows& a, int per_group) {
+  const int used = min(max(offsets[a.G], 0), a.rows);
   return (used + NT * kTile - 1) / (NT * kTile) * per_group;
 }
 
@@ -403,9 +426,9 @@ __device__ __forceinline__ int used_items(const LoraArgs& a, int per_group) {
 template <int NT>
 struct Runs {
   int group[NT], i, n, g;
-  __device__ __forceinline__ Runs(const LoraArgs& a, int tile0) : i(0), n(0), g(-1) {
+  __device__ __forceinline__ Runs(const Rows& a, int tile0) : i(0), n(0), g(-1) {
     const int tile = tile0 + (int)(threadIdx.x & (NT - 1));
-    const int v = tile < a.tiles ? tile_group(a, tile) : -1;
+    const int v = tile < a.tiles() ? tile_group(a, tile) : -1;
 #pragma unroll
     for (int j = 0; j < NT; ++j) group[j] = __builtin_amdgcn_readlane(v, j);
   }
@@ -449,7 +472,7 @@ constexpr int kShrinkTiles = 4;     // tiles of a workgroup, as many as waves
 constexpr int kExpandTiles = 4;
 
 template <int RF, int NT, int KC, int NS>
-__global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const LoraArgs a) {
+__global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const FirstMany a) {
   constexpr int ROW = 2 * KC, NC = KC / 8;      // bytes and 16-byte chunks of a row
   constexpr int RPC = 1024 / ROW;               // rows of one wave copy
   constexpr int X_BYTES = NT * kTile * ROW, STAGE = X_BYTES + 16 * RF * ROW;
@@ -469,11 +492,11 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const LoraArgs a) 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
   const int tile_w = wave / TW * TW, frag_w = wave % TW * FW;
-  const int items = used_items<NT>(a, a.S);
+  const int items = used_items<NT>(a.offsets, a, a.S);
   if ((int)blockIdx.x >= items) return;
   const int item = xcd_item(blockIdx.x, items);
   const int tile0 = item / a.S * NT, slice = item % a.S;
-  const int k_lo = min(a.K, slice * a.k_per), k_hi = min(a.K, k_lo + a.k_per);
+  const int k_per = 128 * a.k_units, k_lo = min(a.K, slice * k_per), k_hi = min(a.K, k_lo + k_per);
   const int stages = (k_hi - k_lo) / KC;
 
   Runs<NT> run(a, tile0);
@@ -488,12 +511,12 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const LoraArgs a) 
     for (int c = 0; c < XC; ++c) {
       const int row = 16 * wave + RPC * c + cr;
       const int t = wave >= i && wave < i + nt ? row_token(a, tile0 * kTile + row) : -1;
-      xs[c] = a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane % NC) ^ (row * ROW / 256 % NC));
+      xs[c] = a.X + 8 * (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane % NC) ^ (row * ROW / 256 % NC));
     }
 #pragma unroll
     for (int c = 0; c < AC; ++c) {
       const int row = AR * wave + RPC * c + cr;
-      as[c] = a.A + (int64_t)g * a.stride_a + (int64_t)min(row, a.r - 1) * a.lda + k_lo +
+      as[c] = a.A + 8 * ((int64_t)g * a.stride_a + (int64_t)min(row, a.r - 1) * a.lda) + k_lo +
               8 * ((lane % NC) ^ (row * ROW / 256 % NC));
     }
     auto issue = [&](int s, int buf) {
@@ -551,22 +574,22 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const LoraArgs a) 
         const int t = row_token(a, row);
         const uint16_t* ap[FW];
         a_rows<FW>(a, g, frag_w, ap);
-        tail_steps<FW>(a.X + (int64_t)(t < 0 ? t0 : t) * a.ldx + 8 * lq, ap, k_lo + KC * stages, k_hi, 32, acc[j]);
+        tail_steps<FW>(a.X + 8 * ((int64_t)(t < 0 ? t0 : t) * a.ldx + lq), ap, k_lo + KC * stages, k_hi, 32, acc[j]);
       }
 #pragma unroll
       for (int f = 0; f < FW; ++f)
         if (16 * (frag_w + f) + 4 * lq < a.r)   // r % 8 == 0
-          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles * kTile + row) * a.r + 16 * (frag_w + f) + 4 * lq) = acc[j][f];
+          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles() * kTile + row) * a.r + 16 * (frag_w + f) + 4 * lq) = acc[j][f];
     }
   }
 }
 
 template <int RF>
-__global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const LoraArgs a) {
+__global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const Second a) {
   __shared__ URows<RF> u;
   __shared__ Scratch scratch[kSplitWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const int item = xcd_item(blockIdx.x, a.items);
   const int tile = item / a.col_blocks, cb = item % a.col_blocks;
   const int blocks = (a.N + 63) / 64, c_lo = cb * a.cols_per, c_hi = min(blocks, c_lo + a.cols_per);
   const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
@@ -581,7 +604,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const LoraArgs
       if (4 * r4 < a.r && row_token(a, tile * kTile + row) >= 0) {
         const float* up = a.U + ((int64_t)tile * kTile + row) * a.r + 4 * r4;
 #pragma unroll 8
-        for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles * kTile * a.r);
+        for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles() * kTile * a.r);
       }
       u.put(row, 4 * r4, s * v, a.r);
     }
@@ -592,11 +615,11 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const LoraArgs
 // Between the two for many tokens: the slabs of U summed, scaled and split into the second
 // product's two bf16 terms once, instead of by every workgroup that needs a row.  Row
 // layout of UW: 32*RK hi terms, then 32*RK lo terms, zeros past r.
-__global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) {
-  const int quads = ranks / 4;
+__global__ __launch_bounds__(256) void join_kernel(const Join a) {
+  const int quads = a.ranks / 4, tiles = (a.rows + kTile - 1) / kTile;
   const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int row = (int)(j / quads), r4 = (int)(j - (int64_t)row * quads);
-  if (row >= a.tiles * kTile) return;
+  if (row >= tiles * kTile) return;
   const int g = a.row_group[min(row / kTile * kTile, a.rows - 1)];
   if ((uint32_t)g >= (uint32_t)a.G) return;
   const float s = a.scale ? a.scale[g] : 1.0f;
@@ -604,7 +627,7 @@ __global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) 
   if (4 * r4 < a.r) {
     const float* up = a.U + (int64_t)row * a.r + 4 * r4;
 #pragma unroll 4
-    for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * a.tiles * kTile * a.r);
+    for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * tiles * kTile * a.r);
   }
   bf16x4_t h, l;
 #pragma unroll
@@ -614,8 +637,8 @@ __global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) 
     h[e] = hh;
     l[e] = ll;
   }
-  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * ranks + 4 * r4) = h;
-  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * ranks + ranks + 4 * r4) = l;
+  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * a.ranks + 4 * r4) = h;
+  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * a.ranks + a.ranks + 4 * r4) = l;
 }
 
 // Second product for many tokens: a workgroup takes 64 rows, a tile a wave, and CB blocks
@@ -625,14 +648,14 @@ __global__ __launch_bounds__(256) void join_kernel(const LoraArgs a, int ranks) 
 // 256 % chunks), as in the first product's ring.
 template <int RF, int CB>
 __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_eu(RF == 8 ? 2 : 3))) void expand_many_kernel(
-    const LoraArgs a) {
+    const SecondMany a) {
   constexpr int RK = URows<RF>::RK, NC = 4 * RK, ROW = 16 * NC;   // 16-byte chunks and bytes of a row
   constexpr int ROWS = 64 * CB, RPC = 1024 / ROW;                   // rows, and rows of one wave copy
   __shared__ __attribute__((aligned(1024))) uint8_t bl[ROWS * ROW];
   __shared__ Scratch scratch[kSplitWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int items = used_items<kExpandTiles>(a, a.col_blocks);
+  const int items = used_items<kExpandTiles>(a.offsets, a, a.col_blocks);
   if ((int)blockIdx.x >= items) return;
   const int item = xcd_item(blockIdx.x, items);
   const int tile0 = item / a.col_blocks * kExpandTiles, c0 = item % a.col_blocks * CB;
@@ -642,7 +665,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   bool first = true;
   while (run.next()) {
     const bool mine = wave >= run.i && wave < run.i + run.n;
-    const uint16_t* const bg = a.B + (int64_t)run.g * a.stride_b;
+    const uint16_t* const bg = a.B + 8 * (int64_t)run.g * a.stride_b;
     if (!first) stage_barrier<0>();     // (every wave has read the previous run's rows)
     first = false;
 #pragma unroll
@@ -650,7 +673,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
       const int row0 = (q * kSplitWaves + wave) * RPC, row = row0 + lane / NC;
       const int chunk = (lane % NC) ^ ((row * ROW / 256) % NC);
       // rows past N repeat the last one, chunks past r the first: neither is used
-      lds_copy(bg + (int64_t)min(64 * c0 + row, a.N - 1) * a.ldb + (8 * chunk < a.r ? 8 * chunk : 0), bl + row0 * ROW);
+      lds_copy(bg + 8 * ((int64_t)min(64 * c0 + row, a.N - 1) * a.ldb + (8 * chunk < a.r ? chunk : 0)), bl + row0 * ROW);
     }
     u32x4_t base[CB][2];
     bf16x8_t uh[RK], ul[RK];
@@ -692,7 +715,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
 
 constexpr int64_t kMaxRows = int64_t(1) << 26;          // with kMaxBlocks: work-items of a launch
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // (256 a workgroup) fit 32 bits
-constexpr int64_t kMaxK = int64_t(1) << 30;
+constexpr int64_t kMaxK = int64_t(1) << 22;             // 128-element units of K fit 16 bits
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
@@ -732,37 +755,43 @@ static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K, int64_t r) {
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
 
+struct Call {
+  First first;
+  Second second;
+  const int32_t* offsets;
+};
+
 template <int RF>
-static void launch(LoraArgs& a, int copy_blocks, hipStream_t st) {
-  a.k_per = (int)ceil_div(ceil_div(a.K, a.S), 128) * 128;
+static void launch(const Call& c, int copy_blocks, hipStream_t st) {
+  First a = c.first;
+  const int64_t tiles = ceil_div(a.rows, kTile), blocks = ceil_div(a.N, 64);
   const dim3 threads(64 * kSplitWaves);
-  const int blocks = (int)ceil_div(a.N, 64);
-  if (a.tiles > 0 && many_tokens(a.T, a.G, a.r)) {
+  if (a.items > 0 && many_tokens(a.T, a.G, a.r)) {
     constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
-    constexpr int CB = RF == 8 ? 2 : 4;
-    a.items = (int)ceil_div(a.tiles, kShrinkTiles) * a.S;
+    constexpr int CB = RF == 8 ? 2 : 4, ranks = 32 * URows<RF>::RK;
+    a.items = (int)(ceil_div(tiles, kShrinkTiles) * a.S);
     hipLaunchKernelGGL((shrink_many_kernel<RF, kShrinkTiles, KC, NS>), dim3((unsigned)(a.items + copy_blocks)),
-                       dim3(64 * kShrinkTiles), 0, st, a);
-    constexpr int ranks = 32 * URows<RF>::RK;
-    a.UW = (__bf16*)(a.U + (int64_t)a.S * a.tiles * kTile * a.r);
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div((int64_t)a.tiles * kTile * (ranks / 4), 256)), dim3(256), 0,
-                       st, a, ranks);
-    a.col_blocks = (int)ceil_div(blocks, CB);
-    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)(ceil_div(a.tiles, kExpandTiles) * a.col_blocks)),
-                       threads, 0, st, a);
+                       dim3(64 * kShrinkTiles), 0, st, (FirstMany{a, c.offsets}));
+    __bf16* const UW = (__bf16*)(a.U + (int64_t)a.S * tiles * kTile * a.r);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(tiles * kTile * (ranks / 4), 256)), dim3(256), 0, st,
+                       (Join{a.U, UW, c.second.scale, a.row_group, a.rows, a.G, a.r, a.S, ranks}));
+    SecondMany b = {c.second, c.second.B, UW, c.offsets, c.second.ldb, c.second.stride_b, (int)ceil_div(blocks, CB)};
+    b.items = (int)(ceil_div(tiles, kExpandTiles) * b.col_blocks);
+    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)b.items), threads, 0, st, b);
     return;
   }
-  const int rf = rank_fragments(a.tiles, a.S, a.r);
-  a.parts = (int)ceil_div(a.r, 16 * rf);
-  a.items = a.tiles * a.S * a.parts;
+  const int rf = rank_fragments(tiles, a.S, a.r);
+  if (a.items > 0) a.items = (int)(tiles * a.S * ceil_div(a.r, 16 * rf));
   auto* const shrink = rf == 1 ? shrink_kernel<1> : (rf == 2 ? shrink_kernel<2> : (rf == 4 ? shrink_kernel<4> : shrink_kernel<8>));
   hipLaunchKernelGGL(shrink, dim3((unsigned)(a.items + copy_blocks)), threads, 0, st, a);
-  if (a.tiles == 0) return;
+  if (a.items == 0) return;
   // columns: workgroups for the whole chip, at least one block of 64 a wave
-  const int want = (int)ceil_div(1024, a.tiles), most = (int)ceil_div(blocks, kSplitWaves);
-  a.cols_per = (int)ceil_div(ceil_div(blocks, want < most ? want : most), kSplitWaves) * kSplitWaves;
-  a.col_blocks = (int)ceil_div(blocks, a.cols_per);
-  hipLaunchKernelGGL(expand_kernel<RF>, dim3((unsigned)(a.tiles * a.col_blocks)), threads, 0, st, a);
+  Second b = c.second;
+  const int64_t want = ceil_div(1024, tiles), most = ceil_div(blocks, kSplitWaves);
+  b.cols_per = (int)ceil_div(ceil_div(blocks, want < most ? want : most), kSplitWaves) * kSplitWaves;
+  b.col_blocks = (int)ceil_div(blocks, b.cols_per);
+  b.items = (int)(tiles * b.col_blocks);
+  hipLaunchKernelGGL(expand_kernel<RF>, dim3((unsigned)b.items), threads, 0, st, b);
 }
 
 }  // namespace bsg_lora
@@ -797,57 +826,62 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   if (((uintptr_t)offsets | (uintptr_t)row_of | (uintptr_t)pair_of | (uintptr_t)row_group | (uintptr_t)scale) & 3)
     return BSG_ERR_MISALIGNED;
   if (rows > 0 && (!pair_of || !row_group || !offsets)) return BSG_ERR_INVALID_ARG;
-  const int64_t big = int64_t(1) << 40;
+  const int64_t kMaxLd = (int64_t(1) << 31) - 1, kMaxStride = 8 * kMaxLd;     // 32 bits, of X, A and B in eights
   if (adapt) {
     if (!X || !A || !B || ldx < K || lda < K || ldb < r || stride_a < 0 || stride_b < 0)
       return BSG_ERR_INVALID_ARG;
-    if (G > 1 && (stride_a < (r - 1) * lda + K || stride_b < (N - 1) * ldb + r)) return BSG_ERR_INVALID_ARG;
-    if (ldx > big || lda > big / 128 || ldb > big / N || stride_a > big || stride_b > big)
+    if (ldx > kMaxStride || lda > kMaxStride || ldb > kMaxStride || stride_a > kMaxStride || stride_b > kMaxStride)
       return BSG_ERR_UNSUPPORTED_SHAPE;
+    if (G > 1 && (stride_a < (r - 1) * lda + K || stride_b < (N - 1) * ldb + r)) return BSG_ERR_INVALID_ARG;
     if (((uintptr_t)X | (uintptr_t)A | (uintptr_t)B) & 15) return BSG_ERR_MISALIGNED;
     if (ldx % 8 || lda % 8 || ldb % 8 || stride_a % 8 || stride_b % 8) return BSG_ERR_MISALIGNED;
     const int64_t need = lora_add_workspace(T, rows, G, N, K, r);
     if (workspace_bytes < need || (need > 0 && !workspace)) return BSG_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 15) return BSG_ERR_MISALIGNED;
   }
-  if (ldo > big || ld_base > big) return BSG_ERR_UNSUPPORTED_SHAPE;
-  LoraArgs a = {};
-  a.X = (const uint16_t*)X;
-  a.ldx = ldx;
-  a.A = (const uint16_t*)A;
-  a.lda = lda;
-  a.stride_a = stride_a;
-  a.B = (const uint16_t*)B;
-  a.ldb = ldb;
-  a.stride_b = stride_b;
-  a.scale = scale;
-  a.offsets = offsets;
-  a.row_of = row_of;
-  a.pair_of = pair_of;
-  a.row_group = row_group;
-  a.base = (const uint16_t*)base;
-  a.ld_base = ld_base;
-  a.out = (uint16_t*)out;
-  a.ldo = ldo;
-  a.U = (float*)workspace;
-  a.T = (int32_t)T;
-  a.G = G;
-  a.K = (int32_t)K;
-  a.N = (int32_t)N;
-  a.r = r;
-  a.rows = (int32_t)rows;
-  a.tiles = adapt ? (int32_t)ceil_div(rows, kTile) : 0;
-  a.plain = !adapt;
-  a.S = adapt ? slices(T, G, a.tiles, K, r) : 1;
+  if (ldo > kMaxLd || ld_base > kMaxLd) return BSG_ERR_UNSUPPORTED_SHAPE;
+  Call c = {};
+  Rows rw = {};
+  rw.pair_of = pair_of;
+  rw.row_group = row_group;
+  rw.base = (const uint16_t*)base;
+  rw.out = (uint16_t*)out;
+  rw.ld_base = (int32_t)ld_base;
+  rw.ldo = (int32_t)ldo;
+  rw.T = (int32_t)T;
+  rw.N = (int32_t)N;
+  rw.rows = (int32_t)rows;
+  rw.items = adapt;      // (until the launch is laid out: whether there are any)
+  rw.G = (uint16_t)G;
+  rw.r = (uint16_t)r;
+  const int S = adapt ? slices(T, G, ceil_div(rows, kTile), K, r) : 1;
+  rw.S = (uint16_t)S;
+  (Rows&)c.first = rw;
+  c.first.k_units = (uint16_t)ceil_div(ceil_div(K, S), 128);
+  c.first.K = (int32_t)K;
+  c.first.X = (const uint16_t*)X;
+  c.first.A = (const uint16_t*)A;
+  c.first.row_of = row_of;
+  c.first.U = (float*)workspace;
+  c.first.ldx = (int32_t)(ldx / 8);
+  c.first.lda = (int32_t)(lda / 8);
+  c.first.stride_a = (int32_t)(stride_a / 8);
+  (Rows&)c.second = rw;
+  c.second.B = (const uint16_t*)B;
+  c.second.scale = scale;
+  c.second.U = (const float*)workspace;
+  c.second.ldb = (int32_t)(ldb / 8);
+  c.second.stride_b = (int32_t)(stride_b / 8);
+  c.offsets = offsets;
   const hipStream_t st = (hipStream_t)stream;
   // tokens without an adapter: nothing to do in place
   const int copy_blocks = base == out ? 0 : (int)ceil_div(T, 16);
-  if (a.tiles + copy_blocks == 0) return BSG_OK;      // in place and nothing to add
+  if (!adapt && copy_blocks == 0) return BSG_OK;      // in place and nothing to add
   (void)hipGetLastError();
-  if (r <= 16) launch<1>(a, copy_blocks, st);
-  else if (r <= 32) launch<2>(a, copy_blocks, st);
-  else if (r <= 64) launch<4>(a, copy_blocks, st);
-  else launch<8>(a, copy_blocks, st);
+  if (r <= 16) launch<1>(c, copy_blocks, st);
+  else if (r <= 32) launch<2>(c, copy_blocks, st);
+  else if (r <= 64) launch<4>(c, copy_blocks, st);
+  else launch<8>(c, copy_blocks, st);
   return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
 }
 

@@ -67,12 +67,12 @@ struct SortArgs {
   int32_t flat;      // ids are contiguous: pair p's id is ids[p]
   int32_t n;         // pairs, T*k
   int32_t G;
-  int32_t bits;      // of the largest id, G - 1
   int32_t align;
   int32_t cap;       // > 0: masked layout
   int32_t chunk;     // pairs per workgroup, a multiple of kSortThreads
   int32_t nchunks;
   int32_t share;     // workgroups that share the placing of a chunk
+  int32_t blocks;    // workgroups (gridDim would bring 256 bytes of arguments along, and 1 us a launch)
   int32_t* offsets;
   int32_t* row_of;
   int32_t* pair_of;
@@ -95,8 +95,9 @@ __device__ __forceinline__ int pair_group(const SortArgs& a, int p) {
 }
 
 // Lanes of the wave whose g equals this lane's (g >= 0; for g = -1 the result is not used).
-__device__ __forceinline__ uint64_t same_group(int g, int bits) {
+__device__ __forceinline__ uint64_t same_group(int g, int G) {
   uint64_t peers = __ballot(g >= 0);
+  const int bits = G > 1 ? 32 - __builtin_clz((unsigned)(G - 1)) : 0;      // of the largest id
   for (int b = 0; b < bits; ++b) {
     const uint64_t set = __ballot((g >> b) & 1);
     peers &= (g >> b) & 1 ? set : ~set;
@@ -175,7 +176,7 @@ __device__ __forceinline__ void place(const SortArgs& a, int p, int g, int at, c
 // size(g): group g's pairs.  One thread per group for short paddings, a wave for long.
 template <class F>
 __device__ __forceinline__ void fill_rest(const SortArgs& a, const int32_t* start, F&& size) {
-  const int tid = blockIdx.x * kSortThreads + threadIdx.x, threads = gridDim.x * kSortThreads;
+  const int tid = blockIdx.x * kSortThreads + threadIdx.x, threads = a.blocks * kSortThreads;
   if (a.align > 1 || a.cap > 0) {
     const int tpg = a.cap > 0 || a.align > 32 ? 64 : 1;
     for (int g = tid / tpg; g < a.G; g += threads / tpg)
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_single_kernel(const SortArg
     for (int x = lane; x < (a.G + 1) / 2; x += 64) ((uint32_t*)mine)[x] = 0;
     // (a wave's own row: its LDS accesses execute in order)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    const uint64_t peers = same_group(g[s], a.bits);
+    const uint64_t peers = same_group(g[s], a.G);
     rank[s] = __popcll(peers & ((1ull << lane) - 1));
     if (g[s] >= 0 && rank[s] == 0) mine[g[s]] = (uint16_t)__popcll(peers);
   }
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_single_kernel(const SortArg
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int w = s * kSortWaves + wave;
-    if (w % gridDim.x == blockIdx.x)
+    if (w % a.blocks == (int)blockIdx.x)
       place(a, s * kSortThreads + tid, g[s], g[s] >= 0 ? wcnt[w][g[s]] + rank[s] : 0, start);
   }
   fill_rest(a, start, [&](int gg) { return total[gg]; });
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
     for (int x = lane; x < (a.G + 1) / 2; x += 64) ((uint32_t*)&wcnt[wave][0])[x] = 0;
     // (a wave's own row: its LDS accesses execute in order)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    const uint64_t peers = same_group(g, a.bits);
+    const uint64_t peers = same_group(g, a.G);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
     if (g >= 0 && rank == 0) wcnt[wave][g] = (uint16_t)__popcll(peers);
     __syncthreads();
@@ -644,11 +645,12 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ dO, int64_t ldo, const uint16_t* __restrict__ Y, int64_t ldy,
     const int32_t* __restrict__ row_of, const int32_t* __restrict__ pair_of,
     const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
-    uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw, int segs,
-    int pad_blocks) {
+    uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw) {
   __shared__ float part[kWaves][KC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t row_bytes = 2u * (uint32_t)H;
+  // (from the sizes: more than 112 bytes of arguments cost 1 us a launch)
+  const int segs = (H + 64 * VEC - 1) / (64 * VEC), pad_blocks = (rows + kPadRows - 1) / kPadRows;
   if ((int)blockIdx.x < pad_blocks) {
     padding_rows(pair_of, rows, blockIdx.x, [&](int r, int ln) {
       zero_row<VEC, AUX>(row_rsrc(dY, r, rows, 2 * lddy, row_bytes), row_bytes, ln);
@@ -815,7 +817,6 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
   a.rows = (int32_t)rows;
   a.hist = (uint32_t*)workspace;
   a.flat = ld_ids == k || T <= 1;
-  a.bits = G > 1 ? 32 - __builtin_clz((unsigned)(G - 1)) : 0;
   const int64_t steps = ceil_div(n > 0 ? n : 1, kSortThreads);
   const hipStream_t st_ = (hipStream_t)stream;
   (void)hipGetLastError();
@@ -828,8 +829,8 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
     int64_t blocks = ceil_div(n, kSharePairs);
     blocks = blocks > ceil_div(rows, kFillRows) ? blocks : ceil_div(rows, kFillRows);
     blocks = blocks < 1 ? 1 : (blocks < kMaxChunks ? blocks : kMaxChunks);
+    a.blocks = (int32_t)blocks;
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kSortThreads), 0, st_, a); };
-    a.nchunks = 1;
     if (steps <= 1 || G == 0) go(sort_single_kernel<1>);
     else if (steps <= 2) go(sort_single_kernel<2>);
     else go(sort_single_kernel<4>);
@@ -838,7 +839,8 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
     a.nchunks = (int32_t)ceil_div(n, a.chunk);
     hipLaunchKernelGGL(sort_hist_kernel, dim3(a.nchunks), dim3(kSortThreads), 0, st_, a);
     a.share = kMaxChunks / a.nchunks < kSortWaves ? kMaxChunks / a.nchunks : kSortWaves;
-    hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.nchunks * a.share), dim3(kSortThreads), 0, st_, a);
+    a.blocks = a.nchunks * a.share;
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3((unsigned)a.blocks), dim3(kSortThreads), 0, st_, a);
   }
   return launch_status();
 }
@@ -953,7 +955,6 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
   }
   const bool v = (T == 0 || vec8(dO, ldo, H)) && (rows == 0 || vec8(dY, lddy, H)) &&
                  (!dW || rows == 0 || vec8(Y, ldy, H));
-  const int64_t segs = ceil_div(H, v ? 512 : 64);
   const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? T : 0);
   if (blocks == 0) return BSG_OK;
   if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
@@ -961,7 +962,7 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,
                        ldo, (const uint16_t*)Y, ldy, row_of, pair_of, W, ldw, (int)T, k, (int)rows, (int)H,
-                       (uint16_t*)dY, lddy, dW, lddw, (int)segs, (int)pads);
+                       (uint16_t*)dY, lddy, dW, lddw);
   };
   if (v)
     with_chunk(k, 2 * T * k * H >= kStreamBytes,
