@@ -44,7 +44,7 @@ def _binding_command(target: str) -> list:
     return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
         ["-isystem" + i for i in include] + [BINDING_SOURCE, "-o", target, "-L" + lib, "-ltorch_python",
-                                              "-ltorch_cpu", "-lc10"]
+                                              "-ltorch_cpu", "-ltorch_hip", "-lc10"]
 
 
 def build(force: bool = True, verbose: bool = False) -> str:
