@@ -56,11 +56,12 @@ struct First : Rows {
   const uint16_t* X;
   const uint16_t* A;       // [G][r][K]
   const int32_t* row_of;   // [T]
-  float* U;                // [S][tiles*16][r]
+  float* U;                // [slabs][tiles*16][r]
   int32_t ldx, lda, stride_a, K;
 };
 struct FirstMany : First {
   const int32_t* offsets;  // [G+1]
+  int32_t cap;             // most items there can be
 };
 struct Second : Rows {
   const uint16_t* B;       // [G][N][r]
@@ -74,14 +75,14 @@ struct SecondMany : Rows {
   const __bf16* UW;        // [tiles*16][hi, lo][rank padded to 32]
   const int32_t* offsets;
   int32_t ldb, stride_b;
-  int32_t col_blocks;
+  int32_t col_blocks, cap;
 };
 struct Join {
   const float* U;
   __bf16* UW;
   const float* scale;
-  const int32_t* row_group;
-  int32_t rows, G, r, S, ranks;   // ranks: r padded to 32
+  const int32_t* offsets;
+  int32_t rows, G, r, S, K, ranks, cap;   // ranks: r padded to 32
 };
 static_assert(sizeof(First) <= 112 && sizeof(Second) <= 112, "see above");
 
@@ -410,44 +411,65 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const First a)
 // 16-byte chunk c of row r sits at chunk c ^ (r * row bytes / 256 % chunks), so that 16
 // rows' reads of one chunk cover the banks once.
 //
-// The plan's capacity exceeds the rows in use (padding, tokens without an adapter), and
-// the unused rows are the last ones: only the used ones are dealt to the XCDs, or the
-// last XCD would stand idle.
-// Work items per group of NT tiles times the groups in use.
+// Items: NT tiles of one adapter.  (Groups of NT tiles that ignore where an adapter ends
+// need a pass per adapter in a group, and where everything runs at once the launch lasts
+// as long as the workgroup with the most passes.)  They are found from the offsets by
+// every wave, as only the device knows them; the items in use, not the plan's capacity,
+// are dealt to the workgroups and XCDs.
 template <int NT>
-__device__ __forceinline__ int used_items(const int32_t* offsets, const Rows& a, int per_group) {
-  const int used = min(max(offsets[a.G], 0), a.rows);
-  return (used + NT * kTile - 1) / (NT * kTile) * per_group;
-}
-
-// The adapters of NT tiles from tile0 on (-1: no token, or past the end), and the runs of
-// tiles that share one: next() moves to the tiles [i, i + n) of adapter g.  Wave-uniform;
-// one load.
-template <int NT>
-struct Runs {
-  int group[NT], i, n, g;
-  __device__ __forceinline__ Runs(const Rows& a, int tile0) : i(0), n(0), g(-1) {
-    const int tile = tile0 + (int)(threadIdx.x & (NT - 1));
-    const int v = tile < a.tiles() ? tile_group(a, tile) : -1;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) group[j] = __builtin_amdgcn_readlane(v, j);
+struct Items {
+  const int32_t* offsets;
+  int G, rows, incl, total;      // incl: items up to this lane's of the first 64 adapters
+  int g, tile0, nt;              // find(): the item's adapter, first tile and tiles
+  // tiles of adapter g, from tile `first`
+  __device__ __forceinline__ int tiles_of(int g, int& first) const {
+    const int lo = min(max(offsets[min(g, G)], 0), rows), hi = min(max(offsets[min(g + 1, G)], 0), rows);
+    first = lo / kTile;
+    return hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
   }
-  __device__ __forceinline__ bool next() {
-    i += n;
-    n = 1;
+  // items of the 64 adapters from g0 on, summed up to this lane's
+  __device__ __forceinline__ int scan(int g0) const {
+    const int lane = threadIdx.x & 63;
+    int first, v = (tiles_of(g0 + lane, first) + NT - 1) / NT;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      if (j >= i && group[j] < 0 && j == i) ++i;
-    if (i >= NT) return false;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      if (j == i) g = group[j];
-#pragma unroll
-    for (int j = 1; j < NT; ++j)
-      if (j == i + n && group[j] == g) ++n;
-    return true;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(v, d, 64);
+      if (lane >= d) v += u;
+    }
+    return v;
+  }
+  __device__ __forceinline__ Items(const int32_t* offsets, int G, int rows, int cap) : offsets(offsets), G(G), rows(rows) {
+    incl = scan(0);
+    total = __builtin_amdgcn_readlane(incl, 63);
+    for (int g0 = 64; g0 < G; g0 += 64) total += __builtin_amdgcn_readlane(scan(g0), 63);
+    total = min(total, cap);     // (more only if offsets are broken)
+  }
+  __device__ __forceinline__ void find(int item) {
+    int v = incl, before = 0, g0 = 0;
+    for (int n; item >= before + (n = __builtin_amdgcn_readlane(v, 63)) && g0 + 64 < G;) {
+      before += n;
+      g0 += 64;
+      v = scan(g0);
+    }
+    const uint64_t past = __ballot(before + v > item);
+    const int lane = past ? __builtin_ctzll(past) : 63;
+    g = __builtin_amdgcn_readfirstlane(min(g0 + lane, G - 1));
+    const int at = NT * (item - before - (lane > 0 ? __builtin_amdgcn_readlane(v, max(lane, 1) - 1) : 0));
+    int first;
+    const int n = tiles_of(g, first);
+    tile0 = __builtin_amdgcn_readfirstlane(first + max(at, 0));
+    nt = __builtin_amdgcn_readfirstlane(min(n - at, NT));
   }
 };
+
+// The first product's work is cut evenly: stages of KC elements, item by item, in one
+// sequence, quota() of them a workgroup, so a workgroup may end one item and begin the
+// next.  A piece goes to the slab of U that counts the item's workgroups; at most S + 1.
+constexpr int kStage = 64;                 // KC
+constexpr int kFirstWorkgroups = 512;      // two a CU
+__device__ __forceinline__ int quota(int total, int stages, int S) {
+  return max((total * stages + kFirstWorkgroups - 1) / kFirstWorkgroups, (stages + S - 1) / S);
+}
 
 template <int AUX = 0>
 __device__ __forceinline__ void lds_copy(const uint16_t* src, uint8_t* dst) {
@@ -468,8 +490,7 @@ __device__ __forceinline__ void stage_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-constexpr int kShrinkTiles = 4;     // tiles of a workgroup, as many as waves
-constexpr int kExpandTiles = 4;
+constexpr int kItemTiles = 4;       // tiles of an item, as many as waves
 
 template <int RF, int NT, int KC, int NS>
 __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const FirstMany a) {
@@ -492,25 +513,28 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const FirstMany a)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
   const int tile_w = wave / TW * TW, frag_w = wave % TW * FW;
-  const int items = used_items<NT>(a.offsets, a, a.S);
-  if ((int)blockIdx.x >= items) return;
-  const int item = xcd_item(blockIdx.x, items);
-  const int tile0 = item / a.S * NT, slice = item % a.S;
-  const int k_per = 128 * a.k_units, k_lo = min(a.K, slice * k_per), k_hi = min(a.K, k_lo + k_per);
-  const int stages = (k_hi - k_lo) / KC;
+  const int all = (a.K + KC - 1) / KC;          // stages of an item, the last one perhaps partial
+  Items<NT> items(a.offsets, a.G, a.rows, a.cap);
+  const int share = quota(items.total, all, a.S), end = items.total * all;
+  const int used = (end + share - 1) / share;
+  if ((int)blockIdx.x >= used) return;
+  const int me = xcd_item(blockIdx.x, used);
 
-  Runs<NT> run(a, tile0);
-  while (run.next()) {
-    const int i = run.i, nt = run.n, g = run.g;
-    // this run's rows are [16 i, 16 (i + nt)) of the group; the others, and rows without a
-    // token, read the run's first token (columns of their own, not used)
-    const int t0 = max(__builtin_amdgcn_readfirstlane(row_token(a, (tile0 + i) * kTile)), 0);
+  for (int pos = me * share, next; pos < min(end, (me + 1) * share); pos = next) {
+    const int item = pos / all, first = pos - item * all, last = min(all, first + (me + 1) * share - pos);
+    next = pos + last - first;
+    const int slab = me - item * all / share, k_lo = first * KC;
+    const int stages = min(last, a.K / KC) - first;
+    items.find(item);
+    const int tile0 = items.tile0, nt = items.nt, g = items.g;
+    // rows without a token read the item's first token (columns of their own, not used)
+    const int t0 = max(__builtin_amdgcn_readfirstlane(row_token(a, tile0 * kTile)), 0);
     const uint16_t *xs[XC], *as[AC];
     const int cr = lane / NC;                   // row of a copy
 #pragma unroll
     for (int c = 0; c < XC; ++c) {
       const int row = 16 * wave + RPC * c + cr;
-      const int t = wave >= i && wave < i + nt ? row_token(a, tile0 * kTile + row) : -1;
+      const int t = wave < nt ? row_token(a, tile0 * kTile + row) : -1;
       xs[c] = a.X + 8 * (int64_t)(t < 0 ? t0 : t) * a.ldx + k_lo + 8 * ((lane % NC) ^ (row * ROW / 256 % NC));
     }
 #pragma unroll
@@ -547,7 +571,7 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const FirstMany a)
         for (int j = 0; j < TW; ++j) mul_step<FW>(xv[j], av, acc[j]);
       }
     };
-    // (every wave has read the previous run's stages)
+    // (every wave has read the previous item's stages)
     stage_barrier<0>();
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
@@ -568,18 +592,18 @@ __global__ __launch_bounds__(64 * NT) void shrink_many_kernel(const FirstMany a)
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
       const int tile = tile_w + j;
-      if (tile < i || tile >= i + nt) continue;
+      if (tile >= nt) continue;
       const int row = (tile0 + tile) * kTile + l16;
-      if (k_lo + KC * stages < k_hi) {          // K's last elements
+      if (last == all && a.K % KC) {            // K's last elements
         const int t = row_token(a, row);
         const uint16_t* ap[FW];
         a_rows<FW>(a, g, frag_w, ap);
-        tail_steps<FW>(a.X + 8 * ((int64_t)(t < 0 ? t0 : t) * a.ldx + lq), ap, k_lo + KC * stages, k_hi, 32, acc[j]);
+        tail_steps<FW>(a.X + 8 * ((int64_t)(t < 0 ? t0 : t) * a.ldx + lq), ap, a.K / KC * KC, a.K, 32, acc[j]);
       }
 #pragma unroll
       for (int f = 0; f < FW; ++f)
         if (16 * (frag_w + f) + 4 * lq < a.r)   // r % 8 == 0
-          *(f32x4_t*)(a.U + ((int64_t)slice * a.tiles() * kTile + row) * a.r + 16 * (frag_w + f) + 4 * lq) = acc[j][f];
+          *(f32x4_t*)(a.U + ((int64_t)slab * a.tiles() * kTile + row) * a.r + 16 * (frag_w + f) + 4 * lq) = acc[j][f];
     }
   }
 }
@@ -612,33 +636,40 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const Second a
   });
 }
 
-// Between the two for many tokens: the slabs of U summed, scaled and split into the second
-// product's two bf16 terms once, instead of by every workgroup that needs a row.  Row
-// layout of UW: 32*RK hi terms, then 32*RK lo terms, zeros past r.
+// Between the two for many tokens: a tile's slabs of U summed, scaled and split into the
+// second product's two bf16 terms once, instead of by every workgroup that needs a row.
+// Row layout of UW: `ranks` hi terms, then `ranks` lo terms, zeros past r.
 __global__ __launch_bounds__(256) void join_kernel(const Join a) {
-  const int quads = a.ranks / 4, tiles = (a.rows + kTile - 1) / kTile;
-  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int row = (int)(j / quads), r4 = (int)(j - (int64_t)row * quads);
-  if (row >= tiles * kTile) return;
-  const int g = a.row_group[min(row / kTile * kTile, a.rows - 1)];
-  if ((uint32_t)g >= (uint32_t)a.G) return;
-  const float s = a.scale ? a.scale[g] : 1.0f;
-  f32x4_t v = {0, 0, 0, 0};
-  if (4 * r4 < a.r) {
-    const float* up = a.U + (int64_t)row * a.r + 4 * r4;
+  Items<kItemTiles> items(a.offsets, a.G, a.rows, a.cap);
+  const int item = blockIdx.x / kItemTiles;
+  if (item >= items.total) return;
+  items.find(item);
+  if ((int)(blockIdx.x % kItemTiles) >= items.nt) return;
+  const int tile = items.tile0 + blockIdx.x % kItemTiles, quads = a.ranks / 4;
+  const int all = (a.K + kStage - 1) / kStage, share = quota(items.total, all, a.S);
+  const int slabs = ((item + 1) * all - 1) / share - item * all / share + 1;
+  const int64_t slab = (int64_t)((a.rows + kTile - 1) / kTile) * kTile * a.r;
+  const float s = a.scale ? a.scale[items.g] : 1.0f;
+  for (int j = threadIdx.x; j < kTile * quads; j += 256) {
+    const int64_t row = tile * kTile + j / quads;
+    const int r4 = j % quads;
+    f32x4_t v = {0, 0, 0, 0};
+    if (4 * r4 < a.r) {
+      const float* up = a.U + row * a.r + 4 * r4;
 #pragma unroll 4
-    for (int sl = 0; sl < a.S; ++sl) v += *(const f32x4_t*)(up + (int64_t)sl * tiles * kTile * a.r);
-  }
-  bf16x4_t h, l;
+      for (int sl = 0; sl < slabs; ++sl) v += *(const f32x4_t*)(up + sl * slab);
+    }
+    bf16x4_t h, l;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    __bf16 hh, ll;
-    split_bf16(4 * r4 < a.r ? s * v[e] : 0.0f, hh, ll);    // (zero also where s is infinite)
-    h[e] = hh;
-    l[e] = ll;
+    for (int e = 0; e < 4; ++e) {
+      __bf16 hh, ll;
+      split_bf16(4 * r4 < a.r ? s * v[e] : 0.0f, hh, ll);    // (zero also where s is infinite)
+      h[e] = hh;
+      l[e] = ll;
+    }
+    *(bf16x4_t*)(a.UW + row * 2 * a.ranks + 4 * r4) = h;
+    *(bf16x4_t*)(a.UW + row * 2 * a.ranks + a.ranks + 4 * r4) = l;
   }
-  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * a.ranks + 4 * r4) = h;
-  *(bf16x4_t*)(a.UW + (int64_t)row * 2 * a.ranks + a.ranks + 4 * r4) = l;
 }
 
 // Second product for many tokens: a workgroup takes 64 rows, a tile a wave, and CB blocks
@@ -655,61 +686,54 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   __shared__ Scratch scratch[kSplitWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int items = used_items<kExpandTiles>(a.offsets, a, a.col_blocks);
-  if ((int)blockIdx.x >= items) return;
-  const int item = xcd_item(blockIdx.x, items);
-  const int tile0 = item / a.col_blocks * kExpandTiles, c0 = item % a.col_blocks * CB;
-  const int tile = tile0 + wave;
-  const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
-  Runs<kExpandTiles> run(a, tile0);
-  bool first = true;
-  while (run.next()) {
-    const bool mine = wave >= run.i && wave < run.i + run.n;
-    const uint16_t* const bg = a.B + 8 * (int64_t)run.g * a.stride_b;
-    if (!first) stage_barrier<0>();     // (every wave has read the previous run's rows)
-    first = false;
+  Items<kItemTiles> items(a.offsets, a.G, a.rows, a.cap);
+  const int n = items.total * a.col_blocks;
+  if ((int)blockIdx.x >= n) return;
+  const int at = xcd_item(blockIdx.x, n), item = at / a.col_blocks, c0 = (at - item * a.col_blocks) * CB;
+  items.find(item);
+  const bool mine = wave < items.nt;
+  const int tile = items.tile0 + (mine ? wave : 0);
+  const int t[2] = {mine ? row_token(a, tile * kTile + (lane >> 3)) : -1,
+                    mine ? row_token(a, tile * kTile + 8 + (lane >> 3)) : -1};
+  const uint16_t* const bg = a.B + 8 * (int64_t)items.g * a.stride_b;
 #pragma unroll
-    for (int q = 0; q < ROWS / RPC / kSplitWaves; ++q) {
-      const int row0 = (q * kSplitWaves + wave) * RPC, row = row0 + lane / NC;
-      const int chunk = (lane % NC) ^ ((row * ROW / 256) % NC);
-      // rows past N repeat the last one, chunks past r the first: neither is used
-      lds_copy(bg + 8 * ((int64_t)min(64 * c0 + row, a.N - 1) * a.ldb + (8 * chunk < a.r ? chunk : 0)), bl + row0 * ROW);
-    }
-    u32x4_t base[CB][2];
-    bf16x8_t uh[RK], ul[RK];
-    if (mine) {
-      const __bf16* up = a.UW + ((int64_t)tile * kTile + l16) * (64 * RK) + 8 * lq;
+  for (int q = 0; q < ROWS / RPC / kSplitWaves; ++q) {
+    const int row0 = (q * kSplitWaves + wave) * RPC, row = row0 + lane / NC;
+    const int chunk = (lane % NC) ^ ((row * ROW / 256) % NC);
+    // rows past N repeat the last one, chunks past r the first: neither is used
+    lds_copy(bg + 8 * ((int64_t)min(64 * c0 + row, a.N - 1) * a.ldb + (8 * chunk < a.r ? chunk : 0)), bl + row0 * ROW);
+  }
+  u32x4_t base[CB][2];
+  bf16x8_t uh[RK], ul[RK];
+  const __bf16* up = a.UW + ((int64_t)tile * kTile + l16) * (64 * RK) + 8 * lq;
+#pragma unroll
+  for (int k = 0; k < RK; ++k) {
+    uh[k] = *(const bf16x8_t*)(up + 32 * k);
+    ul[k] = *(const bf16x8_t*)(up + 32 * RK + 32 * k);
+  }
+#pragma unroll
+  for (int c = 0; c < CB; ++c) load_base(a, t, c0 + c, base[c]);
+  stage_barrier<0>();
+  if (!mine) return;
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    if (64 * (c0 + c) >= a.N) break;
+    u32x4_t b[RK][4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int k = 0; k < RK; ++k) {
-        uh[k] = *(const bf16x8_t*)(up + 32 * k);
-        ul[k] = *(const bf16x8_t*)(up + 32 * RK + 32 * k);
+        const int row = 64 * c + 16 * f + l16;
+        b[k][f] = *(const u32x4_t*)(bl + row * ROW + (((4 * k + lq) ^ ((row * ROW / 256) % NC)) << 4));
       }
+    if (a.r % 32) {
 #pragma unroll
-      for (int c = 0; c < CB; ++c) load_base(a, t, c0 + c, base[c]);
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int k = 0; k < RK; ++k)
+          if (32 * k + 8 * lq >= a.r) b[k][f] = (u32x4_t){0, 0, 0, 0};
     }
-    stage_barrier<0>();
-    if (mine) {
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        if (64 * (c0 + c) >= a.N) break;
-        u32x4_t b[RK][4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-          for (int k = 0; k < RK; ++k) {
-            const int row = 64 * c + 16 * f + l16;
-            b[k][f] = *(const u32x4_t*)(bl + row * ROW + (((4 * k + lq) ^ ((row * ROW / 256) % NC)) << 4));
-          }
-        if (a.r % 32) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int k = 0; k < RK; ++k)
-              if (32 * k + 8 * lq >= a.r) b[k][f] = (u32x4_t){0, 0, 0, 0};
-        }
-        add_block<RK>(a, t, c0 + c, b, uh, ul, base[c], scratch[wave]);
-      }
-    }
+    add_block<RK>(a, t, c0 + c, b, uh, ul, base[c], scratch[wave]);
   }
 }
 
@@ -745,12 +769,19 @@ static int rank_fragments(int64_t tiles, int64_t S, int64_t r) {
 // The rank up to which the kernels' fragments reach.
 static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
 
+// Most items of kItemTiles tiles, each of one adapter, among the plan's tiles (at most 2^30
+// stages in all: more than an X that fits the memory has).
+static int64_t most_items(int64_t tiles, int64_t G, int64_t K) {
+  const int64_t n = ceil_div(tiles, kItemTiles) + (G < tiles ? G : tiles), most = (int64_t(1) << 30) / ceil_div(K, kStage);
+  return n < most ? n : most;
+}
+
 // Slices of K in the two-launch form: workgroups for the whole chip; with few tokens at
 // least 1024 elements a slice (two units a wave), as every workgroup of the second launch
 // adds the slabs.
 static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K, int64_t r) {
   const bool many = many_tokens(T, G, r);
-  const int64_t s = many ? ceil_div(512, ceil_div(tiles, kShrinkTiles)) : 512 / tiles;
+  const int64_t s = many ? ceil_div(kFirstWorkgroups, ceil_div(tiles, kItemTiles)) : 512 / tiles;
   const int64_t most = ceil_div(K, many ? 256 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
@@ -767,16 +798,17 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
   const int64_t tiles = ceil_div(a.rows, kTile), blocks = ceil_div(a.N, 64);
   const dim3 threads(64 * kSplitWaves);
   if (a.items > 0 && many_tokens(a.T, a.G, a.r)) {
-    constexpr int KC = 64, NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);     // at most 72 KiB: two workgroups a CU
-    constexpr int CB = RF == 8 ? 2 : 4, ranks = 32 * URows<RF>::RK;
-    a.items = (int)(ceil_div(tiles, kShrinkTiles) * a.S);
-    hipLaunchKernelGGL((shrink_many_kernel<RF, kShrinkTiles, KC, NS>), dim3((unsigned)(a.items + copy_blocks)),
-                       dim3(64 * kShrinkTiles), 0, st, (FirstMany{a, c.offsets}));
-    __bf16* const UW = (__bf16*)(a.U + (int64_t)a.S * tiles * kTile * a.r);
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(tiles * kTile * (ranks / 4), 256)), dim3(256), 0, st,
-                       (Join{a.U, UW, c.second.scale, a.row_group, a.rows, a.G, a.r, a.S, ranks}));
-    SecondMany b = {c.second, c.second.B, UW, c.offsets, c.second.ldb, c.second.stride_b, (int)ceil_div(blocks, CB)};
-    b.items = (int)(ceil_div(tiles, kExpandTiles) * b.col_blocks);
+    constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // at most 72 KiB: two workgroups a CU
+    constexpr int CB = 4, ranks = 32 * URows<RF>::RK;      // columns: 256 a workgroup
+    const int cap = (int)most_items(tiles, a.G, a.K);
+    a.items = (int)(cap * (int64_t)a.S < kFirstWorkgroups ? cap * a.S : kFirstWorkgroups);
+    hipLaunchKernelGGL((shrink_many_kernel<RF, kItemTiles, kStage, NS>), dim3((unsigned)(a.items + copy_blocks)),
+                       dim3(64 * kItemTiles), 0, st, (FirstMany{a, c.offsets, cap}));
+    __bf16* const UW = (__bf16*)(a.U + (int64_t)(a.S + 1) * tiles * kTile * a.r);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(cap * kItemTiles)), dim3(256), 0, st,
+                       (Join{a.U, UW, c.second.scale, c.offsets, a.rows, a.G, a.r, a.S, a.K, ranks, cap}));
+    SecondMany b = {c.second, c.second.B, UW, c.offsets, c.second.ldb, c.second.stride_b, (int)ceil_div(blocks, CB), cap};
+    b.items = cap * b.col_blocks;
     hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)b.items), threads, 0, st, b);
     return;
   }
@@ -803,8 +835,9 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  const int64_t joined = many_tokens(T, G, r) ? 4 * tiles * kTile * padded_rank(r) : 0;
-  return 4 * (int64_t)slices(T, G, tiles, K, r) * tiles * kTile * r + joined;
+  const bool many = many_tokens(T, G, r);
+  const int64_t joined = many ? 4 * tiles * kTile * padded_rank(r) : 0;
+  return 4 * ((int64_t)slices(T, G, tiles, K, r) + many) * tiles * kTile * r + joined;
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
@@ -815,7 +848,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   if (T < 0 || G < 0 || N < 0 || K < 0 || r < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
   if (r > 128 || r % 8 || K % 8) return BSG_ERR_UNSUPPORTED_SHAPE;
   if (T > kMaxRows || rows > kMaxRows || N > (int64_t(1) << 23) || K > kMaxK || G > 1024 ||
-      ceil_div(rows, kExpandTiles * kTile) * ceil_div(N, 128) > kMaxBlocks)
+      (ceil_div(rows, kItemTiles * kTile) + G) * ceil_div(N, 256) > kMaxBlocks)
     return BSG_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || N == 0) return BSG_OK;
   if (!out || ldo < N || !row_of || (base && ld_base < N)) return BSG_ERR_INVALID_ARG;
