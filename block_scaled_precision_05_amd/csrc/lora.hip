@@ -12,10 +12,10 @@
 // move once, at the rate of HBM, and the adapters come from L2.
 //   Few tokens: shrink_kernel (U in S slices of K), expand_kernel; operands go straight
 //     from global memory to MFMA fragments.  64 tokens of 32 adapters, rank 16, 7168 to
-//     2048 wide: 4.7 + 5.2 us; 1 token, rank 8: 3.8 + 5.0.
+//     2048 wide: 4.4 + 4.7 us; 1 token, rank 8: 3.4 + 5.2.
 //   Many tokens: shrink_many_kernel, join_kernel, expand_many_kernel; 64 tokens share an
 //     adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64, 7168 to 4096
-//     wide: 36 + 5 + 27 us, where the 263 MB take 54 us at the rate of a copy.
+//     wide: 31 + 5 + 24 us, where the 263 MB take 54 us at the rate of a copy.
 // A token without an adapter is copied by the first launch's last workgroups.
 //
 // U = s_g A_g x is summed in fp32 and keeps that precision through the second product:
@@ -403,8 +403,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const First a)
   }
 }
 
-// First product for many tokens: NT tiles of the plan against the whole rank, K in stages of
-// KC elements (128 or 256 bytes a row).  Fragments straight from global memory would ask for 64
+// First product for many tokens: NT tiles of an adapter against its whole rank, K in stages
+// of KC elements (128 bytes a row).  Fragments straight from global memory would ask for 64
 // bytes of each of 16 rows at a time, and what bounds the kernel is the number of requests
 // a CU keeps in flight; here the stages of X and A_g are copied to LDS by whole lines,
 // NS - 1 stages ahead, and each wave reads its 16 tokens' and A_g's fragments from there.
@@ -465,8 +465,11 @@ struct Items {
 // The first product's work is cut evenly: stages of KC elements, item by item, in one
 // sequence, quota() of them a workgroup, so a workgroup may end one item and begin the
 // next.  A piece goes to the slab of U that counts the item's workgroups; at most S + 1.
+// (Whole slices of groups of 64 rows, 492 workgroups at once, some with two passes: 36 us
+// for 8192 tokens of 16 adapters, rank 64, 7168 wide, against 31.  Two workgroups a CU:
+// the same there, 41 against 38 us in all for 8192 tokens, rank 128, 2048 to 1024 wide.)
 constexpr int kStage = 64;                 // KC
-constexpr int kFirstWorkgroups = 512;      // two a CU
+constexpr int kFirstWorkgroups = 256;      // one a CU
 __device__ __forceinline__ int quota(int total, int stages, int S) {
   return max((total * stages + kFirstWorkgroups - 1) / kFirstWorkgroups, (stages + S - 1) / S);
 }
@@ -744,14 +747,10 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
 // read a whole adapter from L2, T r / 16 elements a column; grouped, 64 tokens share it,
-// for one more launch and a pass per adapter in a group, of which there are more the more
-// adapters there are, four at most.  K = N = 4096, in us, tile by tile / grouped:
-//   G 1:  r 8, T 2048 16.3 / 16.7, T 4096 28.7 / 24.7;  r 128, T 256 16.6 / 15.2;
-//   G 8:  r 16, T 4096 32 / 33, r 32 40 / 34;  r 64, T 1024 21 / 24, T 2048 33 / 31;
-//   G 64: r 32, T 2048 27 / 30, T 4096 42 / 37;  r 64, T 1024 31 / 37, T 2048 40 / 38.
-static bool many_tokens(int64_t T, int64_t G, int64_t r) {
-  return T * r >= 2048 * (G < 15 ? 12 + 3 * G : 57);
-}
+// for one more launch.  K = N = 4096, in us, tile by tile / grouped, 1, 8 and 64 adapters:
+//   T r = 32768:  T 2048: 17 / 18, 17 / 20, 22 / 19;   T 512: 14 / 15, 15 / 15, 23 / 26;
+//   T r = 65536:  T 2048: 22 / 19, 22 / 21, 27 / 22;   T 512: 24 / 21, 26 / 21, 42 / 37.
+static bool many_tokens(int64_t T, int64_t r) { return T * r >= 40 * 1024; }
 
 // Rank fragments of a workgroup of the first product for few tokens: the whole rank, or
 // parts of it, each of which reads X again, for about 1024 workgroups (1 token, rank 128:
@@ -776,13 +775,14 @@ static int64_t most_items(int64_t tiles, int64_t G, int64_t K) {
   return n < most ? n : most;
 }
 
-// Slices of K in the two-launch form: workgroups for the whole chip; with few tokens at
-// least 1024 elements a slice (two units a wave), as every workgroup of the second launch
-// adds the slabs.
-static int slices(int64_t T, int64_t G, int64_t tiles, int64_t K, int64_t r) {
-  const bool many = many_tokens(T, G, r);
+// Slices of K, workgroups for the whole chip: with few tokens at least 1024 elements (two
+// units a wave), as every workgroup of the second launch adds the slabs; with many at
+// least 512, and quota() may cut one slice more (256 elements: 1024 tokens, rank 128, 28
+// against 24 us).
+static int slices(int64_t T, int64_t tiles, int64_t K, int64_t r) {
+  const bool many = many_tokens(T, r);
   const int64_t s = many ? ceil_div(kFirstWorkgroups, ceil_div(tiles, kItemTiles)) : 512 / tiles;
-  const int64_t most = ceil_div(K, many ? 256 : 1024);
+  const int64_t most = ceil_div(K, many ? 512 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
 
@@ -797,8 +797,8 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
   First a = c.first;
   const int64_t tiles = ceil_div(a.rows, kTile), blocks = ceil_div(a.N, 64);
   const dim3 threads(64 * kSplitWaves);
-  if (a.items > 0 && many_tokens(a.T, a.G, a.r)) {
-    constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // at most 72 KiB: two workgroups a CU
+  if (a.items > 0 && many_tokens(a.T, a.r)) {
+    constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // (twice as many: no faster)
     constexpr int CB = 4, ranks = 32 * URows<RF>::RK;      // columns: 256 a workgroup
     const int cap = (int)most_items(tiles, a.G, a.K);
     a.items = (int)(cap * (int64_t)a.S < kFirstWorkgroups ? cap * a.S : kFirstWorkgroups);
@@ -835,9 +835,9 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  const bool many = many_tokens(T, G, r);
+  const bool many = many_tokens(T, r);
   const int64_t joined = many ? 4 * tiles * kTile * padded_rank(r) : 0;
-  return 4 * ((int64_t)slices(T, G, tiles, K, r) + many) * tiles * kTile * r + joined;
+  return 4 * ((int64_t)slices(T, tiles, K, r) + many) * tiles * kTile * r + joined;
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
@@ -887,7 +887,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   rw.items = adapt;      // (until the launch is laid out: whether there are any)
   rw.G = (uint16_t)G;
   rw.r = (uint16_t)r;
-  const int S = adapt ? slices(T, G, ceil_div(rows, kTile), K, r) : 1;
+  const int S = adapt ? slices(T, ceil_div(rows, kTile), K, r) : 1;
   rw.S = (uint16_t)S;
   (Rows&)c.first = rw;
   c.first.k_units = (uint16_t)ceil_div(ceil_div(K, S), 128);
