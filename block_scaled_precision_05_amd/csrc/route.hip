@@ -438,7 +438,8 @@ __device__ __forceinline__ bool has_rows(const int32_t* row_of, int k) {
 
 // ---------------------------------------------------------------------------
 // Dispatch, bf16: row row_of[t][j] of the output is token t's row.  A wave owns one
-// segment of 64*VEC elements of one token, reads it once and writes it k times.
+// segment of 64*VEC elements of one token, reads it once and writes it k times (4095
+// tokens, 8 choices, 2048 wide: 26 us, 5.9 TB/s).
 // ---------------------------------------------------------------------------
 template <int VEC, int AUX>
 __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
@@ -475,7 +476,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
 // Dispatch with quantisation: token t's row is quantised once (the codes and scale
 // bytes of the per-token quantisers, bit for bit) and its codes and packed scale words
 // written to its k rows.  A wave owns 1024 elements of one token, 16 a lane, so a
-// row's codes leave in 16-byte (e4m3) or 8-byte (e2m1) stores.
+// row's codes leave in 16-byte (e4m3) or 8-byte (e2m1) stores.  A scale word is two bytes
+// of a line that 32 rows of a group share; with many tokens each XCD takes a contiguous
+// part of them, so that most lines fill up in one L2 (835 MB written in place of 872, 212
+// us in place of 214, 5.1 TB/s for 16384 tokens, 6 choices, 7168 wide; 512 tokens on an
+// eighth of the experts 4.7 us).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a),
@@ -534,11 +539,19 @@ __device__ __forceinline__ int quantize16(uint32_t (&w)[8], uint32_t (&q)[4]) {
   return byte;
 }
 
+// The work item of workgroup b of n: workgroups are dealt round-robin to the 8 XCDs, so
+// XCD x gets a contiguous chunk of the items.
+__device__ __forceinline__ int xcd_item(int b, int n) {
+  const int x = b & 7, q = n >> 3, rem = n & 7;
+  return x * q + min(x, rem) + (b >> 3);
+}
+
 template <int FMT, int RULE, int AUX>
 __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ row_of,
     const int32_t* __restrict__ pair_of, int T, int k, int rows, int H, uint8_t* __restrict__ Q,
-    int64_t ldq, int16_t* __restrict__ sf, int64_t ld_sf, int segs, int pad_blocks) {
+    int64_t ldq, int16_t* __restrict__ sf, int64_t ld_sf, int segs, int pad_blocks,
+    int blocks) {
   constexpr int GK = Fmt<FMT>::GK;
   constexpr int LPB = GK / 16;               // lanes per block
   constexpr int WPS = kQElems / GK / 2;      // packed words per segment: 4 (e4m3), 16 (e2m1)
@@ -557,7 +570,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
     return;
   }
   const int64_t task =
-      (int64_t)(blockIdx.x - pad_blocks) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      (int64_t)(AUX ? xcd_item(blockIdx.x - pad_blocks, blocks) : blockIdx.x - pad_blocks) * kWaves +
+      __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (int)(task / segs), s = (int)(task - (int64_t)t * segs);
   if (t >= T || !has_rows(row_of + (int64_t)t * k, k)) return;
   const __amdgpu_buffer_rsrc_t xr = row_rsrc(X, t, T, 2 * ldx, 2u * (uint32_t)H);
@@ -600,7 +614,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
 // Combine: out[t] = bf16( sum_j w[t][j] * Y[row_of[t][j]] ), fp32 sums in the order of
 // j, rounded once.  A wave owns 64*VEC elements of one token; the loads of KC rows (all
 // of them up to eight choices) are in flight together.  A pair without a row reads zeros
-// through an empty buffer and its weight counts as zero.
+// through an empty buffer and its weight counts as zero.  16384 tokens, 6 choices, 7168
+// wide: 271 us, 6.1 TB/s; 33 tokens, 8 choices: 3.3 us.
 // ---------------------------------------------------------------------------
 template <int VEC, int KC, int AUX>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
@@ -638,7 +653,9 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
 // <dO[t], Y[row_of[t][j]]> in fp32.  A workgroup owns a token: its waves take the
 // token's segments in turn, keep one partial dot product per choice and lane, and add
 // them over lanes and waves in a fixed order.  dO is read once per KC choices (all of
-// them up to eight), Y once, dY written once.
+// them up to eight), Y once, dY written once.  8192 tokens, 6 choices, 7168 wide, groups
+// of 128 rows: 349 us, 5.2 TB/s with the padding rows; 257 tokens, 2 choices, 2056 wide:
+// 3.9 us.
 // ---------------------------------------------------------------------------
 template <int VEC, int KC, int AUX>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
@@ -892,7 +909,7 @@ static int dispatch_quant(const void* X, int64_t ldx, const int32_t* row_of, con
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)X,
                        ldx, row_of, pair_of, (int)T, k, (int)rows, (int)H, (uint8_t*)Q, ldq, sf, ld_sf,
-                       (int)segs, (int)pads);
+                       (int)segs, (int)pads, (int)(blocks - pads));
   };
   if (rule == BSG_SCALE_CEIL)
     big ? go(dispatch_quant_kernel<FMT, BSG_SCALE_CEIL, kStreamAux>) : go(dispatch_quant_kernel<FMT, BSG_SCALE_CEIL, 0>);
