@@ -247,3 +247,30 @@ def test_lora_wrong_arguments_raise_on_the_gpu():
                      (lambda: bsg.lora_add_bf16(X, A, B, plan, workspace=scale), bsg.BsgError)):
         with pytest.raises(error):
             f()
+
+
+# several items of 64 rows a workgroup; more adapters than a wave has lanes, most of them
+# with less than an item; in place
+@pytest.mark.parametrize("T,G,K,N,r", [(40000, 5, 64, 24, 8), (30000, 3, 200, 40, 24), (20000, 1024, 72, 40, 16),
+                                       (5000, 700, 128, 300, 72)])
+def test_lora_many_tokens_in_place(T, G, K, N, r):
+    _say(f"lora_add in place T={T} G={G} K={K} N={N} r={r}")
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T)
+    mine = base.clone()
+    assert bsg.lora_add_bf16(X, A, B, plan, scale, mine, out=mine) is mine
+    _check(mine, X, A, B, ids, scale, base, "many tokens, in place")
+
+
+def test_lora_spare_rows_and_workspace():
+    """A plan with more rows than it needs, and a workspace of which nothing behind the
+    documented size is touched."""
+    T, G, K, N, r = 3000, 6, 520, 136, 64
+    ids, _, X, A, B, scale, base = _case(T, G, K, N, r, 8)
+    rows = T + 16 * G + 4096
+    e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+    plan = bsg.sort_tokens(ids, G, align=16, out=bsg.TokenSort(e(G + 1), e(T, 1), e(rows), e(rows)))
+    need = bsg.lib().lora_add_workspace(T, rows, G, N, K, r)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device=DEV)     # NaN as floats
+    out = bsg.lora_add_bf16(X, A, B, plan, scale, base, workspace=ws)
+    _check(out, X, A, B, ids, scale, base, "spare rows")
+    assert torch.all(ws[need:] == 255)
