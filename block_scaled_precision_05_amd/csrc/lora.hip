@@ -13,8 +13,8 @@
 //   Few tokens: shrink_kernel (U in S slices of K), expand_kernel; operands go straight
 //     from global memory to MFMA fragments.  64 tokens of 32 adapters, rank 16, 7168 to
 //     2048 wide: 4.4 + 4.7 us; 1 token, rank 8: 3.4 + 5.2.
-//   Many tokens: shrink_many_kernel, join_kernel, expand_many_kernel; 64 tokens share an
-//     adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64, 7168 to 4096
+//   Many tokens: shrink_many_kernel, where U is large join_kernel, expand_many_kernel; 64
+//     tokens share an adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64, 7168 to 4096
 //     wide: 31 + 5 + 24 us, where the 263 MB take 54 us at the rate of a copy.
 // A token without an adapter is copied by the first launch's last workgroups.
 //
@@ -72,10 +72,12 @@ struct Second : Rows {
 };
 struct SecondMany : Rows {
   const uint16_t* B;
-  const __bf16* UW;        // [tiles*16][hi, lo][rank padded to 32]
+  const float* U;
+  const __bf16* UW;        // [tiles*16][hi, lo][rank padded to 32], or null: U's slabs as they are
+  const float* scale;
   const int32_t* offsets;
   int32_t ldb, stride_b;
-  int32_t col_blocks, cap;
+  int32_t col_blocks, cap, K;
 };
 struct Join {
   const float* U;
@@ -473,6 +475,11 @@ constexpr int kFirstWorkgroups = 256;      // one a CU
 __device__ __forceinline__ int quota(int total, int stages, int S) {
   return max((total * stages + kFirstWorkgroups - 1) / kFirstWorkgroups, (stages + S - 1) / S);
 }
+// Slabs of an item.
+__device__ __forceinline__ int slabs_of(int item, int total, int K, int S) {
+  const int stages = (K + kStage - 1) / kStage, share = quota(total, stages, S);
+  return ((item + 1) * stages - 1) / share - item * stages / share + 1;
+}
 
 template <int AUX = 0>
 __device__ __forceinline__ void lds_copy(const uint16_t* src, uint8_t* dst) {
@@ -639,9 +646,10 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const Second a
   });
 }
 
-// Between the two for many tokens: a tile's slabs of U summed, scaled and split into the
-// second product's two bf16 terms once, instead of by every workgroup that needs a row.
-// Row layout of UW: `ranks` hi terms, then `ranks` lo terms, zeros past r.
+// Between the two for many tokens, where the slabs are large: a tile's slabs of U summed,
+// scaled and split into the second product's two bf16 terms once, instead of by every
+// workgroup that needs a row.  Row layout of UW: `ranks` hi terms, then `ranks` lo terms,
+// zeros past r.
 __global__ __launch_bounds__(256) void join_kernel(const Join a) {
   Items<kItemTiles> items(a.offsets, a.G, a.rows, a.cap);
   const int item = blockIdx.x / kItemTiles;
@@ -649,8 +657,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Join a) {
   items.find(item);
   if ((int)(blockIdx.x % kItemTiles) >= items.nt) return;
   const int tile = items.tile0 + blockIdx.x % kItemTiles, quads = a.ranks / 4;
-  const int all = (a.K + kStage - 1) / kStage, share = quota(items.total, all, a.S);
-  const int slabs = ((item + 1) * all - 1) / share - item * all / share + 1;
+  const int slabs = slabs_of(item, items.total, a.K, a.S);
   const int64_t slab = (int64_t)((a.rows + kTile - 1) / kTile) * kTile * a.r;
   const float s = a.scale ? a.scale[items.g] : 1.0f;
   for (int j = threadIdx.x; j < kTile * quads; j += 256) {
@@ -680,7 +687,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Join a) {
 // wave reads from memory (base, U, its share of B_g) is asked for at once; workgroups side
 // by side on a CU cover the wait.  Chunk c of B_g row n sits at chunk c ^ (n * row bytes /
 // 256 % chunks), as in the first product's ring.
-template <int RF, int CB>
+template <int RF, int CB, bool JOINED>
 __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_eu(RF == 8 ? 2 : 3))) void expand_many_kernel(
     const SecondMany a) {
   constexpr int RK = URows<RF>::RK, NC = 4 * RK, ROW = 16 * NC;   // 16-byte chunks and bytes of a row
@@ -708,14 +715,51 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
   }
   u32x4_t base[CB][2];
   bf16x8_t uh[RK], ul[RK];
-  const __bf16* up = a.UW + ((int64_t)tile * kTile + l16) * (64 * RK) + 8 * lq;
+  f32x4_t u[JOINED ? 1 : 3][RK][2];
+  int slabs = 0;
+  const int64_t slab = (int64_t)a.tiles() * kTile * a.r;
+  const float* const up = a.U + ((int64_t)tile * kTile + l16) * a.r + 8 * lq;
+  if (JOINED) {
+    const __bf16* wp = a.UW + ((int64_t)tile * kTile + l16) * (64 * RK) + 8 * lq;
 #pragma unroll
-  for (int k = 0; k < RK; ++k) {
-    uh[k] = *(const bf16x8_t*)(up + 32 * k);
-    ul[k] = *(const bf16x8_t*)(up + 32 * RK + 32 * k);
+    for (int k = 0; k < RK; ++k) {
+      uh[k] = *(const bf16x8_t*)(wp + 32 * k);
+      ul[k] = *(const bf16x8_t*)(wp + 32 * RK + 32 * k);
+    }
+  } else {
+    slabs = slabs_of(item, items.total, a.K, a.S);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)      // (three at once; there are seldom more)
+#pragma unroll
+      for (int k = 0; k < RK; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u[x][k][e] = (f32x4_t){0, 0, 0, 0};
+          if (x < slabs && 32 * k + 8 * lq < a.r) u[x][k][e] = *(const f32x4_t*)(up + x * slab + 32 * k + 4 * e);
+        }
   }
 #pragma unroll
   for (int c = 0; c < CB; ++c) load_base(a, t, c0 + c, base[c]);
+  if (!JOINED) {
+    const float s = a.scale ? a.scale[items.g] : 1.0f;
+#pragma unroll
+    for (int k = 0; k < RK; ++k) {
+      const bool in = 32 * k + 8 * lq < a.r;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f32x4_t v = u[0][k][e] + u[JOINED ? 0 : 1][k][e] + u[JOINED ? 0 : 2][k][e];
+        for (int x = 3; x < slabs; ++x)
+          if (in) v += *(const f32x4_t*)(up + x * slab + 32 * k + 4 * e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          __bf16 h, l;
+          split_bf16(in ? s * v[i] : 0.0f, h, l);     // (zero also where s is infinite)
+          uh[k][4 * e + i] = h;
+          ul[k][4 * e + i] = l;
+        }
+      }
+    }
+  }
   stage_barrier<0>();
   if (!mine) return;
 #pragma unroll
@@ -786,6 +830,17 @@ static int slices(int64_t T, int64_t tiles, int64_t K, int64_t r) {
   return (int)(s < 1 ? 1 : (s < most ? s : most));
 }
 
+// Whether the second product for many tokens adds U's slabs itself, once per 256 columns,
+// or takes them joined by a launch of their own: itself while those reads are few and the
+// slabs, which it takes one after the other past the third, too (tokens, adapters, K, N,
+// rank: reads x slices, us joined / itself: 8192, 16, 7168, 4096, 16: 27 MB x 2, 50.5 / 47;
+// 8192, 8, 4096, 4096, 32: 51 x 2, 43 / 40;  3000, 8, 4096, 2048, 32: 22 x 6, 19.4 / 18.1;
+// 4096, 4, 2048, 2048, 64: 43 x 4, 22.7 / 23.2;  8192, 16, 7168, 4096, 64: 103 x 2, 62 /
+// 63.5;  1024, 8, 4096, 4096, 64: 42 x 8, 18 / 21).
+static bool adds_slabs(int64_t S, int64_t slab_bytes, int64_t col_blocks) {
+  return (S + 1) * slab_bytes * col_blocks <= (int64_t(160) << 20) / S;
+}
+
 struct Call {
   First first;
   Second second;
@@ -804,12 +859,21 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
     a.items = (int)(cap * (int64_t)a.S < kFirstWorkgroups ? cap * a.S : kFirstWorkgroups);
     hipLaunchKernelGGL((shrink_many_kernel<RF, kItemTiles, kStage, NS>), dim3((unsigned)(a.items + copy_blocks)),
                        dim3(64 * kItemTiles), 0, st, (FirstMany{a, c.offsets, cap}));
-    __bf16* const UW = (__bf16*)(a.U + (int64_t)(a.S + 1) * tiles * kTile * a.r);
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(cap * kItemTiles)), dim3(256), 0, st,
-                       (Join{a.U, UW, c.second.scale, c.offsets, a.rows, a.G, a.r, a.S, a.K, ranks, cap}));
-    SecondMany b = {c.second, c.second.B, UW, c.offsets, c.second.ldb, c.second.stride_b, (int)ceil_div(blocks, CB), cap};
+    SecondMany b = {c.second, c.second.B, a.U, nullptr, c.second.scale, c.offsets, c.second.ldb, c.second.stride_b};
+    b.col_blocks = (int)ceil_div(blocks, CB);
+    b.cap = cap;
+    b.K = a.K;
     b.items = cap * b.col_blocks;
-    hipLaunchKernelGGL((expand_many_kernel<RF, CB>), dim3((unsigned)b.items), threads, 0, st, b);
+    const int64_t slab = 4 * tiles * kTile * a.r;
+    if (adds_slabs(a.S, slab, b.col_blocks)) {
+      hipLaunchKernelGGL((expand_many_kernel<RF, CB, false>), dim3((unsigned)b.items), threads, 0, st, b);
+    } else {
+      __bf16* const UW = (__bf16*)((uint8_t*)a.U + (a.S + 1) * slab);
+      b.UW = UW;
+      hipLaunchKernelGGL(join_kernel, dim3((unsigned)(cap * kItemTiles)), dim3(256), 0, st,
+                         (Join{a.U, UW, c.second.scale, c.offsets, a.rows, a.G, a.r, a.S, a.K, ranks, cap}));
+      hipLaunchKernelGGL((expand_many_kernel<RF, CB, true>), dim3((unsigned)b.items), threads, 0, st, b);
+    }
     return;
   }
   const int rf = rank_fragments(tiles, a.S, a.r);

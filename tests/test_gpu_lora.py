@@ -274,3 +274,22 @@ def test_lora_spare_rows_and_workspace():
     out = bsg.lora_add_bf16(X, A, B, plan, scale, base, workspace=ws)
     _check(out, X, A, B, ids, scale, base, "spare rows")
     assert torch.all(ws[need:] == 255)
+
+
+# U large: its slabs joined by a launch of their own
+@pytest.mark.parametrize("T,G,K,N,r", [(2000, 3, 4096, 2000, 128), (700, 4, 5000, 3000, 104), (1300, 6, 6000, 1500, 40),
+                                       (1280, 70, 7168, 1500, 32), (2560, 3, 4000, 4610, 16)])
+def test_lora_many_tokens_long_rows(T, G, K, N, r):
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r}")
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T)
+    _check(bsg.lora_add_bf16(X, A, B, plan, scale, base), X, A, B, ids, scale, base, "many tokens, long rows")
+    X2 = X.clone()
+    t = int(torch.nonzero(ids[:, 0] == 1)[0])
+    X2[t] = float("nan")
+    got, want = (bsg.lora_add_bf16(x, A, B, plan, scale, base) for x in (X2, X))
+    rest = torch.arange(T, device=DEV) != t
+    assert torch.equal(got[rest], want[rest]) and torch.all(torch.isnan(got[t]))
+    scale[1] = float("inf")
+    got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
+    one = ids[:, 0] == 1
+    assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
