@@ -10,6 +10,7 @@
 // matrix cores' rate (v_mfma_f32_16x16x32_bf16, 16 rows of A_g or B_g against 16 tokens):
 // the work is bound by memory, and for few tokens by latency.  X, base and out should
 // move once, at the rate of HBM, and the adapters come from L2.
+//   Little work: whole_kernel.  1 token, rank 16, 1024 to 1024 wide: 4.1 us.
 //   Few tokens: shrink_kernel (U in S slices of K), expand_kernel; operands go straight
 //     from global memory to MFMA fragments.  64 tokens of 32 adapters, rank 16, 7168 to
 //     2048 wide: 4.4 + 4.7 us; 1 token, rank 8: 3.4 + 5.2.
@@ -86,7 +87,15 @@ struct Join {
   const int32_t* offsets;
   int32_t rows, G, r, S, K, ranks, cap;   // ranks: r padded to 32
 };
-static_assert(sizeof(First) <= 112 && sizeof(Second) <= 112, "see above");
+struct Both {              // one launch for little work
+  const int32_t *pair_of, *row_group, *row_of;
+  const uint16_t *X, *A, *B, *base;
+  const float* scale;
+  uint16_t* out;
+  int32_t ld_base, ldo, N, items, stride_a, stride_b;
+  uint16_t T, rows, ldx, lda, ldb, K8, G, r;      // K8: K / 8
+};
+static_assert(sizeof(First) <= 112 && sizeof(Second) <= 112 && sizeof(Both) <= 112, "see above");
 
 // The work item of workgroup b of n: workgroups are dealt round-robin to the 8 XCDs, so
 // XCD x gets a contiguous chunk of the items.
@@ -646,6 +655,68 @@ __global__ __launch_bounds__(64 * kSplitWaves) void expand_kernel(const Second a
   });
 }
 
+// Both products in one launch, for little work (whole_launch() below): every workgroup of a
+// tile, which has 256 columns, forms the tile's U for itself.
+template <int RF>
+__global__ __launch_bounds__(64 * kSplitWaves) void whole_kernel(const Both b) {
+  __shared__ f32x4_t sums[kSplitWaves][RF][64];
+  __shared__ URows<RF> u;
+  __shared__ Scratch scratch[kSplitWaves];
+  First a;
+  a.pair_of = b.pair_of;
+  a.row_group = b.row_group;
+  a.base = b.base;
+  a.out = b.out;
+  a.ld_base = b.ld_base;
+  a.ldo = b.ldo;
+  a.T = b.T;
+  a.N = b.N;
+  a.rows = b.rows;
+  a.items = b.items;
+  a.G = b.G;
+  a.r = b.r;
+  Second c;
+  (Rows&)c = a;
+  a.row_of = b.row_of;
+  a.A = b.A;
+  a.lda = b.lda;
+  a.stride_a = b.stride_a;
+  c.B = b.B;
+  c.ldb = b.ldb;
+  c.stride_b = b.stride_b;
+  if ((int)blockIdx.x >= a.items) {
+    copy_tokens(a, blockIdx.x - a.items, kSplitWaves);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blocks = (a.N + 63) / 64, col_blocks = (blocks + kSplitWaves - 1) / kSplitWaves;
+  const int item = xcd_item(blockIdx.x, a.items), tile = item / col_blocks;
+  const int c0 = (item - tile * col_blocks) * kSplitWaves + wave;
+  const int tx = row_token(a, tile * kTile + (lane & 15));
+  const int t[2] = {row_token(a, tile * kTile + (lane >> 3)), row_token(a, tile * kTile + 8 + (lane >> 3))};
+  const int g = __builtin_amdgcn_readfirstlane(tile_group(a, tile));
+  if (g < 0) return;
+  const int t0 = max(__builtin_amdgcn_readfirstlane(tx), 0);
+  add_columns<RF>(c, g, t, u, scratch[wave], c0, min(blocks, c0 + 1), 1, [&] {
+    const float s = b.scale ? b.scale[g] : 1.0f;
+    f32x4_t acc[RF];
+    low_rank_rows<RF, 4 / RF>(a, g, 0, b.X + 8 * (int64_t)(tx < 0 ? t0 : tx) * b.ldx, 0, 8 * b.K8, wave, kSplitWaves, acc);
+#pragma unroll
+    for (int f = 0; f < RF; ++f) sums[wave][f][lane] = acc[f];
+    __syncthreads();
+    constexpr int QUADS = URows<RF>::QUADS;
+    for (int j = threadIdx.x; j < QUADS * kTile; j += 64 * kSplitWaves) {
+      const int r4 = j % QUADS, row = j / QUADS;
+      f32x4_t v = {0, 0, 0, 0};
+      if (4 * r4 < a.r)
+#pragma unroll
+        for (int w = 0; w < kSplitWaves; ++w) v += sums[w][r4 >> 2][16 * (r4 & 3) + row];
+      u.put(row, 4 * r4, s * v, a.r);
+    }
+    __syncthreads();
+  });
+}
+
 // Between the two for many tokens, where the slabs are large: a tile's slabs of U summed,
 // scaled and split into the second product's two bf16 terms once, instead of by every
 // workgroup that needs a row.  Row layout of UW: `ranks` hi terms, then `ranks` lo terms,
@@ -841,6 +912,17 @@ static bool adds_slabs(int64_t S, int64_t slab_bytes, int64_t col_blocks) {
   return (S + 1) * slab_bytes * col_blocks <= (int64_t(160) << 20) / S;
 }
 
+// Whether both products go into one launch: while what its workgroups read of K, which
+// each of a tile's does again, takes less time than a second launch (3.3 us and up; two
+// launches 5 and up, and twice the host's work).  us in one launch / in two, replayed:
+//   K 256, N 1024, rank 8:  1 token 3.3 / 5.0, 512 tokens 3.8 / 5.6;
+//   K 2048, N 4096, rank 16:  16 tokens 5.9 / 6.5, 256 tokens 10.6 / 7.5;
+//   K 4096, N 4096, 1 token:  rank 8 6.2 / 6.7, rank 16 7.4 / 7.0;
+//   K 1024, N 1024, rank 32:  64 tokens 5.9 / 6.8;   K 2048: 16 tokens 7.6 / 6.7.
+static bool whole_launch(int64_t T, int64_t workgroups, int64_t K, int64_t r) {
+  return r <= 32 && 2 * K * (r + 8) + K * (T < 16 ? T : 16) <= 160000 * 128 / (workgroups < 128 ? 128 : workgroups);
+}
+
 struct Call {
   First first;
   Second second;
@@ -875,6 +957,18 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
       hipLaunchKernelGGL((expand_many_kernel<RF, CB, true>), dim3((unsigned)b.items), threads, 0, st, b);
     }
     return;
+  }
+  if constexpr (RF <= 2) {
+    const int64_t workgroups = tiles * ceil_div(blocks, kSplitWaves), most = (1 << 16) - 1;
+    if (a.items > 0 && whole_launch(a.T, workgroups, a.K, a.r) && a.T <= most && a.rows <= most && a.ldx <= most &&
+        a.lda <= most && c.second.ldb <= most) {
+      const Both b = {a.pair_of, a.row_group, a.row_of, a.X, a.A, c.second.B, a.base, c.second.scale, a.out,
+                      a.ld_base, a.ldo, a.N, (int)workgroups, a.stride_a, c.second.stride_b,
+                      (uint16_t)a.T, (uint16_t)a.rows, (uint16_t)a.ldx, (uint16_t)a.lda, (uint16_t)c.second.ldb,
+                      (uint16_t)(a.K / 8), a.G, a.r};
+      hipLaunchKernelGGL(whole_kernel<RF>, dim3((unsigned)(workgroups + copy_blocks)), threads, 0, st, b);
+      return;
+    }
   }
   const int rf = rank_fragments(tiles, a.S, a.r);
   if (a.items > 0) a.items = (int)(tiles * a.S * ceil_div(a.r, 16 * rf));

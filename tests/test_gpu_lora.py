@@ -293,3 +293,44 @@ def test_lora_many_tokens_long_rows(T, G, K, N, r):
     got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
     one = ids[:, 0] == 1
     assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
+
+
+def test_lora_little_work_with_far_rows_and_spare_rows():
+    """Sizes that take one launch, with strides and rows past what its arguments hold, each
+    in turn; and the same bits as with close ones where the sums are the same."""
+    T, G, K, N, r = 20, 3, 64, 72, 8
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 4)
+    want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    _check(want, X, A, B, ids, scale, base, "one launch")
+
+    def far(x, ld):
+        y = torch.zeros(*x.shape[:-1], ld, dtype=x.dtype, device=DEV)[..., :x.shape[-1]]
+        return y.copy_(x)
+    e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+    spare = bsg.sort_tokens(ids, G, align=16, out=bsg.TokenSort(e(G + 1), e(T, 1), e(70000), e(70000)))
+    ld = 65536 * 8
+    for what, args in (("X", (far(X, ld), A, B, plan)), ("A", (X, far(A, ld), B, plan)),
+                       ("B", (X, A, far(B, ld), plan)), ("rows", (X, A, B, spare))):
+        _check(bsg.lora_add_bf16(*args, scale, base), X, A, B, ids, scale, base, what)
+    for what, args in (("X", (far(X, ld - 8), A, B, plan)), ("A", (X, far(A, ld - 8), B, plan)),
+                       ("B", (X, A, far(B, ld - 8), plan))):
+        assert torch.equal(bsg.lora_add_bf16(*args, scale, base), want), what
+    assert torch.equal(bsg.lora_add_bf16(X, A, B, plan, scale, far(base, 4097)), want)
+
+
+def test_lora_little_work_that_must_not_spread():
+    """As above where both products take one launch."""
+    T, G, K, N, r = 40, 4, 512, 128, 24
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 3)
+    want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    t = int(torch.nonzero(ids[:, 0] == 1)[0])
+    X2, A2 = X.clone(), A.clone()
+    X2[t] = float("nan")
+    A2[2] = float("inf")
+    got = bsg.lora_add_bf16(X2, A2, B, plan, scale, base)
+    rest = (ids[:, 0] != 2) & (torch.arange(T, device=DEV) != t)
+    assert torch.equal(got[rest], want[rest]) and torch.all(torch.isnan(got[t]))
+    scale[1] = float("inf")
+    got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
+    one = ids[:, 0] == 1
+    assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
