@@ -680,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const int n = k - j0;      // choices left; the last round may hold fewer than KC
     int r[KC];
     float w[KC], dot[KC] = {};
-    // (a token without rows in this round reads nothing; its gradients are zeros)
+    // (a token without rows among these choices reads nothing; its gradients are zeros)
     const int my_segs = choice_rows(row_of + (int64_t)t * k + j0, n, r) ? segs : 0;
 #pragma unroll
     for (int j = 0; j < KC; ++j) w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;

@@ -334,3 +334,45 @@ def test_lora_little_work_that_must_not_spread():
     got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
     one = ids[:, 0] == 1
     assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
+
+
+@pytest.mark.parametrize("T,K,N,r", [(3000, 520, 264, 40), (1300, 6000, 1500, 40), (200, 4104, 500, 72)])
+def test_lora_captured_and_on_two_streams(T, K, N, r):
+    """Each form captured and replayed on new requests with eager calls in between, two graphs
+    in turn, and two calls at once on streams of their own."""
+    _say(f"lora_add captured, T={T} K={K} N={N} r={r}")
+    G = 9
+    ids, _, X, A, B, scale, base = _case(T, G, K, N, r, 1)
+
+    def step():
+        return bsg.lora_add_bf16(X, A, B, bsg.sort_tokens(ids, G, align=16), scale, base)
+    step()
+    torch.cuda.synchronize()
+    graphs, results = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            results.append(step())
+    rng = np.random.default_rng(0)
+    for i in range(4):
+        ids.copy_(torch.from_numpy(rng.integers(-1, G, (T, 1)).astype(np.int32)))
+        X.copy_(torch.randn(T, K, device=DEV))
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        for out in results:
+            assert torch.equal(out, want)
+    plan = bsg.sort_tokens(ids, G, align=16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        outs = []
+        for stream in streams:
+            with torch.cuda.stream(stream):
+                outs.append(bsg.lora_add_bf16(X, A, B, plan, scale, base))
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out, want)
