@@ -38,12 +38,13 @@ static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : B
 // dependent steps, and the scattered 4-byte writes, of which one CU finishes some two a
 // ns.  Up to kSingle pairs there is one launch, in which every workgroup sorts all the
 // pairs for itself, in LDS, and writes a share of the results (4096 pairs, 256 groups
-// padded to 128 rows: 7.4 us, 10.9 where one workgroup writes everything, 9.1 in two
+// padded to 128 rows: 7.4 us, 10.9 where one workgroup writes everything, 8.5 in two
 // launches; 768 pairs, 384 groups: 3.6 us).  More pairs are cut into chunks, counted by a
 // first launch (hist[chunk][g]); in a second one every workgroup sums the counts of all
-// chunks itself (coalesced reads from L2) instead of waiting for a scan launch, and
-// places its chunk, or a share of it where chunks are few (98304 pairs, 384 groups: 12.6
-// us with the gap between the launches; 24576 pairs 9.2, unshared 9.7).
+// chunks itself (coalesced reads from L2, under which it forms the first ranks) instead of
+// waiting for a scan launch, and places its chunk, or a share of it where chunks are few
+// (98304 pairs, 384 groups: 11.2 us with the gap between the launches, 2.5 + 8.8 in the
+// kernels at 256; 24576 pairs in shares 8.5, half a us less than unshared).
 //
 // Ranks, in pair order: a wave takes 64 pairs; a lane's peers, the lanes with its id,
 // come from one ballot per id bit; its rank in the wave is the number of peers below it,
@@ -253,70 +254,86 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const SortAr
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int chunk = blockIdx.x / a.share, part = blockIdx.x % a.share;
   const int p0 = chunk * a.chunk;
-  int g = pair_group(a, p0 + tid);
+  int g = pair_group(a, p0 + tid), rank = 0, run = 0;
 
-  total[tid] = next[tid] = 0;      // kSortThreads == kMaxGroups
-  __syncthreads();
-  {
-    // 2^s threads share a word (two groups) and take every 2^s-th chunk (integer sums by
-    // LDS atomics: any order gives the same result)
-    const int words = (a.G + 1) / 2;
-    int s = 0;
-    while ((words << (s + 1)) <= kSortThreads) ++s;
-    const int parts = 1 << s, w = tid % words, first = tid / words;
-    if (first < parts) {
-      int sum0 = 0, sum1 = 0, mine0 = 0, mine1 = 0;
-      for (int c0 = first; c0 < a.nchunks; c0 += 16 * parts) {
-        uint32_t v[16];       // in flight together
+  // The chunks' counts: 2^s threads share a word (two groups) and take every 2^s-th chunk,
+  // 16 loads in flight together, which the first pairs' ranks are formed under.
+  const int words = (a.G + 1) / 2;
+  int s = 0;
+  while ((words << (s + 1)) <= kSortThreads) ++s;
+  const int parts = 1 << s, w = tid % words, first = tid / words;
+  uint32_t v[16];
+  auto load_counts = [&](int c0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = c0 + i * parts;
-          v[i] = a.hist[min(c, a.nchunks - 1) * words + w];
-          if (c >= a.nchunks) v[i] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool before = c0 + i * parts < chunk;
-          sum0 += v[i] & 0xFFFF;
-          sum1 += v[i] >> 16;
-          mine0 += before ? v[i] & 0xFFFF : 0;
-          mine1 += before ? v[i] >> 16 : 0;
-        }
-      }
-      atomicAdd(&total[2 * w], sum0);
-      atomicAdd(&total[2 * w + 1], sum1);
-      atomicAdd(&next[2 * w], mine0);
-      atomicAdd(&next[2 * w + 1], mine1);
+    for (int i = 0; i < 16; ++i) {
+      const int c = c0 + i * parts;
+      v[i] = a.hist[min(c, a.nchunks - 1) * words + w];
+      if (c >= a.nchunks) v[i] = 0;
     }
-  }
-  __syncthreads();
-  group_starts(a, tid < a.G ? total[tid] : 0, start, wave_sum);
+  };
+  if (first < parts) load_counts(first);
+  total[tid] = next[tid] = 0;      // kSortThreads == kMaxGroups
 
-  for (int i0 = 0; i0 < a.chunk && p0 + i0 < a.n; i0 += kSortThreads) {   // uniform over the workgroup
-    if (i0 > 0) g = pair_group(a, p0 + i0 + tid);
-    for (int x = lane; x < (a.G + 1) / 2; x += 64) ((uint32_t*)&wcnt[wave][0])[x] = 0;
+  // a pair's rank in its wave, and the wave's counts
+  auto rank_wave = [&] {
+    for (int x = lane; x < words; x += 64) ((uint32_t*)&wcnt[wave][0])[x] = 0;
     // (a wave's own row: its LDS accesses execute in order)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     const uint64_t peers = same_group(g, a.G);
-    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    rank = __popcll(peers & ((1ull << lane) - 1));
     if (g >= 0 && rank == 0) wcnt[wave][g] = (uint16_t)__popcll(peers);
-    __syncthreads();
-    int run = 0;
+  };
+  // counts to the waves' bases in their groups; run: the workgroup's pairs of group tid
+  auto wave_bases = [&] {
+    run = 0;
     if (tid < a.G) {
       int c[kSortWaves];
 #pragma unroll
-      for (int w = 0; w < kSortWaves; ++w) c[w] = wcnt[w][tid];
+      for (int x = 0; x < kSortWaves; ++x) c[x] = wcnt[x][tid];
 #pragma unroll
-      for (int w = 0; w < kSortWaves; ++w) {
-        wcnt[w][tid] = (uint16_t)run;
-        run += c[w];
+      for (int x = 0; x < kSortWaves; ++x) {
+        wcnt[x][tid] = (uint16_t)run;
+        run += c[x];
       }
     }
-    __syncthreads();
+  };
+  rank_wave();
+  __syncthreads();
+  if (first < parts) {
+    int sum0 = 0, sum1 = 0, mine0 = 0, mine1 = 0;
+    for (int c0 = first; c0 < a.nchunks; c0 += 16 * parts) {
+      if (c0 > first) load_counts(c0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool before = c0 + i * parts < chunk;
+        sum0 += v[i] & 0xFFFF;
+        sum1 += v[i] >> 16;
+        mine0 += before ? v[i] & 0xFFFF : 0;
+        mine1 += before ? v[i] >> 16 : 0;
+      }
+    }
+    // (integer sums: any order gives the same result)
+    atomicAdd(&total[2 * w], sum0);
+    atomicAdd(&total[2 * w + 1], sum1);
+    atomicAdd(&next[2 * w], mine0);
+    atomicAdd(&next[2 * w + 1], mine1);
+  }
+  wave_bases();
+  __syncthreads();
+  group_starts(a, tid < a.G ? total[tid] : 0, start, wave_sum);
+
+  for (int i0 = 0;; i0 += kSortThreads) {   // uniform over the workgroup
+    if (i0 > 0) {
+      if (tid < a.G) next[tid] += run;
+      g = pair_group(a, p0 + i0 + tid);
+      rank_wave();
+      __syncthreads();
+      wave_bases();
+      __syncthreads();
+    }
     if (wave % a.share == part) place(a, p0 + i0 + tid, g, g >= 0 ? next[g] + wcnt[wave][g] + rank : 0, start);
-    __syncthreads();
-    if (tid < a.G) next[tid] += run;
-    __syncthreads();
+    if (i0 + kSortThreads >= a.chunk || p0 + i0 + kSortThreads >= a.n) break;
+    __syncthreads();      // (every wave has read next and wcnt)
   }
   fill_rest(a, start, [&](int gg) { return total[gg]; });
 }
