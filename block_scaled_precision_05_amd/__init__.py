@@ -682,9 +682,8 @@ def sort_tokens(ids, G: int, align: int = 1, cap: int = 0, out: TokenSort | None
     plan.offsets are the masked GEMM's counts.  ``out`` may pass a plan's four tensors
     (rows at least T*k + min(G, T*k)*(align-1), or G*cap), ``workspace`` a contiguous
     tensor of at least sort_tokens_workspace(T*k, G) bytes."""
-    if stream is None and ids.is_cuda:
-        dev = _current_device()
-        r = (_native_module or _native()).sort_tokens(dev, _raw_stream(dev), ids, G, align, cap) if out is workspace is None \
+    if stream is None:
+        r = (_native_module or _native()).sort_tokens(ids, G, align, cap) if out is workspace is None \
             else None
         if r is not None:
             return r
@@ -760,9 +759,8 @@ def moe_dispatch_bf16(X, plan, out=None, stream=None):
     rows are zero and rows of no group (pair_of -2) keep what ``out`` held (they are
     uninitialised in a tensor allocated here).  The gradient with respect to X is
     moe_combine(gradient, plan)."""
-    if stream is None and X.is_cuda:
-        dev = _current_device()
-        r = (_native_module or _native()).moe_dispatch_bf16(dev, _raw_stream(dev), X, plan, out)
+    if stream is None:
+        r = (_native_module or _native()).moe_dispatch_bf16(X, plan, out)
         if r is not None:
             return r
     row_of, pair_of, _, T, k, rows = _plan(plan, X, out)
@@ -780,10 +778,9 @@ def moe_dispatch_bf16(X, plan, out=None, stream=None):
 
 
 def _dispatch_quant(fn, X, plan, rule, per, gk, out, sf_out, stream):
-    if stream is None and X.is_cuda:
-        dev = _current_device()
+    if stream is None:
         r = (_native_module or _native()).moe_dispatch_quantized(
-            dev, _raw_stream(dev), per == 2, X, plan, SCALE_RULES.get(rule, -1), out, sf_out)
+            per == 2, X, plan, SCALE_RULES.get(rule, -1), out, sf_out)
         if r is not None:
             return r
     row_of, pair_of, _, T, k, rows = _plan(plan, X, out, sf_out)
@@ -829,9 +826,8 @@ def moe_combine(Y, plan, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * Y[plan.row_of[t, j]] (bf16 [T, H], fp32 sums, rounded
     once); weights float32 [T, k], or None for ones (the gradient of the dispatch).  A
     pair without a row adds nothing."""
-    if stream is None and Y.is_cuda:
-        dev = _current_device()
-        r = (_native_module or _native()).moe_combine(dev, _raw_stream(dev), Y, plan, weights, out)
+    if stream is None:
+        r = (_native_module or _native()).moe_combine(Y, plan, weights, out)
         if r is not None:
             return r
     row_of, _, _, T, k, rows = _plan(plan, Y, weights, out)
@@ -854,10 +850,9 @@ def moe_combine_backward(dout, Y, plan, weights=None, need_weights: bool = True,
     """Gradients of moe_combine: (dY bf16 [rows, H], dW float32 [T, k]) from dout bf16
     [T, H].  Padding rows of dY are zero, rows of no group keep what ``out`` held.  With
     need_weights False dW is None and Y is not read (it may be None)."""
-    if stream is None and dout.is_cuda:
-        dev = _current_device()
+    if stream is None:
         r = (_native_module or _native()).moe_combine_backward(
-            dev, _raw_stream(dev), dout, Y, plan, weights, out) if need_weights else None
+            dout, Y, plan, weights, out) if need_weights else None
         if r is not None:
             return r
     row_of, pair_of, _, T, k, rows = _plan(plan, dout, Y, weights, out)
@@ -886,10 +881,9 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
     align) with align a multiple of 16; scale float32 [G] or None; base bf16 [T, N] or
     None (zeros).  ``out`` may be ``base`` (in place).  ``workspace`` may pass a 16-byte
     aligned contiguous tensor of at least lora_add_workspace(T, rows, G, N, K, r) bytes."""
-    if stream is None and X.is_cuda:
-        dev = _current_device()
+    if stream is None:
         r = (_native_module or _native()).lora_add_bf16(
-            dev, _raw_stream(dev), X, A, B, plan, scale, base, out) if workspace is None else None
+            X, A, B, plan, scale, base, out) if workspace is None else None
         if r is not None:
             return r
     row_of, pair_of, row_group, T, k, rows = _plan(plan, X, A, B, scale, base, out, workspace)

@@ -40,11 +40,11 @@ def _binding_command(target: str) -> list:
     import torch
     from torch.utils import cpp_extension
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    include = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")] + cpp_extension.include_paths()
-    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    include = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")] + cpp_extension.include_paths("cuda")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
         ["-isystem" + i for i in include] + [BINDING_SOURCE, "-o", target, "-L" + lib, "-ltorch_python",
-                                              "-ltorch_cpu", "-ltorch_hip", "-lc10"]
+                                              "-ltorch_cpu", "-ltorch_hip", "-lc10_hip", "-lc10"]
 
 
 def build(force: bool = True, verbose: bool = False) -> str:

@@ -12,6 +12,8 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
 #include <stdint.h>
 
 #include "../../include/bsg.h"
@@ -121,23 +123,27 @@ struct Plan {
   }
 };
 
-// (device, stream, ...) of every call
-bool place(PyObject* const* a, int64_t& dev, void*& stream) {
-  dev = PyLong_AsLongLong(a[0]);
-  stream = PyLong_AsVoidPtr(a[1]);
-  return !PyErr_Occurred();
+// The current device and its current stream; false where the call's first tensor is not on
+// a GPU.
+bool place(PyObject* first, int64_t& dev, void*& stream) {
+  if (!THPVariable_Check(first) || !THPVariable_Unpack(first).is_cuda()) return false;
+  const auto d = c10::hip::current_device();
+  dev = d;
+  stream = c10::hip::getCurrentHIPStream(d).stream();
+  return true;
 }
 
-// sort_tokens(dev, stream, ids, G, align, cap)
+// sort_tokens(ids, G, align, cap)
 PyObject* sort_tokens_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 6 || !place(a, dev, stream)) return n == 6 ? nullptr : (PyErr_BadArgument(), nullptr);
-  const int64_t G = PyLong_AsLongLong(a[3]), align = PyLong_AsLongLong(a[4]), cap = PyLong_AsLongLong(a[5]);
+  if (n != 4) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
+  const int64_t G = PyLong_AsLongLong(a[1]), align = PyLong_AsLongLong(a[2]), cap = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred()) return nullptr;
   bool ok = G >= 1 && G <= 1024 && align >= 1 && align <= 65536 && cap >= 0 && cap <= (1 << 20);
-  const at::Tensor* ids = tensor(a[2], at::kInt, dev, ok);
+  const at::Tensor* ids = tensor(a[0], at::kInt, dev, ok);
   if (!ok || ids->dim() != 2) Py_RETURN_NONE;
   const int64_t T = ids->size(0), k = ids->size(1), pairs = T * k;
   const int64_t ld = matrix(ids, T, k, ok);
@@ -171,18 +177,19 @@ PyObject* sort_tokens_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// moe_dispatch_bf16(dev, stream, X, plan, out)
+// moe_dispatch_bf16(X, plan, out)
 PyObject* moe_dispatch_bf16_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 5 || !place(a, dev, stream)) return n == 5 ? nullptr : (PyErr_BadArgument(), nullptr);
+  if (n != 3) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
   bool ok = true;
-  const Plan p(a[3], dev, ok);
-  const at::Tensor* X = tensor(a[2], at::kBFloat16, dev, ok);
+  const Plan p(a[1], dev, ok);
+  const at::Tensor* X = tensor(a[0], at::kBFloat16, dev, ok);
   if (!ok || X->dim() != 2) Py_RETURN_NONE;
   const int64_t H = X->size(1), ldx = matrix(X, p.T, H, ok);
-  const at::Tensor* out = a[4] == Py_None ? nullptr : tensor(a[4], at::kBFloat16, dev, ok);
+  const at::Tensor* out = a[2] == Py_None ? nullptr : tensor(a[2], at::kBFloat16, dev, ok);
   const int64_t ldo = out ? matrix(out, p.rows, H, ok) : H;
   if (!ok) Py_RETURN_NONE;
   at::Tensor made;
@@ -194,27 +201,28 @@ PyObject* moe_dispatch_bf16_(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                  (int32_t)p.k, p.rows, H, out ? out->data_ptr() : made.data_ptr(), ldo, stream);
   }
   if (status != BSG_OK) Py_RETURN_NONE;
-  return out ? Py_NewRef(a[4]) : THPVariable_Wrap(std::move(made));
+  return out ? Py_NewRef(a[2]) : THPVariable_Wrap(std::move(made));
   END_HANDLE_TH_ERRORS
 }
 
-// moe_dispatch_quantized(dev, stream, fp4, X, plan, rule, out, sf_out) -> (codes, scales)
+// moe_dispatch_quantized(fp4, X, plan, rule, out, sf_out) -> (codes, scales)
 PyObject* moe_dispatch_quantized_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 8 || !place(a, dev, stream)) return n == 8 ? nullptr : (PyErr_BadArgument(), nullptr);
-  const bool fp4 = a[2] == Py_True;
-  const int64_t rule = PyLong_AsLongLong(a[5]);
+  if (n != 6) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[1], dev, stream)) Py_RETURN_NONE;
+  const bool fp4 = a[0] == Py_True;
+  const int64_t rule = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred()) return nullptr;
   bool ok = true;
-  const Plan p(a[4], dev, ok);
-  const at::Tensor* X = tensor(a[3], at::kBFloat16, dev, ok);
+  const Plan p(a[2], dev, ok);
+  const at::Tensor* X = tensor(a[1], at::kBFloat16, dev, ok);
   if (!ok || X->dim() != 2) Py_RETURN_NONE;
   const int64_t H = X->size(1), ldx = matrix(X, p.T, H, ok);
   const int64_t gk = fp4 ? 32 : 128, cols = fp4 ? H / 2 : H, kp = (H / gk + 1) / 2;
-  const at::Tensor* out = a[6] == Py_None ? nullptr : tensor(a[6], at::kByte, dev, ok);
-  const at::Tensor* sf = a[7] == Py_None ? nullptr : tensor(a[7], at::kShort, dev, ok);
+  const at::Tensor* out = a[4] == Py_None ? nullptr : tensor(a[4], at::kByte, dev, ok);
+  const at::Tensor* sf = a[5] == Py_None ? nullptr : tensor(a[5], at::kShort, dev, ok);
   const int64_t ldq = out ? matrix(out, p.rows, cols, ok) : cols;
   if (!ok || H == 0 || H % gk) Py_RETURN_NONE;
   if (sf && (sf->dim() != 2 || sf->size(1) < p.rows)) Py_RETURN_NONE;
@@ -234,26 +242,27 @@ PyObject* moe_dispatch_quantized_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (status != BSG_OK) Py_RETURN_NONE;
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;
-  PyTuple_SET_ITEM(r, 0, out ? Py_NewRef(a[6]) : THPVariable_Wrap(std::move(q)));
-  PyTuple_SET_ITEM(r, 1, sf ? Py_NewRef(a[7]) : THPVariable_Wrap(std::move(s)));
+  PyTuple_SET_ITEM(r, 0, out ? Py_NewRef(a[4]) : THPVariable_Wrap(std::move(q)));
+  PyTuple_SET_ITEM(r, 1, sf ? Py_NewRef(a[5]) : THPVariable_Wrap(std::move(s)));
   return r;
   END_HANDLE_TH_ERRORS
 }
 
-// moe_combine(dev, stream, Y, plan, weights, out)
+// moe_combine(Y, plan, weights, out)
 PyObject* moe_combine_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 6 || !place(a, dev, stream)) return n == 6 ? nullptr : (PyErr_BadArgument(), nullptr);
+  if (n != 4) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
   bool ok = true;
-  const Plan p(a[3], dev, ok);
-  const at::Tensor* Y = tensor(a[2], at::kBFloat16, dev, ok);
+  const Plan p(a[1], dev, ok);
+  const at::Tensor* Y = tensor(a[0], at::kBFloat16, dev, ok);
   if (!ok || Y->dim() != 2) Py_RETURN_NONE;
   const int64_t H = Y->size(1), ldy = matrix(Y, p.rows, H, ok);
-  const at::Tensor* W = a[4] == Py_None ? nullptr : tensor(a[4], at::kFloat, dev, ok);
+  const at::Tensor* W = a[2] == Py_None ? nullptr : tensor(a[2], at::kFloat, dev, ok);
   const int64_t ldw = W ? matrix(W, p.T, p.k, ok) : p.k;
-  const at::Tensor* out = a[5] == Py_None ? nullptr : tensor(a[5], at::kBFloat16, dev, ok);
+  const at::Tensor* out = a[3] == Py_None ? nullptr : tensor(a[3], at::kBFloat16, dev, ok);
   const int64_t ldo = out ? matrix(out, p.T, H, ok) : H;
   if (!ok) Py_RETURN_NONE;
   at::Tensor made;
@@ -265,25 +274,26 @@ PyObject* moe_combine_(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            p.rows, H, out ? out->data_ptr() : made.data_ptr(), ldo, stream);
   }
   if (status != BSG_OK) Py_RETURN_NONE;
-  return out ? Py_NewRef(a[5]) : THPVariable_Wrap(std::move(made));
+  return out ? Py_NewRef(a[3]) : THPVariable_Wrap(std::move(made));
   END_HANDLE_TH_ERRORS
 }
 
-// moe_combine_backward(dev, stream, dout, Y, plan, weights, out) -> (dY, dW)
+// moe_combine_backward(dout, Y, plan, weights, out) -> (dY, dW)
 PyObject* moe_combine_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 7 || !place(a, dev, stream)) return n == 7 ? nullptr : (PyErr_BadArgument(), nullptr);
+  if (n != 5) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
   bool ok = true;
-  const Plan p(a[4], dev, ok);
-  const at::Tensor* dO = tensor(a[2], at::kBFloat16, dev, ok);
-  const at::Tensor* Y = tensor(a[3], at::kBFloat16, dev, ok);
+  const Plan p(a[2], dev, ok);
+  const at::Tensor* dO = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* Y = tensor(a[1], at::kBFloat16, dev, ok);
   if (!ok || dO->dim() != 2) Py_RETURN_NONE;
   const int64_t H = dO->size(1), ldd = matrix(dO, p.T, H, ok), ldy = matrix(Y, p.rows, H, ok);
-  const at::Tensor* W = a[5] == Py_None ? nullptr : tensor(a[5], at::kFloat, dev, ok);
+  const at::Tensor* W = a[3] == Py_None ? nullptr : tensor(a[3], at::kFloat, dev, ok);
   const int64_t ldw = W ? matrix(W, p.T, p.k, ok) : p.k;
-  const at::Tensor* out = a[6] == Py_None ? nullptr : tensor(a[6], at::kBFloat16, dev, ok);
+  const at::Tensor* out = a[4] == Py_None ? nullptr : tensor(a[4], at::kBFloat16, dev, ok);
   const int64_t ldo = out ? matrix(out, p.rows, H, ok) : H;
   if (!ok) Py_RETURN_NONE;
   at::Tensor dY, dW;
@@ -299,29 +309,30 @@ PyObject* moe_combine_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (status != BSG_OK) Py_RETURN_NONE;
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;
-  PyTuple_SET_ITEM(r, 0, out ? Py_NewRef(a[6]) : THPVariable_Wrap(std::move(dY)));
+  PyTuple_SET_ITEM(r, 0, out ? Py_NewRef(a[4]) : THPVariable_Wrap(std::move(dY)));
   PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(dW)));
   return r;
   END_HANDLE_TH_ERRORS
 }
 
-// lora_add_bf16(dev, stream, X, A, B, plan, scale, base, out)
+// lora_add_bf16(X, A, B, plan, scale, base, out)
 PyObject* lora_add_bf16_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
   void* stream;
-  if (n != 9 || !place(a, dev, stream)) return n == 9 ? nullptr : (PyErr_BadArgument(), nullptr);
+  if (n != 7) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
   bool ok = true;
-  const Plan p(a[5], dev, ok);
-  const at::Tensor* X = tensor(a[2], at::kBFloat16, dev, ok);
-  const at::Tensor* A = tensor(a[3], at::kBFloat16, dev, ok);
-  const at::Tensor* B = tensor(a[4], at::kBFloat16, dev, ok);
+  const Plan p(a[3], dev, ok);
+  const at::Tensor* X = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* A = tensor(a[1], at::kBFloat16, dev, ok);
+  const at::Tensor* B = tensor(a[2], at::kBFloat16, dev, ok);
   if (!ok || p.k != 1 || A->dim() != 3 || B->dim() != 3) Py_RETURN_NONE;
   const int64_t G = A->size(0), r = A->size(1), K = A->size(2), N = B->size(1);
   const int64_t ldx = matrix(X, p.T, K, ok);
-  const at::Tensor* scale = a[6] == Py_None ? nullptr : tensor(a[6], at::kFloat, dev, ok);
-  const at::Tensor* base = a[7] == Py_None ? nullptr : tensor(a[7], at::kBFloat16, dev, ok);
-  const at::Tensor* out = a[8] == Py_None ? nullptr : tensor(a[8], at::kBFloat16, dev, ok);
+  const at::Tensor* scale = a[4] == Py_None ? nullptr : tensor(a[4], at::kFloat, dev, ok);
+  const at::Tensor* base = a[5] == Py_None ? nullptr : tensor(a[5], at::kBFloat16, dev, ok);
+  const at::Tensor* out = a[6] == Py_None ? nullptr : tensor(a[6], at::kBFloat16, dev, ok);
   if (!ok || G == 0 || G > 1024 || r == 0 || K == 0 || N == 0 || B->size(0) != G || B->size(2) != r ||
       A->stride(2) != 1 || B->stride(2) != 1 || p.offsets->numel() != G + 1 ||
       (scale && (scale->dim() != 1 || scale->size(0) != G || !scale->is_contiguous())))
@@ -344,7 +355,7 @@ PyObject* lora_add_bf16_(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              need ? ws.data_ptr() : nullptr, need, stream);
   }
   if (status != BSG_OK) Py_RETURN_NONE;
-  return out ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(made));
+  return out ? Py_NewRef(a[6]) : THPVariable_Wrap(std::move(made));
   END_HANDLE_TH_ERRORS
 }
 
