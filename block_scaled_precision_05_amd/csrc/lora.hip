@@ -861,11 +861,16 @@ constexpr int64_t kMaxK = int64_t(1) << 22;             // 128-element units of 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
-// read a whole adapter from L2, T r / 16 elements a column; grouped, 64 tokens share it,
-// for one more launch.  K = N = 4096, in us, tile by tile / grouped, 1, 8 and 64 adapters:
-//   T r = 32768:  T 2048: 17 / 18, 17 / 20, 22 / 19;   T 512: 14 / 15, 15 / 15, 23 / 26;
-//   T r = 65536:  T 2048: 22 / 19, 22 / 21, 27 / 22;   T 512: 24 / 21, 26 / 21, 42 / 37.
-static bool many_tokens(int64_t T, int64_t r) { return T * r >= 40 * 1024; }
+// read a whole adapter from L2, T r (K + N) / 8 bytes; grouped, 64 tokens share it, for
+// one more launch or two and workgroups that do more each.  T, K, N, r, in M of T r (K + N), us
+// tile by tile / grouped:
+//   2048, 512, 512, 32:    67,  6.3 / 10.4;    1000, 1000, 1000, 64: 128,  9.5 / 13.5;
+//   600, 2000, 2000, 96:  230, 12 / 19;        4000, 4000, 512, 16:  289, 16 / 16;
+//   512, 4096, 4096, 64:  268, 14 / 15;        8192, 4096, 256, 8:   285, 24 / 18;
+//   2048, 4096, 4096, 32: 537, 22 / 20;        8192, 1024, 128, 64:  604, 21 / 15.
+static bool many_tokens(int64_t T, int64_t N, int64_t K, int64_t r) {
+  return T * r * (K + N) >= int64_t(270) << 20;
+}
 
 // Rank fragments of a workgroup of the first product for few tokens: the whole rank, or
 // parts of it, each of which reads X again, for about 1024 workgroups (1 token, rank 128:
@@ -894,8 +899,7 @@ static int64_t most_items(int64_t tiles, int64_t G, int64_t K) {
 // units a wave), as every workgroup of the second launch adds the slabs; with many at
 // least 512, and quota() may cut one slice more (256 elements: 1024 tokens, rank 128, 28
 // against 24 us).
-static int slices(int64_t T, int64_t tiles, int64_t K, int64_t r) {
-  const bool many = many_tokens(T, r);
+static int slices(bool many, int64_t tiles, int64_t K) {
   const int64_t s = many ? ceil_div(kFirstWorkgroups, ceil_div(tiles, kItemTiles)) : 512 / tiles;
   const int64_t most = ceil_div(K, many ? 512 : 1024);
   return (int)(s < 1 ? 1 : (s < most ? s : most));
@@ -903,13 +907,14 @@ static int slices(int64_t T, int64_t tiles, int64_t K, int64_t r) {
 
 // Whether the second product for many tokens adds U's slabs itself, once per 256 columns,
 // or takes them joined by a launch of their own: itself while those reads are few and the
-// slabs, which it takes one after the other past the third, too (tokens, adapters, K, N,
+// slabs, which it takes one after the other past the third, few and narrow (tokens, adapters, K, N,
 // rank: reads x slices, us joined / itself: 8192, 16, 7168, 4096, 16: 27 MB x 2, 50.5 / 47;
 // 8192, 8, 4096, 4096, 32: 51 x 2, 43 / 40;  3000, 8, 4096, 2048, 32: 22 x 6, 19.4 / 18.1;
 // 4096, 4, 2048, 2048, 64: 43 x 4, 22.7 / 23.2;  8192, 16, 7168, 4096, 64: 103 x 2, 62 /
-// 63.5;  1024, 8, 4096, 4096, 64: 42 x 8, 18 / 21).
-static bool adds_slabs(int64_t S, int64_t slab_bytes, int64_t col_blocks) {
-  return (S + 1) * slab_bytes * col_blocks <= (int64_t(160) << 20) / S;
+// 63.5;  1024, 8, 4096, 4096, 64: 42 x 8, 18 / 21;  1000, 8, 4000, 128, 128: 5 x 8, 23 /
+// 31;  2500, 8, 7168, 128, 24: 2 x 7, 18 / 16).
+static bool adds_slabs(int64_t S, int64_t r, int64_t slab_bytes, int64_t col_blocks) {
+  return S * r < 512 && (S + 1) * slab_bytes * col_blocks <= (int64_t(160) << 20) / S;
 }
 
 // Whether both products go into one launch: while what its workgroups read of K, which
@@ -927,6 +932,7 @@ struct Call {
   First first;
   Second second;
   const int32_t* offsets;
+  bool many;
 };
 
 template <int RF>
@@ -934,7 +940,7 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
   First a = c.first;
   const int64_t tiles = ceil_div(a.rows, kTile), blocks = ceil_div(a.N, 64);
   const dim3 threads(64 * kSplitWaves);
-  if (a.items > 0 && many_tokens(a.T, a.r)) {
+  if (a.items > 0 && c.many) {
     constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // (twice as many: no faster)
     constexpr int CB = 4, ranks = 32 * URows<RF>::RK;      // columns: 256 a workgroup
     const int cap = (int)most_items(tiles, a.G, a.K);
@@ -947,7 +953,7 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
     b.K = a.K;
     b.items = cap * b.col_blocks;
     const int64_t slab = 4 * tiles * kTile * a.r;
-    if (adds_slabs(a.S, slab, b.col_blocks)) {
+    if (adds_slabs(a.S, a.r, slab, b.col_blocks)) {
       hipLaunchKernelGGL((expand_many_kernel<RF, CB, false>), dim3((unsigned)b.items), threads, 0, st, b);
     } else {
       __bf16* const UW = (__bf16*)((uint8_t*)a.U + (a.S + 1) * slab);
@@ -993,9 +999,9 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  const bool many = many_tokens(T, r);
+  const bool many = many_tokens(T, N, K, r);
   const int64_t joined = many ? 4 * tiles * kTile * padded_rank(r) : 0;
-  return 4 * ((int64_t)slices(T, tiles, K, r) + many) * tiles * kTile * r + joined;
+  return 4 * ((int64_t)slices(many, tiles, K) + many) * tiles * kTile * r + joined;
 }
 
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
@@ -1045,7 +1051,8 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   rw.items = adapt;      // (until the launch is laid out: whether there are any)
   rw.G = (uint16_t)G;
   rw.r = (uint16_t)r;
-  const int S = adapt ? slices(T, ceil_div(rows, kTile), K, r) : 1;
+  const bool many = many_tokens(T, N, K, r);
+  const int S = adapt ? slices(many, ceil_div(rows, kTile), K) : 1;
   rw.S = (uint16_t)S;
   (Rows&)c.first = rw;
   c.first.k_units = (uint16_t)ceil_div(ceil_div(K, S), 128);
@@ -1064,6 +1071,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   c.second.ldb = (int32_t)(ldb / 8);
   c.second.stride_b = (int32_t)(stride_b / 8);
   c.offsets = offsets;
+  c.many = many;
   const hipStream_t st = (hipStream_t)stream;
   // tokens without an adapter: nothing to do in place
   const int copy_blocks = base == out ? 0 : (int)ceil_div(T, 16);

@@ -75,8 +75,8 @@ def test_lora_matches_oracle(T, G, K, N, r, align):
     _check(mine, X, A, B, ids, scale, base, "in place")
 
 
-# T * r large for the number of adapters: tiles taken in groups; several adapters to a group
-# of 64 rows; K with and without elements past the last whole stage of 64
+# many tokens of narrow adapters; several adapters to 64 rows; K with and without elements past
+# the last whole 64
 @pytest.mark.parametrize("T,G,K,N,r", [(8000, 7, 128, 72, 16), (9000, 40, 64, 40, 64), (16300, 3, 136, 24, 8),
                                        (15500, 90, 96, 33, 128), (16000, 1, 64, 64, 40), (4096, 100, 264, 130, 128),
                                        (3000, 20, 1032, 520, 64), (2100, 2, 40, 300, 48), (2500, 1, 2048, 257, 104)])
@@ -177,7 +177,7 @@ def test_lora_beside_a_projection_captured_and_streamed():
 
 
 def test_lora_many_tokens_without_anything_to_add():
-    """K = 0 and a plan of no rows, with as many tokens as the grouped forms take."""
+    """K = 0 and a plan of no rows, with many tokens."""
     _say("lora_add many tokens, K = 0, no rows")
     e = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)
     T, G, N, r = 4096, 2, 40, 64
@@ -189,8 +189,8 @@ def test_lora_many_tokens_without_anything_to_add():
 
 
 def test_lora_many_tokens_that_must_not_spread():
-    """As above where tiles are grouped; an infinite scale, at a rank that is not a multiple
-    of 32, gives infinities and no NaN."""
+    """As above with many tokens; an infinite scale, at a rank that is not a multiple of 32,
+    gives infinities and no NaN."""
     T, G, K, N, r = 4200, 4, 192, 72, 40
     ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 3)
     want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
@@ -201,7 +201,7 @@ def test_lora_many_tokens_that_must_not_spread():
     got = bsg.lora_add_bf16(X2, A2, B, plan, scale, base)
     rest = (ids[:, 0] != 2) & (torch.arange(T, device=DEV) != t)
     assert torch.equal(got[rest], want[rest]) and torch.all(torch.isnan(got[t]))
-    for T in (T, 60):       # grouped, and few tokens
+    for T in (T, 60):
         ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 4)
         scale[1] = float("inf")
         got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
@@ -249,8 +249,7 @@ def test_lora_wrong_arguments_raise_on_the_gpu():
             f()
 
 
-# several items of 64 rows a workgroup; more adapters than a wave has lanes, most of them
-# with less than an item; in place
+# more adapters than a wave has lanes, many tokens, in place
 @pytest.mark.parametrize("T,G,K,N,r", [(40000, 5, 64, 24, 8), (30000, 3, 200, 40, 24), (20000, 1024, 72, 40, 16),
                                        (5000, 700, 128, 300, 72)])
 def test_lora_many_tokens_in_place(T, G, K, N, r):
@@ -376,3 +375,68 @@ def test_lora_captured_and_on_two_streams(T, K, N, r):
         torch.cuda.synchronize()
         for out in outs:
             assert torch.equal(out, want)
+
+
+# T r (K + N) large, so that tiles are grouped: K with and without elements past the last whole
+# stage of 64, several adapters to 64 rows, more adapters than a wave has lanes, odd N, one
+# and several items a workgroup
+@pytest.mark.parametrize("T,G,K,N,r", [(8000, 7, 2200, 72, 16), (9000, 40, 520, 40, 64), (16300, 3, 2200, 24, 8),
+                                       (15500, 90, 136, 33, 128), (4096, 100, 264, 300, 128), (20000, 1024, 1064, 40, 16),
+                                       (40000, 5, 1000, 24, 8), (5000, 700, 600, 300, 72), (3000, 2, 128, 2313, 40),
+                                       (30000, 1, 40, 290, 32)])
+def test_lora_grouped_tiles(T, G, K, N, r):
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r}")
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T)
+    _check(bsg.lora_add_bf16(X, A, B, plan, scale, base), X, A, B, ids, scale, base, "grouped")
+    _check(bsg.lora_add_bf16(X, A, B, plan), X, A, B, ids, None, None, "grouped, neither")
+    mine = base.clone()
+    assert bsg.lora_add_bf16(X, A, B, plan, scale, mine, out=mine) is mine
+    _check(mine, X, A, B, ids, scale, base, "grouped, in place")
+
+
+def test_lora_grouped_tiles_that_must_not_spread_and_broken_plans():
+    T, G, K, N, r = 4200, 4, 1800, 72, 40
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 3)
+    want = bsg.lora_add_bf16(X, A, B, plan, scale, base)
+    t = int(torch.nonzero(ids[:, 0] == 1)[0])
+    X2, A2 = X.clone(), A.clone()
+    X2[t] = float("nan")
+    A2[2] = float("inf")
+    got = bsg.lora_add_bf16(X2, A2, B, plan, scale, base)
+    rest = (ids[:, 0] != 2) & (torch.arange(T, device=DEV) != t)
+    assert torch.equal(got[rest], want[rest]) and torch.all(torch.isnan(got[t]))
+    scale[1] = float("inf")
+    got = bsg.lora_add_bf16(X.abs(), A.abs(), B.abs(), plan, scale, base)
+    one = ids[:, 0] == 1
+    assert torch.all(got[one] == float("inf")) and torch.all(torch.isfinite(got[~one]))
+    plan.row_group[:16] = 4
+    plan.row_group[16:32] = 2 ** 31 - 1
+    plan.pair_of[40::3] = 2 ** 31 - 1
+    offsets = plan.offsets.clone()
+    for at, value in ((-1, 2 ** 31 - 1), (-1, -5), (1, 2 ** 31 - 1), (2, -1), (0, 777), (3, 0)):
+        plan.offsets.copy_(offsets)
+        plan.offsets[at] = value
+        bsg.lora_add_bf16(X, A, B, plan, scale, base)
+        torch.cuda.synchronize()
+
+
+def test_lora_grouped_tiles_captured():
+    T, G, K, N, r = 9000, 12, 520, 264, 40
+    ids, _, X, A, B, scale, base = _case(T, G, K, N, r, 1)
+
+    def step():
+        return bsg.lora_add_bf16(X, A, B, bsg.sort_tokens(ids, G, align=16), scale, base)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    rng = np.random.default_rng(0)
+    for i in range(4):
+        ids.copy_(torch.from_numpy(np.minimum(rng.integers(-1, G, (T, 1)), i + 3).astype(np.int32)))
+        X.copy_(torch.randn(T, K, device=DEV))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = captured.clone()
+        assert torch.equal(got, step())
