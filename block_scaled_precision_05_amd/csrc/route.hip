@@ -667,20 +667,24 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
 
 // ---------------------------------------------------------------------------
 // Gradient of combine: dY[row_of[t][j]] = bf16( w[t][j] * dO[t] ) and dW[t][j] =
-// <dO[t], Y[row_of[t][j]]> in fp32.  A workgroup owns a token: its waves take the
-// token's segments in turn, keep one partial dot product per choice and lane, and add
-// them over lanes and waves in a fixed order.  dO is read once per KC choices (all of
-// them up to eight), Y once, dY written once.  8192 tokens, 6 choices, 7168 wide, groups
-// of 128 rows: 349 us, 5.2 TB/s with the padding rows; 257 tokens, 2 choices, 2056 wide:
-// 3.9 us.
+// <dO[t], Y[row_of[t][j]]> in fp32.  A workgroup owns KC of a token's choices (all of them
+// up to eight; fewer where tokens are fewer than CUs, of which one moves some 25 bytes a
+// ns): its waves take the token's segments in turn, keep one partial dot product per
+// choice and lane, and add them over lanes and waves in a fixed order.  Where rows are
+// short a wave does that alone (WPT 1).  dO is read once per KC choices, Y once, dY written
+// once.  8192 tokens, 6 choices, 7168 wide, groups of 128 rows: 347 us, 5.2 TB/s with the
+// padding rows;  257 tokens, 2 choices, 2056 wide: 3.9 us;  1 token, 8 choices, 7168 wide:
+// 3.4 us (7.1 in one workgroup);  8192 tokens, 8 choices, 128 wide: 14 us (31 with a
+// workgroup a token;  1024 wide, past the L2s: 55, and 52 with a workgroup).
 // ---------------------------------------------------------------------------
-template <int VEC, int KC, int AUX>
+template <int VEC, int KC, int AUX, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ dO, int64_t ldo, const uint16_t* __restrict__ Y, int64_t ldy,
     const int32_t* __restrict__ row_of, const int32_t* __restrict__ pair_of,
     const float* __restrict__ W, int64_t ldw, int T, int k, int rows, int H,
     uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dW, int64_t lddw) {
-  __shared__ float part[kWaves][KC];
+  static_assert(WPT == 1 || WPT == kWaves, "a wave or a workgroup");
+  __shared__ float part[WPT > 1 ? kWaves : 1][KC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t row_bytes = 2u * (uint32_t)H;
   // (from the sizes: more than 112 bytes of arguments cost 1 us a launch)
@@ -691,60 +695,67 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     });
     return;
   }
-  const int t = blockIdx.x - pad_blocks;
+  const int parts = (k + KC - 1) / KC;
+  const int at = ((int)blockIdx.x - pad_blocks) * (kWaves / WPT) + wave / WPT, t = at / parts;
+  if (t >= T) return;
+  const int j0 = (at - t * parts) * KC, n = k - j0;      // choices from j0 on, n or KC of them
   const __amdgpu_buffer_rsrc_t g = row_rsrc(dO, t, T, 2 * ldo, row_bytes);
-  for (int j0 = 0; j0 < k; j0 += KC) {
-    const int n = k - j0;      // choices left; the last round may hold fewer than KC
-    int r[KC];
-    float w[KC], dot[KC] = {};
-    // (a token without rows among these choices reads nothing; its gradients are zeros)
-    const int my_segs = choice_rows(row_of + (int64_t)t * k + j0, n, r) ? segs : 0;
+  int r[KC];
+  float w[KC], dot[KC] = {};
+  // (a token without rows among these choices reads nothing; its gradients are zeros)
+  const int my_segs = choice_rows(row_of + (int64_t)t * k + j0, n, r) ? segs : 0;
 #pragma unroll
-    for (int j = 0; j < KC; ++j) w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
-    for (int s = wave; s < my_segs; s += kWaves) {
-      const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
-      Vec<VEC> d, y[KC];
-      d.template load<0>(g, off);
-      if (dW) {
+  for (int j = 0; j < KC; ++j) w[j] = j < n ? (W ? W[(int64_t)t * ldw + j0 + j] : 1.0f) : 0.0f;
+  for (int s = wave % WPT; s < my_segs; s += WPT) {
+    const uint32_t off = 2u * VEC * (uint32_t)(s * 64 + lane);
+    Vec<VEC> d, y[KC];
+    d.template load<0>(g, off);
+    if (dW) {
 #pragma unroll
-        for (int j = 0; j < KC; ++j) y[j].template load<AUX>(row_rsrc(Y, r[j], rows, 2 * ldy, row_bytes), off);
-      }
-#pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        float v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = w[j] * d.get(i);
-        Vec<VEC> o;
-        o.set(v);
-        // (choices past the last have no row: the store is dropped)
-        o.template store<AUX>(row_rsrc(dY, r[j], rows, 2 * lddy, row_bytes), off);
-      }
-      if (dW) {
-#pragma unroll
-        for (int j = 0; j < KC; ++j)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
-      }
+      for (int j = 0; j < KC; ++j) y[j].template load<AUX>(row_rsrc(Y, r[j], rows, 2 * ldy, row_bytes), off);
     }
-    if (!dW) continue;
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
-      float v = dot[j];
+      float v[VEC];
 #pragma unroll
-      for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-      if (lane == 0) part[wave][j] = v;
+      for (int i = 0; i < VEC; ++i) v[i] = w[j] * d.get(i);
+      Vec<VEC> o;
+      o.set(v);
+      // (choices past the last have no row: the store is dropped)
+      o.template store<AUX>(row_rsrc(dY, r[j], rows, 2 * lddy, row_bytes), off);
     }
-    __syncthreads();
-    if ((int)threadIdx.x < (n < KC ? n : KC)) {
-      float v = 0.0f;
+    if (dW) {
 #pragma unroll
-      for (int x = 0; x < kWaves; ++x) v += part[x][threadIdx.x];
-      // (a pair without a row has read zeros; an infinity in dO must not turn its
-      // gradient into NaN)
-      const int rr = row_of[(int64_t)t * k + j0 + threadIdx.x];
-      dW[(int64_t)t * lddw + j0 + threadIdx.x] = (uint32_t)rr < (uint32_t)rows ? v : 0.0f;
+      for (int j = 0; j < KC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
     }
-    __syncthreads();
+  }
+  if (!dW) return;
+#pragma unroll
+  for (int j = 0; j < KC; ++j) {
+    float v = dot[j];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+    if (WPT == 1) {
+      if (lane == j) dot[0] = v;
+    } else if (lane == 0) {
+      part[wave][j] = v;
+    }
+  }
+  const int j = WPT == 1 ? lane : (int)threadIdx.x;
+  if (WPT > 1) __syncthreads();
+  if (j < (n < KC ? n : KC)) {
+    float v = dot[0];
+    if (WPT > 1) {
+      v = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) v += part[x][j];
+    }
+    // (a pair without a row has read zeros; an infinity in dO must not turn its
+    // gradient into NaN)
+    const int rr = row_of[(int64_t)t * k + j0 + j];
+    dW[(int64_t)t * lddw + j0 + j] = (uint32_t)rr < (uint32_t)rows ? v : 0.0f;
   }
 }
 
@@ -774,6 +785,8 @@ static void with_chunk(int k, bool stream, F&& f) {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;   // of kThreads: work-items of a launch fit 32 bits
 constexpr int kMaxK = 64;
+constexpr int64_t kCUs = 256;
+constexpr int64_t kShortRow = 1024;                      // elements, two segments; one past the L2s
 static_assert(kMaxBlocks * kThreads <= 0xFFFFFFFFll, "work-items of a launch");
 
 // Checks shared by the operators that use a sorted plan.  rows_used: tensors indexed by
@@ -989,7 +1002,15 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
   }
   const bool v = (T == 0 || vec8(dO, ldo, H)) && (rows == 0 || vec8(dY, lddy, H)) &&
                  (!dW || rows == 0 || vec8(Y, ldy, H));
-  const int64_t pads = ceil_div(rows, kPadRows), blocks = pads + (k > 0 ? T : 0);
+  const int64_t pads = ceil_div(rows, kPadRows);
+  const bool big = 2 * T * k * H >= kStreamBytes;
+  int64_t kc = v && k < kChunk ? k : kChunk, tasks = k > 0 ? T * ceil_div(k, kc) : 0;
+  if (v && tasks > 0 && tasks < kCUs) {
+    kc = ceil_div(kc, ceil_div(kCUs, tasks));
+    tasks = T * ceil_div(k, kc);
+  }
+  const bool waves = v && H <= (big ? kShortRow / 2 : kShortRow) && tasks >= kCUs;
+  const int64_t blocks = pads + (waves ? ceil_div(tasks, kWaves) : tasks);
   if (blocks == 0) return BSG_OK;
   if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
@@ -999,10 +1020,12 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
                        (uint16_t*)dY, lddy, dW, lddw);
   };
   if (v)
-    with_chunk(k, 2 * T * k * H >= kStreamBytes,
-               [&](auto kc, auto aux) { go(combine_backward_kernel<8, kc.value, aux.value>); });
+    with_chunk((int)kc, big, [&](auto c, auto aux) {
+      if (waves) go(combine_backward_kernel<8, c.value, aux.value, 1>);
+      else go(combine_backward_kernel<8, c.value, aux.value, kWaves>);
+    });
   else
-    go(combine_backward_kernel<1, kChunk, 0>);
+    go(combine_backward_kernel<1, kChunk, 0, kWaves>);
   return launch_status();
 }
 

@@ -472,7 +472,7 @@ int moe_combine(const void* Y, int64_t ldy, const int32_t* row_of, const float* 
  *   dW[t][j] = sum_h dO[t][h] * Y[row_of[t*k + j]][h]  (fp32; 0 for a pair without a
  *              row), in an order that is the same on every run.
  *   dW may be NULL (then Y is not read and may be NULL); W NULL means weights of one.
- *   T + rows / 16 < 2^24.
+ *   T * ceil(k / 8) + rows / 16 < 2^24.
  *   dY must not overlap dO or Y.  Alignment as moe_dispatch_bf16. */
 int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy, const int32_t* row_of,
                          const int32_t* pair_of, const float* W, int64_t ldw, int64_t T, int32_t k,

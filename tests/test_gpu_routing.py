@@ -486,3 +486,30 @@ def test_wrong_arguments_raise_on_the_gpu():
             (lambda: bsg.moe_combine_backward(dO, short, plan, W), ValueError)):
         with pytest.raises(error):
             f()
+
+
+# choices shared out to several workgroups, and a wave a token: few and many tokens, short
+# rows, more than eight choices, tokens without rows, unweighted, without the weights' gradient
+@pytest.mark.parametrize("T,k,G,H", [(1, 8, 64, 7168), (2, 3, 5, 2048), (7, 7, 9, 1024), (40, 20, 30, 520), (100, 64, 70, 256),
+                                     (255, 2, 8, 512), (256, 5, 8, 1024), (700, 9, 12, 136), (3000, 6, 20, 512),
+                                     (1200, 1, 4, 8), (9000, 4, 40, 512), (5000, 8, 30, 1024)])
+def test_combine_backward_shared_out(T, k, G, H):
+    _say(f"moe_combine_backward T={T} k={k} G={G} H={H}")
+    plan, _, Y, W, dO, rows = _case(T, k, G, 16, H, T + k)
+    row_of, pair_of = _np(plan.row_of), _np(plan.pair_of)
+    for w in (W, None):
+        out = torch.full((rows, H), 3.0, dtype=torch.bfloat16, device=DEV)
+        dY, dW = bsg.moe_combine_backward(dO, Y, plan, w, out=out)
+        again, none = bsg.moe_combine_backward(dO, None, plan, w, need_weights=False, out=torch.full_like(out, 3.0))
+        assert none is None and torch.equal(again, dY)
+        have = torch.from_numpy(row_of >= 0).to(DEV)
+        t, j = torch.nonzero(have, as_tuple=True)
+        r = plan.row_of[t, j].long()
+        f = 1.0 if w is None else w[t, j][:, None]
+        assert torch.equal(dY[r], (f * dO[t].float()).to(torch.bfloat16))     # one product, rounded once
+        assert torch.all(dY[plan.pair_of == -1] == 0) and torch.all(dY[plan.pair_of == -2] == 3.0)
+        prod = dO[t].double() * Y[r].double()
+        want, mag = torch.zeros(T, k, dtype=torch.float64, device=DEV), torch.zeros(T, k, dtype=torch.float64, device=DEV)
+        want[t, j], mag[t, j] = prod.sum(1), prod.abs().sum(1)
+        assert torch.all((dW.double() - want).abs() <= H * U24 * mag)
+        assert torch.all(dW[~have] == 0)
