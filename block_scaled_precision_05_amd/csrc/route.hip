@@ -1010,9 +1010,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
     tasks = T * ceil_div(k, kc);
   }
   const bool waves = v && H <= (big ? kShortRow / 2 : kShortRow) && tasks >= kCUs;
+  if (pads + tasks == 0) return BSG_OK;
+  if (pads + tasks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   const int64_t blocks = pads + (waves ? ceil_div(tasks, kWaves) : tasks);
-  if (blocks == 0) return BSG_OK;
-  if (blocks > kMaxBlocks) return BSG_ERR_UNSUPPORTED_SHAPE;
   (void)hipGetLastError();
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, (hipStream_t)stream, (const uint16_t*)dO,
