@@ -15,8 +15,8 @@
 //     from global memory to MFMA fragments.  64 tokens of 32 adapters, rank 16, 7168 to
 //     2048 wide: 4.4 + 4.7 us; 1 token, rank 8: 3.4 + 5.2.
 //   Many tokens: shrink_many_kernel, where U is large join_kernel, expand_many_kernel; 64
-//     tokens share an adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64, 7168 to 4096
-//     wide: 31 + 5 + 24 us, where the 263 MB take 54 us at the rate of a copy.
+//     tokens share an adapter's rows through LDS.  8192 tokens of 16 adapters, rank 64,
+//     7168 to 4096 wide: 31 + 5 + 24 us; the 263 MB take 54 us at the rate of a copy.
 // A token without an adapter is copied by the first launch's last workgroups.
 //
 // U = s_g A_g x is summed in fp32 and keeps that precision through the second product:
@@ -239,7 +239,8 @@ struct URows {
 // base are in flight while this one is formed, the first block's while form_u puts U into
 // LDS.  out is stored with the non-temporal hint: it is not read here, and left in L2 it
 // would evict the adapters.  base and out may start at any element (8192 tokens, rank 64,
-// 7168 to 4097 wide: 95 us, by single elements 149; 4096 wide 73).
+// 7168 to 4097 wide, with the products as they then were: 95 us, by single elements 149;
+// 4096 wide 73; now 84 and 62).
 // ---------------------------------------------------------------------------
 // Four columns (quad) of a row sit at quad ^ row, so that 16 rows' writes of one quad, and
 // two rows' reads of eight, cover the banks once.
@@ -373,8 +374,8 @@ __device__ __forceinline__ void copy_tokens(const First& a, int block, int waves
 // Few tokens: two launches.  What one CU can keep in flight bounds a workgroup to some 25
 // bytes per ns (one launch in which a workgroup took its tile from X to out: one token of
 // rank 8, 7168 to 2048 wide, 10 us against 4 + 4), so each tile's slices of K and parts of
-// the rank, and then its blocks of columns, go to workgroups of their own.  The S slices' sums lie in slabs
-// of U that every workgroup of the second launch adds in order.
+// the rank, and then its blocks of columns, go to workgroups of their own.  The S slices'
+// sums lie in slabs of U that every workgroup of the second launch adds in order.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWaves = 4;
 
@@ -420,7 +421,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void shrink_kernel(const First a)
 // a CU keeps in flight; here the stages of X and A_g are copied to LDS by whole lines,
 // NS - 1 stages ahead, and each wave reads its 16 tokens' and A_g's fragments from there.
 // 16-byte chunk c of row r sits at chunk c ^ (r * row bytes / 256 % chunks), so that 16
-// rows' reads of one chunk cover the banks once.
+// rows' reads of one chunk cover the banks once.  8192 tokens, rank 64, 7168 wide: 31 us,
+// 4.7 TB/s of X and U, and as much of the adapters from L2.
 //
 // Items: NT tiles of one adapter.  (Groups of NT tiles that ignore where an adapter ends
 // need a pass per adapter in a group, and where everything runs at once the launch lasts
@@ -757,7 +759,8 @@ __global__ __launch_bounds__(256) void join_kernel(const Join a) {
 // of 64 columns, whose rows of B_g it copies to LDS once for its waves.  Everything a
 // wave reads from memory (base, U, its share of B_g) is asked for at once; workgroups side
 // by side on a CU cover the wait.  Chunk c of B_g row n sits at chunk c ^ (n * row bytes /
-// 256 % chunks), as in the first product's ring.
+// 256 % chunks), as in the first product's ring.  8192 tokens, rank 64, 4096 wide: 24 us,
+// 5.7 TB/s of base, out and U.
 template <int RF, int CB, bool JOINED>
 __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_eu(RF == 8 ? 2 : 3))) void expand_many_kernel(
     const SecondMany a) {
@@ -907,8 +910,8 @@ static int slices(bool many, int64_t tiles, int64_t K) {
 
 // Whether the second product for many tokens adds U's slabs itself, once per 256 columns,
 // or takes them joined by a launch of their own: itself while those reads are few and the
-// slabs, which it takes one after the other past the third, few and narrow (tokens, adapters, K, N,
-// rank: reads x slices, us joined / itself: 8192, 16, 7168, 4096, 16: 27 MB x 2, 50.5 / 47;
+// slabs, which it takes one after the other past the third, few and narrow (tokens,
+// adapters, K, N, rank: reads x slices, us joined / itself: 8192, 16, 7168, 4096, 16: 27 MB x 2, 50.5 / 47;
 // 8192, 8, 4096, 4096, 32: 51 x 2, 43 / 40;  3000, 8, 4096, 2048, 32: 22 x 6, 19.4 / 18.1;
 // 4096, 4, 2048, 2048, 64: 43 x 4, 22.7 / 23.2;  8192, 16, 7168, 4096, 64: 103 x 2, 62 /
 // 63.5;  1024, 8, 4096, 4096, 64: 42 x 8, 18 / 21;  1000, 8, 4000, 128, 128: 5 x 8, 23 /
