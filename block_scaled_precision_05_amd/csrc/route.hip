@@ -58,6 +58,8 @@ constexpr int kMaxSteps = 4;
 constexpr int kSingle = kMaxSteps * kSortThreads;   // most pairs a workgroup sorts alone
 constexpr int kMaxChunks = 256;                     // workgroups of the two-launch form
 constexpr int64_t kMaxPairs = int64_t(1) << 23;      // a chunk's counts fit 16 bits
+// Rows are stepped through in 32 bits by at most kMaxChunks workgroups: the step past the last must fit.
+constexpr int64_t kMaxSortRows = (int64_t(1) << 31) - kMaxChunks * kSortThreads;
 constexpr int kSharePairs = 64, kFillRows = 2048;   // pairs and rows that a workgroup of the one-launch form writes
 static_assert(kMaxGroups == kSortThreads && kMaxPairs / kMaxChunks < 65536, "one thread a group, 16-bit counts");
 
@@ -789,8 +791,8 @@ constexpr int64_t kCUs = 256;
 constexpr int64_t kShortRow = 1024;                      // elements, two segments; one past the L2s
 static_assert(kMaxBlocks * kThreads <= 0xFFFFFFFFll, "work-items of a launch");
 
-// Checks shared by the operators that use a sorted plan.  rows_used: tensors indexed by
-// row are touched.
+// Checks shared by the operators that use a sorted plan.  need_pairs: pair_of is read or
+// written.
 static int plan_check(const int32_t* row_of, const int32_t* pair_of, bool need_pairs, int64_t T,
                       int32_t k, int64_t rows, int64_t H) {
   if (T < 0 || k < 0 || rows < 0 || H < 0) return BSG_ERR_INVALID_ARG;
@@ -846,7 +848,7 @@ int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_
   const int64_t need = cap > 0 ? (int64_t)G * cap
                                : (G > 0 ? n + (G < n ? G : n) * (int64_t)(align - 1) : 0);
   if (rows < need) return BSG_ERR_INVALID_ARG;
-  if (need > kMaxDim - kSortThreads) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (rows > kMaxSortRows) return BSG_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < sort_tokens_workspace(n, G) || (sort_tokens_workspace(n, G) > 0 && !workspace))
     return BSG_ERR_INVALID_ARG;
   SortArgs a = {};

@@ -415,7 +415,7 @@ int moe_ffn_fp8_noalloc(const void* A, int64_t lda, const int16_t* sfa, int64_t 
  *   workspace: sort_tokens_workspace(T*k, G) bytes, 4-byte aligned (may be NULL when
  *   that is 0); its contents need no initial value.  Calls that overlap need a
  *   workspace each.
- *   Requires G <= 1024, k <= 64, T*k <= 2^23 and rows below 2^31 - 1024. */
+ *   Requires G <= 1024, k <= 64, T*k <= 2^23 and rows <= 2^31 - 2^18. */
 int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_t G, int32_t align,
                 int32_t cap, int32_t* offsets, int32_t* row_of, int32_t* pair_of, int32_t* row_group,
                 int64_t rows, void* workspace, int64_t workspace_bytes, void* stream);

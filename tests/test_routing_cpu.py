@@ -170,3 +170,20 @@ def test_binding_refuses_host_tensors():
         bsg.moe_combine_backward(X, X, _plan())
     with pytest.raises(ValueError):
         bsg.lora_add_bf16(X, X[None], X[None], _plan(k=1))
+
+
+def test_sort_refuses_rows_that_a_grid_could_step_past():
+    """Rows are walked in 32 bits by up to 2^18 work-items: the step past the last row must
+    not wrap, so plans of more than 2^31 - 2^18 rows are refused.  (A workspace that is
+    missing is refused after the sizes, so that nothing here launches.)"""
+    L = bsg.lib()
+    most = 2 ** 31 - 2 ** 18
+    for T, k, align, cap in ((1, 1, 1, 0), (10000, 4, 16, 0), (10000, 4, 1, 5)):
+        #       ids ld T  k  G  al     cap  off row pair grp rows ws bytes stream
+        args = [P, k, T, k, 8, align, cap, P2, P3, P4, P5, most, 0, 0, None]
+        for rows in (most + 1, 2 ** 31 - 1025, 2 ** 31 - 1, 2 ** 31):
+            args[11] = rows
+            assert L.sort_tokens(*args) == SHAPE, (T, rows)
+        if T > 1:
+            args[11] = most
+            assert L.sort_tokens(*args) == INV
