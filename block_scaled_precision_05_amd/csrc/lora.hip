@@ -863,6 +863,11 @@ constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // (256 a workgroup) fit
 constexpr int64_t kMaxK = int64_t(1) << 22;             // 128-element units of K fit 16 bits
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Most items of kItemTiles tiles, each of one adapter, among the plan's tiles.
+static int64_t most_items(int64_t tiles, int64_t G) {
+  return ceil_div(tiles, kItemTiles) + (G < tiles ? G : tiles);
+}
+
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
 // read a whole adapter from L2, T r (K + N) / 8 bytes; grouped, 64 tokens share it, for
 // one more launch or two and workgroups that do more each.  T, K, N, r, in M of T r (K + N), us
@@ -871,8 +876,11 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   600, 2000, 2000, 96:  230, 12 / 19;        4000, 4000, 512, 16:  289, 16 / 16;
 //   512, 4096, 4096, 64:  268, 14 / 15;        8192, 4096, 256, 8:   285, 24 / 18;
 //   2048, 4096, 4096, 32: 537, 22 / 20;        8192, 1024, 128, 64:  604, 21 / 15.
-static bool many_tokens(int64_t T, int64_t N, int64_t K, int64_t r) {
-  return T * r * (K + N) >= int64_t(270) << 20;
+// (Stages of the items, of kStage elements of K, are counted in 32 bits: a plan that can have
+// more than 2^30, most of it padding, is taken tile by tile.)
+static bool many_tokens(int64_t T, int64_t rows, int64_t G, int64_t N, int64_t K, int64_t r) {
+  return T * r * (K + N) >= int64_t(270) << 20 &&
+         most_items(ceil_div(rows, kTile), G) * ceil_div(K, kStage) <= int64_t(1) << 30;
 }
 
 // Rank fragments of a workgroup of the first product for few tokens: the whole rank, or
@@ -890,13 +898,6 @@ static int rank_fragments(int64_t tiles, int64_t S, int64_t r) {
 
 // The rank up to which the kernels' fragments reach.
 static int64_t padded_rank(int64_t r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
-
-// Most items of kItemTiles tiles, each of one adapter, among the plan's tiles (at most 2^30
-// stages in all: more than an X that fits the memory has).
-static int64_t most_items(int64_t tiles, int64_t G, int64_t K) {
-  const int64_t n = ceil_div(tiles, kItemTiles) + (G < tiles ? G : tiles), most = (int64_t(1) << 30) / ceil_div(K, kStage);
-  return n < most ? n : most;
-}
 
 // Slices of K, workgroups for the whole chip: with few tokens at least 1024 elements (two
 // units a wave), as every workgroup of the second launch adds the slabs; with many at
@@ -946,7 +947,7 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
   if (a.items > 0 && c.many) {
     constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // (twice as many: no faster)
     constexpr int CB = 4, ranks = 32 * URows<RF>::RK;      // columns: 256 a workgroup
-    const int cap = (int)most_items(tiles, a.G, a.K);
+    const int cap = (int)most_items(tiles, a.G);
     a.items = (int)(cap * (int64_t)a.S < kFirstWorkgroups ? cap * a.S : kFirstWorkgroups);
     hipLaunchKernelGGL((shrink_many_kernel<RF, kItemTiles, kStage, NS>), dim3((unsigned)(a.items + copy_blocks)),
                        dim3(64 * kItemTiles), 0, st, (FirstMany{a, c.offsets, cap}));
@@ -1002,7 +1003,7 @@ extern "C" {
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r) {
   if (T <= 0 || rows <= 0 || G <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
   const int64_t tiles = ceil_div(rows, kTile);
-  const bool many = many_tokens(T, N, K, r);
+  const bool many = many_tokens(T, rows, G, N, K, r);
   const int64_t joined = many ? 4 * tiles * kTile * padded_rank(r) : 0;
   return 4 * ((int64_t)slices(many, tiles, K) + many) * tiles * kTile * r + joined;
 }
@@ -1054,7 +1055,7 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   rw.items = adapt;      // (until the launch is laid out: whether there are any)
   rw.G = (uint16_t)G;
   rw.r = (uint16_t)r;
-  const bool many = many_tokens(T, N, K, r);
+  const bool many = many_tokens(T, rows, G, N, K, r);
   const int S = adapt ? slices(many, ceil_div(rows, kTile), K) : 1;
   rw.S = (uint16_t)S;
   (Rows&)c.first = rw;

@@ -440,3 +440,29 @@ def test_lora_grouped_tiles_captured():
         torch.cuda.synchronize()
         got = captured.clone()
         assert torch.equal(got, step())
+
+
+def test_lora_plan_of_more_padding_than_grouped_tiles_can_count():
+    """Adapters padded to 2^20 rows, K = 2^22: more stages of grouped tiles than 32 bits count.
+    X is sparse and everything integer, so that the sums are exact: fp64, rounded once."""
+    T, G, K, N, r, align = 16, 2, 1 << 22, 8, 8, (1 << 20) - 16
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r} align={align}")
+    g = torch.Generator(device=DEV).manual_seed(2)
+    ids = torch.arange(T, dtype=torch.int32, device=DEV)[:, None] % G
+    rows = T + G * (align - 1)
+    plan = bsg.sort_tokens(ids, G, align=align)
+    assert plan.pair_of.numel() == rows
+    cols = torch.randint(0, K, (100,), generator=g, device=DEV)
+
+    def ints(*shape, top):
+        return torch.randint(-top, top + 1, shape, generator=g, device=DEV).to(torch.bfloat16)
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
+    X[:, cols] = ints(T, 100, top=1)
+    A, B, base = ints(G, r, K, top=2), ints(G, N, r, top=2), ints(T, N, top=9)
+    out = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    bsg.lora_add_bf16(X, A, B, plan, base=base, out=out)
+    cols = cols.unique()
+    for t in range(T):
+        u = A[t % G][:, cols].double() @ X[t, cols].double()
+        want = base[t].double() + B[t % G].double() @ u
+        assert torch.equal(out[t], want.to(torch.bfloat16)), t

@@ -187,3 +187,22 @@ def test_sort_refuses_rows_that_a_grid_could_step_past():
         if T > 1:
             args[11] = most
             assert L.sort_tokens(*args) == INV
+
+
+def _tiles_apart(T, rows, G, N, K, r):
+    """Whether lora_add_bf16 takes the plan's tiles one by one: its workspace is then S slabs
+    of fp32 sums, a slice of at least 1024 elements of K each, and nothing behind them."""
+    tiles = -(-rows // 16)
+    S = max(1, min(512 // tiles, -(-K // 1024)))
+    return bsg.lib().lora_add_workspace(T, rows, G, N, K, r) == 4 * S * tiles * 16 * r
+
+
+def test_lora_groups_no_more_tiles_than_it_can_count():
+    """Grouped tiles are taken by stages of K that are counted in 32 bits.  A plan that is
+    mostly padding can have more than 2^30 of them: its tiles are not grouped, whatever the
+    number of its tokens."""
+    K = 1 << 22                               # 65536 stages an item of four tiles
+    rows = 64 * ((1 << 14) - 2)
+    assert not _tiles_apart(16, rows, 2, 8, K, 8)           # 2^14 items
+    assert _tiles_apart(16, rows + 64, 2, 8, K, 8)          # one more
+    assert _tiles_apart(1 << 20, 1 << 26, 1024, 1024, 1 << 20, 128)
