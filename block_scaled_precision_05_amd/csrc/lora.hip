@@ -860,6 +860,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) __attribute__((amdgpu_waves_per_e
 
 constexpr int64_t kMaxRows = int64_t(1) << 26;          // with kMaxBlocks: work-items of a launch
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // (256 a workgroup) fit 32 bits
+constexpr int kColBlocks = 4;                           // 64-column blocks a workgroup, many tokens
 constexpr int64_t kMaxK = int64_t(1) << 22;             // 128-element units of K fit 16 bits
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -946,7 +947,7 @@ static void launch(const Call& c, int copy_blocks, hipStream_t st) {
   const dim3 threads(64 * kSplitWaves);
   if (a.items > 0 && c.many) {
     constexpr int NS = RF == 1 ? 6 : (RF == 8 ? 3 : 4);       // (twice as many: no faster)
-    constexpr int CB = 4, ranks = 32 * URows<RF>::RK;      // columns: 256 a workgroup
+    constexpr int CB = kColBlocks, ranks = 32 * URows<RF>::RK;
     const int cap = (int)most_items(tiles, a.G);
     a.items = (int)(cap * (int64_t)a.S < kFirstWorkgroups ? cap * a.S : kFirstWorkgroups);
     hipLaunchKernelGGL((shrink_many_kernel<RF, kItemTiles, kStage, NS>), dim3((unsigned)(a.items + copy_blocks)),
@@ -1015,15 +1016,16 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
                   int32_t r, void* workspace, int64_t workspace_bytes, void* stream) {
   if (T < 0 || G < 0 || N < 0 || K < 0 || r < 0 || rows < 0) return BSG_ERR_INVALID_ARG;
   if (r > 128 || r % 8 || K % 8) return BSG_ERR_UNSUPPORTED_SHAPE;
-  if (T > kMaxRows || rows > kMaxRows || N > (int64_t(1) << 23) || K > kMaxK || G > 1024 ||
-      (ceil_div(rows, kItemTiles * kTile) + G) * ceil_div(N, 256) > kMaxBlocks)
-    return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (T > kMaxRows || rows > kMaxRows || N > (int64_t(1) << 23) || K > kMaxK || G > 1024) return BSG_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || N == 0) return BSG_OK;
   if (!out || ldo < N || !row_of || (base && ld_base < N)) return BSG_ERR_INVALID_ARG;
   if (((uintptr_t)out | (uintptr_t)base) & 1) return BSG_ERR_MISALIGNED;
   // in place only onto the same elements
   if (base == out && ld_base != ldo) return BSG_ERR_INVALID_ARG;
-  const bool adapt = rows > 0 && G > 0 && K > 0 && r > 0;
+  const bool adapt = rows > 0 && G > 0 && K > 0 && r > 0, many = many_tokens(T, rows, G, N, K, r);
+  // (tile by tile a launch has some 1024 workgroups, or one a tile, and one per 16 tokens)
+  if (adapt && many && most_items(ceil_div(rows, kTile), G) * ceil_div(N, 64 * kColBlocks) > kMaxBlocks)
+    return BSG_ERR_UNSUPPORTED_SHAPE;
   if (((uintptr_t)offsets | (uintptr_t)row_of | (uintptr_t)pair_of | (uintptr_t)row_group | (uintptr_t)scale) & 3)
     return BSG_ERR_MISALIGNED;
   if (rows > 0 && (!pair_of || !row_group || !offsets)) return BSG_ERR_INVALID_ARG;
@@ -1055,7 +1057,6 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
   rw.items = adapt;      // (until the launch is laid out: whether there are any)
   rw.G = (uint16_t)G;
   rw.r = (uint16_t)r;
-  const bool many = many_tokens(T, rows, G, N, K, r);
   const int S = adapt ? slices(many, ceil_div(rows, kTile), K) : 1;
   rw.S = (uint16_t)S;
   (Rows&)c.first = rw;

@@ -497,8 +497,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   workspace: lora_add_workspace(T, rows, G, N, K, r) bytes, 16-byte aligned, no initial value
  *   needed; calls that overlap need one each.
  *   Requires r % 8 == 0, r <= 128, K % 8 == 0, K <= 2^22, G <= 1024, T and rows <= 2^26,
- *   N <= 2^23, rows * N below 2^37, ld_base and ldo below 2^31, the other leading
- *   dimensions and strides below 2^34; X, A, B 16-byte aligned with leading dimensions and strides
+ *   N <= 2^23, ld_base and ldo below 2^31, the other leading dimensions and strides below
+ *   2^34, and for T r (K + N) >= 270 * 2^20 (tiles of 16 rows are then taken four together)
+ *   (ceil(rows/64) + min(G, ceil(rows/16))) * ceil(N/256) < 2^24; X, A, B 16-byte aligned with leading dimensions and strides
  *   multiples of 8; any N, base and out 2-byte aligned (fastest where their rows start
  *   at multiples of 128 bytes). */
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,

@@ -466,3 +466,13 @@ def test_lora_plan_of_more_padding_than_grouped_tiles_can_count():
         u = A[t % G][:, cols].double() @ X[t, cols].double()
         want = base[t].double() + B[t % G].double() @ u
         assert torch.equal(out[t], want.to(torch.bfloat16)), t
+
+
+def test_lora_tile_by_tile_with_the_most_spare_rows():
+    """One token, a plan of 2^26 rows, 4096 columns: more than grouped tiles could launch."""
+    T, G, K, N, r, rows = 1, 1, 64, 4096, 8, 1 << 26
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r} rows={rows}")
+    ids, _, X, A, B, scale, base = _case(T, G, K, N, r, 5, missing=0.0)
+    e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+    plan = bsg.sort_tokens(ids, G, align=16, out=bsg.TokenSort(e(G + 1), e(T, 1), e(rows), e(rows)))
+    _check(bsg.lora_add_bf16(X, A, B, plan, scale, base), X, A, B, ids, scale, base, "spare rows")

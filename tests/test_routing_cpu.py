@@ -206,3 +206,24 @@ def test_lora_groups_no_more_tiles_than_it_can_count():
     assert not _tiles_apart(16, rows, 2, 8, K, 8)           # 2^14 items
     assert _tiles_apart(16, rows + 64, 2, 8, K, 8)          # one more
     assert _tiles_apart(1 << 20, 1 << 26, 1024, 1024, 1 << 20, 128)
+
+
+def test_lora_limits_follow_the_form():
+    """The limit of a launch's workgroups is that of grouped tiles: a call that takes its
+    tiles one by one is not refused for it.  (The missing workspace is refused after the
+    sizes, so that nothing here launches.)"""
+    L = bsg.lib()
+
+    def status(T, rows, G, N, K, r):
+        #                      X  ldx A  lda sa     B  ldb sb     sc off row pair grp rows  base ldb out ldo
+        return L.lora_add_bf16(P, K, P, K, r * K, P, r, N * r, 0, P2, P2, P3, P4, rows, P5, N, 0x90000, N,
+                               T, G, N, K, r, 0, 0, None)
+    for T, rows, G, N, K, r in ((1, 16, 1024, 1 << 22, 8, 8),       # many adapters, a wide output
+                                (1, 16, 1024, 1 << 23, 8, 8),
+                                (1, 1 << 26, 1, 4096, 8, 8),        # many spare rows
+                                (4, 64, 1024, 1 << 23, 8, 8),       # the widest
+                                (5, 80, 1024, 1 << 23, 8, 8)):      # grouped: 2 + 5 items of 2^15 blocks
+        assert status(T, rows, G, N, K, r) == INV, (T, rows, G, N)
+    # grouped: 4096 items and one more per adapter, 4096 blocks of 256 columns
+    assert status(1 << 16, 1 << 18, 4, 1 << 20, 64, 8) == SHAPE      # 4100 * 4096
+    assert status(1 << 16, (1 << 18) - 320, 4, 1 << 20, 64, 8) == INV  # 4095 * 4096
