@@ -483,8 +483,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   out[t] = bf16( base[t] + scale[g] * B_g (A_g x_t) ),  g = the adapter of token t,
  *   out[t] = base[t] for a token without an adapter (row_of[t] < 0).
  * A_g x_t is summed in fp32 and enters the second product as two bf16 terms, with a
- * relative error of at most 2^-16; the result is rounded once.  (A zero second term
- * against an infinite element of B_g gives NaN where the product would be infinite.)
+ * relative error of at most 2^-16; the result is rounded once.  (Against an infinite
+ * element of B_g a second term that is zero, or of the other sign than the first, gives
+ * NaN where the product would be infinite.)
  *   X: bf16 [T][ldx], K wide; A: bf16 [G][r][lda >= K], B: bf16 [G][N][ldb >= r] (expert
  *   strides in elements; adapters of lower rank are padded with zero rows of A and
  *   columns of B); scale: fp32 [G], or NULL for one.
