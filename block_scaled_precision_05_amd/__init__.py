@@ -162,8 +162,6 @@ def _mat(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    if t.numel() == 0:      # an empty tensor's strides mean nothing
-        return t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -662,6 +660,8 @@ def _ld(t, name, dtype, rows, cols):
     ld, step = t.stride()
     if step == 1 and ld >= cols:
         return ld
+    if t.numel() == 0:      # an empty tensor's strides mean nothing
+        return cols
     return _mat(t, name)
 
 

@@ -227,3 +227,14 @@ def test_lora_limits_follow_the_form():
     # grouped: 4096 items and one more per adapter, 4096 blocks of 256 columns
     assert status(1 << 16, 1 << 18, 4, 1 << 20, 64, 8) == SHAPE      # 4100 * 4096
     assert status(1 << 16, (1 << 18) - 320, 4, 1 << 20, 64, 8) == INV  # 4095 * 4096
+
+
+def test_empty_operands():
+    """The matrix operands of the products keep their check of the strides when they are
+    empty; the operators on grouped rows take empty operands of any stride."""
+    odd = torch.zeros(8, 16, dtype=torch.bfloat16)[:0, ::2]       # [0, 8], every second column
+    with pytest.raises(ValueError, match="unit stride"):
+        bsg._mat(odd, "A")
+    assert bsg._mat(torch.zeros(8, 16)[:0, :8], "A") == 16
+    assert bsg._ld(odd, "X", torch.bfloat16, 0, 8) == 8
+    assert bsg._ld(torch.zeros(0, 5, dtype=torch.bfloat16).t(), "X", torch.bfloat16, 5, 0) == 0
