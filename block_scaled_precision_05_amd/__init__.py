@@ -38,6 +38,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsg.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 BSG_OK = 0
 BSG_ERR_INVALID_ARG = 1
@@ -613,6 +614,10 @@ def _native():
     loaded libbsg.so."""
     global _native_module
     if _native_module is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it with "
+                "`python -m block_scaled_precision_05_amd.build`")
         from . import _binding
         with _native_lock:
             _binding.init(TokenSort, {n: ctypes.cast(getattr(lib(), n), _vp).value

@@ -12,12 +12,13 @@ if HERE not in sys.path:
 
 
 def _ensure_built():
-    """Build the oracle and the GPU library once if they are missing (a fresh
-    checkout); an existing build is used as it is."""
+    """Build the oracle and the GPU library (with its binding) once if they are missing (a
+    fresh checkout); an existing build is used as it is."""
     import oracle
     if not os.path.exists(os.path.join(ROOT, "oracle", "liboracle.so")):
         oracle.build(force=False)
-    if not os.path.exists(os.path.join(ROOT, "block_scaled_precision_05_amd", "libbsg.so")):
+    if not all(os.path.exists(os.path.join(ROOT, "block_scaled_precision_05_amd", f))
+               for f in ("libbsg.so", "_binding.so")):
         from block_scaled_precision_05_amd import build
         build.build(force=False)
 

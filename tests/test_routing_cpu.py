@@ -238,3 +238,14 @@ def test_empty_operands():
     assert bsg._mat(torch.zeros(8, 16)[:0, :8], "A") == 16
     assert bsg._ld(odd, "X", torch.bfloat16, 0, 8) == 8
     assert bsg._ld(torch.zeros(0, 5, dtype=torch.bfloat16).t(), "X", torch.bfloat16, 5, 0) == 0
+
+
+def test_a_missing_binding_is_named(monkeypatch, tmp_path):
+    """Without _binding.so (a library built before there was one) the operators that use it
+    raise as every call does without libbsg.so: naming the file and the build command."""
+    monkeypatch.setattr(bsg, "BINDING_PATH", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(bsg, "_native_module", None)
+    for f in (lambda: bsg.sort_tokens(torch.zeros(4, 2, dtype=torch.int32), 2),
+              lambda: bsg.moe_combine(torch.zeros(8, 128, dtype=torch.bfloat16), _plan())):
+        with pytest.raises(RuntimeError, match="_binding.so is missing: build it with"):
+            f()
