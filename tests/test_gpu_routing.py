@@ -513,3 +513,133 @@ def test_combine_backward_shared_out(T, k, G, H):
         want[t, j], mag[t, j] = prod.sum(1), prod.abs().sum(1)
         assert torch.all((dW.double() - want).abs() <= H * U24 * mag)
         assert torch.all(dW[~have] == 0)
+
+
+# ---------------------------------------------------------------------------
+# Matrices past 32 MiB: copies with the non-temporal hint, and in the quantising dispatch
+# another order of the workgroups.  Widths whose last segment is partial (and an odd number
+# of scale blocks), numbers of workgroups that are no multiple of 8, padding and spare rows,
+# tokens without rows; k up to, at and past eight.
+# ---------------------------------------------------------------------------
+STREAM = 32 << 20
+
+
+def _stream_case(T, k, G, align, H, cap=0):
+    """_case with every 17th token without a row."""
+    ids = _ids(T, k, G, T + k)
+    ids[::17] = -1
+    rows = routing.rows_needed(T, k, G, align, cap) + 5
+    plan = bsg.TokenSort(*(torch.from_numpy(x).to(DEV)
+                           for x in routing.sort_tokens(ids, G, align, cap, rows)))
+    g = torch.Generator(device=DEV).manual_seed(T)
+    mat = lambda n, h: torch.randn(n, h, generator=g, device=DEV).to(torch.bfloat16)
+    return plan, mat, rows, torch.randn(T, k, generator=g, device=DEV)
+
+
+@pytest.mark.parametrize("T,k", [(8170, 1), (4099, 2), (2731, 3), (2049, 4), (1640, 5), (1367, 6), (1171, 7),
+                                 (1025, 8), (750, 11), (130, 64)])
+def test_streamed_dispatch_bf16_and_combine(T, k):
+    H, G, align = 2056, 30, 16
+    assert 2 * T * k * H >= STREAM
+    _say(f"past 32 MiB: moe_dispatch_bf16, moe_combine T={T} k={k} H={H}")
+    plan, mat, rows, W = _stream_case(T, k, G, align, H)
+    pair = plan.pair_of.long()
+    holds, pad = pair >= 0, pair == -1
+    X = mat(T, H)
+    buf = torch.full((rows, H + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+    bsg.moe_dispatch_bf16(X, plan, out=buf[:, :H])
+    want = torch.full_like(buf, 3.0)
+    want[pad, :H] = 0
+    want[holds, :H] = X[pair[holds] // k]
+    assert torch.equal(buf, want)
+
+    Y = mat(rows, H)
+    Y[~holds] = float("nan")                     # rows without a pair: not read
+    have = plan.row_of >= 0
+    W[~have] = float("nan")                      # weights of pairs without a row: not used
+    for w in (W, None):
+        buf = torch.full((T, H + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+        out = bsg.moe_combine(Y, plan, w, out=buf[:, :H])
+        sum_, mag = (torch.zeros(T, H, dtype=torch.float64, device=DEV) for _ in range(2))
+        for j in range(k):
+            m = have[:, j]
+            v = Y[plan.row_of[m, j].long()].double() * (1.0 if w is None else w[m, j, None].double())
+            sum_[m] += v
+            mag[m] += v.abs()
+        assert torch.all((out.double() - sum_).abs() <= U8 * sum_.abs() + (1 + U8) * k * U24 * mag)
+        assert torch.all(buf[:, H:] == 3.0)
+
+
+@pytest.mark.parametrize("rule", ["ceil", "ocp_mx"])
+@pytest.mark.parametrize("fmt,T,k,G,align,H,cap", [
+    ("fp8", 29131, 1, 12, 16, 1152, 0), ("fp8", 4863, 6, 40, 16, 1152, 0), ("fp8", 3240, 9, 40, 1, 1152, 0),
+    ("fp8", 4863, 6, 40, 1, 1152, 700), ("fp8", 670, 7, 9, 128, 7168, 0),
+    ("fp4", 9987, 6, 40, 16, 1120, 0), ("fp4", 3525, 17, 30, 7, 1120, 0), ("fp4", 2710, 6, 20, 1, 4128, 800)])
+def test_streamed_dispatch_quantised(fmt, T, k, G, align, H, cap, rule):
+    per, gk = (1, 128) if fmt == "fp8" else (2, 32)
+    assert T * k * H // per >= STREAM
+    _say(f"past 32 MiB: moe_dispatch_{fmt} T={T} k={k} G={G} align={align} H={H} cap={cap} {rule}")
+    plan, _, rows, _ = _stream_case(T, k, G, align, H, cap)
+    X = workloads.activations(T, H, seed=T + H, device=DEV)
+    X[1] = 0.0
+    X[2] = (X[2].float() * 2.0 ** -120).to(torch.bfloat16)
+    quant = bsg.quantize_fp8_per_token if fmt == "fp8" else bsg.quantize_fp4_per_token
+    disp = bsg.moe_dispatch_fp8 if fmt == "fp8" else bsg.moe_dispatch_fp4
+    Qx, Px = quant(X, rule)
+    Q0, P0 = quant(torch.zeros(1, H, dtype=torch.bfloat16, device=DEV), rule)
+    buf = torch.full((rows, H // per + 16), 0xA5, dtype=torch.uint8, device=DEV)
+    sf = torch.full(((H // gk + 1) // 2, rows + 3), 0x5A5A, dtype=torch.int16, device=DEV)
+    disp(X, plan, rule, out=buf[:, :H // per], sf_out=sf)
+    pair = plan.pair_of.long()
+    holds, pad = pair >= 0, pair == -1
+    want = torch.full_like(buf, 0xA5)
+    want[pad, :H // per] = Q0
+    want[holds, :H // per] = Qx[pair[holds] // k]
+    assert torch.equal(buf, want), "codes"
+    # scales with a row's words side by side
+    want = torch.full_like(sf, 0x5A5A).t().contiguous()
+    of_x, of_0 = Px.t().contiguous(), P0.t().contiguous()
+    want[:rows][pad] = of_0
+    want[:rows][holds] = of_x[pair[holds] // k]
+    assert torch.equal(sf.t().contiguous(), want), "scales"
+
+
+def test_streamed_chain_captured():
+    """sort -> FP8 dispatch and bf16 dispatch -> combine past 32 MiB, captured and replayed on
+    new ids and tokens, with the same calls made eagerly in between."""
+    T, k, G, H, align = 4870, 6, 40, 1152, 16
+    assert T * k * H >= STREAM
+    rows = routing.rows_needed(T, k, G, align)
+    ids = torch.from_numpy(_ids(T, k, G, 1)).to(DEV)
+    X = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    W = torch.rand(T, k, device=DEV)
+    A = torch.zeros(rows, H, dtype=torch.bfloat16, device=DEV)
+    Q = torch.zeros(rows, H, dtype=torch.uint8, device=DEV)
+    P = torch.zeros((H // 128 + 1) // 2, rows, dtype=torch.int16, device=DEV)
+
+    def chain():
+        plan = bsg.sort_tokens(ids, G, align=align)
+        bsg.moe_dispatch_bf16(X, plan, out=A)
+        bsg.moe_dispatch_fp8(X, plan, out=Q, sf_out=P)
+        return bsg.moe_combine(A, plan, W)
+
+    def snap(out):
+        torch.cuda.synchronize()
+        r = [t.clone() for t in (out, A, Q, P)]
+        for t in (A, Q, P):
+            t.zero_()
+        torch.cuda.synchronize()
+        return r
+    snap(chain())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = chain()
+    snap(captured)
+    for seed in (1, 2, 3, 2):
+        ids.copy_(torch.from_numpy(_ids(T, k, G, seed)))
+        X.copy_(workloads.activations(T, H, seed=seed, device=DEV))
+        torch.cuda.synchronize()
+        graph.replay()
+        got = snap(captured)
+        for a, b in zip(got, snap(chain()), strict=True):
+            assert torch.equal(a, b)
