@@ -476,3 +476,132 @@ def test_lora_tile_by_tile_with_the_most_spare_rows():
     e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
     plan = bsg.sort_tokens(ids, G, align=16, out=bsg.TokenSort(e(G + 1), e(T, 1), e(rows), e(rows)))
     _check(bsg.lora_add_bf16(X, A, B, plan, scale, base), X, A, B, ids, scale, base, "spare rows")
+
+
+# ---------------------------------------------------------------------------
+# The four forms, each known by what it leaves of a workspace that held 0xFF bytes:
+#   one       one launch: all of it
+#   apart     tile by tile: S slabs of U and nothing else, S slices of at least 1024 of K
+#   adds      grouped tiles whose slabs the second product adds: the rows behind them
+#   joined    grouped tiles, slabs joined in those rows
+# ---------------------------------------------------------------------------
+def _form(X, A, B, plan, scale, base):
+    """(form, out) of a call with a workspace, of which nothing behind its size is touched."""
+    (T, K), (G, r, _), N, rows = X.shape, A.shape, B.shape[1], plan.pair_of.numel()
+    need = bsg.lib().lora_add_workspace(T, rows, G, N, K, r)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device=DEV)     # NaN as floats
+    out = bsg.lora_add_bf16(X, A, B, plan, scale, base, workspace=ws)
+    assert torch.all(ws[need:] == 255), "touched behind the workspace"
+    tiles = -(-rows // 16)
+    behind = 4 * tiles * 16 * (32 if r <= 32 else 64 if r <= 64 else 128)
+    if torch.all(ws == 255):
+        return "one", out
+    if need == 4 * max(1, min(512 // tiles, -(-K // 1024))) * tiles * 16 * r:
+        return "apart", out
+    return "adds" if torch.all(ws[need - behind:] == 255) else "joined", out
+
+
+FORMS = [  # T, G, K, N, r, spare rows, form
+    (20, 3, 64, 72, 8, 0, "one"), (300, 5, 256, 1000, 8, 4096, "one"),
+    (300, 5, 256, 1000, 24, 4096, "apart"),         # (284 tiles of 4 workgroups with the spare rows)
+    (64, 32, 1032, 512, 16, 0, "one"), (64, 32, 2056, 512, 32, 0, "apart"), (200, 3, 4104, 304, 128, 4096, "apart"), (3000, 6, 520, 136, 64, 4096, "apart"),
+    (9000, 40, 520, 264, 48, 4096, "adds"), (4096, 100, 264, 400, 128, 4096, "adds"), (16300, 3, 2400, 24, 8, 0, "adds"),
+    (1300, 9, 6000, 1500, 40, 4096, "adds"),        # (fewer slices with the spare rows)
+    (1300, 9, 6000, 1500, 40, 0, "joined"), (2000, 3, 4096, 2000, 128, 4096, "joined"), (3000, 20, 4104, 129, 128, 0, "joined")]
+
+
+@pytest.mark.parametrize("T,G,K,N,r,spare,form", FORMS)
+def test_lora_forms(T, G, K, N, r, spare, form):
+    """Each form with spare rows, a workspace, padded and unaligned rows, in place, through
+    both ways into the library."""
+    _say(f"lora_add T={T} G={G} K={K} N={N} r={r} spare={spare}: {form}")
+    for pad in (0, 3):
+        ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, T, pad=pad)
+        if spare:
+            rows = T + 15 * G + spare
+            e = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+            plan = bsg.sort_tokens(ids, G, align=16, out=bsg.TokenSort(e(G + 1), e(T, 1), e(rows), e(rows)))
+        got, out = _form(X, A, B, plan, scale, base)
+        assert got == form
+        _check(out, X, A, B, ids, scale, base, f"pad {pad}")
+        assert torch.equal(bsg.lora_add_bf16(X, A, B, plan, scale, base), out)
+        wide = torch.full((T, N + 5), 3.0, dtype=torch.bfloat16, device=DEV)
+        mine = wide[:, :N]
+        mine.copy_(base)
+        assert bsg.lora_add_bf16(X, A, B, plan, scale, mine, out=mine) is mine
+        assert torch.equal(mine, out) and torch.all(wide[:, N:] == 3.0)
+
+
+@pytest.mark.parametrize("T,K,N,r,form", [(40, 256, 256, 8, "one"), (3000, 520, 264, 40, "apart"),
+                                          (9000, 520, 264, 48, "adds"), (1300, 6000, 1500, 40, "joined")])
+def test_lora_forms_captured_and_on_two_streams(T, K, N, r, form):
+    """As test_lora_captured_and_on_two_streams, for each of the forms."""
+    _say(f"lora_add captured, T={T} K={K} N={N} r={r}: {form}")
+    G = 9
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 1)
+    assert _form(X, A, B, plan, scale, base)[0] == form
+
+    def step():
+        return bsg.lora_add_bf16(X, A, B, bsg.sort_tokens(ids, G, align=16), scale, base)
+    step()
+    torch.cuda.synchronize()
+    graphs, results = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            results.append(step())
+    rng = np.random.default_rng(0)
+    for i in range(4):
+        ids.copy_(torch.from_numpy(np.minimum(rng.integers(-1, G, (T, 1)), i + 3).astype(np.int32)))
+        X.copy_(torch.randn(T, K, device=DEV))
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        for out in results:
+            assert torch.equal(out, want)
+    plan = bsg.sort_tokens(ids, G, align=16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        outs = []
+        for stream in streams:
+            with torch.cuda.stream(stream):
+                outs.append(bsg.lora_add_bf16(X, A, B, plan, scale, base))
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out, want)
+
+
+def test_lora_grouped_tiles_without_anything_to_add():
+    """K = 0, and a plan of no rows, at sizes that would group tiles."""
+    T, G, N, r = 4096, 2, 1200, 64
+    _say(f"lora_add T={T} N={N} r={r}, K = 0, no rows")
+    e = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)
+    plan = bsg.sort_tokens(torch.zeros(T, 1, dtype=torch.int32, device=DEV), G, align=16)
+    assert T * r * N >= 270 << 20
+    assert torch.equal(bsg.lora_add_bf16(e(T, 0), e(G, r, 0), e(G, N, r), plan, base=e(T, N)), e(T, N))
+    i = lambda *s: torch.full(s, -1, dtype=torch.int32, device=DEV)
+    none = (i(G + 1), i(T, 1), i(0), i(0))
+    assert torch.equal(bsg.lora_add_bf16(e(T, 64), e(G, r, 64), e(G, N, r), none, base=e(T, N)), e(T, N))
+    # rows, but no token with an adapter
+    plan = bsg.sort_tokens(torch.full((T, 1), -1, dtype=torch.int32, device=DEV), G, align=16)
+    assert torch.equal(bsg.lora_add_bf16(e(T, 64), e(G, r, 64), e(G, N, r), plan, base=e(T, N)), e(T, N))
+
+
+def test_lora_joined_broken_plan_stays_in_bounds():
+    """Broken groups, pairs and offsets where the slabs are joined."""
+    T, G, K, N, r = 2000, 4, 4096, 2000, 128
+    ids, plan, X, A, B, scale, base = _case(T, G, K, N, r, 5, missing=0.0)
+    assert _form(X, A, B, plan, scale, base)[0] == "joined"
+    plan.row_group[:16] = 4
+    plan.row_group[16:32] = 2 ** 31 - 1
+    plan.pair_of[40::3] = 2 ** 31 - 1
+    offsets = plan.offsets.clone()
+    for at, value in ((-1, 2 ** 31 - 1), (-1, -5), (1, 2 ** 31 - 1), (2, -1), (0, 777), (3, 0)):
+        plan.offsets.copy_(offsets)
+        plan.offsets[at] = value
+        bsg.lora_add_bf16(X, A, B, plan, scale, base)
+        torch.cuda.synchronize()

@@ -249,3 +249,16 @@ def test_a_missing_binding_is_named(monkeypatch, tmp_path):
               lambda: bsg.moe_combine(torch.zeros(8, 128, dtype=torch.bfloat16), _plan())):
         with pytest.raises(RuntimeError, match="_binding.so is missing: build it with"):
             f()
+
+
+def test_lora_workspace_refusals_of_grouped_tiles():
+    """As in test_lora_refusals, at sizes that group tiles (with the slabs added by the second
+    product, and joined)."""
+    L = bsg.lib()
+    G = 4
+    for T, rows, K, N, r in ((8192, 8256, 512, 512, 48), (1024, 1104, 8192, 4096, 128)):
+        assert not _tiles_apart(T, rows, G, N, K, r)
+        need = L.lora_add_workspace(T, rows, G, N, K, r)
+        for ws, size, status in ((0, need, INV), (0x80000, need - 1, INV), (0x80000, 0, INV), (0x80008, need, ALIGN)):
+            assert L.lora_add_bf16(P, K, P, K, r * K, P, r, N * r, P2, P2, P2, P3, P4, rows, P5, N, 0x90000, N,
+                                   T, G, N, K, r, ws, size, None) == status, (T, ws, size)
