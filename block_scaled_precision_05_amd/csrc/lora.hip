@@ -871,12 +871,18 @@ static int64_t most_items(int64_t tiles, int64_t G) {
 
 // Whether tiles are grouped (the forms for many tokens).  Tile by tile, every 16 tokens
 // read a whole adapter from L2, T r (K + N) / 8 bytes; grouped, 64 tokens share it, for
-// one more launch or two and workgroups that do more each.  T, K, N, r, in M of T r (K + N), us
-// tile by tile / grouped:
-//   2048, 512, 512, 32:    67,  6.3 / 10.4;    1000, 1000, 1000, 64: 128,  9.5 / 13.5;
-//   600, 2000, 2000, 96:  230, 12 / 19;        4000, 4000, 512, 16:  289, 16 / 16;
-//   512, 4096, 4096, 64:  268, 14 / 15;        8192, 4096, 256, 8:   285, 24 / 18;
-//   2048, 4096, 4096, 32: 537, 22 / 20;        8192, 1024, 128, 64:  604, 21 / 15.
+// one more launch or two and workgroups that do more each.  Tokens, adapters (drawn evenly),
+// K, N, rank, 2^20s of T r (K + N): us tile by tile / grouped, replayed:
+//   2048, 8,  512,  512, 32:   64,  6.5 / 10.0;     1000, 8, 1000, 1000, 64: 122, 10.0 / 13.6;
+//    600, 8, 2000, 2000, 96:  220, 12.3 / 18.5;      512, 8, 4096, 4096, 64: 256, 14.5 / 15.6;
+//   8192, 8, 4096,  256,  8:  272, 24.4 / 18.2;     4000, 8, 4000,  512, 16: 275, 16.4 / 16.3;
+//   2048, 8, 4096, 4096, 32:  512, 22.3 / 19.0;     512, 8, 4096, 4096, 128: 512, 25.8 / 21.0;
+//   512, 64, 4096, 4096, 128: 512, 41.2 / 36.1;     8192, 8, 1024, 128, 64:  576, 20.7 / 14.9;
+//   8192, 8, 512, 2048, 128: 2560, 68.1 / 33.5;     8192, 16, 7168, 4096, 64: 5632, 138 / 62.
+// The product knows neither how many items there are nor how many columns they share, and
+// decides these for the slower form:
+//   1000, 8, 4000, 128, 128:  504, 19.3 / 23.0;     2000, 8, 2000, 256, 64:  275, 12.2 / 15.3;
+//   2000, 8, 4000, 256, 64:   520, 17.2 / 18.6;     4096, 32, 1024, 512, 32: 192, 12.1 / 11.2.
 // (Stages of the items, of kStage elements of K, are counted in 32 bits: a plan that can have
 // more than 2^30, most of it padding, is taken tile by tile.)
 static bool many_tokens(int64_t T, int64_t rows, int64_t G, int64_t N, int64_t K, int64_t r) {
@@ -885,10 +891,13 @@ static bool many_tokens(int64_t T, int64_t rows, int64_t G, int64_t N, int64_t K
 }
 
 // Rank fragments of a workgroup of the first product for few tokens: the whole rank, or
-// parts of it, each of which reads X again, for about 1024 workgroups (1 token, rank 128:
-// 17.6 us with the whole rank, 9.3 in 8 parts; 1024 tokens of 64 adapters, rank 64: 29.5
-// whole, 30.8 in halves, 34.1 in quarters; 256 tokens, rank 128: 45 whole, 38 in halves,
-// 36 in quarters).
+// parts of it, each of which reads X again, for about 1024 workgroups.  K = N = 4096, us of
+// both products with 1 / 2 / 4 / 8 fragments of 16 a workgroup, replayed:
+//      1 token, rank 128:                   9.2 / 10.1 / 12.2 / 16.6  (1 chosen);
+//     16 tokens of 1, rank 128:            11.0 / 11.7 / 13.8 / 17.9  (1);
+//    256 tokens of 1 or 8, rank 128:       16.7 / 16.5 / 16.0 / 20.2  (1);
+//    256 tokens of 64, rank 128:           38.1 / 35.3 / 36.8 / 43.2  (4);
+//   1024 tokens of 64, rank 64:            33.4 / 30.5 / 29.2         (2).
 constexpr int kFewItems = 1024;
 static int rank_fragments(int64_t tiles, int64_t S, int64_t r) {
   const int64_t all = r <= 16 ? 1 : (r <= 32 ? 2 : (r <= 64 ? 4 : 8)), frags = ceil_div(r, 16);
@@ -925,10 +934,10 @@ static bool adds_slabs(int64_t S, int64_t r, int64_t slab_bytes, int64_t col_blo
 // Whether both products go into one launch: while what its workgroups read of K, which
 // each of a tile's does again, takes less time than a second launch (3.3 us and up; two
 // launches 5 and up, and twice the host's work).  us in one launch / in two, replayed:
-//   K 256, N 1024, rank 8:  1 token 3.3 / 5.0, 512 tokens 3.8 / 5.6;
-//   K 2048, N 4096, rank 16:  16 tokens 5.9 / 6.5, 256 tokens 10.6 / 7.5;
-//   K 4096, N 4096, 1 token:  rank 8 6.2 / 6.7, rank 16 7.4 / 7.0;
-//   K 1024, N 1024, rank 32:  64 tokens 5.9 / 6.8;   K 2048: 16 tokens 7.6 / 6.7.
+//   K 256, N 1024, rank 8:  1 token 3.4 / 5.3, 512 tokens of 8 adapters 3.9 / 5.5;
+//   K 2048, N 4096, rank 16:  16 tokens of 1 6.7 / 7.0, of 8 5.6 / 6.5, 256 of 8 10.6 / 7.4;
+//   K 4096, N 4096, 1 token:  rank 8 6.3 / 6.8, rank 16 7.5 / 6.9;
+//   N 1024, rank 32:  K 1024, 64 tokens of 8 5.8 / 6.7;   K 2048, 16 tokens of 8 7.5 / 6.6.
 static bool whole_launch(int64_t T, int64_t workgroups, int64_t K, int64_t r) {
   return r <= 32 && 2 * K * (r + 8) + K * (T < 16 ? T : 16) <= 160000 * 128 / (workgroups < 128 ? 128 : workgroups);
 }

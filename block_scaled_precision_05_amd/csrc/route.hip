@@ -37,14 +37,15 @@ static int launch_status() { return hipGetLastError() == hipSuccess ? BSG_OK : B
 // Only a few bytes per pair move (4 read, 12 written), so the cost is latency: launches,
 // dependent steps, and the scattered 4-byte writes, of which one CU finishes some two a
 // ns.  Up to kSingle pairs there is one launch, in which every workgroup sorts all the
-// pairs for itself, in LDS, and writes a share of the results (4096 pairs, 256 groups
-// padded to 128 rows: 7.4 us, 10.9 where one workgroup writes everything, 8.5 in two
-// launches; 768 pairs, 384 groups: 3.6 us).  More pairs are cut into chunks, counted by a
-// first launch (hist[chunk][g]); in a second one every workgroup sums the counts of all
-// chunks itself (coalesced reads from L2, under which it forms the first ranks) instead of
-// waiting for a scan launch, and places its chunk, or a share of it where chunks are few
-// (98304 pairs, 384 groups: 11.2 us with the gap between the launches, 2.5 + 8.8 in the
-// kernels at 256; 24576 pairs in shares 8.5, half a us less than unshared).
+// pairs for itself, in LDS, and writes a share of the results (replayed from a graph, us
+// shared / where one workgroup writes everything: 4096 pairs, 256 groups 7.2 / 8.2, and 8.0
+// in two launches; 2048 pairs, 256 groups 4.9 / 6.0; 768 pairs, 384 groups 3.8 / 3.7).  More
+// pairs are cut into chunks, counted by a first launch (hist[chunk][g]); in a second one
+// every workgroup sums the counts of all chunks itself (coalesced reads from L2, under which
+// it forms the first ranks) instead of waiting for a scan launch, and places its chunk, or a
+// share of it where chunks are few (98304 pairs, 384 groups: 11.1 us with the gap between the
+// launches, at 256 groups 2.5 + 8.2 in the kernels; 24576 pairs in shares 8.5, half a us
+// less than unshared; masked, 24576 pairs, 48 groups of 1024 7.7).
 //
 // Ranks, in pair order: a wave takes 64 pairs; a lane's peers, the lanes with its id,
 // come from one ballot per id bit; its rank in the wave is the number of peers below it,
@@ -383,7 +384,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* base, int
                                            __builtin_amdgcn_readfirstlane(in ? (int)bytes : 0), kRsrcWord3);
 }
 
-// Loads and stores of VEC bf16 elements a lane: 8 (one 16-byte access) or 1.
+// Loads and stores of VEC bf16 elements a lane: 8 (one 16-byte access) or 1, where a width, a
+// leading dimension or an address is not a multiple of 8 elements (4095 tokens, 8 choices,
+// 2048 against 2047 wide, us: dispatch 25 / 74, combine 27 / 69, gradient 52 / 73).
 template <int VEC>
 struct Vec;
 template <>
@@ -499,7 +502,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_bf16_kernel(
 // of a line that 32 rows of a group share; with many tokens each XCD takes a contiguous
 // part of them, so that most lines fill up in one L2 (835 MB written in place of 872, 212
 // us in place of 214, 5.1 TB/s for 16384 tokens, 6 choices, 7168 wide; 512 tokens on an
-// eighth of the experts 4.7 us).
+// eighth of the experts 4.7 us).  FP4 of the same sizes, either rule: 253 us, 238 MB read and
+// 656 written at 3.5 TB/s (a row has 112 scale words of 2 bytes in as many lines, FP8 has
+// 28); 4.7 us for the 512 tokens.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a),
@@ -634,7 +639,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(
 // j, rounded once.  A wave owns 64*VEC elements of one token; the loads of KC rows (all
 // of them up to eight choices) are in flight together.  A pair without a row reads zeros
 // through an empty buffer and its weight counts as zero.  16384 tokens, 6 choices, 7168
-// wide: 271 us, 6.1 TB/s; 33 tokens, 8 choices: 3.3 us.
+// wide: 271 us, 6.1 TB/s, while the output is one 235 MB buffer, which the memory-side
+// cache (256 MB) holds; 296 where two outputs alternate.  33 tokens, 8 choices: 3.3 us.
 // ---------------------------------------------------------------------------
 template <int VEC, int KC, int AUX>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
@@ -675,7 +681,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
 // choice and lane, and add them over lanes and waves in a fixed order.  Where rows are
 // short a wave does that alone (WPT 1).  dO is read once per KC choices, Y once, dY written
 // once.  8192 tokens, 6 choices, 7168 wide, groups of 128 rows: 347 us, 5.2 TB/s with the
-// padding rows;  257 tokens, 2 choices, 2056 wide: 3.9 us;  1 token, 8 choices, 7168 wide:
+// padding rows (370 where three dO of 117 MB take turns, more than the memory-side cache
+// holds);  257 tokens, 2 choices, 2056 wide: 3.9 us;  1 token, 8 choices, 7168 wide:
 // 3.4 us (7.1 in one workgroup);  8192 tokens, 8 choices, 128 wide: 14 us (31 with a
 // workgroup a token;  1024 wide, past the L2s: 55, and 52 with a workgroup).
 // ---------------------------------------------------------------------------
