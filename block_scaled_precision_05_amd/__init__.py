@@ -26,6 +26,10 @@ if ``libbsg.so`` is missing or cannot be loaded, every call raises.
     D = moe_combine(Y, plan, W)                 # sum_j w * experts' row, back in token order
     dY, dW = moe_combine_backward(dD, Y, plan, W)
     D = lora_add_bf16(X, A, B, plan, scale, base)  # base + s_g B_g (A_g x), an adapter per token
+
+No function records an autograd graph: the results are detached whatever their inputs
+require, and training calls the gradients' functions itself (from a
+torch.autograd.Function, say).
 """
 from __future__ import annotations
 

@@ -643,3 +643,52 @@ def test_streamed_chain_captured():
         got = snap(captured)
         for a, b in zip(got, snap(chain()), strict=True):
             assert torch.equal(a, b)
+
+
+def test_expert_layer_under_autograd():
+    """The functions record no graph; in training they stand in autograd Functions.  All
+    values are integers and powers of two, so that every sum is exact: equal to fp64."""
+    _say("dispatch -> experts -> combine, trained")
+    T, k, G, H, align = 70, 3, 6, 64, 16
+    g = torch.Generator(device=DEV).manual_seed(6)
+    ids = torch.from_numpy(_ids(T, k, G, 9)).to(DEV)
+    plan = bsg.sort_tokens(ids, G, align=align)
+    rows = plan.pair_of.numel()
+
+    class Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X):
+            return bsg.moe_dispatch_bf16(X, plan, out=X.new_zeros(rows, H))
+
+        @staticmethod
+        def backward(ctx, dA):
+            return bsg.moe_combine(dA.contiguous(), plan)
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, Y, W):
+            ctx.save_for_backward(Y, W)
+            return bsg.moe_combine(Y, plan, W)
+
+        @staticmethod
+        def backward(ctx, dO):
+            Y, W = ctx.saved_tensors
+            return bsg.moe_combine_backward(dO.contiguous(), Y, plan, W, out=torch.zeros_like(Y))
+
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV)
+    X, dO = ints(T, H).to(torch.bfloat16), ints(T, H).to(torch.bfloat16)
+    W = torch.exp2(-torch.randint(0, 3, (T, k), generator=g, device=DEV).float())
+    s = torch.exp2(torch.randint(-1, 2, (G,), generator=g, device=DEV).float())
+    assert not bsg.moe_dispatch_bf16(X.clone().requires_grad_(), plan).requires_grad
+    X.requires_grad_(), W.requires_grad_()
+    Y = Dispatch.apply(X) * s[plan.row_group.clamp_min(0).long(), None].to(torch.bfloat16)
+    out = Combine.apply(Y, W)
+    out.backward(dO)
+
+    Xd, Wd = X.detach().double().requires_grad_(), W.detach().double().requires_grad_()
+    kept = (ids >= 0) & (ids < G)
+    f = torch.where(kept, s.double()[ids.clamp(0, G - 1).long()], 0.0)
+    want = (Wd * f).sum(1, keepdim=True) * Xd
+    want.backward(dO.double())
+    assert torch.equal(out.double(), want)
+    assert torch.equal(X.grad.double(), Xd.grad) and torch.equal(W.grad.double(), Wd.grad)
