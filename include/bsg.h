@@ -415,7 +415,8 @@ int moe_ffn_fp8_noalloc(const void* A, int64_t lda, const int16_t* sfa, int64_t 
  *   workspace: sort_tokens_workspace(T*k, G) bytes, 4-byte aligned (may be NULL when
  *   that is 0); its contents need no initial value.  Calls that overlap need a
  *   workspace each.
- *   Requires G <= 1024, k <= 64, T*k <= 2^23 and rows <= 2^31 - 2^18. */
+ *   Requires G <= 1024, k <= 64, T*k <= 2^23, align < 2^20, G*cap < 2^30 and
+ *   rows <= 2^31 - 2^18. */
 int sort_tokens(const int32_t* ids, int64_t ld_ids, int64_t T, int32_t k, int32_t G, int32_t align,
                 int32_t cap, int32_t* offsets, int32_t* row_of, int32_t* pair_of, int32_t* row_group,
                 int64_t rows, void* workspace, int64_t workspace_bytes, void* stream);
@@ -430,9 +431,10 @@ int64_t sort_tokens_workspace(int64_t pairs, int32_t G);
  *   (X and out 16-byte aligned with ldx, ldo and H multiples of 8 move 16 bytes at a
  *   time).  X and out must not overlap.
  *   The gradient with respect to X is moe_combine of the gradient of out, without
- *   weights.  k <= 64, H <= 2^28; a call of more than 2^24 - 1 workgroups (one per 16
- *   rows and one per 4 KiB of X, per 512 bytes where it moves single elements) is
- *   refused, as in the operators below. */
+ *   weights.  k <= 64, H <= 2^28, T*k and rows below 2^31 - 1024, leading dimensions at
+ *   most 2^40; a call of more than 2^24 - 1 workgroups (one per 16 rows and one per 4 KiB
+ *   of X, per 512 bytes where it moves single elements) is refused, as in the operators
+ *   below. */
 int moe_dispatch_bf16(const void* X, int64_t ldx, const int32_t* row_of, const int32_t* pair_of,
                       int64_t T, int32_t k, int64_t rows, int64_t H, void* out, int64_t ldo,
                       void* stream);
@@ -500,9 +502,9 @@ int moe_combine_backward(const void* dO, int64_t ldo, const void* Y, int64_t ldy
  *   Requires r % 8 == 0, r <= 128, K % 8 == 0, K <= 2^22, G <= 1024, T and rows <= 2^26,
  *   N <= 2^23, ld_base and ldo below 2^31, the other leading dimensions and strides below
  *   2^34, and for T r (K + N) >= 270 * 2^20 (tiles of 16 rows are then taken four together)
- *   (ceil(rows/64) + min(G, ceil(rows/16))) * ceil(N/256) < 2^24; X, A, B 16-byte aligned with leading dimensions and strides
- *   multiples of 8; any N, base and out 2-byte aligned (fastest where their rows start
- *   at multiples of 128 bytes). */
+ *   (ceil(rows/64) + min(G, ceil(rows/16))) * ceil(N/256) < 2^24; X, A, B 16-byte aligned
+ *   with leading dimensions and strides multiples of 8; any N, base and out 2-byte aligned
+ *   (fastest where their rows start at multiples of 128 bytes). */
 int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B,
                   int64_t ldb, int64_t stride_b, const float* scale, const int32_t* offsets,
                   const int32_t* row_of, const int32_t* pair_of, const int32_t* row_group, int64_t rows,

@@ -262,3 +262,28 @@ def test_lora_workspace_refusals_of_grouped_tiles():
         for ws, size, status in ((0, need, INV), (0x80000, need - 1, INV), (0x80000, 0, INV), (0x80008, need, ALIGN)):
             assert L.lora_add_bf16(P, K, P, K, r * K, P, r, N * r, P2, P2, P2, P3, P4, rows, P5, N, 0x90000, N,
                                    T, G, N, K, r, ws, size, None) == status, (T, ws, size)
+
+
+def test_documented_limits_are_the_checked_ones():
+    """The largest sizes that the header allows pass the check of the sizes (a missing pointer
+    is refused after it, so that nothing launches), the next ones do not."""
+    L = bsg.lib()
+
+    def sort(T=10000, G=8, align=1, cap=0, rows=2 ** 31 - 2 ** 18):
+        return L.sort_tokens(P, 4, T, 4, G, align, cap, P2, P3, P4, P5, rows, 0, 0, None)
+    assert sort(align=2 ** 20 - 1) == INV and sort(align=2 ** 20) == SHAPE
+    assert sort(cap=2 ** 27 - 1) == INV and sort(cap=2 ** 27) == SHAPE
+    assert sort(T=2 ** 21) == INV and sort(T=2 ** 21 + 1) == SHAPE
+    assert sort(G=1024) == INV and sort(G=1025) == SHAPE
+
+    def dispatch(T=100, k=4, rows=500, H=256, ldx=2 ** 40):
+        return L.moe_dispatch_bf16(P, ldx, P2, P3, T, k, rows, H, 0, 2 ** 40, None)
+
+    def combine(T=100, k=4, rows=500, H=256, ldx=2 ** 40):
+        return L.moe_combine(P, ldx, P2, P3, k, T, k, rows, H, 0, 2 ** 40, None)
+    for f in (dispatch, combine):
+        assert f() == INV and f(ldx=2 ** 40 + 1) == SHAPE
+        assert f(k=64) == INV and f(k=65) == SHAPE
+        assert f(H=2 ** 28) == INV and f(H=2 ** 28 + 1) == SHAPE
+        assert f(rows=2 ** 31 - 1025) == INV and f(rows=2 ** 31 - 1024) == SHAPE
+        assert f(T=2 ** 31 - 1025, k=1) == INV and f(T=2 ** 31 - 1024, k=1) == SHAPE
