@@ -26,6 +26,10 @@ if ``libbsg.so`` is missing or cannot be loaded, every call raises.
     D = moe_combine(Y, plan, W)                 # sum_j w * experts' row, back in token order
     dY, dW = moe_combine_backward(dD, Y, plan, W)
     D = lora_add_bf16(X, A, B, plan, scale, base)  # base + s_g B_g (A_g x), an adapter per token
+    D = gemm_bf16_act(A, B, bias, act, residual)       # residual + f(A B^T + bias); also _fp8, _fp4
+    dA, dB, dbias = gemm_bf16_act_backward(dD, A, B, preact, act)
+    H = gemm_bf16_glu(X, W13, act)              # f(X Wg^T) * (X Wu^T), W13 = [Wg; Wu]
+    dX, dW13 = gemm_bf16_glu_backward(dH, X, W13, preact, act)
 
 No function records an autograd graph: the results are detached whatever their inputs
 require, and training calls the gradients' functions itself (from a
@@ -51,6 +55,7 @@ BSG_ERR_MISALIGNED = 3
 BSG_ERR_HIP = 4
 
 SCALE_RULES = {"ceil": 0, "ocp_mx": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lock = threading.Lock()
 _lib = None
@@ -104,11 +109,28 @@ EXPORTS = {
                              _vp, _i64, _vp, _i64, _vp],
     "lora_add_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
                       _vp, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp],
+    "gemm_bf16_act": [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64,
+                      _vp, _i64, _vp],
+    "gemm_fp8_act": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _i64, _vp, _i64,
+                     _i64, _i64, _i64, _vp, _i64, _vp],
+    "gemm_fp4_act": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _i64,
+                     _i64, _i64, _i64, _vp, _i64, _vp],
+    "gemm_bf16_act_backward": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp,
+                               _i64, _i64, _i64, _vp, _i64, _vp],
+    "gemm_bf16_glu": [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp],
+    "gemm_bf16_glu_backward": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64,
+                               _i64, _i64, _i64, _vp, _i64, _vp],
 }
 # functions that return a number of bytes, not a status
 SIZES = {
     "sort_tokens_workspace": [_i64, _i32],
     "lora_add_workspace": [_i64, _i64, _i32, _i64, _i64, _i32],
+    "gemm_bf16_act_workspace": [_i64, _i64, _i64],
+    "gemm_fp8_act_workspace": [_i64, _i64, _i64],
+    "gemm_fp4_act_workspace": [_i64, _i64, _i64],
+    "gemm_bf16_act_backward_workspace": [_i64, _i64, _i64],
+    "gemm_bf16_glu_workspace": [_i64, _i64, _i64],
+    "gemm_bf16_glu_backward_workspace": [_i64, _i64, _i64],
 }
 
 
@@ -936,4 +958,196 @@ def lora_add_bf16(X, A, B, plan, scale=None, base=None, out=None, workspace=None
             row_group.data_ptr(), rows,
             _ptr(base), ld_base, D.data_ptr(), ldo, T, G, N, K, r, _ptr(ws), size, st))
         return D
+    return _launch(X, stream, body)
+
+
+# Dense products with work in their epilogues, and their gradients.
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _space(workspace, need, device):
+    """(tensor, its bytes) of a call's workspace, allocated when none was given."""
+    if workspace is None:
+        if not need:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _epilogue(M, N, bias, residual, out, preact=None):
+    """Leading dimensions of the residual, the output and the pre-activation."""
+    if bias is not None:
+        if bias.dtype != torch.bfloat16:
+            raise TypeError(f"bias must be {torch.bfloat16}, got {bias.dtype}")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous vector [{N}]")
+    ldr = 0 if residual is None else _ld(residual, "residual", torch.bfloat16, M, N)
+    ldd = N if out is None else _ld(out, "out", torch.bfloat16, M, N)
+    ldz = 0 if preact is None else _ld(preact, "preact", torch.bfloat16, M, N)
+    return ldr, ldd, ldz
+
+
+def gemm_bf16_act(A, B, bias=None, act: str = "none", residual=None, out=None, preact=None, workspace=None,
+                  stream=None):
+    """D = residual + f(A B^T + bias): A bf16 [M, K], B bf16 [N, K], bias bf16 [N] or None,
+    act one of "none", "relu", "silu", "gelu", "gelu_tanh", residual bf16 [M, N] or None
+    (``out`` may be the residual: added in place).  ``preact`` (bf16 [M, N]), where given,
+    receives A B^T + bias, which gemm_bf16_act_backward takes.  Sums are fp32, each output
+    rounded once.  ``workspace`` may pass a 16-byte aligned contiguous tensor of at least
+    gemm_bf16_act_workspace(M, N, K) bytes."""
+    _one_gpu(A, B, bias, residual, out, preact, workspace)
+    M, K = A.shape[0], _width(A, "A")
+    N = B.shape[0]
+    lda, ldb = _ld(A, "A", torch.bfloat16, M, K), _ld(B, "B", torch.bfloat16, N, K)
+    code = _act(act)
+    ldr, ldd, ldz = _epilogue(M, N, bias, residual, out, preact)
+    L = lib()
+
+    def body(st):
+        D = torch.empty((M, N), dtype=torch.bfloat16, device=A.device) if out is None else out
+        ws, size = _space(workspace, L.gemm_bf16_act_workspace(M, N, K), A.device)
+        _check("gemm_bf16_act", L.gemm_bf16_act(
+            A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(bias), code, _ptr(residual), ldr, D.data_ptr(), ldd,
+            _ptr(preact), ldz, M, N, K, _ptr(ws), size, st))
+        return D
+    return _launch(A, stream, body)
+
+
+def _act_scaled(fn, A, sfa, B, sfb, gran, bias, act, residual, K, out, workspace, stream):
+    _one_gpu(A, sfa, B, sfb, bias, residual, out, workspace)
+    A, B = _bytes_u8(A), _bytes_u8(B)
+    M, N = A.shape[0], B.shape[0]
+    lda, ldb = _mat(A, "A"), _mat(B, "B")
+    ld_sfa, ld_sfb = _packed(sfa, "sfa"), _packed(sfb, "sfb")
+    gk = 128 if fn == "gemm_fp8_act" else 32
+    kp = (K // gk + 1) // 2
+    rows_b = N if gran == 1 else (N + 127) // 128
+    if sfa.shape[0] < kp or sfa.shape[1] < M or sfb.shape[0] < kp or sfb.shape[1] < rows_b:
+        raise ValueError(f"sfa must be packed int16 [{kp}, >={M}] and sfb [{kp}, >={rows_b}]")
+    code = _act(act)
+    ldr, ldd, _ = _epilogue(M, N, bias, residual, out)
+    L = lib()
+
+    def body(st):
+        D = torch.empty((M, N), dtype=torch.bfloat16, device=A.device) if out is None else out
+        ws, size = _space(workspace, getattr(L, fn + "_workspace")(M, N, K), A.device)
+        scales = (B.data_ptr(), ldb, sfb.data_ptr(), ld_sfb) + ((gran,) if fn == "gemm_fp8_act" else ())
+        _check(fn, getattr(L, fn)(
+            A.data_ptr(), lda, sfa.data_ptr(), ld_sfa, *scales, _ptr(bias), code, _ptr(residual), ldr,
+            D.data_ptr(), ldd, M, N, K, _ptr(ws), size, st))
+        return D
+    return _launch(A, stream, body)
+
+
+def gemm_fp8_act(A, sfa, B, sfb, bias=None, act: str = "none", residual=None, out=None, workspace=None,
+                 stream=None, sfb_gran_mn: int = 128):
+    """gemm_bf16_act on the operands of gemm_fp8_blockscaled (e4m3 codes with packed UE8M0
+    scales; sfb per 128x128 block of B, or per row with sfb_gran_mn = 1), without preact."""
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError("A must be [M, K] and B [N, K]")
+    return _act_scaled("gemm_fp8_act", A, sfa, B, sfb, sfb_gran_mn, bias, act, residual, A.shape[1], out,
+                       workspace, stream)
+
+
+def gemm_fp4_act(A, sfa, B, sfb, bias=None, act: str = "none", residual=None, K: int | None = None, out=None,
+                 workspace=None, stream=None):
+    """gemm_bf16_act on the operands of gemm_fp4_blockscaled (e2m1 codes, two per byte, with
+    packed 1x32 scales on both), without preact."""
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A must be [M, K/2] and B [N, K/2]")
+    K = 2 * A.shape[1] if K is None else K
+    if A.shape[1] * 2 < K or B.shape[1] * 2 < K:
+        raise ValueError("K larger than the operands")
+    return _act_scaled("gemm_fp4_act", A, sfa, B, sfb, 1, bias, act, residual, K, out, workspace, stream)
+
+
+def gemm_bf16_act_backward(dout, A, B, preact=None, act: str = "none", need=(True, True, True), workspace=None,
+                           stream=None):
+    """Gradients of gemm_bf16_act: (dA bf16 [M, K], dB bf16 [N, K], dbias float32 [N]) from
+    dout bf16 [M, N] and the forward call's ``preact`` (with act "none" not read, may be
+    None).  The residual's gradient is dout itself.  ``need`` tells which of the three are
+    computed, the others are None.  ``workspace`` may pass at least
+    gemm_bf16_act_backward_workspace(M, N, K) bytes."""
+    _one_gpu(dout, A, B, preact, workspace)
+    M, K = A.shape[0], _width(A, "A")
+    N = B.shape[0]
+    lda, ldb = _ld(A, "A", torch.bfloat16, M, K), _ld(B, "B", torch.bfloat16, N, K)
+    ldd = _ld(dout, "dout", torch.bfloat16, M, N)
+    code = _act(act)
+    if preact is None and code:
+        raise ValueError(f"the gradient of {act} needs preact")
+    ldz = 0 if preact is None else _ld(preact, "preact", torch.bfloat16, M, N)
+    need_a, need_b, need_bias = need
+    L = lib()
+
+    def body(st):
+        dA = torch.empty((M, K), dtype=torch.bfloat16, device=A.device) if need_a else None
+        dB = torch.empty((N, K), dtype=torch.bfloat16, device=A.device) if need_b else None
+        dbias = torch.empty(N, dtype=torch.float32, device=A.device) if need_bias else None
+        ws, size = _space(workspace, L.gemm_bf16_act_backward_workspace(M, N, K), A.device)
+        _check("gemm_bf16_act_backward", L.gemm_bf16_act_backward(
+            dout.data_ptr(), ldd, _ptr(preact), ldz, A.data_ptr(), lda, B.data_ptr(), ldb, code, _ptr(dA), K,
+            _ptr(dB), K, _ptr(dbias), M, N, K, _ptr(ws), size, st))
+        return dA, dB, dbias
+    return _launch(A, stream, body)
+
+
+def _glu_sizes(X, W13):
+    M, K = X.shape[0], _width(X, "X")
+    two_i = W13.shape[0]
+    if two_i % 2:
+        raise ValueError("W13 must be [2*inter, K]: gate rows, then up rows")
+    return M, two_i // 2, K, _ld(X, "X", torch.bfloat16, M, K), _ld(W13, "W13", torch.bfloat16, two_i, K)
+
+
+def gemm_bf16_glu(X, W13, act: str = "silu", out=None, preact=None, workspace=None, stream=None):
+    """H = f(X Wg^T) * (X Wu^T), the gated block's first half: X bf16 [M, K], W13 bf16
+    [2*inter, K] (gate rows, then up rows), H bf16 [M, inter].  ``preact`` (bf16 [M,
+    2*inter]), where given, receives both projections, which gemm_bf16_glu_backward takes.
+    ``workspace`` may pass at least gemm_bf16_glu_workspace(M, inter, K) bytes."""
+    _one_gpu(X, W13, out, preact, workspace)
+    M, inter, K, ldx, ldw = _glu_sizes(X, W13)
+    code = _act(act)
+    ldh = inter if out is None else _ld(out, "out", torch.bfloat16, M, inter)
+    ldz = 0 if preact is None else _ld(preact, "preact", torch.bfloat16, M, 2 * inter)
+    L = lib()
+
+    def body(st):
+        H = torch.empty((M, inter), dtype=torch.bfloat16, device=X.device) if out is None else out
+        ws, size = _space(workspace, L.gemm_bf16_glu_workspace(M, inter, K), X.device)
+        _check("gemm_bf16_glu", L.gemm_bf16_glu(
+            X.data_ptr(), ldx, W13.data_ptr(), ldw, code, H.data_ptr(), ldh, _ptr(preact), ldz, M, inter, K,
+            _ptr(ws), size, st))
+        return H
+    return _launch(X, stream, body)
+
+
+def gemm_bf16_glu_backward(dout, X, W13, preact, act: str = "silu", need=(True, True), workspace=None,
+                           stream=None):
+    """Gradients of gemm_bf16_glu: (dX bf16 [M, K], dW13 bf16 [2*inter, K]) from dout bf16
+    [M, inter] and the forward call's ``preact``.  ``need`` tells which of the two are
+    computed.  ``workspace`` may pass at least gemm_bf16_glu_backward_workspace(M, inter, K)
+    bytes."""
+    _one_gpu(dout, X, W13, preact, workspace)
+    M, inter, K, ldx, ldw = _glu_sizes(X, W13)
+    ldd = _ld(dout, "dout", torch.bfloat16, M, inter)
+    ldz = _ld(preact, "preact", torch.bfloat16, M, 2 * inter)
+    code = _act(act)
+    need_x, need_w = need
+    L = lib()
+
+    def body(st):
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if need_x else None
+        dW = torch.empty((2 * inter, K), dtype=torch.bfloat16, device=X.device) if need_w else None
+        ws, size = _space(workspace, L.gemm_bf16_glu_backward_workspace(M, inter, K), X.device)
+        _check("gemm_bf16_glu_backward", L.gemm_bf16_glu_backward(
+            dout.data_ptr(), ldd, preact.data_ptr(), ldz, X.data_ptr(), ldx, W13.data_ptr(), ldw, code,
+            _ptr(dX), K, _ptr(dW), K, M, inter, K, _ptr(ws), size, st))
+        return dX, dW
     return _launch(X, stream, body)

@@ -12,13 +12,15 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libbsg.so")
 SOURCES = [os.path.join(HERE, "csrc", "api.hip"), os.path.join(HERE, "csrc", "quant.hip"),
            os.path.join(HERE, "csrc", "mqa.hip"), os.path.join(HERE, "csrc", "route.hip"),
-           os.path.join(HERE, "csrc", "lora.hip")]
+           os.path.join(HERE, "csrc", "lora.hip"), os.path.join(HERE, "csrc", "dense.hip"),
+           os.path.join(HERE, "csrc", "dense_bf16.hip"), os.path.join(HERE, "csrc", "dense_fp8.hip"),
+           os.path.join(HERE, "csrc", "dense_fp4.hip"), os.path.join(HERE, "csrc", "dense_strided.hip")]
 PROBE_LIB = os.path.join(HERE, "libbsg_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "probe.hip")]
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")
-HEADERS = [os.path.join(HERE, "csrc", h) for h in ("gemm_kernel.h", "configs.h", "internal.h",
-                                                       "quant_math.h")] + \
+HEADERS = [os.path.join(HERE, "csrc", h) for h in ("gemm_kernel.h", "gemm_launch.h", "configs.h",
+                                                       "internal.h", "quant_math.h", "act_math.h")] + \
     [os.path.join(ROOT, "include", "bsg.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

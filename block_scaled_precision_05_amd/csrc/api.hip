@@ -9,6 +9,7 @@
 #include "../../include/bsg.h"
 #include "configs.h"
 #include "gemm_kernel.h"
+#include "gemm_launch.h"
 #include "internal.h"
 
 namespace bsg {
@@ -82,85 +83,10 @@ __global__ void unpack_kernel(const int16_t* __restrict__ packed, int64_t mn, in
   }
 }
 
-static int g_num_cus[64];
-
-static int num_cus() {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (g_num_cus[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-      n = 256;
-    g_num_cus[dev] = n;
-  }
-  return g_num_cus[dev];
-}
-
-template <int KIND, int BM, int BN, int WM, int WN, int SB, int NS, int PR, bool GROUPED, int SV = 0,
-          int EPI = 0>
-static int launch(GemmArgs a, hipStream_t stream) {
-  using T = GemmTile<KIND, BM, BN, WM, WN, SB, NS, PR, SV, GROUPED>;
-  a.d_vec = (((uintptr_t)a.D & 15) == 0 && (a.ldd % 8) == 0) ? 2
-            : (((uintptr_t)a.D & 7) == 0 && (a.ldd % 4) == 0) ? 1 : 0;
-  a.tiles_m = (a.M + BM - 1) / BM;
-  a.tiles_n = (a.N + BN - 1) / BN;
-  a.nk = (a.k_bytes + SB - 1) / SB;
-  int grid;
-  if (GROUPED) {
-    grid = num_cus();
-  } else {
-    // As many tiles per workgroup as the CUs require, then as few workgroups as give
-    // every one that many: 448 tiles run as 224 workgroups of two rather than 256 of
-    // one or two.  The idle CUs leave power to the busy ones (1-1.4% faster at
-    // 4096x7168x16384 in an alternating A/B).  A multiple of 8, so a workgroup's later
-    // tiles stay on its XCD (tile i runs on XCD i % 8; see xcd_remap).
-    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    const int64_t cus = num_cus();
-    const int64_t per = (tiles + cus - 1) / cus;
-    int64_t g = (tiles + per - 1) / per;
-    if (per > 1) g = (g + 7) / 8 * 8;
-    grid = (int)(g < cus ? g : cus);
-  }
-  // Leading dead stages of the first round: nk padded up to whole rounds of U
-  // stages, the padding rounded down to an even count (paired stages).  BF16 and FP4
-  // peel it at any size (at K = 16384, 8 of 520 and 2 of 130 stages: 0.7% and 0.4%
-  // faster than the same padding at the end, in an alternating A/B).  FP8 keeps a
-  // padding under 2% of the loop at the end, where it multiplies zeros: its 8-register
-  // fragments leave the peeled round no registers to spare (the dense kernel spills
-  // there, 2% slower at K = 16384).
-  constexpr int U = T::U;
-  int koff = a.nk % U ? (U - a.nk % U) & ~1 : 0;
-  if (KIND == KIND_FP8 && koff * 50 <= a.nk + koff) koff = 0;
-  (void)hipGetLastError();
-  int st = BSG_OK;
-  auto go = [&](auto kc) {
-    constexpr int KO = decltype(kc)::value;
-    if constexpr (KO < U)
-      hipLaunchKernelGGL((gemm_kernel<KIND, BM, BN, WM, WN, SB, NS, PR, GROUPED, SV, KO, EPI>), dim3(grid),
-                         dim3(T::NT), 0, stream, a);
-    else
-      st = BSG_ERR_UNSUPPORTED_SHAPE;   // not reached: koff < U by construction
-  };
-  static_assert(U <= 16, "leading dead stages are instantiated up to 14");
-  switch (koff) {
-    case 0: go(std::integral_constant<int, 0>{}); break;
-    case 2: go(std::integral_constant<int, 2>{}); break;
-    case 4: go(std::integral_constant<int, 4>{}); break;
-    case 6: go(std::integral_constant<int, 6>{}); break;
-    case 8: go(std::integral_constant<int, 8>{}); break;
-    case 10: go(std::integral_constant<int, 10>{}); break;
-    case 12: go(std::integral_constant<int, 12>{}); break;
-    case 14: go(std::integral_constant<int, 14>{}); break;
-    default: return BSG_ERR_UNSUPPORTED_SHAPE;
-  }
-  if (st != BSG_OK) return st;
-  return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
-}
-
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // A packed scale array whose rows of four int16 can be fetched as one 8-byte word.
-static bool sv_ok(const int16_t* sf, int64_t ld) { return ((uintptr_t)sf % 8 == 0) && (ld % 4 == 0); }
+bool sv_ok(const int16_t* sf, int64_t ld) { return ((uintptr_t)sf % 8 == 0) && (ld % 4 == 0); }
 
 // Byte strides must keep 256 rows of offsets inside 31 bits.
 static const int64_t kMaxRowBytes = (int64_t(1) << 31) / 256 - 1;
@@ -168,7 +94,7 @@ static const int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 // Shared checks of the dense entry points.  elem: bytes per stored element of A/B
 // (2 for bf16, 1 for e4m3, 1/2 for e2m1 expressed as k_bytes = K/2).
-static int check_dense(const void* A, int64_t lda, const void* B, int64_t ldb, const void* D,
+int check_dense(const void* A, int64_t lda, const void* B, int64_t ldb, const void* D,
                        int64_t ldd, int64_t M, int64_t N, int64_t K, int64_t kgran, int64_t k_bytes,
                        int64_t elem_bytes) {
   if (M < 0 || N < 0 || K < 0) return BSG_ERR_INVALID_ARG;
@@ -191,7 +117,7 @@ static int check_dense(const void* A, int64_t lda, const void* B, int64_t ldb, c
 // Packed scale arrays of kp = ceil(K / kgran / 2) rows.  The kernels address them
 // with 32-bit byte offsets, up to one packed row past the last (FP4 lane groups on a
 // K tail), so 2 (kp + 1) ld bytes must stay inside 31 bits.
-static int check_scales(const int16_t* sfa, int64_t ld_sfa, int64_t rows_a, const int16_t* sfb,
+int check_scales(const int16_t* sfa, int64_t ld_sfa, int64_t rows_a, const int16_t* sfb,
                         int64_t ld_sfb, int64_t rows_b, int64_t K, int64_t kgran) {
   if (K == 0) return BSG_OK;
   if (!sfa || !sfb) return BSG_ERR_INVALID_ARG;

@@ -35,3 +35,12 @@
 // for 128x256 with four stages (72 KiB in flight).  256-row tiles would multiply
 // mostly empty rows (419 against 340 us).
 #define BSG_MASKED_CFG 128, 256, 1, 4, 64, 6, 1
+
+// Smaller tiles of the dense products with epilogues and of the gradients' products, for
+// calls whose 256x256 tiles would leave CUs idle.  BF16: 128x128 over 2x2 waves of 64x64, a
+// ring of four 16 KiB stages, so that two workgroups share a CU and U = 4 stages make a
+// round (little padding for short parts of a contraction).  FP8: the masked tile (its row
+// permutation needs 128-row waves).  FP4: 128x128 over two waves of 128x64.
+#define BSG_BF16_SMALL_CFG 128, 128, 2, 2, 64, 4, 1
+#define BSG_FP8_SMALL_CFG 128, 256, 1, 4, 64, 6, 1
+#define BSG_FP4_SMALL_CFG 128, 128, 1, 2, 64, 4, 1

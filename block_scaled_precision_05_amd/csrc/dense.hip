@@ -1,0 +1,552 @@
+// dense.hip -- dense products with work in their epilogues (bias, activation, residual; the
+// gated block) and their gradients: entry points, the choice of kernel, and the kernels
+// around the matrix products (see include/bsg.h).
+//
+// The products themselves are instances of gemm_kernel (gemm_kernel.h) with an epilogue
+// that finishes the fp32 accumulators in the kernel, or, for calls with too few tiles to
+// fill the GPU, write fp32 sums of parts of the contraction that join_kernel finishes.
+//
+// Gradients.  dz = dD f'(z) is formed once, in one pass over dD and Z (and W in the gated
+// form), rounded to bf16 for the matrix cores and read by two products: dA = dz B and
+// dB = dz^T A.  Their contractions run over the rows of B, and of dz and A: neither
+// operand is transposed in memory; the kernel copies rows as they lie and transposes when
+// it reads them from LDS.  The bias's gradient is summed from the unrounded dz in the same
+// pass, in an order fixed by the sizes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/bsg.h"
+#include "act_math.h"
+#include "gemm_kernel.h"
+#include "internal.h"
+
+namespace bsg {
+
+static const int64_t kMaxTiles = int64_t(1) << 24;
+static const int64_t kMaxRow = (int64_t(1) << 31) / 256 - 1;   // bytes of a row (32-bit offsets)
+static const int64_t kMaxRows = (int64_t(1) << 30) - 1;
+
+DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K) {
+  const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
+  if (big >= 192 || K == 0) return {DENSE_BIG, 1};
+  const int64_t bn = kind == KIND_FP8 ? 256 : 128, cap = kind == KIND_FP8 ? 256 : 512, U = kind == KIND_FP8 ? 6 : 4;
+  const int64_t tiles = (M + 127) / 128 * ((N + bn - 1) / bn);
+  const int64_t bytes = kind == KIND_BF16 ? 2 * K : (kind == KIND_FP8 ? K : K / 2);
+  const int64_t stages = (bytes + 63) / 64;
+  int64_t s = tiles > 0 ? cap / tiles : 1;
+  if (s > stages / (4 * U)) s = stages / (4 * U);
+  if (s <= 1) return {DENSE_SMALL, 1};
+  const int64_t per = ((stages + s - 1) / s + U - 1) / U * U;
+  s = (stages + per - 1) / per;
+  return s > 1 ? DensePlan{DENSE_PART, (int)s} : DensePlan{DENSE_SMALL, 1};
+}
+
+// Joins the parts of a split contraction: one thread finishes eight consecutive columns of
+// a row, 32 bytes of each part.  Bound by the parts' bytes, which mostly come from L2 and
+// the cache behind it, where the product has just written them.
+template <bool GLU>
+__global__ __launch_bounds__(256) void join_kernel(const GemmArgs args) {
+  typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+  const int cols = GLU ? args.inter : args.N, per = (cols + 7) / 8;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = idx / per;
+  const int n = 8 * (int)(idx - m * per);
+  if (m >= args.M) return;
+  const float* p = args.P + m * args.ldp + n;
+  auto sum = [&](const float* q, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    for (int s = 0; s < args.splits; ++s, q += args.part_stride) {
+      const f32x4_t lo = *(const f32x4_t*)q, hi = *(const f32x4_t*)(q + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+  };
+  const int cnt = cols - n < 8 ? cols - n : 8;
+  const bool vec = args.e_vec && cnt == 8;
+  float z[8];
+  sum(p, z);
+  uint16_t* const Z = args.Z ? args.Z + m * args.ldz + n : nullptr;
+  uint16_t* const D = args.D + m * args.ldd + n;
+  if constexpr (GLU) {
+    float u[8];
+    sum(p + args.inter, u);
+    glu_row8(args.act, z, u, Z, args.inter, D, vec);
+  } else {
+    const uint16_t* const R = args.R ? args.R + m * args.ldr + n : nullptr;
+    am_i32x4_t r16 = {0, 0, 0, 0};
+    if (R && vec) r16 = *(const am_i32x4_t*)R;
+    if (args.bias)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < cnt) z[e] += bf16_f32(args.bias[n + e]);
+    act_row8(args.act, z, Z, R, r16, D, vec, cnt);
+  }
+}
+
+static int launched() { return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP; }
+
+int dense_join(const GemmArgs& a, bool glu, void* stream) {
+  const int64_t per = ((glu ? a.inter : a.N) + 7) / 8, blocks = (a.M * per + 255) / 256;
+  if (blocks == 0) return BSG_OK;
+  (void)hipGetLastError();
+  if (glu)
+    hipLaunchKernelGGL(join_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+  else
+    hipLaunchKernelGGL(join_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+  return launched();
+}
+
+// dz of a block of 256 columns x 64 rows: thread (x, y) takes columns 8x .. 8x+7 of rows y,
+// y + 8, ...  Bound by memory: dD and Z read, dz written, each once.  The columns' sums
+// of dz stay in registers over the rows, then meet in LDS, one partial row a block.
+//   GLU: columns are those of H; dz gets dg there and du inter columns further on.
+//   ldq: leading dimension of dz, a multiple of 8; columns N .. ldq-1 are zeroed (the
+//   products read whole 16-byte chunks).  dz or part may be null.
+constexpr int DZ_ROWS = 64;
+template <bool GLU>
+__global__ __launch_bounds__(256) void dz_kernel(const uint16_t* __restrict__ dD, int64_t lddd,
+                                                 const uint16_t* __restrict__ Z, int64_t ldz, uint16_t* __restrict__ dz,
+                                                 int64_t ldq, float* __restrict__ part, int64_t M, int64_t N, int act,
+                                                 int vec) {
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t per = (N + 255) / 256, by = blockIdx.x / per, bx = blockIdx.x - by * per;
+  const int64_t n = bx * 256 + 8 * x, m0 = by * DZ_ROWS;
+  const int cnt = N - n >= 8 ? 8 : (N > n ? (int)(N - n) : 0);
+  const bool v16 = vec && cnt == 8;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  auto load = [&](const uint16_t* p, float (&v)[8]) {
+    if (v16) {
+      unpack8(*(const am_i32x4_t*)p, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < cnt ? bf16_f32(p[e]) : 0.0f;
+    }
+  };
+  if (n < ldq && cnt > 0) {
+    for (int64_t m = m0 + y; m < m0 + DZ_ROWS && m < M; m += 8) {
+      float d[8], z[8], w[8];
+      load(dD + m * lddd + n, d);
+      if (act != BSG_ACT_NONE || GLU) load(Z + m * ldz + n, z);
+      if constexpr (GLU) load(Z + m * ldz + N + n, w);
+      with_act(act, [&](auto a) {
+        constexpr int A = decltype(a)::value;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (GLU) {
+            float f;
+            const float df = act_df<A>(z[e], f);
+            z[e] = d[e] * w[e] * df;
+            w[e] = d[e] * f;
+          } else {
+            float f;
+            // (relu: a select, so that an infinite dD meets no 0 * inf)
+            if constexpr (A == BSG_ACT_NONE) z[e] = d[e];
+            else if constexpr (A == BSG_ACT_RELU) z[e] = z[e] <= 0.0f ? 0.0f : d[e];
+            else z[e] = d[e] * act_df<A>(z[e], f);
+          }
+        }
+      });
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e >= cnt) z[e] = 0.0f;
+        sum[e] += z[e];
+      }
+      if (dz) *(am_i32x4_t*)(dz + m * ldq + n) = pack8(z);
+      if constexpr (GLU) *(am_i32x4_t*)(dz + m * ldq + N + n) = pack8(w);
+    }
+  }
+  if constexpr (!GLU) {
+    if (!part) return;
+    __shared__ float s[8][256];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[y][8 * x + e] = sum[e];
+    __syncthreads();
+    const int64_t c = bx * 256 + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += s[k][threadIdx.x];
+    if (c < N) part[by * N + c] = t;
+  }
+}
+
+// dbias from the blocks' partial rows: a block sums 32 columns, eight rows at a time.
+__global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int64_t rows, int64_t N,
+                                                    float* __restrict__ dbias) {
+  __shared__ float s[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * 32 + x;
+  float t = 0.0f;
+  if (n < N)
+    for (int64_t r = y; r < rows; r += 8) t += part[r * N + n];
+  s[y][x] = t;
+  __syncthreads();
+  if (y == 0 && n < N) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t += s[k][x];
+    dbias[n] = t;
+  }
+}
+
+static bool al16(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
+
+static bool bad_act(int32_t act) { return act < BSG_ACT_NONE || act > BSG_ACT_GELU_TANH; }
+
+// A row-major bf16 operand without alignment of its own: null, leading dimension, 2 bytes.
+static int check_rows(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  if (rows == 0 || cols == 0) return BSG_OK;
+  if (!p || ld < cols) return BSG_ERR_INVALID_ARG;
+  if ((uintptr_t)p & 1) return BSG_ERR_MISALIGNED;
+  return ld > kMaxRows ? BSG_ERR_UNSUPPORTED_SHAPE : BSG_OK;
+}
+
+// An operand of a product: 16-byte aligned rows, 32-bit row offsets.
+static int check_operand(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  if (rows == 0 || cols == 0) return BSG_OK;
+  if (!p || ld < cols) return BSG_ERR_INVALID_ARG;
+  if (2 * ld > kMaxRow) return BSG_ERR_UNSUPPORTED_SHAPE;
+  return al16(p, ld) ? BSG_OK : BSG_ERR_MISALIGNED;
+}
+
+static int check_tiles(int64_t M, int64_t N) {
+  return (M + 127) / 128 * ((N + 127) / 128) >= kMaxTiles ? BSG_ERR_UNSUPPORTED_SHAPE : BSG_OK;
+}
+
+static int check_workspace(const void* ws, int64_t bytes, int64_t need) {
+  if (need == 0) return BSG_OK;
+  if (!ws || bytes < need) return BSG_ERR_INVALID_ARG;
+  return ((uintptr_t)ws & 15) ? BSG_ERR_MISALIGNED : BSG_OK;
+}
+
+// Epilogue operands of an act call; sets the fields of a.
+static int act_args(GemmArgs& a, int kind, const void* bias, int32_t act, const void* R, int64_t ldr, void* D,
+                    int64_t ldd, void* Z, int64_t ldz, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes,
+                    DensePlan& plan) {
+  if (bad_act(act)) return BSG_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return BSG_OK;
+  if ((uintptr_t)bias & 1) return BSG_ERR_MISALIGNED;
+  int st = R ? check_rows(R, ldr, M, N) : BSG_OK;
+  if (st == BSG_OK && Z) st = check_rows(Z, ldz, M, N);
+  if (st == BSG_OK) st = check_tiles(M, N);
+  if (st != BSG_OK) return st;
+  plan = dense_plan(kind, M, N, K);
+  st = check_workspace(ws, ws_bytes, dense_part_bytes(plan, M, N));
+  if (st != BSG_OK) return st;
+  a.D = (uint16_t*)D;
+  a.ldd = ldd;
+  a.M = (int32_t)M;
+  a.N = (int32_t)N;
+  a.K = (int32_t)K;
+  a.act = act;
+  a.bias = (const uint16_t*)bias;
+  a.R = (const uint16_t*)R;
+  a.Z = (uint16_t*)Z;
+  a.ldr = R ? ldr : 0;
+  a.ldz = Z ? ldz : 0;
+  a.P = (float*)ws;
+  a.ldp = dense_ldp(N);
+  a.part_stride = M * a.ldp;
+  a.splits = plan.splits;
+  a.e_vec = al16(D, ldd) && (!R || al16(R, ldr)) && (!Z || al16(Z, ldz));
+  return BSG_OK;
+}
+
+}  // namespace bsg
+
+using namespace bsg;
+
+extern "C" {
+
+int64_t gemm_bf16_act_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K < 0) return 0;
+  return dense_part_bytes(dense_plan(KIND_BF16, M, N, K), M, N);
+}
+int64_t gemm_fp8_act_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K < 0) return 0;
+  return dense_part_bytes(dense_plan(KIND_FP8, M, N, K), M, N);
+}
+int64_t gemm_fp4_act_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K < 0) return 0;
+  return dense_part_bytes(dense_plan(KIND_FP4, M, N, K), M, N);
+}
+int64_t gemm_bf16_glu_workspace(int64_t M, int64_t inter, int64_t K) {
+  return gemm_bf16_act_workspace(M, 2 * inter, K);
+}
+
+int gemm_bf16_act(const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias, int32_t act,
+                  const void* R, int64_t ldr, void* D, int64_t ldd, void* Z, int64_t ldz, int64_t M, int64_t N,
+                  int64_t K, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = check_dense(A, lda, B, ldb, D, ldd, M, N, K, 8, 2 * K, 2);
+  if (st != BSG_OK) return st;
+  GemmArgs a = {};
+  DensePlan plan = {};
+  st = act_args(a, KIND_BF16, bias, act, R, ldr, D, ldd, Z, ldz, M, N, K, workspace, workspace_bytes, plan);
+  if (st != BSG_OK || M == 0 || N == 0) return st;
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.lda = K ? lda * 2 : 0;
+  a.ldb = K ? ldb * 2 : 0;
+  a.k_bytes = (int32_t)(2 * K);
+  st = dense_bf16(a, plan.form, EPI_ACT, stream);
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+}
+
+int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
+                 const int16_t* sfb, int64_t ld_sfb, int32_t sfb_gran_mn, const void* bias, int32_t act,
+                 const void* R, int64_t ldr, void* D, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                 void* workspace, int64_t workspace_bytes, void* stream) {
+  if (sfb_gran_mn != 128 && sfb_gran_mn != 1) return BSG_ERR_UNSUPPORTED_SHAPE;
+  int st = check_dense(A, lda, B, ldb, D, ldd, M, N, K, 128, K, 1);
+  if (st != BSG_OK) return st;
+  const int64_t sfb_rows = (N + sfb_gran_mn - 1) / sfb_gran_mn;
+  if (M > 0 && N > 0) st = check_scales(sfa, ld_sfa, M, sfb, ld_sfb, sfb_rows, K, 128);
+  if (st != BSG_OK) return st;
+  GemmArgs a = {};
+  DensePlan plan = {};
+  st = act_args(a, KIND_FP8, bias, act, R, ldr, D, ldd, nullptr, 0, M, N, K, workspace, workspace_bytes, plan);
+  if (st != BSG_OK || M == 0 || N == 0) return st;
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.sfa = sfa;
+  a.sfb = sfb;
+  a.lda = K ? lda : 0;
+  a.ldb = K ? ldb : 0;
+  a.ld_sfa = K ? ld_sfa : 0;
+  a.ld_sfb = K ? ld_sfb : 0;
+  a.k_bytes = (int32_t)K;
+  a.kp_count = (int32_t)((K / 128 + 1) / 2);
+  a.sfb_rows = (int32_t)sfb_rows;
+  st = dense_fp8(a, plan.form, (K && sv_ok(sfa, ld_sfa) ? 1 : 0) + (sfb_gran_mn == 1 ? 2 : 0), stream);
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+}
+
+int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
+                 const int16_t* sfb, int64_t ld_sfb, const void* bias, int32_t act, const void* R, int64_t ldr,
+                 void* D, int64_t ldd, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                 void* stream) {
+  int st = check_dense(A, lda, B, ldb, D, ldd, M, N, K, 32, K / 2, 1);
+  if (st != BSG_OK) return st;
+  if (M > 0 && N > 0) st = check_scales(sfa, ld_sfa, M, sfb, ld_sfb, N, K, 32);
+  if (st != BSG_OK) return st;
+  GemmArgs a = {};
+  DensePlan plan = {};
+  st = act_args(a, KIND_FP4, bias, act, R, ldr, D, ldd, nullptr, 0, M, N, K, workspace, workspace_bytes, plan);
+  if (st != BSG_OK || M == 0 || N == 0) return st;
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.sfa = sfa;
+  a.sfb = sfb;
+  a.lda = K ? lda : 0;
+  a.ldb = K ? ldb : 0;
+  a.ld_sfa = K ? ld_sfa : 0;
+  a.ld_sfb = K ? ld_sfb : 0;
+  a.k_bytes = (int32_t)(K / 2);
+  a.kp_count = (int32_t)((K / 32 + 1) / 2);
+  a.sfb_rows = (int32_t)N;
+  st = dense_fp4(a, plan.form, K && sv_ok(sfa, ld_sfa) && sv_ok(sfb, ld_sfb) ? 1 : 0, stream);
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+}
+
+int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int32_t act, void* H, int64_t ldh,
+                  void* Z, int64_t ldz, int64_t M, int64_t inter, int64_t K, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+  if (inter < 0 || inter > kMaxRows) return inter < 0 ? BSG_ERR_INVALID_ARG : BSG_ERR_UNSUPPORTED_SHAPE;
+  if (inter % 8) return BSG_ERR_UNSUPPORTED_SHAPE;
+  // (ldh holds inter columns: checked below)
+  int st = check_dense(X, ldx, W13, ldw, H, ldh < inter ? ldh : 2 * inter, M, 2 * inter, K, 8, 2 * K, 2);
+  if (st != BSG_OK) return st;
+  if (bad_act(act)) return BSG_ERR_INVALID_ARG;
+  if (M == 0 || inter == 0) return BSG_OK;
+  st = check_rows(H, ldh, M, inter);
+  if (st == BSG_OK && Z) st = check_rows(Z, ldz, M, 2 * inter);
+  if (st == BSG_OK) st = check_tiles(M, 2 * inter);
+  if (st != BSG_OK) return st;
+  const DensePlan plan = dense_plan(KIND_BF16, M, 2 * inter, K);
+  st = check_workspace(workspace, workspace_bytes, dense_part_bytes(plan, M, 2 * inter));
+  if (st != BSG_OK) return st;
+  GemmArgs a = {};
+  a.A = (const uint8_t*)X;
+  a.B = (const uint8_t*)W13;
+  a.D = (uint16_t*)H;
+  a.Z = (uint16_t*)Z;
+  a.lda = K ? ldx * 2 : 0;
+  a.ldb = K ? ldw * 2 : 0;
+  a.ldd = ldh;
+  a.ldz = Z ? ldz : 0;
+  a.M = (int32_t)M;
+  a.N = (int32_t)(2 * inter);
+  a.K = (int32_t)K;
+  a.k_bytes = (int32_t)(2 * K);
+  a.inter = (int32_t)inter;
+  a.act = act;
+  a.P = (float*)workspace;
+  a.ldp = dense_ldp(2 * inter);
+  a.part_stride = M * a.ldp;
+  a.splits = plan.splits;
+  a.e_vec = al16(H, ldh) && (!Z || al16(Z, ldz));
+  st = dense_bf16(a, plan.form, EPI_GLU, stream);
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, true, stream) : st;
+}
+
+}  // extern "C"
+
+namespace bsg {
+
+// D [M][N] = (A's rows or columns) x (B's columns), K long: tr 2 contracts B's rows with
+// A's columns, tr 3 the rows of both; operands bf16 with leading dimensions in elements.
+static int strided(int tr, const void* A, int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, int64_t M,
+                   int64_t N, int64_t K, void* ws, void* stream) {
+  if (M == 0 || N == 0) return BSG_OK;
+  const DensePlan plan = dense_plan(KIND_BF16, M, N, K);
+  GemmArgs a = {};
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.D = (uint16_t*)D;
+  a.lda = K ? lda * 2 : 0;
+  a.ldb = K ? ldb * 2 : 0;
+  a.ldd = ldd;
+  a.M = (int32_t)M;
+  a.N = (int32_t)N;
+  a.K = (int32_t)K;
+  // (a row of A holds whole 16-byte chunks: its columns past K are zeros, and rows of B
+  // past K read zero)
+  a.k_bytes = (int32_t)(2 * ((K + 7) / 8 * 8));
+  a.P = (float*)ws;
+  a.ldp = dense_ldp(N);
+  a.part_stride = M * a.ldp;
+  a.splits = plan.splits;
+  a.e_vec = al16(D, ldd);
+  const int st = dense_strided(a, plan.form, tr, stream);
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+}
+
+static int64_t strided_bytes(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && N > 0 ? dense_part_bytes(dense_plan(KIND_BF16, M, N, K), M, N) : 0;
+}
+
+static int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
+
+// Workspace of a backward pass: dz [M][ldq], the bias's partial rows, the larger of the two
+// products' parts (they run one after the other).
+struct GradSpace {
+  int64_t ldq, part_at, sums_at, bytes;
+  GradSpace(int64_t M, int64_t cols, int64_t K, bool bias) {
+    ldq = (cols + 7) / 8 * 8;
+    part_at = 2 * M * ldq;
+    sums_at = part_at + (bias ? up16(4 * ((M + DZ_ROWS - 1) / DZ_ROWS) * cols) : 0);
+    const int64_t p = strided_bytes(M, K, cols), q = strided_bytes(cols, K, M);
+    bytes = sums_at + (p > q ? p : q);
+  }
+};
+
+// Both products of a backward pass from dz [M][ldq].
+static int grad_products(const void* dz, int64_t ldq, const void* A, int64_t lda, const void* B, int64_t ldb,
+                         void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N, int64_t K, void* ws,
+                         void* stream) {
+  int st = dA ? strided(2, dz, ldq, B, ldb, dA, ldda, M, K, N, ws, stream) : BSG_OK;
+  if (st == BSG_OK && dB) st = strided(3, dz, ldq, A, lda, dB, lddb, N, K, M, ws, stream);
+  return st;
+}
+
+static int check_grad(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return BSG_ERR_INVALID_ARG;
+  if (K % 8 || M > kMaxRows || 2 * (N + 7) > kMaxRow || 2 * K > kMaxRow) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if ((M + DZ_ROWS - 1) / DZ_ROWS * ((N + 255) / 256) >= kMaxTiles) return BSG_ERR_UNSUPPORTED_SHAPE;
+  int st = check_tiles(M, N);
+  if (st == BSG_OK) st = check_tiles(M, K);
+  return st == BSG_OK ? check_tiles(N, K) : st;
+}
+
+}  // namespace bsg
+
+extern "C" {
+
+int64_t gemm_bf16_act_backward_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return 0;
+  return GradSpace(M, N, K, true).bytes;
+}
+int64_t gemm_bf16_glu_backward_workspace(int64_t M, int64_t inter, int64_t K) {
+  if (M < 0 || inter < 0 || K < 0) return 0;
+  return GradSpace(M, 2 * inter, K, false).bytes;
+}
+
+int gemm_bf16_act_backward(const void* dD, int64_t lddd, const void* Z, int64_t ldz, const void* A, int64_t lda,
+                           const void* B, int64_t ldb, int32_t act, void* dA, int64_t ldda, void* dB, int64_t lddb,
+                           float* dbias, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  if (bad_act(act)) return BSG_ERR_INVALID_ARG;
+  int st = check_grad(M, N, K);
+  if (st == BSG_OK) st = check_rows(dD, lddd, M, N);
+  if (st == BSG_OK && act != BSG_ACT_NONE) st = check_rows(Z, ldz, M, N);
+  if (st == BSG_OK && dA) st = check_rows(dA, ldda, M, K);
+  if (st == BSG_OK && dB) st = check_rows(dB, lddb, N, K);
+  if (st == BSG_OK && dA && M > 0) st = check_operand(B, ldb, N, K);
+  if (st == BSG_OK && dB && N > 0) st = check_operand(A, lda, M, K);
+  if (st == BSG_OK && ((uintptr_t)dbias & 3)) st = BSG_ERR_MISALIGNED;
+  if (st != BSG_OK) return st;
+  const GradSpace w(M, N, K, true);
+  st = check_workspace(workspace, workspace_bytes, w.bytes);
+  if (st != BSG_OK) return st;
+  uint8_t* const ws = (uint8_t*)workspace;
+  // without an activation an aligned dD is dz itself
+  const bool own = act == BSG_ACT_NONE && al16(dD, lddd) && N % 8 == 0 && 2 * lddd <= kMaxRow;
+  const void* const dz = own ? dD : ws;
+  const int64_t ldq = own ? lddd : w.ldq, blocks = (M + DZ_ROWS - 1) / DZ_ROWS;
+  float* const part = (float*)(ws + w.part_at);
+  const bool products = dA || dB;
+  (void)hipGetLastError();
+  if (M > 0 && N > 0 && (dbias || (products && !own))) {
+    const int vec = al16(dD, lddd) && (act == BSG_ACT_NONE || al16(Z, ldz));
+    hipLaunchKernelGGL(dz_kernel<false>, dim3((unsigned)((N + 255) / 256 * blocks)), dim3(256), 0,
+                       (hipStream_t)stream, (const uint16_t*)dD, lddd, (const uint16_t*)Z, ldz,
+                       products && !own ? (uint16_t*)ws : nullptr, w.ldq, dbias ? part : nullptr, M, N, act, vec);
+    st = launched();
+    if (st != BSG_OK) return st;
+  }
+  if (dbias && N > 0) {
+    hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, (hipStream_t)stream, part, blocks,
+                       N, dbias);
+    st = launched();
+    if (st != BSG_OK) return st;
+  }
+  return K > 0 ? grad_products(dz, ldq, A, lda, B, ldb, dA, ldda, dB, lddb, M, N, K, ws + w.sums_at, stream) : BSG_OK;
+}
+
+int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t ldz, const void* X, int64_t ldx,
+                           const void* W13, int64_t ldw, int32_t act, void* dX, int64_t lddx, void* dW13,
+                           int64_t lddw, int64_t M, int64_t inter, int64_t K, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  if (bad_act(act)) return BSG_ERR_INVALID_ARG;
+  if (inter < 0) return BSG_ERR_INVALID_ARG;
+  if (inter % 8 || inter > kMaxRows) return BSG_ERR_UNSUPPORTED_SHAPE;
+  const int64_t N = 2 * inter;
+  int st = check_grad(M, N, K);
+  if (st == BSG_OK) st = check_rows(dH, lddh, M, inter);
+  if (st == BSG_OK) st = check_rows(Z, ldz, M, N);
+  if (st == BSG_OK && dX) st = check_rows(dX, lddx, M, K);
+  if (st == BSG_OK && dW13) st = check_rows(dW13, lddw, N, K);
+  if (st == BSG_OK && dX && M > 0) st = check_operand(W13, ldw, N, K);
+  if (st == BSG_OK && dW13 && N > 0) st = check_operand(X, ldx, M, K);
+  if (st != BSG_OK) return st;
+  const GradSpace w(M, N, K, false);
+  st = check_workspace(workspace, workspace_bytes, w.bytes);
+  if (st != BSG_OK || K == 0 || (!dX && !dW13)) return st;
+  uint8_t* const ws = (uint8_t*)workspace;
+  if (M > 0 && inter > 0) {
+    (void)hipGetLastError();
+    const int vec = al16(dH, lddh) && al16(Z, ldz);
+    hipLaunchKernelGGL(dz_kernel<true>, dim3((unsigned)((inter + 255) / 256 * ((M + DZ_ROWS - 1) / DZ_ROWS))),
+                       dim3(256), 0, (hipStream_t)stream, (const uint16_t*)dH, lddh, (const uint16_t*)Z, ldz,
+                       (uint16_t*)ws, w.ldq, nullptr, M, inter, act, vec);
+    st = launched();
+    if (st != BSG_OK) return st;
+  }
+  return grad_products(ws, w.ldq, X, ldx, W13, ldw, dX, lddx, dW13, lddw, M, N, K, ws + w.sums_at, stream);
+}
+
+}  // extern "C"

@@ -43,6 +43,7 @@
 
 #include <type_traits>
 
+#include "act_math.h"
 #include "quant_math.h"
 #include <utility>
 
@@ -95,7 +96,31 @@ struct GemmArgs {
   int64_t ldy;
   int64_t ld_sfy;
   int32_t inter;
+  // Epilogues of the dense products with bias, activation and residual, of the gated
+  // block, and of a split contraction (EPI_ACT, EPI_GLU, EPI_PART below).
+  int32_t act;              // bsg_activation
+  const uint16_t* bias;     // bf16 [N], or null
+  const uint16_t* R;        // residual bf16 [M][ldr], or null (may be D)
+  uint16_t* Z;              // pre-activation bf16 [M][ldz] (EPI_GLU: gate, then up), or null
+  float* P;                 // EPI_PART: fp32 [splits][M][ldp], part_stride elements apart
+  int64_t ldr;
+  int64_t ldz;
+  int64_t ldp;              // a multiple of 8
+  int64_t part_stride;
+  int32_t splits;           // EPI_PART: parts of the contraction, nk stages each (the last
+                            // may be shorter)
+  int32_t e_vec;            // D, R and Z (where given) take 16-byte accesses
 };
+
+// What a kernel instance does with its accumulators, and how its operands lie (EPI):
+//   0            D = bf16(acc)
+//   1 + rule     SwiGLU and FP8 1x128 requantisation (grouped FP8)
+//   EPI_ACT      D = R + f(acc + bias), optionally Z = acc + bias
+//   EPI_GLU      D = f(gate) * up: B holds gate rows [0, inter), then up rows
+//   EPI_PART     the fp32 sums of one part of the contraction
+//   + EPI_TRA    A is stored [K][lda], M contiguous (the contraction strides)
+//   + EPI_TRB    B is stored [K][ldb], N contiguous
+constexpr int EPI_ACT = 3, EPI_GLU = 4, EPI_PART = 5, EPI_TRA = 8, EPI_TRB = 16;
 
 // Buffer resource word 3 for raw (unswizzled, stride 0) byte-addressed buffers on
 // gfx9-family GPUs; out-of-range loads return zero.
@@ -111,12 +136,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
   const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
   return __builtin_amdgcn_make_buffer_rsrc((void*)(lo | (hi << 32)), (short)0,
                                            __builtin_amdgcn_readfirstlane((int)bytes), kRsrcWord3);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __bf16 a = (__bf16)lo;   // v_cvt_pk_bf16_f32: round to nearest even
-  __bf16 b = (__bf16)hi;
-  return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
 
 // Scaled MFMA (32x32x64, fp32 accumulate).  FMT 0 = e4m3, 4 = e2m1; the scale byte
@@ -185,6 +204,7 @@ struct GemmTile {
   // issues the same number of copies and the vmcnt arithmetic holds for all of them.
   static constexpr bool DUMMY = A_LOADS * NWC != A_COPIES || B_LOADS * NWC != B_COPIES;
   static constexpr int LDS_BYTES = NS * STAGE_BYTES + (DUMMY ? 1024 : 0);
+  static constexpr int WGS = LDS_BYTES <= 81920 ? 2 : 1;   // workgroups that share a CU
   // Epilogue staging: each wave's TM x TN bf16 block, row-major (EPI_ROW bytes a
   // row) in the ring's LDS; 16-byte chunk c of row r sits at chunk c ^ epi_swz(r),
   // which walks the chunks along the rows that one lane-row group writes at once
@@ -510,17 +530,142 @@ __device__ __forceinline__ void ring_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Epilogue of the dense products (EPI_ACT, EPI_GLU, EPI_PART): one wave's TM x 64 block of
+// fp32 accumulators.  The block goes through the wave's part of the idle LDS ring as fp32,
+// half of its rows at a time (what the bf16 epilogue takes for all of them), so that a lane
+// reads back eight consecutive columns of a row: rows of bias, residual, Z and D are then
+// accessed 16 bytes a lane, and the activation is one rolled loop for every kind of
+// fragment instead of code unrolled over all accumulators.  Staged row s is 256 bytes, its
+// 16-byte chunk c at c ^ (s & 15): the 16 rows one staging store touches lie in different
+// banks.
+//   row0: the block's first row of D, rows_w of them exist; n_base: its first column of D.
+template <class T, int FM, int FN, int E>
+__device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&acc)[FM][FN], uint8_t* stg, int el,
+                                               int row0, int rows_w, int n_base, int n_end, int part) {
+  typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+  constexpr bool GLU = E == EPI_GLU, PART = E == EPI_PART;
+  constexpr int HF = FM / 2, HR = 32 * HF;              // fragments and rows of a half
+  constexpr int LPR = GLU ? T::TN / 16 : T::TN / 8;     // lanes a row, eight outputs each
+  constexpr int RPI = 64 / LPR, IT = HR / RPI;
+  const int el32 = el & 31, elg = el >> 5;
+  const int rr = el / LPR, seg = el % LPR;
+  const int n = n_base + 8 * seg;
+  const bool vec = args.e_vec && n + 8 <= n_end;
+  float b8[8];
+  if constexpr (E == EPI_ACT) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      b8[e] = args.bias && n + e < n_end ? bf16_f32(args.bias[n + e]) : 0.0f;
+  }
+  auto real_row = [&](int half, int s) { return T::PERM_A ? 4 * (s & 31) + half * HF + (s >> 5) : half * HR + s; };
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    // the residual's rows, two iterations ahead of their use
+    auto load_r = [&](int it) {
+      i32x4_t v = {0, 0, 0, 0};
+      if constexpr (E == EPI_ACT) {
+        const int row = real_row(half, it * RPI + rr);
+        if (args.R && vec && it < IT && row < rows_w)
+          v = *(const i32x4_t*)(args.R + (int64_t)(row0 + row) * args.ldr + n);
+      }
+      return v;
+    };
+    i32x4_t r0 = load_r(0), r1 = load_r(1);
+#pragma unroll
+    for (int a = 0; a < HF; ++a) {
+      const int s = 32 * a + el32;
+      uint8_t* const line = stg + 256 * s;
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int fa = half * HF + a;
+          if constexpr (T::PERM) {
+            // column 2*(8q + 4*elg + r) + b is register 4q + r of fragment b; chunk b of
+            // the pair holds r = 2b and 2b + 1
+            const f32x4_t v = {acc[fa][0][4 * q + 2 * b], acc[fa][1][4 * q + 2 * b], acc[fa][0][4 * q + 2 * b + 1],
+                               acc[fa][1][4 * q + 2 * b + 1]};
+            *(f32x4_t*)(line + 16 * ((4 * q + 2 * elg + b) ^ (s & 15))) = v;
+          } else {
+            const f32x4_t v = {acc[fa][b][4 * q], acc[fa][b][4 * q + 1], acc[fa][b][4 * q + 2], acc[fa][b][4 * q + 3]};
+            *(f32x4_t*)(line + 16 * ((8 * b + 2 * q + elg) ^ (s & 15))) = v;
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (a wave reads back only what it wrote; its LDS accesses execute in order)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll 1
+    for (int it = 0; it < IT; ++it) {
+      const int s = it * RPI + rr, row = real_row(half, s);
+      const i32x4_t r2 = load_r(it + 2);
+      auto read8 = [&](int chunk, float (&v)[8]) {
+        const f32x4_t lo = *(const f32x4_t*)(stg + 256 * s + 16 * (chunk ^ (s & 15)));
+        const f32x4_t hi = *(const f32x4_t*)(stg + 256 * s + 16 * ((chunk + 1) ^ (s & 15)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = lo[e];
+          v[4 + e] = hi[e];
+        }
+      };
+      float z[8];
+      read8(2 * seg, z);
+      if (row < rows_w && n < n_end) {
+        const int64_t m = row0 + row;
+        if constexpr (PART) {
+          // (P's rows are padded to a multiple of 8 columns)
+          float* const d = args.P + (int64_t)part * args.part_stride + m * args.ldp + n;
+          *(f32x4_t*)d = (f32x4_t){z[0], z[1], z[2], z[3]};
+          *(f32x4_t*)(d + 4) = (f32x4_t){z[4], z[5], z[6], z[7]};
+        } else if constexpr (GLU) {
+          float u[8];
+          read8(8 + 2 * seg, u);
+          // (inter is a multiple of 8: eight gate columns always exist together)
+          glu_row8(args.act, z, u, args.Z ? args.Z + m * args.ldz + n : nullptr, args.inter,
+                   args.D + m * args.ldd + n, vec);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] += b8[e];
+          act_row8(args.act, z, args.Z ? args.Z + m * args.ldz + n : nullptr,
+                   args.R ? args.R + m * args.ldr + n : nullptr, r0, args.D + m * args.ldd + n, vec,
+                   n_end - n < 8 ? n_end - n : 8);
+        }
+      }
+      r0 = r1;
+      r1 = r2;
+    }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  }
+}
+
 template <int KIND, int BM, int BN, int WM, int WN, int SB, int NS, int PR, bool GROUPED, int SV = 0,
           int KOFF = 0, int EPI = 0>
 __global__ __launch_bounds__(WM* WN * 64)
-__attribute__((amdgpu_waves_per_eu((WM * WN + 3) / 4, (WM * WN + 3) / 4)))
+__attribute__((amdgpu_waves_per_eu(
+    (GemmTile<KIND, BM, BN, WM, WN, SB, NS, PR, SV, GROUPED>::WGS * WM * WN + 3) / 4,
+    (GemmTile<KIND, BM, BN, WM, WN, SB, NS, PR, SV, GROUPED>::WGS * WM * WN + 3) / 4)))
 void gemm_kernel(const GemmArgs args) {
   using T = GemmTile<KIND, BM, BN, WM, WN, SB, NS, PR, SV, GROUPED>;
   constexpr int FM = T::FM, FN = T::FN, J = T::J, RPF = T::RPF, NC = T::NC, SW = T::SW;
-  // EPI: 0 = bf16 D; 1 + rule = SwiGLU and FP8 1x128 requantisation (rule CEIL / OCP_MX)
-  static_assert(EPI == 0 || (KIND == KIND_FP8 && GROUPED && !T::PERM_B && T::ONE_B_SCALE &&
+  // LDS reads of a k-step's fragments (transposing reads fetch 8 bytes a lane)
+  constexpr int NDS = FM * (EPI & EPI_TRA ? 2 : RPF) + FN * (EPI & EPI_TRB ? 2 : RPF);
+  constexpr int E = EPI & 7;
+  constexpr bool QSW = E == 1 || E == 2;   // SwiGLU and requantisation
+  constexpr bool GLU = E == EPI_GLU, PART = E == EPI_PART;
+  constexpr bool TRA = (EPI & EPI_TRA) != 0, TRB = (EPI & EPI_TRB) != 0;
+  static_assert(!QSW || (KIND == KIND_FP8 && GROUPED && !T::PERM_B && T::ONE_B_SCALE &&
                              (BN / 2) % (T::NWC * T::ROWS_PER_COPY) == 0 && BN / 2 == 128 && T::TN <= 64),
                 "the SwiGLU epilogue: FP8 grouped tiles whose B copies and scale blocks stay in one half");
+  static_assert(E < 3 || (!GROUPED && FM % 2 == 0 && T::TN == 64), "dense epilogues: 64 columns a wave");
+  // Gated block: the B slots of each wave's 64 columns are 32 gate rows and the 32 up
+  // rows of the same output columns, so one lane holds both values of an output.
+  static_assert(!GLU || (KIND == KIND_BF16 && T::NWC == 4 && FN == 2), "the gated epilogue's B rows");
+  // Operands with a strided contraction: a stage is 32 rows of BM (BN) contiguous
+  // elements, copied as they lie and transposed by the LDS reads (ds_read_b64_tr_b16).
+  // The stage's 64-byte blocks are XORed with the row, so the four rows that one read
+  // touches lie in different banks.
+  static_assert(!(TRA || TRB) || (KIND == KIND_BF16 && SB == 64 && (E == 0 || PART)),
+                "transposed operands: BF16, plain or partial sums");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
 
   const int tid = threadIdx.x;
@@ -548,7 +693,7 @@ void gemm_kernel(const GemmArgs args) {
   if constexpr (GROUPED) {
     total_tiles = grouped_total_row_tiles<BM>(args.offsets, args.G, args.cap, args.M) * args.tiles_n;
   } else {
-    total_tiles = args.tiles_m * args.tiles_n;
+    total_tiles = args.tiles_m * args.tiles_n * (PART ? args.splits : 1);
   }
 
   // Per-lane LDS byte offsets of this lane's fragment reads for k-step j (fragment
@@ -569,6 +714,20 @@ void gemm_kernel(const GemmArgs args) {
       a_rd[j][h] = T::lds_off(a_row0, c);
       b_rd[j][h] = (uint32_t)(BM * SB) + T::lds_off(b_row0, c);
     }
+  // Transposed operands: the 16 lanes of a transposing read fetch four rows k of 16
+  // columns, lane i row i/4, columns 4*(i%4) .. +3, and lane i receives column i of the
+  // four rows.  Fragment f's k-step j and half h: rows 16j + 8lg + 4h + 0..3; the row's
+  // low two bits, which swizzle the 64-byte block, are i/4 throughout.
+  uint32_t a_tr[FM] = {}, b_tr[FN] = {};
+  if constexpr (TRA || TRB) {
+    const uint32_t r4 = (lane >> 2) & 3, c8 = 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+      a_tr[f] = (8 * lg + r4) * (2 * BM) + 64 * ((wm * FM + f) ^ r4) + c8;
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      b_tr[f] = (uint32_t)(BM * SB) + (8 * lg + r4) * (2 * BN) + 64 * ((wn * FN + f) ^ r4) + c8;
+  }
 
   // Copy lanes: lane t of a wave copy covering rows r0 .. r0 + 1024/SB - 1 writes
   // LDS bytes r0*SB + 16t, i.e. row r0 + t/NC, physical chunk t%NC, which holds
@@ -578,10 +737,25 @@ void gemm_kernel(const GemmArgs args) {
   static_assert((4 * T::NWC) % NC == 0, "copy swizzle must not depend on the copy index");
   const int cp_row = lane / NC;
   const int cp_c16 = 16 * ((lane % NC) ^ ((4 * wave + cp_row / T::RPS) % NC));
+  // Transposed operands: copy ci covers stage rows ci*RPC .. of RPC = 1024 / row bytes;
+  // LDS chunk c of row k holds the row's chunk c ^ 4*(k & 3).
+  constexpr int RPC_A = 512 / BM, RPC_B = 512 / BN, CPR_A = BM / 8, CPR_B = BN / 8;
+  static_assert(!TRA || (BM <= 256 && (T::NWC * RPC_A) % 4 == 0), "the row's swizzle must not depend on the copy");
+  static_assert(!TRB || (BN <= 256 && (T::NWC * RPC_B) % 4 == 0), "the row's swizzle must not depend on the copy");
+  const int tra_row = TRA ? RPC_A * wave + lane / CPR_A : 0, trb_row = TRB ? RPC_B * wave + lane / CPR_B : 0;
+  const int tra_c16 = TRA ? 16 * ((lane % CPR_A) ^ (4 * (tra_row & 3))) : 0;
+  const int trb_c16 = TRB ? 16 * ((lane % CPR_B) ^ (4 * (trb_row & 3))) : 0;
 
   for (int i = blockIdx.x; i < total_tiles; i += gridDim.x) {
-    const int p = xcd_remap(i, total_tiles);
+    int p = xcd_remap(i, total_tiles);
     int m0, m_end, n0;
+    int part = 0, ks = 0;   // part of the contraction and its first stage
+    if constexpr (PART) {
+      // part after part, so the tiles that run together read the same stages
+      part = __builtin_amdgcn_readfirstlane(p / (args.tiles_m * args.tiles_n));
+      p -= part * (args.tiles_m * args.tiles_n);
+      ks = part * nk;
+    }
     const uint8_t* Bbase = args.B;
     const int16_t* sfb = args.sfb;
     if constexpr (GROUPED) {
@@ -597,7 +771,7 @@ void gemm_kernel(const GemmArgs args) {
       raster<2>(p - tile0 * args.tiles_n, ntl, args.tiles_n, tm, tn);
       m0 = row_lo + tm * BM;
       m_end = m0 + BM < row_hi ? m0 + BM : row_hi;
-      n0 = tn * (EPI ? BN / 2 : BN);
+      n0 = tn * (QSW ? BN / 2 : BN);
       Bbase += (int64_t)g * args.stride_b;
       sfb += (int64_t)g * args.stride_sfb;
     } else {
@@ -605,7 +779,7 @@ void gemm_kernel(const GemmArgs args) {
       raster<4>(p, args.tiles_m, args.tiles_n, tm, tn);
       m0 = tm * BM;
       m_end = m0 + BM < args.M ? m0 + BM : args.M;
-      n0 = tn * BN;
+      n0 = tn * (GLU ? BN / 2 : BN);
     }
     m0 = __builtin_amdgcn_readfirstlane(m0);
     m_end = __builtin_amdgcn_readfirstlane(m_end);
@@ -620,21 +794,45 @@ void gemm_kernel(const GemmArgs args) {
     auto tile_body = [&](auto mm_c, auto iss_c) __attribute__((always_inline)) {
       constexpr bool MM = decltype(mm_c)::value;
       constexpr bool ISS = decltype(iss_c)::value;   // the wave issues copies
-      const int n_end = n0 + BN < args.N ? n0 + BN : args.N;
+      const int n_lim = GLU ? args.inter : args.N, n_tile = GLU ? BN / 2 : BN;
+      const int n_end = n0 + n_tile < n_lim ? n0 + n_tile : n_lim;
       const int rows_a = m_end - m0, rows_b = n_end - n0;
+      // bytes of K from this part's first stage on, and (transposed operands) rows
+      const int k_bytes = PART ? args.k_bytes - ks * SB : args.k_bytes;
+      const int k_rows = PART ? args.K - ks * (SB / 2) : args.K;
 
       // Buffer resources cover exactly the bytes of this tile's rows: rows past the
       // end of the matrix (or of the expert) read as zero.
-      const __amdgpu_buffer_rsrc_t ra =
-          make_rsrc(args.A + (int64_t)m0 * args.lda, (uint32_t)((rows_a - 1) * args.lda + args.k_bytes));
-      const __amdgpu_buffer_rsrc_t rb = make_rsrc(
-          Bbase + (int64_t)n0 * args.ldb,
-          (uint32_t)(((EPI ? args.inter + BN / 2 : rows_b) - 1) * args.ldb + args.k_bytes));
+      // (A part of the contraction starts ks stages further on.  Gated block: waves 0 and
+      // 1 copy gate rows, waves 2 and 3 up rows, each through its own resource.)
+      const uint8_t* const Ab = TRA ? args.A + 2 * (int64_t)m0 + (int64_t)ks * (SB / 2) * args.lda
+                                    : args.A + (int64_t)m0 * args.lda + (PART ? (int64_t)ks * SB : 0);
+      const uint8_t* const Bb = TRB ? args.B + 2 * (int64_t)n0 + (int64_t)ks * (SB / 2) * args.ldb
+                                    : Bbase + (int64_t)n0 * args.ldb + (PART ? (int64_t)ks * SB : 0) +
+                                          (GLU ? (int64_t)((wave >> 1) & 1) * args.inter * args.ldb : 0);
+      const __amdgpu_buffer_rsrc_t ra = make_rsrc(Ab, (uint32_t)((rows_a - 1) * args.lda + k_bytes));
+      const __amdgpu_buffer_rsrc_t rb =
+          make_rsrc(Bb, (uint32_t)(((QSW ? args.inter + BN / 2 : rows_b) - 1) * args.ldb + k_bytes));
+      // Transposed operands: a resource of its own for each stage, whose record ends with
+      // the operand's last row, so offsets stay small for any K and rows past K read zero.
+      // (Columns past the tile's edge read whatever lies there: they only reach outputs
+      // that are never stored.  The operand's width is a multiple of 8.)
+      auto stage_rsrc = [&](const uint8_t* base, int64_t ld, int cols, int kt) {
+        int rows = k_rows - kt * (SB / 2);
+        rows = (uint32_t)kt < (uint32_t)nk && rows > 0 ? (rows < SB / 2 ? rows : SB / 2) : 0;
+        return make_rsrc(base + (int64_t)kt * (SB / 2) * ld,
+                         rows ? (uint32_t)((rows - 1) * ld + 2 * ((cols + 7) & ~7)) : 0u);
+      };
       // Copy q of a copying wave fills LDS rows (slots) (q*NWC + wave) * ROWS_PER_COPY + cp_row
       // from tile row perm(slot); the lane part and the q part of the slot occupy
       // disjoint bits, so perm splits into a per-lane row and a per-q row.
-      uint32_t a_vbase = (uint32_t)(T::perm_a(T::ROWS_PER_COPY * wave + cp_row) * args.lda) + cp_c16;
-      uint32_t b_vbase = (uint32_t)(T::perm_b(T::ROWS_PER_COPY * wave + cp_row) * args.ldb) + cp_c16;
+      uint32_t a_vbase = TRA ? (uint32_t)(tra_row * args.lda) + tra_c16
+                             : (uint32_t)(T::perm_a(T::ROWS_PER_COPY * wave + cp_row) * args.lda) + cp_c16;
+      // (gated block: slot 64w + 32b + i is row 32w + i of the gate (b = 0) or up rows;
+      // copy q of wave w' covers slots 64q + 16w' .. 64q + 16w' + 15)
+      uint32_t b_vbase = TRB ? (uint32_t)(trb_row * args.ldb) + trb_c16
+                         : GLU ? (uint32_t)((16 * (wave & 1) + cp_row) * args.ldb) + cp_c16
+                               : (uint32_t)(T::perm_b(T::ROWS_PER_COPY * wave + cp_row) * args.ldb) + cp_c16;
       // Opaque per tile: otherwise the compiler hoists every copy offset of the
       // prologue out of the tile loop and spills them all.
       asm volatile("" : "+v"(a_vbase), "+v"(b_vbase));
@@ -647,11 +845,18 @@ void gemm_kernel(const GemmArgs args) {
         uint8_t* sB = sA + BM * SB;
         const int kb = kt * SB;
         // outside the K extent the offset gets bit 31, which no record count reaches
-        const uint32_t oob = (uint32_t)kt < (uint32_t)nk && kb + cp_c16 < args.k_bytes ? 0u : kOOB;
+        const uint32_t oob = (uint32_t)kt < (uint32_t)nk && kb + cp_c16 < k_bytes ? 0u : kOOB;
         uint8_t* const spare = smem + NS * T::STAGE_BYTES;
         if (q < T::A_LOADS) {
           const int ci = q * T::NWC + wave;
           const bool dummy = T::DUMMY && ci >= T::A_COPIES;
+          if constexpr (TRA) {
+            static_assert(!T::DUMMY, "transposed copies split evenly");
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                stage_rsrc(Ab, args.lda, rows_a, kt), (__attribute__((address_space(3))) void*)(sA + 1024 * ci), 16,
+                a_vbase + (uint32_t)(q * T::NWC * RPC_A) * (uint32_t)args.lda, 0, 0, 0);
+            return;
+          }
           const uint32_t qrow = (uint32_t)T::perm_a(q * T::NWC * T::ROWS_PER_COPY);
           // The row and K parts stay below 2^31 (256 rows of at most 2^31/256
           // bytes), so OR-ing or adding the out-of-range bit give the same offset;
@@ -666,9 +871,15 @@ void gemm_kernel(const GemmArgs args) {
           const int qb = q - T::A_LOADS;
           const int ci = qb * T::NWC + wave;
           const bool dummy = T::DUMMY && ci >= T::B_COPIES;
-          const uint32_t qrow0 = (uint32_t)T::perm_b(qb * T::NWC * T::ROWS_PER_COPY);
+          if constexpr (TRB) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                stage_rsrc(Bb, args.ldb, rows_b, kt), (__attribute__((address_space(3))) void*)(sB + 1024 * ci), 16,
+                b_vbase + (uint32_t)(qb * T::NWC * RPC_B) * (uint32_t)args.ldb, 0, 0, 0);
+            return;
+          }
+          const uint32_t qrow0 = (uint32_t)(GLU ? 32 * qb : T::perm_b(qb * T::NWC * T::ROWS_PER_COPY));
           // (SwiGLU epilogue: tile rows past BN/2 are up rows, inter rows further on)
-          const uint32_t qrow = EPI && qrow0 >= (uint32_t)(BN / 2) ? qrow0 - BN / 2 + (uint32_t)args.inter : qrow0;
+          const uint32_t qrow = QSW && qrow0 >= (uint32_t)(BN / 2) ? qrow0 - BN / 2 + (uint32_t)args.inter : qrow0;
           const uint32_t off = GROUPED ? (b_vbase + qrow * (uint32_t)args.ldb + kb) | oob | (dummy ? kOOB : 0u)
                                        : b_vbase + qrow * (uint32_t)args.ldb + (uint32_t)kb + (oob | (dummy ? kOOB : 0u));
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -722,7 +933,7 @@ void gemm_kernel(const GemmArgs args) {
       uint32_t sa_voff = 2u * (uint32_t)(m0 + wm * T::TM + (T::PERM_A ? 4 * l32 : l32)) +
                          2u * lg_rows * (uint32_t)lg * ld_a;
       asm volatile("" : "+v"(sa_voff));
-      const int brow0 = EPI && wn * T::TN >= BN / 2 ? args.inter + n0 + wn * T::TN - BN / 2 : n0 + wn * T::TN;
+      const int brow0 = QSW && wn * T::TN >= BN / 2 ? args.inter + n0 + wn * T::TN - BN / 2 : n0 + wn * T::TN;
       uint32_t sb_voff = KIND == KIND_FP8 && !T::B_ROW
                              ? 2u * (uint32_t)(brow0 / 128)
                              : 2u * (uint32_t)(n0 + wn * T::TN + (T::PERM_B ? FN * l32 : l32)) +
@@ -743,6 +954,7 @@ void gemm_kernel(const GemmArgs args) {
       // round read the same words), and decode_scales keeps every result alive.
       auto load_scales = [&](int kt, auto slot) {
         constexpr int sl = decltype(slot)::value;
+        if constexpr (PART) kt += ks;
         if constexpr (MM && KIND != KIND_BF16) {
 #pragma unroll
           for (int w = 0; w < SW; ++w) {
@@ -800,6 +1012,7 @@ void gemm_kernel(const GemmArgs args) {
       auto decode_scales = [&](int kt, auto slot, uint32_t (&sa)[FM], uint32_t (&sb)[FN]) {
         if constexpr (!MM) return;
         constexpr int sl = decltype(slot)::value;
+        if constexpr (PART) kt += ks;
         if constexpr (KIND == KIND_FP8) {
           const int sh = ((kt * SB / 128) & 1) * 8;
           if constexpr (T::WIDE) {
@@ -845,8 +1058,21 @@ void gemm_kernel(const GemmArgs args) {
       auto read_frags = [&](int buf, int j, frag_t (&xa)[FM], frag_t (&xb)[FN]) {
         if constexpr (!MM) return;
         const uint8_t* base = smem + buf * T::STAGE_BYTES;
+        // rows k .. k+3 and k+4 .. k+7 of a fragment of a transposed operand
+        auto tr_frag = [&](uint32_t off, int row_bytes) {
+          typedef __attribute__((ext_vector_type(4))) short i16x4_t;
+          typedef __attribute__((ext_vector_type(8))) short i16x8_t;
+          typedef __attribute__((address_space(3))) i16x4_t lds_t;
+          const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(base + off + 16 * j * row_bytes));
+          const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(base + off + (16 * j + 4) * row_bytes));
+          return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
+          if constexpr (TRA) {
+            xa[f] = tr_frag(a_tr[f], 2 * BM);
+            continue;
+          }
           const uint8_t* p0 = base + a_rd[j][0] + 32 * SB * f;
           if constexpr (KIND == KIND_BF16) {
             xa[f] = *(const bf16x8_t*)p0;
@@ -861,6 +1087,10 @@ void gemm_kernel(const GemmArgs args) {
         }
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
+          if constexpr (TRB) {
+            xb[f] = tr_frag(b_tr[f], 2 * BN);
+            continue;
+          }
           const uint8_t* p0 = base + b_rd[j][0] + 32 * SB * f;
           if constexpr (KIND == KIND_BF16) {
             xb[f] = *(const bf16x8_t*)p0;
@@ -1007,7 +1237,7 @@ void gemm_kernel(const GemmArgs args) {
               if constexpr (!DEAD) mfmas(jc, fa[ca], fb[cu], sa_cur, sb_cur);
               read_frags(buf, j + 1, fa[na], fb[nx]);
             }
-            if constexpr (MM && !DEAD) interleave<FM * FN, (FM + FN) * RPF, nvm>();
+            if constexpr (MM && !DEAD) interleave<FM * FN, NDS, nvm>();
             __builtin_amdgcn_sched_barrier(0);
           } else {
             // Stage s+1 has landed once no more than wait_at() of this wave's copies
@@ -1036,7 +1266,7 @@ void gemm_kernel(const GemmArgs args) {
               if constexpr (!DEAD) mfmas(jc, fa[ca], fb[cu], sa_cur, sb_cur);
               read_frags(nbuf, 0, fa[na], fb[nx]);
             }
-            if constexpr (MM && !DEAD) interleave<FM * FN, (FM + FN) * RPF, nvm>();
+            if constexpr (MM && !DEAD) interleave<FM * FN, NDS, nvm>();
             __builtin_amdgcn_sched_barrier(0);
             // (shared scales: stage s+1 reads the set of its pair's first stage)
             constexpr int sbuf = T::SHARED_SCALES ? T::pmod(((si + 1) & ~1), NS) : nbuf;
@@ -1090,7 +1320,7 @@ void gemm_kernel(const GemmArgs args) {
       // matrix edge): a wave with none skips its part
       const int rows_w = m_end - (m0 + wm * T::TM) < T::TM ? m_end - (m0 + wm * T::TM) : T::TM;
       // (the SwiGLU epilogue has every wave meet one more barrier: no early exit)
-      if (EPI == 0 && rows_w <= 0) return;
+      if (!QSW && rows_w <= 0) return;
       uint8_t* const stg = smem + wave * T::EPI_WAVE_BYTES;
       // The lane index, made opaque here: every staging address derives from it,
       // and the compiler would otherwise hoist all of them out of the tile loop and
@@ -1098,6 +1328,11 @@ void gemm_kernel(const GemmArgs args) {
       int el = lane;
       asm volatile("" : "+v"(el));
       const int el32 = el & 31, elg = el >> 5;
+      if constexpr (E >= 3) {
+        dense_epilogue<T, FM, FN, E>(args, acc, stg, el, m0 + wm * T::TM, rows_w,
+                                     n0 + wn * (GLU ? T::TN / 2 : T::TN), n_end, part);
+        return;
+      }
       auto stage_quad = [&](int row, int col, float v0, float v1, float v2, float v3) {
         // four consecutive columns col .. col+3 (col a multiple of 4) of `row`
         const int chunk = (col >> 3) ^ T::epi_swz(row);
@@ -1137,7 +1372,7 @@ void gemm_kernel(const GemmArgs args) {
         // accumulator into VGPRs first and spill
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (EPI > 0) {
+      if constexpr (QSW) {
         // SwiGLU and FP8 1x128 requantisation.  Tile row r's gate values (tile columns
         // 0 .. BN/2-1) and up values (BN/2 .. BN-1) lie in the staged blocks of other
         // waves, so every wave's block must be in place first.  Wave w then takes
@@ -1145,7 +1380,7 @@ void gemm_kernel(const GemmArgs args) {
         // exactly the arithmetic of the SwiGLU quantiser, on the same bf16 values.
         wait_vm_lds<63>();
         ring_barrier();
-        constexpr int RULE = EPI - 1;
+        constexpr int RULE = E - 1;
         const int seg = el & 15, rsub = el >> 4;
         const int blk = n0 / 128, kb_total = args.inter / 128;
         const int gcol = 8 * seg, ucol = BN / 2 + 8 * seg;

@@ -81,6 +81,15 @@ enum bsg_scale_rule {
   BSG_SCALE_OCP_MX = 1, /* OCP Microscaling: 2^(floor(log2 amax) - emax), larger values saturate */
 };
 
+/* Activations of the products with epilogues (below). */
+enum bsg_activation {
+  BSG_ACT_NONE = 0,      /* f(z) = z */
+  BSG_ACT_RELU = 1,      /* max(z, 0) */
+  BSG_ACT_SILU = 2,      /* z / (1 + e^-z) */
+  BSG_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+  BSG_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+};
+
 /* Human-readable name of a status code (static storage). */
 const char* bsg_status_string(int status);
 
@@ -513,6 +522,96 @@ int lora_add_bf16(const void* X, int64_t ldx, const void* A, int64_t lda, int64_
 
 /* Workspace bytes of lora_add_bf16 for a plan of that many rows. */
 int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_t K, int32_t r);
+
+/* ---------------------------------------------------------------------------
+ * Dense products with work in their epilogues, and their gradients: the halves of a
+ * feed-forward block.  A gated block is gemm_bf16_glu followed by a gemm_*_act with the
+ * residual stream; one without a gate is two gemm_*_act calls.
+ *
+ * Common to the calls below:
+ *  - workspace: the bytes the call's *_workspace function gives for the same sizes,
+ *    16-byte aligned (may be NULL when that is 0); no initial value needed, nothing in it
+ *    lasts; calls that overlap in time need one each.  Calls that are too small to fill
+ *    the GPU with whole tiles split the contraction and join fp32 sums kept there, in an
+ *    order that is the same on every run.
+ *  - sums and everything formed from them are fp32, rounded to bf16 once at each store.
+ *  - M and N (inter) may be anything from 0 on; rows of A, of B and of the contraction's
+ *    operands follow the dense products' rules for K.  ceil(M/128) * ceil(columns/128)
+ *    must be below 2^24 (BSG_ERR_UNSUPPORTED_SHAPE).
+ * ------------------------------------------------------------------------- */
+
+/* D = R + f(A B^T + bias), and the pre-activation beside it:
+ *   z[m][n] = sum_k A[m][k] B[n][k] + bias[n];  Z[m][n] = bf16(z);
+ *   D[m][n] = bf16( R[m][n] + f(z[m][n]) )
+ *   A, B, D: as gemm_bf16; bias: bf16 [N] or NULL; act: bsg_activation;
+ *   R: bf16 [M][ldr >= N] or NULL (no residual; ldr is then ignored); R == D adds in
+ *   place, any other overlap of an output with another operand is not allowed;
+ *   Z: bf16 [M][ldz >= N] or NULL: the pre-activation, which gemm_bf16_act_backward takes.
+ *   Requirements of gemm_bf16; bias, R and Z 2-byte aligned (16-byte aligned with leading
+ *   dimensions multiples of 8, R, Z and D move 16 bytes at a time).  K == 0 gives
+ *   D = R + f(bias). */
+int gemm_bf16_act(const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias, int32_t act,
+                  const void* R, int64_t ldr, void* D, int64_t ldd, void* Z, int64_t ldz, int64_t M, int64_t N,
+                  int64_t K, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t gemm_bf16_act_workspace(int64_t M, int64_t N, int64_t K);
+
+/* The same with the operands and scales of gemm_fp8_blockscaled (sfb_gran_mn 128 or 1) and
+ * of gemm_fp4_blockscaled, without Z. */
+int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
+                 const int16_t* sfb, int64_t ld_sfb, int32_t sfb_gran_mn, const void* bias, int32_t act,
+                 const void* R, int64_t ldr, void* D, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                 void* workspace, int64_t workspace_bytes, void* stream);
+int64_t gemm_fp8_act_workspace(int64_t M, int64_t N, int64_t K);
+int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
+                 const int16_t* sfb, int64_t ld_sfb, const void* bias, int32_t act, const void* R, int64_t ldr,
+                 void* D, int64_t ldd, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+int64_t gemm_fp4_act_workspace(int64_t M, int64_t N, int64_t K);
+
+/* Gradients of gemm_bf16_act from dD, the gradient of D (that of R is dD itself):
+ *   dz[m][n] = dD[m][n] f'(z[m][n]), z read from Z (bf16, as the forward call wrote it);
+ *   dA[m][k] = bf16( sum_n bf16(dz[m][n]) B[n][k] )       bf16 [M][ldda >= K]
+ *   dB[n][k] = bf16( sum_m bf16(dz[m][n]) A[m][k] )       bf16 [N][lddb >= K]
+ *   dbias[n] = sum_m dz[m][n]                             fp32 [N]
+ * dz is rounded to bf16 where it enters a product (the matrix cores' operand type), not in
+ * dbias.  Where z <= 0, BSG_ACT_RELU's gradient is 0.
+ *   dA, dB, dbias: each may be NULL (not computed); A is read for dB only, B for dA only.
+ *   Z: bf16 [M][ldz >= N]; with BSG_ACT_NONE it is not read and may be NULL.
+ *   Requires K % 8 == 0; A and B 16-byte aligned with leading dimensions multiples of 8;
+ *   dD, Z, dA and dB 2-byte aligned, dbias 4-byte; M and N below 2^30.  An output must not
+ *   overlap another operand.  M == 0 zeroes dB and dbias, N == 0 zeroes dA. */
+int gemm_bf16_act_backward(const void* dD, int64_t lddd, const void* Z, int64_t ldz, const void* A, int64_t lda,
+                           const void* B, int64_t ldb, int32_t act, void* dA, int64_t ldda, void* dB, int64_t lddb,
+                           float* dbias, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+int64_t gemm_bf16_act_backward_workspace(int64_t M, int64_t N, int64_t K);
+
+/* The gated block's first half: both projections, the activation and the product.
+ *   g[m][i] = sum_k X[m][k] W13[i][k],  u[m][i] = sum_k X[m][k] W13[inter + i][k];
+ *   H[m][i] = bf16( f(g[m][i]) u[m][i] )                  bf16 [M][ldh >= inter]
+ *   Z[m] = [bf16(g[m]), bf16(u[m])]                       bf16 [M][ldz >= 2*inter], or NULL
+ *   X: bf16 [M][ldx], W13: bf16 [2*inter][ldw] (gate rows, then up rows, as moe_ffn_fp8's),
+ *   act: bsg_activation (BSG_ACT_SILU: SwiGLU).
+ *   Requires inter % 8 == 0 and gemm_bf16's rules with N = 2*inter; H and Z 2-byte aligned
+ *   (fastest 16-byte aligned with leading dimensions multiples of 8).  An output must not
+ *   overlap another operand. */
+int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int32_t act, void* H, int64_t ldh,
+                  void* Z, int64_t ldz, int64_t M, int64_t inter, int64_t K, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+int64_t gemm_bf16_glu_workspace(int64_t M, int64_t inter, int64_t K);
+
+/* Its gradients, from dH and the Z of the forward call:
+ *   dg = dH u f'(g), du = dH f(g), dz = [bf16(dg), bf16(du)];
+ *   dX[m][k]   = bf16( sum_j dz[m][j] W13[j][k] )         bf16 [M][lddx >= K]
+ *   dW13[j][k] = bf16( sum_m dz[m][j] X[m][k] )           bf16 [2*inter][lddw >= K]
+ *   dX and dW13 may each be NULL.  Requires inter % 8 == 0, K % 8 == 0; X and W13 16-byte
+ *   aligned with leading dimensions multiples of 8; the others 2-byte aligned; M and
+ *   2*inter below 2^30. */
+int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t ldz, const void* X, int64_t ldx,
+                           const void* W13, int64_t ldw, int32_t act, void* dX, int64_t lddx, void* dW13,
+                           int64_t lddw, int64_t M, int64_t inter, int64_t K, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+int64_t gemm_bf16_glu_backward_workspace(int64_t M, int64_t inter, int64_t K);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,477 @@
+"""GPU parity of the dense products with epilogues, of the gated block and of their gradients
+against the fp64 forms of oracle/dense.py, whose bounds on the error before the final
+rounding are derived there; the final rounding to bf16 adds at most 2^-8 of the value.
+Beside the elements' bounds, the relative 2-norm of the error stays below 2^-8 wherever the
+sums of the products are not cancelled away: the output's rounding and that of dz (in the
+gradients) each contribute at most 2^-8 / sqrt(3) there."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_05_amd as bsg
+import oracle
+from block_scaled_precision_05_amd import workloads
+from oracle import dense
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U8 = 2.0 ** -8
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+def _say(msg):
+    print(f"[gpu-test] {msg}", flush=True)
+
+
+def _f64(t):
+    return None if t is None else t.detach().to(torch.float64).cpu().numpy()
+
+
+def _mat(g, rows, cols, pad=0, by=1.0, shift=0):
+    """bf16 [rows, cols], rows `pad` elements apart, starting `shift` elements into a buffer."""
+    buf = by * torch.randn(rows * (cols + pad) + shift, generator=g, device=DEV)
+    return buf.to(torch.bfloat16)[shift:].view(rows, cols + pad)[:, :cols]
+
+
+def _near(out, want, err, what, rounded=True):
+    got = _f64(out)
+    assert got.shape == want.shape, what
+    tol = (U8 * (np.abs(want) + err) if rounded else 0.0) + err
+    d = np.abs(got - want)
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    assert np.all(d <= tol), f"{what}: {np.max(d - tol):.3e} over the bound at {np.argmax((d - tol))}"
+    norm = np.linalg.norm(want)
+    rel = np.linalg.norm(d) / norm if norm else 0.0
+    if rounded and want.size > 64:
+        assert rel <= U8, f"{what}: relative 2-norm {rel:.2e}"
+    _say(f"  {what}: {np.max(d / np.maximum(tol, 1e-300), initial=0):.2f} of the bound, 2-norm {rel:.1e}")
+
+
+def _z(A, B):
+    a, b = _f64(A), _f64(B)
+    return a @ b.T, np.abs(a) @ np.abs(b).T
+
+
+# M, N, K: single rows and columns, odd sizes, a contraction shorter than one stage and with a
+# tail, tiles of every form (parts of the contraction, 128-row tiles, 256-row tiles)
+SIZES = [(1, 1, 8), (1, 129, 2048), (2, 7168, 520), (5, 3, 40), (16, 520, 4096), (17, 100, 1032), (33, 65, 264),
+         (64, 2048, 1024), (130, 257, 1000), (200, 1001, 2056), (1001, 1003, 520), (2048, 1920, 96),
+         (3900, 3400, 136), (3841, 3457, 328)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_act(M, N, K):
+    act = ACTS[(M + N) % 5]
+    _say(f"gemm_bf16_act {M}x{N}x{K} {act}")
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    A, B = _mat(g, M, K), _mat(g, N, K, by=K ** -0.5)
+    bias, R = _mat(g, 1, N)[0], _mat(g, M, N)
+    z, mag = _z(A, B)
+    for b, r, a, keep in ((bias, R, act, True), (None, None, ACTS[(M + N + 1) % 5], False), (None, R, "none", True),
+                          (bias, None, ACTS[(M + N + 3) % 5], False)):
+        Z = torch.full((M, N), 9.0, dtype=torch.bfloat16, device=DEV) if keep else None
+        D = bsg.gemm_bf16_act(A, B, bias=b, act=a, residual=r, preact=Z)
+        want, err, wz, ez = dense.act_forward(z, mag, K, _f64(b), a, _f64(r))
+        _near(D, want, err, f"{a}, bias {b is not None}, residual {r is not None}")
+        if keep:
+            _near(Z, wz, ez, "pre-activation")
+    mine = R.clone()
+    assert bsg.gemm_bf16_act(A, B, bias=bias, act=act, residual=mine, out=mine) is mine
+    assert torch.equal(mine, bsg.gemm_bf16_act(A, B, bias=bias, act=act, residual=R))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(3, 40, 16), (150, 264, 2048), (3900, 3400, 64)])
+def test_act_every_activation(M, N, K, act):
+    """Every activation in every form, over a range of z that reaches both tails."""
+    _say(f"gemm_bf16_act {M}x{N}x{K} {act}")
+    g = torch.Generator(device=DEV).manual_seed(M)
+    A, B = _mat(g, M, K), _mat(g, N, K, by=4 * K ** -0.5)
+    z, mag = _z(A, B)
+    want, err, _, _ = dense.act_forward(z, mag, K, None, act, None)
+    _near(bsg.gemm_bf16_act(A, B, act=act), want, err, act)
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (4, 1), (0, 3)])
+@pytest.mark.parametrize("M,N,K", [(40, 200, 1040), (300, 515, 72), (3900, 3400, 40)])
+def test_act_strides(M, N, K, pad, shift):
+    """Rows of bias, residual, Z and D at any element; what lies between them stays."""
+    _say(f"gemm_bf16_act {M}x{N}x{K} rows {pad} apart from {shift}")
+    g = torch.Generator(device=DEV).manual_seed(pad)
+    A, B = _mat(g, M, K, pad=16, shift=8), _mat(g, N, K, pad=8, by=K ** -0.5)
+    bias = _mat(g, 1, N, shift=shift)[0]
+    R = _mat(g, M, N, pad=pad, shift=shift)
+    bufs = [torch.full((M * (N + pad) + shift,), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    D, Z = (b[shift:].view(M, N + pad)[:, :N] for b in bufs)
+    need = bsg.lib().gemm_bf16_act_workspace(M, N, K)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)     # NaN as floats
+    assert bsg.gemm_bf16_act(A, B, bias=bias, act="silu", residual=R, out=D, preact=Z, workspace=ws) is D
+    z, mag = _z(A, B)
+    want, err, wz, ez = dense.act_forward(z, mag, K, _f64(bias), "silu", _f64(R))
+    _near(D, want, err, "D")
+    _near(Z, wz, ez, "Z")
+    for b in bufs:
+        assert torch.all(b[:shift] == 7) and torch.all(b[shift:].view(M, N + pad)[:, N:] == 7)
+    assert torch.all(ws[need:] == 255)
+
+
+def _scaled(fmt, M, N, K, seed, gran=128):
+    """Operands of an FP8 or FP4 product, its exact result and the norms' product."""
+    g = torch.Generator().manual_seed(seed)
+    if fmt == "fp8":
+        A, sa = workloads.fp8_operand(M, K, 1, g, "cpu")[:2]
+        B, sb = workloads.fp8_operand(N, K, gran, g, "cpu")[:2]
+    else:
+        A, sa = workloads.fp4_operand(M, K, g, "cpu")[:2]
+        B, sb = workloads.fp4_operand(N, K, g, "cpu")[:2]
+    pa, pb = (oracle.pack_scales(s.numpy()) for s in (sa, sb))
+    if fmt == "fp8":
+        z = oracle.gemm_fp8(A.numpy(), pa, B.numpy(), pb, sfb_gran_mn=gran)
+        na, nb = oracle.row_norms("e4m3", A.numpy(), pa), oracle.row_norms("e4m3", B.numpy(), pb, gran_mn=gran)
+    else:
+        z = oracle.gemm_fp4(A.numpy(), pa, B.numpy(), pb, K)
+        na, nb = oracle.row_norms("e2m1", A.numpy(), pa, K=K), oracle.row_norms("e2m1", B.numpy(), pb, K=K)
+    dev = [torch.from_numpy(x).to(DEV) if isinstance(x, np.ndarray) else x.to(DEV) for x in (A, pa, B, pb)]
+    return dev, z, na[:, None] * nb[None, :]
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [
+    ("fp8", 1, 7168, 256), ("fp8", 3, 40, 128), ("fp8", 64, 520, 2048), ("fp8", 130, 257, 896),
+    ("fp8", 300, 1000, 1152), ("fp8", 3900, 3400, 128), ("fp8", 3841, 3457, 384),
+    ("fp4", 1, 1024, 96), ("fp4", 8, 40, 32), ("fp4", 8, 512, 7168), ("fp4", 130, 257, 1056),
+    ("fp4", 1000, 515, 544), ("fp4", 3900, 3400, 160), ("fp4", 3841, 3457, 96)])
+def test_act_scaled(fmt, M, N, K):
+    for gran in ((128, 1) if fmt == "fp8" else (1,)):
+        act = ACTS[(M + gran) % 5]
+        _say(f"gemm_{fmt}_act {M}x{N}x{K} {act}, B scales per {gran}")
+        (A, sfa, B, sfb), z, mag = _scaled(fmt, M, N, K, M + N + K, gran)
+        z, mag = z / 8, mag / 8                        # a smaller z: the activations' curved part
+        sfa = _minus3(sfa)
+        g = torch.Generator(device=DEV).manual_seed(K)
+        bias, R = _mat(g, 1, N)[0], _mat(g, M, N)
+        kw = {"sfb_gran_mn": gran} if fmt == "fp8" else {"K": K}
+        fn = bsg.gemm_fp8_act if fmt == "fp8" else bsg.gemm_fp4_act
+        for b, r, a in ((bias, R, act), (None, None, "none"), (None, R, "gelu"), (bias, None, "relu")):
+            D = fn(A, sfa, B, sfb, bias=b, act=a, residual=r, **kw)
+            want, err, _, _ = dense.act_forward(z, mag, K, _f64(b), a, _f64(r), dense.CUT if fmt == "fp8" else 0.0)
+            _near(D, want, err, f"{a}, bias {b is not None}, residual {r is not None}")
+        # a scale array whose rows take no 8-byte loads
+        odd = torch.full((sfa.shape[0], sfa.shape[1] + 1 + sfa.shape[1] % 2), 0x7F7F, dtype=torch.int16, device=DEV)
+        odd[:, :sfa.shape[1]] = sfa
+        assert torch.equal(fn(A, odd[:, :sfa.shape[1]], B, sfb, bias=bias, act=act, residual=R, **kw),
+                           fn(A, sfa, B, sfb, bias=bias, act=act, residual=R, **kw))
+
+
+def _minus3(packed):
+    """Both scale bytes of every word three lower (the operand an eighth)."""
+    return (packed.to(torch.int32) - 0x0303).to(torch.int16)
+
+
+GLU = [(1, 8, 8), (1, 2048, 512), (3, 40, 264), (32, 1024, 1024), (48, 200, 2048), (130, 264, 1000), (777, 1000, 264),
+       (2000, 2040, 72), (3841, 1800, 200), (4100, 3000, 40)]
+
+
+@pytest.mark.parametrize("M,inter,K", GLU)
+def test_glu(M, inter, K):
+    act = ACTS[(M + 2) % 5]
+    _say(f"gemm_bf16_glu {M}x{inter}x{K} {act}")
+    g = torch.Generator(device=DEV).manual_seed(M + inter + K)
+    X, W = _mat(g, M, K), _mat(g, 2 * inter, K, by=2 * K ** -0.5)
+    z, mag = _z(X, W)
+    for a, keep in ((act, True), ("silu", False), (ACTS[(M + 4) % 5], True)):
+        Z = torch.empty(M, 2 * inter, dtype=torch.bfloat16, device=DEV) if keep else None
+        H = bsg.gemm_bf16_glu(X, W, act=a, preact=Z)
+        want, err, wz, ez = dense.glu_forward(z, mag, K, a)
+        _near(H, want, err, f"{a}, kept {keep}")
+        if keep:
+            _near(Z, wz, ez, "pre-activations")
+
+
+@pytest.mark.parametrize("M,inter,K", [(40, 200, 1040), (300, 520, 72), (4000, 1720, 40)])
+def test_glu_strides(M, inter, K):
+    for pad, shift in ((8, 0), (3, 1)):
+        _say(f"gemm_bf16_glu {M}x{inter}x{K} rows {pad} apart from {shift}")
+        g = torch.Generator(device=DEV).manual_seed(pad)
+        X, W = _mat(g, M, K, pad=8), _mat(g, 2 * inter, K, pad=16, shift=8, by=K ** -0.5)
+        bh = torch.full((M * (inter + pad) + shift,), 7.0, dtype=torch.bfloat16, device=DEV)
+        bz = torch.full((M * (2 * inter + pad) + shift,), 7.0, dtype=torch.bfloat16, device=DEV)
+        H, Z = bh[shift:].view(M, -1)[:, :inter], bz[shift:].view(M, -1)[:, :2 * inter]
+        need = bsg.lib().gemm_bf16_glu_workspace(M, inter, K)
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
+        assert bsg.gemm_bf16_glu(X, W, out=H, preact=Z, workspace=ws) is H
+        want, err, wz, ez = dense.glu_forward(*_z(X, W), K)
+        _near(H, want, err, "H")
+        _near(Z, wz, ez, "Z")
+        assert torch.all(bh[:shift] == 7) and torch.all(bh[shift:].view(M, -1)[:, inter:] == 7)
+        assert torch.all(bz[:shift] == 7) and torch.all(bz[shift:].view(M, -1)[:, 2 * inter:] == 7)
+        assert torch.all(ws[need:] == 255)
+
+
+BWD = [(1, 1, 8), (1, 300, 2048), (3, 5, 40), (64, 7, 264), (40, 2048, 1024), (130, 257, 1000), (1001, 1003, 520),
+       (600, 128, 3400), (3900, 131, 3400), (3900, 3401, 136), (97, 3457, 3841 // 8 * 8)]
+
+
+@pytest.mark.parametrize("M,N,K", BWD)
+def test_act_backward(M, N, K):
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    A, B = _mat(g, M, K, pad=8), _mat(g, N, K, by=N ** -0.5)
+    for act, pad in ((ACTS[(M + 1) % 5], 0), ("none", 0), ("none", 3), ("gelu", 1)):
+        _say(f"gemm_bf16_act_backward {M}x{N}x{K} {act}, rows {pad} apart")
+        dD, Z = _mat(g, M, N, pad=pad), _mat(g, M, N, pad=pad, by=2.0)
+        got = bsg.gemm_bf16_act_backward(dD, A, B, Z if act != "none" else None, act=act)
+        want = dense.act_backward(_f64(dD), _f64(Z), _f64(A), _f64(B), act)
+        for name, out, (w, e) in zip(("dA", "dB", "dbias"), got, want):
+            assert out.dtype == (torch.float32 if name == "dbias" else torch.bfloat16)
+            _near(out, w, e + (dense.U * np.abs(w) if name == "dbias" else 0), f"{act} {name}", name != "dbias")
+    for need in ((True, False, False), (False, True, False), (False, False, True)):
+        part = bsg.gemm_bf16_act_backward(dD, A, B, Z, act="gelu", need=need)
+        for n, p, w in zip(need, part, got):
+            assert torch.equal(p, w) if n else p is None
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_backward_every_activation(act):
+    """Both tails of every derivative, in the plain and the gated form."""
+    M, N, K = 70, 136, 64
+    g = torch.Generator(device=DEV).manual_seed(4)
+    A, B, dD = _mat(g, M, K), _mat(g, N, K), _mat(g, M, N)
+    Z = _mat(g, M, N, by=4.0)
+    Z[0] = torch.linspace(-40, 40, N).to(torch.bfloat16)
+    Z[1, :6] = torch.tensor([0.0, -0.0, 3e4, -3e4, 1e30, -1e30]).to(torch.bfloat16)
+    got = bsg.gemm_bf16_act_backward(dD, A, B, Z, act=act)
+    for out, (w, e), r in zip(got, dense.act_backward(_f64(dD), np.clip(_f64(Z), -1e3, 1e3), _f64(A), _f64(B), act),
+                              (True, True, False)):
+        _near(out, w, e + (0 if r else dense.U * np.abs(w)), act, r)
+    Z2 = torch.cat([Z, _mat(g, M, N)], 1)
+    W = _mat(g, 2 * N, K)
+    Z2[1, :6] = 0
+    got = bsg.gemm_bf16_glu_backward(dD, A, W, Z2, act=act)
+    for out, (w, e) in zip(got, dense.glu_backward(_f64(dD), _f64(Z2), _f64(A), _f64(W), act)):
+        _near(out, w, e, "gated " + act)
+
+
+@pytest.mark.parametrize("M,inter,K", [(1, 8, 8), (1, 1000, 264), (33, 40, 1000), (777, 1000, 1032), (130, 520, 72),
+                                       (3900, 64, 3400), (4000, 1720, 136)])
+def test_glu_backward(M, inter, K):
+    g = torch.Generator(device=DEV).manual_seed(M + inter + K)
+    X, W = _mat(g, M, K), _mat(g, 2 * inter, K, pad=8, by=inter ** -0.5)
+    for act, pad in ((ACTS[(M + 1) % 5], 0), ("silu", 3)):
+        _say(f"gemm_bf16_glu_backward {M}x{inter}x{K} {act}, rows {pad} apart")
+        dH, Z = _mat(g, M, inter, pad=pad), _mat(g, M, 2 * inter, pad=pad)
+        got = bsg.gemm_bf16_glu_backward(dH, X, W, Z, act=act)
+        want = dense.glu_backward(_f64(dH), _f64(Z), _f64(X), _f64(W), act)
+        for name, out, (w, e) in zip(("dX", "dW13"), got, want):
+            _near(out, w, e, f"{act} {name}")
+    assert bsg.gemm_bf16_glu_backward(dH, X, W, Z, need=(True, False))[1] is None
+    assert torch.equal(bsg.gemm_bf16_glu_backward(dH, X, W, Z, need=(False, True))[1], got[1])
+
+
+def test_gradients_against_differences():
+    """The forward calls' outputs along a direction: their difference quotient against the
+    backward calls' gradients.  D is affine in bias, and in A and B between the two points
+    for act none; with an activation the direction is that of the bias, a step h = 2^-3 and
+    |f''| < 1.2 leave at most 1.2 h^2 / 2 per element and the outputs' roundings 2^-8 |D|
+    each over 2h."""
+    M, N, K = 40, 96, 128
+    g = torch.Generator(device=DEV).manual_seed(9)
+    A, B = _mat(g, M, K), _mat(g, N, K, by=K ** -0.5)
+    dD = _mat(g, M, N)
+    h = 0.125
+    w = _f64(dD)
+    for act in ACTS[2:]:
+        b0 = torch.zeros(N, dtype=torch.bfloat16, device=DEV)
+        Z = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+        bsg.gemm_bf16_act(A, B, bias=b0, act=act, preact=Z)
+        lo, hi = (_f64(bsg.gemm_bf16_act(A, B, bias=b0 + s, act=act)) for s in (-h, h))
+        db = _f64(bsg.gemm_bf16_act_backward(dD, A, B, Z, act=act, need=(False, False, True))[2])
+        diff = (w * (hi - lo)).sum(0) / (2 * h)
+        # (z itself is kept in bf16: |f''| 2^-8 |z| more)
+        tol = (np.abs(w) * (1.2 * h * h / 2 + U8 * (np.abs(hi) + np.abs(lo)) / (2 * h) + 1.2 * U8 * np.abs(_f64(Z)))).sum(0)
+        assert np.all(np.abs(diff - db) <= tol), act
+    # the gated block is linear in the up rows
+    inter = N // 2
+    W = _mat(g, 2 * inter, K, by=K ** -0.5)
+    dH = _mat(g, M, inter)
+    dirw = _mat(g, inter, K, by=K ** -0.5)
+    Z = torch.empty(M, 2 * inter, dtype=torch.bfloat16, device=DEV)
+    bsg.gemm_bf16_glu(A, W, preact=Z)
+    W1, W2 = W.clone(), W.clone()
+    W1[inter:], W2[inter:] = 0, dirw
+    h2 = _f64(bsg.gemm_bf16_glu(A, W2))
+    dW = _f64(bsg.gemm_bf16_glu_backward(dH, A, W, Z)[1])[inter:]
+    assert torch.all(bsg.gemm_bf16_glu(A, W1) == 0)
+    want = (_f64(dH) * h2).sum()
+    got = (dW * _f64(dirw)).sum()
+    f = np.abs(dense.f(_f64(Z)[:, :inter], "silu"))
+    mag = (np.abs(_f64(dH)) * np.abs(h2)).sum() * U8
+    # roundings: h2, the kept gate (slope < 1.13), bf16 dz, bf16 dW
+    up = np.abs(_f64(A) @ _f64(dirw).T)
+    tol = mag + (np.abs(_f64(dH)) * up * U8 * (1.13 * np.abs(_f64(Z)[:, :inter]) + f)).sum() + \
+        U8 * (np.abs(dW) * np.abs(_f64(dirw))).sum()
+    assert abs(want - got) <= tol
+
+
+def test_empty_and_zero_k():
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=DEV)
+    assert bsg.gemm_bf16_act(e(0, 64), e(8, 64)).shape == (0, 8)
+    assert bsg.gemm_bf16_act(e(4, 64), e(0, 64)).shape == (4, 0)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    bias, R = _mat(g, 1, 300)[0], _mat(g, 70, 300)
+    Z = e(70, 300)
+    D = bsg.gemm_bf16_act(e(70, 0), e(300, 0), bias=bias, act="silu", residual=R, preact=Z)
+    want, err, _, _ = dense.act_forward(np.zeros((70, 300)), np.zeros((70, 300)), 0, _f64(bias), "silu", _f64(R))
+    _near(D, want, err, "K = 0")
+    assert torch.equal(Z, bias.expand(70, 300))
+    assert torch.all(bsg.gemm_bf16_glu(e(70, 0), e(64, 0)) == 0)
+    assert bsg.gemm_bf16_glu(e(0, 64), e(16, 64)).shape == (0, 8)
+    assert bsg.gemm_bf16_glu(e(3, 64), e(0, 64)).shape == (3, 0)
+    # no rows: zero weight gradients; no columns: a zero input gradient
+    dA, dB, db = bsg.gemm_bf16_act_backward(e(0, 24), e(0, 64), e(24, 64), e(0, 24), act="gelu")
+    assert dA.shape == (0, 64) and torch.all(dB == 0) and torch.all(db == 0)
+    dA, dB, db = bsg.gemm_bf16_act_backward(e(5, 0), e(5, 64), e(0, 64), e(5, 0), act="gelu")
+    assert torch.all(dA == 0) and dB.shape == (0, 64) and db.shape == (0,)
+    dA, dB, db = bsg.gemm_bf16_act_backward(R, e(70, 0), e(300, 0))
+    assert dA.shape == (70, 0) and dB.shape == (300, 0)
+    _near(db, _f64(R).sum(0), 74 * dense.U * np.abs(_f64(R)).sum(0), "dbias, K = 0", rounded=False)
+    dX, dW = bsg.gemm_bf16_glu_backward(e(0, 8), e(0, 64), e(16, 64), e(0, 16))
+    assert dX.shape == (0, 64) and torch.all(dW == 0)
+    dX, dW = bsg.gemm_bf16_glu_backward(e(3, 0), e(3, 64), e(0, 64), e(3, 0))
+    assert torch.all(dX == 0) and dW.shape == (0, 64)
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    """A row of A full of NaN, a NaN row of B and an infinite residual touch their own
+    outputs only, in every form and in the gradients."""
+    for M, N, K in ((40, 200, 1040), (300, 520, 72), (3900, 3400, 40)):
+        g = torch.Generator(device=DEV).manual_seed(2)
+        A, B, R = _mat(g, M, K), _mat(g, N, K, by=K ** -0.5), _mat(g, M, N)
+        want = bsg.gemm_bf16_act(A, B, act="gelu", residual=R)
+        A2, B2, R2 = A.clone(), B.clone(), R.clone()
+        A2[3], B2[7], R2[5, 11] = float("nan"), float("nan"), float("inf")
+        got = bsg.gemm_bf16_act(A2, B2, act="gelu", residual=R2)
+        assert torch.all(torch.isnan(got[3])) and torch.all(torch.isnan(got[:, 7])) and got[5, 11] == float("inf")
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[3], keep[:, 7], keep[5, 11] = False, False, False
+        assert torch.equal(got[keep], want[keep])
+        for act in ACTS:
+            assert torch.all(torch.isnan(bsg.gemm_bf16_act(A2, B, act=act)[3])), act
+        # gradients: a NaN row of dD reaches its row of dA, all of dB; rows past the end none
+        dD, Z = _mat(g, M, N), _mat(g, M, N)
+        want = bsg.gemm_bf16_act_backward(dD, A, B, Z, act="silu")[0]
+        dD2 = dD.clone()
+        dD2[3] = float("nan")
+        got = bsg.gemm_bf16_act_backward(dD2, A, B, Z, act="silu")[0]
+        assert torch.all(torch.isnan(got[3]))
+        rest = torch.arange(M, device=DEV) != 3
+        assert torch.equal(got[rest], want[rest])
+
+
+def test_what_lies_behind_the_operands():
+    """Operands cut out of buffers full of NaN: what lies behind their rows and columns, or
+    after their last row, reaches no output."""
+    nan = float("nan")
+
+    def cut(rows, cols, pad, g):
+        buf = torch.full((rows + 3, cols + pad), nan, dtype=torch.bfloat16, device=DEV)
+        buf[:rows, :cols] = torch.randn(rows, cols, generator=g, device=DEV)
+        return buf[:rows, :cols]
+    for M, N, K in ((40, 203, 1040), (300, 515, 72), (3900, 3403, 40), (3845, 131, 3416)):
+        g = torch.Generator(device=DEV).manual_seed(2)
+        A, B, dD, Z = cut(M, K, 8, g), cut(N, K, 8, g), cut(M, N, 5, g), cut(M, N, 5, g)
+        plain = [t.contiguous() for t in (A, B, dD, Z)]
+        assert torch.equal(bsg.gemm_bf16_act(A, B, act="relu", residual=dD),
+                           bsg.gemm_bf16_act(plain[0], plain[1], act="relu", residual=plain[2]))
+        for act in ("none", "silu"):
+            for x, y in zip(bsg.gemm_bf16_act_backward(dD, A, B, Z, act=act),
+                            bsg.gemm_bf16_act_backward(plain[2], plain[0], plain[1], plain[3], act=act)):
+                assert torch.all(torch.isfinite(x)) and torch.equal(x, y)
+
+
+def _block(X, W13, W2, R, dout=None):
+    """A feed-forward block, and its gradients: what a model does with the calls together."""
+    Z = torch.empty(X.shape[0], W13.shape[0], dtype=torch.bfloat16, device=X.device)
+    H = bsg.gemm_bf16_glu(X, W13, preact=Z)
+    Y = bsg.gemm_bf16_act(H, W2, residual=R)
+    if dout is None:
+        return (Y,)
+    dH, dW2, _ = bsg.gemm_bf16_act_backward(dout, H, W2, need=(True, True, False))
+    dX, dW13 = bsg.gemm_bf16_glu_backward(dH, X, W13, Z)
+    return Y, dX, dW13, dW2
+
+
+@pytest.mark.parametrize("T,hidden,inter", [(1, 512, 256), (37, 1024, 520), (700, 1024, 1032)])
+def test_feed_forward_block(T, hidden, inter):
+    """The calls together: every result against fp64 autograd of the block, within what the
+    bf16 roundings of H, dH, dz and the outputs leave (each at most 2^-8, together 4 of them
+    on any path, in the 2-norm)."""
+    _say(f"block {T} tokens, {hidden} wide, inter {inter}")
+    g = torch.Generator(device=DEV).manual_seed(T)
+    X, R, dout = (_mat(g, T, hidden) for _ in range(3))
+    W13, W2 = _mat(g, 2 * inter, hidden, by=hidden ** -0.5), _mat(g, hidden, inter, by=inter ** -0.5)
+    got = _block(X, W13, W2, R, dout)
+    x, w13, w2 = (t.detach().cpu().double().requires_grad_() for t in (X, W13, W2))
+    p = x @ w13.t()
+    y = R.cpu().double() + (torch.nn.functional.silu(p[:, :inter]) * p[:, inter:]) @ w2.t()
+    want = (y.detach(),) + torch.autograd.grad(y, (x, w13, w2), dout.cpu().double())
+    for name, a, b in zip(("Y", "dX", "dW13", "dW2"), got, want):
+        rel = float((a.cpu().double() - b).norm() / b.norm())
+        _say(f"  {name}: {rel:.1e}")
+        assert rel <= 4 * U8, name
+
+
+def test_block_captured_and_on_streams():
+    """The block captured, replayed several times among eager work, and on two streams at
+    once: the bits of the eager call each time."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    cases = []
+    for T, hidden, inter in ((9, 512, 1024), (200, 1024, 520)):
+        X, R, dout = (_mat(g, T, hidden) for _ in range(3))
+        cases.append((X, _mat(g, 2 * inter, hidden, by=hidden ** -0.5), _mat(g, hidden, inter, by=inter ** -0.5), R, dout))
+    want = [[t.clone() for t in _block(*c)] for c in cases]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _block(*cases[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [_block(*c) for c in cases]
+    for k in range(4):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        graph.replay()
+        eager = _block(*cases[k % 2])
+        torch.cuda.synchronize()
+        for o, w in zip(outs + [eager], want + [want[k % 2]]):
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), k
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    res = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                res[i].append(_block(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in res[i]:
+            assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
+    # a stream passed by hand: work waits in its order
+    s = streams[0]
+    X, W13 = cases[0][:2]
+    H = bsg.gemm_bf16_glu(X, W13, stream=s)
+    s.synchronize()
+    assert torch.equal(H, bsg.gemm_bf16_glu(X, W13))
+
+
+def test_same_bits_on_every_run():
+    g = torch.Generator(device=DEV).manual_seed(5)
+    for M, N, K in ((1, 2048, 2048), (64, 2048, 4096), (500, 1000, 2048), (3900, 3400, 264)):
+        A, B, dD, Z = _mat(g, M, K), _mat(g, N, K), _mat(g, M, N), _mat(g, M, N)
+        first = (bsg.gemm_bf16_act(A, B, act="gelu"),) + bsg.gemm_bf16_act_backward(dD, A, B, Z, act="gelu")
+        for _ in range(3):
+            again = (bsg.gemm_bf16_act(A, B, act="gelu"),) + bsg.gemm_bf16_act_backward(dD, A, B, Z, act="gelu")
+            assert all(torch.equal(a, b) for a, b in zip(first, again))
