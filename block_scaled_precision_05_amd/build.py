@@ -14,7 +14,8 @@ SOURCES = [os.path.join(HERE, "csrc", "api.hip"), os.path.join(HERE, "csrc", "qu
            os.path.join(HERE, "csrc", "mqa.hip"), os.path.join(HERE, "csrc", "route.hip"),
            os.path.join(HERE, "csrc", "lora.hip"), os.path.join(HERE, "csrc", "dense.hip"),
            os.path.join(HERE, "csrc", "dense_bf16.hip"), os.path.join(HERE, "csrc", "dense_fp8.hip"),
-           os.path.join(HERE, "csrc", "dense_fp4.hip"), os.path.join(HERE, "csrc", "dense_strided.hip")]
+           os.path.join(HERE, "csrc", "dense_fp4.hip"), os.path.join(HERE, "csrc", "dense_strided.hip"),
+           os.path.join(HERE, "csrc", "dense_few.hip")]
 PROBE_LIB = os.path.join(HERE, "libbsg_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "probe.hip")]
 BINDING = os.path.join(HERE, "_binding.so")

@@ -1,5 +1,5 @@
 // act_math.h -- activations of the dense products' epilogues, their derivatives, and the
-// finishing of eight consecutive outputs of a row (bias, activation, residual, gate),
+// finishing of consecutive outputs of a row (bias, activation, residual, gate),
 // shared by the matrix kernels' epilogues, the few-row kernel and the kernels that join a
 // split contraction, so that all of them round and evaluate alike.
 //
@@ -16,7 +16,12 @@
 
 namespace bsg {
 
-typedef __attribute__((ext_vector_type(4))) int am_i32x4_t;
+// V consecutive bf16 as one access: 16 bytes (V = 8) or 8 (V = 4).
+template <int V>
+struct Bf16s {
+  typedef __attribute__((ext_vector_type(V / 2))) int t;
+  typedef t any __attribute__((aligned(2)));   // the same at any element of a row
+};
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __bf16 a = (__bf16)lo;   // v_cvt_pk_bf16_f32: round to nearest even
@@ -30,18 +35,52 @@ __device__ __forceinline__ uint16_t bf16_of(float v) {
 
 __device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
-// The eight bf16 of a 16-byte vector.
-__device__ __forceinline__ void unpack8(const am_i32x4_t& v, float (&x)[8]) {
+template <int V>
+__device__ __forceinline__ void unpack(const typename Bf16s<V>::t& v, float (&x)[V]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < V / 2; ++j) {
     x[2 * j] = __uint_as_float((uint32_t)v[j] << 16);
     x[2 * j + 1] = __uint_as_float((uint32_t)v[j] & 0xFFFF0000u);
   }
 }
 
-__device__ __forceinline__ am_i32x4_t pack8(const float (&x)[8]) {
-  return (am_i32x4_t){(int)pack_bf16x2(x[0], x[1]), (int)pack_bf16x2(x[2], x[3]), (int)pack_bf16x2(x[4], x[5]),
-                      (int)pack_bf16x2(x[6], x[7])};
+template <int V>
+__device__ __forceinline__ typename Bf16s<V>::t pack(const float (&x)[V]) {
+  typename Bf16s<V>::t v;
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) v[j] = (int)pack_bf16x2(x[2 * j], x[2 * j + 1]);
+  return v;
+}
+
+// V consecutive bf16 at any element of a row: where all V exist one access, which the
+// hardware takes at any even address, else the cnt that do, one by one (the rest read 0).
+template <int V>
+__device__ __forceinline__ typename Bf16s<V>::t load_bf16s(const uint16_t* p, int cnt) {
+  typename Bf16s<V>::t v;
+  if (cnt >= V) {
+    v = *(const typename Bf16s<V>::any*)p;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j)
+      v[j] = (2 * j < cnt ? p[2 * j] : 0) | (uint32_t)(2 * j + 1 < cnt ? p[2 * j + 1] : 0) << 16;
+  }
+  return v;
+}
+
+// Stores carry the non-temporal hint where every row is aligned (vec): outputs are written
+// once here and read, if at all, by another kernel.
+template <int V>
+__device__ __forceinline__ void store_bf16s(uint16_t* p, const float (&x)[V], bool vec, int cnt) {
+  if (cnt >= V) {
+    if (vec)
+      __builtin_nontemporal_store(pack<V>(x), (typename Bf16s<V>::t*)p);
+    else
+      *(typename Bf16s<V>::any*)p = pack<V>(x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < cnt) p[e] = bf16_of(x[e]);
+  }
 }
 
 // e^x through the hardware's 2^x; inf and 0 past the range.
@@ -130,64 +169,39 @@ __device__ __forceinline__ void with_act(int act, F body) {
   }
 }
 
-// Eight consecutive outputs of a row: z (bias already added) -> Z, D = R + f(z).  Z and R
-// may be null.  vec: all eight exist and every given row takes 16-byte accesses; r16 then
-// holds the residual's eight values.  Otherwise cnt of the eight exist, accessed one by
-// one.  Z and D carry the non-temporal hint: they are written once here and read, if at
-// all, by another kernel.
-__device__ __forceinline__ void act_row8(int act, float (&z)[8], uint16_t* Z, const uint16_t* R,
-                                         const am_i32x4_t& r16, uint16_t* D, bool vec, int cnt) {
-  if (Z) {
-    if (vec)
-      __builtin_nontemporal_store(pack8(z), (am_i32x4_t*)Z);
-    else
-      for (int e = 0; e < 8; ++e)
-        if (e < cnt) Z[e] = bf16_of(z[e]);
-  }
+// V consecutive outputs of a row, cnt of which exist: z (bias already added) -> Z,
+// D = r + f(z).  Z may be null; r holds the residual (zeros without one).
+template <int V>
+__device__ __forceinline__ void act_row(int act, float (&z)[V], uint16_t* Z, const typename Bf16s<V>::t& r, bool add,
+                                        uint16_t* D, bool vec, int cnt) {
+  if (Z) store_bf16s<V>(Z, z, vec, cnt);
   with_act(act, [&](auto a) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = act_f<decltype(a)::value>(z[e]);
+    for (int e = 0; e < V; ++e) z[e] = act_f<decltype(a)::value>(z[e]);
   });
-  if (vec) {
-    if (R) {
-      float r[8];
-      unpack8(r16, r);
+  if (add) {
+    float x[V];
+    unpack<V>(r, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += r[e];
-    }
-    __builtin_nontemporal_store(pack8(z), (am_i32x4_t*)D);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < cnt) D[e] = bf16_of(R ? z[e] + bf16_f32(R[e]) : z[e]);
+    for (int e = 0; e < V; ++e) z[e] += x[e];
   }
+  store_bf16s<V>(D, z, vec, cnt);
 }
 
-// Eight consecutive outputs of the gated block: D = f(g) u, Z = [g .. | inter further on: u ..].
-__device__ __forceinline__ void glu_row8(int act, float (&g)[8], const float (&u)[8], uint16_t* Z, int64_t inter,
-                                         uint16_t* D, bool vec) {
+// V consecutive outputs of the gated block (inter is a multiple of 8: all of them exist):
+// D = f(g) u, Z = [g .. | inter further on: u ..].
+template <int V>
+__device__ __forceinline__ void glu_row(int act, float (&g)[V], const float (&u)[V], uint16_t* Z, int64_t inter,
+                                        uint16_t* D, bool vec) {
   if (Z) {
-    if (vec) {
-      __builtin_nontemporal_store(pack8(g), (am_i32x4_t*)Z);
-      __builtin_nontemporal_store(pack8(u), (am_i32x4_t*)(Z + inter));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        Z[e] = bf16_of(g[e]);
-        Z[inter + e] = bf16_of(u[e]);
-      }
-    }
+    store_bf16s<V>(Z, g, vec, V);
+    store_bf16s<V>(Z + inter, u, vec, V);
   }
   with_act(act, [&](auto a) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = act_f<decltype(a)::value>(g[e]) * u[e];
+    for (int e = 0; e < V; ++e) g[e] = act_f<decltype(a)::value>(g[e]) * u[e];
   });
-  if (vec) {
-    __builtin_nontemporal_store(pack8(g), (am_i32x4_t*)D);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) D[e] = bf16_of(g[e]);
-  }
+  store_bf16s<V>(D, g, vec, V);
 }
 
 }  // namespace bsg

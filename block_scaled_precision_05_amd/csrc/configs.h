@@ -44,3 +44,8 @@
 #define BSG_BF16_SMALL_CFG 128, 128, 2, 2, 64, 4, 1
 #define BSG_FP8_SMALL_CFG 128, 256, 1, 4, 64, 6, 1
 #define BSG_FP4_SMALL_CFG 128, 128, 1, 2, 64, 4, 1
+// 256x256 tiles over parts of a contraction: a ring of four stages, so that a part is any
+// multiple of U = 4 stages.
+#define BSG_BF16_PART_CFG 256, 256, 2, 4, 64, 4, 1
+#define BSG_FP8_PART_CFG 256, 256, 2, 4, 64, 4, 1
+#define BSG_FP4_PART_CFG 256, 256, 2, 4, 64, 4, 1

@@ -26,71 +26,118 @@ static const int64_t kMaxTiles = int64_t(1) << 24;
 static const int64_t kMaxRow = (int64_t(1) << 31) / 256 - 1;   // bytes of a row (32-bit offsets)
 static const int64_t kMaxRows = (int64_t(1) << 30) - 1;
 
-DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K) {
-  const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
-  if (big >= 192 || K == 0) return {DENSE_BIG, 1};
-  const int64_t bn = kind == KIND_FP8 ? 256 : 128, cap = kind == KIND_FP8 ? 256 : 512, U = kind == KIND_FP8 ? 6 : 4;
-  const int64_t tiles = (M + 127) / 128 * ((N + bn - 1) / bn);
-  const int64_t bytes = kind == KIND_BF16 ? 2 * K : (kind == KIND_FP8 ? K : K / 2);
-  const int64_t stages = (bytes + 63) / 64;
-  int64_t s = tiles > 0 ? cap / tiles : 1;
-  if (s > stages / (4 * U)) s = stages / (4 * U);
-  if (s <= 1) return {DENSE_SMALL, 1};
-  const int64_t per = ((stages + s - 1) / s + U - 1) / U * U;
-  s = (stages + per - 1) / per;
-  return s > 1 ? DensePlan{DENSE_PART, (int)s} : DensePlan{DENSE_SMALL, 1};
+// What a form costs, in microseconds, fitted to sweeps of every form over 128 to 2048 rows
+// (BF16 7168 x 2048, 2048 x 7168, the gated block and both strided products; FP8 4096 x
+// 7168, 7168 x 2048; FP4 4096 x 7168): time per stage of one tile, rising from few tiles on
+// the GPU to a full round of them, and a fixed part for launch, first stage and epilogue.
+// The parts' fp32 sums pass through memory twice at about 5.5 TB/s, and the join is a
+// launch of its own.
+//   BF16 example, 1024 x 2048 over K = 7168: 256-row tiles 112 us, 128-row tiles 80, 128-row
+//   tiles in 4 parts 44, 256-row tiles in 4 parts 50.
+struct TileCost {
+  int64_t bm, bn, lo_tiles, cap;   // tile, tiles up to which `lo` holds, tiles of a full round
+  double lo, hi, fixed;
+  int round;                       // stages of a round of the ring
+};
+static const TileCost kSmall[3] = {{128, 128, 256, 512, 0.33, 0.42, 5.5, 4},
+                                   {128, 256, 128, 256, 0.38, 0.43, 5.5, 6},
+                                   {128, 128, 256, 512, 0.49, 0.59, 5.5, 4}};
+static const TileCost kBig[3] = {{256, 256, 128, 256, 0.50, 0.60, 8.0, 4},
+                                 {256, 256, 128, 256, 0.55, 0.58, 8.0, 4},
+                                 {256, 256, 128, 256, 0.55, 0.60, 8.0, 4}};
+
+static double tiles_cost(const TileCost& c, int64_t tiles, int64_t stages) {
+  const int64_t full = tiles / c.cap, rest = tiles % c.cap;
+  double t = full * (stages * c.hi + c.fixed);
+  if (rest) {
+    const double x = rest <= c.lo_tiles ? 0.0 : (double)(rest - c.lo_tiles) / (c.cap - c.lo_tiles);
+    t += stages * (c.lo + x * (c.hi - c.lo)) + c.fixed;
+  }
+  return t;
 }
 
-// Joins the parts of a split contraction: one thread finishes eight consecutive columns of
-// a row, 32 bytes of each part.  Bound by the parts' bytes, which mostly come from L2 and
-// the cache behind it, where the product has just written them.
+DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
+  const int64_t bytes = kind == KIND_BF16 ? 2 * K : (kind == KIND_FP8 ? K : K / 2);
+  const int64_t stages = (bytes + 63) / 64;
+  // Few rows: the stream of B through registers.  Up to 32 rows at any K; up to 64 where a
+  // row is at most 8 KiB (64 rows, BF16 7168 x 2048: 12.2 us against 15.8 in parts; 2048 x
+  // 7168: 21.3 against 18.1: every workgroup reads all of A).
+  if (!strided && (M <= 32 || (M <= 64 && bytes <= 8192))) return {DENSE_FEW, 1};
+  DensePlan best = {DENSE_BIG, 1};
+  double t_best = 1e30;
+  for (int big = 0; big < 2; ++big) {
+    const TileCost& c = (big ? kBig : kSmall)[kind];
+    const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
+    const double t1 = tiles_cost(c, tiles, stages);
+    if (t1 < t_best) {
+      t_best = t1;
+      best = {big ? DENSE_BIG : DENSE_SMALL, 1};
+    }
+    // parts of at least 8 stages, all of them in one round
+    for (int64_t s = 2; s <= 16 && s * tiles <= c.cap && 8 * s <= stages; ++s) {
+      const int64_t per = ((stages + s - 1) / s + c.round - 1) / c.round * c.round;
+      if ((stages + per - 1) / per != s) continue;
+      const double t = tiles_cost(c, s * tiles, per) + 3.0 + (8.0 * s + 2.0) * M * N / 5.5e6;
+      if (t < t_best) {
+        t_best = t;
+        best = {big ? DENSE_BIG_PART : DENSE_SMALL_PART, (int)s};
+      }
+    }
+  }
+  return best;
+}
+
+// Joins the parts of a split contraction: one thread finishes four consecutive columns of
+// a row, 16 bytes of each part, four parts' loads at a time.  Bound by the parts' bytes,
+// which mostly come from L2 and the cache behind it, where the product has just written
+// them.
 template <bool GLU>
 __global__ __launch_bounds__(256) void join_kernel(const GemmArgs args) {
   typedef __attribute__((ext_vector_type(4))) float f32x4_t;
-  const int cols = GLU ? args.inter : args.N, per = (cols + 7) / 8;
+  const int cols = GLU ? args.inter : args.N, per = (cols + 3) / 4;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = idx / per;
-  const int n = 8 * (int)(idx - m * per);
+  const int n = 4 * (int)(idx - m * per);
   if (m >= args.M) return;
-  const float* p = args.P + m * args.ldp + n;
-  auto sum = [&](const float* q, float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    for (int s = 0; s < args.splits; ++s, q += args.part_stride) {
-      const f32x4_t lo = *(const f32x4_t*)q, hi = *(const f32x4_t*)(q + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += lo[e];
-        v[4 + e] += hi[e];
-      }
+  const float* const p = args.P + m * args.ldp + n;
+  const int cnt = cols - n < 4 ? cols - n : 4;
+  Bf16s<4>::t r = {0, 0};
+  float b[4] = {};
+  if constexpr (!GLU) {
+    if (args.R) r = load_bf16s<4>(args.R + m * args.ldr + n, cnt);
+    if (args.bias) unpack<4>(load_bf16s<4>(args.bias + n, cnt), b);
+  }
+  auto sum = [&](const float* q, float (&v)[4]) {
+    f32x4_t t = {0, 0, 0, 0};
+    int s = 0;
+    for (; s + 4 <= args.splits; s += 4, q += 4 * args.part_stride) {
+      const f32x4_t a = *(const f32x4_t*)q, c = *(const f32x4_t*)(q + args.part_stride),
+                    d = *(const f32x4_t*)(q + 2 * args.part_stride), e = *(const f32x4_t*)(q + 3 * args.part_stride);
+      t += (a + c) + (d + e);
     }
+    for (; s < args.splits; ++s, q += args.part_stride) t += *(const f32x4_t*)q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
   };
-  const int cnt = cols - n < 8 ? cols - n : 8;
-  const bool vec = args.e_vec && cnt == 8;
-  float z[8];
+  float z[4];
   sum(p, z);
   uint16_t* const Z = args.Z ? args.Z + m * args.ldz + n : nullptr;
   uint16_t* const D = args.D + m * args.ldd + n;
   if constexpr (GLU) {
-    float u[8];
+    float u[4];
     sum(p + args.inter, u);
-    glu_row8(args.act, z, u, Z, args.inter, D, vec);
+    glu_row<4>(args.act, z, u, Z, args.inter, D, args.e_vec);
   } else {
-    const uint16_t* const R = args.R ? args.R + m * args.ldr + n : nullptr;
-    am_i32x4_t r16 = {0, 0, 0, 0};
-    if (R && vec) r16 = *(const am_i32x4_t*)R;
-    if (args.bias)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < cnt) z[e] += bf16_f32(args.bias[n + e]);
-    act_row8(args.act, z, Z, R, r16, D, vec, cnt);
+    for (int e = 0; e < 4; ++e) z[e] += b[e];
+    act_row<4>(args.act, z, Z, r, args.R != nullptr, D, args.e_vec, cnt);
   }
 }
 
 static int launched() { return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP; }
 
 int dense_join(const GemmArgs& a, bool glu, void* stream) {
-  const int64_t per = ((glu ? a.inter : a.N) + 7) / 8, blocks = (a.M * per + 255) / 256;
+  const int64_t per = ((glu ? a.inter : a.N) + 3) / 4, blocks = (a.M * per + 255) / 256;
   if (blocks == 0) return BSG_OK;
   (void)hipGetLastError();
   if (glu)
@@ -100,55 +147,53 @@ int dense_join(const GemmArgs& a, bool glu, void* stream) {
   return launched();
 }
 
-// dz of a block of 256 columns x 64 rows: thread (x, y) takes columns 8x .. 8x+7 of rows y,
-// y + 8, ...  Bound by memory: dD and Z read, dz written, each once.  The columns' sums
-// of dz stay in registers over the rows, then meet in LDS, one partial row a block.
+// dz of a block of 256 columns x `rows` rows (a multiple of 8): thread (x, y) takes columns
+// 8x .. 8x+7 of rows y, y + 8, ...  Bound by memory: dD and Z read, dz written, each once.
+// The columns' sums of dz stay in registers over the rows, then meet in LDS, one partial
+// row a block.
 //   GLU: columns are those of H; dz gets dg there and du inter columns further on.
 //   ldq: leading dimension of dz, a multiple of 8; columns N .. ldq-1 are zeroed (the
 //   products read whole 16-byte chunks).  dz or part may be null.
-constexpr int DZ_ROWS = 64;
 template <bool GLU>
 __global__ __launch_bounds__(256) void dz_kernel(const uint16_t* __restrict__ dD, int64_t lddd,
                                                  const uint16_t* __restrict__ Z, int64_t ldz, uint16_t* __restrict__ dz,
                                                  int64_t ldq, float* __restrict__ part, int64_t M, int64_t N, int act,
-                                                 int vec) {
+                                                 int rows) {
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t per = (N + 255) / 256, by = blockIdx.x / per, bx = blockIdx.x - by * per;
-  const int64_t n = bx * 256 + 8 * x, m0 = by * DZ_ROWS;
+  const int64_t n = bx * 256 + 8 * x, m0 = by * rows;
   const int cnt = N - n >= 8 ? 8 : (N > n ? (int)(N - n) : 0);
-  const bool v16 = vec && cnt == 8;
-  float sum[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-  auto load = [&](const uint16_t* p, float (&v)[8]) {
-    if (v16) {
-      unpack8(*(const am_i32x4_t*)p, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < cnt ? bf16_f32(p[e]) : 0.0f;
-    }
-  };
-  if (n < ldq && cnt > 0) {
-    for (int64_t m = m0 + y; m < m0 + DZ_ROWS && m < M; m += 8) {
+  float sum[8] = {};
+  if (cnt > 0) {
+    const int64_t m1 = m0 + rows < M ? m0 + rows : M;
+    Bf16s<8>::t vd, vz = {}, vw = {};
+    auto load = [&](int64_t m) {
+      vd = load_bf16s<8>(dD + m * lddd + n, cnt);
+      if (act != BSG_ACT_NONE || GLU) vz = load_bf16s<8>(Z + m * ldz + n, cnt);
+      if constexpr (GLU) vw = load_bf16s<8>(Z + m * ldz + N + n, cnt);
+    };
+    if (m0 + y < m1) load(m0 + y);
+    for (int64_t m = m0 + y; m < m1; m += 8) {
       float d[8], z[8], w[8];
-      load(dD + m * lddd + n, d);
-      if (act != BSG_ACT_NONE || GLU) load(Z + m * ldz + n, z);
-      if constexpr (GLU) load(Z + m * ldz + N + n, w);
+      unpack<8>(vd, d);
+      unpack<8>(vz, z);
+      unpack<8>(vw, w);
+      if (m + 8 < m1) load(m + 8);   // the next row's loads run under this row's arithmetic
       with_act(act, [&](auto a) {
         constexpr int A = decltype(a)::value;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          float f;
           if constexpr (GLU) {
-            float f;
             const float df = act_df<A>(z[e], f);
             z[e] = d[e] * w[e] * df;
             w[e] = d[e] * f;
+          } else if constexpr (A == BSG_ACT_NONE) {
+            z[e] = d[e];
+          } else if constexpr (A == BSG_ACT_RELU) {
+            z[e] = z[e] <= 0.0f ? 0.0f : d[e];   // (a select: an infinite dD meets no 0 * inf)
           } else {
-            float f;
-            // (relu: a select, so that an infinite dD meets no 0 * inf)
-            if constexpr (A == BSG_ACT_NONE) z[e] = d[e];
-            else if constexpr (A == BSG_ACT_RELU) z[e] = z[e] <= 0.0f ? 0.0f : d[e];
-            else z[e] = d[e] * act_df<A>(z[e], f);
+            z[e] = d[e] * act_df<A>(z[e], f);
           }
         }
       });
@@ -157,8 +202,8 @@ __global__ __launch_bounds__(256) void dz_kernel(const uint16_t* __restrict__ dD
         if (e >= cnt) z[e] = 0.0f;
         sum[e] += z[e];
       }
-      if (dz) *(am_i32x4_t*)(dz + m * ldq + n) = pack8(z);
-      if constexpr (GLU) *(am_i32x4_t*)(dz + m * ldq + N + n) = pack8(w);
+      if (dz) *(Bf16s<8>::t*)(dz + m * ldq + n) = pack<8>(z);
+      if constexpr (GLU) *(Bf16s<8>::t*)(dz + m * ldq + N + n) = pack<8>(w);
     }
   }
   if constexpr (!GLU) {
@@ -175,6 +220,13 @@ __global__ __launch_bounds__(256) void dz_kernel(const uint16_t* __restrict__ dD
   }
 }
 
+// Rows of a dz block: 64, or fewer where that leaves less than four blocks a CU.
+static int dz_rows(int64_t M, int64_t N) {
+  int rows = 64;
+  while (rows > 8 && (M + rows - 1) / rows * ((N + 255) / 256) < 1024) rows /= 2;
+  return rows;
+}
+
 // dbias from the blocks' partial rows: a block sums 32 columns, eight rows at a time.
 __global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int64_t rows, int64_t N,
                                                     float* __restrict__ dbias) {
@@ -183,6 +235,7 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ pa
   const int64_t n = (int64_t)blockIdx.x * 32 + x;
   float t = 0.0f;
   if (n < N)
+#pragma unroll 4
     for (int64_t r = y; r < rows; r += 8) t += part[r * N + n];
   s[y][x] = t;
   __syncthreads();
@@ -252,7 +305,7 @@ static int act_args(GemmArgs& a, int kind, const void* bias, int32_t act, const 
   a.ldp = dense_ldp(N);
   a.part_stride = M * a.ldp;
   a.splits = plan.splits;
-  a.e_vec = al16(D, ldd) && (!R || al16(R, ldr)) && (!Z || al16(Z, ldz));
+  a.e_vec = al16(D, ldd) && (!Z || al16(Z, ldz));
   return BSG_OK;
 }
 
@@ -292,8 +345,8 @@ int gemm_bf16_act(const void* A, int64_t lda, const void* B, int64_t ldb, const 
   a.lda = K ? lda * 2 : 0;
   a.ldb = K ? ldb * 2 : 0;
   a.k_bytes = (int32_t)(2 * K);
-  st = dense_bf16(a, plan.form, EPI_ACT, stream);
-  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+  st = plan.form == DENSE_FEW ? dense_few(KIND_BF16, a, false, stream) : dense_bf16(a, plan.form, EPI_ACT, stream);
+  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
 }
 
 int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
@@ -321,8 +374,9 @@ int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa,
   a.k_bytes = (int32_t)K;
   a.kp_count = (int32_t)((K / 128 + 1) / 2);
   a.sfb_rows = (int32_t)sfb_rows;
-  st = dense_fp8(a, plan.form, (K && sv_ok(sfa, ld_sfa) ? 1 : 0) + (sfb_gran_mn == 1 ? 2 : 0), stream);
-  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+  st = plan.form == DENSE_FEW ? dense_few(KIND_FP8, a, false, stream)
+                              : dense_fp8(a, plan.form, (K && sv_ok(sfa, ld_sfa) ? 1 : 0) + (sfb_gran_mn == 1 ? 2 : 0), stream);
+  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
 }
 
 int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
@@ -348,8 +402,9 @@ int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa,
   a.k_bytes = (int32_t)(K / 2);
   a.kp_count = (int32_t)((K / 32 + 1) / 2);
   a.sfb_rows = (int32_t)N;
-  st = dense_fp4(a, plan.form, K && sv_ok(sfa, ld_sfa) && sv_ok(sfb, ld_sfb) ? 1 : 0, stream);
-  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+  st = plan.form == DENSE_FEW ? dense_few(KIND_FP4, a, false, stream)
+                              : dense_fp4(a, plan.form, K && sv_ok(sfa, ld_sfa) && sv_ok(sfb, ld_sfb) ? 1 : 0, stream);
+  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
 }
 
 int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int32_t act, void* H, int64_t ldh,
@@ -389,8 +444,8 @@ int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int3
   a.part_stride = M * a.ldp;
   a.splits = plan.splits;
   a.e_vec = al16(H, ldh) && (!Z || al16(Z, ldz));
-  st = dense_bf16(a, plan.form, EPI_GLU, stream);
-  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, true, stream) : st;
+  st = plan.form == DENSE_FEW ? dense_few(KIND_BF16, a, true, stream) : dense_bf16(a, plan.form, EPI_GLU, stream);
+  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, true, stream) : st;
 }
 
 }  // extern "C"
@@ -402,7 +457,7 @@ namespace bsg {
 static int strided(int tr, const void* A, int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, int64_t M,
                    int64_t N, int64_t K, void* ws, void* stream) {
   if (M == 0 || N == 0) return BSG_OK;
-  const DensePlan plan = dense_plan(KIND_BF16, M, N, K);
+  const DensePlan plan = dense_plan(KIND_BF16, M, N, K, true);
   GemmArgs a = {};
   a.A = (const uint8_t*)A;
   a.B = (const uint8_t*)B;
@@ -422,11 +477,11 @@ static int strided(int tr, const void* A, int64_t lda, const void* B, int64_t ld
   a.splits = plan.splits;
   a.e_vec = al16(D, ldd);
   const int st = dense_strided(a, plan.form, tr, stream);
-  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
+  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
 }
 
 static int64_t strided_bytes(int64_t M, int64_t N, int64_t K) {
-  return M > 0 && N > 0 ? dense_part_bytes(dense_plan(KIND_BF16, M, N, K), M, N) : 0;
+  return M > 0 && N > 0 ? dense_part_bytes(dense_plan(KIND_BF16, M, N, K, true), M, N) : 0;
 }
 
 static int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
@@ -434,11 +489,13 @@ static int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 // Workspace of a backward pass: dz [M][ldq], the bias's partial rows, the larger of the two
 // products' parts (they run one after the other).
 struct GradSpace {
-  int64_t ldq, part_at, sums_at, bytes;
+  int64_t ldq, rows, blocks, part_at, sums_at, bytes;
   GradSpace(int64_t M, int64_t cols, int64_t K, bool bias) {
     ldq = (cols + 7) / 8 * 8;
     part_at = 2 * M * ldq;
-    sums_at = part_at + (bias ? up16(4 * ((M + DZ_ROWS - 1) / DZ_ROWS) * cols) : 0);
+    rows = dz_rows(M, bias ? cols : cols / 2);
+    blocks = (M + rows - 1) / rows;
+    sums_at = part_at + (bias ? up16(4 * blocks * cols) : 0);
     const int64_t p = strided_bytes(M, K, cols), q = strided_bytes(cols, K, M);
     bytes = sums_at + (p > q ? p : q);
   }
@@ -456,7 +513,7 @@ static int grad_products(const void* dz, int64_t ldq, const void* A, int64_t lda
 static int check_grad(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0) return BSG_ERR_INVALID_ARG;
   if (K % 8 || M > kMaxRows || 2 * (N + 7) > kMaxRow || 2 * K > kMaxRow) return BSG_ERR_UNSUPPORTED_SHAPE;
-  if ((M + DZ_ROWS - 1) / DZ_ROWS * ((N + 255) / 256) >= kMaxTiles) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if ((M + 63) / 64 * ((N + 255) / 256) >= kMaxTiles) return BSG_ERR_UNSUPPORTED_SHAPE;
   int st = check_tiles(M, N);
   if (st == BSG_OK) st = check_tiles(M, K);
   return st == BSG_OK ? check_tiles(N, K) : st;
@@ -496,20 +553,19 @@ int gemm_bf16_act_backward(const void* dD, int64_t lddd, const void* Z, int64_t 
   // without an activation an aligned dD is dz itself
   const bool own = act == BSG_ACT_NONE && al16(dD, lddd) && N % 8 == 0 && 2 * lddd <= kMaxRow;
   const void* const dz = own ? dD : ws;
-  const int64_t ldq = own ? lddd : w.ldq, blocks = (M + DZ_ROWS - 1) / DZ_ROWS;
+  const int64_t ldq = own ? lddd : w.ldq;
   float* const part = (float*)(ws + w.part_at);
   const bool products = dA || dB;
   (void)hipGetLastError();
   if (M > 0 && N > 0 && (dbias || (products && !own))) {
-    const int vec = al16(dD, lddd) && (act == BSG_ACT_NONE || al16(Z, ldz));
-    hipLaunchKernelGGL(dz_kernel<false>, dim3((unsigned)((N + 255) / 256 * blocks)), dim3(256), 0,
+    hipLaunchKernelGGL(dz_kernel<false>, dim3((unsigned)((N + 255) / 256 * w.blocks)), dim3(256), 0,
                        (hipStream_t)stream, (const uint16_t*)dD, lddd, (const uint16_t*)Z, ldz,
-                       products && !own ? (uint16_t*)ws : nullptr, w.ldq, dbias ? part : nullptr, M, N, act, vec);
+                       products && !own ? (uint16_t*)ws : nullptr, w.ldq, dbias ? part : nullptr, M, N, act, (int)w.rows);
     st = launched();
     if (st != BSG_OK) return st;
   }
   if (dbias && N > 0) {
-    hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, (hipStream_t)stream, part, blocks,
+    hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, (hipStream_t)stream, part, w.blocks,
                        N, dbias);
     st = launched();
     if (st != BSG_OK) return st;
@@ -539,10 +595,9 @@ int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t 
   uint8_t* const ws = (uint8_t*)workspace;
   if (M > 0 && inter > 0) {
     (void)hipGetLastError();
-    const int vec = al16(dH, lddh) && al16(Z, ldz);
-    hipLaunchKernelGGL(dz_kernel<true>, dim3((unsigned)((inter + 255) / 256 * ((M + DZ_ROWS - 1) / DZ_ROWS))),
+    hipLaunchKernelGGL(dz_kernel<true>, dim3((unsigned)((inter + 255) / 256 * w.blocks)),
                        dim3(256), 0, (hipStream_t)stream, (const uint16_t*)dH, lddh, (const uint16_t*)Z, ldz,
-                       (uint16_t*)ws, w.ldq, nullptr, M, inter, act, vec);
+                       (uint16_t*)ws, w.ldq, nullptr, M, inter, act, (int)w.rows);
     st = launched();
     if (st != BSG_OK) return st;
   }

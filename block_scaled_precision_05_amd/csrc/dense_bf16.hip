@@ -11,7 +11,8 @@ namespace bsg {
 
 int dense_bf16(const GemmArgs& a, int form, int epi, void* stream) {
   const hipStream_t st = (hipStream_t)stream;
-  if (form == DENSE_PART) return launch<KIND_BF16, BSG_BF16_SMALL_CFG, false, 0, EPI_PART>(a, st);
+  if (form == DENSE_SMALL_PART) return launch<KIND_BF16, BSG_BF16_SMALL_CFG, false, 0, EPI_PART>(a, st);
+  if (form == DENSE_BIG_PART) return launch<KIND_BF16, BSG_BF16_PART_CFG, false, 0, EPI_PART>(a, st);
   if (epi == EPI_GLU)
     return form == DENSE_BIG ? launch<KIND_BF16, BSG_BF16_CFG, false, 0, EPI_GLU>(a, st)
                              : launch<KIND_BF16, BSG_BF16_SMALL_CFG, false, 0, EPI_GLU>(a, st);

@@ -1,0 +1,259 @@
+// dense_few.hip -- the dense products with epilogues for few rows (a decode step): up to 64
+// rows of A, where the product is a stream of B from memory.
+//
+// One workgroup of W waves owns 16 NF rows of B (16 NF columns of D; in the gated block 16
+// gate rows and their 16 up rows) and shares out the contraction: wave w takes the
+// 128-byte steps w, w + W, ... of every row.  A wave loads a batch of UN steps into
+// registers, four lanes to 64 consecutive bytes of a row, while the batch before it goes
+// through the wave's own LDS pieces into fragments and the matrix cores; no barrier until
+// the end.  (Loaded straight into the fragments' layout, neighbouring lanes hold different
+// rows, and the CU's address unit takes 64 cycles for a load instead of 16: one row, 512 x
+// 7168: 10.7 us against 7.9; 32 rows: 27 against 13.)  The waves' sums meet in LDS in the
+// order of the waves (the same bits on every run), and the epilogue finishes four
+// consecutive columns a lane.
+//
+// Bound by the stream of B once that is long (one row, gated 2 x 2048 x 7168: 58.7 MB in
+// 13.0 us, 4.5 TB/s), by launch and first access when short (7.3 MB: 6.7 us), and from
+// some 32 rows on by A, which every workgroup reads whole.
+//
+// Fragments (16x16x32 BF16, 16x16x128 FP8 and FP4): lane l holds row l % 16, bytes
+// 64 h + 16 (l / 16) .. +15 of the step (piece h = 0, 1).  For BF16 and FP4 each piece
+// feeds one instruction, for FP8 both feed one; the order of K inside an instruction is the same
+// for both operands and does not matter otherwise.  Scales: an FP8 step is one 128-wide
+// K-block, an FP4 lane's 16 bytes one 32-wide block, so each lane loads the scale byte of
+// its row and block.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/bsg.h"
+#include "act_math.h"
+#include "gemm_kernel.h"
+#include "internal.h"
+
+namespace bsg {
+
+typedef __attribute__((ext_vector_type(4))) float few_f32x4_t;
+
+template <int KIND, int MF, int NF, bool GLU, int W, int UN>
+__global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
+  static_assert(!GLU || (KIND == KIND_BF16 && NF == 2), "gate and up fragment");
+  constexpr int NO = GLU ? 1 : NF;          // output fragments along N
+  // a wave's batch on its way to the fragments; at the end its sums
+  constexpr int PIECES = UN * 2 * (MF + NF);
+  static_assert(MF * NF <= PIECES, "the sums take the batch's place");
+  __shared__ __attribute__((aligned(16))) i32x4_t smem[W][PIECES][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int n_lim = GLU ? args.inter : args.N;
+  const int n0 = blockIdx.x * (16 * NO);
+  const int rows_n = n_lim - n0 < 16 * NO ? n_lim - n0 : 16 * NO;
+
+  // the epilogue's part of this thread: fragment (fm, fn), row m, columns n .. n+3
+  const int fq = tid >> 6, fm = fq / NO, fn = fq % NO;
+  const int m = 16 * fm + r16, n = n0 + 16 * fn + 4 * lg;
+  const bool mine = fq < MF * NO && m < args.M && n < n_lim;
+  const int cnt = n_lim - n < 4 ? n_lim - n : 4;
+  Bf16s<4>::t res = {0, 0};
+  float bias[4] = {};
+  if (!GLU && mine) {
+    if (args.R) res = load_bf16s<4>(args.R + (int64_t)m * args.ldr + n, cnt);
+    if (args.bias) unpack<4>(load_bf16s<4>(args.bias + n, cnt), bias);
+  }
+
+  // records end with the operands' last byte: rows past M or N read zero
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(args.A, (uint32_t)((args.M - 1) * args.lda + args.k_bytes));
+  const uint8_t* const B0 = args.B + (int64_t)n0 * args.ldb;
+  const uint32_t rec_b = (uint32_t)((rows_n - 1) * args.ldb + args.k_bytes);
+  const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(B0, rec_b);
+  const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(GLU ? B0 + (int64_t)args.inter * args.ldb : B0, rec_b);
+  uint32_t va[MF], vb[NF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) va[f] = (uint32_t)((16 * f + (lane >> 2)) * args.lda) + 16 * (lane & 3);
+#pragma unroll
+  for (int f = 0; f < NF; ++f) vb[f] = (uint32_t)(((GLU ? 0 : 16 * f) + (lane >> 2)) * args.ldb) + 16 * (lane & 3);
+  // piece (16 rows x 64 bytes): row r's chunk c at 4r + (c ^ (r >> 2)), so that both the
+  // stores (4 rows of 4 chunks) and the fragment reads (one chunk of 16 rows) of 16 lanes
+  // cover all banks once
+  const int put = (lane & ~3) | ((lane & 3) ^ ((lane >> 4) & 3)), get = 4 * r16 + (lg ^ (r16 >> 2));
+
+  // scale bytes: packed word of (K-block pair, row), the block's byte of it
+  const __amdgpu_buffer_rsrc_t rsa =
+      make_rsrc(args.sfa, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfa + args.M)));
+  const __amdgpu_buffer_rsrc_t rsb =
+      make_rsrc(args.sfb, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfb + args.sfb_rows)));
+  const bool b_row = KIND == KIND_FP4 || args.sfb_rows == args.N;
+  const int kblocks = KIND == KIND_FP8 ? args.k_bytes / 128 : args.k_bytes / 16;
+  auto scale = [&](const __amdgpu_buffer_rsrc_t& rs, int64_t ld, int row, int kb) {
+    const uint32_t off = 2u * ((uint32_t)(kb >> 1) * (uint32_t)ld + (uint32_t)row) + (kb & 1);
+    const uint32_t b = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, off, 0, 0);
+    return kb < kblocks ? b : 127u;   // (past K: the data are zeros, the scale must be finite)
+  };
+
+  few_f32x4_t acc[MF][NF] = {};
+  const int steps = (args.k_bytes + 127) / 128;
+  constexpr int NSC = KIND == KIND_BF16 ? 0 : (KIND == KIND_FP8 ? 1 : 2);   // scale bytes a fragment and step
+  // Two batches of UN steps a wave: one is multiplied while the other's loads are in flight.
+  struct Batch {
+    i32x4_t a[UN][2][MF], b[UN][2][NF];
+    uint32_t sa[UN][NSC ? NSC : 1][MF], sb[UN][NSC ? NSC : 1][NF];
+  };
+  auto load = [&](Batch& t, int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int s = s0 + u * W;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t k = 128u * s + 64 * h;
+        // past K (and past the last step) the offset leaves every record
+        const uint32_t oob = (int)(k + 16 * (lane & 3)) < args.k_bytes ? 0u : kOOB;
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          t.b[u][h][f] = __builtin_bit_cast(
+              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(GLU && f ? rb1 : rb0, (vb[f] + k) | oob, 0, 0));
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          t.a[u][h][f] = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (va[f] + k) | oob, 0, 0));
+      }
+#pragma unroll
+      for (int h = 0; h < NSC; ++h) {
+        const int kb = KIND == KIND_FP8 ? s : 8 * s + 4 * h + lg;
+#pragma unroll
+        for (int f = 0; f < MF; ++f) t.sa[u][h][f] = scale(rsa, args.ld_sfa, 16 * f + r16, kb);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const int row = n0 + 16 * f + r16;
+          t.sb[u][h][f] = scale(rsb, args.ld_sfb, b_row ? row : row / 128, kb);
+        }
+      }
+    }
+  };
+  auto multiply = [&](const Batch& t) __attribute__((always_inline)) {
+    i32x4_t(*const mine_)[64] = smem[wave];
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) mine_[(2 * u + h) * (MF + NF) + f][put] = t.b[u][h][f];
+#pragma unroll
+        for (int f = 0; f < MF; ++f) mine_[(2 * u + h) * (MF + NF) + NF + f][put] = t.a[u][h][f];
+      }
+    // (only this wave uses its pieces, and its LDS accesses execute in order)
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      i32x4_t a[2][MF], b[2][NF];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) b[h][f] = mine_[(2 * u + h) * (MF + NF) + f][get];
+#pragma unroll
+        for (int f = 0; f < MF; ++f) a[h][f] = mine_[(2 * u + h) * (MF + NF) + NF + f][get];
+      }
+#pragma unroll
+      for (int fa = 0; fa < MF; ++fa)
+#pragma unroll
+        for (int fb = 0; fb < NF; ++fb) {
+          if constexpr (KIND == KIND_FP8) {
+            const i32x4_t bl = b[0][fb], bh = b[1][fb], al = a[0][fa], ah = a[1][fa];
+            acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                (i32x8_t){bl[0], bl[1], bl[2], bl[3], bh[0], bh[1], bh[2], bh[3]},
+                (i32x8_t){al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]}, acc[fa][fb], 0, 0, 0,
+                (int)t.sb[u][0][fb], 0, (int)t.sa[u][0][fa]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const i32x4_t bv = b[h][fb], av = a[h][fa];
+              if constexpr (KIND == KIND_BF16)
+                acc[fa][fb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8_t, bv), __builtin_bit_cast(bf16x8_t, av), acc[fa][fb], 0, 0, 0);
+              else
+                acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    (i32x8_t){bv[0], bv[1], bv[2], bv[3], 0, 0, 0, 0},
+                    (i32x8_t){av[0], av[1], av[2], av[3], 0, 0, 0, 0}, acc[fa][fb], 4, 4, 0, (int)t.sb[u][h][fb], 0,
+                    (int)t.sa[u][h][fa]);
+            }
+          }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  Batch t0, t1;
+  load(t0, wave);
+  for (int s = wave; s < steps; s += 2 * W * UN) {
+    load(t1, s + W * UN);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    load(t0, s + 2 * W * UN);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(t1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // lane l's register r: column 4 (l / 16) + r, row l % 16 of the fragment
+#pragma unroll
+  for (int fa = 0; fa < MF; ++fa)
+#pragma unroll
+    for (int fb = 0; fb < NF; ++fb) smem[wave][fa * NF + fb][lane] = __builtin_bit_cast(i32x4_t, acc[fa][fb]);
+  __syncthreads();
+  if (!mine) return;
+  auto sum = [&](int f, float (&v)[4]) {
+    few_f32x4_t t = __builtin_bit_cast(few_f32x4_t, smem[0][f][lane]);
+#pragma unroll
+    for (int w = 1; w < W; ++w) t += __builtin_bit_cast(few_f32x4_t, smem[w][f][lane]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
+  };
+  float z[4];
+  uint16_t* const Z = args.Z ? args.Z + (int64_t)m * args.ldz + n : nullptr;
+  uint16_t* const D = args.D + (int64_t)m * args.ldd + n;
+  if constexpr (GLU) {
+    float u[4];
+    sum(fm * NF, z);
+    sum(fm * NF + 1, u);
+    glu_row<4>(args.act, z, u, Z, args.inter, D, args.e_vec);
+  } else {
+    sum(fm * NF + fn, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] += bias[e];
+    act_row<4>(args.act, z, Z, res, args.R != nullptr, D, args.e_vec, cnt);
+  }
+}
+
+template <int KIND, int MF, int NF, bool GLU, int W>
+static int go(const GemmArgs& a, hipStream_t st) {
+  const int per = GLU ? 16 : 16 * NF, n = GLU ? a.inter : a.N;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((few_kernel<KIND, MF, NF, GLU, W, 1>), dim3((unsigned)((n + per - 1) / per)), dim3(W * 64), 0, st,
+                     a);
+  return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
+}
+
+// Waves and columns of a workgroup.  Up to 16 rows: 16 waves of 16 columns (BF16 7168 x 2048,
+// one row: 7.9 us; 8 waves 8.7; 32 columns no faster).  More rows: 32 columns halve what is
+// read of A (32 rows, 7168 x 2048: 9.4 us against 10.3) where that leaves most CUs a
+// workgroup, 16 otherwise (2048 x 7168: 14.0 against 18.1); 64 rows: 4 waves of 32 columns
+// 12.2 us against 13.3 with 8.
+template <int KIND>
+static int go_rows(const GemmArgs& a, hipStream_t st) {
+  if (a.M <= 16) return go<KIND, 1, 1, false, 16>(a, st);
+  const bool wide = a.N >= 32 * 192;
+  if (a.M <= 32) return wide ? go<KIND, 2, 2, false, 8>(a, st) : go<KIND, 2, 1, false, 8>(a, st);
+  return wide ? go<KIND, 4, 2, false, 4>(a, st) : go<KIND, 4, 1, false, 8>(a, st);
+}
+
+int dense_few(int kind, const GemmArgs& a, bool glu, void* stream) {
+  const hipStream_t st = (hipStream_t)stream;
+  if (glu)
+    return a.M <= 16 ? go<KIND_BF16, 1, 2, true, 16>(a, st)
+                     : (a.M <= 32 ? go<KIND_BF16, 2, 2, true, 8>(a, st) : go<KIND_BF16, 4, 2, true, 8>(a, st));
+  switch (kind) {
+    case KIND_BF16: return go_rows<KIND_BF16>(a, st);
+    case KIND_FP8: return go_rows<KIND_FP8>(a, st);
+    default: return go_rows<KIND_FP4>(a, st);
+  }
+}
+
+}  // namespace bsg

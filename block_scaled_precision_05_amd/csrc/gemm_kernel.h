@@ -109,7 +109,7 @@ struct GemmArgs {
   int64_t part_stride;
   int32_t splits;           // EPI_PART: parts of the contraction, nk stages each (the last
                             // may be shorter)
-  int32_t e_vec;            // D, R and Z (where given) take 16-byte accesses
+  int32_t e_vec;            // rows of D and Z (where given) are 16-byte aligned
 };
 
 // What a kernel instance does with its accumulators, and how its operands lie (EPI):
@@ -530,6 +530,16 @@ __device__ __forceinline__ void ring_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Transposing LDS read.  (The restrict parameter gives the read its own alias scope.  The
+// compiler makes an LDS read without any alias information wait for every copy into LDS
+// in flight, which would empty the ring at each k-step; which stage a read may touch is
+// settled by the ring's own waits and barriers.)
+typedef __attribute__((ext_vector_type(4))) short i16x4_t;
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+__device__ __forceinline__ i16x4_t read_tr16(const lds_i16x4_t* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)p);
+}
+
 // Epilogue of the dense products (EPI_ACT, EPI_GLU, EPI_PART): one wave's TM x 64 block of
 // fp32 accumulators.  The block goes through the wave's part of the idle LDS ring as fp32,
 // half of its rows at a time (what the bf16 epilogue takes for all of them), so that a lane
@@ -550,7 +560,8 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
   const int el32 = el & 31, elg = el >> 5;
   const int rr = el / LPR, seg = el % LPR;
   const int n = n_base + 8 * seg;
-  const bool vec = args.e_vec && n + 8 <= n_end;
+  const int cnt = n_end - n < 8 ? n_end - n : 8;   // (none, for lanes past the last column)
+  const bool vec = args.e_vec;
   float b8[8];
   if constexpr (E == EPI_ACT) {
 #pragma unroll
@@ -562,15 +573,15 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
   for (int half = 0; half < 2; ++half) {
     // the residual's rows, two iterations ahead of their use
     auto load_r = [&](int it) {
-      i32x4_t v = {0, 0, 0, 0};
+      Bf16s<8>::t v = {0, 0, 0, 0};
       if constexpr (E == EPI_ACT) {
         const int row = real_row(half, it * RPI + rr);
-        if (args.R && vec && it < IT && row < rows_w)
-          v = *(const i32x4_t*)(args.R + (int64_t)(row0 + row) * args.ldr + n);
+        if (args.R && cnt > 0 && it < IT && row < rows_w)
+          v = load_bf16s<8>(args.R + (int64_t)(row0 + row) * args.ldr + n, cnt);
       }
       return v;
     };
-    i32x4_t r0 = load_r(0), r1 = load_r(1);
+    Bf16s<8>::t r0 = load_r(0), r1 = load_r(1);
 #pragma unroll
     for (int a = 0; a < HF; ++a) {
       const int s = 32 * a + el32;
@@ -598,7 +609,7 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
 #pragma unroll 1
     for (int it = 0; it < IT; ++it) {
       const int s = it * RPI + rr, row = real_row(half, s);
-      const i32x4_t r2 = load_r(it + 2);
+      const Bf16s<8>::t r2 = load_r(it + 2);
       auto read8 = [&](int chunk, float (&v)[8]) {
         const f32x4_t lo = *(const f32x4_t*)(stg + 256 * s + 16 * (chunk ^ (s & 15)));
         const f32x4_t hi = *(const f32x4_t*)(stg + 256 * s + 16 * ((chunk + 1) ^ (s & 15)));
@@ -610,7 +621,7 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
       };
       float z[8];
       read8(2 * seg, z);
-      if (row < rows_w && n < n_end) {
+      if (row < rows_w && cnt > 0) {
         const int64_t m = row0 + row;
         if constexpr (PART) {
           // (P's rows are padded to a multiple of 8 columns)
@@ -620,15 +631,13 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
         } else if constexpr (GLU) {
           float u[8];
           read8(8 + 2 * seg, u);
-          // (inter is a multiple of 8: eight gate columns always exist together)
-          glu_row8(args.act, z, u, args.Z ? args.Z + m * args.ldz + n : nullptr, args.inter,
-                   args.D + m * args.ldd + n, vec);
+          glu_row<8>(args.act, z, u, args.Z ? args.Z + m * args.ldz + n : nullptr, args.inter,
+                     args.D + m * args.ldd + n, vec);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] += b8[e];
-          act_row8(args.act, z, args.Z ? args.Z + m * args.ldz + n : nullptr,
-                   args.R ? args.R + m * args.ldr + n : nullptr, r0, args.D + m * args.ldd + n, vec,
-                   n_end - n < 8 ? n_end - n : 8);
+          act_row<8>(args.act, z, args.Z ? args.Z + m * args.ldz + n : nullptr, r0, args.R != nullptr,
+                     args.D + m * args.ldd + n, vec, cnt);
         }
       }
       r0 = r1;
@@ -1060,12 +1069,9 @@ void gemm_kernel(const GemmArgs args) {
         const uint8_t* base = smem + buf * T::STAGE_BYTES;
         // rows k .. k+3 and k+4 .. k+7 of a fragment of a transposed operand
         auto tr_frag = [&](uint32_t off, int row_bytes) {
-          typedef __attribute__((ext_vector_type(4))) short i16x4_t;
-          typedef __attribute__((ext_vector_type(8))) short i16x8_t;
-          typedef __attribute__((address_space(3))) i16x4_t lds_t;
-          const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(base + off + 16 * j * row_bytes));
-          const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(base + off + (16 * j + 4) * row_bytes));
-          return __builtin_bit_cast(bf16x8_t, (i16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          const i16x4_t lo = read_tr16((const lds_i16x4_t*)(base + off + 16 * j * row_bytes));
+          const i16x4_t hi = read_tr16((const lds_i16x4_t*)(base + off + (16 * j + 4) * row_bytes));
+          return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         };
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
