@@ -631,6 +631,8 @@ _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_DENSE = tuple(n + w for n in ("gemm_bf16_act", "gemm_fp8_act", "gemm_fp4_act", "gemm_bf16_act_backward",
+                               "gemm_bf16_glu", "gemm_bf16_glu_backward") for w in ("", "_workspace"))
 _native_lock = threading.Lock()
 _native_module = None
 
@@ -650,7 +652,7 @@ def _native():
                                       for n in ("sort_tokens", "sort_tokens_workspace", "moe_dispatch_bf16",
                                                 "moe_dispatch_fp8", "moe_dispatch_fp4", "moe_combine",
                                                 "moe_combine_backward", "lora_add_bf16",
-                                                "lora_add_workspace")})
+                                                "lora_add_workspace") + _DENSE})
             _native_module = _binding
     return _native_module
 
@@ -1001,6 +1003,10 @@ def gemm_bf16_act(A, B, bias=None, act: str = "none", residual=None, out=None, p
     receives A B^T + bias, which gemm_bf16_act_backward takes.  Sums are fp32, each output
     rounded once.  ``workspace`` may pass a 16-byte aligned contiguous tensor of at least
     gemm_bf16_act_workspace(M, N, K) bytes."""
+    if stream is None and workspace is None:
+        r = (_native_module or _native()).gemm_bf16_act(A, B, bias, ACTIVATIONS.get(act, -1), residual, out, preact)
+        if r is not None:
+            return r
     _one_gpu(A, B, bias, residual, out, preact, workspace)
     M, K = A.shape[0], _width(A, "A")
     N = B.shape[0]
@@ -1049,6 +1055,11 @@ def gemm_fp8_act(A, sfa, B, sfb, bias=None, act: str = "none", residual=None, ou
                  stream=None, sfb_gran_mn: int = 128):
     """gemm_bf16_act on the operands of gemm_fp8_blockscaled (e4m3 codes with packed UE8M0
     scales; sfb per 128x128 block of B, or per row with sfb_gran_mn = 1), without preact."""
+    if stream is None and workspace is None:
+        r = (_native_module or _native()).gemm_scaled_act(
+            False, A, sfa, B, sfb, sfb_gran_mn, bias, ACTIVATIONS.get(act, -1), residual, out)
+        if r is not None:
+            return r
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("A must be [M, K] and B [N, K]")
     return _act_scaled("gemm_fp8_act", A, sfa, B, sfb, sfb_gran_mn, bias, act, residual, A.shape[1], out,
@@ -1059,6 +1070,11 @@ def gemm_fp4_act(A, sfa, B, sfb, bias=None, act: str = "none", residual=None, K:
                  workspace=None, stream=None):
     """gemm_bf16_act on the operands of gemm_fp4_blockscaled (e2m1 codes, two per byte, with
     packed 1x32 scales on both), without preact."""
+    if stream is None and workspace is None and K is None:
+        r = (_native_module or _native()).gemm_scaled_act(
+            True, A, sfa, B, sfb, 1, bias, ACTIVATIONS.get(act, -1), residual, out)
+        if r is not None:
+            return r
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A must be [M, K/2] and B [N, K/2]")
     K = 2 * A.shape[1] if K is None else K
@@ -1074,6 +1090,11 @@ def gemm_bf16_act_backward(dout, A, B, preact=None, act: str = "none", need=(Tru
     None).  The residual's gradient is dout itself.  ``need`` tells which of the three are
     computed, the others are None.  ``workspace`` may pass at least
     gemm_bf16_act_backward_workspace(M, N, K) bytes."""
+    if stream is None and workspace is None:
+        r = (_native_module or _native()).gemm_bf16_act_backward(
+            dout, A, B, preact, ACTIVATIONS.get(act, -1), *need)
+        if r is not None:
+            return r
     _one_gpu(dout, A, B, preact, workspace)
     M, K = A.shape[0], _width(A, "A")
     N = B.shape[0]
@@ -1111,6 +1132,10 @@ def gemm_bf16_glu(X, W13, act: str = "silu", out=None, preact=None, workspace=No
     [2*inter, K] (gate rows, then up rows), H bf16 [M, inter].  ``preact`` (bf16 [M,
     2*inter]), where given, receives both projections, which gemm_bf16_glu_backward takes.
     ``workspace`` may pass at least gemm_bf16_glu_workspace(M, inter, K) bytes."""
+    if stream is None and workspace is None:
+        r = (_native_module or _native()).gemm_bf16_glu(X, W13, ACTIVATIONS.get(act, -1), out, preact)
+        if r is not None:
+            return r
     _one_gpu(X, W13, out, preact, workspace)
     M, inter, K, ldx, ldw = _glu_sizes(X, W13)
     code = _act(act)
@@ -1134,6 +1159,11 @@ def gemm_bf16_glu_backward(dout, X, W13, preact, act: str = "silu", need=(True, 
     [M, inter] and the forward call's ``preact``.  ``need`` tells which of the two are
     computed.  ``workspace`` may pass at least gemm_bf16_glu_backward_workspace(M, inter, K)
     bytes."""
+    if stream is None and workspace is None:
+        r = (_native_module or _native()).gemm_bf16_glu_backward(
+            dout, X, W13, preact, ACTIVATIONS.get(act, -1), *need)
+        if r is not None:
+            return r
     _one_gpu(dout, X, W13, preact, workspace)
     M, inter, K, ldx, ldw = _glu_sizes(X, W13)
     ldd = _ld(dout, "dout", torch.bfloat16, M, inter)

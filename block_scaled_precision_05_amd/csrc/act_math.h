@@ -169,16 +169,21 @@ __device__ __forceinline__ void with_act(int act, F body) {
   }
 }
 
+template <int V>
+__device__ __forceinline__ void act_all(int act, float (&z)[V]) {
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) z[e] = act_f<decltype(a)::value>(z[e]);
+  });
+}
+
 // V consecutive outputs of a row, cnt of which exist: z (bias already added) -> Z,
 // D = r + f(z).  Z may be null; r holds the residual (zeros without one).
 template <int V>
 __device__ __forceinline__ void act_row(int act, float (&z)[V], uint16_t* Z, const typename Bf16s<V>::t& r, bool add,
                                         uint16_t* D, bool vec, int cnt) {
   if (Z) store_bf16s<V>(Z, z, vec, cnt);
-  with_act(act, [&](auto a) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) z[e] = act_f<decltype(a)::value>(z[e]);
-  });
+  act_all<V>(act, z);
   if (add) {
     float x[V];
     unpack<V>(r, x);

@@ -1,4 +1,5 @@
-// binding.cpp -- marshalling of the grouped-row operators' usual calls in native code.
+// binding.cpp -- marshalling of the grouped-row operators' and the dense epilogue products'
+// usual calls in native code.
 //
 // These operators are short (a decode step's combine runs 4 us on the GPU), and their
 // Python wrappers' checks and ctypes calls take longer than that.  The functions here do
@@ -29,6 +30,18 @@ decltype(&::moe_combine) p_moe_combine;
 decltype(&::moe_combine_backward) p_moe_combine_backward;
 decltype(&::lora_add_bf16) p_lora_add_bf16;
 decltype(&::lora_add_workspace) p_lora_add_workspace;
+decltype(&::gemm_bf16_act) p_gemm_bf16_act;
+decltype(&::gemm_fp8_act) p_gemm_fp8_act;
+decltype(&::gemm_fp4_act) p_gemm_fp4_act;
+decltype(&::gemm_bf16_act_backward) p_gemm_bf16_act_backward;
+decltype(&::gemm_bf16_glu) p_gemm_bf16_glu;
+decltype(&::gemm_bf16_glu_backward) p_gemm_bf16_glu_backward;
+decltype(&::gemm_bf16_act_workspace) p_gemm_bf16_act_workspace;
+decltype(&::gemm_fp8_act_workspace) p_gemm_fp8_act_workspace;
+decltype(&::gemm_fp4_act_workspace) p_gemm_fp4_act_workspace;
+decltype(&::gemm_bf16_act_backward_workspace) p_gemm_bf16_act_backward_workspace;
+decltype(&::gemm_bf16_glu_workspace) p_gemm_bf16_glu_workspace;
+decltype(&::gemm_bf16_glu_backward_workspace) p_gemm_bf16_glu_backward_workspace;
 PyTypeObject* plan_type;      // the named tuple that sort_tokens returns
 
 struct Entry {
@@ -45,6 +58,18 @@ const Entry kEntries[] = {
     {"moe_combine_backward", (void**)&p_moe_combine_backward},
     {"lora_add_bf16", (void**)&p_lora_add_bf16},
     {"lora_add_workspace", (void**)&p_lora_add_workspace},
+    {"gemm_bf16_act", (void**)&p_gemm_bf16_act},
+    {"gemm_fp8_act", (void**)&p_gemm_fp8_act},
+    {"gemm_fp4_act", (void**)&p_gemm_fp4_act},
+    {"gemm_bf16_act_backward", (void**)&p_gemm_bf16_act_backward},
+    {"gemm_bf16_glu", (void**)&p_gemm_bf16_glu},
+    {"gemm_bf16_glu_backward", (void**)&p_gemm_bf16_glu_backward},
+    {"gemm_bf16_act_workspace", (void**)&p_gemm_bf16_act_workspace},
+    {"gemm_fp8_act_workspace", (void**)&p_gemm_fp8_act_workspace},
+    {"gemm_fp4_act_workspace", (void**)&p_gemm_fp4_act_workspace},
+    {"gemm_bf16_act_backward_workspace", (void**)&p_gemm_bf16_act_backward_workspace},
+    {"gemm_bf16_glu_workspace", (void**)&p_gemm_bf16_glu_workspace},
+    {"gemm_bf16_glu_backward_workspace", (void**)&p_gemm_bf16_glu_backward_workspace},
 };
 
 // Allocation and launch run without the interpreter lock, as torch's own calls do.
@@ -359,6 +384,242 @@ PyObject* lora_add_bf16_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Scratch memory of a call, freed (to torch's allocator, on the stream) when it returns.
+struct Scratch {
+  at::Tensor t;
+  void* p = nullptr;
+  int64_t bytes;
+  explicit Scratch(int64_t need) : bytes(need) {
+    if (need) {
+      t = empty({need}, at::kByte);
+      p = t.data_ptr();
+    }
+  }
+};
+
+// bias [N], residual [M, N] and output [M, N] of an act call.
+struct Epilogue {
+  const at::Tensor *bias, *R, *out;
+  int64_t ldr, ldd;
+  Epilogue(PyObject* bias_, PyObject* R_, PyObject* out_, int64_t M, int64_t N, int64_t dev, bool& ok) {
+    bias = bias_ == Py_None ? nullptr : tensor(bias_, at::kBFloat16, dev, ok);
+    R = R_ == Py_None ? nullptr : tensor(R_, at::kBFloat16, dev, ok);
+    out = out_ == Py_None ? nullptr : tensor(out_, at::kBFloat16, dev, ok);
+    if (ok && bias && (bias->dim() != 1 || bias->size(0) != N || !bias->is_contiguous())) ok = false;
+    ldr = R ? matrix(R, M, N, ok) : 0;
+    ldd = out ? matrix(out, M, N, ok) : N;
+  }
+};
+
+// gemm_bf16_act(A, B, bias, act, residual, out, preact)
+PyObject* gemm_bf16_act_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int64_t dev;
+  void* stream;
+  if (n != 7) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
+  const int64_t act = PyLong_AsLongLong(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  bool ok = true;
+  const at::Tensor* A = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* B = tensor(a[1], at::kBFloat16, dev, ok);
+  if (!ok || A->dim() != 2 || B->dim() != 2) Py_RETURN_NONE;
+  const int64_t M = A->size(0), K = A->size(1), N = B->size(0);
+  const int64_t lda = matrix(A, M, K, ok), ldb = matrix(B, N, K, ok);
+  const Epilogue e(a[2], a[4], a[5], M, N, dev, ok);
+  const at::Tensor* Z = a[6] == Py_None ? nullptr : tensor(a[6], at::kBFloat16, dev, ok);
+  const int64_t ldz = Z ? matrix(Z, M, N, ok) : 0;
+  if (!ok || M == 0 || N == 0 || K == 0) Py_RETURN_NONE;
+  at::Tensor made;
+  int status;
+  {
+    NoGil g;
+    if (!e.out) made = empty({M, N}, at::kBFloat16);
+    const Scratch ws(p_gemm_bf16_act_workspace(M, N, K));
+    status = p_gemm_bf16_act(A->const_data_ptr(), lda, B->const_data_ptr(), ldb, ptr<void>(e.bias), (int32_t)act,
+                             ptr<void>(e.R), e.ldr, e.out ? e.out->data_ptr() : made.data_ptr(), e.ldd, ptr<void>(Z),
+                             ldz, M, N, K, ws.p, ws.bytes, stream);
+  }
+  if (status != BSG_OK) Py_RETURN_NONE;
+  return e.out ? Py_NewRef(a[5]) : THPVariable_Wrap(std::move(made));
+  END_HANDLE_TH_ERRORS
+}
+
+// A tensor of codes: bytes, or e4m3 values.
+const at::Tensor* codes(PyObject* o, bool fp4, int64_t dev, bool& ok) {
+  if (!THPVariable_Check(o)) {
+    ok = false;
+    return nullptr;
+  }
+  const at::ScalarType t = THPVariable_Unpack(o).scalar_type();
+  return tensor(o, !fp4 && t == at::kFloat8_e4m3fn ? t : at::kByte, dev, ok);
+}
+
+// gemm_scaled_act(fp4, A, sfa, B, sfb, sfb_gran_mn, bias, act, residual, out)
+PyObject* gemm_scaled_act_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int64_t dev;
+  void* stream;
+  if (n != 10) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[1], dev, stream)) Py_RETURN_NONE;
+  const bool fp4 = a[0] == Py_True;
+  const int64_t gran = PyLong_AsLongLong(a[5]), act = PyLong_AsLongLong(a[7]);
+  if (PyErr_Occurred()) return nullptr;
+  bool ok = gran == 1 || gran == 128;
+  const at::Tensor* A = codes(a[1], fp4, dev, ok);
+  const at::Tensor* B = codes(a[3], fp4, dev, ok);
+  const at::Tensor* sfa = tensor(a[2], at::kShort, dev, ok);
+  const at::Tensor* sfb = tensor(a[4], at::kShort, dev, ok);
+  if (!ok || A->dim() != 2 || B->dim() != 2 || sfa->dim() != 2 || sfb->dim() != 2) Py_RETURN_NONE;
+  const int64_t M = A->size(0), bytes = A->size(1), N = B->size(0), K = fp4 ? 2 * bytes : bytes, gk = fp4 ? 32 : 128;
+  const int64_t lda = matrix(A, M, bytes, ok), ldb = matrix(B, N, bytes, ok);
+  const int64_t kp = (K / gk + 1) / 2, rows_b = (N + gran - 1) / gran;
+  if (sfa->size(1) < M || sfb->size(1) < rows_b) ok = false;
+  const int64_t ld_sfa = matrix(sfa, kp, sfa->size(1), ok), ld_sfb = matrix(sfb, kp, sfb->size(1), ok);
+  const Epilogue e(a[6], a[8], a[9], M, N, dev, ok);
+  if (!ok || M == 0 || N == 0 || K == 0) Py_RETURN_NONE;
+  at::Tensor made;
+  int status;
+  {
+    NoGil g;
+    if (!e.out) made = empty({M, N}, at::kBFloat16);
+    void* const D = e.out ? e.out->data_ptr() : made.data_ptr();
+    const Scratch ws((fp4 ? p_gemm_fp4_act_workspace : p_gemm_fp8_act_workspace)(M, N, K));
+    status = fp4 ? p_gemm_fp4_act(A->const_data_ptr(), lda, ptr<int16_t>(sfa), ld_sfa, B->const_data_ptr(), ldb,
+                                  ptr<int16_t>(sfb), ld_sfb, ptr<void>(e.bias), (int32_t)act, ptr<void>(e.R), e.ldr, D,
+                                  e.ldd, M, N, K, ws.p, ws.bytes, stream)
+                 : p_gemm_fp8_act(A->const_data_ptr(), lda, ptr<int16_t>(sfa), ld_sfa, B->const_data_ptr(), ldb,
+                                  ptr<int16_t>(sfb), ld_sfb, (int32_t)gran, ptr<void>(e.bias), (int32_t)act,
+                                  ptr<void>(e.R), e.ldr, D, e.ldd, M, N, K, ws.p, ws.bytes, stream);
+  }
+  if (status != BSG_OK) Py_RETURN_NONE;
+  return e.out ? Py_NewRef(a[9]) : THPVariable_Wrap(std::move(made));
+  END_HANDLE_TH_ERRORS
+}
+
+// The result tuple of a backward call: what was not asked for is None.
+PyObject* results(at::Tensor* t, int count) {
+  PyObject* r = PyTuple_New(count);
+  if (!r) return nullptr;
+  for (int i = 0; i < count; ++i)
+    PyTuple_SET_ITEM(r, i, t[i].defined() ? THPVariable_Wrap(std::move(t[i])) : Py_NewRef(Py_None));
+  return r;
+}
+
+// gemm_bf16_act_backward(dout, A, B, preact, act, need_a, need_b, need_bias) -> (dA, dB, dbias)
+PyObject* gemm_bf16_act_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int64_t dev;
+  void* stream;
+  if (n != 8) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
+  const int64_t act = PyLong_AsLongLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  bool need[3];
+  for (int i = 0; i < 3; ++i) {
+    const int v = PyObject_IsTrue(a[5 + i]);
+    if (v < 0) return nullptr;
+    need[i] = v;
+  }
+  bool ok = true;
+  const at::Tensor* dO = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* A = tensor(a[1], at::kBFloat16, dev, ok);
+  const at::Tensor* B = tensor(a[2], at::kBFloat16, dev, ok);
+  const at::Tensor* Z = a[3] == Py_None ? nullptr : tensor(a[3], at::kBFloat16, dev, ok);
+  if (!ok || A->dim() != 2 || B->dim() != 2 || (!Z && act != 0)) Py_RETURN_NONE;
+  const int64_t M = A->size(0), K = A->size(1), N = B->size(0);
+  const int64_t lda = matrix(A, M, K, ok), ldb = matrix(B, N, K, ok), ldd = matrix(dO, M, N, ok);
+  const int64_t ldz = Z ? matrix(Z, M, N, ok) : 0;
+  if (!ok || M == 0 || N == 0 || K == 0) Py_RETURN_NONE;
+  at::Tensor out[3];
+  int status;
+  {
+    NoGil g;
+    if (need[0]) out[0] = empty({M, K}, at::kBFloat16);
+    if (need[1]) out[1] = empty({N, K}, at::kBFloat16);
+    if (need[2]) out[2] = empty({N}, at::kFloat);
+    const Scratch ws(p_gemm_bf16_act_backward_workspace(M, N, K));
+    status = p_gemm_bf16_act_backward(dO->const_data_ptr(), ldd, ptr<void>(Z), ldz, A->const_data_ptr(), lda,
+                                      B->const_data_ptr(), ldb, (int32_t)act, need[0] ? out[0].data_ptr() : nullptr, K,
+                                      need[1] ? out[1].data_ptr() : nullptr, K,
+                                      need[2] ? ptr<float>(&out[2]) : nullptr, M, N, K, ws.p, ws.bytes, stream);
+  }
+  if (status != BSG_OK) Py_RETURN_NONE;
+  return results(out, 3);
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm_bf16_glu(X, W13, act, out, preact)
+PyObject* gemm_bf16_glu_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int64_t dev;
+  void* stream;
+  if (n != 5) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
+  const int64_t act = PyLong_AsLongLong(a[2]);
+  if (PyErr_Occurred()) return nullptr;
+  bool ok = true;
+  const at::Tensor* X = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* W = tensor(a[1], at::kBFloat16, dev, ok);
+  const at::Tensor* out = a[3] == Py_None ? nullptr : tensor(a[3], at::kBFloat16, dev, ok);
+  const at::Tensor* Z = a[4] == Py_None ? nullptr : tensor(a[4], at::kBFloat16, dev, ok);
+  if (!ok || X->dim() != 2 || W->dim() != 2 || W->size(0) % 2) Py_RETURN_NONE;
+  const int64_t M = X->size(0), K = X->size(1), inter = W->size(0) / 2;
+  const int64_t ldx = matrix(X, M, K, ok), ldw = matrix(W, 2 * inter, K, ok);
+  const int64_t ldh = out ? matrix(out, M, inter, ok) : inter, ldz = Z ? matrix(Z, M, 2 * inter, ok) : 0;
+  if (!ok || M == 0 || inter == 0 || K == 0) Py_RETURN_NONE;
+  at::Tensor made;
+  int status;
+  {
+    NoGil g;
+    if (!out) made = empty({M, inter}, at::kBFloat16);
+    const Scratch ws(p_gemm_bf16_glu_workspace(M, inter, K));
+    status = p_gemm_bf16_glu(X->const_data_ptr(), ldx, W->const_data_ptr(), ldw, (int32_t)act,
+                             out ? out->data_ptr() : made.data_ptr(), ldh, ptr<void>(Z), ldz, M, inter, K, ws.p,
+                             ws.bytes, stream);
+  }
+  if (status != BSG_OK) Py_RETURN_NONE;
+  return out ? Py_NewRef(a[3]) : THPVariable_Wrap(std::move(made));
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm_bf16_glu_backward(dout, X, W13, preact, act, need_x, need_w) -> (dX, dW13)
+PyObject* gemm_bf16_glu_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int64_t dev;
+  void* stream;
+  if (n != 7) return (PyErr_BadArgument(), nullptr);
+  if (!place(a[0], dev, stream)) Py_RETURN_NONE;
+  const int64_t act = PyLong_AsLongLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const int need_x = PyObject_IsTrue(a[5]), need_w = PyObject_IsTrue(a[6]);
+  if (need_x < 0 || need_w < 0) return nullptr;
+  bool ok = true;
+  const at::Tensor* dO = tensor(a[0], at::kBFloat16, dev, ok);
+  const at::Tensor* X = tensor(a[1], at::kBFloat16, dev, ok);
+  const at::Tensor* W = tensor(a[2], at::kBFloat16, dev, ok);
+  const at::Tensor* Z = tensor(a[3], at::kBFloat16, dev, ok);
+  if (!ok || X->dim() != 2 || W->dim() != 2 || W->size(0) % 2) Py_RETURN_NONE;
+  const int64_t M = X->size(0), K = X->size(1), inter = W->size(0) / 2;
+  const int64_t ldx = matrix(X, M, K, ok), ldw = matrix(W, 2 * inter, K, ok), ldd = matrix(dO, M, inter, ok);
+  const int64_t ldz = matrix(Z, M, 2 * inter, ok);
+  if (!ok || M == 0 || inter == 0 || K == 0) Py_RETURN_NONE;
+  at::Tensor out[2];
+  int status;
+  {
+    NoGil g;
+    if (need_x) out[0] = empty({M, K}, at::kBFloat16);
+    if (need_w) out[1] = empty({2 * inter, K}, at::kBFloat16);
+    const Scratch ws(p_gemm_bf16_glu_backward_workspace(M, inter, K));
+    status = p_gemm_bf16_glu_backward(dO->const_data_ptr(), ldd, Z->const_data_ptr(), ldz, X->const_data_ptr(), ldx,
+                                      W->const_data_ptr(), ldw, (int32_t)act, need_x ? out[0].data_ptr() : nullptr, K,
+                                      need_w ? out[1].data_ptr() : nullptr, K, M, inter, K, ws.p, ws.bytes, stream);
+  }
+  if (status != BSG_OK) Py_RETURN_NONE;
+  return results(out, 2);
+  END_HANDLE_TH_ERRORS
+}
+
 // init(plan_type, {name: address of the library's entry point})
 PyObject* init_(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2 || !PyType_Check(a[0]) || !PyType_IsSubtype((PyTypeObject*)a[0], &PyTuple_Type) || !PyDict_Check(a[1])) {
@@ -387,9 +648,14 @@ PyMethodDef methods[] = {
     {"moe_combine", (PyCFunction)(void (*)(void))moe_combine_, METH_FASTCALL, nullptr},
     {"moe_combine_backward", (PyCFunction)(void (*)(void))moe_combine_backward_, METH_FASTCALL, nullptr},
     {"lora_add_bf16", (PyCFunction)(void (*)(void))lora_add_bf16_, METH_FASTCALL, nullptr},
+    {"gemm_bf16_act", (PyCFunction)(void (*)(void))gemm_bf16_act_, METH_FASTCALL, nullptr},
+    {"gemm_scaled_act", (PyCFunction)(void (*)(void))gemm_scaled_act_, METH_FASTCALL, nullptr},
+    {"gemm_bf16_act_backward", (PyCFunction)(void (*)(void))gemm_bf16_act_backward_, METH_FASTCALL, nullptr},
+    {"gemm_bf16_glu", (PyCFunction)(void (*)(void))gemm_bf16_glu_, METH_FASTCALL, nullptr},
+    {"gemm_bf16_glu_backward", (PyCFunction)(void (*)(void))gemm_bf16_glu_backward_, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Marshalling of the grouped-row operators.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Marshalling of the grouped-row operators and the dense epilogue products.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

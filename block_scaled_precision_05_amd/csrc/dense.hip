@@ -26,25 +26,27 @@ static const int64_t kMaxTiles = int64_t(1) << 24;
 static const int64_t kMaxRow = (int64_t(1) << 31) / 256 - 1;   // bytes of a row (32-bit offsets)
 static const int64_t kMaxRows = (int64_t(1) << 30) - 1;
 
-// What a form costs, in microseconds, fitted to sweeps of every form over 128 to 2048 rows
+// What a form costs, in microseconds, fitted to sweeps of every form over 128 to 4096 rows
 // (BF16 7168 x 2048, 2048 x 7168, the gated block and both strided products; FP8 4096 x
 // 7168, 7168 x 2048; FP4 4096 x 7168): time per stage of one tile, rising from few tiles on
 // the GPU to a full round of them, and a fixed part for launch, first stage and epilogue.
 // The parts' fp32 sums pass through memory twice at about 5.5 TB/s, and the join is a
 // launch of its own.
-//   BF16 example, 1024 x 2048 over K = 7168: 256-row tiles 112 us, 128-row tiles 80, 128-row
-//   tiles in 4 parts 44, 256-row tiles in 4 parts 50.
+//   BF16 examples over K = 7168: 1024 x 2048: 256-row tiles 113 us, 128-row tiles 80, with the
+//   deep ring 52, deep in 2 parts 41; 2048 x 2048: 113, 84, 65, 76; 4096 x 2048: 133, 122
+//   (128-row tiles), 127 (deep).
 struct TileCost {
+  int form;
   int64_t bm, bn, lo_tiles, cap;   // tile, tiles up to which `lo` holds, tiles of a full round
   double lo, hi, fixed;
-  int round;                       // stages of a round of the ring
+  int round;                       // stages of a round of the ring; 0: no parts
 };
-static const TileCost kSmall[3] = {{128, 128, 256, 512, 0.33, 0.42, 5.5, 4},
-                                   {128, 256, 128, 256, 0.38, 0.43, 5.5, 6},
-                                   {128, 128, 256, 512, 0.49, 0.59, 5.5, 4}};
-static const TileCost kBig[3] = {{256, 256, 128, 256, 0.50, 0.60, 8.0, 4},
-                                 {256, 256, 128, 256, 0.55, 0.58, 8.0, 4},
-                                 {256, 256, 128, 256, 0.55, 0.60, 8.0, 4}};
+static const TileCost kForms[3][3] = {
+    {{DENSE_BIG, 256, 256, 128, 256, 0.50, 0.60, 8.0, 0},
+     {DENSE_SMALL, 128, 128, 256, 512, 0.33, 0.55, 5.5, 0},
+     {DENSE_DEEP, 128, 128, 128, 256, 0.20, 0.26, 7.0, 8}},
+    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.58, 8.0, 0}, {DENSE_SMALL, 128, 256, 128, 256, 0.38, 0.43, 5.5, 6}, {}},
+    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.60, 8.0, 0}, {DENSE_SMALL, 128, 128, 256, 512, 0.49, 0.59, 5.5, 4}, {}}};
 
 static double tiles_cost(const TileCost& c, int64_t tiles, int64_t stages) {
   const int64_t full = tiles / c.cap, rest = tiles % c.cap;
@@ -65,22 +67,22 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
   if (!strided && (M <= 32 || (M <= 64 && bytes <= 8192))) return {DENSE_FEW, 1};
   DensePlan best = {DENSE_BIG, 1};
   double t_best = 1e30;
-  for (int big = 0; big < 2; ++big) {
-    const TileCost& c = (big ? kBig : kSmall)[kind];
+  for (const TileCost& c : kForms[kind]) {
+    if (!c.bm) continue;
     const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
     const double t1 = tiles_cost(c, tiles, stages);
     if (t1 < t_best) {
       t_best = t1;
-      best = {big ? DENSE_BIG : DENSE_SMALL, 1};
+      best = {c.form, 1};
     }
     // parts of at least 8 stages, all of them in one round
-    for (int64_t s = 2; s <= 16 && s * tiles <= c.cap && 8 * s <= stages; ++s) {
+    for (int64_t s = 2; c.round && s <= 16 && s * tiles <= c.cap && 8 * s <= stages; ++s) {
       const int64_t per = ((stages + s - 1) / s + c.round - 1) / c.round * c.round;
       if ((stages + per - 1) / per != s) continue;
       const double t = tiles_cost(c, s * tiles, per) + 3.0 + (8.0 * s + 2.0) * M * N / 5.5e6;
       if (t < t_best) {
         t_best = t;
-        best = {big ? DENSE_BIG_PART : DENSE_SMALL_PART, (int)s};
+        best = {DENSE_PART, (int)s};
       }
     }
   }
@@ -91,9 +93,22 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
 // a row, 16 bytes of each part, four parts' loads at a time.  Bound by the parts' bytes,
 // which mostly come from L2 and the cache behind it, where the product has just written
 // them.
+static __device__ __forceinline__ void sum_parts(const float* q, int64_t stride, int splits, float (&v)[4]) {
+  typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+  f32x4_t t = {0, 0, 0, 0};
+  int s = 0;
+  for (; s + 4 <= splits; s += 4, q += 4 * stride) {
+    const f32x4_t a = *(const f32x4_t*)q, c = *(const f32x4_t*)(q + stride), d = *(const f32x4_t*)(q + 2 * stride),
+                  e = *(const f32x4_t*)(q + 3 * stride);
+    t += (a + c) + (d + e);
+  }
+  for (; s < splits; ++s, q += stride) t += *(const f32x4_t*)q;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = t[e];
+}
+
 template <bool GLU>
 __global__ __launch_bounds__(256) void join_kernel(const GemmArgs args) {
-  typedef __attribute__((ext_vector_type(4))) float f32x4_t;
   const int cols = GLU ? args.inter : args.N, per = (cols + 3) / 4;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = idx / per;
@@ -107,25 +122,13 @@ __global__ __launch_bounds__(256) void join_kernel(const GemmArgs args) {
     if (args.R) r = load_bf16s<4>(args.R + m * args.ldr + n, cnt);
     if (args.bias) unpack<4>(load_bf16s<4>(args.bias + n, cnt), b);
   }
-  auto sum = [&](const float* q, float (&v)[4]) {
-    f32x4_t t = {0, 0, 0, 0};
-    int s = 0;
-    for (; s + 4 <= args.splits; s += 4, q += 4 * args.part_stride) {
-      const f32x4_t a = *(const f32x4_t*)q, c = *(const f32x4_t*)(q + args.part_stride),
-                    d = *(const f32x4_t*)(q + 2 * args.part_stride), e = *(const f32x4_t*)(q + 3 * args.part_stride);
-      t += (a + c) + (d + e);
-    }
-    for (; s < args.splits; ++s, q += args.part_stride) t += *(const f32x4_t*)q;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = t[e];
-  };
   float z[4];
-  sum(p, z);
+  sum_parts(p, args.part_stride, args.splits, z);
   uint16_t* const Z = args.Z ? args.Z + m * args.ldz + n : nullptr;
   uint16_t* const D = args.D + m * args.ldd + n;
   if constexpr (GLU) {
     float u[4];
-    sum(p + args.inter, u);
+    sum_parts(p + args.inter, args.part_stride, args.splits, u);
     glu_row<4>(args.act, z, u, Z, args.inter, D, args.e_vec);
   } else {
 #pragma unroll
@@ -227,12 +230,36 @@ static int dz_rows(int64_t M, int64_t N) {
   return rows;
 }
 
-// dbias from the blocks' partial rows: a block sums 32 columns, eight rows at a time.
-__global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int64_t rows, int64_t N,
-                                                    float* __restrict__ dbias) {
+// What is left after a backward pass's products, in one launch: the parts of either
+// product joined, and dbias summed from the blocks' partial rows.
+struct Joined {
+  const float* P;
+  uint16_t* D;
+  int64_t ldd, ldp, part_stride, M;
+  int32_t N, splits, vec, blocks;   // blocks: workgroups of this product (0: it was not split)
+};
+
+static __device__ __forceinline__ void join_rows(const Joined& a, int block) {
+  const int per = (a.N + 3) / 4;
+  const int64_t idx = (int64_t)block * 256 + threadIdx.x, m = idx / per;
+  const int n = 4 * (int)(idx - m * per);
+  if (m >= a.M) return;
+  float z[4];
+  sum_parts(a.P + m * a.ldp + n, a.part_stride, a.splits, z);
+  store_bf16s<4>(a.D + m * a.ldd + n, z, a.vec, a.N - n < 4 ? a.N - n : 4);
+}
+
+// A dbias block sums 32 columns, eight rows at a time.
+__global__ __launch_bounds__(256) void tail_kernel(const Joined a, const Joined b, const float* __restrict__ part,
+                                                   int64_t rows, int64_t N, float* __restrict__ dbias) {
+  int block = blockIdx.x;
+  if (block < a.blocks) return join_rows(a, block);
+  block -= a.blocks;
+  if (block < b.blocks) return join_rows(b, block);
+  block -= b.blocks;
   __shared__ float s[8][32];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t n = (int64_t)blockIdx.x * 32 + x;
+  const int64_t n = (int64_t)block * 32 + x;
   float t = 0.0f;
   if (n < N)
 #pragma unroll 4
@@ -346,7 +373,7 @@ int gemm_bf16_act(const void* A, int64_t lda, const void* B, int64_t ldb, const 
   a.ldb = K ? ldb * 2 : 0;
   a.k_bytes = (int32_t)(2 * K);
   st = plan.form == DENSE_FEW ? dense_few(KIND_BF16, a, false, stream) : dense_bf16(a, plan.form, EPI_ACT, stream);
-  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
 }
 
 int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
@@ -376,7 +403,7 @@ int gemm_fp8_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa,
   a.sfb_rows = (int32_t)sfb_rows;
   st = plan.form == DENSE_FEW ? dense_few(KIND_FP8, a, false, stream)
                               : dense_fp8(a, plan.form, (K && sv_ok(sfa, ld_sfa) ? 1 : 0) + (sfb_gran_mn == 1 ? 2 : 0), stream);
-  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
 }
 
 int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa, const void* B, int64_t ldb,
@@ -404,7 +431,7 @@ int gemm_fp4_act(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa,
   a.sfb_rows = (int32_t)N;
   st = plan.form == DENSE_FEW ? dense_few(KIND_FP4, a, false, stream)
                               : dense_fp4(a, plan.form, K && sv_ok(sfa, ld_sfa) && sv_ok(sfb, ld_sfb) ? 1 : 0, stream);
-  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, false, stream) : st;
 }
 
 int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int32_t act, void* H, int64_t ldh,
@@ -445,7 +472,7 @@ int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int3
   a.splits = plan.splits;
   a.e_vec = al16(H, ldh) && (!Z || al16(Z, ldz));
   st = plan.form == DENSE_FEW ? dense_few(KIND_BF16, a, true, stream) : dense_bf16(a, plan.form, EPI_GLU, stream);
-  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, true, stream) : st;
+  return st == BSG_OK && plan.form == DENSE_PART ? dense_join(a, true, stream) : st;
 }
 
 }  // extern "C"
@@ -453,9 +480,10 @@ int gemm_bf16_glu(const void* X, int64_t ldx, const void* W13, int64_t ldw, int3
 namespace bsg {
 
 // D [M][N] = (A's rows or columns) x (B's columns), K long: tr 2 contracts B's rows with
-// A's columns, tr 3 the rows of both; operands bf16 with leading dimensions in elements.
+// A's columns, tr 3 the rows of both; operands bf16 with leading dimensions in elements.  A
+// split product leaves its parts in ws and says in `left` how to join them.
 static int strided(int tr, const void* A, int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd, int64_t M,
-                   int64_t N, int64_t K, void* ws, void* stream) {
+                   int64_t N, int64_t K, void* ws, Joined& left, void* stream) {
   if (M == 0 || N == 0) return BSG_OK;
   const DensePlan plan = dense_plan(KIND_BF16, M, N, K, true);
   GemmArgs a = {};
@@ -475,9 +503,10 @@ static int strided(int tr, const void* A, int64_t lda, const void* B, int64_t ld
   a.ldp = dense_ldp(N);
   a.part_stride = M * a.ldp;
   a.splits = plan.splits;
-  a.e_vec = al16(D, ldd);
-  const int st = dense_strided(a, plan.form, tr, stream);
-  return st == BSG_OK && dense_parts(plan.form) ? dense_join(a, false, stream) : st;
+  if (plan.form == DENSE_PART)
+    left = {a.P, a.D, ldd, a.ldp, a.part_stride, M, a.N, plan.splits, al16(D, ldd),
+            (int32_t)((M * ((N + 3) / 4) + 255) / 256)};
+  return dense_strided(a, plan.form, tr, stream);
 }
 
 static int64_t strided_bytes(int64_t M, int64_t N, int64_t K) {
@@ -486,28 +515,35 @@ static int64_t strided_bytes(int64_t M, int64_t N, int64_t K) {
 
 static int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 
-// Workspace of a backward pass: dz [M][ldq], the bias's partial rows, the larger of the two
-// products' parts (they run one after the other).
+// Workspace of a backward pass: dz [M][ldq], the bias's partial rows, the parts of dA and of
+// dB where they are split.
 struct GradSpace {
-  int64_t ldq, rows, blocks, part_at, sums_at, bytes;
+  int64_t ldq, rows, blocks, part_at, da_at, db_at, bytes;
   GradSpace(int64_t M, int64_t cols, int64_t K, bool bias) {
     ldq = (cols + 7) / 8 * 8;
     part_at = 2 * M * ldq;
     rows = dz_rows(M, bias ? cols : cols / 2);
     blocks = (M + rows - 1) / rows;
-    sums_at = part_at + (bias ? up16(4 * blocks * cols) : 0);
-    const int64_t p = strided_bytes(M, K, cols), q = strided_bytes(cols, K, M);
-    bytes = sums_at + (p > q ? p : q);
+    da_at = part_at + (bias ? up16(4 * blocks * cols) : 0);
+    db_at = da_at + strided_bytes(M, K, cols);
+    bytes = db_at + strided_bytes(cols, K, M);
   }
 };
 
-// Both products of a backward pass from dz [M][ldq].
+// Both products of a backward pass from dz [M][ldq], and the launch that finishes them and
+// dbias (part: its partial rows).
 static int grad_products(const void* dz, int64_t ldq, const void* A, int64_t lda, const void* B, int64_t ldb,
-                         void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N, int64_t K, void* ws,
-                         void* stream) {
-  int st = dA ? strided(2, dz, ldq, B, ldb, dA, ldda, M, K, N, ws, stream) : BSG_OK;
-  if (st == BSG_OK && dB) st = strided(3, dz, ldq, A, lda, dB, lddb, N, K, M, ws, stream);
-  return st;
+                         void* dA, int64_t ldda, void* dB, int64_t lddb, float* dbias, int64_t M, int64_t N, int64_t K,
+                         uint8_t* ws, const GradSpace& w, void* stream) {
+  Joined a = {}, b = {};
+  int st = dA ? strided(2, dz, ldq, B, ldb, dA, ldda, M, K, N, ws + w.da_at, a, stream) : BSG_OK;
+  if (st == BSG_OK && dB) st = strided(3, dz, ldq, A, lda, dB, lddb, N, K, M, ws + w.db_at, b, stream);
+  const int64_t blocks = a.blocks + b.blocks + (dbias ? (N + 31) / 32 : 0);
+  if (st != BSG_OK || blocks == 0) return st;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(tail_kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a, b,
+                     (const float*)(ws + w.part_at), w.blocks, N, dbias);
+  return launched();
 }
 
 static int check_grad(int64_t M, int64_t N, int64_t K) {
@@ -564,13 +600,8 @@ int gemm_bf16_act_backward(const void* dD, int64_t lddd, const void* Z, int64_t 
     st = launched();
     if (st != BSG_OK) return st;
   }
-  if (dbias && N > 0) {
-    hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, (hipStream_t)stream, part, w.blocks,
-                       N, dbias);
-    st = launched();
-    if (st != BSG_OK) return st;
-  }
-  return K > 0 ? grad_products(dz, ldq, A, lda, B, ldb, dA, ldda, dB, lddb, M, N, K, ws + w.sums_at, stream) : BSG_OK;
+  return grad_products(dz, ldq, A, lda, B, ldb, K ? dA : nullptr, ldda, K ? dB : nullptr, lddb, dbias, M, N, K, ws, w,
+                       stream);
 }
 
 int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t ldz, const void* X, int64_t ldx,
@@ -601,7 +632,7 @@ int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t 
     st = launched();
     if (st != BSG_OK) return st;
   }
-  return grad_products(ws, w.ldq, X, ldx, W13, ldw, dX, lddx, dW13, lddw, M, N, K, ws + w.sums_at, stream);
+  return grad_products(ws, w.ldq, X, ldx, W13, ldw, dX, lddx, dW13, lddw, nullptr, M, N, K, ws, w, stream);
 }
 
 }  // extern "C"

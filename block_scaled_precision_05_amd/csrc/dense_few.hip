@@ -34,10 +34,12 @@ namespace bsg {
 
 typedef __attribute__((ext_vector_type(4))) float few_f32x4_t;
 
-template <int KIND, int MF, int NF, bool GLU, int W, int UN>
+// GLU: 0 no gate, 1 a gate and an up fragment, 2 one fragment of eight gate and eight up rows.
+template <int KIND, int MF, int NF, int GLU, int W, int UN>
 __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
-  static_assert(!GLU || (KIND == KIND_BF16 && NF == 2), "gate and up fragment");
-  constexpr int NO = GLU ? 1 : NF;          // output fragments along N
+  static_assert(!GLU || (KIND == KIND_BF16 && NF == (GLU == 1 ? 2 : 1)), "gate and up rows");
+  constexpr int NO = GLU ? 1 : NF;            // output fragments along N
+  constexpr int NC = GLU == 2 ? 8 : 16 * NO;  // output columns
   // a wave's batch on its way to the fragments; at the end its sums
   constexpr int PIECES = UN * 2 * (MF + NF);
   static_assert(MF * NF <= PIECES, "the sums take the batch's place");
@@ -46,32 +48,45 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
   const int n_lim = GLU ? args.inter : args.N;
-  const int n0 = blockIdx.x * (16 * NO);
-  const int rows_n = n_lim - n0 < 16 * NO ? n_lim - n0 : 16 * NO;
+  const int n0 = blockIdx.x * NC;
+  const int rows_n = n_lim - n0 < NC ? n_lim - n0 : NC;
 
-  // the epilogue's part of this thread: fragment (fm, fn), row m, columns n .. n+3
-  const int fq = tid >> 6, fm = fq / NO, fn = fq % NO;
-  const int m = 16 * fm + r16, n = n0 + 16 * fn + 4 * lg;
-  const bool mine = fq < MF * NO && m < args.M && n < n_lim;
-  const int cnt = n_lim - n < 4 ? n_lim - n : 4;
-  Bf16s<4>::t res = {0, 0};
-  float bias[4] = {};
-  if (!GLU && mine) {
-    if (args.R) res = load_bf16s<4>(args.R + (int64_t)m * args.ldr + n, cnt);
-    if (args.bias) unpack<4>(load_bf16s<4>(args.bias + n, cnt), bias);
+  // The epilogue's part of this thread: output fragments wave, wave + W, ...; in each row m,
+  // columns n .. n+3.  What it reads is loaded ahead of the product.
+  constexpr int Q = (MF * NO + W - 1) / W;
+  auto row_of = [&](int q) { return 16 * ((wave + q * W) / NO) + r16; };
+  auto col_of = [&](int q) { return n0 + 16 * ((wave + q * W) % NO) + 4 * lg; };
+  auto mine = [&](int q) {
+    return wave + q * W < MF * NO && row_of(q) < args.M && col_of(q) < n_lim && (GLU != 2 || lg < 2);
+  };
+  Bf16s<4>::t res[Q] = {};
+  float bias[Q][4] = {};
+  if constexpr (!GLU) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (!mine(q)) continue;
+      const int n = col_of(q), cnt = n_lim - n < 4 ? n_lim - n : 4;
+      if (args.R) res[q] = load_bf16s<4>(args.R + (int64_t)row_of(q) * args.ldr + n, cnt);
+      if (args.bias) unpack<4>(load_bf16s<4>(args.bias + n, cnt), bias[q]);
+    }
   }
 
   // records end with the operands' last byte: rows past M or N read zero
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(args.A, (uint32_t)((args.M - 1) * args.lda + args.k_bytes));
   const uint8_t* const B0 = args.B + (int64_t)n0 * args.ldb;
-  const uint32_t rec_b = (uint32_t)((rows_n - 1) * args.ldb + args.k_bytes);
+  // (both kinds of rows through one resource: the launcher keeps its record below 2^31)
+  const uint32_t rec_b = (uint32_t)((rows_n - 1 + (GLU == 2 ? (int64_t)args.inter : 0)) * args.ldb + args.k_bytes);
   const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(B0, rec_b);
-  const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(GLU ? B0 + (int64_t)args.inter * args.ldb : B0, rec_b);
+  const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(GLU == 1 ? B0 + (int64_t)args.inter * args.ldb : B0, rec_b);
   uint32_t va[MF], vb[NF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) va[f] = (uint32_t)((16 * f + (lane >> 2)) * args.lda) + 16 * (lane & 3);
 #pragma unroll
-  for (int f = 0; f < NF; ++f) vb[f] = (uint32_t)(((GLU ? 0 : 16 * f) + (lane >> 2)) * args.ldb) + 16 * (lane & 3);
+  for (int f = 0; f < NF; ++f) {
+    const int r = lane >> 2;
+    const int64_t row = GLU == 2 ? (r & 7) + (r >> 3) * args.inter : (GLU ? 0 : 16 * f) + r;
+    vb[f] = (uint32_t)(row * args.ldb) + 16 * (lane & 3);
+  }
   // piece (16 rows x 64 bytes): row r's chunk c at 4r + (c ^ (r >> 2)), so that both the
   // stores (4 rows of 4 chunks) and the fragment reads (one chunk of 16 rows) of 16 lanes
   // cover all banks once
@@ -110,7 +125,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
 #pragma unroll
         for (int f = 0; f < NF; ++f)
           t.b[u][h][f] = __builtin_bit_cast(
-              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(GLU && f ? rb1 : rb0, (vb[f] + k) | oob, 0, 0));
+              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(GLU == 1 && f ? rb1 : rb0, (vb[f] + k) | oob, 0, 0));
 #pragma unroll
         for (int f = 0; f < MF; ++f)
           t.a[u][h][f] = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (va[f] + k) | oob, 0, 0));
@@ -198,33 +213,38 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
 #pragma unroll
     for (int fb = 0; fb < NF; ++fb) smem[wave][fa * NF + fb][lane] = __builtin_bit_cast(i32x4_t, acc[fa][fb]);
   __syncthreads();
-  if (!mine) return;
-  auto sum = [&](int f, float (&v)[4]) {
-    few_f32x4_t t = __builtin_bit_cast(few_f32x4_t, smem[0][f][lane]);
+  auto sum = [&](int f, float (&v)[4], int ln) {
+    few_f32x4_t t = __builtin_bit_cast(few_f32x4_t, smem[0][f][ln]);
 #pragma unroll
-    for (int w = 1; w < W; ++w) t += __builtin_bit_cast(few_f32x4_t, smem[w][f][lane]);
+    for (int w = 1; w < W; ++w) t += __builtin_bit_cast(few_f32x4_t, smem[w][f][ln]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = t[e];
   };
-  float z[4];
-  uint16_t* const Z = args.Z ? args.Z + (int64_t)m * args.ldz + n : nullptr;
-  uint16_t* const D = args.D + (int64_t)m * args.ldd + n;
-  if constexpr (GLU) {
-    float u[4];
-    sum(fm * NF, z);
-    sum(fm * NF + 1, u);
-    glu_row<4>(args.act, z, u, Z, args.inter, D, args.e_vec);
-  } else {
-    sum(fm * NF + fn, z);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] += bias[e];
-    act_row<4>(args.act, z, Z, res, args.R != nullptr, D, args.e_vec, cnt);
+  for (int q = 0; q < Q; ++q) {
+    if (!mine(q)) continue;
+    const int fm = (wave + q * W) / NO, fn = (wave + q * W) % NO, n = col_of(q);
+    const int64_t m = row_of(q);
+    uint16_t* const Z = args.Z ? args.Z + m * args.ldz + n : nullptr;
+    uint16_t* const D = args.D + m * args.ldd + n;
+    float z[4];
+    if constexpr (GLU) {
+      float u[4];
+      sum(fm * NF, z, lane);
+      sum(fm * NF + (GLU == 1 ? 1 : 0), u, GLU == 1 ? lane : lane + 32);   // (up rows: 8 .. 15 of the fragment)
+      glu_row<4>(args.act, z, u, Z, args.inter, D, args.e_vec);
+    } else {
+      sum(fm * NF + fn, z, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] += bias[q][e];
+      act_row<4>(args.act, z, Z, res[q], args.R != nullptr, D, args.e_vec, n_lim - n < 4 ? n_lim - n : 4);
+    }
   }
 }
 
-template <int KIND, int MF, int NF, bool GLU, int W>
+template <int KIND, int MF, int NF, int GLU, int W>
 static int go(const GemmArgs& a, hipStream_t st) {
-  const int per = GLU ? 16 : 16 * NF, n = GLU ? a.inter : a.N;
+  const int per = GLU == 2 ? 8 : (GLU ? 16 : 16 * NF), n = GLU ? a.inter : a.N;
   (void)hipGetLastError();
   hipLaunchKernelGGL((few_kernel<KIND, MF, NF, GLU, W, 1>), dim3((unsigned)((n + per - 1) / per)), dim3(W * 64), 0, st,
                      a);
@@ -238,17 +258,20 @@ static int go(const GemmArgs& a, hipStream_t st) {
 // 12.2 us against 13.3 with 8.
 template <int KIND>
 static int go_rows(const GemmArgs& a, hipStream_t st) {
-  if (a.M <= 16) return go<KIND, 1, 1, false, 16>(a, st);
+  if (a.M <= 16) return go<KIND, 1, 1, 0, 16>(a, st);
   const bool wide = a.N >= 32 * 192;
-  if (a.M <= 32) return wide ? go<KIND, 2, 2, false, 8>(a, st) : go<KIND, 2, 1, false, 8>(a, st);
-  return wide ? go<KIND, 4, 2, false, 4>(a, st) : go<KIND, 4, 1, false, 8>(a, st);
+  if (a.M <= 32) return wide ? go<KIND, 2, 2, 0, 8>(a, st) : go<KIND, 2, 1, 0, 8>(a, st);
+  return wide ? go<KIND, 4, 2, 0, 4>(a, st) : go<KIND, 4, 1, 0, 8>(a, st);
 }
 
 int dense_few(int kind, const GemmArgs& a, bool glu, void* stream) {
   const hipStream_t st = (hipStream_t)stream;
-  if (glu)
-    return a.M <= 16 ? go<KIND_BF16, 1, 2, true, 16>(a, st)
-                     : (a.M <= 32 ? go<KIND_BF16, 2, 2, true, 8>(a, st) : go<KIND_BF16, 4, 2, true, 8>(a, st));
+  if (glu) {
+    const bool narrow = a.inter < 16 * 192 && (a.inter + 8) * a.ldb < (int64_t)1 << 31;
+    if (a.M <= 16) return narrow ? go<KIND_BF16, 1, 1, 2, 16>(a, st) : go<KIND_BF16, 1, 2, 1, 16>(a, st);
+    if (a.M <= 32) return narrow ? go<KIND_BF16, 2, 1, 2, 8>(a, st) : go<KIND_BF16, 2, 2, 1, 8>(a, st);
+    return narrow ? go<KIND_BF16, 4, 1, 2, 8>(a, st) : go<KIND_BF16, 4, 2, 1, 8>(a, st);
+  }
   switch (kind) {
     case KIND_BF16: return go_rows<KIND_BF16>(a, st);
     case KIND_FP8: return go_rows<KIND_FP8>(a, st);

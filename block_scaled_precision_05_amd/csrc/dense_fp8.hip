@@ -11,8 +11,7 @@ namespace bsg {
 
 template <int SV>
 static int go(const GemmArgs& a, int form, hipStream_t st) {
-  if (form == DENSE_SMALL_PART) return launch<KIND_FP8, BSG_FP8_SMALL_CFG, false, SV, EPI_PART>(a, st);
-  if (form == DENSE_BIG_PART) return launch<KIND_FP8, BSG_FP8_PART_CFG, false, SV, EPI_PART>(a, st);
+  if (form == DENSE_PART) return launch<KIND_FP8, BSG_FP8_SMALL_CFG, false, SV, EPI_PART>(a, st);
   return form == DENSE_BIG ? launch<KIND_FP8, BSG_FP8_CFG, false, SV, EPI_ACT>(a, st)
                            : launch<KIND_FP8, BSG_FP8_SMALL_CFG, false, SV, EPI_ACT>(a, st);
 }

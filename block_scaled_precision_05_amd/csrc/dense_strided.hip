@@ -12,8 +12,8 @@ namespace bsg {
 
 template <int TR>
 static int go(const GemmArgs& a, int form, hipStream_t st) {
-  if (form == DENSE_SMALL_PART) return launch<KIND_BF16, BSG_BF16_SMALL_CFG, false, 0, TR + EPI_PART>(a, st);
-  if (form == DENSE_BIG_PART) return launch<KIND_BF16, BSG_BF16_PART_CFG, false, 0, TR + EPI_PART>(a, st);
+  if (form == DENSE_PART) return launch<KIND_BF16, BSG_BF16_DEEP_CFG, false, 0, TR + EPI_PART>(a, st);
+  if (form == DENSE_DEEP) return launch<KIND_BF16, BSG_BF16_DEEP_CFG, false, 0, TR>(a, st);
   return form == DENSE_BIG ? launch<KIND_BF16, BSG_BF16_CFG, false, 0, TR>(a, st)
                            : launch<KIND_BF16, BSG_BF16_SMALL_CFG, false, 0, TR>(a, st);
 }

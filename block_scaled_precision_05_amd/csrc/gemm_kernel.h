@@ -569,19 +569,25 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
       b8[e] = args.bias && n + e < n_end ? bf16_f32(args.bias[n + e]) : 0.0f;
   }
   auto real_row = [&](int half, int s) { return T::PERM_A ? 4 * (s & 31) + half * HF + (s >> 5) : half * HR + s; };
+  // The residual's rows, all of them before the first store: loads and stores complete in
+  // one order, so a load waited for between the stores would wait for those before it
+  // (FP8 tiles of 128 rows: 5 us a tile).  The second half's come when the first half of
+  // the accumulators has left the registers.
+  Bf16s<8>::t res[2][IT] = {};
+  auto load_res = [&](int half) {
+    if constexpr (E == EPI_ACT) {
+      if (args.R && cnt > 0) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          const int row = real_row(half, it * RPI + rr);
+          if (row < rows_w) res[half][it] = load_bf16s<8>(args.R + (int64_t)(row0 + row) * args.ldr + n, cnt);
+        }
+      }
+    }
+  };
+  load_res(0);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    // the residual's rows, two iterations ahead of their use
-    auto load_r = [&](int it) {
-      Bf16s<8>::t v = {0, 0, 0, 0};
-      if constexpr (E == EPI_ACT) {
-        const int row = real_row(half, it * RPI + rr);
-        if (args.R && cnt > 0 && it < IT && row < rows_w)
-          v = load_bf16s<8>(args.R + (int64_t)(row0 + row) * args.ldr + n, cnt);
-      }
-      return v;
-    };
-    Bf16s<8>::t r0 = load_r(0), r1 = load_r(1);
 #pragma unroll
     for (int a = 0; a < HF; ++a) {
       const int s = 32 * a + el32;
@@ -604,44 +610,81 @@ __device__ __forceinline__ void dense_epilogue(const GemmArgs& args, f32x16_t (&
         }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (half == 0) load_res(1);
     // (a wave reads back only what it wrote; its LDS accesses execute in order)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    auto read8 = [&](int s, int chunk, float (&v)[8]) {
+      const f32x4_t lo = *(const f32x4_t*)(stg + 256 * s + 16 * (chunk ^ (s & 15)));
+      const f32x4_t hi = *(const f32x4_t*)(stg + 256 * s + 16 * ((chunk + 1) ^ (s & 15)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+      }
+    };
+    // The usual epilogue of a down-projection, a residual and no activation, in one
+    // unrolled pass; an activation goes through a rolled loop, its results back into the
+    // staged rows where a residual (registers: unrolled) is still to be added.
+    const bool only_add = E == EPI_ACT && args.R && args.act == BSG_ACT_NONE;
+    static_assert(IT % 2 == 0, "two iterations at a time: the second's LDS reads under the first's arithmetic");
 #pragma unroll 1
-    for (int it = 0; it < IT; ++it) {
-      const int s = it * RPI + rr, row = real_row(half, s);
-      const Bf16s<8>::t r2 = load_r(it + 2);
-      auto read8 = [&](int chunk, float (&v)[8]) {
-        const f32x4_t lo = *(const f32x4_t*)(stg + 256 * s + 16 * (chunk ^ (s & 15)));
-        const f32x4_t hi = *(const f32x4_t*)(stg + 256 * s + 16 * ((chunk + 1) ^ (s & 15)));
+    for (int it0 = 0; it0 < (only_add ? 0 : IT); it0 += 2) {
+      float zz[2][8], uu[GLU ? 2 : 1][8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = lo[e];
-          v[4 + e] = hi[e];
-        }
-      };
-      float z[8];
-      read8(2 * seg, z);
-      if (row < rows_w && cnt > 0) {
-        const int64_t m = row0 + row;
-        if constexpr (PART) {
-          // (P's rows are padded to a multiple of 8 columns)
-          float* const d = args.P + (int64_t)part * args.part_stride + m * args.ldp + n;
-          *(f32x4_t*)d = (f32x4_t){z[0], z[1], z[2], z[3]};
-          *(f32x4_t*)(d + 4) = (f32x4_t){z[4], z[5], z[6], z[7]};
-        } else if constexpr (GLU) {
-          float u[8];
-          read8(8 + 2 * seg, u);
-          glu_row<8>(args.act, z, u, args.Z ? args.Z + m * args.ldz + n : nullptr, args.inter,
-                     args.D + m * args.ldd + n, vec);
-        } else {
+      for (int j = 0; j < 2; ++j) {
+        const int s = (it0 + j) * RPI + rr;
+        read8(s, 2 * seg, zz[j]);
+        if constexpr (GLU) read8(s, 8 + 2 * seg, uu[j]);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] += b8[e];
-          act_row<8>(args.act, z, args.Z ? args.Z + m * args.ldz + n : nullptr, r0, args.R != nullptr,
-                     args.D + m * args.ldd + n, vec, cnt);
+      for (int j = 0; j < 2; ++j) {
+        const int s = (it0 + j) * RPI + rr, row = real_row(half, s);
+        float(&z)[8] = zz[j];
+        if (row < rows_w && cnt > 0) {
+          const int64_t m = row0 + row;
+          if constexpr (PART) {
+            // (P's rows are padded to a multiple of 8 columns)
+            float* const d = args.P + (int64_t)part * args.part_stride + m * args.ldp + n;
+            *(f32x4_t*)d = (f32x4_t){z[0], z[1], z[2], z[3]};
+            *(f32x4_t*)(d + 4) = (f32x4_t){z[4], z[5], z[6], z[7]};
+          } else if constexpr (GLU) {
+            glu_row<8>(args.act, z, uu[j], args.Z ? args.Z + m * args.ldz + n : nullptr, args.inter,
+                       args.D + m * args.ldd + n, vec);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += b8[e];
+            if (args.Z) store_bf16s<8>(args.Z + m * args.ldz + n, z, vec, cnt);
+            act_all<8>(args.act, z);
+            if (args.R) {
+              *(f32x4_t*)(stg + 256 * s + 16 * ((2 * seg) ^ (s & 15))) = (f32x4_t){z[0], z[1], z[2], z[3]};
+              *(f32x4_t*)(stg + 256 * s + 16 * ((2 * seg + 1) ^ (s & 15))) = (f32x4_t){z[4], z[5], z[6], z[7]};
+            } else {
+              store_bf16s<8>(args.D + m * args.ldd + n, z, vec, cnt);
+            }
+          }
         }
       }
-      r0 = r1;
-      r1 = r2;
+    }
+    if constexpr (E == EPI_ACT) {
+      if (args.R) {
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          const int s = it * RPI + rr, row = real_row(half, s);
+          float z[8], r[8];
+          read8(s, 2 * seg, z);
+          unpack<8>(res[half][it], r);
+          if (only_add) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += b8[e];
+            if (args.Z && row < rows_w && cnt > 0)
+              store_bf16s<8>(args.Z + (int64_t)(row0 + row) * args.ldz + n, z, vec, cnt);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] += r[e];
+          if (row < rows_w && cnt > 0) store_bf16s<8>(args.D + (int64_t)(row0 + row) * args.ldd + n, z, vec, cnt);
+        }
+      }
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   }

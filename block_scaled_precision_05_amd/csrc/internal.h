@@ -40,13 +40,13 @@ int grouped_fp8_swiglu(const void* A, int64_t lda, const int16_t* sfa, int64_t l
 struct GemmArgs;
 
 // Dense products with epilogues and with strided contractions: how a call is carried out.
-//   DENSE_BIG         256x256 tiles, the epilogue in the kernel
-//   DENSE_SMALL       smaller tiles (128 rows), the epilogue in the kernel
-//   DENSE_BIG_PART    256x256 or
-//   DENSE_SMALL_PART  smaller tiles over `splits` parts of the contraction, fp32 sums in a
-//                     workspace [splits][M][ldp], joined by a second kernel with the epilogue
-//   DENSE_FEW         up to 64 rows of A: B streamed through registers
-enum DenseForm { DENSE_BIG, DENSE_SMALL, DENSE_BIG_PART, DENSE_SMALL_PART, DENSE_FEW };
+//   DENSE_BIG    256x256 tiles, the epilogue in the kernel
+//   DENSE_SMALL  smaller tiles (128 rows), the epilogue in the kernel
+//   DENSE_DEEP   the same with a deeper ring, for at most one workgroup a CU (BF16)
+//   DENSE_PART   smaller tiles over `splits` parts of the contraction, fp32 sums in a
+//                workspace [splits][M][ldp], joined by a second kernel with the epilogue
+//   DENSE_FEW    up to 64 rows of A: B streamed through registers
+enum DenseForm { DENSE_BIG, DENSE_SMALL, DENSE_DEEP, DENSE_PART, DENSE_FEW };
 struct DensePlan {
   int form;
   int splits;
@@ -55,10 +55,9 @@ struct DensePlan {
 // The plan of a product of M x N outputs over K elements (kind 0 BF16, 1 FP8, 2 FP4);
 // strided: one of the gradients' products.
 DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided = false);
-inline bool dense_parts(int form) { return form == DENSE_BIG_PART || form == DENSE_SMALL_PART; }
 inline int64_t dense_ldp(int64_t N) { return (N + 7) / 8 * 8; }
 inline int64_t dense_part_bytes(const DensePlan& p, int64_t M, int64_t N) {
-  return dense_parts(p.form) ? 4 * p.splits * M * dense_ldp(N) : 0;
+  return p.form == DENSE_PART ? 4 * p.splits * M * dense_ldp(N) : 0;
 }
 
 // Launches of the kernel instances, one function a translation unit.  epi: EPI_ACT or

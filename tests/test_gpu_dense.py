@@ -56,7 +56,7 @@ def _z(A, B):
 # M, N, K: single rows and columns, odd sizes, a contraction shorter than one stage and with a
 # tail, tiles of every form (parts of the contraction, 128-row tiles, 256-row tiles)
 SIZES = [(1, 1, 8), (1, 129, 2048), (2, 7168, 520), (5, 3, 40), (16, 520, 4096), (17, 100, 1032), (33, 65, 264),
-         (64, 2048, 1024), (130, 257, 1000), (200, 1001, 2056), (1001, 1003, 520), (2048, 1920, 96),
+         (64, 2048, 1024), (20, 6200, 264), (32, 7168, 128), (45, 6151, 72), (64, 7168, 2048), (130, 257, 1000), (200, 1001, 2056), (1001, 1003, 520), (2048, 1920, 96),
          (3900, 3400, 136), (3841, 3457, 328)]
 
 
@@ -137,7 +137,8 @@ def _scaled(fmt, M, N, K, seed, gran=128):
 
 
 @pytest.mark.parametrize("fmt,M,N,K", [
-    ("fp8", 1, 7168, 256), ("fp8", 3, 40, 128), ("fp8", 64, 520, 2048), ("fp8", 130, 257, 896),
+    ("fp8", 1, 7168, 256), ("fp8", 3, 40, 128), ("fp8", 30, 6160, 384), ("fp8", 64, 7168, 2048), ("fp8", 50, 6147, 128),
+    ("fp4", 25, 6145, 288), ("fp4", 64, 6400, 512), ("fp4", 40, 1000, 2080), ("fp8", 20, 515, 1152), ("fp8", 64, 520, 2048), ("fp8", 130, 257, 896),
     ("fp8", 300, 1000, 1152), ("fp8", 3900, 3400, 128), ("fp8", 3841, 3457, 384),
     ("fp4", 1, 1024, 96), ("fp4", 8, 40, 32), ("fp4", 8, 512, 7168), ("fp4", 130, 257, 1056),
     ("fp4", 1000, 515, 544), ("fp4", 3900, 3400, 160), ("fp4", 3841, 3457, 96)])
@@ -168,7 +169,8 @@ def _minus3(packed):
     return (packed.to(torch.int32) - 0x0303).to(torch.int16)
 
 
-GLU = [(1, 8, 8), (1, 2048, 512), (3, 40, 264), (32, 1024, 1024), (48, 200, 2048), (130, 264, 1000), (777, 1000, 264),
+GLU = [(1, 8, 8), (1, 2048, 512), (3, 40, 264), (5, 3080, 72), (20, 3200, 136), (30, 72, 264), (50, 3144, 264),
+       (64, 248, 1024), (33, 1000, 4096), (32, 1024, 1024), (48, 200, 2048), (130, 264, 1000), (777, 1000, 264),
        (2000, 2040, 72), (3841, 1800, 200), (4100, 3000, 40)]
 
 
