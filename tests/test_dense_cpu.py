@@ -1,0 +1,245 @@
+"""Dense products with epilogues, the gated block and their gradients: what the entry points
+refuse, before any HIP call (no GPU needed: pointers are numbers here), their workspaces,
+and pins of the fp64 forms in oracle/dense.py."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_05_amd as bsg
+from oracle import dense
+
+OK, INVALID, SHAPE, ALIGN = bsg.BSG_OK, bsg.BSG_ERR_INVALID_ARG, bsg.BSG_ERR_UNSUPPORTED_SHAPE, bsg.BSG_ERR_MISALIGNED
+P = 1 << 20          # an aligned address that no refused call touches
+BIG = 1 << 31
+
+
+def _call(fn, order, base, **kw):
+    """The status of fn with the arguments of `base`, some replaced."""
+    assert set(kw) <= set(base)
+    a = {**base, **kw}
+    return getattr(bsg.lib(), fn)(*[a[k] for k in order.split()])
+
+
+ACT = "A lda B ldb bias act R ldr D ldd Z ldz M N K ws bytes stream"
+ACT_OK = dict(A=P, lda=64, B=P, ldb=64, bias=P, act=3, R=P, ldr=40, D=P, ldd=40, Z=P, ldz=40, M=100, N=40, K=64,
+              ws=P, bytes=1 << 40, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=-1), INVALID), (dict(act=5), INVALID), (dict(M=-1), INVALID), (dict(N=-1), INVALID),
+    (dict(K=-8), INVALID), (dict(K=60), SHAPE), (dict(A=0), INVALID), (dict(B=0), INVALID), (dict(D=0), INVALID),
+    (dict(lda=56), INVALID), (dict(ldb=56), INVALID), (dict(ldd=39), INVALID), (dict(ldr=39), INVALID),
+    (dict(ldz=39), INVALID), (dict(A=P + 8), ALIGN), (dict(B=P + 2), ALIGN), (dict(lda=68), ALIGN),
+    (dict(ldb=68), ALIGN), (dict(D=P + 1), ALIGN), (dict(R=P + 1), ALIGN), (dict(Z=P + 1), ALIGN),
+    (dict(bias=P + 1), ALIGN), (dict(M=BIG), SHAPE), (dict(N=BIG, ldd=BIG), SHAPE), (dict(lda=BIG), SHAPE),
+    (dict(ldr=BIG), SHAPE), (dict(ldz=BIG), SHAPE), (dict(M=1 << 30, N=1 << 20, ldd=1 << 20, ldr=1 << 20, ldz=1 << 20), SHAPE)])
+def test_act_refusals(kw, status):
+    assert _call("gemm_bf16_act", ACT, ACT_OK, **kw) == status
+
+
+def test_act_workspace_refusals():
+    # a call that is split: 100 x 40 over a long contraction
+    need = bsg.lib().gemm_bf16_act_workspace(100, 40, 8192)
+    assert need > 0 and need % 16 == 0
+    long = dict(K=8192, lda=8192, ldb=8192)
+    assert _call("gemm_bf16_act", ACT, ACT_OK, **long, ws=0) == INVALID
+    assert _call("gemm_bf16_act", ACT, ACT_OK, **long, bytes=need - 1) == INVALID
+    assert _call("gemm_bf16_act", ACT, ACT_OK, **long, ws=P + 4) == ALIGN
+    assert bsg.lib().gemm_bf16_act_workspace(1, 40, 8192) == 0       # few rows: one kernel
+    for f in ("gemm_bf16_act", "gemm_fp8_act", "gemm_fp4_act", "gemm_bf16_glu"):
+        size = getattr(bsg.lib(), f + "_workspace")
+        assert size(0, 8, 64) == size(8, 0, 64) == size(-1, 8, 64) == size(8, 8, 0) == 0
+
+
+def test_empty_calls_need_nothing():
+    assert _call("gemm_bf16_act", ACT, ACT_OK, M=0, A=0, B=0, D=0, R=0, Z=0, bias=0, ws=0, bytes=0) == OK
+    assert _call("gemm_bf16_act", ACT, ACT_OK, N=0, A=0, B=0, D=0, R=0, Z=0, bias=0, ws=0, bytes=0) == OK
+    assert _call("gemm_bf16_act", ACT, ACT_OK, M=0, act=9) == INVALID
+
+
+FP8 = "A lda sfa ld_sfa B ldb sfb ld_sfb gran bias act R ldr D ldd M N K ws bytes stream"
+FP8_OK = dict(A=P, lda=256, sfa=P, ld_sfa=100, B=P, ldb=256, sfb=P, ld_sfb=40, gran=128, bias=0, act=0, R=0, ldr=0,
+              D=P, ldd=40, M=100, N=40, K=256, ws=P, bytes=1 << 40, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(gran=64), SHAPE), (dict(K=192), SHAPE), (dict(sfa=0), INVALID), (dict(sfb=0), INVALID),
+    (dict(ld_sfa=99), INVALID), (dict(ld_sfb=0), INVALID), (dict(gran=1, ld_sfb=39), INVALID), (dict(sfa=P + 1), ALIGN),
+    (dict(sfb=P + 1), ALIGN), (dict(act=7), INVALID), (dict(lda=264), ALIGN), (dict(R=P, ldr=39), INVALID),
+    (dict(ld_sfa=1 << 30), SHAPE), (dict(D=0), INVALID), (dict(bias=P + 1), ALIGN)])
+def test_fp8_act_refusals(kw, status):
+    assert _call("gemm_fp8_act", FP8, FP8_OK, **kw) == status
+
+
+FP4 = FP8.replace(" gran", "")
+FP4_OK = {k: v for k, v in {**FP8_OK, "lda": 128, "ldb": 128}.items() if k != "gran"}
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=240), SHAPE), (dict(ld_sfb=39), INVALID), (dict(ld_sfa=99), INVALID), (dict(lda=112), INVALID),
+    (dict(ldb=136), ALIGN), (dict(sfa=P + 1), ALIGN), (dict(act=-2), INVALID), (dict(R=P + 1, ldr=40), ALIGN)])
+def test_fp4_act_refusals(kw, status):
+    assert _call("gemm_fp4_act", FP4, FP4_OK, **kw) == status
+
+
+BWD = "dD lddd Z ldz A lda B ldb act dA ldda dB lddb dbias M N K ws bytes stream"
+BWD_OK = dict(dD=P, lddd=40, Z=P, ldz=40, A=P, lda=64, B=P, ldb=64, act=2, dA=P, ldda=64, dB=P, lddb=64, dbias=P,
+              M=100, N=40, K=64, ws=P, bytes=1 << 40, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=5), INVALID), (dict(M=-1), INVALID), (dict(K=-8), INVALID), (dict(K=60), SHAPE), (dict(dD=0), INVALID),
+    (dict(Z=0), INVALID), (dict(lddd=39), INVALID), (dict(ldz=39), INVALID), (dict(A=0), INVALID), (dict(B=0), INVALID),
+    (dict(lda=56), INVALID), (dict(ldb=56), INVALID), (dict(ldda=63), INVALID), (dict(lddb=63), INVALID),
+    (dict(A=P + 8), ALIGN), (dict(B=P + 8), ALIGN), (dict(lda=68), ALIGN), (dict(dA=P + 1), ALIGN),
+    (dict(dB=P + 1), ALIGN), (dict(dD=P + 1), ALIGN), (dict(Z=P + 1), ALIGN), (dict(dbias=P + 2), ALIGN),
+    (dict(ws=0), INVALID), (dict(ws=P + 8), ALIGN), (dict(bytes=100 * 40 * 2 - 1), INVALID), (dict(M=1 << 30), SHAPE),
+    (dict(N=1 << 23, lddd=1 << 23, ldz=1 << 23), SHAPE), (dict(K=1 << 23, lda=1 << 23, ldb=1 << 23), SHAPE),
+    (dict(M=(1 << 30) - 1, N=4096, lddd=4096, ldz=4096), SHAPE)])
+def test_act_backward_refusals(kw, status):
+    assert _call("gemm_bf16_act_backward", BWD, BWD_OK, **kw) == status
+
+
+GLU = "X ldx W ldw act H ldh Z ldz M inter K ws bytes stream"
+GLU_OK = dict(X=P, ldx=64, W=P, ldw=64, act=2, H=P, ldh=40, Z=P, ldz=80, M=100, inter=40, K=64, ws=P, bytes=1 << 40,
+              stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(inter=-8), INVALID), (dict(inter=36), SHAPE), (dict(K=4), SHAPE), (dict(ldh=39), INVALID),
+    (dict(ldz=79), INVALID), (dict(X=0), INVALID), (dict(W=0), INVALID), (dict(H=0), INVALID), (dict(act=8), INVALID),
+    (dict(X=P + 8), ALIGN), (dict(ldw=72, W=P + 4), ALIGN), (dict(H=P + 1), ALIGN), (dict(Z=P + 1), ALIGN),
+    (dict(inter=1 << 30), SHAPE), (dict(M=BIG), SHAPE), (dict(ldx=56), INVALID)])
+def test_glu_refusals(kw, status):
+    assert _call("gemm_bf16_glu", GLU, GLU_OK, **kw) == status
+
+
+GBW = "dH lddh Z ldz X ldx W ldw act dX lddx dW lddw M inter K ws bytes stream"
+GBW_OK = dict(dH=P, lddh=40, Z=P, ldz=80, X=P, ldx=64, W=P, ldw=64, act=2, dX=P, lddx=64, dW=P, lddw=64, M=100,
+              inter=40, K=64, ws=P, bytes=1 << 40, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(inter=36), SHAPE), (dict(inter=-8), INVALID), (dict(K=60), SHAPE), (dict(dH=0), INVALID),
+    (dict(Z=0), INVALID), (dict(lddh=39), INVALID), (dict(ldz=79), INVALID), (dict(X=0), INVALID), (dict(W=0), INVALID),
+    (dict(lddx=63), INVALID), (dict(lddw=63), INVALID), (dict(X=P + 8), ALIGN), (dict(W=P + 8), ALIGN),
+    (dict(dX=P + 1), ALIGN), (dict(ws=0), INVALID), (dict(bytes=100 * 80 * 2 - 1), INVALID), (dict(act=-1), INVALID),
+    (dict(M=1 << 30), SHAPE), (dict(inter=1 << 22, lddh=1 << 22, ldz=1 << 23), SHAPE)])
+def test_glu_backward_refusals(kw, status):
+    assert _call("gemm_bf16_glu_backward", GBW, GBW_OK, **kw) == status
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        bsg.gemm_bf16_act(b(4, 64), b(8, 64))
+    with pytest.raises(ValueError):
+        bsg.gemm_bf16_glu(b(4, 64), b(16, 64))
+    with pytest.raises(ValueError):
+        bsg.gemm_bf16_act_backward(b(4, 8), b(4, 64), b(8, 64))
+    with pytest.raises(ValueError):
+        bsg.gemm_bf16_glu_backward(b(4, 8), b(4, 64), b(16, 64), b(4, 16))
+    u = torch.zeros(4, 128, dtype=torch.uint8)
+    s = torch.zeros(1, 4, dtype=torch.int16)
+    with pytest.raises(ValueError):
+        bsg.gemm_fp8_act(u, s, u, s)
+    with pytest.raises(ValueError):
+        bsg.gemm_fp4_act(u, s, u, s)
+    assert sorted(bsg.ACTIVATIONS) == ["gelu", "gelu_tanh", "none", "relu", "silu"]
+
+
+# ---- pins of oracle/dense.py ---------------------------------------------------------------
+
+def test_activations_worked_values():
+    """silu(1) = 1/(1 + 1/e); gelu(1) = Phi(1) = (1 + erf(1/sqrt 2))/2; the tanh form of it;
+    odd parts: gelu(-z) = gelu(z) - z, silu(-z) = silu(z) - z."""
+    z = np.array([1.0, -1.0, 0.0, 2.0])
+    assert dense.f(z, "silu")[0] == pytest.approx(1 / (1 + math.exp(-1)), rel=1e-14)
+    assert dense.f(z, "gelu")[0] == pytest.approx(0.5 * (1 + math.erf(1 / math.sqrt(2))), rel=1e-14)
+    t = math.tanh(math.sqrt(2 / math.pi) * 1.044715)
+    assert dense.f(z, "gelu_tanh")[0] == pytest.approx(0.5 * (1 + t), rel=1e-14)
+    assert dense.f(z, "relu").tolist() == [1, 0, 0, 2] and dense.f(z, "none") is z
+    x = np.linspace(-6, 6, 101)
+    for a in ("silu", "gelu", "gelu_tanh"):
+        assert np.allclose(dense.f(-x, a), dense.f(x, a) - x, atol=1e-14)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_derivatives_against_differences(act):
+    x = np.linspace(-8, 8, 400) + 0.01          # (away from relu's corner)
+    h = 1e-5
+    d, terms = dense.df(x, act)
+    assert np.allclose(d, (dense.f(x + h, act) - dense.f(x - h, act)) / (2 * h), atol=2e-9)
+    assert np.all(terms >= np.abs(d) - 1e-15)
+    assert np.max(np.abs(d)) < 1.13             # the slope the forward bounds use
+
+
+def _rand(*s, seed=0):
+    return np.random.default_rng(seed).standard_normal(s)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh"])
+def test_gradients_against_differences(act):
+    """Every element of every gradient by central differences of the forward form."""
+    M, N, K, h = 3, 4, 5, 1e-5
+    A, B, b, dD = _rand(M, K, seed=1), _rand(N, K, seed=2), _rand(N, seed=3), _rand(M, N, seed=4)
+
+    def loss(A, B, b):
+        return (dense.act_forward(A @ B.T, 0.0, K, b, act)[0] * dD).sum()
+    got = [g for g, _ in dense.act_backward(dD, A @ B.T + b, A, B, act)]
+    for i, g in enumerate(got):
+        for at in np.ndindex(g.shape):
+            hi, lo = ([A.copy(), B.copy(), b.copy()] for _ in range(2))
+            hi[i][at] += h
+            lo[i][at] -= h
+            assert g[at] == pytest.approx((loss(*hi) - loss(*lo)) / (2 * h), abs=1e-8)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_gradients_against_differences(act):
+    M, I, K, h = 3, 4, 5, 1e-5
+    X, W, dH = _rand(M, K, seed=5), _rand(2 * I, K, seed=6), _rand(M, I, seed=7)
+
+    def loss(X, W):
+        return (dense.glu_forward(X @ W.T, np.zeros((M, 2 * I)), K, act)[0] * dH).sum()
+    got = [g for g, _ in dense.glu_backward(dH, X @ W.T, X, W, act)]
+    for i, g in enumerate(got):
+        for at in np.ndindex(g.shape):
+            hi, lo = ([X.copy(), W.copy()] for _ in range(2))
+            hi[i][at] += h
+            lo[i][at] -= h
+            assert g[at] == pytest.approx((loss(*hi) - loss(*lo)) / (2 * h), abs=1e-8)
+
+
+def test_forward_forms_against_torch():
+    z = _rand(7, 12, seed=8) * 3
+    t = torch.from_numpy(z)
+    F = torch.nn.functional
+    named = {"none": lambda v: v, "relu": F.relu, "silu": F.silu, "gelu": F.gelu,
+             "gelu_tanh": lambda v: F.gelu(v, approximate="tanh")}
+    b, R = _rand(12, seed=9), _rand(7, 12, seed=10)
+    for a, f in named.items():
+        d, e, zb, _ = dense.act_forward(z, np.abs(z), 5, b, a, R)
+        assert np.allclose(d, R + f(t + torch.from_numpy(b)).numpy(), atol=1e-14) and np.allclose(zb, z + b)
+        assert np.all(e > 0)
+        h, e, _, _ = dense.glu_forward(z, np.abs(z), 5, a)
+        assert np.allclose(h, (f(t[:, :6]) * t[:, 6:]).numpy(), atol=1e-14) and np.all(e > 0)
+
+
+def test_bounds_hold_for_an_fp32_evaluation():
+    """A plain fp32 evaluation of the forward forms stays inside the bounds (so they are no
+    looser than what fp32 needs by construction, nor tighter)."""
+    M, N, K = 20, 24, 300
+    A, B = _rand(M, K, seed=11).astype(np.float32), (_rand(N, K, seed=12) / 16).astype(np.float32)
+    z, mag = A.astype(np.float64) @ B.astype(np.float64).T, np.abs(A.astype(np.float64)) @ np.abs(B.astype(np.float64)).T
+    z32 = np.zeros((M, N), np.float32)
+    for k in range(K):
+        z32 += A[:, k:k + 1] * B[None, :, k]
+    for a in ("silu", "gelu_tanh"):
+        d, e, _, _ = dense.act_forward(z, mag, K, None, a)
+        x = z32 / (1 + np.exp(-z32)) if a == "silu" else \
+            np.float32(0.5) * z32 * (1 + np.tanh(np.float32(dense.C) * (z32 + np.float32(dense.A3) * z32 ** 3)))
+        assert np.all(np.abs(x - d) <= e + 2.0 ** -24 * np.abs(z))
