@@ -118,9 +118,11 @@ __device__ __forceinline__ float act_f(float z) {
   } else if constexpr (ACT == BSG_ACT_SILU) {
     return z * sigmoid_f32(z);
   } else if constexpr (ACT == BSG_ACT_GELU) {
+    // z Phi(z): z q below zero, z - z q above (past 20, where q is 0, an infinite z has to
+    // stay one)
     float e;
-    const float q = normal_tail(fabsf(z), e);   // z Phi(z): z q below zero, z - z q above
-    return z < 0.0f ? z * q : __builtin_fmaf(-z, q, z);
+    const float zc = z > 20.0f ? 20.0f : z, q = normal_tail(fabsf(zc), e);
+    return z < 0.0f ? z * q : __builtin_fmaf(-zc, q, z);
   } else if constexpr (ACT == BSG_ACT_GELU_TANH) {
     // 1 + tanh(u) = 2 sigmoid(2u)
     return z * sigmoid_f32(2.0f * kGeluC * z * __builtin_fmaf(kGeluA * z, z, 1.0f));
@@ -145,7 +147,7 @@ __device__ __forceinline__ float act_df(float z, float& f) {
   } else if constexpr (ACT == BSG_ACT_GELU) {
     float e;
     const float q = normal_tail(fabsf(zc), e);
-    f = z < 0.0f ? z * q : __builtin_fmaf(-z, q, z);
+    f = z < 0.0f ? z * q : __builtin_fmaf(-zc, q, z);
     return (z < 0.0f ? q : 1.0f - q) + zc * e * 0.3989422804014327f;
   } else if constexpr (ACT == BSG_ACT_GELU_TANH) {
     const float s = sigmoid_f32(2.0f * kGeluC * z * __builtin_fmaf(kGeluA * z, z, 1.0f));

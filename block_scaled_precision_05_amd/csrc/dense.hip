@@ -24,7 +24,7 @@ namespace bsg {
 
 static const int64_t kMaxTiles = int64_t(1) << 24;
 static const int64_t kMaxRow = (int64_t(1) << 31) / 256 - 1;   // bytes of a row (32-bit offsets)
-static const int64_t kMaxRows = (int64_t(1) << 30) - 1;
+static const int64_t kMaxRows = (int64_t(1) << 29) - 1;        // a contraction's bytes stay in 31 bits
 
 // What a form costs, in microseconds, fitted to sweeps of every form over 128 to 4096 rows
 // (BF16 7168 x 2048, 2048 x 7168, the gated block and both strided products; FP8 4096 x
@@ -64,7 +64,8 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
   // Few rows: the stream of B through registers.  Up to 32 rows at any K; up to 64 where a
   // row is at most 8 KiB (64 rows, BF16 7168 x 2048: 12.2 us against 15.8 in parts; 2048 x
   // 7168: 21.3 against 18.1: every workgroup reads all of A).
-  if (!strided && (M <= 32 || (M <= 64 && bytes <= 8192))) return {DENSE_FEW, 1};
+  // (one workgroup of up to 1024 threads to 16 columns, 2^32 threads to a launch)
+  if (!strided && (M <= 32 || (M <= 64 && bytes <= 8192)) && N < (int64_t)1 << 25) return {DENSE_FEW, 1};
   DensePlan best = {DENSE_BIG, 1};
   double t_best = 1e30;
   for (const TileCost& c : kForms[kind]) {
@@ -282,7 +283,7 @@ static int check_rows(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return BSG_OK;
   if (!p || ld < cols) return BSG_ERR_INVALID_ARG;
   if ((uintptr_t)p & 1) return BSG_ERR_MISALIGNED;
-  return ld > kMaxRows ? BSG_ERR_UNSUPPORTED_SHAPE : BSG_OK;
+  return ld > (int64_t)1 << 30 ? BSG_ERR_UNSUPPORTED_SHAPE : BSG_OK;
 }
 
 // An operand of a product: 16-byte aligned rows, 32-bit row offsets.
@@ -311,6 +312,7 @@ static int act_args(GemmArgs& a, int kind, const void* bias, int32_t act, const 
   if (M == 0 || N == 0) return BSG_OK;
   if ((uintptr_t)bias & 1) return BSG_ERR_MISALIGNED;
   int st = R ? check_rows(R, ldr, M, N) : BSG_OK;
+  if (R && R == D && M > 1 && ldr != ldd) return BSG_ERR_INVALID_ARG;   // in place: the same rows
   if (st == BSG_OK && Z) st = check_rows(Z, ldz, M, N);
   if (st == BSG_OK) st = check_tiles(M, N);
   if (st != BSG_OK) return st;

@@ -544,8 +544,9 @@ int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_
  *   z[m][n] = sum_k A[m][k] B[n][k] + bias[n];  Z[m][n] = bf16(z);
  *   D[m][n] = bf16( R[m][n] + f(z[m][n]) )
  *   A, B, D: as gemm_bf16; bias: bf16 [N] or NULL; act: bsg_activation;
- *   R: bf16 [M][ldr >= N] or NULL (no residual; ldr is then ignored); R == D adds in
- *   place, any other overlap of an output with another operand is not allowed;
+ *   R: bf16 [M][ldr >= N] or NULL (no residual; ldr is then ignored); R == D (with
+ *   ldr == ldd) adds in place, any other overlap of an output with another operand is not
+ *   allowed;
  *   Z: bf16 [M][ldz >= N] or NULL: the pre-activation, which gemm_bf16_act_backward takes.
  *   Requirements of gemm_bf16; bias, R and Z 2-byte aligned (16-byte aligned with leading
  *   dimensions multiples of 8, R, Z and D move 16 bytes at a time).  K == 0 gives
@@ -578,8 +579,8 @@ int64_t gemm_fp4_act_workspace(int64_t M, int64_t N, int64_t K);
  *   dA, dB, dbias: each may be NULL (not computed); A is read for dB only, B for dA only.
  *   Z: bf16 [M][ldz >= N]; with BSG_ACT_NONE it is not read and may be NULL.
  *   Requires K % 8 == 0; A and B 16-byte aligned with leading dimensions multiples of 8;
- *   dD, Z, dA and dB 2-byte aligned, dbias 4-byte; M and N below 2^30.  An output must not
- *   overlap another operand.  M == 0 zeroes dB and dbias, N == 0 zeroes dA. */
+ *   dD, Z, dA and dB 2-byte aligned, dbias 4-byte; M below 2^29, N and K at most
+ *   2^22 - 8.  An output must not overlap another operand.  M == 0 zeroes dB and dbias, N == 0 zeroes dA. */
 int gemm_bf16_act_backward(const void* dD, int64_t lddd, const void* Z, int64_t ldz, const void* A, int64_t lda,
                            const void* B, int64_t ldb, int32_t act, void* dA, int64_t ldda, void* dB, int64_t lddb,
                            float* dbias, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
@@ -605,8 +606,8 @@ int64_t gemm_bf16_glu_workspace(int64_t M, int64_t inter, int64_t K);
  *   dX[m][k]   = bf16( sum_j dz[m][j] W13[j][k] )         bf16 [M][lddx >= K]
  *   dW13[j][k] = bf16( sum_m dz[m][j] X[m][k] )           bf16 [2*inter][lddw >= K]
  *   dX and dW13 may each be NULL.  Requires inter % 8 == 0, K % 8 == 0; X and W13 16-byte
- *   aligned with leading dimensions multiples of 8; the others 2-byte aligned; M and
- *   2*inter below 2^30. */
+ *   aligned with leading dimensions multiples of 8; the others 2-byte aligned; M below
+ *   2^29, 2*inter and K at most 2^22 - 8. */
 int gemm_bf16_glu_backward(const void* dH, int64_t lddh, const void* Z, int64_t ldz, const void* X, int64_t ldx,
                            const void* W13, int64_t ldw, int32_t act, void* dX, int64_t lddx, void* dW13,
                            int64_t lddw, int64_t M, int64_t inter, int64_t K, void* workspace,

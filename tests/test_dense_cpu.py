@@ -35,7 +35,7 @@ ACT_OK = dict(A=P, lda=64, B=P, ldb=64, bias=P, act=3, R=P, ldr=40, D=P, ldd=40,
     (dict(ldz=39), INVALID), (dict(A=P + 8), ALIGN), (dict(B=P + 2), ALIGN), (dict(lda=68), ALIGN),
     (dict(ldb=68), ALIGN), (dict(D=P + 1), ALIGN), (dict(R=P + 1), ALIGN), (dict(Z=P + 1), ALIGN),
     (dict(bias=P + 1), ALIGN), (dict(M=BIG), SHAPE), (dict(N=BIG, ldd=BIG), SHAPE), (dict(lda=BIG), SHAPE),
-    (dict(ldr=BIG), SHAPE), (dict(ldz=BIG), SHAPE), (dict(M=1 << 30, N=1 << 20, ldd=1 << 20, ldr=1 << 20, ldz=1 << 20), SHAPE)])
+    (dict(ldr=BIG, R=2 * P), SHAPE), (dict(R=P + 2048, D=P + 2048, ldr=48), INVALID), (dict(ldz=BIG), SHAPE), (dict(M=1 << 30, N=1 << 20, ldd=1 << 20, ldr=1 << 20, ldz=1 << 20), SHAPE)])
 def test_act_refusals(kw, status):
     assert _call("gemm_bf16_act", ACT, ACT_OK, **kw) == status
 
@@ -97,8 +97,8 @@ BWD_OK = dict(dD=P, lddd=40, Z=P, ldz=40, A=P, lda=64, B=P, ldb=64, act=2, dA=P,
     (dict(A=P + 8), ALIGN), (dict(B=P + 8), ALIGN), (dict(lda=68), ALIGN), (dict(dA=P + 1), ALIGN),
     (dict(dB=P + 1), ALIGN), (dict(dD=P + 1), ALIGN), (dict(Z=P + 1), ALIGN), (dict(dbias=P + 2), ALIGN),
     (dict(ws=0), INVALID), (dict(ws=P + 8), ALIGN), (dict(bytes=100 * 40 * 2 - 1), INVALID), (dict(M=1 << 30), SHAPE),
-    (dict(N=1 << 23, lddd=1 << 23, ldz=1 << 23), SHAPE), (dict(K=1 << 23, lda=1 << 23, ldb=1 << 23), SHAPE),
-    (dict(M=(1 << 30) - 1, N=4096, lddd=4096, ldz=4096), SHAPE)])
+    (dict(M=1 << 29), SHAPE), (dict(N=1 << 23, lddd=1 << 23, ldz=1 << 23), SHAPE), (dict(K=1 << 23, lda=1 << 23, ldb=1 << 23), SHAPE),
+    (dict(M=(1 << 29) - 1, N=8192, lddd=8192, ldz=8192), SHAPE), (dict(M=(1 << 28), N=16384, lddd=16384, ldz=16384), SHAPE)])
 def test_act_backward_refusals(kw, status):
     assert _call("gemm_bf16_act_backward", BWD, BWD_OK, **kw) == status
 

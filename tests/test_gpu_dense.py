@@ -325,6 +325,8 @@ def test_empty_and_zero_k():
     want, err, _, _ = dense.act_forward(np.zeros((70, 300)), np.zeros((70, 300)), 0, _f64(bias), "silu", _f64(R))
     _near(D, want, err, "K = 0")
     assert torch.equal(Z, bias.expand(70, 300))
+    few = bsg.gemm_bf16_act(e(5, 0), e(300, 0), bias=bias, act="silu", residual=R[:5])
+    assert torch.equal(few, D[:5])
     assert torch.all(bsg.gemm_bf16_glu(e(70, 0), e(64, 0)) == 0)
     assert bsg.gemm_bf16_glu(e(0, 64), e(16, 64)).shape == (0, 8)
     assert bsg.gemm_bf16_glu(e(3, 64), e(0, 64)).shape == (3, 0)
@@ -358,6 +360,17 @@ def test_nan_and_infinity_stay_in_their_rows():
         assert torch.equal(got[keep], want[keep])
         for act in ACTS:
             assert torch.all(torch.isnan(bsg.gemm_bf16_act(A2, B, act=act)[3])), act
+        # an infinite z of either sign: f's limit above, below 0 (relu) or, as the formulas
+        # have it, -inf times 0
+        A2 = A.clone()
+        A2[3, 0] = float("inf")
+        up = B[:, 0] > 0
+        for act in ACTS:
+            got = bsg.gemm_bf16_act(A2, B, act=act)[3]
+            assert torch.all(got[up] == float("inf")), act
+            low = got[B[:, 0] < 0]
+            assert torch.all(low == (0.0 if act == "relu" else -float("inf"))) if act in ("none", "relu") \
+                else torch.all(torch.isnan(low)), act
         # gradients: a NaN row of dD reaches its row of dA, all of dB; rows past the end none
         dD, Z = _mat(g, M, N), _mat(g, M, N)
         want = bsg.gemm_bf16_act_backward(dD, A, B, Z, act="silu")[0]
