@@ -40,20 +40,25 @@ struct TileCost {
   int64_t bm, bn, lo_tiles, cap;   // tile, tiles up to which `lo` holds, tiles of a full round
   double lo, hi, fixed;
   int round;                       // stages of a round of the ring; 0: no parts
+  double fixed_part;               // a part's epilogue only stores its sums
 };
 static const TileCost kForms[3][3] = {
-    {{DENSE_BIG, 256, 256, 128, 256, 0.50, 0.60, 8.0, 0},
-     {DENSE_SMALL, 128, 128, 256, 512, 0.33, 0.55, 5.5, 0},
-     {DENSE_DEEP, 128, 128, 128, 256, 0.20, 0.26, 7.0, 8}},
-    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.58, 8.0, 0}, {DENSE_SMALL, 128, 256, 128, 256, 0.38, 0.43, 5.5, 6}, {}},
-    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.60, 8.0, 0}, {DENSE_SMALL, 128, 128, 256, 512, 0.49, 0.59, 5.5, 4}, {}}};
+    {{DENSE_BIG, 256, 256, 128, 256, 0.50, 0.60, 8.0, 0, 0},
+     {DENSE_SMALL, 128, 128, 256, 512, 0.33, 0.55, 5.5, 0, 0},
+     {DENSE_DEEP, 128, 128, 128, 256, 0.20, 0.26, 7.0, 8, 4.6}},
+    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.58, 9.0, 0, 0},
+     {DENSE_SMALL, 128, 256, 128, 256, 0.38, 0.43, 10.5, 6, 6.0},
+     {}},
+    {{DENSE_BIG, 256, 256, 128, 256, 0.55, 0.60, 9.0, 0, 0},
+     {DENSE_SMALL, 128, 128, 256, 512, 0.49, 0.59, 9.5, 4, 5.5},
+     {}}};
 
-static double tiles_cost(const TileCost& c, int64_t tiles, int64_t stages) {
+static double tiles_cost(const TileCost& c, int64_t tiles, int64_t stages, double fixed) {
   const int64_t full = tiles / c.cap, rest = tiles % c.cap;
-  double t = full * (stages * c.hi + c.fixed);
+  double t = full * (stages * c.hi + fixed);
   if (rest) {
     const double x = rest <= c.lo_tiles ? 0.0 : (double)(rest - c.lo_tiles) / (c.cap - c.lo_tiles);
-    t += stages * (c.lo + x * (c.hi - c.lo)) + c.fixed;
+    t += stages * (c.lo + x * (c.hi - c.lo)) + fixed;
   }
   return t;
 }
@@ -71,16 +76,18 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
   for (const TileCost& c : kForms[kind]) {
     if (!c.bm) continue;
     const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
-    const double t1 = tiles_cost(c, tiles, stages);
+    const double t1 = tiles_cost(c, tiles, stages, c.fixed);
     if (t1 < t_best) {
       t_best = t1;
       best = {c.form, 1};
     }
-    // parts of at least 8 stages, all of them in one round
-    for (int64_t s = 2; c.round && s <= 16 && s * tiles <= c.cap && 8 * s <= stages; ++s) {
+    // Parts of whole rounds of the ring, all of them on the GPU at once.  (One part: the
+    // epilogue moves to the join, whose threads are many; FP8 and FP4 tiles of few, tall
+    // waves gain by it at small K: FP8 472 x 728 x 896 16.0 us in one kernel, 12.9 apart.)
+    for (int64_t s = kind == KIND_BF16 ? 2 : 1; c.round && s <= 16 && s * tiles <= c.cap && c.round * (s - 1) < stages; ++s) {
       const int64_t per = ((stages + s - 1) / s + c.round - 1) / c.round * c.round;
       if ((stages + per - 1) / per != s) continue;
-      const double t = tiles_cost(c, s * tiles, per) + 3.0 + (8.0 * s + 2.0) * M * N / 5.5e6;
+      const double t = tiles_cost(c, s * tiles, per, c.fixed_part) + 3.0 + 0.2 * s + (8.0 * s + 2.0) * M * N / 5.5e6;
       if (t < t_best) {
         t_best = t;
         best = {DENSE_PART, (int)s};

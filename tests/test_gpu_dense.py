@@ -57,7 +57,7 @@ def _z(A, B):
 # tail, tiles of every form (parts of the contraction, 128-row tiles, 256-row tiles)
 SIZES = [(1, 1, 8), (1, 129, 2048), (2, 7168, 520), (5, 3, 40), (16, 520, 4096), (17, 100, 1032), (33, 65, 264),
          (64, 2048, 1024), (20, 6200, 264), (32, 7168, 128), (45, 6151, 72), (64, 7168, 2048), (130, 257, 1000), (200, 1001, 2056), (1001, 1003, 520), (2048, 1920, 96),
-         (3900, 3400, 136), (3841, 3457, 328)]
+         (2050, 2400, 1032), (3900, 3400, 136), (3841, 3457, 328)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -139,7 +139,7 @@ def _scaled(fmt, M, N, K, seed, gran=128):
 @pytest.mark.parametrize("fmt,M,N,K", [
     ("fp8", 1, 7168, 256), ("fp8", 3, 40, 128), ("fp8", 30, 6160, 384), ("fp8", 64, 7168, 2048), ("fp8", 50, 6147, 128),
     ("fp4", 25, 6145, 288), ("fp4", 64, 6400, 512), ("fp4", 40, 1000, 2080), ("fp8", 20, 515, 1152), ("fp8", 64, 520, 2048), ("fp8", 130, 257, 896),
-    ("fp8", 300, 1000, 1152), ("fp8", 3900, 3400, 128), ("fp8", 3841, 3457, 384),
+    ("fp8", 300, 1000, 1152), ("fp8", 1900, 3000, 1152), ("fp4", 1900, 3000, 1056), ("fp8", 3900, 3400, 128), ("fp8", 3841, 3457, 384),
     ("fp4", 1, 1024, 96), ("fp4", 8, 40, 32), ("fp4", 8, 512, 7168), ("fp4", 130, 257, 1056),
     ("fp4", 1000, 515, 544), ("fp4", 3900, 3400, 160), ("fp4", 3841, 3457, 96)])
 def test_act_scaled(fmt, M, N, K):
@@ -170,7 +170,7 @@ def _minus3(packed):
 
 
 GLU = [(1, 8, 8), (1, 2048, 512), (3, 40, 264), (5, 3080, 72), (20, 3200, 136), (30, 72, 264), (50, 3144, 264),
-       (64, 248, 1024), (33, 1000, 4096), (32, 1024, 1024), (48, 200, 2048), (130, 264, 1000), (777, 1000, 264),
+       (64, 248, 1024), (33, 1000, 4096), (700, 1000, 1032), (2050, 1200, 1032), (32, 1024, 1024), (48, 200, 2048), (130, 264, 1000), (777, 1000, 264),
        (2000, 2040, 72), (3841, 1800, 200), (4100, 3000, 40)]
 
 
@@ -211,7 +211,7 @@ def test_glu_strides(M, inter, K):
 
 
 BWD = [(1, 1, 8), (1, 300, 2048), (3, 5, 40), (64, 7, 264), (40, 2048, 1024), (130, 257, 1000), (1001, 1003, 520),
-       (600, 128, 3400), (3900, 131, 3400), (3900, 3401, 136), (97, 3457, 3841 // 8 * 8)]
+       (600, 128, 3400), (2050, 1032, 2400), (3900, 131, 3400), (3900, 3401, 136), (97, 3457, 3841 // 8 * 8)]
 
 
 @pytest.mark.parametrize("M,N,K", BWD)
