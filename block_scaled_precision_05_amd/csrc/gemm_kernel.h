@@ -86,7 +86,7 @@ struct GemmArgs {
   int32_t d_vec;            // widest D store: 2 = 16 bytes (D and ldd*2 16-aligned), 1 = 8, 0 = 2
   int32_t cap;              // grouped: 0 = contiguous experts, rows [offsets[g], offsets[g+1]);
                             // > 0 = masked layout, rows [g*cap, g*cap + min(offsets[g], cap))
-  // SwiGLU epilogue (up-projection of an FFN, EPI > 0): B holds [gate; up] rows of
+  // SwiGLU epilogue (up-projection of an FFN, EPI 1 + rule): B holds [gate; up] rows of
   // each expert, gate in rows [0, inter), up in [inter, 2*inter); a tile of BN B
   // rows takes BN/2 gate and the matching BN/2 up rows; instead of D the tile writes
   // Y = fp8(silu(gate) * up) [M][ldy bytes] and its 1x128 UE8M0 scales, packed int16

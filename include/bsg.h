@@ -15,7 +15,9 @@
  * the MQA logits of a lightning-indexer step in FP8 and FP4.  Around the grouped
  * products it sorts tokens by expert (or adapter), dispatches their rows, combines
  * the experts' rows with the router's weights, gives the gradient of that, and adds
- * low-rank adapters to a shared projection.
+ * low-rank adapters to a shared projection.  Dense products also come with bias,
+ * activation and residual in their epilogues and as the gated half of a feed-forward
+ * block, with the gradients of the BF16 ones.
  *
  * The pages this follows list BF16, FP8 and FP4 dense GEMM plus grouped (MoE)
  * GEMM as the library's coverage ("DeepGEMM-Ascend cobre quantas operacoes no
