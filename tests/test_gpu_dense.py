@@ -490,3 +490,92 @@ def test_same_bits_on_every_run():
         for _ in range(3):
             again = (bsg.gemm_bf16_act(A, B, act="gelu"),) + bsg.gemm_bf16_act_backward(dD, A, B, Z, act="gelu")
             assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_offsets_past_32_bits():
+    """Operands and outputs of more than 2^31 elements and 2^32 bytes: the last rows and
+    columns, and sums over all rows."""
+    M, N, K = 270_000, 8_200, 64
+    _say(f"outputs of {M} x {N}")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    A, B = _mat(g, M, K), _mat(g, N, K, by=K ** -0.5)
+    rows = torch.tensor([0, 131_071, 261_900, M - 1], device=DEV)     # the last two past 2^31 elements
+    Z = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    D = bsg.gemm_bf16_act(A, B, act="silu", preact=Z)
+    z, mag = _z(A[rows], B)
+    want, err, wz, ez = dense.act_forward(z, mag, K, None, "silu", None)
+    _near(D[rows], want, err, "D")
+    _near(Z[rows], wz, ez, "Z")
+    dA, dB, db = bsg.gemm_bf16_act_backward(D, A, B, Z, act="silu")
+    d, zz = _f64(D[rows]), _f64(Z[rows])
+    (w, e), _, _ = dense.act_backward(d, zz, _f64(A[rows]), _f64(B), "silu")
+    _near(dA[rows], w, e, "dA")
+    for c in (0, 8_191, N - 1):
+        _, (w, e), (wb, eb) = dense.act_backward(_f64(D[:, c:c + 1]), _f64(Z[:, c:c + 1]), _f64(A), _f64(B[c:c + 1]), "silu")
+        _near(dB[c:c + 1], w, e, f"dB row {c}")
+        _near(db[c:c + 1], wb, eb + dense.U * np.abs(wb), f"dbias {c}", rounded=False)
+    del D, Z, dA, dB
+    H = bsg.gemm_bf16_glu(A, B[:8192])
+    z, mag = _z(A[rows], B[:8192])
+    want, err, _, _ = dense.glu_forward(z, mag, K)
+    _near(H[rows], want, err, "H")
+    del H
+    # few rows of A against more than 4 GiB of B
+    N, K = 300_000, 8_192
+    _say(f"few rows against {N} x {K}")
+    B = torch.empty(N, K, dtype=torch.bfloat16, device=DEV).normal_(0, K ** -0.5, generator=g)
+    cols = torch.tensor([0, 262_143, 262_144, N - 1], device=DEV)
+    for M in (2, 40, 70):
+        A = _mat(g, M, K)
+        D = bsg.gemm_bf16_act(A, B, act="relu")
+        z, mag = _z(A, B[cols])
+        want, err, _, _ = dense.act_forward(z, mag, K, None, "relu", None)
+        _near(D[:, cols], want, err, f"{M} rows")
+    H = bsg.gemm_bf16_glu(A[:3], B)
+    i = N // 2
+    pick = torch.tensor([0, i - 1], device=DEV)
+    z, mag = _z(A[:3], B[torch.cat([pick, i + pick])])
+    want, err, _, _ = dense.glu_forward(z, mag, K)
+    _near(H[:, pick], want, err, "gated, few rows")
+
+
+def test_binding_raises():
+    """What the binding refuses, on tensors of the GPU; nothing is written."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    A, B, dD = _mat(g, 40, 64), _mat(g, 24, 64), _mat(g, 40, 24)
+    bad = [
+        (TypeError, lambda: bsg.gemm_bf16_act(A.float(), B)), (ValueError, lambda: bsg.gemm_bf16_act(A, B[:, :56])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, act="swish")), (ValueError, lambda: bsg.gemm_bf16_act(A, B, act=None)),
+        (TypeError, lambda: bsg.gemm_bf16_act(A, B, bias=dD[0].float())),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, bias=dD[0, :8])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, residual=dD[:8])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, out=dD[:, :16])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, preact=dD[:8])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, residual=dD.cpu())),
+        (ValueError, lambda: bsg.gemm_bf16_act(A.t(), B)),
+        (bsg.BsgError, lambda: bsg.gemm_bf16_act(A[:, :60], B[:, :60])),
+        (bsg.BsgError, lambda: bsg.gemm_bf16_act(A[:, 4:60], B[:, :56])),
+        (bsg.BsgError, lambda: bsg.gemm_bf16_act(A[:1].expand(40, 64), B)),
+        (bsg.BsgError, lambda: bsg.gemm_bf16_act(A, B, residual=dD[:1].expand(40, 24))),
+        (ValueError, lambda: bsg.gemm_bf16_act_backward(dD, A, B, act="silu")),
+        (ValueError, lambda: bsg.gemm_bf16_act_backward(dD[:8], A, B)),
+        (bsg.BsgError, lambda: bsg.gemm_bf16_act_backward(dD, A, B, workspace=A[0])),
+        (ValueError, lambda: bsg.gemm_bf16_glu(A, B[:23])), (bsg.BsgError, lambda: bsg.gemm_bf16_glu(A, B[:20])),
+        (ValueError, lambda: bsg.gemm_bf16_glu_backward(dD[:, :12], A, B, dD[:, :16])),
+        (ValueError, lambda: bsg.gemm_bf16_act(A, B, workspace=torch.zeros(64, 64, device=DEV).t()[:, :8])),
+    ]
+    for i, (kind, call) in enumerate(bad):
+        with pytest.raises(kind):
+            call()
+            pytest.fail(f"case {i} was taken")
+    codes = torch.zeros(40, 256, dtype=torch.uint8, device=DEV)
+    sf = torch.zeros(1, 40, dtype=torch.int16, device=DEV)
+    for kind, call in ((TypeError, lambda: bsg.gemm_fp8_act(codes, sf.float(), codes, sf)),
+                       (ValueError, lambda: bsg.gemm_fp8_act(codes, sf[:, :39], codes, sf)),
+                       (ValueError, lambda: bsg.gemm_fp8_act(codes, sf, codes[:, :128], sf)),
+                       (bsg.BsgError, lambda: bsg.gemm_fp8_act(codes, sf, codes, sf, sfb_gran_mn=64)),
+                       (ValueError, lambda: bsg.gemm_fp4_act(codes, sf, codes, sf)),
+                       (ValueError, lambda: bsg.gemm_fp4_act(codes, sf, codes, sf, K=1024))):
+        with pytest.raises(kind):
+            call()
+    torch.cuda.synchronize()
