@@ -21,7 +21,7 @@ PROBE_SOURCES = [os.path.join(HERE, "csrc", "probe.hip")]
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")
 HEADERS = [os.path.join(HERE, "csrc", h) for h in ("gemm_kernel.h", "gemm_launch.h", "configs.h",
-                                                       "internal.h", "quant_math.h", "act_math.h")] + \
+                                                       "internal.h", "quant_math.h", "act_math.h", "scale_record.h")] + \
     [os.path.join(ROOT, "include", "bsg.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -93,10 +93,8 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
   const int put = (lane & ~3) | ((lane & 3) ^ ((lane >> 4) & 3)), get = 4 * r16 + (lg ^ (r16 >> 2));
 
   // scale bytes: packed word of (K-block pair, row), the block's byte of it
-  const __amdgpu_buffer_rsrc_t rsa =
-      make_rsrc(args.sfa, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfa + args.M)));
-  const __amdgpu_buffer_rsrc_t rsb =
-      make_rsrc(args.sfb, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfb + args.sfb_rows)));
+  const __amdgpu_buffer_rsrc_t rsa = make_rsrc(args.sfa, scale_record(args.kp_count, args.ld_sfa, args.M));
+  const __amdgpu_buffer_rsrc_t rsb = make_rsrc(args.sfb, scale_record(args.kp_count, args.ld_sfb, args.sfb_rows));
   const bool b_row = KIND == KIND_FP4 || args.sfb_rows == args.N;
   const int kblocks = KIND == KIND_FP8 ? args.k_bytes / 128 : args.k_bytes / 16;
   auto scale = [&](const __amdgpu_buffer_rsrc_t& rs, int64_t ld, int row, int kb) {
@@ -195,7 +193,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
     __builtin_amdgcn_wave_barrier();
   };
   Batch t0, t1;
-  load(t0, wave);
+  if (wave < steps) load(t0, wave);
   for (int s = wave; s < steps; s += 2 * W * UN) {
     load(t1, s + W * UN);
     __builtin_amdgcn_sched_barrier(0);

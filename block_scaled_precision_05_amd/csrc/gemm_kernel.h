@@ -45,6 +45,7 @@
 
 #include "act_math.h"
 #include "quant_math.h"
+#include "scale_record.h"
 #include <utility>
 
 namespace bsg {
@@ -974,10 +975,8 @@ void gemm_kernel(const GemmArgs args) {
       constexpr bool SV_B = T::WIDE && T::PERM_B;
       const int a_rows = T::WIDE ? (args.M + 3) & ~3 : args.M;
       const int b_rows = SV_B ? (args.sfb_rows + 3) & ~3 : args.sfb_rows;
-      const __amdgpu_buffer_rsrc_t rsa = make_rsrc(
-          args.sfa, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfa + a_rows)));
-      const __amdgpu_buffer_rsrc_t rsb = make_rsrc(
-          sfb, (uint32_t)(2 * ((int64_t)(args.kp_count - 1) * args.ld_sfb + b_rows)));
+      const __amdgpu_buffer_rsrc_t rsa = make_rsrc(args.sfa, scale_record(args.kp_count, args.ld_sfa, a_rows));
+      const __amdgpu_buffer_rsrc_t rsb = make_rsrc(sfb, scale_record(args.kp_count, args.ld_sfb, b_rows));
       // (FP4: the lane's fragment rows are 4*l32 .. 4*l32 + 3 of the wave block)
       // (FP4: lane group lg reads packed rows (NC/4)*lg further on)
       const uint32_t ld_a = (uint32_t)args.ld_sfa, ld_b = (uint32_t)args.ld_sfb;

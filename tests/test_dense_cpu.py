@@ -3,6 +3,9 @@ refuse, before any HIP call (no GPU needed: pointers are numbers here), their wo
 and pins of the fp64 forms in oracle/dense.py."""
 import ctypes
 import math
+import os
+import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -243,3 +246,28 @@ def test_bounds_hold_for_an_fp32_evaluation():
         x = z32 / (1 + np.exp(-z32)) if a == "silu" else \
             np.float32(0.5) * z32 * (1 + np.tanh(np.float32(dense.C) * (z32 + np.float32(dense.A3) * z32 ** 3)))
         assert np.all(np.abs(x - d) <= e + 2.0 ** -24 * np.abs(z))
+
+
+# ---- records of the packed scales ----------------------------------------------------------
+
+def test_scale_record_is_empty_without_k_blocks(tmp_path):
+    """With K == 0 the scale pointers may be null, and the kernels issue scale loads ahead of
+    their stage loops all the same: the record must be empty for any leading dimension and
+    any number of rows.  Otherwise it ends with the last row's last word."""
+    csrc = os.path.join(os.path.dirname(bsg.__file__), "csrc")
+    src, so = tmp_path / "rec.cpp", tmp_path / "rec.so"
+    src.write_text('#include "scale_record.h"\n'
+                   'extern "C" uint32_t rec(int32_t kp, int64_t ld, int32_t rows) { return bsg::scale_record(kp, ld, rows); }\n')
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I" + csrc, str(src), "-o", str(so)], check=True)
+    rec = ctypes.CDLL(str(so)).rec
+    rec.argtypes, rec.restype = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32], ctypes.c_uint32
+    for ld in (0, 1, 4, 64, 1 << 29):
+        for rows in (1, 3, 64, 4096, (1 << 31) - 256):
+            assert rec(0, ld, rows) == 0
+    for kp, ld, rows in ((1, 0, 5), (1, 40, 40), (3, 40, 37), (9, 1 << 20, 3), (2, (1 << 29) - 8, (1 << 29) - 8)):
+        assert rec(kp, ld, rows) == 2 * ((kp - 1) * ld + rows)
+    # both kernels take their records from there
+    for name in ("gemm_kernel.h", "dense_few.hip"):
+        text = open(os.path.join(csrc, name)).read()
+        made = re.findall(r"make_rsrc\(\s*(?:args\.)?(sfa|sfb),\s*(\w+)\(", text)
+        assert made == [("sfa", "scale_record"), ("sfb", "scale_record")], name

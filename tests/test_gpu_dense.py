@@ -579,3 +579,29 @@ def test_binding_raises():
         with pytest.raises(kind):
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [5, 64, 70, 300, 3900])
+def test_scaled_zero_k(M):
+    """K = 0 with scales: empty scale tensors (null pointers), and empty ones of wider rows.
+    D = R + f(bias) with epilogues, zeros without, in every form (few rows, small and large
+    tiles)."""
+    N = 3400 if M == 3900 else 300
+    g = torch.Generator(device=DEV).manual_seed(M)
+    bias, R = _mat(g, 1, N)[0], _mat(g, M, N)
+    want, err, _, _ = dense.act_forward(np.zeros((M, N)), np.zeros((M, N)), 0, _f64(bias), "gelu", _f64(R))
+    u8 = lambda rows: torch.empty(rows, 0, dtype=torch.uint8, device=DEV)
+    sf = lambda rows: torch.empty(0, rows, dtype=torch.int16, device=DEV)
+    for pad in (0, 8, 1000):
+        for fmt, gran in (("fp8", 128), ("fp8", 1), ("fp4", 1)):
+            _say(f"{fmt}, {M}x{N}x0, B scales per {gran}, {pad} more")
+            sfa, sfb = sf(M + pad), sf((N + gran - 1) // gran + pad)
+            if fmt == "fp8":
+                D = bsg.gemm_fp8_act(u8(M), sfa, u8(N), sfb, bias=bias, act="gelu", residual=R, sfb_gran_mn=gran)
+                plain = bsg.gemm_fp8_blockscaled(u8(M), sfa, u8(N), sfb, sfb_gran_mn=gran)
+            else:
+                D = bsg.gemm_fp4_act(u8(M), sfa, u8(N), sfb, bias=bias, act="gelu", residual=R)
+                plain = bsg.gemm_fp4_blockscaled(u8(M), sfa, u8(N), sfb)
+            _near(D, want, err, fmt)
+            assert torch.all(plain == 0)
+            torch.cuda.synchronize()
