@@ -197,7 +197,10 @@ __global__ __launch_bounds__(256) void dz_kernel(const uint16_t* __restrict__ dD
           float f;
           if constexpr (GLU) {
             const float df = act_df<A>(z[e], f);
-            z[e] = d[e] * w[e] * df;
+            if constexpr (A == BSG_ACT_RELU)
+              z[e] = z[e] <= 0.0f ? 0.0f : d[e] * w[e];   // (a select, as below)
+            else
+              z[e] = d[e] * w[e] * df;
             w[e] = d[e] * f;
           } else if constexpr (A == BSG_ACT_NONE) {
             z[e] = d[e];

@@ -605,3 +605,36 @@ def test_scaled_zero_k(M):
             _near(D, want, err, fmt)
             assert torch.all(plain == 0)
             torch.cuda.synchronize()
+
+
+def test_gated_relu_gradient_where_the_gate_is_shut():
+    """dg = dH u f'(g) is 0 wherever g <= 0 under ReLU, whatever dH and u hold (infinite, NaN,
+    or a product past fp32's range), as it is in gemm_bf16_act_backward and in autograd;
+    du = dH f(g) meets f(g) = 0 and is NaN only for an infinite or NaN dH."""
+    inf, nan = float("inf"), float("nan")
+    for M, inter, K in ((5, 16, 24), (300, 520, 72)):
+        _say(f"gemm_bf16_glu_backward {M}x{inter}x{K} relu")
+        g = torch.Generator(device=DEV).manual_seed(M)
+        X, W, dH, Z = _mat(g, M, K), _mat(g, 2 * inter, K), _mat(g, M, inter), _mat(g, M, 2 * inter)
+        Z[3, :6] = torch.tensor([-1.0, 0.0, -0.0, -2.0, -inf, -3.0]).to(torch.bfloat16)
+        at = slice(inter, inter + 6)
+        # u infinite or NaN, and dH u past the range: all gradients as for u = 1
+        Z[3, at] = 1.0
+        want = bsg.gemm_bf16_glu_backward(dH, X, W, Z, act="relu")
+        Z2 = Z.clone()
+        Z2[3, at] = torch.tensor([inf, -inf, nan, 3e38, inf, -3e38]).to(torch.bfloat16)
+        got = bsg.gemm_bf16_glu_backward(dH, X, W, Z2, act="relu")
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        dH2 = dH.clone()
+        dH2[3, 3] = 3e38
+        Z2[3, inter + 3] = -3e38
+        got = bsg.gemm_bf16_glu_backward(dH2, X, W, Z2, act="relu")
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # dH infinite: dg stays 0, so the gate's rows of dW13 keep their values
+        dH2[3, 1] = inf
+        dX, dW = bsg.gemm_bf16_glu_backward(dH2, X, W, Z2, act="relu")
+        assert torch.equal(dW[:inter], want[1][:inter])
+        keep = torch.arange(inter, device=DEV) != 1
+        assert torch.equal(dW[inter:][keep], want[1][inter:][keep]) and torch.all(torch.isnan(dW[inter + 1]))
+        rest = torch.arange(M, device=DEV) != 3
+        assert torch.equal(dX[rest], want[0][rest]) and torch.all(torch.isnan(dX[3]))
