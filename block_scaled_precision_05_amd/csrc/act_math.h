@@ -6,7 +6,8 @@
 // Everything is formed in fp32 from fp32 sums and rounded to bf16 once at the store.  The
 // exponential is the hardware's (v_exp_f32 of x log2 e), the reciprocal v_rcp_f32: a few
 // 2^-23 relative, plus |x| 2^-24 from the rounded exponent, far below the 2^-9 of the bf16
-// store and, for the fp32 sums of the bias gradient, averaged over the rows.
+// store and, for the fp32 sums of the bias gradient, averaged over the rows.  What sinks
+// below the exponential's range is lost: at most 2^-120 of a result.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -86,7 +87,12 @@ __device__ __forceinline__ void store_bf16s(uint16_t* p, const float (&x)[V], bo
 // e^x through the hardware's 2^x; inf and 0 past the range.
 __device__ __forceinline__ float exp_f32(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+// 1 / (1 + e^-x).  v_rcp_f32 gives 0 for a result below 2^-126 (x < -87.3), the multiply
+// keeps it: the reciprocal is taken of 2^-8 (1 + e^-x).  0 from x = -88.7 on, where e^-x
+// overflows (the value is below 2^-128).
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return 0x1p-8f * __builtin_amdgcn_rcpf(__builtin_fmaf(exp_f32(-x), 0x1p-8f, 0x1p-8f));
+}
 
 // The normal distribution's upper tail Q(x) = erfc(x / sqrt 2) / 2 for x >= 0, and
 // e^(-x^2/2) beside it.  Q(x) = e^(-x^2/2) t P(t) with t = 1 / (1 + 0.3 x): P, of degree 7,

@@ -17,7 +17,7 @@ The leading product itself has 8 bits and loses nothing, so a group of products 
 than 7 * 2^-13 max |p|, and a row at most CUT = 7 * 2^-13 times the sum of the magnitudes.
 (e2m1 products are multiples of 1/4 up to 36, 8 bits: nothing is cut.)"""
 import numpy as np
-from scipy.special import erfc
+from scipy.special import erfc, expit
 
 U, U8 = 2.0 ** -24, 2.0 ** -8
 CUT = 7 * 2.0 ** -13
@@ -28,11 +28,11 @@ def f(z, act):
     if act == "relu":
         return np.maximum(z, 0.0)
     if act == "silu":
-        return z / (1 + np.exp(-z))
+        return z * expit(z)
     if act == "gelu":
         return 0.5 * z * erfc(-z * np.sqrt(0.5))
     if act == "gelu_tanh":
-        return 0.5 * z * (1 + np.tanh(C * (z + A3 * z ** 3)))
+        return z * expit(2 * C * (z + A3 * z ** 3))      # (1 + tanh(u) = 2 / (1 + e^-2u), which cancels nothing)
     return z
 
 
@@ -42,13 +42,13 @@ def df(z, act):
         d = (z > 0).astype(np.float64)
         return d, d
     if act == "silu":
-        s = 1 / (1 + np.exp(-z))
+        s = expit(z)
         return s + z * s * (1 - s), s + np.abs(z) * s * (1 - s)
     if act == "gelu":
         p, q = 0.5 * erfc(-z * np.sqrt(0.5)), z * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
         return p + q, p + np.abs(q)
     if act == "gelu_tanh":
-        s = 0.5 * (1 + np.tanh(C * (z + A3 * z ** 3)))
+        s = expit(2 * C * (z + A3 * z ** 3))
         q = z * s * (1 - s) * 2 * C * (1 + 3 * A3 * z * z)
         return s + q, s + np.abs(q)
     return np.ones_like(z), np.ones_like(z)

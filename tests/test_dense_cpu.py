@@ -271,3 +271,14 @@ def test_scale_record_is_empty_without_k_blocks(tmp_path):
         text = open(os.path.join(csrc, name)).read()
         made = re.findall(r"make_rsrc\(\s*(?:args\.)?(sfa|sfb),\s*(\w+)\(", text)
         assert made == [("sfa", "scale_record"), ("sfb", "scale_record")], name
+
+
+def test_forms_keep_their_tails():
+    """Far below zero f and f' keep their digits: silu(z) = z e^z and its derivative
+    (1 + z) e^z up to e^2z, gelu_tanh(z) = z e^2u, u = sqrt(2/pi) (z + 0.044715 z^3)."""
+    z = np.array([-40.0, -87.5, -96.0])
+    assert np.allclose(dense.f(z, "silu"), z * np.exp(z), rtol=1e-13, atol=0)
+    assert np.allclose(dense.df(z, "silu")[0], (1 + z) * np.exp(z), rtol=1e-13, atol=0)
+    z = np.array([-7.0, -9.0, -10.5])
+    u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    assert np.allclose(dense.f(z, "gelu_tanh"), z * np.exp(2 * u), rtol=1e-12, atol=0)

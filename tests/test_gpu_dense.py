@@ -638,3 +638,34 @@ def test_gated_relu_gradient_where_the_gate_is_shut():
         assert torch.equal(dW[inter:][keep], want[1][inter:][keep]) and torch.all(torch.isnan(dW[inter + 1]))
         rest = torch.arange(M, device=DEV) != 3
         assert torch.equal(dX[rest], want[0][rest]) and torch.all(torch.isnan(dX[3]))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_at_the_end_of_their_tails(act):
+    """f and f' where they sink below the smallest normal number, z exact (one product by 1):
+    off by the evaluation, the store's rounding and at most 2^-120, in every form."""
+    z = torch.cat([torch.arange(-96, -80, 0.5), torch.arange(-15, -9, 1 / 16), torch.arange(-6, 6, 0.25)])
+    z = torch.cat([z, z.new_zeros(-len(z) % 8)]).to(torch.bfloat16).to(DEV)
+    zd = _f64(z)
+    f = dense.f(zd, act)
+    d, terms = dense.df(zd, act)
+    ev = dense._eval(zd, act)
+    def near(got, want, tol):
+        over = np.abs(got - want) - tol
+        assert np.max(over) <= 0, f"{np.max(over):.2e} over at z = {zd[np.argmax(over) % len(zd)]}"
+    one = lambda M: torch.eye(1, 8, dtype=torch.bfloat16, device=DEV).expand(M, 8).contiguous()
+    tol = U8 * np.abs(f) + 2 * ev * np.abs(f) + 2.0 ** -120
+    for M, copies in ((1, 1), (70, 1), (3900, 3400 // len(z) + 1)):
+        zz = z.repeat(copies)
+        B = torch.zeros(len(zz), 8, dtype=torch.bfloat16, device=DEV)
+        B[:, 0] = zz
+        _say(f"{act} {M}x{len(zz)}")
+        got = _f64(bsg.gemm_bf16_act(one(M), B, act=act)).reshape(M, copies, len(z))
+        near(got, f, tol)
+        up = torch.zeros_like(B)
+        up[:, 0] = 1
+        got = _f64(bsg.gemm_bf16_glu(one(M), torch.cat([B, up]), act=act)).reshape(M, copies, len(z))
+        near(got, f, tol)
+    db = _f64(bsg.gemm_bf16_act_backward(torch.ones(1, len(z), dtype=torch.bfloat16, device=DEV), one(1), B[:len(z)], z[None],
+                                         act=act, need=(False, False, True))[2])
+    near(db, d, 2 * ev * terms + 2 * dense.U * np.abs(d) + 2.0 ** -120)
