@@ -669,3 +669,128 @@ def test_activations_at_the_end_of_their_tails(act):
     db = _f64(bsg.gemm_bf16_act_backward(torch.ones(1, len(z), dtype=torch.bfloat16, device=DEV), one(1), B[:len(z)], z[None],
                                          act=act, need=(False, False, True))[2])
     near(db, d, 2 * ev * terms + 2 * dense.U * np.abs(d) + 2.0 ** -120)
+
+
+SCALED = [("fp8", 128), ("fp8", 1), ("fp4", 1)]
+# few rows, parts of the contraction (FP8, FP4), small tiles, large tiles
+SCALED_SIZES = [(40, 200, 1152), (300, 515, 1152), (1900, 3000, 384), (3900, 3400, 128)]
+
+
+def _scaled_call(fmt, gran):
+    if fmt == "fp8":
+        return lambda A, sfa, B, sfb, **kw: bsg.gemm_fp8_act(A, sfa, B, sfb, sfb_gran_mn=gran, **kw)
+    return bsg.gemm_fp4_act
+
+
+def _inside(t, lead, more, fill):
+    """t's values inside a larger buffer of `fill`: two rows more, each `more` elements longer,
+    t starting `lead` elements into the first."""
+    buf = torch.full((t.shape[0] + 2, t.shape[1] + more), fill, dtype=t.dtype, device=DEV)
+    buf[:t.shape[0], lead:lead + t.shape[1]] = t
+    return buf[:t.shape[0], lead:lead + t.shape[1]]
+
+
+@pytest.mark.parametrize("fmt,gran", SCALED)
+@pytest.mark.parametrize("M,N,K", SCALED_SIZES)
+def test_act_scaled_strides(fmt, gran, M, N, K):
+    """Operands and scales cut out of buffers whose other bytes are NaN (FP4 codes: 6), bias,
+    residual and output at any element, added in place, with a workspace of NaN: the bits of
+    the plain call, nothing else written."""
+    _say(f"gemm_{fmt}_act {M}x{N}x{K}, B scales per {gran}")
+    fn = _scaled_call(fmt, gran)
+    (A, sfa, B, sfb), z, mag = _scaled(fmt, M, N, K, M + N + K, gran)
+    z, mag, sfa = z / 8, mag / 8, _minus3(sfa)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    bias, R = _mat(g, 1, N)[0], _mat(g, M, N)
+    want = fn(A, sfa, B, sfb, bias=bias, act="silu", residual=R)
+    w, e, _, _ = dense.act_forward(z, mag, K, _f64(bias), "silu", _f64(R), dense.CUT if fmt == "fp8" else 0.0)
+    _near(want, w, e, "silu, bias, residual")
+    code = 0x7F if fmt == "fp8" else 0x77
+    need = getattr(bsg.lib(), f"gemm_{fmt}_act_workspace")(M, N, K)
+    for (pad, shift), lead in zip(((8, 0), (1, 0), (4, 1), (0, 3)), (0, 4, 3, 1)):
+        a, b = _inside(A, 16, 48, code), _inside(B, 32, 32, code)
+        # (every second case: rows that take the 8-byte scale loads)
+        sa, sb = (_inside(s, lead, (4 if lead % 4 == 0 else 5) + lead + -s.shape[1] % 4, -1) for s in (sfa, sfb))
+        vb = _inside(bias[None], shift, 8, float("nan"))[0]
+        r = _inside(R, shift, pad + shift, float("nan"))
+        buf = torch.full((M * (N + pad) + shift,), 7.0, dtype=torch.bfloat16, device=DEV)
+        D = buf[shift:].view(M, N + pad)[:, :N]
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
+        assert fn(a, sa, b, sb, bias=vb, act="silu", residual=r, out=D, workspace=ws) is D
+        assert torch.equal(D, want)
+        assert torch.all(buf[:shift] == 7) and torch.all(buf[shift:].view(M, N + pad)[:, N:] == 7)
+        assert torch.all(ws[need:] == 255)
+        assert fn(a, sa, b, sb, bias=vb, act="silu", residual=r, out=r) is r
+        assert torch.equal(r, want)
+        outside = torch.as_strided(r, (M + 2, N + pad + shift), (N + pad + shift, 1), 0).clone()
+        outside[:M, shift:shift + N] = float("nan")
+        assert torch.all(torch.isnan(outside))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt,gran", SCALED)
+@pytest.mark.parametrize("M,N,K", SCALED_SIZES)
+def test_act_scaled_nan_and_infinity(fmt, gran, M, N, K):
+    """A NaN row of A, a NaN row of B (FP8: e4m3 has a NaN), a NaN bias and an infinite
+    residual touch their own outputs only."""
+    _say(f"gemm_{fmt}_act {M}x{N}x{K}, B scales per {gran}")
+    fn = _scaled_call(fmt, gran)
+    (A, sfa, B, sfb), _, _ = _scaled(fmt, M, N, K, M + N, gran)
+    sfa = _minus3(sfa)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    bias, R = _mat(g, 1, N)[0], _mat(g, M, N)
+    want = fn(A, sfa, B, sfb, bias=bias, act="gelu", residual=R)
+    bias2, R2, A2, B2 = bias.clone(), R.clone(), A.clone(), B.clone()
+    bias2[9], R2[5, 11] = float("nan"), float("inf")
+    nan = torch.zeros(M, N, dtype=torch.bool, device=DEV)
+    nan[:, 9] = True
+    if fmt == "fp8":
+        A2[3, 1], B2[7, K - 1] = 0x7F, 0xFF
+        A2[M - 1], B2[N - 1] = 0x7F, 0x7F
+        nan[3], nan[M - 1], nan[:, 7], nan[:, N - 1] = True, True, True, True
+    got = fn(A2, sfa, B2, sfb, bias=bias2, act="gelu", residual=R2)
+    assert got[5, 11] == float("inf")
+    assert torch.equal(torch.isnan(got), nan)
+    nan[5, 11] = True
+    assert torch.equal(got[~nan], want[~nan])
+
+
+def test_scaled_captured_and_on_streams():
+    """FP8 and FP4 calls captured together, replayed several times among eager work, and on
+    two streams at once: the bits of the eager call each time."""
+    cases = []
+    for i, (M, N, K) in enumerate(SCALED_SIZES):
+        for fmt, gran in SCALED:
+            (A, sfa, B, sfb), _, _ = _scaled(fmt, M, N, K, i, gran)
+            g = torch.Generator(device=DEV).manual_seed(i)
+            args = (A, _minus3(sfa), B, sfb)
+            kw = {"bias": _mat(g, 1, N)[0], "act": ACTS[i % 5], "residual": _mat(g, M, N)}
+            cases.append(lambda fn=_scaled_call(fmt, gran), args=args, kw=kw: fn(*args, **kw))
+    want = [c().clone() for c in cases]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cases[0]()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [c() for c in cases]
+    for k in range(4):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        eager = cases[k]()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[k]) and all(torch.equal(o, w) for o, w in zip(outs, want)), k
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    res = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i, c in enumerate(cases):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                res[j].append(cases[(i + j) % len(cases)]())
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, want[(i + j) % len(cases)]) for i, o in enumerate(res[j]))
