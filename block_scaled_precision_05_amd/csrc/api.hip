@@ -91,6 +91,8 @@ bool sv_ok(const int16_t* sf, int64_t ld) { return ((uintptr_t)sf % 8 == 0) && (
 // Byte strides must keep 256 rows of offsets inside 31 bits.
 static const int64_t kMaxRowBytes = (int64_t(1) << 31) / 256 - 1;
 static const int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Rows and columns of D, rounded up to whole 256-row tiles, must stay inside 31 bits.
+static const int64_t kMaxSize = (int64_t(1) << 31) - 256;
 
 // Shared checks of the dense entry points.  elem: bytes per stored element of A/B
 // (2 for bf16, 1 for e4m3, 1/2 for e2m1 expressed as k_bytes = K/2).
@@ -98,7 +100,7 @@ int check_dense(const void* A, int64_t lda, const void* B, int64_t ldb, const vo
                        int64_t ldd, int64_t M, int64_t N, int64_t K, int64_t kgran, int64_t k_bytes,
                        int64_t elem_bytes) {
   if (M < 0 || N < 0 || K < 0) return BSG_ERR_INVALID_ARG;
-  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMaxSize || N > kMaxSize || K > kMaxDim) return BSG_ERR_UNSUPPORTED_SHAPE;
   if (K % kgran) return BSG_ERR_UNSUPPORTED_SHAPE;
   if (M == 0 || N == 0) return BSG_OK;
   if (!D || ldd < N) return BSG_ERR_INVALID_ARG;

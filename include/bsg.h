@@ -55,7 +55,8 @@
  *    A, B nor the scales (their pointers may then be NULL).
  *  - A wrongly laid out scale array cannot be detected: it gives wrong numbers,
  *    not an error (the pages warn of exactly this failure mode).
- *  - Sizes: every leading dimension times 256 must stay below 2^31 bytes.  A
+ *  - Sizes: M and N of the GEMMs are at most 2^31 - 256; every leading dimension of
+ *    their operands times 256 must stay below 2^31 bytes.  A
  *    packed scale array of the GEMMs, kp packed rows of ld_sf int16, must keep
  *    2 (kp + 1) ld_sf below 2^31 bytes (the kernels address one packed row past
  *    the last on a K tail).  Larger shapes return BSG_ERR_UNSUPPORTED_SHAPE.
@@ -189,7 +190,7 @@ int m_grouped_gemm_fp4(const void* A, int64_t lda, const int16_t* sfa, int64_t l
  *     D[g*max_m + r][n] = bf16( sum_k a[g*max_m + r][k] * 2^(sa-127) * b_g[n][k] * 2^(sb_g-127) )
  * with B_g, sfb_g as in m_grouped_gemm_fp8.  Rows r >= m_g are not written.
  *   masked_m: DEVICE int32 [G] (read by the kernel; no host synchronisation).
- *   G == 0 or max_m == 0 is a no-op.  Requires G * max_m < 2^31 plus the
+ *   G == 0 or max_m == 0 is a no-op.  Requires G * max_m <= 2^31 - 256 plus the
  *   requirements of m_grouped_gemm_fp8 with M_total = G * max_m. */
 int m_grouped_gemm_fp8_masked(const void* A, int64_t lda, const int16_t* sfa, int64_t ld_sfa,
                               const void* B, int64_t ldb, int64_t stride_b,

@@ -282,3 +282,27 @@ def test_forms_keep_their_tails():
     z = np.array([-7.0, -9.0, -10.5])
     u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
     assert np.allclose(dense.f(z, "gelu_tanh"), z * np.exp(2 * u), rtol=1e-12, atol=0)
+
+
+@pytest.mark.parametrize("dim", ["M", "N"])
+@pytest.mark.parametrize("size", [(1 << 31) - 255, (1 << 31) - 128, (1 << 31) - 1])
+def test_sizes_that_a_tile_would_carry_past_31_bits(dim, size):
+    """Rounded up to whole 256-row tiles these sizes leave the kernels' 32-bit indexes: the
+    tile counts came out negative and nothing was computed."""
+    kw = {dim: size}
+    if dim == "N":
+        kw.update(ldd=size, ldr=size, ldz=size, M=1)
+    else:
+        kw.update(N=1)
+    assert _call("gemm_bf16_act", ACT, ACT_OK, **kw) == SHAPE
+    kw.pop("ldz", None)
+    assert _call("gemm_fp8_act", FP8, FP8_OK, K=0, **kw) == SHAPE
+    assert _call("gemm_fp4_act", FP4, FP4_OK, K=0, **kw) == SHAPE
+    M, N = (size, 1) if dim == "M" else (1, size)
+    L = bsg.lib()
+    assert L.gemm_bf16(P, 64, P, 64, P, N, M, N, 64, 0) == SHAPE
+    assert L.gemm_fp8_blockscaled(P, 128, P, M, 1, P, 128, P, N, 128, P, N, M, N, 0, 0) == SHAPE
+    assert L.gemm_fp4_blockscaled(P, 128, P, M, P, 128, P, N, P, N, M, N, 0, 0) == SHAPE
+    if dim == "M":
+        assert L.gemm_bf16_glu(P, 64, P, 64, 2, P, 8, 0, 0, M, 8, 64, P, 1 << 40, 0) == SHAPE
+        assert L.m_grouped_gemm_bf16(P, 64, P, 64, 64, P, N, P, 1, M, N, 64, 0) == SHAPE
