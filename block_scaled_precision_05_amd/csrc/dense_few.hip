@@ -3,9 +3,8 @@
 //
 // One workgroup of W waves owns 16 NF rows of B (16 NF columns of D; in the gated block 16
 // gate rows and their 16 up rows) and shares out the contraction: wave w takes the
-// 128-byte steps w, w + W, ... of every row.  A wave loads a batch of UN steps into
-// registers, four lanes to 64 consecutive bytes of a row, while the batch before it goes
-// through the wave's own LDS pieces into fragments and the matrix cores; no barrier until
+// 128-byte steps w, w + W, ... of every row.  A wave loads a step into registers, four
+// lanes to 64 consecutive bytes of a row, while the step before it goes through the wave's own LDS pieces into fragments and the matrix cores; no barrier until
 // the end.  (Loaded straight into the fragments' layout, neighbouring lanes hold different
 // rows, and the CU's address unit takes 64 cycles for a load instead of 16: one row, 512 x
 // 7168: 10.7 us against 7.9; 32 rows: 27 against 13.)  The waves' sums meet in LDS in the
@@ -35,14 +34,14 @@ namespace bsg {
 typedef __attribute__((ext_vector_type(4))) float few_f32x4_t;
 
 // GLU: 0 no gate, 1 a gate and an up fragment, 2 one fragment of eight gate and eight up rows.
-template <int KIND, int MF, int NF, int GLU, int W, int UN>
+template <int KIND, int MF, int NF, int GLU, int W>
 __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
   static_assert(!GLU || (KIND == KIND_BF16 && NF == (GLU == 1 ? 2 : 1)), "gate and up rows");
   constexpr int NO = GLU ? 1 : NF;            // output fragments along N
   constexpr int NC = GLU == 2 ? 8 : 16 * NO;  // output columns
-  // a wave's batch on its way to the fragments; at the end its sums
-  constexpr int PIECES = UN * 2 * (MF + NF);
-  static_assert(MF * NF <= PIECES, "the sums take the batch's place");
+  // a wave's step on its way to the fragments; at the end its sums
+  constexpr int PIECES = 2 * (MF + NF);
+  static_assert(MF * NF <= PIECES, "the sums take the step's place");
   __shared__ __attribute__((aligned(16))) i32x4_t smem[W][PIECES][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -106,100 +105,91 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const GemmArgs args) {
   few_f32x4_t acc[MF][NF] = {};
   const int steps = (args.k_bytes + 127) / 128;
   constexpr int NSC = KIND == KIND_BF16 ? 0 : (KIND == KIND_FP8 ? 1 : 2);   // scale bytes a fragment and step
-  // Two batches of UN steps a wave: one is multiplied while the other's loads are in flight.
-  struct Batch {
-    i32x4_t a[UN][2][MF], b[UN][2][NF];
-    uint32_t sa[UN][NSC ? NSC : 1][MF], sb[UN][NSC ? NSC : 1][NF];
+  // Two steps a wave: one is multiplied while the other's loads are in flight.
+  struct Step {
+    i32x4_t a[2][MF], b[2][NF];
+    uint32_t sa[NSC ? NSC : 1][MF], sb[NSC ? NSC : 1][NF];
   };
-  auto load = [&](Batch& t, int s0) __attribute__((always_inline)) {
+  auto load = [&](Step& t, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int s = s0 + u * W;
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t k = 128u * s + 64 * h;
+      // past K (and past the last step) the offset leaves every record
+      const uint32_t oob = (int)(k + 16 * (lane & 3)) < args.k_bytes ? 0u : kOOB;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t k = 128u * s + 64 * h;
-        // past K (and past the last step) the offset leaves every record
-        const uint32_t oob = (int)(k + 16 * (lane & 3)) < args.k_bytes ? 0u : kOOB;
+      for (int f = 0; f < NF; ++f)
+        t.b[h][f] = __builtin_bit_cast(
+            i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(GLU == 1 && f ? rb1 : rb0, (vb[f] + k) | oob, 0, 0));
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-          t.b[u][h][f] = __builtin_bit_cast(
-              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(GLU == 1 && f ? rb1 : rb0, (vb[f] + k) | oob, 0, 0));
+      for (int f = 0; f < MF; ++f)
+        t.a[h][f] = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (va[f] + k) | oob, 0, 0));
+    }
 #pragma unroll
-        for (int f = 0; f < MF; ++f)
-          t.a[u][h][f] = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (va[f] + k) | oob, 0, 0));
-      }
+    for (int h = 0; h < NSC; ++h) {
+      const int kb = KIND == KIND_FP8 ? s : 8 * s + 4 * h + lg;
 #pragma unroll
-      for (int h = 0; h < NSC; ++h) {
-        const int kb = KIND == KIND_FP8 ? s : 8 * s + 4 * h + lg;
+      for (int f = 0; f < MF; ++f) t.sa[h][f] = scale(rsa, args.ld_sfa, 16 * f + r16, kb);
 #pragma unroll
-        for (int f = 0; f < MF; ++f) t.sa[u][h][f] = scale(rsa, args.ld_sfa, 16 * f + r16, kb);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const int row = n0 + 16 * f + r16;
-          t.sb[u][h][f] = scale(rsb, args.ld_sfb, b_row ? row : row / 128, kb);
-        }
+      for (int f = 0; f < NF; ++f) {
+        const int row = n0 + 16 * f + r16;
+        t.sb[h][f] = scale(rsb, args.ld_sfb, b_row ? row : row / 128, kb);
       }
     }
   };
-  auto multiply = [&](const Batch& t) __attribute__((always_inline)) {
+  auto multiply = [&](const Step& t) __attribute__((always_inline)) {
     i32x4_t(*const mine_)[64] = smem[wave];
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int f = 0; f < NF; ++f) mine_[h * (MF + NF) + f][put] = t.b[h][f];
 #pragma unroll
-        for (int f = 0; f < NF; ++f) mine_[(2 * u + h) * (MF + NF) + f][put] = t.b[u][h][f];
-#pragma unroll
-        for (int f = 0; f < MF; ++f) mine_[(2 * u + h) * (MF + NF) + NF + f][put] = t.a[u][h][f];
-      }
+      for (int f = 0; f < MF; ++f) mine_[h * (MF + NF) + NF + f][put] = t.a[h][f];
+    }
     // (only this wave uses its pieces, and its LDS accesses execute in order)
     __builtin_amdgcn_wave_barrier();
+    i32x4_t a[2][MF], b[2][NF];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      i32x4_t a[2][MF], b[2][NF];
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int f = 0; f < NF; ++f) b[h][f] = mine_[h * (MF + NF) + f][get];
 #pragma unroll
-        for (int f = 0; f < NF; ++f) b[h][f] = mine_[(2 * u + h) * (MF + NF) + f][get];
+      for (int f = 0; f < MF; ++f) a[h][f] = mine_[h * (MF + NF) + NF + f][get];
+    }
 #pragma unroll
-        for (int f = 0; f < MF; ++f) a[h][f] = mine_[(2 * u + h) * (MF + NF) + NF + f][get];
-      }
+    for (int fa = 0; fa < MF; ++fa)
 #pragma unroll
-      for (int fa = 0; fa < MF; ++fa)
+      for (int fb = 0; fb < NF; ++fb) {
+        if constexpr (KIND == KIND_FP8) {
+          const i32x4_t bl = b[0][fb], bh = b[1][fb], al = a[0][fa], ah = a[1][fa];
+          acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              (i32x8_t){bl[0], bl[1], bl[2], bl[3], bh[0], bh[1], bh[2], bh[3]},
+              (i32x8_t){al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]}, acc[fa][fb], 0, 0, 0,
+              (int)t.sb[0][fb], 0, (int)t.sa[0][fa]);
+        } else {
 #pragma unroll
-        for (int fb = 0; fb < NF; ++fb) {
-          if constexpr (KIND == KIND_FP8) {
-            const i32x4_t bl = b[0][fb], bh = b[1][fb], al = a[0][fa], ah = a[1][fa];
-            acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                (i32x8_t){bl[0], bl[1], bl[2], bl[3], bh[0], bh[1], bh[2], bh[3]},
-                (i32x8_t){al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]}, acc[fa][fb], 0, 0, 0,
-                (int)t.sb[u][0][fb], 0, (int)t.sa[u][0][fa]);
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const i32x4_t bv = b[h][fb], av = a[h][fa];
-              if constexpr (KIND == KIND_BF16)
-                acc[fa][fb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8_t, bv), __builtin_bit_cast(bf16x8_t, av), acc[fa][fb], 0, 0, 0);
-              else
-                acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    (i32x8_t){bv[0], bv[1], bv[2], bv[3], 0, 0, 0, 0},
-                    (i32x8_t){av[0], av[1], av[2], av[3], 0, 0, 0, 0}, acc[fa][fb], 4, 4, 0, (int)t.sb[u][h][fb], 0,
-                    (int)t.sa[u][h][fa]);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const i32x4_t bv = b[h][fb], av = a[h][fa];
+            if constexpr (KIND == KIND_BF16)
+              acc[fa][fb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8_t, bv), __builtin_bit_cast(bf16x8_t, av), acc[fa][fb], 0, 0, 0);
+            else
+              acc[fa][fb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  (i32x8_t){bv[0], bv[1], bv[2], bv[3], 0, 0, 0, 0},
+                  (i32x8_t){av[0], av[1], av[2], av[3], 0, 0, 0, 0}, acc[fa][fb], 4, 4, 0, (int)t.sb[h][fb], 0,
+                  (int)t.sa[h][fa]);
           }
         }
-    }
+      }
     __builtin_amdgcn_wave_barrier();
   };
-  Batch t0, t1;
+  Step t0, t1;
   if (wave < steps) load(t0, wave);
-  for (int s = wave; s < steps; s += 2 * W * UN) {
-    load(t1, s + W * UN);
+  for (int s = wave; s < steps; s += 2 * W) {
+    load(t1, s + W);
     __builtin_amdgcn_sched_barrier(0);
     multiply(t0);
     __builtin_amdgcn_sched_barrier(0);
-    load(t0, s + 2 * W * UN);
+    load(t0, s + 2 * W);
     __builtin_amdgcn_sched_barrier(0);
     multiply(t1);
     __builtin_amdgcn_sched_barrier(0);
@@ -244,7 +234,7 @@ template <int KIND, int MF, int NF, int GLU, int W>
 static int go(const GemmArgs& a, hipStream_t st) {
   const int per = GLU == 2 ? 8 : (GLU ? 16 : 16 * NF), n = GLU ? a.inter : a.N;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((few_kernel<KIND, MF, NF, GLU, W, 1>), dim3((unsigned)((n + per - 1) / per)), dim3(W * 64), 0, st,
+  hipLaunchKernelGGL((few_kernel<KIND, MF, NF, GLU, W>), dim3((unsigned)((n + per - 1) / per)), dim3(W * 64), 0, st,
                      a);
   return hipGetLastError() == hipSuccess ? BSG_OK : BSG_ERR_HIP;
 }
