@@ -134,7 +134,7 @@ def log(msg):
 # Kernel sources behind each measured kind: a change to any of them detaches the
 # committed rocprofv3 counters from the kernel.
 SOURCES = {
-    "gemm": ("gemm_kernel.h", "configs.h", "quant_math.h"),
+    "gemm": ("gemm_kernel.h", "act_math.h", "scale_record.h", "configs.h", "quant_math.h"),
     "quant": ("quant.hip", "quant_math.h"),
     "mqa": ("mqa.hip",),
 }

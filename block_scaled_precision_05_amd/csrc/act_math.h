@@ -97,7 +97,7 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
 // The normal distribution's upper tail Q(x) = erfc(x / sqrt 2) / 2 for x >= 0, and
 // e^(-x^2/2) beside it.  Q(x) = e^(-x^2/2) t P(t) with t = 1 / (1 + 0.3 x): P, of degree 7,
 // fitted here to Q e^(x^2/2) / t for 0 <= x <= 15 by reweighted least squares (largest
-// relative error 1.8e-7, 3.2e-7 evaluated in fp32); beyond 13.5 both factors underflow.
+// relative error 1.8e-7, 4.8e-7 evaluated in fp32); beyond 13.5 both factors underflow.
 // The relative form keeps the tail's digits, which 1 + erf would cancel.
 __device__ __forceinline__ float normal_tail(float x, float& e) {
   e = exp_f32(-0.5f * x * x);

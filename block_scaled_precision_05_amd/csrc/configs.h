@@ -40,8 +40,8 @@
 // calls whose 256x256 tiles would leave CUs idle.  BF16: 128x128 over 2x2 waves of 64x64.
 // The copies' latency bounds them, so a CU has to keep many in flight: a ring of four
 // 16 KiB stages where two workgroups share a CU, of eight where there is one to a CU at most
-// (2048 x 2048 over K = 7168, 256 tiles: 65 us with eight stages, 84 with four; 1024 x 7168
-// over K = 2048, 448 tiles: 42 and 37).  FP8: the masked tile (its row permutation needs
+// (2048 x 2048 over K = 7168, 256 tiles: 61 us with eight stages, 82 with four; 1024 x 7168
+// over K = 2048, 448 tiles: 40 and 35).  FP8: the masked tile (its row permutation needs
 // 128-row waves).  FP4: 128x128 over two waves of 128x64 (eight stages measured no faster).
 #define BSG_BF16_SMALL_CFG 128, 128, 2, 2, 64, 4, 1
 #define BSG_BF16_DEEP_CFG 128, 128, 2, 2, 64, 8, 1

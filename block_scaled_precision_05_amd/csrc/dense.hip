@@ -32,9 +32,13 @@ static const int64_t kMaxRows = (int64_t(1) << 29) - 1;        // a contraction'
 // the GPU to a full round of them, and a fixed part for launch, first stage and epilogue.
 // The parts' fp32 sums pass through memory twice at about 5.5 TB/s, and the join is a
 // launch of its own.
-//   BF16 examples over K = 7168: 1024 x 2048: 256-row tiles 113 us, 128-row tiles 80, with the
-//   deep ring 52, deep in 2 parts 41; 2048 x 2048: 113, 84, 65, 76; 4096 x 2048: 133, 122
-//   (128-row tiles), 127 (deep).
+//   BF16 examples over K = 7168: 1024 x 2048: 256-row tiles 113 us, 128-row tiles 79, with the
+//   deep ring 49, deep in 2 parts 40; 2048 x 2048: 112, 82, 61; 4096 x 2048: 123, 123, 141.
+// Over 220 random sizes (64 .. 4096 rows, 256 .. 6800 columns, contractions of 128 .. 7900)
+// the pick takes 2% more than the fastest form on average and 15% at most in BF16, 4% and
+// 26% in FP8, 10% and 45% in FP4, whose short contractions it prices too low in 256-row
+// tiles.  The costs are those of scale arrays that take 8-byte loads: with others, 256-row
+// FP4 tiles take up to 8 us more (517 x 432 over 288: 20 us where parts take 9.4).
 struct TileCost {
   int form;
   int64_t bm, bn, lo_tiles, cap;   // tile, tiles up to which `lo` holds, tiles of a full round
@@ -67,8 +71,8 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
   const int64_t bytes = kind == KIND_BF16 ? 2 * K : (kind == KIND_FP8 ? K : K / 2);
   const int64_t stages = (bytes + 63) / 64;
   // Few rows: the stream of B through registers.  Up to 32 rows at any K; up to 64 where a
-  // row is at most 8 KiB (64 rows, BF16 7168 x 2048: 12.2 us against 15.8 in parts; 2048 x
-  // 7168: 21.3 against 18.1: every workgroup reads all of A).
+  // row is at most 8 KiB (64 rows, BF16 7168 x 2048: 12.0 us against 14.6 in parts; 2048 x
+  // 7168: 21.0 against 15.1: every workgroup reads all of A).
   // (one workgroup of up to 1024 threads to 16 columns, 2^32 threads to a launch)
   if (!strided && (M <= 32 || (M <= 64 && bytes <= 8192)) && N < (int64_t)1 << 25) return {DENSE_FEW, 1};
   DensePlan best = {DENSE_BIG, 1};
@@ -83,7 +87,8 @@ DensePlan dense_plan(int kind, int64_t M, int64_t N, int64_t K, bool strided) {
     }
     // Parts of whole rounds of the ring, all of them on the GPU at once.  (One part: the
     // epilogue moves to the join, whose threads are many; FP8 and FP4 tiles of few, tall
-    // waves gain by it at small K: FP8 472 x 728 x 896 16.0 us in one kernel, 12.9 apart.)
+    // waves gain by it at small K: FP8 472 x 728 x 896 16.0 us in one kernel, 14.8 apart.  At most 16
+    // parts: the costs were fitted up to there.)
     for (int64_t s = kind == KIND_BF16 ? 2 : 1; c.round && s <= 16 && s * tiles <= c.cap && c.round * (s - 1) < stages; ++s) {
       const int64_t per = ((stages + s - 1) / s + c.round - 1) / c.round * c.round;
       if ((stages + per - 1) / per != s) continue;

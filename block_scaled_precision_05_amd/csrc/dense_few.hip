@@ -1,5 +1,6 @@
 // dense_few.hip -- the dense products with epilogues for few rows (a decode step): up to 64
-// rows of A, where the product is a stream of B from memory.
+// rows of A, where the product is a stream of B from memory.  (Times here: us a call in graphs
+// of six calls over three sets of operands.)
 //
 // One workgroup of W waves owns 16 NF rows of B (16 NF columns of D; in the gated block 16
 // gate rows and their 16 up rows) and shares out the contraction: wave w takes the
@@ -12,7 +13,7 @@
 // consecutive columns a lane.
 //
 // Bound by the stream of B once that is long (one row, gated 2 x 2048 x 7168: 58.7 MB in
-// 13.0 us, 4.5 TB/s), by launch and first access when short (7.3 MB: 6.7 us), and from
+// 12.2 us, 4.8 TB/s), by launch and first access when short (7.3 MB: 7.8 us), and from
 // some 32 rows on by A, which every workgroup reads whole.
 //
 // Fragments (16x16x32 BF16, 16x16x128 FP8 and FP4): lane l holds row l % 16, bytes
@@ -240,10 +241,10 @@ static int go(const GemmArgs& a, hipStream_t st) {
 }
 
 // Waves and columns of a workgroup.  Up to 16 rows: 16 waves of 16 columns (BF16 7168 x 2048,
-// one row: 7.9 us; 8 waves 8.7; 32 columns no faster).  More rows: 32 columns halve what is
-// read of A (32 rows, 7168 x 2048: 9.4 us against 10.3) where that leaves most CUs a
-// workgroup, 16 otherwise (2048 x 7168: 14.0 against 18.1); 64 rows: 4 waves of 32 columns
-// 12.2 us against 13.3 with 8.
+// one row: 7.8 us; 8 waves 8.7; 32 columns no faster).  More rows: 32 columns halve what is
+// read of A (32 rows, 7168 x 2048: 9.5 us against 10.3) where that leaves most CUs a
+// workgroup, 16 otherwise (2048 x 7168: 13.7 against 18.1); 64 rows: 4 waves of 32 columns
+// 12.0 us against 13.3 with 8.
 template <int KIND>
 static int go_rows(const GemmArgs& a, hipStream_t st) {
   if (a.M <= 16) return go<KIND, 1, 1, 0, 16>(a, st);

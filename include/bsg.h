@@ -532,15 +532,17 @@ int64_t lora_add_workspace(int64_t T, int64_t rows, int32_t G, int64_t N, int64_
  * residual stream; one without a gate is two gemm_*_act calls.
  *
  * Common to the calls below:
- *  - workspace: the bytes the call's *_workspace function gives for the same sizes,
- *    16-byte aligned (may be NULL when that is 0); no initial value needed, nothing in it
- *    lasts; calls that overlap in time need one each.  Calls that are too small to fill
- *    the GPU with whole tiles split the contraction and join fp32 sums kept there, in an
- *    order that is the same on every run.
+ *  - workspace: the bytes the call's *_workspace function gives for the same sizes
+ *    (enough for any activation and any choice of outputs), 16-byte aligned (may be NULL
+ *    when that is 0); no initial value needed, nothing in it lasts; calls that overlap in
+ *    time need one each.  Calls that are too small to fill the GPU with whole tiles split
+ *    the contraction and join fp32 sums kept there, in an order that is the same on every
+ *    run.
  *  - sums and everything formed from them are fp32, rounded to bf16 once at each store.
- *  - M and N (inter) may be anything from 0 on; rows of A, of B and of the contraction's
- *    operands follow the dense products' rules for K.  ceil(M/128) * ceil(columns/128)
- *    must be below 2^24 (BSG_ERR_UNSUPPORTED_SHAPE).
+ *  - M and N may be anything from 0 on, within the limits of each call (inter is a multiple
+ *    of 8); rows of A, of B and of the contraction's operands follow the dense products'
+ *    rules for K.  ceil(M/128) * ceil(columns/128) must be below 2^24
+ *    (BSG_ERR_UNSUPPORTED_SHAPE).
  * ------------------------------------------------------------------------- */
 
 /* D = R + f(A B^T + bias), and the pre-activation beside it:
@@ -578,7 +580,7 @@ int64_t gemm_fp4_act_workspace(int64_t M, int64_t N, int64_t K);
  *   dB[n][k] = bf16( sum_m bf16(dz[m][n]) A[m][k] )       bf16 [N][lddb >= K]
  *   dbias[n] = sum_m dz[m][n]                             fp32 [N]
  * dz is rounded to bf16 where it enters a product (the matrix cores' operand type), not in
- * dbias.  Where z <= 0, BSG_ACT_RELU's gradient is 0.
+ * dbias.  Where z <= 0, BSG_ACT_RELU's gradient is 0 (here and in the gated block's dg).
  *   dA, dB, dbias: each may be NULL (not computed); A is read for dB only, B for dA only.
  *   Z: bf16 [M][ldz >= N]; with BSG_ACT_NONE it is not read and may be NULL.
  *   Requires K % 8 == 0; A and B 16-byte aligned with leading dimensions multiples of 8;
