@@ -34,7 +34,7 @@ static const int64_t kMaxRows = (int64_t(1) << 29) - 1;        // a contraction'
 // launch of its own.
 //   BF16 examples over K = 7168: 1024 x 2048: 256-row tiles 113 us, 128-row tiles 79, with the
 //   deep ring 49, deep in 2 parts 40; 2048 x 2048: 112, 82, 61; 4096 x 2048: 123, 123, 141.
-// Over 220 random sizes (64 .. 4096 rows, 256 .. 6800 columns, contractions of 128 .. 7900)
+// Over 218 random sizes (64 .. 4096 rows, 256 .. 6800 columns, contractions of 128 .. 7900)
 // the pick takes 2% more than the fastest form on average and 15% at most in BF16, 4% and
 // 26% in FP8, 10% and 45% in FP4, whose short contractions it prices too low in 256-row
 // tiles.  The costs are those of scale arrays that take 8-byte loads: with others, 256-row
